@@ -33,6 +33,10 @@ SOURCES = [
     "noalloc.cu",
     "fp8_gather_kernel.cu",
     "absorbed_kernel.cu",
+    "tree_abi.cpp",
+    "tables_kernel.cu",
+    "tree_kernels.cu",
+    "tree_attn_kernel.cu",
 ]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -114,6 +114,67 @@ struct AbsorbedParams {
 cudaError_t launch_absorbed(const CUtensorMap& tq, const CUtensorMap& tc, const CUtensorMap& tb,
                             const CUtensorMap& t4, const AbsorbedParams& p, int num_units, cudaStream_t stream);
 
+// ---- speculative decoding: block tables, tree masks, tree attention, commit -------
+constexpr int kMaxTableBatch = 8192;             // requests whose sums fit one CTA's shared memory
+constexpr int kMaxMaskWords = 1024;              // 64 nodes a word
+constexpr int64_t kMaxTreePairs = 0x7fffff00;    // (row, head) pairs: TMA row coordinates
+
+struct TablesParams {
+  const int32_t *seq_lens, *new_lens;   // [batch]
+  int batch, block_size;
+  int32_t* block_table;                 // [batch, max_blocks]
+  int max_blocks;
+  int32_t* num_held;                    // [batch] table entries in use
+  int32_t* free_blocks;                 // stack of block ids, the next to take at count - 1
+  int32_t free_capacity;
+  int32_t* free_count;                  // [1]
+  int32_t *qo_indptr, *kv_lens;         // [batch + 1], [batch], or null
+  int64_t* slot_mapping;                // [num_tokens] or null
+  int64_t num_tokens;
+  int32_t* status;
+};
+cudaError_t launch_tables(const TablesParams& p, cudaStream_t stream);
+
+cudaError_t launch_tree_mask(const int32_t* parents, const int32_t* qo_indptr, const int32_t* kv_lens, int batch,
+                             int64_t total_rows, int words, int64_t* mask, int32_t* positions, int32_t* status,
+                             cudaStream_t stream);
+
+struct TreeParams {
+  const __nv_bfloat16* q;               // [total_rows, H, 576]
+  const __nv_bfloat16* cache;           // [num_blocks, block_size, 576]
+  int64_t num_blocks;
+  int block_size;
+  const int32_t* block_table;           // [batch, max_blocks]
+  int max_blocks;
+  const int32_t *qo_indptr, *kv_lens;   // [batch + 1], [batch]
+  const int64_t* mask;                  // [total_rows, mask_words] or null: node i sees nodes 0 .. i
+  int mask_words;
+  int batch;
+  int64_t total_rows;
+  int num_heads;
+  float sm_scale, soft_cap;             // soft_cap 0: none
+  __nv_bfloat16* o;                     // [total_rows, H, 512]
+  float* lse;                           // [total_rows, H] or null
+  void* workspace;
+  int32_t* status;
+};
+int64_t tree_workspace_bytes();         // on the current device; 0 on error
+cudaError_t launch_tree_attention(const TreeParams& p, cudaStream_t stream);
+
+struct CommitParams {
+  uint4* cache;                         // layer l, slot s, chunk c: cache[l * layer_chunks + s * row_chunks + c]
+  int num_layers;
+  int64_t layer_chunks;
+  int64_t num_blocks;
+  int block_size, row_chunks;
+  const int32_t* block_table;           // [batch, max_blocks]
+  int max_blocks;
+  const int32_t *seq_lens, *paths, *counts;   // [batch], [batch, max_accept], [batch]
+  int max_accept;
+  int32_t* status;
+};
+cudaError_t launch_tree_commit(const CommitParams& p, int batch, cudaStream_t stream);
+
 // MLA_PLAN_CTA_PAIRS: 1 when "1" (plan prefills on CTA pairs), 0 when "0", -1 otherwise.
 int cta_pair_mode();
 

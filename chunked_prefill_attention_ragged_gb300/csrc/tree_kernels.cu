@@ -1,0 +1,153 @@
+// The two small steps around tree attention: visibility of drafted nodes before it, and the
+// accepted nodes' cache rows after it.
+//
+// tree_mask: a drafted node sees itself and its ancestors.  With parent(i) < i,
+//   M(i) = {i} u M(parent(i)),  depth(i) = 1 + depth(parent(i)),  M(-1) = {}, depth(-1) = -1,
+// written as bits, and its token position, context length + depth.  Each node is one thread
+// that walks up its own chain: no thread waits for another, and a chain is as long as the
+// tree is deep.
+//
+// tree_commit: row (s + path[i]) of the request moves to row (s + i), for i = 0 .. count - 1
+// with path strictly increasing, so path[j] >= j.  A thread owns 16 bytes of the row in one
+// layer and goes up i in groups of eight, all eight loads before the eight stores: a store to
+// row i cannot hit a later source, because path[j] >= j > i.  No scratch, no barrier between
+// the moves.  Bound by latency for one layer (path -> table -> row -> row), by HBM for many.
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kMaskThreads = 128;
+constexpr int kMaskWords = 4;   // words of a row collected per walk
+
+__device__ __forceinline__ void flag(int32_t* status) {
+  if (status) atomicOr(status, MLA_DEVSTAT_BAD_INDEX);
+}
+
+__global__ void __launch_bounds__(kMaskThreads)
+tree_mask_kernel(const int32_t* __restrict__ parents, const int32_t* __restrict__ qo_indptr,
+                 const int32_t* __restrict__ kv_lens, int64_t total_rows, int words, int64_t* __restrict__ mask,
+                 int32_t* __restrict__ positions, int32_t* status) {
+  const int r = blockIdx.x;
+  const int64_t q0 = qo_indptr[r], q1 = qo_indptr[r + 1];
+  if (q0 < 0 || q1 < q0 || q1 > total_rows) {
+    if (threadIdx.x == 0) flag(status);
+    return;
+  }
+  const int n = (int)(q1 - q0);
+  const int base = kv_lens ? kv_lens[r] - n : 0;
+  const int32_t* par = parents + q0;
+  for (int i = threadIdx.x; i < n; i += kMaskThreads) {
+    bool bad = i >= 64 * (int64_t)words;
+    int depth = 0;
+    for (int w0 = 0; w0 < words; w0 += kMaskWords) {
+      uint64_t bits[kMaskWords] = {0, 0, 0, 0};
+      int up = i;
+      depth = -1;
+      while (up >= 0) {   // strictly downwards: ends
+        ++depth;
+#pragma unroll
+        for (int k = 0; k < kMaskWords; ++k)
+          if ((up >> 6) == w0 + k) bits[k] |= 1ull << (up & 63);
+        const int next = __ldg(par + up);
+        if (next < -1 || next >= up) {
+          bad = true;
+          break;
+        }
+        up = next;
+      }
+#pragma unroll
+      for (int k = 0; k < kMaskWords; ++k)
+        if (w0 + k < words) mask[(q0 + i) * words + w0 + k] = (int64_t)bits[k];
+    }
+    if (positions) positions[q0 + i] = base + depth;
+    if (bad) flag(status);
+  }
+}
+
+constexpr int kCommitThreads = 256;
+constexpr int kCommitRows = 128;   // accepted rows resolved at a time
+constexpr int kGroup = 8;
+
+__global__ void __launch_bounds__(kCommitThreads)
+tree_commit_kernel(const CommitParams p) {
+  __shared__ int64_t src[kCommitRows], dst[kCommitRows];   // flat slots; -1: leave this row
+  __shared__ int stop;
+  const int r = blockIdx.y, tid = threadIdx.x;
+  int count = p.counts[r];
+  if (count < 0 || count > p.max_accept) {
+    if (tid == 0 && blockIdx.x == 0) flag(p.status);
+    count = min(max(count, 0), p.max_accept);
+  }
+  const int64_t base = p.seq_lens[r];
+  const int32_t* path = p.paths + (int64_t)r * p.max_accept;
+  const int chunks = p.row_chunks;
+  const int64_t item = (int64_t)blockIdx.x * kCommitThreads + tid;
+  const bool live = item < (int64_t)p.num_layers * chunks;
+  uint4* column = nullptr;
+  if (live) column = p.cache + (item / chunks) * p.layer_chunks + item % chunks;
+  for (int i0 = 0; i0 < count; i0 += kCommitRows) {
+    const int here = min(kCommitRows, count - i0);
+    if (tid == 0) stop = here;
+    __syncthreads();
+    if (tid < here) {
+      const int i = i0 + tid, node = path[i];
+      if (node < 0 || base < 0 || (i > 0 && path[i - 1] >= node)) atomicMin(&stop, tid);
+      auto slot = [&](int64_t pos) -> int64_t {
+        const int64_t bi = pos / p.block_size;
+        if (pos < 0 || bi >= p.max_blocks) return -1;
+        const int64_t blk = p.block_table[(int64_t)r * p.max_blocks + bi];
+        return blk >= 0 && blk < p.num_blocks ? blk * p.block_size + (pos - bi * p.block_size) : -1;
+      };
+      int64_t a = -1, b = -1;
+      if (node != i) {
+        a = slot(base + node);
+        b = slot(base + i);
+        if (a < 0 || b < 0) {
+          a = -1;
+          if (blockIdx.x == 0) flag(p.status);
+        }
+      }
+      src[tid] = a;
+      dst[tid] = b;
+    }
+    __syncthreads();
+    const int n = stop;
+    if (live) {
+      for (int k0 = 0; k0 < n; k0 += kGroup) {
+        uint4 v[kGroup];
+#pragma unroll
+        for (int k = 0; k < kGroup; ++k)
+          if (k0 + k < n && src[k0 + k] >= 0) v[k] = column[src[k0 + k] * chunks];
+#pragma unroll
+        for (int k = 0; k < kGroup; ++k)
+          if (k0 + k < n && src[k0 + k] >= 0) column[dst[k0 + k] * chunks] = v[k];
+      }
+    }
+    if (n < here) {   // not increasing from here on: nothing more is moved
+      if (tid == 0 && blockIdx.x == 0) flag(p.status);
+      return;
+    }
+    __syncthreads();   // src, dst and stop are reused
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_tree_mask(const int32_t* parents, const int32_t* qo_indptr, const int32_t* kv_lens, int batch,
+                             int64_t total_rows, int words, int64_t* mask, int32_t* positions, int32_t* status,
+                             cudaStream_t stream) {
+  tree_mask_kernel<<<batch, kMaskThreads, 0, stream>>>(parents, qo_indptr, kv_lens, total_rows, words, mask, positions,
+                                                      status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_tree_commit(const CommitParams& p, int batch, cudaStream_t stream) {
+  const int64_t items = (int64_t)p.num_layers * p.row_chunks;
+  const int64_t grid = (items + kCommitThreads - 1) / kCommitThreads;
+  tree_commit_kernel<<<dim3((unsigned)grid, (unsigned)batch), kCommitThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace mla

@@ -63,6 +63,7 @@ extern "C" {
 /* bits a kernel may set in a device status word */
 #define MLA_DEVSTAT_TIMEOUT    0x1
 #define MLA_DEVSTAT_BAD_INDEX  0x2
+#define MLA_DEVSTAT_NO_BLOCKS  0x4   /* mla_block_table_update ran out of free blocks */
 
 /* Name of a status code ("ok", "invalid argument", ...).  Never NULL. */
 MLA_API const char* mla_error_string(int status);
@@ -365,6 +366,130 @@ MLA_API int mla_absorbed_plan(mla_plan_t* out, const int32_t* qo_indptr, const i
 MLA_API int mla_absorbed_run(mla_plan_t plan, const void* q_abs, const void* cache, int64_t num_blocks,
                              const int32_t* block_table, int max_blocks_per_req, void* o_lat, float* lse,
                              void* stream);
+
+/* ======================================================================
+ * Speculative decoding over the paged latent cache.  A step of a request with
+ * s cached tokens: n drafted tokens ("nodes" of a tree whose root is the
+ * context) get cache blocks and slots (mla_block_table_update), their rows are
+ * stored (mla_cache_write), visibility and rotary positions come from the
+ * nodes' parents (mla_tree_mask), every node attends to the context and to its
+ * own ancestors (mla_tree_attention), and the rows of the accepted ones move
+ * to consecutive positions (mla_tree_commit).  One node per request is
+ * ordinary decoding.  Every length is read on the device, so that a captured
+ * graph of the step can be replayed as the requests grow.
+ * [vLLM-V4] slot rule; [sglang] 512 latent + 64 rope per cache row.
+ * ====================================================================== */
+/*
+ * Fit the block tables to the requests' lengths, and map new tokens to slots.
+ *   seq_lens, new_lens : DEVICE int32 [batch], tokens in the cache before the step / new ones
+ *   block_table   : DEVICE int32 [batch, max_blocks_per_req], updated in place
+ *   num_held      : DEVICE int32 [batch], entries of each row in use; updated in place
+ *   free_blocks   : DEVICE int32 [free_capacity], a stack of unused block ids, of which the first
+ *                   free_count[0] are valid and the last of those is taken next; updated
+ *   free_count    : DEVICE int32 [1], updated
+ *   qo_indptr     : DEVICE int32 [batch+1] or NULL: prefix sums of new_lens  (written)
+ *   kv_lens       : DEVICE int32 [batch] or NULL: seq_lens + new_lens        (written)
+ *   slot_mapping  : DEVICE int64 [num_tokens] or NULL (num_tokens must be 0 then): the flat
+ *                   slot of every new token in request order, as mla_cache_write takes it; -1
+ *                   for a token without a block, and behind the last new token   (written)
+ *   status        : DEVICE int32 word or NULL
+ * Row r ends up with ceil((seq_lens[r] + new_lens[r]) / block_size) entries: surplus blocks go
+ * back on the stack first (entries become -1), then missing ones are taken, request by request.
+ * A request is served when all requests up to it can be: otherwise it keeps what it holds, and
+ * MLA_DEVSTAT_NO_BLOCKS is OR-ed into status.  Reserving blocks and giving the same ones back
+ * restores the stack.  seq = new = 0 releases a row.  MLA_DEVSTAT_BAD_INDEX is OR-ed in for a
+ * negative length, num_held or free_count outside its range (clamped), a request that needs
+ * more than max_blocks_per_req blocks (it keeps what it holds), a full stack (the block is
+ * lost), a negative block id taken from the stack, or more new tokens than num_tokens.
+ * Limits: batch <= 8192, batch * max_blocks_per_req < 2^31.  One launch; allocates nothing.
+ * Calls that share a stack must be ordered by the caller.
+ */
+MLA_API int mla_block_table_update(const int32_t* seq_lens, const int32_t* new_lens, int batch, int block_size,
+                                   int32_t* block_table, int max_blocks_per_req, int32_t* num_held,
+                                   int32_t* free_blocks, int32_t free_capacity, int32_t* free_count,
+                                   int32_t* qo_indptr, int32_t* kv_lens, int64_t* slot_mapping, int64_t num_tokens,
+                                   int32_t* status, void* stream);
+
+/*
+ * Visibility bits and token positions of drafted trees.
+ *   parents   : DEVICE int32 [total_rows]; row qo_indptr[r] + i holds the parent of node i of
+ *               request r, a node index below i, or -1 for a child of the context
+ *   qo_indptr : DEVICE int32 [batch+1] (qo_indptr[0] = 0)
+ *   kv_lens   : DEVICE int32 [batch], context + nodes, or NULL
+ *   tree_mask : DEVICE int64 [total_rows, mask_words]: bit j % 64 of word j / 64 of a node's
+ *               row says whether it sees node j, which is itself or an ancestor   (written)
+ *   positions : DEVICE int32 [total_rows] or NULL: the node's depth (a child of the context
+ *               has 0), plus kv_lens[r] - nodes of r when kv_lens is given        (written)
+ *   status    : DEVICE int32 word or NULL; MLA_DEVSTAT_BAD_INDEX is OR-ed in for a parent that
+ *               is not below its node (taken as -1), a node past 64 * mask_words (bits that do
+ *               not fit are left out), or a request whose rows are not inside total_rows (its
+ *               rows are not written)
+ * Rows behind qo_indptr[batch] are left as they were.  mask_words <= 1024.
+ */
+MLA_API int mla_tree_mask(const int32_t* parents, const int32_t* qo_indptr, const int32_t* kv_lens, int batch,
+                          int64_t total_rows, int mask_words, int64_t* tree_mask, int32_t* positions,
+                          int32_t* status, void* stream);
+
+/* Bytes of workspace that mla_tree_attention needs on the current device (of any batch). */
+MLA_API int mla_tree_workspace(int64_t total_rows, int num_heads, int64_t* bytes);
+
+/*
+ * Attention of drafted nodes (or single new tokens) over the paged latent cache, absorbed form.
+ *   q_abs      : bf16 [total_rows, num_heads, 576] (W_UK(h) q_nope(h) || q_rope(h))
+ *   cache      : bf16 [num_blocks, block_size, 576]
+ *   block_table: DEVICE int32 [batch, max_blocks_per_req]
+ *   qo_indptr  : DEVICE int32 [batch+1] (qo_indptr[0] = 0); request r owns rows
+ *                [qo_indptr[r], qo_indptr[r+1]); total_rows is the size of q_abs and o_lat and
+ *                may be more than qo_indptr[batch] (a padded batch): rows behind are left as
+ *                they were
+ *   kv_lens    : DEVICE int32 [batch], cache positions of the request with its nodes' own rows,
+ *                which must be in the cache: node i is at cache position kv_len - nodes + i
+ *   tree_mask  : DEVICE int64 [total_rows, mask_words], as mla_tree_mask writes it: a node sees
+ *                the whole context (positions below kv_len - nodes) and the nodes whose bits
+ *                are set, its own only if set; a node past 64 * mask_words is not seen.  NULL
+ *                (mask_words 0): node i sees nodes 0 .. i, a chain
+ *   sm_scale   : finite and > 0; logits_soft_cap: <= 0 none, c > 0: c * tanh(x / c)
+ *   o_lat      : bf16 [total_rows, num_heads, 512]  (written)
+ *   lse        : fp32 [total_rows, num_heads], natural log, or NULL  (written)
+ *   workspace  : DEVICE, 16-byte aligned, at least mla_tree_workspace bytes, not in use by
+ *                another call that may run at the same time; its contents do not matter
+ *   status     : DEVICE int32 word or NULL
+ * A row that sees no key gets O = 0, LSE = -inf.  Positions at or past kv_len are never read.
+ * Cache rows below kv_len are to be finite: an infinity or NaN in a row that a node does not
+ * see may still reach the other rows of its request.  MLA_DEVSTAT_BAD_INDEX is OR-ed in for a
+ * block id outside [0, num_blocks) (its rows read as zeros), kv_len outside
+ * [0, max_blocks_per_req * block_size] (clamped), or a request whose rows are not inside
+ * total_rows (skipped); MLA_DEVSTAT_TIMEOUT when a pipeline wait gave up.
+ * Needs num_blocks * block_size < 2^31 - 1 and total_rows * num_heads <= 2^31 - 256.
+ * Allocates nothing, does not synchronise; results do not depend on timing.
+ */
+MLA_API int mla_tree_attention(const void* q_abs, const void* cache, int64_t num_blocks, int block_size,
+                               const int32_t* block_table, int max_blocks_per_req, const int32_t* qo_indptr,
+                               const int32_t* kv_lens, const int64_t* tree_mask, int mask_words, int batch,
+                               int64_t total_rows, int num_heads, float sm_scale, float logits_soft_cap, void* o_lat,
+                               float* lse, void* workspace, int64_t workspace_bytes, int32_t* status, void* stream);
+
+/*
+ * Keep the accepted nodes: cache row of position seq_lens[r] + accepted[r][i] moves to position
+ * seq_lens[r] + i, for i < accepted_counts[r], in every layer.
+ *   cache        : bf16, layer l at cache + l * layer_stride (elements), each [num_blocks,
+ *                  block_size, entry_dim] (entry_dim % 8 == 0); layer_stride a multiple of 8
+ *                  and at least a layer's size (ignored for one layer)
+ *   block_table  : DEVICE int32 [batch, max_blocks_per_req]; requests share no block that is
+ *                  written
+ *   seq_lens     : DEVICE int32 [batch], the context: the position of node 0
+ *   accepted     : DEVICE int32 [batch, max_accepted], node indices of the accepted path,
+ *                  strictly increasing
+ *   accepted_counts : DEVICE int32 [batch], 0 .. max_accepted
+ *   status       : DEVICE int32 word or NULL; MLA_DEVSTAT_BAD_INDEX is OR-ed in for a count out
+ *                  of range (clamped), a path that is not increasing (it ends there) or a
+ *                  position without a block (that row is not moved)
+ * Bit-exact copies.  batch <= 65535.
+ */
+MLA_API int mla_tree_commit(void* cache, int num_layers, int64_t layer_stride, int64_t num_blocks, int block_size,
+                            int entry_dim, const int32_t* block_table, int max_blocks_per_req,
+                            const int32_t* seq_lens, const int32_t* accepted, const int32_t* accepted_counts,
+                            int batch, int max_accepted, int32_t* status, void* stream);
 
 /* ======================================================================
  * LSE merge of two partial attention states.  [vLLM-FI]

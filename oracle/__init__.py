@@ -25,7 +25,9 @@ computes, written from the pages' definitions:
     dequantizing gather;
   * the unchunked attention that chunked prefill must reproduce;
   * absorbed-weight attention (multi-query over the 576-wide compressed rows,
-    sglang issue #3849's forward_absorb; explicit sm_scale per TVM PR #17674).
+    sglang issue #3849's forward_absorb; explicit sm_scale per TVM PR #17674);
+  * the speculative-decoding step: block tables and slots from lengths, tree
+    visibility, tree attention over the cache rows, accepted rows moved.
 
 Only ``tests/``, ``__graft_entry__.smoke()`` and the CPU-baseline leg of
 ``bench.py`` may import this package.  It shares no code with the CUDA path
@@ -41,7 +43,8 @@ fixture, round trip through the gather, padding slots), up-projection
 chunked pipeline (split/merge identity), absorbed attention (the
 absorption identity against the MHA oracle over decompressed K/V, brute force),
 fp8 entries (hand-decoded codes, every
-e4m3 code against the library's float8 type, exact products).  No function is "parity unpinned".
+e4m3 code against the library's float8 type, exact products), speculative step
+(hand-written tables and trees, chains against absorbed attention, brute force).  No function is "parity unpinned".
 """
 from .bf16 import bf16_bits_to_f64, round_f64_to_bf16
 from .attention import allowed_mask, attend_request, ragged_attention
@@ -53,10 +56,13 @@ from .chunked import chunked_prefill_attention
 from .absorbed import absorb_query, absorbed_attention, absorbed_output_to_mha
 from .fp8_cache import (dequant_fp8_entries, e4m3_to_f64, f64_to_bf16_bits, gather_latent_fp8,
                         ue8m0_to_f64)
+from .speculative import (pack_bits, tree_attention, tree_commit, tree_visibility,
+                          update_block_table)
 
 __all__ = [
     "bf16_bits_to_f64", "round_f64_to_bf16", "allowed_mask", "attend_request",
     "ragged_attention", "gather_latent", "slot_of", "cache_write", "up_project", "merge_state",
     "chunked_prefill_attention", "dequant_fp8_entries", "e4m3_to_f64", "f64_to_bf16_bits",
     "gather_latent_fp8", "ue8m0_to_f64", "absorb_query", "absorbed_attention", "absorbed_output_to_mha",
+    "pack_bits", "tree_attention", "tree_commit", "tree_visibility", "update_block_table",
 ]
