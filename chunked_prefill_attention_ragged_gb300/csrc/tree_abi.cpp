@@ -89,7 +89,7 @@ int mla_tree_attention(const void* q_abs, const void* cache, int64_t num_blocks,
       num_blocks > 0x7fffffff || num_blocks * (int64_t)block_size >= 0x7fffffff ||
       (int64_t)max_blocks_per_req * block_size > 0x7fffff00)
     return MLA_ERR_UNSUPPORTED;
-  if (!aligned(q_abs, 16) || !aligned(cache, 16) || !aligned(o_lat, 16) || !aligned(workspace, 16) ||
+  if (!aligned(q_abs, 16) || !aligned(cache, 16) || !aligned(o_lat, 16) || !aligned(workspace, 32) ||
       !aligned(block_table, 4) || !aligned(qo_indptr, 4) || !aligned(kv_lens, 4) || !aligned(tree_mask, 8) ||
       !aligned(lse, 4) || !aligned(status, 4))
     return MLA_ERR_INVALID_ARG;

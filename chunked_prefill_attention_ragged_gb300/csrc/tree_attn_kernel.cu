@@ -1,87 +1,929 @@
 // Tree attention over the paged latent cache, absorbed-weight form, with every length on the
-// device: O_lat = softmax(sm_scale * q_abs . c^T) c[:, :512] and the per-row LSE.
+// device: O_lat = softmax(sm_scale * q_abs . c^T) c[:, :512] and the per-row LSE, where row
+// (node i, head h) of a request with n nodes and kv cached positions sees the positions below
+// kv - n and those of the nodes that its mask bits name.
 //
-// Plain form: one warp per (token, head), one key at a time.
+// What is computed follows sglang issue #3849 ("[DeepseekR1] How ragged prefill manage
+// kv_cache?"): every head attends to the compressed cache rows (512 latent + 64 rope, one KV
+// head), and the slot rule of vLLM "vllm/models/deepseek_v4/sparse_mla.py"
+// (_build_c128a_topk_metadata_kernel, decode branch).
+//
+// Mathematics.  A unit is 128 consecutive (node, head) pairs of one request.  Over tiles of 128
+// keys, with scores s in log2 units and a reference m per pair that follows the running maximum,
+//   P = 2^(s - m),  l += sum P,  O += P V;  when a maximum passes m + 8: O, l *= 2^(m - m').
+// A unit's tiles may be shared out to several workers; each leaves (O, m, l) in fp32 and the
+// second kernel joins them: with M = max m, O = sum 2^(m - M) O / sum 2^(m - M) l.
+//
+// Work split.  The tiles of all units, request by request, form one line that is cut into equal
+// pieces, one per worker (a cluster of two CTAs on two SMs).  The lengths are on the device, so
+// every worker finds its piece itself: a prefix sum over the requests.  A piece has at most two
+// parts that do not cover their unit (its first and its last), so the workspace has two slots
+// per worker.
+//
+// A cluster runs a unit with tcgen05 cta_group::2 products of M = 128, 64 pairs in each CTA: a
+// 64 x 512 fp32 accumulator then takes 256 TMEM columns (both lane halves are in use: lanes
+// 0-63 hold the first half of a product's columns for the 64 rows, lanes 64-127 the second),
+// which leaves room for two S buffers.  A single CTA with 128 rows has no room for S beside O and
+// would compute S once per half of the values.  Per CTA in shared memory: its Q rows (64 x 576),
+// its 64 of the tile's 128 keys as the half of S's B operand, the tile's 128 keys x its half of
+// the value columns as the half of P V's B operand, and P (64 x 128).
+//   warp 0     Q and K producer: Q once per unit; K in three groups of three 64-column panels
+//   warp 2     V producer: two 256-column chunks (128 of the columns here)
+//   warp 1     even CTA: issues every product; odd CTA: passes its Q/K arrivals on to the even
+//   warp 3     TMEM allocation; odd CTA: passes its V arrivals on
+//   warps 4-7  softmax: two threads per pair (the two halves of the keys and of O's columns)
+// Order of products: S(t + 1) before P V(t), so that the tensor cores work on the next tile while
+// the softmax does this one.  Key rows come by whole boxes where a 64-row piece lies inside the
+// request and the block size allows, else by gather4 with rows past the end read as zeros.
+// Every wait is bounded: on time-out the CTA records MLA_DEVSTAT_TIMEOUT, drains its copies and
+// products, frees TMEM and returns.
 #include <cuda_bf16.h>
+#include <cuda_runtime.h>
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "tmem_wide.cuh"
 
 namespace mla {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int ROWS = 128;               // pairs per unit, 64 in each CTA
+constexpr int KEYS = 128;               // keys per tile
+constexpr int QP = 64 * 128;            // a [64 rows, 64 columns] panel: 8 KB
+constexpr int NP = 9;                   // 64-column panels of 576
+constexpr int KGROUPS = 3;              // K panels arrive in groups of three
+constexpr int V_CHUNK = 4 * QP;         // [2 key halves][2 panels][64 keys][64 columns]
+constexpr int OFF_Q = 0;
+constexpr int OFF_K = OFF_Q + NP * QP;
+constexpr int OFF_V = OFF_K + NP * QP;
+constexpr int OFF_P = OFF_V + 2 * V_CHUNK;
+constexpr int OFF_XCHG = OFF_P + 2 * QP;            // [2 tiles][2 halves][64 rows] maxima
+constexpr int OFF_BAR = OFF_XCHG + 2 * 2 * 64 * 4;
+enum Bar {
+  QF = 0,              // Q landed
+  QE,                  // the unit's last S done: Q may be replaced
+  KF,                  // [group] K panels landed
+  KE = KF + KGROUPS,   // [group] their products done
+  VF = KE + KGROUPS,   // [chunk] V landed
+  VE = VF + 2,         // [chunk] its product done
+  SF = VE + 2,         // [buffer] S done
+  PR = SF + 2,         // P written (and the S buffer read) by every softmax warp of both CTAs
+  OD,                  // P V done
+  XB,                  // [row half] maxima exchanged between the two warps of 32 rows
+  FIN = XB + 2,        // every product drained
+  NEVER,               // nothing arrives here: the time-out test mode waits on it
+  NBAR
+};
+constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+constexpr int SMEM = OFF_MISC + 64 + 1024;   // + slack for 1024-byte alignment
+static_assert(SMEM <= 227 * 1024, "shared memory budget");
+constexpr int NTHREADS = 256;
+constexpr uint32_t TMEM_COLS = 512;
+__device__ __forceinline__ constexpr uint32_t TM_O(int chunk) { return (uint32_t)chunk * 128u; }
+__device__ __forceinline__ constexpr uint32_t TM_S(int b) { return 256u + (uint32_t)b * 64u; }
+constexpr uint32_t IDESC_QK = idesc_bf16_f32(ROWS, KEYS, false, false);
+constexpr uint32_t IDESC_PV = idesc_bf16_f32(ROWS, 256, false, true);
+constexpr uint64_t DRAIN_LIMIT_NS = 200000000ull;
+constexpr float RESCALE_THRESHOLD = 8.0f;
+constexpr int MIN_TILES = 2;            // fewer tiles than this are not worth another worker
 
-__global__ void __launch_bounds__(kWarps * 32) tree_attn_simple(const TreeParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t pair = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (pair >= p.total_rows * p.num_heads) return;
-  const int64_t t = pair / p.num_heads;
-  if (t >= p.qo_indptr[p.batch]) return;
-  int lo = 0, hi = p.batch;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (p.qo_indptr[mid] <= t) lo = mid; else hi = mid;
+// Workspace: header, one record per worker (where its piece starts), two slots per worker.
+struct Header {
+  int64_t total;       // tiles of all units
+  int workers;         // that share them
+  int pad;
+};
+struct StartRec {
+  int req, unit, tile, pad;
+};
+constexpr int MAX_WORKERS = 256;
+constexpr size_t WS_STARTS = 64;
+constexpr size_t WS_SLOTS = (WS_STARTS + MAX_WORKERS * sizeof(StartRec) + 255) / 256 * 256;
+constexpr size_t SLOT_ML = (size_t)ROWS * 512 * 4;
+constexpr size_t SLOT_BYTES = SLOT_ML + ROWS * 2 * 4;
+
+struct Params {
+  TreeParams t;
+  int workers;
+  int32_t oob_row;     // a row coordinate past the cache: the copy fills it with zeros
+  int piece_rows;      // rows of one box of the block map (0: gather4 only)
+  int grouped;         // 64-row boxes over several panels (the three-dimensional maps)
+  int o_align32;
+  int has_cap;
+  float scale_log2, cap_log2, cap_ex2_scale;
+  uint64_t wait_limit_ns;
+  int force_timeout;
+};
+
+struct Ctx {
+  uint32_t sbase;
+  volatile int* abort_flag;
+  int* status;
+  uint64_t wait_limit_ns;
+  uint32_t rank;
+  __device__ uint32_t bar(int i) const { return sbase + OFF_BAR + 8 * i; }
+  __device__ bool wait(int b, uint32_t parity) const {
+    return mbar_wait_bounded(bar(b), parity, abort_flag, status, MLA_DEVSTAT_TIMEOUT, wait_limit_ns);
   }
-  const int r = lo;
-  const int n = p.qo_indptr[r + 1] - p.qo_indptr[r], i = (int)(t - p.qo_indptr[r]);
-  if (i < 0 || i >= n) return;
-  if (p.qo_indptr[r] < 0 || p.qo_indptr[r + 1] > p.total_rows) {
-    if (lane == 0 && p.status) atomicOr(p.status, MLA_DEVSTAT_BAD_INDEX);
+  // For the even CTA's barriers that threads of the odd one arrive on: acquire at cluster scope.
+  __device__ bool wait_pair(int b, uint32_t parity) const {
+    return mbar_wait_bounded(bar(b), parity, abort_flag, status, MLA_DEVSTAT_TIMEOUT, wait_limit_ns, true);
+  }
+  __device__ void drain(int b, uint32_t parity) const {
+    int dummy = 0;
+    mbar_wait_bounded(bar(b), parity, &dummy, status, MLA_DEVSTAT_TIMEOUT, DRAIN_LIMIT_NS, true);
+  }
+  __device__ void commit_both(int b) const {
+    tc_commit_pair(bar(b));
+    tc_commit_pair(mapa_shared(bar(b), 1));
+  }
+};
+
+// One request as the kernel sees it.
+struct Req {
+  int q0, nodes;       // rows; 0 nodes when the request is empty or refused
+  int64_t ctx;         // positions every node sees (negative: the first nodes are not cached)
+  int kv;              // positions that may be read
+  int units, tiles;
+};
+
+__device__ __forceinline__ Req load_req(const TreeParams& p, int r, bool report) {
+  Req q;
+  const int q0 = __ldg(p.qo_indptr + r), q1 = __ldg(p.qo_indptr + r + 1), len = __ldg(p.kv_lens + r);
+  const int64_t reach = (int64_t)p.max_blocks * p.block_size;
+  const bool rows_ok = q0 >= 0 && q1 >= q0 && q1 <= p.total_rows;
+  const bool len_ok = len >= 0 && len <= reach;
+  if (report && p.status && (!rows_ok || !len_ok)) atomicOr(p.status, MLA_DEVSTAT_BAD_INDEX);
+  q.q0 = q0;
+  q.nodes = rows_ok ? q1 - q0 : 0;
+  q.ctx = (int64_t)len - q.nodes;
+  q.kv = len_ok ? len : (len < 0 ? 0 : (int)reach);
+  q.units = (int)(((int64_t)q.nodes * p.num_heads + ROWS - 1) / ROWS);
+  q.tiles = q.units ? max(1, (q.kv + KEYS - 1) / KEYS) : 0;
+  return q;
+}
+
+// A part of a worker's piece: tiles [lo, hi) of one unit.
+struct Part {
+  Req q;
+  int r;
+  int64_t pair0;       // first pair of the unit, counted over the batch
+  int npairs;
+  int lo, hi;
+  bool whole;          // the unit's every tile
+  int slot;            // 0: the worker's first part, 1: a later one (its last, if not whole)
+};
+
+struct Parts {
+  const TreeParams& p;
+  int64_t left;
+  int r, unit, tile, index;
+  Req q;
+  __device__ Parts(const TreeParams& tp, const StartRec& s, int64_t count)
+      : p(tp), left(count), r(s.req), unit(s.unit), tile(s.tile), index(0) {
+    if (left > 0) q = load_req(p, r, false);
+  }
+  __device__ bool next(Part* out) {
+    if (left <= 0) return false;
+    while (unit >= q.units) {   // to the next request that has rows
+      if (++r >= p.batch) return false;   // (lengths changed under the kernel: out of bounds is not read)
+      unit = 0;
+      q = load_req(p, r, false);
+    }
+    const int n = (int)min((int64_t)(q.tiles - tile), left);
+    out->q = q;
+    out->r = r;
+    const int64_t first = (int64_t)unit * ROWS;
+    out->pair0 = (int64_t)q.q0 * p.num_heads + first;
+    out->npairs = (int)min((int64_t)ROWS, (int64_t)q.nodes * p.num_heads - first);
+    out->lo = tile;
+    out->hi = tile + n;
+    out->whole = n == q.tiles;
+    out->slot = index == 0 ? 0 : 1;
+    ++index;
+    left -= n;
+    tile = 0;
+    ++unit;
+    return true;
+  }
+};
+
+// Cache row of key position `key`; past the readable ones, or in a block that the table does
+// not name, the row past the cache (read as zeros), the latter flagged.
+__device__ __forceinline__ int32_t key_row(const Params& p, const Part& u, int64_t key) {
+  if (key >= u.q.kv) return p.oob_row;
+  const int k = (int)key, bi = k / p.t.block_size;
+  const int32_t blk = __ldg(p.t.block_table + (int64_t)u.r * p.t.max_blocks + bi);
+  if (blk < 0 || (int64_t)blk >= p.t.num_blocks) {
+    if (p.t.status) atomicOr(p.t.status, MLA_DEVSTAT_BAD_INDEX);
+    return p.oob_row;
+  }
+  return (int32_t)((int64_t)blk * p.t.block_size + (k - bi * p.t.block_size));
+}
+
+// The rows of 64 keys from `key0` on, spread over the lanes, and how they are copied.
+struct KeyRows {
+  bool by_block;
+  int32_t piece;       // lane k: row of piece k
+  int32_t r4[4];       // lanes 0-15: rows of keys 4 lane .. 4 lane + 3
+};
+__device__ __forceinline__ KeyRows find_rows(const Params& p, const Part& u, int64_t key0, int lane) {
+  KeyRows k;
+  const int pieces = p.piece_rows > 0 ? 64 / p.piece_rows : 0;
+  k.by_block = pieces > 0 && key0 + 64 <= u.q.kv;
+  k.piece = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) k.r4[j] = 0;
+  if (k.by_block) {
+    if (lane < pieces) k.piece = key_row(p, u, key0 + lane * p.piece_rows);
+  } else if (lane < 16) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) k.r4[j] = key_row(p, u, key0 + 4 * lane + j);
+  }
+  return k;
+}
+
+// 64 keys x panels [panel0, panel0 + n) to n consecutive 8 KB panels at dst.  tg: the map whose
+// boxes hold exactly n panels.
+__device__ __forceinline__ void copy_panels(const Params& p, const KeyRows& k, uint32_t dst, uint32_t bar,
+                                            const CUtensorMap* tc, const CUtensorMap* tb, const CUtensorMap* tg,
+                                            int panel0, int n, int lane) {
+  if (k.by_block && p.grouped) {
+    if (lane == 0) tma_load_3d(dst, tg, bar, 0, k.piece, panel0);
     return;
   }
-  const int64_t reach = (int64_t)p.max_blocks * p.block_size;
-  int64_t kv = p.kv_lens[r];
-  const int64_t ctx = kv - n;
-  if (kv < 0 || kv > reach) {
-    if (lane == 0 && p.status) atomicOr(p.status, MLA_DEVSTAT_BAD_INDEX);
-    kv = kv < 0 ? 0 : reach;
-  }
-  const __nv_bfloat162* q = reinterpret_cast<const __nv_bfloat162*>(p.q + pair * 576);
-  float2 qv[9], acc[8];
-  for (int k = 0; k < 9; ++k) qv[k] = __bfloat1622float2(q[lane + 32 * k]);
-  for (int k = 0; k < 8; ++k) acc[k] = make_float2(0.f, 0.f);
-  float m = -INFINITY, l = 0.f;
-  for (int64_t pos = 0; pos < kv; ++pos) {
-    if (pos >= ctx) {
-      const int64_t j = pos - ctx;
-      bool seen = j <= i;
-      if (p.mask) seen = (j >> 6) < p.mask_words && ((p.mask[t * p.mask_words + (j >> 6)] >> (j & 63)) & 1);
-      if (!seen) continue;
+  for (int i = 0; i < n; ++i) {
+    const int col = (panel0 + i) * 64;
+    if (k.by_block) {
+      if (lane * p.piece_rows < 64) tma_load_2d(dst + i * QP + lane * p.piece_rows * 128, tb, bar, col, k.piece);
+    } else if (lane < 16) {
+      tma_gather4(dst + i * QP + lane * 4 * 128, tc, bar, col, k.r4[0], k.r4[1], k.r4[2], k.r4[3]);
     }
-    const int64_t blk = p.block_table[(int64_t)r * p.max_blocks + pos / p.block_size];
-    float2 kvv[9];
-    if (blk < 0 || blk >= p.num_blocks) {
-      if (lane == 0 && p.status) atomicOr(p.status, MLA_DEVSTAT_BAD_INDEX);
-      for (int k = 0; k < 9; ++k) kvv[k] = make_float2(0.f, 0.f);
-    } else {
-      const __nv_bfloat162* c =
-          reinterpret_cast<const __nv_bfloat162*>(p.cache + (blk * p.block_size + pos % p.block_size) * 576);
-      for (int k = 0; k < 9; ++k) kvv[k] = __bfloat1622float2(c[lane + 32 * k]);
-    }
-    float s = 0.f;
-    for (int k = 0; k < 9; ++k) s += qv[k].x * kvv[k].x + qv[k].y * kvv[k].y;
-    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    s *= p.sm_scale;
-    if (p.soft_cap > 0.f) s = p.soft_cap * tanhf(s / p.soft_cap);
-    const float mn = fmaxf(m, s), a = expf(m - mn), e = expf(s - mn);
-    l = l * a + e;
-    for (int k = 0; k < 8; ++k) acc[k] = make_float2(acc[k].x * a + e * kvv[k].x, acc[k].y * a + e * kvv[k].y);
-    m = mn;
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  __nv_bfloat162* o = reinterpret_cast<__nv_bfloat162*>(p.o + pair * 512);
-  for (int k = 0; k < 8; ++k) o[lane + 32 * k] = __floats2bfloat162_rn(acc[k].x * inv, acc[k].y * inv);
-  if (lane == 0 && p.lse) p.lse[pair] = l > 0.f ? m + logf(l) : -INFINITY;
+}
+
+// ------------------------------------------------------------------ producers
+__device__ void run_producer_qk(const Ctx& c, const Params& p, Parts parts, const CUtensorMap* tq,
+                                const CUtensorMap* tc, const CUtensorMap* tb, const CUtensorMap* t3) {
+  const int lane = threadIdx.x & 31;
+  int tiles = 0, units = 0, q_issued = 0, k_issued[KGROUPS] = {0, 0, 0};
+  bool ok = true;
+  Part u;
+  while (ok && parts.next(&u)) {
+    int go = 1;
+    if (lane == 0) {
+      if (units > 0) go = c.wait(QE, (units - 1) & 1);
+      if (go) {
+        mbar_arrive_expect_tx(c.bar(QF), NP * QP);
+        for (int i = 0; i < NP; ++i)
+          tma_load_2d(c.sbase + OFF_Q + i * QP, tq, c.bar(QF), i * 64, (int32_t)(u.pair0 + 64 * c.rank));
+      }
+    }
+    if (!__shfl_sync(0xffffffffu, go, 0)) break;
+    ++units;
+    ++q_issued;
+    for (int t = u.lo; t < u.hi && ok; ++t, ++tiles) {
+      const KeyRows k = find_rows(p, u, (int64_t)t * KEYS + 64 * c.rank, lane);
+      for (int g = 0; g < KGROUPS; ++g) {
+        int free = 1;
+        if (lane == 0 && tiles > 0) free = c.wait(KE + g, (tiles - 1) & 1);
+        if (!__shfl_sync(0xffffffffu, free, 0)) { ok = false; break; }
+        if (lane == 0) mbar_arrive_expect_tx(c.bar(KF + g), 3 * QP);
+        __syncwarp();
+        copy_panels(p, k, c.sbase + OFF_K + 3 * g * QP, c.bar(KF + g), tc, tb, t3, 3 * g, 3, lane);
+        ++k_issued[g];
+      }
+    }
+  }
+  // Let every copy started here land before the CTA can exit.
+  if (lane == 0) {
+    if (q_issued) c.drain(QF, (q_issued - 1) & 1);
+    for (int g = 0; g < KGROUPS; ++g)
+      if (k_issued[g]) c.drain(KF + g, (k_issued[g] - 1) & 1);
+  }
+}
+
+__device__ void run_producer_v(const Ctx& c, const Params& p, Parts parts, const CUtensorMap* tc,
+                               const CUtensorMap* tb, const CUtensorMap* t2) {
+  const int lane = threadIdx.x & 31;
+  int tiles = 0, issued[2] = {0, 0};
+  bool ok = true;
+  Part u;
+  while (ok && parts.next(&u)) {
+    for (int t = u.lo; t < u.hi && ok; ++t, ++tiles) {
+      const KeyRows k0 = find_rows(p, u, (int64_t)t * KEYS, lane);
+      const KeyRows k1 = find_rows(p, u, (int64_t)t * KEYS + 64, lane);
+      for (int j = 0; j < 2; ++j) {
+        int free = 1;
+        if (lane == 0 && tiles > 0) free = c.wait(VE + j, (tiles - 1) & 1);
+        if (!__shfl_sync(0xffffffffu, free, 0)) { ok = false; break; }
+        if (lane == 0) mbar_arrive_expect_tx(c.bar(VF + j), V_CHUNK);
+        __syncwarp();
+        const uint32_t dst = c.sbase + OFF_V + j * V_CHUNK;
+        const int panel = 4 * j + 2 * (int)c.rank;
+        copy_panels(p, k0, dst, c.bar(VF + j), tc, tb, t2, panel, 2, lane);
+        copy_panels(p, k1, dst + 2 * QP, c.bar(VF + j), tc, tb, t2, panel, 2, lane);
+        ++issued[j];
+      }
+    }
+  }
+  if (lane == 0)
+    for (int j = 0; j < 2; ++j)
+      if (issued[j]) c.drain(VF + j, (issued[j] - 1) & 1);
+}
+
+// The odd CTA's arrivals, passed on to the even CTA's barriers of the same name.
+__device__ void run_forward_qk(const Ctx& c, Parts parts) {
+  int tiles = 0, units = 0;
+  Part u;
+  while (parts.next(&u)) {
+    if (!c.wait(QF, units & 1)) return;
+    mbar_arrive_remote(mapa_shared(c.bar(QF), 0));
+    ++units;
+    for (int t = u.lo; t < u.hi; ++t, ++tiles)
+      for (int g = 0; g < KGROUPS; ++g) {
+        if (!c.wait(KF + g, tiles & 1)) return;
+        mbar_arrive_remote(mapa_shared(c.bar(KF + g), 0));
+      }
+  }
+}
+__device__ void run_forward_v(const Ctx& c, Parts parts) {
+  int tiles = 0;
+  Part u;
+  while (parts.next(&u))
+    for (int t = u.lo; t < u.hi; ++t, ++tiles)
+      for (int j = 0; j < 2; ++j) {
+        if (!c.wait(VF + j, tiles & 1)) return;
+        mbar_arrive_remote(mapa_shared(c.bar(VF + j), 0));
+      }
+}
+
+// ------------------------------------------------------------------ products (even CTA, warp 1)
+__device__ void run_mma(const Ctx& c, const Params& p, Parts parts, uint32_t tmem) {
+  const uint64_t q_desc = sdesc_sw128(c.sbase + OFF_Q, 16, 1024);
+  const uint64_t k_desc = sdesc_sw128(c.sbase + OFF_K, 16, 1024);
+  const uint64_t v_desc = sdesc_sw128(c.sbase + OFF_V, QP, 1024);
+  const uint64_t p_desc = sdesc_sw128(c.sbase + OFF_P, 16, 1024);
+  bool ok = true;
+  if (p.force_timeout) ok = c.wait(NEVER, 0);
+  int st = 0, units = 0;   // S tiles issued
+  auto s_products = [&](bool last) {
+    const int b = st & 1;
+    for (int g = 0; g < KGROUPS; ++g) {
+      if (!c.wait_pair(KF + g, st & 1)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int i = 0; i < 12; ++i) {
+        const uint64_t off = (uint64_t)(((3 * g + (i >> 2)) * QP + (i & 3) * 32) >> 4);
+        mma_ss_pair(tmem + TM_S(b), q_desc + off, k_desc + off, IDESC_QK, (g > 0 || i > 0) ? 1u : 0u);
+      }
+      c.commit_both(KE + g);
+    }
+    c.commit_both(SF + b);
+    if (last) c.commit_both(QE);
+    ++st;
+    return true;
+  };
+  auto pv_products = [&](int t, bool first) {
+    if (!c.wait_pair(PR, t & 1)) return false;
+    for (int j = 0; j < 2; ++j) {
+      if (!c.wait_pair(VF + j, t & 1)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < KEYS / 16; ++kk) {
+        const uint64_t po = (uint64_t)(((kk >> 2) * QP + (kk & 3) * 32) >> 4);
+        const uint64_t vo = (uint64_t)((j * V_CHUNK + (kk >> 2) * 2 * QP + (kk & 3) * 16 * 128) >> 4);
+        mma_ss_pair(tmem + TM_O(j), p_desc + po, v_desc + vo, IDESC_PV, (!first || kk > 0) ? 1u : 0u);
+      }
+      c.commit_both(VE + j);
+    }
+    c.commit_both(OD);
+    return true;
+  };
+  int pv = 0;   // S runs one tile ahead of P V
+  Part u;
+  while (ok && parts.next(&u)) {
+    ok = c.wait_pair(QF, units & 1);
+    ++units;
+    for (int t = u.lo; t < u.hi && ok; ++t) {
+      // S's buffer held P V(pv - 2)'s scores, read before that tile's P was ready.
+      ok = s_products(t == u.hi - 1);
+      if (ok && t > u.lo) ok = pv_products(pv++, t - 1 == u.lo);
+    }
+    // (The next part's Q is only loaded now that S is done: P V does not wait for it.)
+    if (ok) ok = pv_products(pv++, u.hi - u.lo == 1);
+  }
+  tc_commit_pair(c.bar(FIN));
+  c.drain(FIN, 0);
+}
+
+// ------------------------------------------------------------------ softmax (warps 4-7)
+// Visibility of 64 keys from position pos0 on for node i (row t of the batch), bit k for key k.
+__device__ __forceinline__ uint64_t visible(const TreeParams& p, const Part& u, int i, int64_t pos0) {
+  auto window = [&](int64_t j0) -> uint64_t {   // nodes j0 .. j0 + 63, j0 >= 0
+    if (!p.mask) {
+      const int64_t n = (int64_t)i - j0 + 1;
+      return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
+    }
+    const int64_t* row = p.mask + ((int64_t)u.q.q0 + i) * p.mask_words;
+    const int64_t w = j0 >> 6;
+    const int sh = (int)(j0 & 63);
+    uint64_t bits = w < p.mask_words ? (uint64_t)__ldg(row + w) >> sh : 0ull;
+    if (sh && w + 1 < p.mask_words) bits |= (uint64_t)__ldg(row + w + 1) << (64 - sh);
+    return bits;
+  };
+  const int64_t s = pos0 - u.q.ctx;   // node index of the first key
+  uint64_t v;
+  if (s <= -64) v = ~0ull;
+  else if (s >= 0) v = window(s);
+  else v = ((1ull << -s) - 1) | (window(0) << -s);
+  const int64_t room = u.q.kv - pos0;
+  if (room < 64) v &= room <= 0 ? 0ull : (1ull << room) - 1;
+  return v;
+}
+
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void st_shared_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+// Arrive on a barrier of another CTA of the cluster, releasing this thread's (and, after a
+// __syncwarp, its warp's) shared-memory writes at cluster scope.
+__device__ __forceinline__ void arrive_release_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+__device__ void run_softmax(const Ctx& c, const Params& p, Parts parts, uint32_t tmem, char* ws_slots, uint8_t* smem) {
+  const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3;
+  const int half = q4 >> 1, rg = q4 & 1;             // key / column half, group of 32 rows
+  const int row = 32 * rg + lane;                    // of the CTA's 64
+  const uint32_t lane_addr = tmem + ((uint32_t)(q4 * 32) << 16);
+  float* xchg = reinterpret_cast<float*>(smem + OFF_XCHG);
+  const uint32_t p_row = c.sbase + OFF_P + half * QP + row * 128;
+  const uint32_t pr_bar = c.rank ? mapa_shared(c.bar(PR), 0) : c.bar(PR);
+  const float NEG_INF = -__int_as_float(0x7f800000);
+  const float sc = p.has_cap ? 1.f : p.scale_log2;
+  const float2 sc2 = make_float2(sc, sc);
+  bool ok = true;
+  int g = 0, xs = 0;   // tiles and exchanges so far
+  // Swap a value with the thread that has the row's other half.  Two buffers in turn: the
+  // partner read this one's last contents before it arrived for the exchange between.
+  auto exchange = [&](float mine, float* theirs) {
+    float* buf = xchg + (xs & 1) * 128;
+    buf[half * 64 + row] = mine;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(c.bar(XB + rg));
+    if (!__all_sync(0xffffffffu, c.wait(XB + rg, xs & 1))) return false;
+    *theirs = buf[(half ^ 1) * 64 + row];
+    ++xs;
+    return true;
+  };
+  Part u;
+  while (ok && parts.next(&u)) {
+    const int pr0 = 64 * (int)c.rank + row;          // pair inside the unit
+    const bool live = pr0 < u.npairs;
+    const int64_t pair = u.pair0 + pr0;
+    // A row without a pair computes on something harmless: the last node's mask.
+    const int node = min((int)((pair - (int64_t)u.q.q0 * p.t.num_heads) / p.t.num_heads), u.q.nodes - 1);
+    float m_used = NEG_INF, l = 0.f;
+    for (int t = u.lo; t < u.hi; ++t, ++g) {
+      const int sb = g & 1;
+      if (!__all_sync(0xffffffffu, c.wait(SF + sb, (g >> 1) & 1))) { ok = false; break; }
+      tc_fence_after();
+      float sv[64];
+      tmem_ld64_sync(lane_addr + TM_S(sb), reinterpret_cast<uint32_t*>(sv));
+      if (p.has_cap) {
+        // c * tanh(sm_scale * x / c) in log2 units, from tanh(y) = 1 - 2 / (e^(2y) + 1).
+        const float2 k2 = make_float2(p.cap_ex2_scale, p.cap_ex2_scale);
+        const float2 one = make_float2(1.f, 1.f);
+        const float2 m2c = make_float2(-2.f * p.cap_log2, -2.f * p.cap_log2);
+        const float2 c2 = make_float2(p.cap_log2, p.cap_log2);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const float2 a = fmul2(make_float2(sv[2 * k], sv[2 * k + 1]), k2);
+          const float2 d = fadd2(make_float2(ex2_approx(a.x), ex2_approx(a.y)), one);
+          const float2 r = ffma2(make_float2(rcp_approx(d.x), rcp_approx(d.y)), m2c, c2);
+          sv[2 * k] = r.x;
+          sv[2 * k + 1] = r.y;
+        }
+      }
+      const int64_t pos0 = (int64_t)t * KEYS + 64 * half;
+      if (pos0 + 64 > min(u.q.ctx, (int64_t)u.q.kv)) {   // nodes, or the end of the keys
+        const uint64_t v = visible(p.t, u, node, pos0);
+#pragma unroll
+        for (int k = 0; k < 64; ++k)
+          if (!((v >> k) & 1)) sv[k] = NEG_INF;
+      }
+      float mx[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        mx[k] = fmax3(fmax3(sv[8 * k], sv[8 * k + 1], sv[8 * k + 2]),
+                      fmax3(sv[8 * k + 3], sv[8 * k + 4], sv[8 * k + 5]), fmaxf(sv[8 * k + 6], sv[8 * k + 7]));
+      float mt = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * sc;
+      // The row's other thread has the other 64 keys.
+      float other;
+      if (!exchange(mt, &other)) { ok = false; break; }
+      mt = fmaxf(mt, other);
+      float m_new = m_used;
+      bool rescale = false;
+      if (t == u.lo) {
+        m_new = mt;
+      } else if (mt > m_used + RESCALE_THRESHOLD) {
+        m_new = mt;
+        rescale = true;
+      }
+      const float msub = (m_new == NEG_INF) ? 0.f : m_new;
+      const float2 neg_m = make_float2(-msub, -msub);
+      float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      uint32_t pr[32];
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        const float2 a = ffma2(make_float2(sv[2 * k], sv[2 * k + 1]), sc2, neg_m);
+        const float2 e = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+        acc[k & 3] = fadd2(acc[k & 3], e);
+        pr[k] = pack_bf16x2(e.x, e.y);   // the operand type; the sum is of the unrounded values
+      }
+      const float2 s01 = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
+      const float sum = s01.x + s01.y;
+      float alpha = 1.f;
+      if (rescale) alpha = ex2_approx(m_used - m_new);
+      l = l * alpha + sum;
+      // The tile before this one has to be done with P, and with O if it is rescaled.
+      if (g > 0 && !__all_sync(0xffffffffu, c.wait(OD, (g - 1) & 1))) { ok = false; break; }
+      if (__any_sync(0xffffffffu, rescale)) {   // tcgen05.ld/st are warp-collective
+        tc_fence_after();
+        const float2 a2 = make_float2(alpha, alpha);
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          float ov[64];
+          tmem_ld64_sync(lane_addr + q * 64, reinterpret_cast<uint32_t*>(ov));
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const float2 r = fmul2(make_float2(ov[2 * k], ov[2 * k + 1]), a2);
+            ov[2 * k] = r.x;
+            ov[2 * k + 1] = r.y;
+          }
+          tmem_st64_sync(lane_addr + q * 64, reinterpret_cast<uint32_t*>(ov));
+        }
+      }
+      m_used = m_new;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        st_shared_v4(p_row + ((k ^ (row & 7)) << 4), pr[4 * k], pr[4 * k + 1], pr[4 * k + 2], pr[4 * k + 3]);
+      fence_async_shared();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (c.rank) arrive_release_cluster(pr_bar);
+        else mbar_arrive(pr_bar);
+      }
+    }
+    if (!ok) break;
+    // The part's end: the row's sum, then O out of TMEM once the last product is done.
+    float l_other;
+    if (!exchange(l, &l_other)) break;
+    const float l_row = l + l_other;
+    if (!__all_sync(0xffffffffu, c.wait(OD, (g - 1) & 1))) break;
+    tc_fence_after();
+    const bool empty = !(l_row > 0.f);
+    const float inv = u.whole ? (empty ? 0.f : 1.f / l_row) : 1.f;
+    const float2 inv2 = make_float2(inv, inv);
+    char* slot = ws_slots + (size_t)u.slot * SLOT_BYTES;
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+      // TMEM columns 64 q ..: value columns 256 (q / 2) + 128 half + 64 (q % 2) ..
+      const int col = 256 * (q >> 1) + 128 * half + 64 * (q & 1);
+      uint32_t ov[64];
+      tmem_ld64_sync(lane_addr + q * 64, ov);
+      if (!live) continue;
+      if (u.whole) {
+        uint32_t w[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const float2 r = fmul2(make_float2(__uint_as_float(ov[2 * k]), __uint_as_float(ov[2 * k + 1])), inv2);
+          w[k] = empty ? 0u : pack_bf16x2(r.x, r.y);
+        }
+        __nv_bfloat16* d = p.t.o + pair * 512 + col;
+        if (p.o_align32) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) st_global_v8(d + 16 * k, w + 8 * k);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            reinterpret_cast<uint4*>(d)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        }
+      } else {
+        float* d = reinterpret_cast<float*>(slot) + (size_t)pr0 * 512 + col;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) st_global_v8(d + 8 * k, ov + 8 * k);
+      }
+    }
+    if (live && half == 0) {
+      if (u.whole) {
+        float lg;
+        asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(l_row));
+        if (p.t.lse) p.t.lse[pair] = empty ? NEG_INF : (m_used + lg) * 0.6931471805599453f;
+      } else {
+        reinterpret_cast<float2*>(slot + SLOT_ML)[pr0] = make_float2(m_used, l_row);
+      }
+    }
+    tc_fence_before();   // O has been read: the next part's first P-ready lets it be overwritten
+  }
+}
+
+// Where worker w's piece starts, and how long it is; every thread of the CTA calls.
+__device__ void find_piece(const TreeParams& p, int worker, int workers, bool report, StartRec* start,
+                           int64_t* count, Header* head) {
+  __shared__ int64_t warp_sum[NTHREADS / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.batch + NTHREADS - 1) / NTHREADS;
+  const int r0 = min(tid * per, p.batch), r1 = min(r0 + per, p.batch);
+  int64_t mine = 0;
+  for (int r = r0; r < r1; ++r) {
+    const Req q = load_req(p, r, report);
+    mine += (int64_t)q.units * q.tiles;
+  }
+  int64_t incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  int64_t before = incl - mine, total = 0;
+  for (int w = 0; w < NTHREADS / 32; ++w) {
+    if (w < warp) before += warp_sum[w];
+    total += warp_sum[w];
+  }
+  const int n = (int)min((int64_t)workers, (total + MIN_TILES - 1) / MIN_TILES);
+  const int64_t lo = worker < n ? total * worker / n : total, hi = worker < n ? total * (worker + 1) / n : total;
+  if (tid == 0) {
+    *count = hi - lo;
+    *head = Header{total, n, 0};
+  }
+  if (lo < hi && lo >= before && lo < before + mine) {
+    int64_t at = before;
+    for (int r = r0; r < r1; ++r) {
+      const Req q = load_req(p, r, false);
+      const int64_t k = (int64_t)q.units * q.tiles;
+      if (lo < at + k) {
+        *start = StartRec{r, (int)((lo - at) / q.tiles), (int)((lo - at) % q.tiles), 0};
+        break;
+      }
+      at += k;
+    }
+  }
+  __syncthreads();
+}
+
+__global__ void __launch_bounds__(NTHREADS, 1)
+tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_c,
+                 const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_2,
+                 const __grid_constant__ CUtensorMap tm_3, const __grid_constant__ Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ StartRec start;
+  __shared__ int64_t count;
+  __shared__ Header head;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
+  int* abort_flag = reinterpret_cast<int*>(smem + OFF_MISC + 4);
+  const uint32_t rank = cluster_ctarank();
+  const int worker = blockIdx.x >> 1;
+  const Ctx c{smem_addr(smem), abort_flag, p.t.status, p.wait_limit_ns, rank};
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NBAR; ++i) mbar_init(c.bar(i), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(c.bar(XB + i), 2);      // the two warps of 32 rows
+    mbar_init(c.bar(PR), rank == 0 ? 8 : 4);                       // every softmax warp, of both CTAs
+    if (rank == 0) {   // own load (with its bytes) and the odd CTA's forwarded arrival
+      mbar_init(c.bar(QF), 2);
+      for (int i = 0; i < KGROUPS; ++i) mbar_init(c.bar(KF + i), 2);
+      for (int i = 0; i < 2; ++i) mbar_init(c.bar(VF + i), 2);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_c);
+    if (p.piece_rows > 0) tma_prefetch_desc(&tm_b);
+    if (p.grouped) {
+      tma_prefetch_desc(&tm_2);
+      tma_prefetch_desc(&tm_3);
+    }
+  }
+  if (warp == 3) {   // one warp of each CTA of the pair, together
+    tmem_alloc_pair(smem_addr(tmem_slot), TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  find_piece(p.t, worker, p.workers, blockIdx.x == 0, &start, &count, &head);
+  char* ws = static_cast<char*>(p.t.workspace);
+  if (threadIdx.x == 0 && rank == 0) {
+    if (worker == 0) *reinterpret_cast<Header*>(ws) = head;
+    if (count > 0) reinterpret_cast<StartRec*>(ws + WS_STARTS)[worker] = start;
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // both CTAs' barriers exist before any remote arrival
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Parts parts(p.t, start, count);
+  if (warp == 0) {
+    run_producer_qk(c, p, parts, &tm_q, &tm_c, &tm_b, &tm_3);
+  } else if (warp == 2) {
+    run_producer_v(c, p, parts, &tm_c, &tm_b, &tm_2);
+  } else if (warp == 1) {
+    if (lane == 0) {
+      if (rank == 0) run_mma(c, p, parts, tmem);
+      else run_forward_qk(c, parts);
+    }
+  } else if (warp == 3) {
+    if (lane == 0 && rank != 0) run_forward_v(c, parts);
+  } else {
+    run_softmax(c, p, parts, tmem, ws + WS_SLOTS + (size_t)worker * 2 * SLOT_BYTES, smem);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  // Neither CTA leaves (freeing shared memory and TMEM) while the even CTA's products may still
+  // read or write the other's.
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 3) {
+    __syncwarp();
+    tmem_dealloc_pair(tmem, TMEM_COLS);
+  }
+}
+
+// ------------------------------------------------------------------ join
+// One CTA per eight rows of a unit that a boundary between two workers cuts; the unit's first
+// such boundary does it.  A warp has a row: the parts' (m, l) one per lane, then their O rows,
+// 16 columns per lane.
+constexpr int JOIN_WARPS = 8;
+
+__global__ void __launch_bounds__(JOIN_WARPS * 32) tree_join_kernel(const __grid_constant__ Params p) {
+  const char* ws = static_cast<const char*>(p.t.workspace);
+  const Header head = *reinterpret_cast<const Header*>(ws);
+  const int b = blockIdx.x + 1;   // the boundary before worker b
+  if (b >= head.workers) return;
+  const StartRec s = reinterpret_cast<const StartRec*>(ws + WS_STARTS)[b];
+  if (s.tile == 0) return;        // between two units
+  auto lo = [&](int w) { return head.total * w / head.workers; };
+  const int64_t a = lo(b) - s.tile;
+  if (lo(b - 1) > a) return;      // an earlier boundary cuts the same unit
+  const Req q = load_req(p.t, s.req, false);
+  const int64_t end = a + q.tiles;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.y * JOIN_WARPS + warp;
+  const int64_t first = (int64_t)s.unit * ROWS;
+  if (first + row >= (int64_t)q.nodes * p.t.num_heads) return;
+  const int64_t pair = (int64_t)q.q0 * p.t.num_heads + first + row;
+  int n = 1;                      // workers b - 1, b, .. that have a part
+  while (b + n - 1 < head.workers && lo(b + n - 1) < end) ++n;
+  const char* slots = ws + WS_SLOTS;
+  // Part k belongs to worker b - 1 + k: its first part, except that worker b - 1 may have begun
+  // with another unit.
+  auto slot = [&](int k) { return slots + (size_t)(2 * (b - 1 + k) + (k == 0 && lo(b - 1) < a ? 1 : 0)) * SLOT_BYTES; };
+  const float NEG_INF = -__int_as_float(0x7f800000);
+  float m = NEG_INF;
+  for (int k = lane; k < n; k += 32) m = fmaxf(m, reinterpret_cast<const float2*>(slot(k) + SLOT_ML)[row].x);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  const float mref = m == NEG_INF ? 0.f : m;
+  float4 o[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+  for (int k0 = 0; k0 < n; k0 += 32) {
+    float w = 0.f, wl = 0.f;
+    if (k0 + lane < n) {
+      const float2 ml = reinterpret_cast<const float2*>(slot(k0 + lane) + SLOT_ML)[row];
+      w = ex2_approx(ml.x - mref);
+      wl = w * ml.y;
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) wl += __shfl_xor_sync(0xffffffffu, wl, d);
+    l += wl;
+    const int here = min(32, n - k0);
+#pragma unroll 4
+    for (int k = 0; k < here; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      const float4* src = reinterpret_cast<const float4*>(slot(k0 + k)) + (size_t)row * 128 + lane;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 x = src[32 * i];
+        o[i].x += wk * x.x;
+        o[i].y += wk * x.y;
+        o[i].z += wk * x.z;
+        o[i].w += wk * x.w;
+      }
+    }
+  }
+  const bool empty = !(l > 0.f);
+  const float inv = empty ? 0.f : 1.f / l;
+  uint2* d = reinterpret_cast<uint2*>(p.t.o + pair * 512) + lane;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    d[32 * i] = empty ? make_uint2(0u, 0u)
+                      : make_uint2(pack_bf16x2(o[i].x * inv, o[i].y * inv), pack_bf16x2(o[i].z * inv, o[i].w * inv));
+  if (lane == 0 && p.t.lse) p.t.lse[pair] = empty ? NEG_INF : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+cudaLaunchConfig_t pair_config(cudaLaunchAttribute* attr, int workers, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * workers, 1, 1);
+  cfg.blockDim = dim3(NTHREADS, 1, 1);
+  cfg.dynamicSmemBytes = SMEM;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+// Clusters that run at once on the current device (0 on error).
+int max_workers() {
+  static PerDeviceOnce configured;
+  static int workers[PerDeviceOnce::kMaxDevices] = {};
+  const cudaError_t e = configured.run([] {
+    cudaError_t r = cudaFuncSetAttribute(tree_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    int dev = 0, n = 0;
+    if (r == cudaSuccess) r = cudaGetDevice(&dev);
+    if (r != cudaSuccess) return r;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = pair_config(attr, 1, nullptr);
+    r = cudaOccupancyMaxActiveClusters(&n, tree_attn_kernel, &cfg);
+    if (r == cudaSuccess) workers[dev] = n < MAX_WORKERS ? n : MAX_WORKERS;
+    return r;
+  });
+  int dev = 0;
+  if (e != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) return 0;
+  return workers[dev];
 }
 
 }  // namespace
 
-int64_t tree_workspace_bytes() { return 256; }
+int64_t tree_workspace_bytes() {
+  const int n = max_workers();
+  return n > 0 ? (int64_t)(WS_SLOTS + (size_t)n * 2 * SLOT_BYTES) : 0;
+}
 
-cudaError_t launch_tree_attention(const TreeParams& p, cudaStream_t stream) {
-  const int64_t pairs = p.total_rows * p.num_heads;
-  tree_attn_simple<<<(unsigned)((pairs + kWarps - 1) / kWarps), kWarps * 32, 0, stream>>>(p);
+cudaError_t launch_tree_attention(const TreeParams& t, cudaStream_t stream) {
+  Params p;
+  p.t = t;
+  p.workers = max_workers();
+  if (p.workers <= 0) return cudaErrorInvalidConfiguration;
+  const bool any = t.max_blocks > 0;   // some cache row may be read
+  const int bs = t.block_size;
+  const uint64_t slots = any ? (uint64_t)t.num_blocks * (uint64_t)bs : 1;
+  CUtensorMap tq, tc, tb, t2, t3;
+  {
+    const uint64_t dims[2] = {576, (uint64_t)t.total_rows * (uint64_t)t.num_heads}, strides[1] = {576 * 2};
+    const uint32_t box[2] = {64, 64};
+    if (make_tensor_map_bf16(&tq, t.q, 2, dims, strides, box) != MLA_OK) return cudaErrorInvalidValue;
+  }
+  const void* rows = any ? static_cast<const void*>(t.cache) : t.q;   // a map needs a valid base
+  {
+    const uint64_t dims[2] = {576, slots}, strides[1] = {576 * 2};
+    const uint32_t box[2] = {64, 1};   // one row high: rows are fetched four at a time by gather4
+    if (make_tensor_map_bf16(&tc, rows, 2, dims, strides, box) != MLA_OK) return cudaErrorInvalidValue;
+  }
+  // Boxes for 64-key pieces: one when the block size is a multiple of 64, 64 / block_size when
+  // it is 8, 16 or 32 (8 rows keep a box on the swizzle's 1024-byte period); several panels in
+  // one box by a map of the rows as {64 columns, rows, 9 column groups}.
+  p.piece_rows = !any ? 0 : (bs % 64 == 0) ? 64 : (bs % 8 == 0 && 64 % bs == 0) ? bs : 0;
+  p.grouped = p.piece_rows == 64;
+  tb = t2 = t3 = tc;
+  if (p.piece_rows > 0) {
+    const uint64_t dims[2] = {576, slots}, strides[1] = {576 * 2};
+    const uint32_t box[2] = {64, (uint32_t)p.piece_rows};
+    if (make_tensor_map_bf16(&tb, rows, 2, dims, strides, box) != MLA_OK) return cudaErrorInvalidValue;
+  }
+  if (p.grouped) {
+    const uint64_t dims[3] = {64, slots, NP}, strides[2] = {576 * 2, 64 * 2};
+    const uint32_t box2[3] = {64, 64, 2}, box3[3] = {64, 64, 3};
+    if (make_tensor_map_bf16(&t2, rows, 3, dims, strides, box2) != MLA_OK ||
+        make_tensor_map_bf16(&t3, rows, 3, dims, strides, box3) != MLA_OK)
+      return cudaErrorInvalidValue;
+  }
+  p.oob_row = (int32_t)slots;
+  p.o_align32 = (reinterpret_cast<uintptr_t>(t.o) & 31u) == 0;
+  const float LOG2E = 1.4426950408889634f;
+  p.has_cap = t.soft_cap > 0.f;
+  p.scale_log2 = t.sm_scale * LOG2E;
+  p.cap_log2 = p.has_cap ? t.soft_cap * LOG2E : 0.f;
+  p.cap_ex2_scale = p.has_cap ? 2.f * LOG2E * t.sm_scale / t.soft_cap : 0.f;
+  const uint64_t forced = forced_timeout_ns();
+  p.force_timeout = forced != 0;
+  p.wait_limit_ns = forced ? forced : kWaitLimitNs;
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = pair_config(attr, p.workers, stream);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, tree_attn_kernel, tq, tc, tb, t2, t3, p);
+  if (e != cudaSuccess || p.workers < 2) return e;
+  tree_join_kernel<<<dim3(p.workers - 1, ROWS / JOIN_WARPS), JOIN_WARPS * 32, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -451,7 +451,7 @@ MLA_API int mla_tree_workspace(int64_t total_rows, int num_heads, int64_t* bytes
  *   sm_scale   : finite and > 0; logits_soft_cap: <= 0 none, c > 0: c * tanh(x / c)
  *   o_lat      : bf16 [total_rows, num_heads, 512]  (written)
  *   lse        : fp32 [total_rows, num_heads], natural log, or NULL  (written)
- *   workspace  : DEVICE, 16-byte aligned, at least mla_tree_workspace bytes, not in use by
+ *   workspace  : DEVICE, 32-byte aligned, at least mla_tree_workspace bytes, not in use by
  *                another call that may run at the same time; its contents do not matter
  *   status     : DEVICE int32 word or NULL
  * A row that sees no key gets O = 0, LSE = -inf.  Positions at or past kv_len are never read.
