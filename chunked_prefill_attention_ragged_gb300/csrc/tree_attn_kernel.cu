@@ -133,10 +133,6 @@ struct Ctx {
     int dummy = 0;
     mbar_wait_bounded(bar(b), parity, &dummy, status, MLA_DEVSTAT_TIMEOUT, DRAIN_LIMIT_NS, true);
   }
-  __device__ void commit_both(int b) const {
-    tc_commit_pair(bar(b));
-    tc_commit_pair(mapa_shared(bar(b), 1));
-  }
 };
 
 // One request as the kernel sees it.
@@ -359,51 +355,74 @@ __device__ void run_forward_v(const Ctx& c, Parts parts) {
 }
 
 // ------------------------------------------------------------------ products (even CTA, warp 1)
+// The whole warp runs the issue loop and one elected lane (always the same) issues: with a branch
+// for lane 0 around the loop a product took 63-70 clocks to issue, this way an M = 128, N = 128
+// product of the pair takes 32 and an N = 256 one 64, which is the tensor cores' own rate.
+__device__ __forceinline__ void issue(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive on `bar` of both CTAs once the elected lane's products so far have completed.
+__device__ __forceinline__ void commit_both(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}\n" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
 __device__ void run_mma(const Ctx& c, const Params& p, Parts parts, uint32_t tmem) {
   const uint64_t q_desc = sdesc_sw128(c.sbase + OFF_Q, 16, 1024);
   const uint64_t k_desc = sdesc_sw128(c.sbase + OFF_K, 16, 1024);
   const uint64_t v_desc = sdesc_sw128(c.sbase + OFF_V, QP, 1024);
   const uint64_t p_desc = sdesc_sw128(c.sbase + OFF_P, 16, 1024);
+  auto wait = [&](int b, uint32_t parity) { return (bool)__all_sync(0xffffffffu, c.wait_pair(b, parity)); };
   bool ok = true;
-  if (p.force_timeout) ok = c.wait(NEVER, 0);
+  if (p.force_timeout) ok = wait(NEVER, 0);
   int st = 0, units = 0;   // S tiles issued
   auto s_products = [&](bool last) {
     const int b = st & 1;
     for (int g = 0; g < KGROUPS; ++g) {
-      if (!c.wait_pair(KF + g, st & 1)) return false;
+      if (!wait(KF + g, st & 1)) return false;
       tc_fence_after();
 #pragma unroll
       for (int i = 0; i < 12; ++i) {
         const uint64_t off = (uint64_t)(((3 * g + (i >> 2)) * QP + (i & 3) * 32) >> 4);
-        mma_ss_pair(tmem + TM_S(b), q_desc + off, k_desc + off, IDESC_QK, (g > 0 || i > 0) ? 1u : 0u);
+        issue(tmem + TM_S(b), q_desc + off, k_desc + off, IDESC_QK, (g > 0 || i > 0) ? 1u : 0u);
       }
-      c.commit_both(KE + g);
+      commit_both(c.bar(KE + g));
     }
-    c.commit_both(SF + b);
-    if (last) c.commit_both(QE);
+    commit_both(c.bar(SF + b));
+    if (last) commit_both(c.bar(QE));
     ++st;
     return true;
   };
   auto pv_products = [&](int t, bool first) {
-    if (!c.wait_pair(PR, t & 1)) return false;
+    if (!wait(PR, t & 1)) return false;
     for (int j = 0; j < 2; ++j) {
-      if (!c.wait_pair(VF + j, t & 1)) return false;
+      if (!wait(VF + j, t & 1)) return false;
       tc_fence_after();
 #pragma unroll
       for (int kk = 0; kk < KEYS / 16; ++kk) {
         const uint64_t po = (uint64_t)(((kk >> 2) * QP + (kk & 3) * 32) >> 4);
         const uint64_t vo = (uint64_t)((j * V_CHUNK + (kk >> 2) * 2 * QP + (kk & 3) * 16 * 128) >> 4);
-        mma_ss_pair(tmem + TM_O(j), p_desc + po, v_desc + vo, IDESC_PV, (!first || kk > 0) ? 1u : 0u);
+        issue(tmem + TM_O(j), p_desc + po, v_desc + vo, IDESC_PV, (!first || kk > 0) ? 1u : 0u);
       }
-      c.commit_both(VE + j);
+      commit_both(c.bar(VE + j));
     }
-    c.commit_both(OD);
+    commit_both(c.bar(OD));
     return true;
   };
   int pv = 0;   // S runs one tile ahead of P V
   Part u;
   while (ok && parts.next(&u)) {
-    ok = c.wait_pair(QF, units & 1);
+    ok = wait(QF, units & 1);
     ++units;
     for (int t = u.lo; t < u.hi && ok; ++t) {
       // S's buffer held P V(pv - 2)'s scores, read before that tile's P was ready.
@@ -413,8 +432,9 @@ __device__ void run_mma(const Ctx& c, const Params& p, Parts parts, uint32_t tme
     // (The next part's Q is only loaded now that S is done: P V does not wait for it.)
     if (ok) ok = pv_products(pv++, u.hi - u.lo == 1);
   }
-  tc_commit_pair(c.bar(FIN));
+  commit_both(c.bar(FIN));
   c.drain(FIN, 0);
+  __syncwarp();
 }
 
 // ------------------------------------------------------------------ softmax (warps 4-7)
@@ -733,10 +753,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   } else if (warp == 2) {
     run_producer_v(c, p, parts, &tm_c, &tm_b, &tm_2);
   } else if (warp == 1) {
-    if (lane == 0) {
-      if (rank == 0) run_mma(c, p, parts, tmem);
-      else run_forward_qk(c, parts);
-    }
+    if (rank == 0) run_mma(c, p, parts, tmem);
+    else if (lane == 0) run_forward_qk(c, parts);
   } else if (warp == 3) {
     if (lane == 0 && rank != 0) run_forward_v(c, parts);
   } else {
