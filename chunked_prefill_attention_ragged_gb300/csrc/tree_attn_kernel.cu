@@ -28,9 +28,9 @@
 // its 64 of the tile's 128 keys as the half of S's B operand, the tile's 128 keys x its half of
 // the value columns as the half of P V's B operand, and P (64 x 128).
 //   warp 0     Q and K producer: Q once per unit; K in three groups of three 64-column panels
-//   warp 2     V producer: two 256-column chunks (128 of the columns here)
-//   warp 1     even CTA: issues every product; odd CTA: passes its Q/K arrivals on to the even
-//   warp 3     TMEM allocation; odd CTA: passes its V arrivals on
+//   warp 1     even CTA: issues every product
+//   warp 2     V producer: two 256-column chunks (128 of the columns here), by halves of the keys
+//   warp 3     TMEM allocation
 //   warps 4-7  softmax: two threads per pair (the two halves of the keys and of O's columns)
 // Order of products: S(t + 1) before P V(t), so that the tensor cores work on the next tile while
 // the softmax does this one.  Key rows come by whole boxes where a 64-row piece lies inside the
@@ -52,7 +52,7 @@ constexpr int KEYS = 128;               // keys per tile
 constexpr int QP = 64 * 128;            // a [64 rows, 64 columns] panel: 8 KB
 constexpr int NP = 9;                   // 64-column panels of 576
 constexpr int KGROUPS = 3;              // K panels arrive in groups of three
-constexpr int V_CHUNK = 4 * QP;         // [2 key halves][2 panels][64 keys][64 columns]
+constexpr int V_CHUNK = 4 * QP;         // [2 key halves][2 panels][64 keys][64 columns] of one value chunk
 constexpr int OFF_Q = 0;
 constexpr int OFF_K = OFF_Q + NP * QP;
 constexpr int OFF_V = OFF_K + NP * QP;
@@ -64,9 +64,9 @@ enum Bar {
   QE,                  // the unit's last S done: Q may be replaced
   KF,                  // [group] K panels landed
   KE = KF + KGROUPS,   // [group] their products done
-  VF = KE + KGROUPS,   // [chunk] V landed
-  VE = VF + 2,         // [chunk] its product done
-  SF = VE + 2,         // [buffer] S done
+  VF = KE + KGROUPS,   // [chunk, key half] V landed
+  VE = VF + 4,         // [chunk, key half] its products done
+  SF = VE + 4,         // [buffer] S done
   PR = SF + 2,         // P written (and the S buffer read) by every softmax warp of both CTAs
   OD,                  // P V done
   XB,                  // [row half] maxima exchanged between the two warps of 32 rows
@@ -125,9 +125,44 @@ struct Ctx {
   __device__ bool wait(int b, uint32_t parity) const {
     return mbar_wait_bounded(bar(b), parity, abort_flag, status, MLA_DEVSTAT_TIMEOUT, wait_limit_ns);
   }
-  // For the even CTA's barriers that threads of the odd one arrive on: acquire at cluster scope.
-  __device__ bool wait_pair(int b, uint32_t parity) const {
-    return mbar_wait_bounded(bar(b), parity, abort_flag, status, MLA_DEVSTAT_TIMEOUT, wait_limit_ns, true);
+  // The same for a converged warp, polled by one lane: 32 lanes polling, in five warps that wait
+  // most of the time, slow the softmax's exponentials down (they share the queue to the special
+  // function units and shared memory).
+  __device__ bool wait_warp(int b, uint32_t parity) const {
+    const uint32_t a = bar(b);
+    auto poll = [&]() {
+      uint32_t r;
+      asm volatile(
+          "{\n\t.reg .pred p, e;\n\t"
+          "elect.sync _|e, 0xffffffff;\n\t"
+          "setp.ne.b32 p, 0, 0;\n\t"
+          "@e mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}\n"
+          : "=r"(r)
+          : "r"(a), "r"(parity)
+          : "memory");
+      return __any_sync(0xffffffffu, r != 0) != 0;
+    };
+    bool ok = poll();
+    if (!ok) {
+      const uint64_t t0 = global_timer_ns();
+      for (uint32_t it = 1;; ++it) {
+        ok = poll();
+        if (ok) break;
+        if ((it & 63) == 0) {
+          const bool late = global_timer_ns() - t0 > wait_limit_ns;
+          if (__any_sync(0xffffffffu, late || *abort_flag)) {
+            if (late) {
+              *abort_flag = 1;
+              if (status) atomicOr(status, MLA_DEVSTAT_TIMEOUT);
+            }
+            break;
+          }
+        }
+      }
+    }
+    __syncwarp();   // what the polling lane acquired, all lanes see
+    return ok;
   }
   __device__ void drain(int b, uint32_t parity) const {
     int dummy = 0;
@@ -239,132 +274,151 @@ __device__ __forceinline__ KeyRows find_rows(const Params& p, const Part& u, int
   return k;
 }
 
-// 64 keys x panels [panel0, panel0 + n) to n consecutive 8 KB panels at dst.  tg: the map whose
-// boxes hold exactly n panels.
+// 64 keys x panels [panel0, panel0 + n) to n consecutive 8 KB panels at dst, completing on `bar`
+// (of the even CTA).  tg: the map whose boxes hold exactly n panels.
 __device__ __forceinline__ void copy_panels(const Params& p, const KeyRows& k, uint32_t dst, uint32_t bar,
                                             const CUtensorMap* tc, const CUtensorMap* tb, const CUtensorMap* tg,
                                             int panel0, int n, int lane) {
   if (k.by_block && p.grouped) {
-    if (lane == 0) tma_load_3d(dst, tg, bar, 0, k.piece, panel0);
+    if (lane == 0) tma_load_3d_pair(dst, tg, bar, 0, k.piece, panel0);
     return;
   }
+#pragma unroll 1
   for (int i = 0; i < n; ++i) {
     const int col = (panel0 + i) * 64;
     if (k.by_block) {
-      if (lane * p.piece_rows < 64) tma_load_2d(dst + i * QP + lane * p.piece_rows * 128, tb, bar, col, k.piece);
+      if (lane * p.piece_rows < 64) tma_load_2d_pair(dst + i * QP + lane * p.piece_rows * 128, tb, bar, col, k.piece);
     } else if (lane < 16) {
-      tma_gather4(dst + i * QP + lane * 4 * 128, tc, bar, col, k.r4[0], k.r4[1], k.r4[2], k.r4[3]);
+      tma_gather4_pair(dst + i * QP + lane * 4 * 128, tc, bar, col, k.r4[0], k.r4[1], k.r4[2], k.r4[3]);
     }
   }
 }
 
 // ------------------------------------------------------------------ producers
+// The copies of both CTAs complete on the even CTA's barriers, where the products wait for them;
+// its producers announce the bytes of both.  The buffers hold one tile: what a product has read
+// is loaded again at once, so the way from "read" to the copy is kept short (rows looked up a
+// tile ahead, one lane).
+__device__ __forceinline__ void expect_both(const Ctx& c, int b, uint32_t bytes_each) {
+  if (c.rank == 0) mbar_arrive_expect_tx(c.bar(b), 2 * bytes_each);
+}
+// After an abort the odd CTA cannot see its copies land: they have this long.
+__device__ __forceinline__ void settle() {
+  const uint64_t t0 = global_timer_ns();
+  while (global_timer_ns() - t0 < DRAIN_LIMIT_NS) {
+  }
+}
+
 __device__ void run_producer_qk(const Ctx& c, const Params& p, Parts parts, const CUtensorMap* tq,
                                 const CUtensorMap* tc, const CUtensorMap* tb, const CUtensorMap* t3) {
   const int lane = threadIdx.x & 31;
-  int tiles = 0, units = 0, q_issued = 0, k_issued[KGROUPS] = {0, 0, 0};
+  const uint32_t qf = mapa_shared(c.bar(QF), 0), kf = mapa_shared(c.bar(KF), 0);
+  int tiles = 0, units = 0, issued = 0;   // tiles begun, parts, K groups
   bool ok = true;
   Part u;
   while (ok && parts.next(&u)) {
-    int go = 1;
+    KeyRows k = find_rows(p, u, (int64_t)u.lo * KEYS + 64 * c.rank, lane);
     if (lane == 0) {
-      if (units > 0) go = c.wait(QE, (units - 1) & 1);
-      if (go) {
-        mbar_arrive_expect_tx(c.bar(QF), NP * QP);
+      if (units > 0) ok = c.wait(QE, (units - 1) & 1);
+      if (ok) {
+        expect_both(c, QF, NP * QP);
         for (int i = 0; i < NP; ++i)
-          tma_load_2d(c.sbase + OFF_Q + i * QP, tq, c.bar(QF), i * 64, (int32_t)(u.pair0 + 64 * c.rank));
+          tma_load_2d_pair(c.sbase + OFF_Q + i * QP, tq, qf, i * 64, (int32_t)(u.pair0 + 64 * c.rank));
       }
     }
-    if (!__shfl_sync(0xffffffffu, go, 0)) break;
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    if (!ok) break;
     ++units;
-    ++q_issued;
     for (int t = u.lo; t < u.hi && ok; ++t, ++tiles) {
-      const KeyRows k = find_rows(p, u, (int64_t)t * KEYS + 64 * c.rank, lane);
+#pragma unroll 1
       for (int g = 0; g < KGROUPS; ++g) {
-        int free = 1;
-        if (lane == 0 && tiles > 0) free = c.wait(KE + g, (tiles - 1) & 1);
-        if (!__shfl_sync(0xffffffffu, free, 0)) { ok = false; break; }
-        if (lane == 0) mbar_arrive_expect_tx(c.bar(KF + g), 3 * QP);
-        __syncwarp();
-        copy_panels(p, k, c.sbase + OFF_K + 3 * g * QP, c.bar(KF + g), tc, tb, t3, 3 * g, 3, lane);
-        ++k_issued[g];
+        if (lane == 0) {
+          if (tiles > 0) ok = c.wait(KE + g, (tiles - 1) & 1);
+          if (ok) expect_both(c, KF + g, 3 * QP);
+        }
+        if (!(k.by_block && p.grouped)) ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (ok) copy_panels(p, k, c.sbase + OFF_K + 3 * g * QP, kf + 8 * g, tc, tb, t3, 3 * g, 3, lane);
+        if (!ok) break;
+        ++issued;
       }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (t + 1 < u.hi) k = find_rows(p, u, (int64_t)(t + 1) * KEYS + 64 * c.rank, lane);
     }
   }
   // Let every copy started here land before the CTA can exit.
   if (lane == 0) {
-    if (q_issued) c.drain(QF, (q_issued - 1) & 1);
-    for (int g = 0; g < KGROUPS; ++g)
-      if (k_issued[g]) c.drain(KF + g, (k_issued[g] - 1) & 1);
+    if (c.rank == 0) {
+      if (units) c.drain(QF, (units - 1) & 1);
+      for (int g = 0; g < KGROUPS; ++g) {
+        const int n = (issued + KGROUPS - 1 - g) / KGROUPS;
+        if (n) c.drain(KF + g, (n - 1) & 1);
+      }
+    } else if (!ok) {
+      settle();
+    }
   }
 }
 
 __device__ void run_producer_v(const Ctx& c, const Params& p, Parts parts, const CUtensorMap* tc,
                                const CUtensorMap* tb, const CUtensorMap* t2) {
   const int lane = threadIdx.x & 31;
-  int tiles = 0, issued[2] = {0, 0};
+  const uint32_t vf = mapa_shared(c.bar(VF), 0);
+  int tiles = 0, issued = 0;
   bool ok = true;
   Part u;
   while (ok && parts.next(&u)) {
+    KeyRows k0 = find_rows(p, u, (int64_t)u.lo * KEYS, lane);
+    KeyRows k1 = find_rows(p, u, (int64_t)u.lo * KEYS + 64, lane);
     for (int t = u.lo; t < u.hi && ok; ++t, ++tiles) {
-      const KeyRows k0 = find_rows(p, u, (int64_t)t * KEYS, lane);
-      const KeyRows k1 = find_rows(p, u, (int64_t)t * KEYS + 64, lane);
-      for (int j = 0; j < 2; ++j) {
-        int free = 1;
-        if (lane == 0 && tiles > 0) free = c.wait(VE + j, (tiles - 1) & 1);
-        if (!__shfl_sync(0xffffffffu, free, 0)) { ok = false; break; }
-        if (lane == 0) mbar_arrive_expect_tx(c.bar(VF + j), V_CHUNK);
-        __syncwarp();
-        const uint32_t dst = c.sbase + OFF_V + j * V_CHUNK;
-        const int panel = 4 * j + 2 * (int)c.rank;
-        copy_panels(p, k0, dst, c.bar(VF + j), tc, tb, t2, panel, 2, lane);
-        copy_panels(p, k1, dst + 2 * QP, c.bar(VF + j), tc, tb, t2, panel, 2, lane);
-        ++issued[j];
+      const bool fast = k0.by_block && k1.by_block && p.grouped;
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {   // chunk i / 2, key half i % 2
+        if (lane == 0) {
+          if (tiles > 0) ok = c.wait(VE + i, (tiles - 1) & 1);
+          if (ok) expect_both(c, VF + i, 2 * QP);
+        }
+        if (!fast) ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (ok)
+          copy_panels(p, i & 1 ? k1 : k0, c.sbase + OFF_V + i * 2 * QP, vf + 8 * i, tc, tb, t2,
+                      4 * (i >> 1) + 2 * (int)c.rank, 2, lane);
+        if (!ok) break;
+        ++issued;
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (t + 1 < u.hi) {
+        k0 = find_rows(p, u, (int64_t)(t + 1) * KEYS, lane);
+        k1 = find_rows(p, u, (int64_t)(t + 1) * KEYS + 64, lane);
       }
     }
   }
-  if (lane == 0)
-    for (int j = 0; j < 2; ++j)
-      if (issued[j]) c.drain(VF + j, (issued[j] - 1) & 1);
-}
-
-// The odd CTA's arrivals, passed on to the even CTA's barriers of the same name.
-__device__ void run_forward_qk(const Ctx& c, Parts parts) {
-  int tiles = 0, units = 0;
-  Part u;
-  while (parts.next(&u)) {
-    if (!c.wait(QF, units & 1)) return;
-    mbar_arrive_remote(mapa_shared(c.bar(QF), 0));
-    ++units;
-    for (int t = u.lo; t < u.hi; ++t, ++tiles)
-      for (int g = 0; g < KGROUPS; ++g) {
-        if (!c.wait(KF + g, tiles & 1)) return;
-        mbar_arrive_remote(mapa_shared(c.bar(KF + g), 0));
+  if (lane == 0) {
+    if (c.rank == 0) {
+      for (int i = 0; i < 4; ++i) {
+        const int n = (issued + 3 - i) / 4;
+        if (n) c.drain(VF + i, (n - 1) & 1);
       }
+    } else if (!ok) {
+      settle();
+    }
   }
-}
-__device__ void run_forward_v(const Ctx& c, Parts parts) {
-  int tiles = 0;
-  Part u;
-  while (parts.next(&u))
-    for (int t = u.lo; t < u.hi; ++t, ++tiles)
-      for (int j = 0; j < 2; ++j) {
-        if (!c.wait(VF + j, tiles & 1)) return;
-        mbar_arrive_remote(mapa_shared(c.bar(VF + j), 0));
-      }
 }
 
 // ------------------------------------------------------------------ products (even CTA, warp 1)
-// The whole warp runs the issue loop and one elected lane (always the same) issues: with a branch
-// for lane 0 around the loop a product took 63-70 clocks to issue, this way an M = 128, N = 128
-// product of the pair takes 32 and an N = 256 one 64, which is the tensor cores' own rate.
+// The whole warp runs the issue loop and one elected lane (always the same) issues, with every
+// operand in a register that the compiler knows to be the same in all lanes (values from memory
+// are broadcast by a shuffle first).  With a branch for lane 0 around the loop, or operands that
+// may differ by lane, a product took 50-70 clocks to issue; this way an M = 128, N = 128 product
+// of the pair takes 32 and an N = 256 one 64, the tensor cores' own rate.  Descriptors are
+// passed as low and high words: only the low one moves.
 __device__ __forceinline__ void issue(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %4};\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t}\n" ::"r"(d),
+      "r"((uint32_t)a), "r"((uint32_t)b), "r"((uint32_t)(a >> 32)), "r"((uint32_t)(b >> 32)), "r"(idesc),
+      "r"(accumulate)
       : "memory");
 }
 // Arrive on `bar` of both CTAs once the elected lane's products so far have completed.
@@ -382,39 +436,46 @@ __device__ void run_mma(const Ctx& c, const Params& p, Parts parts, uint32_t tme
   const uint64_t k_desc = sdesc_sw128(c.sbase + OFF_K, 16, 1024);
   const uint64_t v_desc = sdesc_sw128(c.sbase + OFF_V, QP, 1024);
   const uint64_t p_desc = sdesc_sw128(c.sbase + OFF_P, 16, 1024);
-  auto wait = [&](int b, uint32_t parity) { return (bool)__all_sync(0xffffffffu, c.wait_pair(b, parity)); };
   bool ok = true;
-  if (p.force_timeout) ok = wait(NEVER, 0);
+  if (p.force_timeout) ok = c.wait_warp(NEVER, 0);
   int st = 0, units = 0;   // S tiles issued
   auto s_products = [&](bool last) {
     const int b = st & 1;
-    for (int g = 0; g < KGROUPS; ++g) {
-      if (!wait(KF + g, st & 1)) return false;
-      tc_fence_after();
-#pragma unroll
-      for (int i = 0; i < 12; ++i) {
-        const uint64_t off = (uint64_t)(((3 * g + (i >> 2)) * QP + (i & 3) * 32) >> 4);
-        issue(tmem + TM_S(b), q_desc + off, k_desc + off, IDESC_QK, (g > 0 || i > 0) ? 1u : 0u);
+    const uint32_t d = __shfl_sync(0xffffffffu, tmem + TM_S(b), 0);
+    // Loops kept small: with all 52 products of a tile unrolled the warps' code no longer fits the
+    // instruction cache together, and the kernel ran 1.3 times as long.
+#pragma unroll 1
+    for (int i = 0; i < NP; ++i) {
+      if (i % 3 == 0) {
+        if (!c.wait_warp(KF + i / 3, st & 1)) return false;
+        tc_fence_after();
       }
-      commit_both(c.bar(KE + g));
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const uint64_t off = (uint64_t)((i * QP + kk * 32) >> 4);
+        issue(d, q_desc + off, k_desc + off, IDESC_QK, kk > 0 ? 1u : i > 0 ? 1u : 0u);
+      }
+      if (i % 3 == 2) commit_both(c.bar(KE + i / 3));
     }
     commit_both(c.bar(SF + b));
     if (last) commit_both(c.bar(QE));
     ++st;
     return true;
   };
-  auto pv_products = [&](int t, bool first) {
-    if (!wait(PR, t & 1)) return false;
-    for (int j = 0; j < 2; ++j) {
-      if (!wait(VF + j, t & 1)) return false;
+  auto pv_products = [&](int t, bool first_tile) {
+    const uint32_t more = __shfl_sync(0xffffffffu, first_tile ? 0u : 1u, 0);
+    if (!c.wait_warp(PR, t & 1)) return false;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {   // chunk i / 2, key half i % 2
+      if (!c.wait_warp(VF + i, t & 1)) return false;
       tc_fence_after();
 #pragma unroll
-      for (int kk = 0; kk < KEYS / 16; ++kk) {
-        const uint64_t po = (uint64_t)(((kk >> 2) * QP + (kk & 3) * 32) >> 4);
-        const uint64_t vo = (uint64_t)((j * V_CHUNK + (kk >> 2) * 2 * QP + (kk & 3) * 16 * 128) >> 4);
-        issue(tmem + TM_O(j), p_desc + po, v_desc + vo, IDESC_PV, (!first || kk > 0) ? 1u : 0u);
+      for (int kk = 0; kk < 4; ++kk) {
+        const uint64_t po = (uint64_t)(((i & 1) * QP + kk * 32) >> 4);
+        const uint64_t vo = (uint64_t)((i * 2 * QP + kk * 16 * 128) >> 4);
+        issue(tmem + TM_O(i >> 1), p_desc + po, v_desc + vo, IDESC_PV, kk > 0 ? 1u : (i & 1) ? 1u : more);
       }
-      commit_both(c.bar(VE + j));
+      commit_both(c.bar(VE + i));
     }
     commit_both(c.bar(OD));
     return true;
@@ -422,15 +483,16 @@ __device__ void run_mma(const Ctx& c, const Params& p, Parts parts, uint32_t tme
   int pv = 0;   // S runs one tile ahead of P V
   Part u;
   while (ok && parts.next(&u)) {
-    ok = wait(QF, units & 1);
+    const int n = __shfl_sync(0xffffffffu, u.hi - u.lo, 0);
+    ok = c.wait_warp(QF, units & 1);
     ++units;
-    for (int t = u.lo; t < u.hi && ok; ++t) {
+    for (int t = 0; t < n && ok; ++t) {
       // S's buffer held P V(pv - 2)'s scores, read before that tile's P was ready.
-      ok = s_products(t == u.hi - 1);
-      if (ok && t > u.lo) ok = pv_products(pv++, t - 1 == u.lo);
+      ok = s_products(t == n - 1);
+      if (ok && t > 0) ok = pv_products(pv++, t == 1);
     }
     // (The next part's Q is only loaded now that S is done: P V does not wait for it.)
-    if (ok) ok = pv_products(pv++, u.hi - u.lo == 1);
+    if (ok) ok = pv_products(pv++, n == 1);
   }
   commit_both(c.bar(FIN));
   c.drain(FIN, 0);
@@ -466,11 +528,6 @@ __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy
 __device__ __forceinline__ void st_shared_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
-// Arrive on a barrier of another CTA of the cluster, releasing this thread's (and, after a
-// __syncwarp, its warp's) shared-memory writes at cluster scope.
-__device__ __forceinline__ void arrive_release_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
 
 __device__ void run_softmax(const Ctx& c, const Params& p, Parts parts, uint32_t tmem, char* ws_slots, uint8_t* smem) {
   const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3;
@@ -492,7 +549,7 @@ __device__ void run_softmax(const Ctx& c, const Params& p, Parts parts, uint32_t
     buf[half * 64 + row] = mine;
     __syncwarp();
     if (lane == 0) mbar_arrive(c.bar(XB + rg));
-    if (!__all_sync(0xffffffffu, c.wait(XB + rg, xs & 1))) return false;
+    if (!c.wait_warp(XB + rg, xs & 1)) return false;
     *theirs = buf[(half ^ 1) * 64 + row];
     ++xs;
     return true;
@@ -507,7 +564,7 @@ __device__ void run_softmax(const Ctx& c, const Params& p, Parts parts, uint32_t
     float m_used = NEG_INF, l = 0.f;
     for (int t = u.lo; t < u.hi; ++t, ++g) {
       const int sb = g & 1;
-      if (!__all_sync(0xffffffffu, c.wait(SF + sb, (g >> 1) & 1))) { ok = false; break; }
+      if (!c.wait_warp(SF + sb, (g >> 1) & 1)) { ok = false; break; }
       tc_fence_after();
       float sv[64];
       tmem_ld64_sync(lane_addr + TM_S(sb), reinterpret_cast<uint32_t*>(sv));
@@ -568,7 +625,7 @@ __device__ void run_softmax(const Ctx& c, const Params& p, Parts parts, uint32_t
       if (rescale) alpha = ex2_approx(m_used - m_new);
       l = l * alpha + sum;
       // The tile before this one has to be done with P, and with O if it is rescaled.
-      if (g > 0 && !__all_sync(0xffffffffu, c.wait(OD, (g - 1) & 1))) { ok = false; break; }
+      if (g > 0 && !c.wait_warp(OD, (g - 1) & 1)) { ok = false; break; }
       if (__any_sync(0xffffffffu, rescale)) {   // tcgen05.ld/st are warp-collective
         tc_fence_after();
         const float2 a2 = make_float2(alpha, alpha);
@@ -593,7 +650,10 @@ __device__ void run_softmax(const Ctx& c, const Params& p, Parts parts, uint32_t
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if (c.rank) arrive_release_cluster(pr_bar);
+        // What this publishes to the even CTA's issuing thread is not generic data: P was handed to
+        // this CTA's async proxy by the fence above, S and O are ordered by the tcgen05 fence.  So a
+        // release at CTA scope does; one at cluster scope took 2-4 thousand clocks here.
+        if (c.rank) mbar_arrive_remote(pr_bar);
         else mbar_arrive(pr_bar);
       }
     }
@@ -602,7 +662,7 @@ __device__ void run_softmax(const Ctx& c, const Params& p, Parts parts, uint32_t
     float l_other;
     if (!exchange(l, &l_other)) break;
     const float l_row = l + l_other;
-    if (!__all_sync(0xffffffffu, c.wait(OD, (g - 1) & 1))) break;
+    if (!c.wait_warp(OD, (g - 1) & 1)) break;
     tc_fence_after();
     const bool empty = !(l_row > 0.f);
     const float inv = u.whole ? (empty ? 0.f : 1.f / l_row) : 1.f;
@@ -705,7 +765,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   __shared__ int64_t count;
   __shared__ Header head;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   int* abort_flag = reinterpret_cast<int*>(smem + OFF_MISC + 4);
   const uint32_t rank = cluster_ctarank();
@@ -714,12 +774,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   if (threadIdx.x == 0) {
     for (int i = 0; i < NBAR; ++i) mbar_init(c.bar(i), 1);
     for (int i = 0; i < 2; ++i) mbar_init(c.bar(XB + i), 2);      // the two warps of 32 rows
-    mbar_init(c.bar(PR), rank == 0 ? 8 : 4);                       // every softmax warp, of both CTAs
-    if (rank == 0) {   // own load (with its bytes) and the odd CTA's forwarded arrival
-      mbar_init(c.bar(QF), 2);
-      for (int i = 0; i < KGROUPS; ++i) mbar_init(c.bar(KF + i), 2);
-      for (int i = 0; i < 2; ++i) mbar_init(c.bar(VF + i), 2);
-    }
+    mbar_init(c.bar(PR), 8);                                        // every softmax warp, of both CTAs
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -746,7 +801,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   __syncthreads();
   cluster_sync();   // both CTAs' barriers exist before any remote arrival
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const Parts parts(p.t, start, count);
   if (warp == 0) {
     run_producer_qk(c, p, parts, &tm_q, &tm_c, &tm_b, &tm_3);
@@ -754,10 +809,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     run_producer_v(c, p, parts, &tm_c, &tm_b, &tm_2);
   } else if (warp == 1) {
     if (rank == 0) run_mma(c, p, parts, tmem);
-    else if (lane == 0) run_forward_qk(c, parts);
-  } else if (warp == 3) {
-    if (lane == 0 && rank != 0) run_forward_v(c, parts);
-  } else {
+  } else if (warp >= 4) {
     run_softmax(c, p, parts, tmem, ws + WS_SLOTS + (size_t)worker * 2 * SLOT_BYTES, smem);
   }
   __syncwarp();
