@@ -30,7 +30,7 @@
 //   warp 0     Q and K producer: Q once per unit; K in three groups of three 64-column panels
 //   warp 1     even CTA: issues every product
 //   warp 2     V producer: two 256-column chunks (128 of the columns here), by halves of the keys
-//   warp 3     TMEM allocation
+//   warp 3     TMEM allocation; brings the next tile's rows into L2
 //   warps 4-7  softmax: two threads per pair (the two halves of the keys and of O's columns)
 // Order of products: S(t + 1) before P V(t), so that the tensor cores work on the next tile while
 // the softmax does this one.  Key rows come by whole boxes where a 64-row piece lies inside the
@@ -125,10 +125,28 @@ struct Ctx {
   __device__ bool wait(int b, uint32_t parity) const {
     return mbar_wait_bounded(bar(b), parity, abort_flag, status, MLA_DEVSTAT_TIMEOUT, wait_limit_ns);
   }
+  // One lane's look at a barrier, whose result can be used later; for wait_warp's `seen`.
+  __device__ uint32_t look(int b, uint32_t parity) const {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, 0, 0;\n\t"
+        "@e mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(r)
+        : "r"(bar(b)), "r"(parity)
+        : "memory");
+    return r;
+  }
   // The same for a converged warp, polled by one lane: 32 lanes polling, in five warps that wait
   // most of the time, slow the softmax's exponentials down (they share the queue to the special
   // function units and shared memory).
-  __device__ bool wait_warp(int b, uint32_t parity) const {
+  __device__ bool wait_warp(int b, uint32_t parity, uint32_t seen = 0) const {
+    if (__any_sync(0xffffffffu, seen != 0)) {
+      __syncwarp();
+      return true;
+    }
     const uint32_t a = bar(b);
     auto poll = [&]() {
       uint32_t r;
@@ -403,6 +421,33 @@ __device__ void run_producer_v(const Ctx& c, const Params& p, Parts parts, const
   }
 }
 
+// Warp 3: this CTA's keys of the tile after the one being loaded, into L2.  The one-tile buffers
+// leave a load less than a tile's time, which DRAM does not keep to: with the rows in L2 it does.
+__device__ void run_prefetch(const Ctx& c, const Params& p, Parts parts, const CUtensorMap* tb,
+                             const CUtensorMap* t3) {
+  if (p.piece_rows == 0) return;
+  const int lane = threadIdx.x & 31, pieces = 64 / p.piece_rows;
+  int tiles = 0;
+  Part u;
+  while (parts.next(&u)) {
+    for (int t = u.lo; t < u.hi; ++t, ++tiles) {
+      const int64_t key0 = (int64_t)(t + 1) * KEYS + 64 * c.rank;
+      if (t + 1 < u.hi && key0 + 64 <= u.q.kv && lane < pieces) {
+        const int32_t row = key_row(p, u, key0 + lane * p.piece_rows);
+        if (p.grouped) {
+#pragma unroll 1
+          for (int g = 0; g < KGROUPS; ++g) tma_prefetch_3d(t3, 0, row, 3 * g);
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < NP; ++i) tma_prefetch_2d(tb, i * 64, row);
+        }
+      }
+      // Not faster than the products: tile t's first panels have been read.
+      if (!c.wait_warp(KE, tiles & 1)) return;
+    }
+  }
+}
+
 // ------------------------------------------------------------------ products (even CTA, warp 1)
 // The whole warp runs the issue loop and one elected lane (always the same) issues, with every
 // operand in a register that the compiler knows to be the same in all lanes (values from memory
@@ -439,36 +484,43 @@ __device__ void run_mma(const Ctx& c, const Params& p, Parts parts, uint32_t tme
   bool ok = true;
   if (p.force_timeout) ok = c.wait_warp(NEVER, 0);
   int st = 0, units = 0;   // S tiles issued
+  // A look at a barrier takes about 100 clocks to come back, so each step's barrier is looked at
+  // before the products of the step before it, and only waited for if it was not complete.
+  uint32_t seen = 0;
   auto s_products = [&](bool last) {
     const int b = st & 1;
     const uint32_t d = __shfl_sync(0xffffffffu, tmem + TM_S(b), 0);
     // Loops kept small: with all 52 products of a tile unrolled the warps' code no longer fits the
     // instruction cache together, and the kernel ran 1.3 times as long.
 #pragma unroll 1
-    for (int i = 0; i < NP; ++i) {
-      if (i % 3 == 0) {
-        if (!c.wait_warp(KF + i / 3, st & 1)) return false;
-        tc_fence_after();
-      }
+    for (int g = 0; g < KGROUPS; ++g) {
+      if (!c.wait_warp(KF + g, st & 1, seen)) return false;
+      tc_fence_after();
+      seen = g + 1 < KGROUPS ? c.look(KF + g + 1, st & 1) : 0;
+#pragma unroll 1
+      for (int i = 3 * g; i < 3 * g + 3; ++i) {
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        const uint64_t off = (uint64_t)((i * QP + kk * 32) >> 4);
-        issue(d, q_desc + off, k_desc + off, IDESC_QK, kk > 0 ? 1u : i > 0 ? 1u : 0u);
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint64_t off = (uint64_t)((i * QP + kk * 32) >> 4);
+          issue(d, q_desc + off, k_desc + off, IDESC_QK, kk > 0 ? 1u : i > 0 ? 1u : 0u);
+        }
       }
-      if (i % 3 == 2) commit_both(c.bar(KE + i / 3));
+      commit_both(c.bar(KE + g));
     }
     commit_both(c.bar(SF + b));
     if (last) commit_both(c.bar(QE));
     ++st;
     return true;
   };
-  auto pv_products = [&](int t, bool first_tile) {
+  auto pv_products = [&](int t, bool first_tile, bool s_next) {
     const uint32_t more = __shfl_sync(0xffffffffu, first_tile ? 0u : 1u, 0);
+    seen = c.look(VF, t & 1);
     if (!c.wait_warp(PR, t & 1)) return false;
 #pragma unroll 1
     for (int i = 0; i < 4; ++i) {   // chunk i / 2, key half i % 2
-      if (!c.wait_warp(VF + i, t & 1)) return false;
+      if (!c.wait_warp(VF + i, t & 1, seen)) return false;
       tc_fence_after();
+      seen = i < 3 ? c.look(VF + i + 1, t & 1) : s_next ? c.look(KF, st & 1) : 0;
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
         const uint64_t po = (uint64_t)(((i & 1) * QP + kk * 32) >> 4);
@@ -486,13 +538,14 @@ __device__ void run_mma(const Ctx& c, const Params& p, Parts parts, uint32_t tme
     const int n = __shfl_sync(0xffffffffu, u.hi - u.lo, 0);
     ok = c.wait_warp(QF, units & 1);
     ++units;
+    seen = 0;
     for (int t = 0; t < n && ok; ++t) {
       // S's buffer held P V(pv - 2)'s scores, read before that tile's P was ready.
       ok = s_products(t == n - 1);
-      if (ok && t > 0) ok = pv_products(pv++, t == 1);
+      if (ok && t > 0) ok = pv_products(pv++, t == 1, t < n - 1);
     }
     // (The next part's Q is only loaded now that S is done: P V does not wait for it.)
-    if (ok) ok = pv_products(pv++, n == 1);
+    if (ok) ok = pv_products(pv++, n == 1, false);
   }
   commit_both(c.bar(FIN));
   c.drain(FIN, 0);
@@ -809,7 +862,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     run_producer_v(c, p, parts, &tm_c, &tm_b, &tm_2);
   } else if (warp == 1) {
     if (rank == 0) run_mma(c, p, parts, tmem);
-  } else if (warp >= 4) {
+  } else if (warp == 3) {
+    run_prefetch(c, p, parts, &tm_b, &tm_3);
+  } else {
     run_softmax(c, p, parts, tmem, ws + WS_SLOTS + (size_t)worker * 2 * SLOT_BYTES, smem);
   }
   __syncwarp();
