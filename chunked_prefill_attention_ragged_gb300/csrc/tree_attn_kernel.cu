@@ -85,7 +85,6 @@ constexpr uint32_t IDESC_QK = idesc_bf16_f32(ROWS, KEYS, false, false);
 constexpr uint32_t IDESC_PV = idesc_bf16_f32(ROWS, 256, false, true);
 constexpr uint64_t DRAIN_LIMIT_NS = 200000000ull;
 constexpr float RESCALE_THRESHOLD = 8.0f;
-constexpr int MIN_TILES = 2;            // fewer tiles than this are not worth another worker
 
 // Workspace: header, one record per worker (where its piece starts), two slots per worker.
 struct Header {
@@ -106,6 +105,7 @@ struct Params {
   TreeParams t;
   int workers;
   int32_t oob_row;     // a row coordinate past the cache: the copy fills it with zeros
+  int block_shift;     // log2 of the block size, or -1
   int piece_rows;      // rows of one box of the block map (0: gather4 only)
   int grouped;         // 64-row boxes over several panels (the three-dimensional maps)
   int o_align32;
@@ -257,39 +257,56 @@ struct Parts {
   }
 };
 
-// Cache row of key position `key`; past the readable ones, or in a block that the table does
-// not name, the row past the cache (read as zeros), the latter flagged.
-__device__ __forceinline__ int32_t key_row(const Params& p, const Part& u, int64_t key) {
-  if (key >= u.q.kv) return p.oob_row;
-  const int k = (int)key, bi = k / p.t.block_size;
-  const int32_t blk = __ldg(p.t.block_table + (int64_t)u.r * p.t.max_blocks + bi);
-  if (blk < 0 || (int64_t)blk >= p.t.num_blocks) {
-    if (p.t.status) atomicOr(p.t.status, MLA_DEVSTAT_BAD_INDEX);
-    return p.oob_row;
-  }
-  return (int32_t)((int64_t)blk * p.t.block_size + (k - bi * p.t.block_size));
-}
-
-// The rows of 64 keys from `key0` on, spread over the lanes, and how they are copied.
+// Where 64 keys from `key0` on are, spread over the lanes: first the blocks as the table has them
+// (the loads are under way while the caller does other things), then the rows to copy.  Whole
+// pieces (by_block) come by boxes, lane k holding piece k; else lanes 0-15 hold keys 4 lane .. + 3
+// each.  A key past the readable ones, or in a block that the table does not name, is the row past
+// the cache (read as zeros), the latter flagged.
+constexpr int32_t PAST_END = -0x7fffffff - 1;
+struct KeyBlocks {
+  int32_t b[4];
+};
 struct KeyRows {
   bool by_block;
-  int32_t piece;       // lane k: row of piece k
-  int32_t r4[4];       // lanes 0-15: rows of keys 4 lane .. 4 lane + 3
+  int32_t r[4];
 };
-__device__ __forceinline__ KeyRows find_rows(const Params& p, const Part& u, int64_t key0, int lane) {
-  KeyRows k;
-  const int pieces = p.piece_rows > 0 ? 64 / p.piece_rows : 0;
-  k.by_block = pieces > 0 && key0 + 64 <= u.q.kv;
-  k.piece = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) k.r4[j] = 0;
-  if (k.by_block) {
-    if (lane < pieces) k.piece = key_row(p, u, key0 + lane * p.piece_rows);
+__device__ __forceinline__ int block_of(const Params& p, int key) {
+  return p.block_shift >= 0 ? key >> p.block_shift : key / p.t.block_size;
+}
+__device__ __forceinline__ bool whole_piece(const Params& p, const Part& u, int64_t key0) {
+  return p.piece_rows > 0 && key0 + 64 <= u.q.kv;
+}
+__device__ __forceinline__ int32_t table_block(const Params& p, const Part& u, int64_t key) {
+  return key < u.q.kv ? __ldg(p.t.block_table + (int64_t)u.r * p.t.max_blocks + block_of(p, (int)key)) : PAST_END;
+}
+__device__ __forceinline__ int32_t block_row(const Params& p, int32_t blk, int64_t key) {
+  if (blk < 0 || (int64_t)blk >= p.t.num_blocks) {
+    if (blk != PAST_END && p.t.status) atomicOr(p.t.status, MLA_DEVSTAT_BAD_INDEX);
+    return p.oob_row;
+  }
+  return (int32_t)((int64_t)blk * p.t.block_size + ((int)key - block_of(p, (int)key) * p.t.block_size));
+}
+__device__ __forceinline__ KeyBlocks find_blocks(const Params& p, const Part& u, int64_t key0, int lane) {
+  KeyBlocks k{{PAST_END, PAST_END, PAST_END, PAST_END}};
+  if (whole_piece(p, u, key0)) {
+    if (lane * p.piece_rows < 64) k.b[0] = table_block(p, u, key0 + lane * p.piece_rows);
   } else if (lane < 16) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) k.r4[j] = key_row(p, u, key0 + 4 * lane + j);
+    for (int j = 0; j < 4; ++j) k.b[j] = table_block(p, u, key0 + 4 * lane + j);
   }
   return k;
+}
+__device__ __forceinline__ KeyRows find_rows(const Params& p, const Part& u, const KeyBlocks& k, int64_t key0,
+                                             int lane) {
+  KeyRows w;
+  w.by_block = whole_piece(p, u, key0);
+  if (w.by_block) {
+    w.r[0] = block_row(p, k.b[0], key0 + lane * p.piece_rows);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w.r[j] = block_row(p, k.b[j], key0 + 4 * lane + j);
+  }
+  return w;
 }
 
 // 64 keys x panels [panel0, panel0 + n) to n consecutive 8 KB panels at dst, completing on `bar`
@@ -298,16 +315,16 @@ __device__ __forceinline__ void copy_panels(const Params& p, const KeyRows& k, u
                                             const CUtensorMap* tc, const CUtensorMap* tb, const CUtensorMap* tg,
                                             int panel0, int n, int lane) {
   if (k.by_block && p.grouped) {
-    if (lane == 0) tma_load_3d_pair(dst, tg, bar, 0, k.piece, panel0);
+    if (lane == 0) tma_load_3d_pair(dst, tg, bar, 0, k.r[0], panel0);
     return;
   }
 #pragma unroll 1
   for (int i = 0; i < n; ++i) {
     const int col = (panel0 + i) * 64;
     if (k.by_block) {
-      if (lane * p.piece_rows < 64) tma_load_2d_pair(dst + i * QP + lane * p.piece_rows * 128, tb, bar, col, k.piece);
+      if (lane * p.piece_rows < 64) tma_load_2d_pair(dst + i * QP + lane * p.piece_rows * 128, tb, bar, col, k.r[0]);
     } else if (lane < 16) {
-      tma_gather4_pair(dst + i * QP + lane * 4 * 128, tc, bar, col, k.r4[0], k.r4[1], k.r4[2], k.r4[3]);
+      tma_gather4_pair(dst + i * QP + lane * 4 * 128, tc, bar, col, k.r[0], k.r[1], k.r[2], k.r[3]);
     }
   }
 }
@@ -335,7 +352,8 @@ __device__ void run_producer_qk(const Ctx& c, const Params& p, Parts parts, cons
   bool ok = true;
   Part u;
   while (ok && parts.next(&u)) {
-    KeyRows k = find_rows(p, u, (int64_t)u.lo * KEYS + 64 * c.rank, lane);
+    int64_t key0 = (int64_t)u.lo * KEYS + 64 * c.rank;
+    KeyBlocks blocks = find_blocks(p, u, key0, lane);
     if (lane == 0) {
       if (units > 0) ok = c.wait(QE, (units - 1) & 1);
       if (ok) {
@@ -347,7 +365,9 @@ __device__ void run_producer_qk(const Ctx& c, const Params& p, Parts parts, cons
     ok = __shfl_sync(0xffffffffu, ok, 0);
     if (!ok) break;
     ++units;
-    for (int t = u.lo; t < u.hi && ok; ++t, ++tiles) {
+    for (int t = u.lo; t < u.hi && ok; ++t, ++tiles, key0 += KEYS) {
+      const KeyRows k = find_rows(p, u, blocks, key0, lane);
+      if (t + 1 < u.hi) blocks = find_blocks(p, u, key0 + KEYS, lane);
 #pragma unroll 1
       for (int g = 0; g < KGROUPS; ++g) {
         if (lane == 0) {
@@ -360,7 +380,6 @@ __device__ void run_producer_qk(const Ctx& c, const Params& p, Parts parts, cons
         ++issued;
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (t + 1 < u.hi) k = find_rows(p, u, (int64_t)(t + 1) * KEYS + 64 * c.rank, lane);
     }
   }
   // Let every copy started here land before the CTA can exit.
@@ -385,9 +404,14 @@ __device__ void run_producer_v(const Ctx& c, const Params& p, Parts parts, const
   bool ok = true;
   Part u;
   while (ok && parts.next(&u)) {
-    KeyRows k0 = find_rows(p, u, (int64_t)u.lo * KEYS, lane);
-    KeyRows k1 = find_rows(p, u, (int64_t)u.lo * KEYS + 64, lane);
-    for (int t = u.lo; t < u.hi && ok; ++t, ++tiles) {
+    int64_t key0 = (int64_t)u.lo * KEYS;
+    KeyBlocks b0 = find_blocks(p, u, key0, lane), b1 = find_blocks(p, u, key0 + 64, lane);
+    for (int t = u.lo; t < u.hi && ok; ++t, ++tiles, key0 += KEYS) {
+      const KeyRows k0 = find_rows(p, u, b0, key0, lane), k1 = find_rows(p, u, b1, key0 + 64, lane);
+      if (t + 1 < u.hi) {
+        b0 = find_blocks(p, u, key0 + KEYS, lane);
+        b1 = find_blocks(p, u, key0 + KEYS + 64, lane);
+      }
       const bool fast = k0.by_block && k1.by_block && p.grouped;
 #pragma unroll 1
       for (int i = 0; i < 4; ++i) {   // chunk i / 2, key half i % 2
@@ -403,10 +427,6 @@ __device__ void run_producer_v(const Ctx& c, const Params& p, Parts parts, const
         ++issued;
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (t + 1 < u.hi) {
-        k0 = find_rows(p, u, (int64_t)(t + 1) * KEYS, lane);
-        k1 = find_rows(p, u, (int64_t)(t + 1) * KEYS + 64, lane);
-      }
     }
   }
   if (lane == 0) {
@@ -433,7 +453,8 @@ __device__ void run_prefetch(const Ctx& c, const Params& p, Parts parts, const C
     for (int t = u.lo; t < u.hi; ++t, ++tiles) {
       const int64_t key0 = (int64_t)(t + 1) * KEYS + 64 * c.rank;
       if (t + 1 < u.hi && key0 + 64 <= u.q.kv && lane < pieces) {
-        const int32_t row = key_row(p, u, key0 + lane * p.piece_rows);
+        const int64_t key = key0 + lane * p.piece_rows;
+        const int32_t row = block_row(p, table_block(p, u, key), key);
         if (p.grouped) {
 #pragma unroll 1
           for (int g = 0; g < KGROUPS; ++g) tma_prefetch_3d(t3, 0, row, 3 * g);
@@ -486,17 +507,26 @@ __device__ void run_mma(const Ctx& c, const Params& p, Parts parts, uint32_t tme
   int st = 0, units = 0;   // S tiles issued
   // A look at a barrier takes about 100 clocks to come back, so each step's barrier is looked at
   // before the products of the step before it, and only waited for if it was not complete.
-  uint32_t seen = 0;
+  // (Each look is of the very phase that the wait it stands for would wait for.)
+  uint32_t seen_k = 0, seen_p = 0, seen_v = 0;   // the next S's first group, the next P V's P and V
+  int pv = 0;              // P V tiles issued: S runs one tile ahead
   auto s_products = [&](bool last) {
     const int b = st & 1;
     const uint32_t d = __shfl_sync(0xffffffffu, tmem + TM_S(b), 0);
     // Loops kept small: with all 52 products of a tile unrolled the warps' code no longer fits the
     // instruction cache together, and the kernel ran 1.3 times as long.
+    uint32_t seen = seen_k;
+    seen_k = 0;
 #pragma unroll 1
     for (int g = 0; g < KGROUPS; ++g) {
       if (!c.wait_warp(KF + g, st & 1, seen)) return false;
       tc_fence_after();
-      seen = g + 1 < KGROUPS ? c.look(KF + g + 1, st & 1) : 0;
+      if (g + 1 < KGROUPS) {
+        seen = c.look(KF + g + 1, st & 1);
+      } else {   // the P V that follows
+        seen_p = c.look(PR, pv & 1);
+        seen_v = c.look(VF, pv & 1);
+      }
 #pragma unroll 1
       for (int i = 3 * g; i < 3 * g + 3; ++i) {
 #pragma unroll
@@ -512,15 +542,18 @@ __device__ void run_mma(const Ctx& c, const Params& p, Parts parts, uint32_t tme
     ++st;
     return true;
   };
-  auto pv_products = [&](int t, bool first_tile, bool s_next) {
+  auto pv_products = [&](bool first_tile, bool s_next) {
+    const int t = pv;
     const uint32_t more = __shfl_sync(0xffffffffu, first_tile ? 0u : 1u, 0);
-    seen = c.look(VF, t & 1);
-    if (!c.wait_warp(PR, t & 1)) return false;
+    uint32_t seen = seen_v;
+    if (!c.wait_warp(PR, t & 1, seen_p)) return false;
+    seen_p = seen_v = 0;
 #pragma unroll 1
     for (int i = 0; i < 4; ++i) {   // chunk i / 2, key half i % 2
       if (!c.wait_warp(VF + i, t & 1, seen)) return false;
       tc_fence_after();
-      seen = i < 3 ? c.look(VF + i + 1, t & 1) : s_next ? c.look(KF, st & 1) : 0;
+      if (i < 3) seen = c.look(VF + i + 1, t & 1);
+      else if (s_next) seen_k = c.look(KF, st & 1);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
         const uint64_t po = (uint64_t)(((i & 1) * QP + kk * 32) >> 4);
@@ -530,22 +563,21 @@ __device__ void run_mma(const Ctx& c, const Params& p, Parts parts, uint32_t tme
       commit_both(c.bar(VE + i));
     }
     commit_both(c.bar(OD));
+    ++pv;
     return true;
   };
-  int pv = 0;   // S runs one tile ahead of P V
   Part u;
   while (ok && parts.next(&u)) {
     const int n = __shfl_sync(0xffffffffu, u.hi - u.lo, 0);
     ok = c.wait_warp(QF, units & 1);
     ++units;
-    seen = 0;
     for (int t = 0; t < n && ok; ++t) {
       // S's buffer held P V(pv - 2)'s scores, read before that tile's P was ready.
       ok = s_products(t == n - 1);
-      if (ok && t > 0) ok = pv_products(pv++, t == 1, t < n - 1);
+      if (ok && t > 0) ok = pv_products(t == 1, t < n - 1);
     }
     // (The next part's Q is only loaded now that S is done: P V does not wait for it.)
-    if (ok) ok = pv_products(pv++, n == 1, false);
+    if (ok) ok = pv_products(n == 1, false);
   }
   commit_both(c.bar(FIN));
   c.drain(FIN, 0);
@@ -788,7 +820,7 @@ __device__ void find_piece(const TreeParams& p, int worker, int workers, bool re
     if (w < warp) before += warp_sum[w];
     total += warp_sum[w];
   }
-  const int n = (int)min((int64_t)workers, (total + MIN_TILES - 1) / MIN_TILES);
+  const int n = (int)min((int64_t)workers, total);   // a tile is worth a worker (700 keys: 26 us, two tiles each: 30)
   const int64_t lo = worker < n ? total * worker / n : total, hi = worker < n ? total * (worker + 1) / n : total;
   if (tid == 0) {
     *count = hi - lo;
@@ -1021,6 +1053,9 @@ cudaError_t launch_tree_attention(const TreeParams& t, cudaStream_t stream) {
   // one box by a map of the rows as {64 columns, rows, 9 column groups}.
   p.piece_rows = !any ? 0 : (bs % 64 == 0) ? 64 : (bs % 8 == 0 && 64 % bs == 0) ? bs : 0;
   p.grouped = p.piece_rows == 64;
+  p.block_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (bs == 1 << i) p.block_shift = i;
   tb = t2 = t3 = tc;
   if (p.piece_rows > 0) {
     const uint64_t dims[2] = {576, slots}, strides[1] = {576 * 2};
