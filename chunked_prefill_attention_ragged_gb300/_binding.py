@@ -538,29 +538,76 @@ def mla_prefill_run_noalloc(qo_indptr, kv_indptr, num_heads: int, q, k, v, o, ls
 
 
 # ---------------------------------------------------------------------------- speculative decoding
-def _on_device(stream, **tensors):
-    """Every given tensor, and the stream, belong to the current device (kernels launch there);
-    returns a context that allocates in the stream's order."""
+# These calls are made once per step or layer on a few rows, so the time to make them counts
+# (about 2 us of launch each): one look per tensor, the raw current stream, no context manager
+# unless a stream is given.
+def _bad_tensor(t, dtype, dev, name):
     import torch
-    for name, t in tensors.items():
-        if t is not None and not (isinstance(t, torch.Tensor) and t.is_cuda):
-            raise TypeError(f"{name} must be a CUDA tensor")
-    dev = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"{name} is on cuda:{t.device.index}, the current device is cuda:{dev}")
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _arg(t, dtype, dev, name, shape=None):
+    """Address of a contiguous tensor of this type (and shape) on the current device; None for None."""
+    if t is None:
+        return None
+    try:
+        ok = t.dtype is dtype and t.get_device() == dev and dev >= 0 and t.is_contiguous()
+    except AttributeError:
+        ok = False
+    if not ok:
+        _bad_tensor(t, dtype, dev, name)
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+class _Torch:
+    """What these calls use of torch, looked up once (the module is imported by the first call)."""
+
+    def __init__(self):
+        import torch
+        self.int32, self.int64, self.uint8 = torch.int32, torch.int64, torch.uint8
+        self.bf16, self.f32 = torch.bfloat16, torch.float32
+        self.empty = torch.empty
+        self.device, self.raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+_torch_parts = None
+
+
+def _here(stream, t, name):
+    """(torch parts, current device, stream object or None, its handle); t: a tensor without
+    which the call means nothing."""
+    global _torch_parts
+    if not getattr(t, "is_cuda", False):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    T = _torch_parts
+    if T is None:
+        T = _torch_parts = _Torch()
+    dev = T.device()
     if stream is None:
-        return torch.cuda.stream(None)
+        return T, dev, None, T.raw_stream(dev)
     if not hasattr(stream, "cuda_stream"):
+        import torch
         stream = torch.cuda.ExternalStream(int(stream))
     elif stream.device.index != dev:
         raise ValueError(f"stream is on cuda:{stream.device.index}, the current device is cuda:{dev}")
-    return torch.cuda.stream(stream)
+    return T, dev, stream, stream.cuda_stream
 
 
-def _shape(t, shape, name):
-    if t is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+def _new(T, shape, dtype, device, stream):
+    """Memory in the order of the stream that the kernels are launched on."""
+    if stream is None:
+        return T.empty(shape, dtype=dtype, device=device)
+    import torch
+    with torch.cuda.stream(stream):
+        return T.empty(shape, dtype=dtype, device=device)
 
 
 def mla_block_table_update(seq_lens, new_lens, block_table, num_held, free_blocks, free_count, block_size: int,
@@ -570,34 +617,25 @@ def mla_block_table_update(seq_lens, new_lens, block_table, num_held, free_block
     giving them back to the stack free_blocks / free_count; block_table, num_held, free_blocks
     and free_count are updated in place.  Returns (qo_indptr [B+1], kv_lens [B], slot_mapping
     [num_tokens] int64), the new tokens' prefix sums, the lengths with them, and their slots."""
-    import torch
-    with _on_device(stream, seq_lens=seq_lens, new_lens=new_lens, block_table=block_table, num_held=num_held,
-                    free_blocks=free_blocks, free_count=free_count, qo_indptr=qo_indptr, kv_lens=kv_lens,
-                    slot_mapping=slot_mapping, status=status):
-        i32 = torch.int32
-        b, n = seq_lens.shape[0], int(num_tokens)
-        if block_table.dim() != 2 or free_blocks.dim() != 1:
-            raise ValueError("block_table must be [B, M] and free_blocks [N]")
-        m = block_table.shape[1]
-        for t, shape, name in ((seq_lens, (b,), "seq_lens"), (new_lens, (b,), "new_lens"), (num_held, (b,), "num_held"),
-                               (block_table, (b, m), "block_table"), (free_count, (1,), "free_count"),
-                               (qo_indptr, (b + 1,), "qo_indptr"), (kv_lens, (b,), "kv_lens"),
-                               (slot_mapping, (n,), "slot_mapping")):
-            _shape(t, shape, name)
-        dev = block_table.device
-        if qo_indptr is None:
-            qo_indptr = torch.empty(b + 1, dtype=i32, device=dev)
-        if kv_lens is None:
-            kv_lens = torch.empty(b, dtype=i32, device=dev)
-        if slot_mapping is None:
-            slot_mapping = torch.empty(n, dtype=torch.int64, device=dev)
-        _check(library().mla_block_table_update(
-            _dev(seq_lens, i32, "seq_lens"), _dev(new_lens, i32, "new_lens"), b, int(block_size),
-            _dev(block_table, i32, "block_table"), m, _dev(num_held, i32, "num_held"),
-            _dev(free_blocks, i32, "free_blocks"), free_blocks.shape[0], _dev(free_count, i32, "free_count"),
-            _dev(qo_indptr, i32, "qo_indptr"), _dev(kv_lens, i32, "kv_lens"),
-            _dev(slot_mapping, torch.int64, "slot_mapping"), n, _dev(status, i32, "status"), _stream(None)),
-            "mla_block_table_update")
+    T, dev, st, handle = _here(stream, block_table, "block_table")
+    int32, int64 = T.int32, T.int64
+    if seq_lens.dim() != 1 or block_table.dim() != 2 or free_blocks.dim() != 1:
+        raise ValueError("seq_lens must be [B], block_table [B, M] and free_blocks [N]")
+    b, n, m = seq_lens.shape[0], int(num_tokens), block_table.shape[1]
+    device = block_table.device
+    if qo_indptr is None:
+        qo_indptr = _new(T, (b + 1,), int32, device, st)
+    if kv_lens is None:
+        kv_lens = _new(T, (b,), int32, device, st)
+    if slot_mapping is None:
+        slot_mapping = _new(T, (n,), int64, device, st)
+    _check((_lib or library()).mla_block_table_update(
+        _arg(seq_lens, int32, dev, "seq_lens"), _arg(new_lens, int32, dev, "new_lens", (b,)), b, int(block_size),
+        _arg(block_table, int32, dev, "block_table", (b, m)), m, _arg(num_held, int32, dev, "num_held", (b,)),
+        _arg(free_blocks, int32, dev, "free_blocks"), free_blocks.shape[0],
+        _arg(free_count, int32, dev, "free_count", (1,)), _arg(qo_indptr, int32, dev, "qo_indptr", (b + 1,)),
+        _arg(kv_lens, int32, dev, "kv_lens", (b,)), _arg(slot_mapping, int64, dev, "slot_mapping", (n,)), n,
+        _arg(status, int32, dev, "status"), handle), "mla_block_table_update")
     return qo_indptr, kv_lens, slot_mapping
 
 
@@ -606,25 +644,23 @@ def mla_tree_mask(parents, qo_indptr, mask_words: int, kv_lens=None, mask=None, 
     """Trees given by parents [T] (node indices inside the request, -1: child of the context)
     -> (mask [T, mask_words] int64 of visibility bits, positions [T] int32: depth, plus the
     context length when kv_lens is given)."""
-    import torch
-    with _on_device(stream, parents=parents, qo_indptr=qo_indptr, kv_lens=kv_lens, mask=mask, positions=positions,
-                    status=status):
-        i32 = torch.int32
-        t, b, w = parents.shape[0], qo_indptr.shape[0] - 1, int(mask_words)
-        if b < 0 or w < 1:
-            raise ValueError("qo_indptr must be [B+1] and mask_words at least 1")
-        for x, shape, name in ((parents, (t,), "parents"), (qo_indptr, (b + 1,), "qo_indptr"), (kv_lens, (b,), "kv_lens"),
-                               (mask, (t, w), "mask"), (positions, (t,), "positions")):
-            _shape(x, shape, name)
-        if mask is None:
-            mask = torch.empty((t, w), dtype=torch.int64, device=parents.device)
-        if positions is None:
-            positions = torch.empty(t, dtype=i32, device=parents.device)
-        _check(library().mla_tree_mask(_dev(parents, i32, "parents"), _dev(qo_indptr, i32, "qo_indptr"),
-                                       _dev(kv_lens, i32, "kv_lens"), b, t, w, _dev(mask, torch.int64, "mask"),
-                                       _dev(positions, i32, "positions"), _dev(status, i32, "status"), _stream(None)),
-               "mla_tree_mask")
+    T, dev, st, handle = _here(stream, parents, "parents")
+    int32, int64 = T.int32, T.int64
+    t, b, w = parents.shape[0], qo_indptr.shape[0] - 1, int(mask_words)
+    if parents.dim() != 1 or qo_indptr.dim() != 1 or b < 0 or w < 1:
+        raise ValueError("parents must be [T], qo_indptr [B+1] and mask_words at least 1")
+    if mask is None:
+        mask = _new(T, (t, w), int64, parents.device, st)
+    if positions is None:
+        positions = _new(T, (t,), int32, parents.device, st)
+    _check((_lib or library()).mla_tree_mask(
+        _arg(parents, int32, dev, "parents"), _arg(qo_indptr, int32, dev, "qo_indptr"),
+        _arg(kv_lens, int32, dev, "kv_lens", (b,)), b, t, w, _arg(mask, int64, dev, "mask", (t, w)),
+        _arg(positions, int32, dev, "positions", (t,)), _arg(status, int32, dev, "status"), handle), "mla_tree_mask")
     return mask, positions
+
+
+_workspace_bytes: dict = {}   # device index -> bytes (a fact of the device)
 
 
 def mla_tree_workspace(total_rows: int, num_heads: int) -> int:
@@ -642,37 +678,36 @@ def mla_tree_attention(q_abs, cache, block_table, qo_indptr, kv_lens, tree_mask=
     device), tree_mask [T, W] int64 from mla_tree_mask (None: each node sees those before it)
     -> (o_lat [T, H, 512] bf16, lse [T, H] fp32 or None).  The workspace (uint8) is allocated
     for the call when not given; one that is given must not serve two calls at a time."""
-    import torch
-    with _on_device(stream, q_abs=q_abs, cache=cache, block_table=block_table, qo_indptr=qo_indptr, kv_lens=kv_lens,
-                    tree_mask=tree_mask, o=o, lse=lse, workspace=workspace, status=status):
-        bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
-        if q_abs.dim() != 3 or q_abs.shape[2] != 576 or cache.dim() != 3 or cache.shape[2] != 576:
-            raise ValueError("q_abs must be [T, H, 576] and cache [NB, BS, 576]")
-        if block_table.dim() != 2:
-            raise ValueError("block_table must be [B, M]")
-        t, h = q_abs.shape[0], q_abs.shape[1]
-        b, m = block_table.shape
-        _shape(qo_indptr, (b + 1,), "qo_indptr")
-        _shape(kv_lens, (b,), "kv_lens")
-        words = 0
-        if tree_mask is not None:
-            if tree_mask.dim() != 2 or tree_mask.shape[0] != t or tree_mask.shape[1] < 1:
-                raise ValueError(f"tree_mask must be [{t}, words], got {list(tree_mask.shape)}")
-            words = tree_mask.shape[1]
-        _shape(o, (t, h, 512), "o")
-        _shape(lse, (t, h), "lse")
-        if o is None:
-            o = torch.empty((t, h, 512), dtype=bf, device=q_abs.device)
-        if return_lse and lse is None:
-            lse = torch.empty((t, h), dtype=f32, device=q_abs.device)
-        if workspace is None:
-            workspace = torch.empty(mla_tree_workspace(t, h), dtype=torch.uint8, device=q_abs.device)
-        _check(library().mla_tree_attention(
-            _dev(q_abs, bf, "q_abs"), _dev(cache, bf, "cache"), cache.shape[0], cache.shape[1],
-            _dev(block_table, i32, "block_table"), m, _dev(qo_indptr, i32, "qo_indptr"), _dev(kv_lens, i32, "kv_lens"),
-            _dev(tree_mask, torch.int64, "tree_mask"), words, b, t, h, float(sm_scale), float(logits_soft_cap),
-            _dev(o, bf, "o"), _dev(lse, f32, "lse"), _dev(workspace, torch.uint8, "workspace"),
-            workspace.numel(), _dev(status, i32, "status"), _stream(None)), "mla_tree_attention")
+    T, dev, st, handle = _here(stream, q_abs, "q_abs")
+    int32, bfloat16, float32, uint8 = T.int32, T.bf16, T.f32, T.uint8
+    if q_abs.dim() != 3 or q_abs.shape[2] != 576 or cache.dim() != 3 or cache.shape[2] != 576:
+        raise ValueError("q_abs must be [T, H, 576] and cache [NB, BS, 576]")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, M]")
+    t, h, _ = q_abs.shape
+    b, m = block_table.shape
+    words = 0
+    if tree_mask is not None:
+        if tree_mask.dim() != 2 or tree_mask.shape[0] != t or tree_mask.shape[1] < 1:
+            raise ValueError(f"tree_mask must be [{t}, words], got {list(tree_mask.shape)}")
+        words = tree_mask.shape[1]
+    device = q_abs.device
+    if o is None:
+        o = _new(T, (t, h, 512), bfloat16, device, st)
+    if return_lse and lse is None:
+        lse = _new(T, (t, h), float32, device, st)
+    if workspace is None:
+        n = _workspace_bytes.get(dev)
+        if n is None:
+            n = _workspace_bytes[dev] = mla_tree_workspace(t, h)
+        workspace = _new(T, (n,), uint8, device, st)
+    _check((_lib or library()).mla_tree_attention(
+        _arg(q_abs, bfloat16, dev, "q_abs"), _arg(cache, bfloat16, dev, "cache"), cache.shape[0], cache.shape[1],
+        _arg(block_table, int32, dev, "block_table"), m, _arg(qo_indptr, int32, dev, "qo_indptr", (b + 1,)),
+        _arg(kv_lens, int32, dev, "kv_lens", (b,)), _arg(tree_mask, T.int64, dev, "tree_mask"), words, b, t, h,
+        float(sm_scale), float(logits_soft_cap), _arg(o, bfloat16, dev, "o", (t, h, 512)),
+        _arg(lse, float32, dev, "lse", (t, h)), _arg(workspace, uint8, dev, "workspace"), workspace.numel(),
+        _arg(status, int32, dev, "status"), handle), "mla_tree_attention")
     return o, lse
 
 
@@ -680,21 +715,17 @@ def mla_tree_commit(cache, block_table, seq_lens, accepted, accepted_counts, sta
     """Move the rows of accepted nodes (accepted [B, A] int32, the first accepted_counts[r] of a
     row, strictly increasing) from position seq_lens[r] + node to seq_lens[r] + i, in cache
     [NB, BS, E] or, all layers at once, [L, NB, BS, E].  Returns the cache (written in place)."""
-    import torch
-    with _on_device(stream, cache=cache, block_table=block_table, seq_lens=seq_lens, accepted=accepted,
-                    accepted_counts=accepted_counts, status=status):
-        i32 = torch.int32
-        if cache.dim() not in (3, 4) or block_table.dim() != 2 or accepted.dim() != 2:
-            raise ValueError("cache must be [NB, BS, E] or [L, NB, BS, E], block_table [B, M], accepted [B, A]")
-        layers = cache.shape[0] if cache.dim() == 4 else 1
-        nb, bs, e = cache.shape[-3:]
-        b, m = block_table.shape
-        a = accepted.shape[1]
-        for x, shape, name in ((seq_lens, (b,), "seq_lens"), (accepted, (b, a), "accepted"),
-                               (accepted_counts, (b,), "accepted_counts")):
-            _shape(x, shape, name)
-        _check(library().mla_tree_commit(_dev(cache, torch.bfloat16, "cache"), layers, nb * bs * e, nb, bs, e,
-                                         _dev(block_table, i32, "block_table"), m, _dev(seq_lens, i32, "seq_lens"),
-                                         _dev(accepted, i32, "accepted"), _dev(accepted_counts, i32, "accepted_counts"),
-                                         b, a, _dev(status, i32, "status"), _stream(None)), "mla_tree_commit")
+    T, dev, _, handle = _here(stream, cache, "cache")
+    int32, bfloat16 = T.int32, T.bf16
+    if cache.dim() not in (3, 4) or block_table.dim() != 2 or accepted.dim() != 2:
+        raise ValueError("cache must be [NB, BS, E] or [L, NB, BS, E], block_table [B, M], accepted [B, A]")
+    layers = cache.shape[0] if cache.dim() == 4 else 1
+    nb, bs, e = cache.shape[-3:]
+    b, m = block_table.shape
+    a = accepted.shape[1]
+    _check((_lib or library()).mla_tree_commit(
+        _arg(cache, bfloat16, dev, "cache"), layers, nb * bs * e, nb, bs, e,
+        _arg(block_table, int32, dev, "block_table"), m, _arg(seq_lens, int32, dev, "seq_lens", (b,)),
+        _arg(accepted, int32, dev, "accepted", (b, a)), _arg(accepted_counts, int32, dev, "accepted_counts", (b,)),
+        b, a, _arg(status, int32, dev, "status"), handle), "mla_tree_commit")
     return cache
