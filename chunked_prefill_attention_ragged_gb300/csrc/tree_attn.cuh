@@ -1,0 +1,308 @@
+// What the kernels of tree attention share: the requests as they see them, the split of the
+// work among workers, the way from key positions to cache rows, visibility, and waits.
+#pragma once
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace mla {
+
+struct TreeLaunch {
+  TreeParams t;
+  int workers;
+  int32_t oob_row;     // a row coordinate past the cache: the copy fills it with zeros
+  int block_shift;     // log2 of the block size, or -1
+  int piece_rows;      // rows of one box of the block map (0: gather4 only)
+  int grouped;         // 64-row boxes over several panels (the three-dimensional maps)
+  int o_align32;
+  int has_cap;
+  float scale_log2, cap_log2, cap_ex2_scale;
+  uint64_t wait_limit_ns;
+  int force_timeout;
+};
+
+// Workspace: header, one record per worker (where its piece starts), two slots per worker.
+struct Header {
+  int64_t total;       // tiles of all units
+  int workers;         // that share them
+  int pad;
+};
+struct StartRec {
+  int req, unit, tile, pad;
+};
+constexpr int MAX_WORKERS = 256;
+constexpr size_t WS_STARTS = 64;
+constexpr size_t WS_SLOTS = (WS_STARTS + MAX_WORKERS * sizeof(StartRec) + 255) / 256 * 256;
+// A slot: the rows' O (fp32), then their (m in log2 units, l).
+__host__ __device__ constexpr size_t slot_ml(int rows) { return (size_t)rows * 512 * 4; }
+__host__ __device__ constexpr size_t slot_bytes(int rows) { return slot_ml(rows) + (size_t)rows * 2 * 4; }
+
+// One lane's look at a barrier, whose result can be used later; for wait_warp's `seen`.
+__device__ __forceinline__ uint32_t look_warp(uint32_t bar, uint32_t parity) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, 0, 0;\n\t"
+      "@e mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return r;
+}
+
+// A bounded wait of a converged warp, polled by one lane: 32 lanes polling, in five warps that
+// wait most of the time, slow the softmax's exponentials down (they share the queue to the
+// special function units and shared memory).
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status,
+                                          uint64_t limit_ns, uint32_t seen = 0) {
+  if (__any_sync(0xffffffffu, seen != 0)) {
+    __syncwarp();
+    return true;
+  }
+  auto poll = [&]() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, 0, 0;\n\t"
+        "@e mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(r)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return __any_sync(0xffffffffu, r != 0) != 0;
+  };
+  bool ok = poll();
+  if (!ok) {
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t it = 1;; ++it) {
+      ok = poll();
+      if (ok) break;
+      if ((it & 63) == 0) {
+        const bool late = global_timer_ns() - t0 > limit_ns;
+        if (__any_sync(0xffffffffu, late || *abort_flag)) {
+          if (late) {
+            *abort_flag = 1;
+            if (status) atomicOr(status, MLA_DEVSTAT_TIMEOUT);
+          }
+          break;
+        }
+      }
+    }
+  }
+  __syncwarp();   // what the polling lane acquired, all lanes see
+  return ok;
+}
+
+// One request as the kernel sees it.
+struct Req {
+  int q0, nodes;       // rows; 0 nodes when the request is empty or refused
+  int64_t ctx;         // positions every node sees (negative: the first nodes are not cached)
+  int kv;              // positions that may be read
+  int units, tiles;
+};
+
+// ROWS pairs a unit, KEYS keys a tile.
+template <int ROWS, int KEYS>
+__device__ __forceinline__ Req load_req(const TreeParams& p, int r, bool report) {
+  Req q;
+  const int q0 = __ldg(p.qo_indptr + r), q1 = __ldg(p.qo_indptr + r + 1), len = __ldg(p.kv_lens + r);
+  const int64_t reach = (int64_t)p.max_blocks * p.block_size;
+  const bool rows_ok = q0 >= 0 && q1 >= q0 && q1 <= p.total_rows;
+  const bool len_ok = len >= 0 && len <= reach;
+  if (report && p.status && (!rows_ok || !len_ok)) atomicOr(p.status, MLA_DEVSTAT_BAD_INDEX);
+  q.q0 = q0;
+  q.nodes = rows_ok ? q1 - q0 : 0;
+  q.ctx = (int64_t)len - q.nodes;
+  q.kv = len_ok ? len : (len < 0 ? 0 : (int)reach);
+  q.units = (int)(((int64_t)q.nodes * p.num_heads + ROWS - 1) / ROWS);
+  q.tiles = q.units ? max(1, (q.kv + KEYS - 1) / KEYS) : 0;
+  return q;
+}
+
+// A part of a worker's piece: tiles [lo, hi) of one unit.
+struct Part {
+  Req q;
+  int r;
+  int64_t pair0;       // first pair of the unit, counted over the batch
+  int npairs;
+  int lo, hi;
+  bool whole;          // the unit's every tile
+  int slot;            // 0: the worker's first part, 1: a later one (its last, if not whole)
+};
+
+template <int ROWS, int KEYS>
+struct Parts {
+  const TreeParams& p;
+  int64_t left;
+  int r, unit, tile, index;
+  Req q;
+  __device__ Parts(const TreeParams& tp, const StartRec& s, int64_t count)
+      : p(tp), left(count), r(s.req), unit(s.unit), tile(s.tile), index(0) {
+    if (left > 0) q = load_req<ROWS, KEYS>(p, r, false);
+  }
+  __device__ bool next(Part* out) {
+    if (left <= 0) return false;
+    while (unit >= q.units) {   // to the next request that has rows
+      if (++r >= p.batch) return false;   // (lengths changed under the kernel: out of bounds is not read)
+      unit = 0;
+      q = load_req<ROWS, KEYS>(p, r, false);
+    }
+    const int n = (int)min((int64_t)(q.tiles - tile), left);
+    out->q = q;
+    out->r = r;
+    const int64_t first = (int64_t)unit * ROWS;
+    out->pair0 = (int64_t)q.q0 * p.num_heads + first;
+    out->npairs = (int)min((int64_t)ROWS, (int64_t)q.nodes * p.num_heads - first);
+    out->lo = tile;
+    out->hi = tile + n;
+    out->whole = n == q.tiles;
+    out->slot = index == 0 ? 0 : 1;
+    ++index;
+    left -= n;
+    tile = 0;
+    ++unit;
+    return true;
+  }
+};
+
+// Where 64 keys from `key0` on are, spread over the lanes: first the blocks as the table has them
+// (the loads are under way while the caller does other things), then the rows to copy.  Whole
+// pieces (by_block) come by boxes, lane k holding piece k; else lanes 0-15 hold keys 4 lane .. + 3
+// each.  A key past the readable ones, or in a block that the table does not name, is the row past
+// the cache (read as zeros), the latter flagged.
+constexpr int32_t PAST_END = -0x7fffffff - 1;
+struct KeyBlocks {
+  int32_t b[4];
+};
+struct KeyRows {
+  bool by_block;
+  int32_t r[4];
+};
+__device__ __forceinline__ int block_of(const TreeLaunch& p, int key) {
+  return p.block_shift >= 0 ? key >> p.block_shift : key / p.t.block_size;
+}
+__device__ __forceinline__ bool whole_piece(const TreeLaunch& p, const Part& u, int64_t key0) {
+  return p.piece_rows > 0 && key0 + 64 <= u.q.kv;
+}
+__device__ __forceinline__ int32_t table_block(const TreeLaunch& p, const Part& u, int64_t key) {
+  return key < u.q.kv ? __ldg(p.t.block_table + (int64_t)u.r * p.t.max_blocks + block_of(p, (int)key)) : PAST_END;
+}
+__device__ __forceinline__ int32_t block_row(const TreeLaunch& p, int32_t blk, int64_t key) {
+  if (blk < 0 || (int64_t)blk >= p.t.num_blocks) {
+    if (blk != PAST_END && p.t.status) atomicOr(p.t.status, MLA_DEVSTAT_BAD_INDEX);
+    return p.oob_row;
+  }
+  return (int32_t)((int64_t)blk * p.t.block_size + ((int)key - block_of(p, (int)key) * p.t.block_size));
+}
+__device__ __forceinline__ KeyBlocks find_blocks(const TreeLaunch& p, const Part& u, int64_t key0, int lane) {
+  KeyBlocks k{{PAST_END, PAST_END, PAST_END, PAST_END}};
+  if (whole_piece(p, u, key0)) {
+    if (lane * p.piece_rows < 64) k.b[0] = table_block(p, u, key0 + lane * p.piece_rows);
+  } else if (lane < 16) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) k.b[j] = table_block(p, u, key0 + 4 * lane + j);
+  }
+  return k;
+}
+__device__ __forceinline__ KeyRows find_rows(const TreeLaunch& p, const Part& u, const KeyBlocks& k, int64_t key0,
+                                             int lane) {
+  KeyRows w;
+  w.by_block = whole_piece(p, u, key0);
+  if (w.by_block) {
+    w.r[0] = block_row(p, k.b[0], key0 + lane * p.piece_rows);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w.r[j] = block_row(p, k.b[j], key0 + 4 * lane + j);
+  }
+  return w;
+}
+
+// Visibility of 64 keys from position pos0 on for node i (row t of the batch), bit k for key k.
+__device__ __forceinline__ uint64_t visible(const TreeParams& p, const Part& u, int i, int64_t pos0) {
+  auto window = [&](int64_t j0) -> uint64_t {   // nodes j0 .. j0 + 63, j0 >= 0
+    if (!p.mask) {
+      const int64_t n = (int64_t)i - j0 + 1;
+      return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
+    }
+    const int64_t* row = p.mask + ((int64_t)u.q.q0 + i) * p.mask_words;
+    const int64_t w = j0 >> 6;
+    const int sh = (int)(j0 & 63);
+    uint64_t bits = w < p.mask_words ? (uint64_t)__ldg(row + w) >> sh : 0ull;
+    if (sh && w + 1 < p.mask_words) bits |= (uint64_t)__ldg(row + w + 1) << (64 - sh);
+    return bits;
+  };
+  const int64_t s = pos0 - u.q.ctx;   // node index of the first key
+  uint64_t v;
+  if (s <= -64) v = ~0ull;
+  else if (s >= 0) v = window(s);
+  else v = ((1ull << -s) - 1) | (window(0) << -s);
+  const int64_t room = u.q.kv - pos0;
+  if (room < 64) v &= room <= 0 ? 0ull : (1ull << room) - 1;
+  return v;
+}
+
+// Where worker w's piece starts, and how long it is; every thread of the CTA calls.
+template <int ROWS, int KEYS, int NTHREADS>
+__device__ __forceinline__ void find_piece(const TreeParams& p, int worker, int workers, bool report, StartRec* start,
+                           int64_t* count, Header* head) {
+  __shared__ int64_t warp_sum[NTHREADS / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.batch + NTHREADS - 1) / NTHREADS;
+  const int r0 = min(tid * per, p.batch), r1 = min(r0 + per, p.batch);
+  int64_t mine = 0;
+  for (int r = r0; r < r1; ++r) {
+    const Req q = load_req<ROWS, KEYS>(p, r, report);
+    mine += (int64_t)q.units * q.tiles;
+  }
+  int64_t incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  int64_t before = incl - mine, total = 0;
+  for (int w = 0; w < NTHREADS / 32; ++w) {
+    if (w < warp) before += warp_sum[w];
+    total += warp_sum[w];
+  }
+  const int n = (int)min((int64_t)workers, total);   // a tile is worth a worker (700 keys: 26 us, two tiles each: 30)
+  const int64_t lo = worker < n ? total * worker / n : total, hi = worker < n ? total * (worker + 1) / n : total;
+  if (tid == 0) {
+    *count = hi - lo;
+    *head = Header{total, n, 0};
+  }
+  if (lo < hi && lo >= before && lo < before + mine) {
+    int64_t at = before;
+    for (int r = r0; r < r1; ++r) {
+      const Req q = load_req<ROWS, KEYS>(p, r, false);
+      const int64_t k = (int64_t)q.units * q.tiles;
+      if (lo < at + k) {
+        *start = StartRec{r, (int)((lo - at) / q.tiles), (int)((lo - at) % q.tiles), 0};
+        break;
+      }
+      at += k;
+    }
+  }
+  __syncthreads();
+}
+
+
+// tree_join_kernel.cu: joins the parts of units of `rows` pairs and tiles of `keys` keys
+// (128 x 128, or 16, 32 or 64 x 64) that several workers left.
+cudaError_t launch_tree_join(const TreeLaunch& p, int rows, cudaStream_t stream);
+
+// tree_few_kernel.cu: units of 16, 32 or 64 pairs.  Workers (0 on error), and the launch.
+int tree_few_workers();
+cudaError_t launch_tree_few(const TreeLaunch& p, int rows, const CUtensorMap& tq, const CUtensorMap& tc,
+                            const CUtensorMap& tb, const CUtensorMap& t2, cudaStream_t stream);
+
+constexpr uint64_t TREE_DRAIN_LIMIT_NS = 200000000ull;   // own copies and products after an abort
+constexpr float TREE_RESCALE_THRESHOLD = 8.0f;           // log2 units
+
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+}  // namespace mla

@@ -43,6 +43,7 @@
 #include "internal.h"
 #include "ptx.cuh"
 #include "tmem_wide.cuh"
+#include "tree_attn.cuh"
 
 namespace mla {
 namespace {
@@ -83,37 +84,8 @@ __device__ __forceinline__ constexpr uint32_t TM_O(int chunk) { return (uint32_t
 __device__ __forceinline__ constexpr uint32_t TM_S(int b) { return 256u + (uint32_t)b * 64u; }
 constexpr uint32_t IDESC_QK = idesc_bf16_f32(ROWS, KEYS, false, false);
 constexpr uint32_t IDESC_PV = idesc_bf16_f32(ROWS, 256, false, true);
-constexpr uint64_t DRAIN_LIMIT_NS = 200000000ull;
-constexpr float RESCALE_THRESHOLD = 8.0f;
-
-// Workspace: header, one record per worker (where its piece starts), two slots per worker.
-struct Header {
-  int64_t total;       // tiles of all units
-  int workers;         // that share them
-  int pad;
-};
-struct StartRec {
-  int req, unit, tile, pad;
-};
-constexpr int MAX_WORKERS = 256;
-constexpr size_t WS_STARTS = 64;
-constexpr size_t WS_SLOTS = (WS_STARTS + MAX_WORKERS * sizeof(StartRec) + 255) / 256 * 256;
-constexpr size_t SLOT_ML = (size_t)ROWS * 512 * 4;
-constexpr size_t SLOT_BYTES = SLOT_ML + ROWS * 2 * 4;
-
-struct Params {
-  TreeParams t;
-  int workers;
-  int32_t oob_row;     // a row coordinate past the cache: the copy fills it with zeros
-  int block_shift;     // log2 of the block size, or -1
-  int piece_rows;      // rows of one box of the block map (0: gather4 only)
-  int grouped;         // 64-row boxes over several panels (the three-dimensional maps)
-  int o_align32;
-  int has_cap;
-  float scale_log2, cap_log2, cap_ex2_scale;
-  uint64_t wait_limit_ns;
-  int force_timeout;
-};
+constexpr size_t SLOT_BYTES = slot_bytes(ROWS), SLOT_ML = slot_ml(ROWS);
+using PairParts = Parts<ROWS, KEYS>;
 
 struct Ctx {
   uint32_t sbase;
@@ -125,193 +97,19 @@ struct Ctx {
   __device__ bool wait(int b, uint32_t parity) const {
     return mbar_wait_bounded(bar(b), parity, abort_flag, status, MLA_DEVSTAT_TIMEOUT, wait_limit_ns);
   }
-  // One lane's look at a barrier, whose result can be used later; for wait_warp's `seen`.
-  __device__ uint32_t look(int b, uint32_t parity) const {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "setp.ne.b32 p, 0, 0;\n\t"
-        "@e mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(r)
-        : "r"(bar(b)), "r"(parity)
-        : "memory");
-    return r;
-  }
-  // The same for a converged warp, polled by one lane: 32 lanes polling, in five warps that wait
-  // most of the time, slow the softmax's exponentials down (they share the queue to the special
-  // function units and shared memory).
+  __device__ uint32_t look(int b, uint32_t parity) const { return look_warp(bar(b), parity); }
   __device__ bool wait_warp(int b, uint32_t parity, uint32_t seen = 0) const {
-    if (__any_sync(0xffffffffu, seen != 0)) {
-      __syncwarp();
-      return true;
-    }
-    const uint32_t a = bar(b);
-    auto poll = [&]() {
-      uint32_t r;
-      asm volatile(
-          "{\n\t.reg .pred p, e;\n\t"
-          "elect.sync _|e, 0xffffffff;\n\t"
-          "setp.ne.b32 p, 0, 0;\n\t"
-          "@e mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}\n"
-          : "=r"(r)
-          : "r"(a), "r"(parity)
-          : "memory");
-      return __any_sync(0xffffffffu, r != 0) != 0;
-    };
-    bool ok = poll();
-    if (!ok) {
-      const uint64_t t0 = global_timer_ns();
-      for (uint32_t it = 1;; ++it) {
-        ok = poll();
-        if (ok) break;
-        if ((it & 63) == 0) {
-          const bool late = global_timer_ns() - t0 > wait_limit_ns;
-          if (__any_sync(0xffffffffu, late || *abort_flag)) {
-            if (late) {
-              *abort_flag = 1;
-              if (status) atomicOr(status, MLA_DEVSTAT_TIMEOUT);
-            }
-            break;
-          }
-        }
-      }
-    }
-    __syncwarp();   // what the polling lane acquired, all lanes see
-    return ok;
+    return mla::wait_warp(bar(b), parity, abort_flag, status, wait_limit_ns, seen);
   }
   __device__ void drain(int b, uint32_t parity) const {
     int dummy = 0;
-    mbar_wait_bounded(bar(b), parity, &dummy, status, MLA_DEVSTAT_TIMEOUT, DRAIN_LIMIT_NS, true);
+    mbar_wait_bounded(bar(b), parity, &dummy, status, MLA_DEVSTAT_TIMEOUT, TREE_DRAIN_LIMIT_NS, true);
   }
 };
-
-// One request as the kernel sees it.
-struct Req {
-  int q0, nodes;       // rows; 0 nodes when the request is empty or refused
-  int64_t ctx;         // positions every node sees (negative: the first nodes are not cached)
-  int kv;              // positions that may be read
-  int units, tiles;
-};
-
-__device__ __forceinline__ Req load_req(const TreeParams& p, int r, bool report) {
-  Req q;
-  const int q0 = __ldg(p.qo_indptr + r), q1 = __ldg(p.qo_indptr + r + 1), len = __ldg(p.kv_lens + r);
-  const int64_t reach = (int64_t)p.max_blocks * p.block_size;
-  const bool rows_ok = q0 >= 0 && q1 >= q0 && q1 <= p.total_rows;
-  const bool len_ok = len >= 0 && len <= reach;
-  if (report && p.status && (!rows_ok || !len_ok)) atomicOr(p.status, MLA_DEVSTAT_BAD_INDEX);
-  q.q0 = q0;
-  q.nodes = rows_ok ? q1 - q0 : 0;
-  q.ctx = (int64_t)len - q.nodes;
-  q.kv = len_ok ? len : (len < 0 ? 0 : (int)reach);
-  q.units = (int)(((int64_t)q.nodes * p.num_heads + ROWS - 1) / ROWS);
-  q.tiles = q.units ? max(1, (q.kv + KEYS - 1) / KEYS) : 0;
-  return q;
-}
-
-// A part of a worker's piece: tiles [lo, hi) of one unit.
-struct Part {
-  Req q;
-  int r;
-  int64_t pair0;       // first pair of the unit, counted over the batch
-  int npairs;
-  int lo, hi;
-  bool whole;          // the unit's every tile
-  int slot;            // 0: the worker's first part, 1: a later one (its last, if not whole)
-};
-
-struct Parts {
-  const TreeParams& p;
-  int64_t left;
-  int r, unit, tile, index;
-  Req q;
-  __device__ Parts(const TreeParams& tp, const StartRec& s, int64_t count)
-      : p(tp), left(count), r(s.req), unit(s.unit), tile(s.tile), index(0) {
-    if (left > 0) q = load_req(p, r, false);
-  }
-  __device__ bool next(Part* out) {
-    if (left <= 0) return false;
-    while (unit >= q.units) {   // to the next request that has rows
-      if (++r >= p.batch) return false;   // (lengths changed under the kernel: out of bounds is not read)
-      unit = 0;
-      q = load_req(p, r, false);
-    }
-    const int n = (int)min((int64_t)(q.tiles - tile), left);
-    out->q = q;
-    out->r = r;
-    const int64_t first = (int64_t)unit * ROWS;
-    out->pair0 = (int64_t)q.q0 * p.num_heads + first;
-    out->npairs = (int)min((int64_t)ROWS, (int64_t)q.nodes * p.num_heads - first);
-    out->lo = tile;
-    out->hi = tile + n;
-    out->whole = n == q.tiles;
-    out->slot = index == 0 ? 0 : 1;
-    ++index;
-    left -= n;
-    tile = 0;
-    ++unit;
-    return true;
-  }
-};
-
-// Where 64 keys from `key0` on are, spread over the lanes: first the blocks as the table has them
-// (the loads are under way while the caller does other things), then the rows to copy.  Whole
-// pieces (by_block) come by boxes, lane k holding piece k; else lanes 0-15 hold keys 4 lane .. + 3
-// each.  A key past the readable ones, or in a block that the table does not name, is the row past
-// the cache (read as zeros), the latter flagged.
-constexpr int32_t PAST_END = -0x7fffffff - 1;
-struct KeyBlocks {
-  int32_t b[4];
-};
-struct KeyRows {
-  bool by_block;
-  int32_t r[4];
-};
-__device__ __forceinline__ int block_of(const Params& p, int key) {
-  return p.block_shift >= 0 ? key >> p.block_shift : key / p.t.block_size;
-}
-__device__ __forceinline__ bool whole_piece(const Params& p, const Part& u, int64_t key0) {
-  return p.piece_rows > 0 && key0 + 64 <= u.q.kv;
-}
-__device__ __forceinline__ int32_t table_block(const Params& p, const Part& u, int64_t key) {
-  return key < u.q.kv ? __ldg(p.t.block_table + (int64_t)u.r * p.t.max_blocks + block_of(p, (int)key)) : PAST_END;
-}
-__device__ __forceinline__ int32_t block_row(const Params& p, int32_t blk, int64_t key) {
-  if (blk < 0 || (int64_t)blk >= p.t.num_blocks) {
-    if (blk != PAST_END && p.t.status) atomicOr(p.t.status, MLA_DEVSTAT_BAD_INDEX);
-    return p.oob_row;
-  }
-  return (int32_t)((int64_t)blk * p.t.block_size + ((int)key - block_of(p, (int)key) * p.t.block_size));
-}
-__device__ __forceinline__ KeyBlocks find_blocks(const Params& p, const Part& u, int64_t key0, int lane) {
-  KeyBlocks k{{PAST_END, PAST_END, PAST_END, PAST_END}};
-  if (whole_piece(p, u, key0)) {
-    if (lane * p.piece_rows < 64) k.b[0] = table_block(p, u, key0 + lane * p.piece_rows);
-  } else if (lane < 16) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) k.b[j] = table_block(p, u, key0 + 4 * lane + j);
-  }
-  return k;
-}
-__device__ __forceinline__ KeyRows find_rows(const Params& p, const Part& u, const KeyBlocks& k, int64_t key0,
-                                             int lane) {
-  KeyRows w;
-  w.by_block = whole_piece(p, u, key0);
-  if (w.by_block) {
-    w.r[0] = block_row(p, k.b[0], key0 + lane * p.piece_rows);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w.r[j] = block_row(p, k.b[j], key0 + 4 * lane + j);
-  }
-  return w;
-}
 
 // 64 keys x panels [panel0, panel0 + n) to n consecutive 8 KB panels at dst, completing on `bar`
 // (of the even CTA).  tg: the map whose boxes hold exactly n panels.
-__device__ __forceinline__ void copy_panels(const Params& p, const KeyRows& k, uint32_t dst, uint32_t bar,
+__device__ __forceinline__ void copy_panels(const TreeLaunch& p, const KeyRows& k, uint32_t dst, uint32_t bar,
                                             const CUtensorMap* tc, const CUtensorMap* tb, const CUtensorMap* tg,
                                             int panel0, int n, int lane) {
   if (k.by_block && p.grouped) {
@@ -340,11 +138,11 @@ __device__ __forceinline__ void expect_both(const Ctx& c, int b, uint32_t bytes_
 // After an abort the odd CTA cannot see its copies land: they have this long.
 __device__ __forceinline__ void settle() {
   const uint64_t t0 = global_timer_ns();
-  while (global_timer_ns() - t0 < DRAIN_LIMIT_NS) {
+  while (global_timer_ns() - t0 < TREE_DRAIN_LIMIT_NS) {
   }
 }
 
-__device__ void run_producer_qk(const Ctx& c, const Params& p, Parts parts, const CUtensorMap* tq,
+__device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, PairParts parts, const CUtensorMap* tq,
                                 const CUtensorMap* tc, const CUtensorMap* tb, const CUtensorMap* t3) {
   const int lane = threadIdx.x & 31;
   const uint32_t qf = mapa_shared(c.bar(QF), 0), kf = mapa_shared(c.bar(KF), 0);
@@ -396,7 +194,7 @@ __device__ void run_producer_qk(const Ctx& c, const Params& p, Parts parts, cons
   }
 }
 
-__device__ void run_producer_v(const Ctx& c, const Params& p, Parts parts, const CUtensorMap* tc,
+__device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, PairParts parts, const CUtensorMap* tc,
                                const CUtensorMap* tb, const CUtensorMap* t2) {
   const int lane = threadIdx.x & 31;
   const uint32_t vf = mapa_shared(c.bar(VF), 0);
@@ -443,7 +241,7 @@ __device__ void run_producer_v(const Ctx& c, const Params& p, Parts parts, const
 
 // Warp 3: this CTA's keys of the tile after the one being loaded, into L2.  The one-tile buffers
 // leave a load less than a tile's time, which DRAM does not keep to: with the rows in L2 it does.
-__device__ void run_prefetch(const Ctx& c, const Params& p, Parts parts, const CUtensorMap* tb,
+__device__ void run_prefetch(const Ctx& c, const TreeLaunch& p, PairParts parts, const CUtensorMap* tb,
                              const CUtensorMap* t3) {
   if (p.piece_rows == 0) return;
   const int lane = threadIdx.x & 31, pieces = 64 / p.piece_rows;
@@ -497,7 +295,7 @@ __device__ __forceinline__ void commit_both(uint32_t bar) {
       : "memory");
 }
 
-__device__ void run_mma(const Ctx& c, const Params& p, Parts parts, uint32_t tmem) {
+__device__ void run_mma(const Ctx& c, const TreeLaunch& p, PairParts parts, uint32_t tmem) {
   const uint64_t q_desc = sdesc_sw128(c.sbase + OFF_Q, 16, 1024);
   const uint64_t k_desc = sdesc_sw128(c.sbase + OFF_K, 16, 1024);
   const uint64_t v_desc = sdesc_sw128(c.sbase + OFF_V, QP, 1024);
@@ -585,36 +383,11 @@ __device__ void run_mma(const Ctx& c, const Params& p, Parts parts, uint32_t tme
 }
 
 // ------------------------------------------------------------------ softmax (warps 4-7)
-// Visibility of 64 keys from position pos0 on for node i (row t of the batch), bit k for key k.
-__device__ __forceinline__ uint64_t visible(const TreeParams& p, const Part& u, int i, int64_t pos0) {
-  auto window = [&](int64_t j0) -> uint64_t {   // nodes j0 .. j0 + 63, j0 >= 0
-    if (!p.mask) {
-      const int64_t n = (int64_t)i - j0 + 1;
-      return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
-    }
-    const int64_t* row = p.mask + ((int64_t)u.q.q0 + i) * p.mask_words;
-    const int64_t w = j0 >> 6;
-    const int sh = (int)(j0 & 63);
-    uint64_t bits = w < p.mask_words ? (uint64_t)__ldg(row + w) >> sh : 0ull;
-    if (sh && w + 1 < p.mask_words) bits |= (uint64_t)__ldg(row + w + 1) << (64 - sh);
-    return bits;
-  };
-  const int64_t s = pos0 - u.q.ctx;   // node index of the first key
-  uint64_t v;
-  if (s <= -64) v = ~0ull;
-  else if (s >= 0) v = window(s);
-  else v = ((1ull << -s) - 1) | (window(0) << -s);
-  const int64_t room = u.q.kv - pos0;
-  if (room < 64) v &= room <= 0 ? 0ull : (1ull << room) - 1;
-  return v;
-}
-
-__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void st_shared_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-__device__ void run_softmax(const Ctx& c, const Params& p, Parts parts, uint32_t tmem, char* ws_slots, uint8_t* smem) {
+__device__ void run_softmax(const Ctx& c, const TreeLaunch& p, PairParts parts, uint32_t tmem, char* ws_slots, uint8_t* smem) {
   const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3;
   const int half = q4 >> 1, rg = q4 & 1;             // key / column half, group of 32 rows
   const int row = 32 * rg + lane;                    // of the CTA's 64
@@ -689,7 +462,7 @@ __device__ void run_softmax(const Ctx& c, const Params& p, Parts parts, uint32_t
       bool rescale = false;
       if (t == u.lo) {
         m_new = mt;
-      } else if (mt > m_used + RESCALE_THRESHOLD) {
+      } else if (mt > m_used + TREE_RESCALE_THRESHOLD) {
         m_new = mt;
         rescale = true;
       }
@@ -795,56 +568,10 @@ __device__ void run_softmax(const Ctx& c, const Params& p, Parts parts, uint32_t
   }
 }
 
-// Where worker w's piece starts, and how long it is; every thread of the CTA calls.
-__device__ void find_piece(const TreeParams& p, int worker, int workers, bool report, StartRec* start,
-                           int64_t* count, Header* head) {
-  __shared__ int64_t warp_sum[NTHREADS / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (p.batch + NTHREADS - 1) / NTHREADS;
-  const int r0 = min(tid * per, p.batch), r1 = min(r0 + per, p.batch);
-  int64_t mine = 0;
-  for (int r = r0; r < r1; ++r) {
-    const Req q = load_req(p, r, report);
-    mine += (int64_t)q.units * q.tiles;
-  }
-  int64_t incl = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += o;
-  }
-  if (lane == 31) warp_sum[warp] = incl;
-  __syncthreads();
-  int64_t before = incl - mine, total = 0;
-  for (int w = 0; w < NTHREADS / 32; ++w) {
-    if (w < warp) before += warp_sum[w];
-    total += warp_sum[w];
-  }
-  const int n = (int)min((int64_t)workers, total);   // a tile is worth a worker (700 keys: 26 us, two tiles each: 30)
-  const int64_t lo = worker < n ? total * worker / n : total, hi = worker < n ? total * (worker + 1) / n : total;
-  if (tid == 0) {
-    *count = hi - lo;
-    *head = Header{total, n, 0};
-  }
-  if (lo < hi && lo >= before && lo < before + mine) {
-    int64_t at = before;
-    for (int r = r0; r < r1; ++r) {
-      const Req q = load_req(p, r, false);
-      const int64_t k = (int64_t)q.units * q.tiles;
-      if (lo < at + k) {
-        *start = StartRec{r, (int)((lo - at) / q.tiles), (int)((lo - at) % q.tiles), 0};
-        break;
-      }
-      at += k;
-    }
-  }
-  __syncthreads();
-}
-
 __global__ void __launch_bounds__(NTHREADS, 1)
 tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_c,
                  const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_2,
-                 const __grid_constant__ CUtensorMap tm_3, const __grid_constant__ Params p) {
+                 const __grid_constant__ CUtensorMap tm_3, const __grid_constant__ TreeLaunch p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ StartRec start;
   __shared__ int64_t count;
@@ -876,7 +603,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     tmem_alloc_pair(smem_addr(tmem_slot), TMEM_COLS);
     tmem_relinquish_pair();
   }
-  find_piece(p.t, worker, p.workers, blockIdx.x == 0, &start, &count, &head);
+  find_piece<ROWS, KEYS, NTHREADS>(p.t, worker, p.workers, blockIdx.x == 0, &start, &count, &head);
   char* ws = static_cast<char*>(p.t.workspace);
   if (threadIdx.x == 0 && rank == 0) {
     if (worker == 0) *reinterpret_cast<Header*>(ws) = head;
@@ -887,7 +614,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   cluster_sync();   // both CTAs' barriers exist before any remote arrival
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  const Parts parts(p.t, start, count);
+  const PairParts parts(p.t, start, count);
   if (warp == 0) {
     run_producer_qk(c, p, parts, &tm_q, &tm_c, &tm_b, &tm_3);
   } else if (warp == 2) {
@@ -910,80 +637,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     __syncwarp();
     tmem_dealloc_pair(tmem, TMEM_COLS);
   }
-}
-
-// ------------------------------------------------------------------ join
-// One CTA per eight rows of a unit that a boundary between two workers cuts; the unit's first
-// such boundary does it.  A warp has a row: the parts' (m, l) one per lane, then their O rows,
-// 16 columns per lane.
-constexpr int JOIN_WARPS = 8;
-
-__global__ void __launch_bounds__(JOIN_WARPS * 32) tree_join_kernel(const __grid_constant__ Params p) {
-  const char* ws = static_cast<const char*>(p.t.workspace);
-  const Header head = *reinterpret_cast<const Header*>(ws);
-  const int b = blockIdx.x + 1;   // the boundary before worker b
-  if (b >= head.workers) return;
-  const StartRec s = reinterpret_cast<const StartRec*>(ws + WS_STARTS)[b];
-  if (s.tile == 0) return;        // between two units
-  auto lo = [&](int w) { return head.total * w / head.workers; };
-  const int64_t a = lo(b) - s.tile;
-  if (lo(b - 1) > a) return;      // an earlier boundary cuts the same unit
-  const Req q = load_req(p.t, s.req, false);
-  const int64_t end = a + q.tiles;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.y * JOIN_WARPS + warp;
-  const int64_t first = (int64_t)s.unit * ROWS;
-  if (first + row >= (int64_t)q.nodes * p.t.num_heads) return;
-  const int64_t pair = (int64_t)q.q0 * p.t.num_heads + first + row;
-  int n = 1;                      // workers b - 1, b, .. that have a part
-  while (b + n - 1 < head.workers && lo(b + n - 1) < end) ++n;
-  const char* slots = ws + WS_SLOTS;
-  // Part k belongs to worker b - 1 + k: its first part, except that worker b - 1 may have begun
-  // with another unit.
-  auto slot = [&](int k) { return slots + (size_t)(2 * (b - 1 + k) + (k == 0 && lo(b - 1) < a ? 1 : 0)) * SLOT_BYTES; };
-  const float NEG_INF = -__int_as_float(0x7f800000);
-  float m = NEG_INF;
-  for (int k = lane; k < n; k += 32) m = fmaxf(m, reinterpret_cast<const float2*>(slot(k) + SLOT_ML)[row].x);
-#pragma unroll
-  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  const float mref = m == NEG_INF ? 0.f : m;
-  float4 o[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-  for (int k0 = 0; k0 < n; k0 += 32) {
-    float w = 0.f, wl = 0.f;
-    if (k0 + lane < n) {
-      const float2 ml = reinterpret_cast<const float2*>(slot(k0 + lane) + SLOT_ML)[row];
-      w = ex2_approx(ml.x - mref);
-      wl = w * ml.y;
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) wl += __shfl_xor_sync(0xffffffffu, wl, d);
-    l += wl;
-    const int here = min(32, n - k0);
-#pragma unroll 4
-    for (int k = 0; k < here; ++k) {
-      const float wk = __shfl_sync(0xffffffffu, w, k);
-      const float4* src = reinterpret_cast<const float4*>(slot(k0 + k)) + (size_t)row * 128 + lane;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 x = src[32 * i];
-        o[i].x += wk * x.x;
-        o[i].y += wk * x.y;
-        o[i].z += wk * x.z;
-        o[i].w += wk * x.w;
-      }
-    }
-  }
-  const bool empty = !(l > 0.f);
-  const float inv = empty ? 0.f : 1.f / l;
-  uint2* d = reinterpret_cast<uint2*>(p.t.o + pair * 512) + lane;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    d[32 * i] = empty ? make_uint2(0u, 0u)
-                      : make_uint2(pack_bf16x2(o[i].x * inv, o[i].y * inv), pack_bf16x2(o[i].z * inv, o[i].w * inv));
-  if (lane == 0 && p.t.lse) p.t.lse[pair] = empty ? NEG_INF : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 cudaLaunchConfig_t pair_config(cudaLaunchAttribute* attr, int workers, cudaStream_t stream) {
@@ -1024,14 +677,21 @@ int max_workers() {
 }  // namespace
 
 int64_t tree_workspace_bytes() {
-  const int n = max_workers();
-  return n > 0 ? (int64_t)(WS_SLOTS + (size_t)n * 2 * SLOT_BYTES) : 0;
+  const size_t n = max_workers(), few = tree_few_workers();
+  if (n == 0 || few == 0) return 0;
+  const size_t a = n * 2 * SLOT_BYTES, b = few * 2 * slot_bytes(64);
+  return (int64_t)(WS_SLOTS + (a > b ? a : b));
 }
 
 cudaError_t launch_tree_attention(const TreeParams& t, cudaStream_t stream) {
-  Params p;
+  TreeLaunch p;
   p.t = t;
-  p.workers = max_workers();
+  // Units of about as many pairs as a request has, by the average (the lengths themselves are on
+  // the device; any unit size is right for any request).
+  const int64_t pairs = t.total_rows * t.num_heads;
+  const int few = pairs <= 16 * (int64_t)t.batch ? 16 : pairs <= 32 * (int64_t)t.batch ? 32
+                  : pairs <= 64 * (int64_t)t.batch ? 64 : 0;
+  p.workers = few ? tree_few_workers() : max_workers();
   if (p.workers <= 0) return cudaErrorInvalidConfiguration;
   const bool any = t.max_blocks > 0;   // some cache row may be read
   const int bs = t.block_size;
@@ -1039,7 +699,7 @@ cudaError_t launch_tree_attention(const TreeParams& t, cudaStream_t stream) {
   CUtensorMap tq, tc, tb, t2, t3;
   {
     const uint64_t dims[2] = {576, (uint64_t)t.total_rows * (uint64_t)t.num_heads}, strides[1] = {576 * 2};
-    const uint32_t box[2] = {64, 64};
+    const uint32_t box[2] = {64, few ? (uint32_t)few : 64u};
     if (make_tensor_map_bf16(&tq, t.q, 2, dims, strides, box) != MLA_OK) return cudaErrorInvalidValue;
   }
   const void* rows = any ? static_cast<const void*>(t.cache) : t.q;   // a map needs a valid base
@@ -1079,12 +739,16 @@ cudaError_t launch_tree_attention(const TreeParams& t, cudaStream_t stream) {
   const uint64_t forced = forced_timeout_ns();
   p.force_timeout = forced != 0;
   p.wait_limit_ns = forced ? forced : kWaitLimitNs;
-  cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = pair_config(attr, p.workers, stream);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, tree_attn_kernel, tq, tc, tb, t2, t3, p);
-  if (e != cudaSuccess || p.workers < 2) return e;
-  tree_join_kernel<<<dim3(p.workers - 1, ROWS / JOIN_WARPS), JOIN_WARPS * 32, 0, stream>>>(p);
-  return cudaGetLastError();
+  cudaError_t e;
+  if (few) {
+    e = launch_tree_few(p, few, tq, tc, tb, t2, stream);
+  } else {
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = pair_config(attr, p.workers, stream);
+    e = cudaLaunchKernelEx(&cfg, tree_attn_kernel, tq, tc, tb, t2, t3, p);
+  }
+  if (e != cudaSuccess) return e;
+  return launch_tree_join(p, few ? few : ROWS, stream);
 }
 
 }  // namespace mla

@@ -257,6 +257,21 @@ ATTENTION = [
     ("softcap", [4, 3], [200, 513], 16, 64, True, 30.0),
     ("softcap_small", [4], [300], 16, 64, True, 2.0),
     ("many_requests", [1, 2, 3] * 30, [5, 70, 140] * 30, 3, 16, True, 0.0),
+    # about 16, 32, 64 and more (node, head) pairs a request, with units that do not fill and
+    # requests of more units than one
+    ("pairs_16_ragged", [1, 9, 1, 1], [90, 300, 64, 1], 5, 64, True, 0.0),
+    ("pairs_32_ragged", [1, 3, 2, 2], [90, 300, 64, 129], 16, 64, True, 0.0),
+    ("pairs_64_ragged", [7, 2, 1, 5], [90, 300, 64, 1000], 16, 64, True, 0.0),
+    ("pairs_64_softcap", [4, 3], [200, 513], 16, 16, True, 20.0),
+    ("pairs_16_block_1", [1, 2], [70, 200], 8, 1, True, 0.0),
+    ("pairs_32_block_8", [2, 2], [200, 131], 16, 8, False, 0.0),
+    ("wide_block_1", [3, 2], [40, 150], 64, 1, True, 0.0),
+    ("wide_block_8", [3], [300], 64, 8, True, 0.0),
+    ("wide_block_16", [2, 2], [130, 300], 64, 16, True, 0.0),
+    ("wide_block_24", [2, 4], [250, 130], 48, 24, True, 0.0),
+    ("wide_block_128", [2, 2], [400, 128], 48, 128, True, 0.0),
+    ("wide_few_keys", [20, 9, 12], [4, 0, 12], 8, 64, True, 0.0),
+    ("wide_softcap", [4, 3], [200, 513], 32, 64, True, 30.0),
 ]
 
 
@@ -269,23 +284,25 @@ def test_tree_attention(name, nodes, kv, heads, bs, tree, cap):
 
 
 @pytest.mark.parametrize("spread", [0.01, 12.0])
-def test_tree_attention_flat_and_peaked(spread):
+@pytest.mark.parametrize("nodes,heads", [([6, 2], 64), ([6, 2], 16), ([2, 2], 16), ([1, 1], 16)])
+def test_tree_attention_flat_and_peaked(spread, nodes, heads):
     """Nearly uniform weights, and logits whose maximum moves by hundreds along the keys."""
-    p = Problem(77, [6, 2], [700, 333], 16, 64, True, spread=spread)
+    p = Problem(77, nodes, [700, 333], heads, 64, True, spread=spread)
     o, lse, st = p.run()
     assert st == 0
     p.check(o, lse)
 
 
 @pytest.mark.parametrize("batch,ctx,nodes,heads", [(1, 20000, 1, 16), (2, 9000, 5, 128), (150, 600, 1, 16),
-                                                   (40, 900, 4, 128)])
+                                                   (40, 900, 4, 128), (170, 400, 2, 16), (3, 7000, 4, 16),
+                                                   (200, 300, 3, 16), (1, 30000, 3, 64)])
 def test_tree_attention_split_and_unsplit(batch, ctx, nodes, heads):
     """A request over the whole GPU, and more requests than it has SMs; sampled."""
     p = Problem(33 + batch, [nodes] * batch, [ctx + 13 * (r % 7) + nodes for r in range(batch)], heads, 64, True)
     o, lse, st = p.run()
     assert st == 0
     some = sorted({0, batch // 2, batch - 1})
-    p.check(o, lse, some, None if heads <= 16 else [0, 63, 64, 127])
+    p.check(o, lse, some, None if heads <= 16 else [0, heads // 2, heads - 1])
 
 
 def test_tree_attention_mask_rows_without_any_node():
@@ -297,19 +314,21 @@ def test_tree_attention_mask_rows_without_any_node():
     p.check(o, lse)
 
 
-def test_tree_attention_repeats_bit_for_bit():
-    p = Problem(6, [3, 9, 1], [5000, 700, 64], 16, 64, True)
+@pytest.mark.parametrize("heads", [3, 7, 12, 40])
+def test_tree_attention_repeats_bit_for_bit(heads):
+    p = Problem(6, [3, 9, 1], [5000, 700, 64], heads, 64, True)
     a = p.run()
     for _ in range(3):
         b = p.run()
         assert np.array_equal(bits_of(a[0]), bits_of(b[0])) and torch.equal(a[1], b[1])
 
 
-def test_tree_attention_does_not_read_past_the_lengths():
+@pytest.mark.parametrize("heads", [4, 8, 16, 64])
+def test_tree_attention_does_not_read_past_the_lengths(heads):
     """NaN everywhere that no request owns: behind the last key of the last block, in other
     blocks, in the rows of the padding."""
-    p = Problem(8, [3, 1, 4], [130, 65, 500], 16, 64, True)
-    before = p.run()
+    p = Problem(8, [3, 1, 4], [130, 65, 500], heads, 64, True)
+    before = p.run(pad=3)   # (as many rows: the kernel is chosen by them)
     own = np.zeros(p.b.cache.shape[:2], dtype=bool)
     for r, k in enumerate(p.kv):
         pos = np.arange(k)
@@ -320,8 +339,9 @@ def test_tree_attention_does_not_read_past_the_lengths():
     assert np.array_equal(bits_of(before[0]), bits_of(after[0])) and torch.equal(before[1], after[1])
 
 
-def test_tree_attention_bad_blocks_read_as_zeros():
-    p = Problem(9, [2, 2], [300, 150], 8, 64, True)
+@pytest.mark.parametrize("heads", [8, 100])
+def test_tree_attention_bad_blocks_read_as_zeros(heads):
+    p = Problem(9, [2, 2], [300, 150], heads, 64, True)
     p.b.block_table[0, 1] = 10 ** 6
     p.b.block_table[1, 0] = -1
     o, lse, st = p.run()
