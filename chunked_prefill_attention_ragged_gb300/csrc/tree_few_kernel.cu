@@ -1,16 +1,14 @@
 // Tree attention for requests with few (node, head) pairs (at most 64): the same function as
 // tree_attn_kernel.cu computes, turned round.  A unit is N = 16, 32 or 64 pairs of one request,
 // run by one CTA over tiles of 64 keys:
-//   S^T = K Q^T  (M = 128 keys, of which 64 count; N pairs),  P^T = 2^(S^T - m),
+//   S^T = K Q^T  (M = 64 keys, N pairs),  P^T = 2^(S^T - m),
 //   O^T += V^T P^T  (M = 128 value columns, four times; N pairs).
 //
 // Why: with few pairs the call is bound by reading the cache from DRAM, and what counts is that
 // every byte is read once and that enough copies are in flight.  The pairs are the products' narrow
 // side, so that 16 of them cost what 16 cost, and the cache rows are their wide side, read by S
 // and by P V from the same place in shared memory (the other kernel needs its V apart from K and
-// pads to 128 pairs).  What shared memory is left over by Q holds two to three tiles.  S's
-// products read 128 rows of the panels from a tile's start: rows 64-127 are whatever lies behind
-// it, and end in accumulator lanes that nothing reads.
+// pads to 128 pairs).  What shared memory is left over by Q holds two to three tiles.
 //
 // Shared memory is two rings: slots of two 64-column panels of 64 keys (four per tile, the values
 // and the latent part of the keys) and slots of one (the rope columns).
@@ -19,10 +17,11 @@
 //              landed first (the results do not depend on the order)
 //   warp 2     TMEM allocation
 //   warp 3     loads Q, once per unit
-//   warps 4-7  warps 4 and 5 have a key per thread (its N scores are one row of S^T); all four
-//              scale and write O (a value column per thread)
-// The maximum of a pair is over lanes: reduced by shuffles inside the two warps and exchanged
-// through shared memory, for every tile; the reference m moves as in the other kernel.
+//   warps 4-7  a key per lane of their lower halves (its N scores are one row of S^T, M = 64), a
+//              value column per thread (of O)
+// The maximum of a pair is over lanes and warps, which takes long to find.  So a tile only asks
+// whether any score has passed m + 8 (one vote and one exchange of flags); if one has, all maxima
+// are found, by shuffles and an exchange of rows, and O is scaled.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -46,12 +45,13 @@ struct Lay {
   static constexpr int PBUF = N == 64 ? 1 : 2;                    // P buffers
   static constexpr int OFF_PAIR = 0;
   static constexpr int OFF_ROPE = OFF_PAIR + PAIRS * PAIR;
-  static constexpr int OFF_Q = OFF_ROPE + ROPES * PANEL;          // (S reads 8 KB past the last rope slot)
+  static constexpr int OFF_Q = OFF_ROPE + ROPES * PANEL;
   static constexpr int QPANEL = N * 128;
   static constexpr int OFF_P = OFF_Q + 9 * QPANEL;
-  static constexpr int OFF_XCHG = OFF_P + PBUF * QPANEL;          // [2][2 warps][N] maxima or sums
-  static constexpr int OFF_ALPHA = OFF_XCHG + 4 * N * 4;          // [N]
-  static constexpr int OFF_BAR = OFF_ALPHA + N * 4;
+  static constexpr int OFF_XCHG = OFF_P + PBUF * QPANEL;          // [4 warps][N] maxima or sums,
+  static constexpr int OFF_FLAGS = OFF_XCHG + 4 * N * 4;          // [2][4 warps] flags,
+  static constexpr int OFF_SCALE = OFF_FLAGS + 32;                // [N] what O is multiplied by
+  static constexpr int OFF_BAR = OFF_SCALE + N * 4;
   // barriers
   static constexpr int QF = 0, QE = 1, SF = 2, PR = 4, OD = 6, XB = 8, FIN = 9, NEVER = 10;
   static constexpr int PF = 11, PE = PF + PAIRS, RF = PE + PAIRS, RE = RF + ROPES, NBAR = RE + ROPES;
@@ -60,7 +60,7 @@ struct Lay {
   static_assert(SMEM + 256 <= 227 * 1024, "shared memory budget");
   static constexpr uint32_t TMEM = N == 16 ? 128 : N == 32 ? 256 : 512;
   static constexpr uint32_t TM_S = 4 * N;                         // two S^T buffers behind O^T's four tiles
-  static constexpr uint32_t IDESC_S = idesc_bf16_f32(128, N, false, false);
+  static constexpr uint32_t IDESC_S = idesc_bf16_f32(64, N, false, false);
   static constexpr uint32_t IDESC_O = idesc_bf16_f32(128, N, true, false);
 };
 
@@ -101,12 +101,8 @@ struct Ring {
 
 // ------------------------------------------------------------------ producers
 __device__ __forceinline__ void copy_keys(const TreeLaunch& p, const KeyRows& k, uint32_t dst, uint32_t bar,
-                                          const CUtensorMap* tc, const CUtensorMap* tb, const CUtensorMap* t2,
-                                          int panel0, int n, int lane) {
-  if (k.by_block && p.grouped && n == 2) {
-    if (lane == 0) tma_load_3d(dst, t2, bar, 0, k.r[0], panel0);
-    return;
-  }
+                                          const CUtensorMap* tc, const CUtensorMap* tb, int panel0, int n,
+                                          int lane) {
 #pragma unroll 1
   for (int i = 0; i < n; ++i) {
     const int col = (panel0 + i) * 64;
@@ -137,17 +133,18 @@ __device__ void run_producer(const Ctx<N>& c, const TreeLaunch& p, Parts<N, KEYS
   };
   Part u;
   while (ok && parts.next(&u)) {
-    int64_t key0 = (int64_t)u.lo * KEYS;
-    KeyBlocks blocks = find_blocks(p, u, key0, lane);
-    for (int t = u.lo; t < u.hi && ok; ++t, key0 += KEYS) {
-      const KeyRows k = find_rows(p, u, blocks, key0, lane);
-      if (t + 1 < u.hi) blocks = find_blocks(p, u, key0 + KEYS, lane);
-      if (k.by_block && p.grouped) {   // one lane, five copies
+    int32_t ahead = -1;   // rows of 32 tiles
+#pragma unroll 1
+    for (int t = u.lo; t < u.hi && ok; ++t) {
+      const int i = (t - u.lo) & 31;
+      if (i == 0 && p.grouped) ahead = piece_rows(p, u, (int64_t)t * KEYS, KEYS, u.hi - t, lane);
+      const int32_t row = __shfl_sync(0xffffffffu, ahead, i);
+      if (row >= 0) {   // one lane, five copies
         if (lane == 0) {
           if (ropes >= L::ROPES) ok = c.wait(L::RE + rr.slot, rr.phase ^ 1);
           if (ok) {
             mbar_arrive_expect_tx(c.bar(L::RF + rr.slot), PANEL);
-            tma_load_2d(c.sbase + L::OFF_ROPE + rr.slot * PANEL, tb, c.bar(L::RF + rr.slot), 8 * 64, k.r[0]);
+            tma_load_2d(c.sbase + L::OFF_ROPE + rr.slot * PANEL, tb, c.bar(L::RF + rr.slot), 8 * 64, row);
             ++ropes;
           }
         }
@@ -158,27 +155,29 @@ __device__ void run_producer(const Ctx<N>& c, const TreeLaunch& p, Parts<N, KEYS
             if (pairs >= L::PAIRS) ok = c.wait(L::PE + pr.slot, pr.phase ^ 1);
             if (ok) {
               mbar_arrive_expect_tx(c.bar(L::PF + pr.slot), PAIR);
-              tma_load_3d(c.sbase + L::OFF_PAIR + pr.slot * PAIR, t2, c.bar(L::PF + pr.slot), 0, k.r[0], 2 * j);
+              tma_load_3d(c.sbase + L::OFF_PAIR + pr.slot * PAIR, t2, c.bar(L::PF + pr.slot), 0, row, 2 * j);
               ++pairs;
             }
           }
           pr.step();
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
-        ropes = __shfl_sync(0xffffffffu, ropes, 0);
-        pairs = __shfl_sync(0xffffffffu, pairs, 0);
         continue;
       }
+      ropes = __shfl_sync(0xffffffffu, ropes, 0);
+      pairs = __shfl_sync(0xffffffffu, pairs, 0);
+      const int64_t key0 = (int64_t)t * KEYS;
+      const KeyRows k = find_rows(p, u, find_blocks(p, u, key0, lane), key0, lane);
       ok = fill(L::RF + rr.slot, L::RE + rr.slot, ropes >= L::ROPES, rr.phase, PANEL);
       if (!ok) break;
-      copy_keys(p, k, c.sbase + L::OFF_ROPE + rr.slot * PANEL, c.bar(L::RF + rr.slot), tc, tb, t2, 8, 1, lane);
+      copy_keys(p, k, c.sbase + L::OFF_ROPE + rr.slot * PANEL, c.bar(L::RF + rr.slot), tc, tb, 8, 1, lane);
       ++ropes;
       rr.step();
 #pragma unroll 1
       for (int j = 0; j < 4; ++j) {
         ok = fill(L::PF + pr.slot, L::PE + pr.slot, pairs >= L::PAIRS, pr.phase, PAIR);
         if (!ok) break;
-        copy_keys(p, k, c.sbase + L::OFF_PAIR + pr.slot * PAIR, c.bar(L::PF + pr.slot), tc, tb, t2, 2 * j, 2, lane);
+        copy_keys(p, k, c.sbase + L::OFF_PAIR + pr.slot * PAIR, c.bar(L::PF + pr.slot), tc, tb, 2 * j, 2, lane);
         ++pairs;
         pr.step();
       }
@@ -376,22 +375,43 @@ __device__ __forceinline__ void reduce_rows(const float* in, float* out, int lan
   else out[lane >> 1] = v[0];
 }
 
+// Which of the unit's pairs see the key at position pos: bit n for pair n.
+template <int N>
+__device__ __forceinline__ uint64_t seen_by(const TreeParams& p, const Part& u, int64_t first_pair, int64_t pos) {
+  int node = (int)(first_pair / p.num_heads), rem = (int)(first_pair % p.num_heads);
+  uint64_t bits = 0;
+  bool seen = false;
+#pragma unroll 1
+  for (int n = 0, look = 1; n < N; ++n) {
+    if (look && node < u.q.nodes) seen = visible(p, u, node, pos) & 1;
+    if (seen) bits |= 1ull << n;
+    look = ++rem == p.num_heads;
+    if (look) {
+      rem = 0;
+      ++node;
+    }
+  }
+  return bits;
+}
+
 template <int N>
 __device__ void run_softmax(const Ctx<N>& c, const TreeLaunch& p, Parts<N, KEYS> parts, uint32_t tmem, char* ws_slots,
                             uint8_t* smem) {
   using L = Lay<N>;
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
-  const bool has_key = w < 2;
-  const int key = 32 * w + lane;                     // of the tile (has_key)
+  const bool has_key = lane < 16;                    // S^T: 16 keys in each quarter of the lanes
+  const int key = 16 * w + (lane & 15);              // of the tile
   const uint32_t lane_addr = tmem + ((uint32_t)(w * 32) << 16);
-  float* xchg = reinterpret_cast<float*>(smem + L::OFF_XCHG);
-  float* alpha = reinterpret_cast<float*>(smem + L::OFF_ALPHA);
+  float* rows = reinterpret_cast<float*>(smem + L::OFF_XCHG);              // [4][N]
+  int* flags = reinterpret_cast<int*>(smem + L::OFF_FLAGS);                // [2][4]
+  float* scale = reinterpret_cast<float*>(smem + L::OFF_SCALE);            // [N]
   const float NEG_INF = -__int_as_float(0x7f800000);
+  // A pair that has seen no key yet: any finite score exceeds this reference, minus infinity does not.
+  constexpr float FRESH = 1e30f;
   const float sc = p.has_cap ? 1.f : p.scale_log2;
   bool ok = true;
   int g = 0, xs = 0;   // tiles and exchanges so far
-  // What the two key warps put into their halves of the buffer, to all four.  Two buffers in
-  // turn: a buffer is written again only after every warp has arrived for the exchange between.
+  // What every warp wrote before, to all four.
   auto exchange = [&]() {
     __syncwarp();
     if (lane == 0) mbar_arrive(c.bar(L::XB));
@@ -401,144 +421,155 @@ __device__ void run_softmax(const Ctx<N>& c, const TreeLaunch& p, Parts<N, KEYS>
   };
   Part u;
   while (ok && parts.next(&u)) {
-    float m[N], l[N];
+    float neg_m[N], l[N];   // the reference's negative; the sum over this thread's keys
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      m[n] = NEG_INF;
+      neg_m[n] = FRESH;
       l[n] = 0.f;
     }
     const int64_t first_pair = u.pair0 - (int64_t)u.q.q0 * p.t.num_heads;   // inside the request
     for (int t = u.lo; t < u.hi; ++t, ++g) {
       const int sb = g & 1;
-      float* mine = xchg + (xs & 1) * 2 * N;
-      float sv[N];
-      if (has_key) {
-        if (!c.wait_all(L::SF + sb, (g >> 1) & 1)) { ok = false; break; }
-        tc_fence_after();
-        tmem_ld_n<N>(lane_addr + L::TM_S + sb * N, reinterpret_cast<uint32_t*>(sv));
+      float a[N];
+      if (!c.wait_all(L::SF + sb, (g >> 1) & 1)) { ok = false; break; }
+      tc_fence_after();
+      // Once for most tiles; three times where a maximum moves (look, find it, use it).  A loop, so
+      // that the code is there once: what runs for the first time waits for its instructions.
+#pragma unroll 1
+      for (int pass = 0;; ++pass) {
+        // Scores in log2 units but for a factor sc; minus infinity where masked.
+        tmem_ld_n<N>(lane_addr + L::TM_S + sb * N, reinterpret_cast<uint32_t*>(a));
         if (p.has_cap) {
           // c * tanh(sm_scale * x / c) in log2 units, from tanh(y) = 1 - 2 / (e^(2y) + 1).
 #pragma unroll
           for (int n = 0; n < N; ++n) {
-            const float r = rcp_approx(ex2_approx(sv[n] * p.cap_ex2_scale) + 1.f);
-            sv[n] = fmaf(r, -2.f * p.cap_log2, p.cap_log2);
+            const float r = rcp_approx(ex2_approx(a[n] * p.cap_ex2_scale) + 1.f);
+            a[n] = fmaf(r, -2.f * p.cap_log2, p.cap_log2);
           }
-        } else {
-#pragma unroll
-          for (int n = 0; n < N; ++n) sv[n] *= sc;
         }
-        const int64_t pos = (int64_t)t * KEYS + key;
         if ((int64_t)t * KEYS + KEYS > min(u.q.ctx, (int64_t)u.q.kv)) {   // nodes, or the end of the keys
-          int node = (int)(first_pair / p.t.num_heads), rem = (int)(first_pair % p.t.num_heads);
-          bool seen = visible(p.t, u, node, pos) & 1;
+          const uint64_t seen = seen_by<N>(p.t, u, first_pair, (int64_t)t * KEYS + key);
 #pragma unroll
-          for (int n = 0; n < N; ++n) {
-            if (!seen) sv[n] = NEG_INF;
-            if (++rem == p.t.num_heads && n + 1 < N) {
-              rem = 0;
-              if (++node < u.q.nodes) seen = visible(p.t, u, node, pos) & 1;
+          for (int n = 0; n < N; ++n)
+            if (!((seen >> n) & 1)) a[n] = NEG_INF;
+        }
+        if (pass == 1) {
+#pragma unroll
+          for (int n = 0; n < N; ++n) a[n] = has_key ? a[n] * sc : NEG_INF;
+          reduce_rows<N>(a, rows + w * N, lane, [](float x, float y) { return fmaxf(x, y); });
+          ok = exchange();
+          if (!ok) break;
+#pragma unroll
+          for (int n = 0; n < N; ++n) {   // a: what O and l are scaled by
+            const float x = fmaxf(fmax3(rows[n], rows[N + n], rows[2 * N + n]), rows[3 * N + n]);
+            a[n] = 1.f;
+            if (x + neg_m[n] > TREE_RESCALE_THRESHOLD) {
+              a[n] = ex2_approx(-neg_m[n] - x);
+              neg_m[n] = -x;
+            }
+            l[n] *= a[n];
+          }
+          if (t > u.lo) {
+            ok = c.wait_all(L::OD + ((g - 1) & 1), ((g - 1) >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+              float ov[N];
+              tmem_ld_n<N>(lane_addr + j * N, reinterpret_cast<uint32_t*>(ov));
+#pragma unroll
+              for (int n = 0; n < N; ++n) ov[n] *= a[n];
+              tmem_st_n<N>(lane_addr + j * N, reinterpret_cast<const uint32_t*>(ov));
             }
           }
+          continue;
         }
-        reduce_rows<N>(sv, mine + w * N, lane, [](float a, float b) { return fmaxf(a, b); });
+        float top[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+#pragma unroll
+        for (int n = 0; n < N; n += 2) {
+          a[n] = fmaf(a[n], sc, neg_m[n]);
+          a[n + 1] = fmaf(a[n + 1], sc, neg_m[n + 1]);
+          top[(n >> 1) & 3] = fmax3(top[(n >> 1) & 3], a[n], a[n + 1]);
+        }
+        if (pass == 2) break;
+        const bool above = has_key && fmaxf(fmax3(top[0], top[1], top[2]), top[3]) > TREE_RESCALE_THRESHOLD;
+        const int any_above = __any_sync(0xffffffffu, above);
+        int* mine = flags + (xs & 1) * 4;   // (written again after the exchange between)
+        if (lane == 0) mine[w] = any_above;
+        ok = exchange();
+        if (!ok) break;
+        const int4 f = *reinterpret_cast<const int4*>(mine);
+        if (!(f.x | f.y | f.z | f.w)) break;   // no maximum has moved: the same in all four warps
       }
-      if (!exchange()) { ok = false; break; }
-      bool move = false;
-#pragma unroll
-      for (int n = 0; n < N; n += 4) {
-        const float4 a = *reinterpret_cast<const float4*>(mine + n), b = *reinterpret_cast<const float4*>(mine + N + n);
-        const float x[4] = {fmaxf(a.x, b.x), fmaxf(a.y, b.y), fmaxf(a.z, b.z), fmaxf(a.w, b.w)};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (t == u.lo) m[n + k] = x[k];
-          else move |= x[k] > m[n + k] + TREE_RESCALE_THRESHOLD;
-        }
+      if (!ok) break;
+      // P's buffer: the product that read it last is done.
+      if (g >= L::PBUF) {
+        const int d = g - L::PBUF;
+        if (!c.wait_all(L::OD + (d & 1), (d >> 1) & 1)) { ok = false; break; }
       }
-      if (move) {   // the same in all four warps
+      uint8_t* at[8];
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-          const float x = fmaxf(mine[n], mine[N + n]);
-          float a = 1.f;
-          if (x > m[n] + TREE_RESCALE_THRESHOLD) {
-            a = ex2_approx(m[n] - x);
-            m[n] = x;
-          }
-          l[n] *= a;
-          if (w == 0 && lane == n % 32) alpha[n] = a;
-        }
-        if (!exchange()) { ok = false; break; }   // alpha; the next is written after the next exchange
-        if (!c.wait_all(L::OD + ((g - 1) & 1), ((g - 1) >> 1) & 1)) { ok = false; break; }
-        tc_fence_after();
-#pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
-          float ov[N];
-          tmem_ld_n<N>(lane_addr + j * N, reinterpret_cast<uint32_t*>(ov));
+      for (int k = 0; k < 8; ++k)
+        at[k] = smem + L::OFF_P + (g % L::PBUF) * L::QPANEL + (((key >> 3) ^ k) << 4) + (key & 7) * 2;
 #pragma unroll
-          for (int n = 0; n < N; ++n) ov[n] *= alpha[n];
-          tmem_st_n<N>(lane_addr + j * N, reinterpret_cast<const uint32_t*>(ov));
-        }
-        __syncwarp();
+      for (int n = 0; n < N; ++n) {
+        const float e = ex2_approx(a[n]);
+        l[n] += e;                                                         // (lanes without a key: unused)
+        if (has_key) *reinterpret_cast<__nv_bfloat16*>(at[n & 7] + n * 128) = __float2bfloat16_rn(e);   // the operand type
       }
-      if (has_key) {
-        // P's buffer: the product that read it last is done.
-        if (g >= L::PBUF) {
-          const int f = g - L::PBUF;
-          if (!c.wait_all(L::OD + (f & 1), (f >> 1) & 1)) { ok = false; break; }
-        }
-        const uint32_t base = c.sbase + L::OFF_P + (g % L::PBUF) * L::QPANEL + (key & 7) * 2;
-        const int chunk = key >> 3;
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-          const float e = ex2_approx(sv[n] - (m[n] == NEG_INF ? 0.f : m[n]));
-          l[n] += e;
-          const uint16_t h = __bfloat16_as_ushort(__float2bfloat16_rn(e));   // the operand type
-          asm volatile("st.shared.u16 [%0], %1;" ::"r"(base + n * 128 + ((chunk ^ (n & 7)) << 4)), "h"(h) : "memory");
-        }
-        fence_async_shared();
-      }
+      fence_async_shared();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(c.bar(L::PR + sb));
     }
     if (!ok) break;
-    // The part's end: the sums over all keys, then O out of TMEM.
-    float* mine = xchg + (xs & 1) * 2 * N;
-    if (has_key) reduce_rows<N>(l, mine + w * N, lane, [](float a, float b) { return a + b; });
+    // The part's end: the sums over all keys; lane n of warp 0 has row n (and n + 32).
+    if (!exchange()) break;   // (rows may still be read by the last tile's third pass)
+#pragma unroll
+    for (int n = 0; n < N; ++n) l[n] = has_key ? l[n] : 0.f;
+    reduce_rows<N>(l, rows + w * N, lane, [](float x, float y) { return x + y; });
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      if (w == 0 && lane == n % 32) scale[n] = neg_m[n];
+    if (!exchange()) break;
+    char* slot = ws_slots + (size_t)u.slot * slot_bytes(N);
+    if (w == 0) {
+#pragma unroll 1
+      for (int n = lane; n < N; n += 32) {
+        const float sum = (rows[n] + rows[N + n]) + (rows[2 * N + n] + rows[3 * N + n]);
+        const bool empty = !(sum > 0.f);
+        const float m = empty ? NEG_INF : -scale[n];
+        scale[n] = !u.whole ? 1.f : empty ? 0.f : 1.f / sum;
+        if (n < u.npairs) {
+          float lg;
+          asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(sum));
+          if (!u.whole) reinterpret_cast<float2*>(slot + slot_ml(N))[n] = make_float2(m, sum);
+          else if (p.t.lse) p.t.lse[u.pair0 + n] = empty ? NEG_INF : (m + lg) * 0.6931471805599453f;
+        }
+      }
+    }
     if (!exchange()) break;
     if (!c.wait_all(L::OD + ((g - 1) & 1), ((g - 1) >> 1) & 1)) break;
     tc_fence_after();
-#pragma unroll
-    for (int n = 0; n < N; ++n) l[n] = mine[n] + mine[N + n];
-    char* slot = ws_slots + (size_t)u.slot * slot_bytes(N);
+    __nv_bfloat16* out = p.t.o + u.pair0 * 512 + 32 * w + lane;
+    float* part = reinterpret_cast<float*>(slot) + 32 * w + lane;
 #pragma unroll 1
     for (int j = 0; j < 4; ++j) {
       float ov[N];
       tmem_ld_n<N>(lane_addr + j * N, reinterpret_cast<uint32_t*>(ov));
-      const int col = 128 * j + 32 * w + lane;
-      if (u.whole) {
-        __nv_bfloat16* d = p.t.o + u.pair0 * 512 + col;
-#pragma unroll
-        for (int n = 0; n < N; ++n)
-          if (n < u.npairs) d[(int64_t)n * 512] = __float2bfloat16_rn(l[n] > 0.f ? ov[n] * (1.f / l[n]) : 0.f);
-      } else {
-        float* d = reinterpret_cast<float*>(slot) + col;
-#pragma unroll
-        for (int n = 0; n < N; ++n)
-          if (n < u.npairs) d[n * 512] = ov[n];
-      }
-    }
-    if (w == 0 && lane == 0) {
-      float2* ml = reinterpret_cast<float2*>(slot + slot_ml(N));
 #pragma unroll
       for (int n = 0; n < N; ++n) {
         if (n < u.npairs) {
-          if (!u.whole) ml[n] = make_float2(m[n], l[n]);
-          else if (p.t.lse) p.t.lse[u.pair0 + n] = l[n] > 0.f ? (m[n] + __log2f(l[n])) * 0.6931471805599453f : NEG_INF;
+          // (O is finite where l is not 0; a row without a key is 0 whatever is there.)
+          const float k = scale[n], x = k == 0.f ? 0.f : ov[n] * k;
+          if (u.whole) out[128 * j + n * 512] = __float2bfloat16_rn(x);
+          else part[128 * j + n * 512] = x;
         }
       }
     }
     tc_fence_before();   // O has been read: the next part's first P-ready lets it be overwritten
     __syncwarp();
+    if (!exchange()) break;   // rows and scale have been read
   }
 }
 
