@@ -20,18 +20,22 @@ struct TreeLaunch {
   int force_timeout;
 };
 
-// Workspace: header, one record per worker (where its piece starts), two slots per worker.
-struct Header {
-  int64_t total;       // tiles of all units
-  int workers;         // that share them
-  int pad;
-};
+// Workspace: one record per worker, two slots per worker.
+// Where a worker's piece starts.
 struct StartRec {
   int req, unit, tile, pad;
 };
+// The unit that the boundary before a worker cuts, if it is the unit's first such boundary: parts
+// k = 0 .. parts - 1 belong to workers w - 1 + k, each that worker's first part (slot 0) except that
+// part 0 may be a later one (slot0).
+struct JoinRec {
+  int64_t pair0;       // first pair of the unit
+  int npairs;
+  int parts;           // 0: nothing to join here
+  int slot0, pad[3];
+};
 constexpr int MAX_WORKERS = 256;
-constexpr size_t WS_STARTS = 64;
-constexpr size_t WS_SLOTS = (WS_STARTS + MAX_WORKERS * sizeof(StartRec) + 255) / 256 * 256;
+constexpr size_t WS_SLOTS = MAX_WORKERS * sizeof(JoinRec);
 // A slot: the rows' O (fp32), then their (m in log2 units, l).
 __host__ __device__ constexpr size_t slot_ml(int rows) { return (size_t)rows * 512 * 4; }
 __host__ __device__ constexpr size_t slot_bytes(int rows) { return slot_ml(rows) + (size_t)rows * 2 * 4; }
@@ -243,10 +247,11 @@ __device__ __forceinline__ uint64_t visible(const TreeParams& p, const Part& u, 
   return v;
 }
 
-// Where worker w's piece starts, and how long it is; every thread of the CTA calls.
+// Where worker w's piece starts and how long it is, and what is to be joined at its start; every
+// thread of the CTA calls.
 template <int ROWS, int KEYS, int NTHREADS>
 __device__ __forceinline__ void find_piece(const TreeParams& p, int worker, int workers, bool report, StartRec* start,
-                           int64_t* count, Header* head) {
+                                           int64_t* count, JoinRec* join) {
   __shared__ int64_t warp_sum[NTHREADS / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.batch + NTHREADS - 1) / NTHREADS;
@@ -269,27 +274,37 @@ __device__ __forceinline__ void find_piece(const TreeParams& p, int worker, int 
     if (w < warp) before += warp_sum[w];
     total += warp_sum[w];
   }
-  const int n = (int)min((int64_t)workers, total);   // a tile is worth a worker (700 keys: 26 us, two tiles each: 30)
-  const int64_t lo = worker < n ? total * worker / n : total, hi = worker < n ? total * (worker + 1) / n : total;
-  if (tid == 0) {
-    *count = hi - lo;
-    *head = Header{total, n, 0};
-  }
+  const int n = (int)min((int64_t)workers, total);   // a tile is worth a worker
+  auto at = [&](int w) { return total * w / n; };
+  const int64_t lo = worker < n ? at(worker) : total, hi = worker < n ? at(worker + 1) : total;
+  if (tid == 0) *count = hi - lo;
+  if (tid == 0 && lo >= hi) *join = JoinRec{0, 0, 0, 0, {}};
   if (lo < hi && lo >= before && lo < before + mine) {
-    int64_t at = before;
+    int64_t sum = before;
     for (int r = r0; r < r1; ++r) {
       const Req q = load_req<ROWS, KEYS>(p, r, false);
       const int64_t k = (int64_t)q.units * q.tiles;
-      if (lo < at + k) {
-        *start = StartRec{r, (int)((lo - at) / q.tiles), (int)((lo - at) % q.tiles), 0};
+      if (lo < sum + k) {
+        const int unit = (int)((lo - sum) / q.tiles), tile = (int)((lo - sum) % q.tiles);
+        *start = StartRec{r, unit, tile, 0};
+        JoinRec j{0, 0, 0, 0, {}};
+        const int64_t first = lo - tile, prev = worker > 0 ? at(worker - 1) : 0;   // the unit's first tile
+        if (tile > 0 && prev <= first) {
+          // The last worker with a part: at(w) < first + tiles, i.e. total * w / n < first + tiles.
+          const int last = (int)min((int64_t)(n - 1), ((first + q.tiles) * n - 1) / total);
+          j.pair0 = (int64_t)q.q0 * p.num_heads + (int64_t)unit * ROWS;
+          j.npairs = (int)min((int64_t)ROWS, (int64_t)q.nodes * p.num_heads - (int64_t)unit * ROWS);
+          j.parts = last - worker + 2;
+          j.slot0 = prev < first ? 1 : 0;
+        }
+        *join = j;
         break;
       }
-      at += k;
+      sum += k;
     }
   }
   __syncthreads();
 }
-
 
 // For block sizes that are multiples of 64: lane i's row of the 64 keys from key0 + i * stride on,
 // i < n; -1 where they are not all readable.  One look-up for 32 tiles: what a producer warp does

@@ -575,7 +575,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   extern __shared__ uint8_t smem_raw[];
   __shared__ StartRec start;
   __shared__ int64_t count;
-  __shared__ Header head;
+  __shared__ JoinRec join;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
@@ -583,6 +583,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   const uint32_t rank = cluster_ctarank();
   const int worker = blockIdx.x >> 1;
   const Ctx c{smem_addr(smem), abort_flag, p.t.status, p.wait_limit_ns, rank};
+  launch_dependents();   // the join kernel, which waits for this one to end
   if (threadIdx.x == 0) {
     for (int i = 0; i < NBAR; ++i) mbar_init(c.bar(i), 1);
     for (int i = 0; i < 2; ++i) mbar_init(c.bar(XB + i), 2);      // the two warps of 32 rows
@@ -603,12 +604,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     tmem_alloc_pair(smem_addr(tmem_slot), TMEM_COLS);
     tmem_relinquish_pair();
   }
-  find_piece<ROWS, KEYS, NTHREADS>(p.t, worker, p.workers, blockIdx.x == 0, &start, &count, &head);
+  find_piece<ROWS, KEYS, NTHREADS>(p.t, worker, p.workers, blockIdx.x == 0, &start, &count, &join);
   char* ws = static_cast<char*>(p.t.workspace);
-  if (threadIdx.x == 0 && rank == 0) {
-    if (worker == 0) *reinterpret_cast<Header*>(ws) = head;
-    if (count > 0) reinterpret_cast<StartRec*>(ws + WS_STARTS)[worker] = start;
-  }
+  if (threadIdx.x == 0 && rank == 0) reinterpret_cast<JoinRec*>(ws)[worker] = join;
   tc_fence_before();
   __syncthreads();
   cluster_sync();   // both CTAs' barriers exist before any remote arrival
@@ -725,9 +723,8 @@ cudaError_t launch_tree_attention(const TreeParams& t, cudaStream_t stream) {
   if (p.grouped) {
     const uint64_t dims[3] = {64, slots, NP}, strides[2] = {576 * 2, 64 * 2};
     const uint32_t box2[3] = {64, 64, 2}, box3[3] = {64, 64, 3};
-    if (make_tensor_map_bf16(&t2, rows, 3, dims, strides, box2) != MLA_OK ||
-        make_tensor_map_bf16(&t3, rows, 3, dims, strides, box3) != MLA_OK)
-      return cudaErrorInvalidValue;
+    if (make_tensor_map_bf16(&t2, rows, 3, dims, strides, box2) != MLA_OK) return cudaErrorInvalidValue;
+    if (!few && make_tensor_map_bf16(&t3, rows, 3, dims, strides, box3) != MLA_OK) return cudaErrorInvalidValue;
   }
   p.oob_row = (int32_t)slots;
   p.o_align32 = (reinterpret_cast<uintptr_t>(t.o) & 31u) == 0;

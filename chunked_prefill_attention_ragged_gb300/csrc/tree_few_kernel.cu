@@ -582,13 +582,14 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
   extern __shared__ uint8_t smem_raw[];
   __shared__ StartRec start;
   __shared__ int64_t count;
-  __shared__ Header head;
+  __shared__ JoinRec join;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   int* abort_flag = reinterpret_cast<int*>(smem + L::OFF_MISC + 4);
   const int worker = blockIdx.x;
   const Ctx<N> c{smem_addr(smem), abort_flag, p.t.status, p.wait_limit_ns};
+  launch_dependents();   // the join kernel, which waits for this one to end
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::NBAR; ++i) mbar_init(c.bar(i), 1);
     mbar_init(c.bar(L::XB), 4);                                  // the four softmax warps
@@ -606,12 +607,9 @@ tree_few_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     tmem_alloc(smem_addr(tmem_slot), L::TMEM);
     tmem_relinquish();
   }
-  find_piece<N, KEYS, NTHREADS>(p.t, worker, p.workers, blockIdx.x == 0, &start, &count, &head);
+  find_piece<N, KEYS, NTHREADS>(p.t, worker, p.workers, blockIdx.x == 0, &start, &count, &join);
   char* ws = static_cast<char*>(p.t.workspace);
-  if (threadIdx.x == 0) {
-    if (worker == 0) *reinterpret_cast<Header*>(ws) = head;
-    if (count > 0) reinterpret_cast<StartRec*>(ws + WS_STARTS)[worker] = start;
-  }
+  if (threadIdx.x == 0) reinterpret_cast<JoinRec*>(ws)[worker] = join;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

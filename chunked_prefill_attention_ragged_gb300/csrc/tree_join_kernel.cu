@@ -6,35 +6,24 @@
 namespace mla {
 namespace {
 
-// One CTA per eight rows of a unit that a boundary between two workers cuts; the unit's first
-// such boundary does it.  A warp has a row: the parts' (m, l) one per lane, then their O rows,
-// 16 columns per lane.
+// One CTA per eight rows of a unit that a boundary between two workers cuts (the unit's first such
+// boundary).  A warp has a row: the parts' (m, l) one per lane, then their O rows, 16 columns per
+// lane.  Bound by latency: record, (m, l), O, result, each waits for the one before.
 constexpr int JOIN_WARPS = 8;
 
-template <int ROWS, int KEYS>
+template <int ROWS>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) tree_join_kernel(const __grid_constant__ TreeLaunch p) {
+  wait_for_previous();   // launched early: everything read here comes from the kernel before
   const char* ws = static_cast<const char*>(p.t.workspace);
-  const Header head = *reinterpret_cast<const Header*>(ws);
   const int b = blockIdx.x + 1;   // the boundary before worker b
-  if (b >= head.workers) return;
-  const StartRec s = reinterpret_cast<const StartRec*>(ws + WS_STARTS)[b];
-  if (s.tile == 0) return;        // between two units
-  auto lo = [&](int w) { return head.total * w / head.workers; };
-  const int64_t a = lo(b) - s.tile;
-  if (lo(b - 1) > a) return;      // an earlier boundary cuts the same unit
-  const Req q = load_req<ROWS, KEYS>(p.t, s.req, false);
-  const int64_t end = a + q.tiles;
+  const JoinRec j = reinterpret_cast<const JoinRec*>(ws)[b];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = blockIdx.y * JOIN_WARPS + warp;
-  const int64_t first = (int64_t)s.unit * ROWS;
-  if (first + row >= (int64_t)q.nodes * p.t.num_heads) return;
-  const int64_t pair = (int64_t)q.q0 * p.t.num_heads + first + row;
-  int n = 1;                      // workers b - 1, b, .. that have a part
-  while (b + n - 1 < head.workers && lo(b + n - 1) < end) ++n;
-  const char* slots = ws + WS_SLOTS;
-  // Part k belongs to worker b - 1 + k: its first part, except that worker b - 1 may have begun
-  // with another unit.
-  auto slot = [&](int k) { return slots + (size_t)(2 * (b - 1 + k) + (k == 0 && lo(b - 1) < a ? 1 : 0)) * slot_bytes(ROWS); };
+  if (row >= j.npairs || j.parts == 0) return;
+  const int64_t pair = j.pair0 + row;
+  const int n = j.parts;
+  const char* slots = ws + WS_SLOTS + (size_t)2 * (b - 1) * slot_bytes(ROWS);
+  auto slot = [&](int k) { return slots + (size_t)(2 * k + (k == 0 ? j.slot0 : 0)) * slot_bytes(ROWS); };
   const float NEG_INF = -__int_as_float(0x7f800000);
   float m = NEG_INF;
   for (int k = lane; k < n; k += 32) m = fmaxf(m, reinterpret_cast<const float2*>(slot(k) + slot_ml(ROWS))[row].x);
@@ -85,14 +74,22 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) tree_join_kernel(const __grid
 cudaError_t launch_tree_join(const TreeLaunch& p, int rows, cudaStream_t stream) {
   if (p.workers < 2) return cudaSuccess;
   const dim3 grid(p.workers - 1, (rows + JOIN_WARPS - 1) / JOIN_WARPS), block(JOIN_WARPS * 32);
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   switch (rows) {
-    case 128: tree_join_kernel<128, 128><<<grid, block, 0, stream>>>(p); break;
-    case 64: tree_join_kernel<64, 64><<<grid, block, 0, stream>>>(p); break;
-    case 32: tree_join_kernel<32, 64><<<grid, block, 0, stream>>>(p); break;
-    case 16: tree_join_kernel<16, 64><<<grid, block, 0, stream>>>(p); break;
+    case 128: return cudaLaunchKernelEx(&cfg, tree_join_kernel<128>, p);
+    case 64: return cudaLaunchKernelEx(&cfg, tree_join_kernel<64>, p);
+    case 32: return cudaLaunchKernelEx(&cfg, tree_join_kernel<32>, p);
+    case 16: return cudaLaunchKernelEx(&cfg, tree_join_kernel<16>, p);
     default: return cudaErrorInvalidValue;
   }
-  return cudaGetLastError();
 }
 
 }  // namespace mla
