@@ -108,14 +108,10 @@ struct Ctx {
 };
 
 // 64 keys x panels [panel0, panel0 + n) to n consecutive 8 KB panels at dst, completing on `bar`
-// (of the even CTA).  tg: the map whose boxes hold exactly n panels.
+// (of the even CTA).
 __device__ __forceinline__ void copy_panels(const TreeLaunch& p, const KeyRows& k, uint32_t dst, uint32_t bar,
-                                            const CUtensorMap* tc, const CUtensorMap* tb, const CUtensorMap* tg,
-                                            int panel0, int n, int lane) {
-  if (k.by_block && p.grouped) {
-    if (lane == 0) tma_load_3d_pair(dst, tg, bar, 0, k.r[0], panel0);
-    return;
-  }
+                                            const CUtensorMap* tc, const CUtensorMap* tb, int panel0, int n,
+                                            int lane) {
 #pragma unroll 1
   for (int i = 0; i < n; ++i) {
     const int col = (panel0 + i) * 64;
@@ -150,8 +146,6 @@ __device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, PairParts par
   bool ok = true;
   Part u;
   while (ok && parts.next(&u)) {
-    int64_t key0 = (int64_t)u.lo * KEYS + 64 * c.rank;
-    KeyBlocks blocks = find_blocks(p, u, key0, lane);
     if (lane == 0) {
       if (units > 0) ok = c.wait(QE, (units - 1) & 1);
       if (ok) {
@@ -163,19 +157,37 @@ __device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, PairParts par
     ok = __shfl_sync(0xffffffffu, ok, 0);
     if (!ok) break;
     ++units;
-    for (int t = u.lo; t < u.hi && ok; ++t, ++tiles, key0 += KEYS) {
-      const KeyRows k = find_rows(p, u, blocks, key0, lane);
-      if (t + 1 < u.hi) blocks = find_blocks(p, u, key0 + KEYS, lane);
+    int32_t ahead = -1;   // rows of 32 tiles
 #pragma unroll 1
-      for (int g = 0; g < KGROUPS; ++g) {
+    for (int t = u.lo; t < u.hi && ok; ++t, ++tiles) {
+      const int i = (t - u.lo) & 31;
+      const int64_t key0 = (int64_t)t * KEYS + 64 * c.rank;
+      if (i == 0 && p.grouped) ahead = piece_rows(p, u, key0, KEYS, u.hi - t, lane);
+      const int32_t row = __shfl_sync(0xffffffffu, ahead, i);
+      if (row >= 0) {   // one lane, three copies
         if (lane == 0) {
-          if (tiles > 0) ok = c.wait(KE + g, (tiles - 1) & 1);
-          if (ok) expect_both(c, KF + g, 3 * QP);
+#pragma unroll 1
+          for (int g = 0; g < KGROUPS; ++g) {
+            if (tiles > 0) ok = c.wait(KE + g, (tiles - 1) & 1);
+            if (!ok) break;
+            expect_both(c, KF + g, 3 * QP);
+            tma_load_3d_pair(c.sbase + OFF_K + 3 * g * QP, t3, kf + 8 * g, 0, row, 3 * g);
+            ++issued;
+          }
         }
-        if (!(k.by_block && p.grouped)) ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (ok) copy_panels(p, k, c.sbase + OFF_K + 3 * g * QP, kf + 8 * g, tc, tb, t3, 3 * g, 3, lane);
-        if (!ok) break;
-        ++issued;
+      } else {
+        const KeyRows k = find_rows(p, u, find_blocks(p, u, key0, lane), key0, lane);
+#pragma unroll 1
+        for (int g = 0; g < KGROUPS; ++g) {
+          if (lane == 0) {
+            if (tiles > 0) ok = c.wait(KE + g, (tiles - 1) & 1);
+            if (ok) expect_both(c, KF + g, 3 * QP);
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          copy_panels(p, k, c.sbase + OFF_K + 3 * g * QP, kf + 8 * g, tc, tb, 3 * g, 3, lane);
+          ++issued;
+        }
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
     }
@@ -202,27 +214,43 @@ __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, PairParts part
   bool ok = true;
   Part u;
   while (ok && parts.next(&u)) {
-    int64_t key0 = (int64_t)u.lo * KEYS;
-    KeyBlocks b0 = find_blocks(p, u, key0, lane), b1 = find_blocks(p, u, key0 + 64, lane);
-    for (int t = u.lo; t < u.hi && ok; ++t, ++tiles, key0 += KEYS) {
-      const KeyRows k0 = find_rows(p, u, b0, key0, lane), k1 = find_rows(p, u, b1, key0 + 64, lane);
-      if (t + 1 < u.hi) {
-        b0 = find_blocks(p, u, key0 + KEYS, lane);
-        b1 = find_blocks(p, u, key0 + KEYS + 64, lane);
-      }
-      const bool fast = k0.by_block && k1.by_block && p.grouped;
+    int32_t ahead0 = -1, ahead1 = -1;   // rows of 32 tiles' first and second halves
 #pragma unroll 1
-      for (int i = 0; i < 4; ++i) {   // chunk i / 2, key half i % 2
+    for (int t = u.lo; t < u.hi && ok; ++t, ++tiles) {
+      const int j = (t - u.lo) & 31;
+      const int64_t key0 = (int64_t)t * KEYS;
+      if (j == 0 && p.grouped) {
+        ahead0 = piece_rows(p, u, key0, KEYS, u.hi - t, lane);
+        ahead1 = piece_rows(p, u, key0 + 64, KEYS, u.hi - t, lane);
+      }
+      const int32_t row0 = __shfl_sync(0xffffffffu, ahead0, j), row1 = __shfl_sync(0xffffffffu, ahead1, j);
+      if (row1 >= 0) {   // (then row0 is, too) one lane, four copies
         if (lane == 0) {
-          if (tiles > 0) ok = c.wait(VE + i, (tiles - 1) & 1);
-          if (ok) expect_both(c, VF + i, 2 * QP);
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {   // chunk i / 2, key half i % 2
+            if (tiles > 0) ok = c.wait(VE + i, (tiles - 1) & 1);
+            if (!ok) break;
+            expect_both(c, VF + i, 2 * QP);
+            tma_load_3d_pair(c.sbase + OFF_V + i * 2 * QP, t2, vf + 8 * i, 0, i & 1 ? row1 : row0,
+                             4 * (i >> 1) + 2 * (int)c.rank);
+            ++issued;
+          }
         }
-        if (!fast) ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (ok)
-          copy_panels(p, i & 1 ? k1 : k0, c.sbase + OFF_V + i * 2 * QP, vf + 8 * i, tc, tb, t2,
+      } else {
+        const KeyRows k0 = find_rows(p, u, find_blocks(p, u, key0, lane), key0, lane);
+        const KeyRows k1 = find_rows(p, u, find_blocks(p, u, key0 + 64, lane), key0 + 64, lane);
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          if (lane == 0) {
+            if (tiles > 0) ok = c.wait(VE + i, (tiles - 1) & 1);
+            if (ok) expect_both(c, VF + i, 2 * QP);
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          copy_panels(p, i & 1 ? k1 : k0, c.sbase + OFF_V + i * 2 * QP, vf + 8 * i, tc, tb,
                       4 * (i >> 1) + 2 * (int)c.rank, 2, lane);
-        if (!ok) break;
-        ++issued;
+          ++issued;
+        }
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
     }
