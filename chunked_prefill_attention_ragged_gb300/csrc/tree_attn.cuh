@@ -307,13 +307,15 @@ __device__ __forceinline__ void find_piece(const TreeParams& p, int worker, int 
 }
 
 // For block sizes that are multiples of 64: lane i's row of the 64 keys from key0 + i * stride on,
-// i < n; -1 where they are not all readable.  One look-up for 32 tiles: what a producer warp does
-// between two copies has to be short (its code is not in the instruction cache when it comes back
-// to it, and costs about 400 clocks for every 60 instructions).
+// i < n, to be copied as one box.  Where only the first of them are readable the others come along
+// (they lie in the same block) and have to be kept from counting; where none is, the box lies past
+// the cache and is filled with zeros.  One look-up for 32 tiles: what a producer warp does between
+// two copies has to be short (its code is not in the instruction cache when it comes back to it,
+// and costs about 400 clocks for every 60 instructions).
 __device__ __forceinline__ int32_t piece_rows(const TreeLaunch& p, const Part& u, int64_t key0, int stride, int n,
                                               int lane) {
   const int64_t key = key0 + (int64_t)lane * stride;
-  return lane < n && key + 64 <= u.q.kv ? block_row(p, table_block(p, u, key), key) : -1;
+  return lane < n && key < u.q.kv ? block_row(p, table_block(p, u, key), key) : p.oob_row;
 }
 
 // tree_join_kernel.cu: joins the parts of units of `rows` pairs and tiles of `keys` keys

@@ -33,8 +33,9 @@
 //   warp 3     TMEM allocation; brings the next tile's rows into L2
 //   warps 4-7  softmax: two threads per pair (the two halves of the keys and of O's columns)
 // Order of products: S(t + 1) before P V(t), so that the tensor cores work on the next tile while
-// the softmax does this one.  Key rows come by whole boxes where a 64-row piece lies inside the
-// request and the block size allows, else by gather4 with rows past the end read as zeros.
+// the softmax does this one.  Key rows come by whole boxes of 64 where the block size is a multiple
+// of that (in the piece where the keys end, what lies behind them is made zero), else by smaller
+// boxes or by gather4 with rows past the end read as zeros.
 // Every wait is bounded: on time-out the CTA records MLA_DEVSTAT_TIMEOUT, drains its copies and
 // products, frees TMEM and returns.
 #include <cuda_bf16.h>
@@ -70,7 +71,9 @@ enum Bar {
   SF = VE + 4,         // [buffer] S done
   PR = SF + 2,         // P written (and the S buffer read) by every softmax warp of both CTAs
   OD,                  // P V done
-  XB,                  // [row half] maxima exchanged between the two warps of 32 rows
+  LB,                  // a partial piece of V landed (in this CTA)
+  ZB,                  // [chunk] the odd CTA's partial piece is ready
+  XB = ZB + 2,         // [row half] maxima exchanged between the two warps of 32 rows
   FIN = XB + 2,        // every product drained
   NEVER,               // nothing arrives here: the time-out test mode waits on it
   NBAR
@@ -157,14 +160,14 @@ __device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, PairParts par
     ok = __shfl_sync(0xffffffffu, ok, 0);
     if (!ok) break;
     ++units;
-    int32_t ahead = -1;   // rows of 32 tiles
+    int32_t ahead = 0;   // rows of 32 tiles
 #pragma unroll 1
     for (int t = u.lo; t < u.hi && ok; ++t, ++tiles) {
       const int i = (t - u.lo) & 31;
       const int64_t key0 = (int64_t)t * KEYS + 64 * c.rank;
       if (i == 0 && p.grouped) ahead = piece_rows(p, u, key0, KEYS, u.hi - t, lane);
       const int32_t row = __shfl_sync(0xffffffffu, ahead, i);
-      if (row >= 0) {   // one lane, three copies
+      if (p.grouped) {   // one lane, three copies
         if (lane == 0) {
 #pragma unroll 1
           for (int g = 0; g < KGROUPS; ++g) {
@@ -207,14 +210,15 @@ __device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, PairParts par
 }
 
 __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, PairParts parts, const CUtensorMap* tc,
-                               const CUtensorMap* tb, const CUtensorMap* t2) {
+                               const CUtensorMap* tb, const CUtensorMap* t2, uint8_t* smem) {
   const int lane = threadIdx.x & 31;
   const uint32_t vf = mapa_shared(c.bar(VF), 0);
   int tiles = 0, issued = 0;
+  int cuts = 0, zeros = 0;   // partial pieces, and tiles that have them
   bool ok = true;
   Part u;
   while (ok && parts.next(&u)) {
-    int32_t ahead0 = -1, ahead1 = -1;   // rows of 32 tiles' first and second halves
+    int32_t ahead0 = 0, ahead1 = 0;   // rows of 32 tiles' first and second halves
 #pragma unroll 1
     for (int t = u.lo; t < u.hi && ok; ++t, ++tiles) {
       const int j = (t - u.lo) & 31;
@@ -224,7 +228,8 @@ __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, PairParts part
         ahead1 = piece_rows(p, u, key0 + 64, KEYS, u.hi - t, lane);
       }
       const int32_t row0 = __shfl_sync(0xffffffffu, ahead0, j), row1 = __shfl_sync(0xffffffffu, ahead1, j);
-      if (row1 >= 0) {   // (then row0 is, too) one lane, four copies
+      const int64_t valid = u.q.kv - key0;   // keys of the tile
+      if (p.grouped && (valid >= KEYS || valid == 64 || valid <= 0)) {   // one lane, four copies
         if (lane == 0) {
 #pragma unroll 1
           for (int i = 0; i < 4; ++i) {   // chunk i / 2, key half i % 2
@@ -236,6 +241,46 @@ __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, PairParts part
             ++issued;
           }
         }
+      } else if (p.grouped) {
+        // The tile in which the keys end.  In that half the rows behind the last key came along: they
+        // are made zero (their P is 0, but 0 times what is there need not be).  Each CTA sees to its
+        // own, then the even one says that the half is there.
+        const int cut = valid < 64 ? 0 : 1, first = (int)(valid & 63);
+#pragma unroll 1
+        for (int i = 0; i < 4 && ok; ++i) {
+          const uint32_t dst = c.sbase + OFF_V + i * 2 * QP;
+          const int panel = 4 * (i >> 1) + 2 * (int)c.rank;
+          const bool mend = (i & 1) == cut;
+          if (lane == 0) {
+            if (tiles > 0) ok = c.wait(VE + i, (tiles - 1) & 1);
+            if (ok) {
+              if (mend) {
+                mbar_arrive_expect_tx(c.bar(LB), 2 * QP);
+                tma_load_3d(dst, t2, c.bar(LB), 0, i & 1 ? row1 : row0, panel);
+                ok = c.wait(LB, cuts & 1);
+                ++cuts;
+              } else {
+                expect_both(c, VF + i, 2 * QP);
+                tma_load_3d_pair(dst, t2, vf + 8 * i, 0, i & 1 ? row1 : row0, panel);
+              }
+              ++issued;
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!mend || !ok) continue;
+          uint8_t* at = smem + OFF_V + i * 2 * QP;
+          for (int k = lane; k < (64 - first) * 16; k += 32)
+            *reinterpret_cast<uint4*>(at + (k & 8 ? QP : 0) + (first + (k >> 4)) * 128 + (k & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            if (c.rank != 0) mbar_arrive_remote(mapa_shared(c.bar(ZB + (i >> 1)), 0));
+            else if ((ok = c.wait(ZB + (i >> 1), zeros & 1))) mbar_arrive(c.bar(VF + i));
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+        ++zeros;
       } else {
         const KeyRows k0 = find_rows(p, u, find_blocks(p, u, key0, lane), key0, lane);
         const KeyRows k1 = find_rows(p, u, find_blocks(p, u, key0 + 64, lane), key0 + 64, lane);
@@ -261,9 +306,8 @@ __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, PairParts part
         const int n = (issued + 3 - i) / 4;
         if (n) c.drain(VF + i, (n - 1) & 1);
       }
-    } else if (!ok) {
-      settle();
     }
+    if (!ok) settle();
   }
 }
 
@@ -644,7 +688,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   if (warp == 0) {
     run_producer_qk(c, p, parts, &tm_q, &tm_c, &tm_b, &tm_3);
   } else if (warp == 2) {
-    run_producer_v(c, p, parts, &tm_c, &tm_b, &tm_2);
+    run_producer_v(c, p, parts, &tm_c, &tm_b, &tm_2, smem);
   } else if (warp == 1) {
     if (rank == 0) run_mma(c, p, parts, tmem);
   } else if (warp == 3) {

@@ -133,13 +133,13 @@ __device__ void run_producer(const Ctx<N>& c, const TreeLaunch& p, Parts<N, KEYS
   };
   Part u;
   while (ok && parts.next(&u)) {
-    int32_t ahead = -1;   // rows of 32 tiles
+    int32_t ahead = 0;   // rows of 32 tiles
 #pragma unroll 1
     for (int t = u.lo; t < u.hi && ok; ++t) {
       const int i = (t - u.lo) & 31;
       if (i == 0 && p.grouped) ahead = piece_rows(p, u, (int64_t)t * KEYS, KEYS, u.hi - t, lane);
       const int32_t row = __shfl_sync(0xffffffffu, ahead, i);
-      if (row >= 0) {   // one lane, five copies
+      if (p.grouped) {   // one lane, five copies
         if (lane == 0) {
           if (ropes >= L::ROPES) ok = c.wait(L::RE + rr.slot, rr.phase ^ 1);
           if (ok) {
@@ -502,6 +502,18 @@ __device__ void run_softmax(const Ctx<N>& c, const TreeLaunch& p, Parts<N, KEYS>
         if (!(f.x | f.y | f.z | f.w)) break;   // no maximum has moved: the same in all four warps
       }
       if (!ok) break;
+      // Copied along behind the last key: zero as values (their P is 0, but 0 times what is there
+      // need not be).  S, which read them too, is done.
+      const int valid = u.q.kv - t * KEYS;
+      if (p.grouped && valid > 0 && valid < KEYS) {
+#pragma unroll 1
+        for (int i = (threadIdx.x & 127); i < (KEYS - valid) * 64; i += 128) {
+          const int panel = (i >> 3) & 7, row = valid + (i >> 6);
+          const int pair_slot = (4 * g + (panel >> 1)) % L::PAIRS;
+          *reinterpret_cast<uint4*>(smem + L::OFF_PAIR + pair_slot * PAIR + (panel & 1) * PANEL + row * 128 +
+                                    (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+      }
       // P's buffer: the product that read it last is done.
       if (g >= L::PBUF) {
         const int d = g - L::PBUF;
