@@ -142,7 +142,8 @@ __device__ __forceinline__ void settle() {
 }
 
 __device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, PairParts parts, const CUtensorMap* tq,
-                                const CUtensorMap* tc, const CUtensorMap* tb, const CUtensorMap* t3) {
+                                const CUtensorMap* tc, const CUtensorMap* tb, const CUtensorMap* t3,
+                                volatile int* begun) {
   const int lane = threadIdx.x & 31;
   const uint32_t qf = mapa_shared(c.bar(QF), 0), kf = mapa_shared(c.bar(KF), 0);
   int tiles = 0, units = 0, issued = 0;   // tiles begun, parts, K groups
@@ -167,6 +168,7 @@ __device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, PairParts par
       const int64_t key0 = (int64_t)t * KEYS + 64 * c.rank;
       if (i == 0 && p.grouped) ahead = piece_rows(p, u, key0, KEYS, u.hi - t, lane);
       const int32_t row = __shfl_sync(0xffffffffu, ahead, i);
+      if (lane == 0) *begun = tiles;
       if (p.grouped) {   // one lane, three copies
         if (lane == 0) {
 #pragma unroll 1
@@ -313,8 +315,10 @@ __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, PairParts part
 
 // Warp 3: this CTA's keys of the tile after the one being loaded, into L2.  The one-tile buffers
 // leave a load less than a tile's time, which DRAM does not keep to: with the rows in L2 it does.
+// It follows the K producer's count of tiles, which only grows (on a barrier's phases a warp that
+// fell two tiles behind would wait for one that never comes), and gives up quietly.
 __device__ void run_prefetch(const Ctx& c, const TreeLaunch& p, PairParts parts, const CUtensorMap* tb,
-                             const CUtensorMap* t3) {
+                             const CUtensorMap* t3, const volatile int* begun) {
   if (p.piece_rows == 0) return;
   const int lane = threadIdx.x & 31, pieces = 64 / p.piece_rows;
   int tiles = 0;
@@ -322,6 +326,12 @@ __device__ void run_prefetch(const Ctx& c, const TreeLaunch& p, PairParts parts,
   while (parts.next(&u)) {
     for (int t = u.lo; t < u.hi; ++t, ++tiles) {
       const int64_t key0 = (int64_t)(t + 1) * KEYS + 64 * c.rank;
+      const uint64_t t0 = global_timer_ns();
+      while (*begun < tiles) {   // tile t is not being loaded yet
+        __nanosleep(200);
+        if (*c.abort_flag || global_timer_ns() - t0 > p.wait_limit_ns) return;
+      }
+      __syncwarp();
       if (t + 1 < u.hi && key0 + 64 <= u.q.kv && lane < pieces) {
         const int64_t key = key0 + lane * p.piece_rows;
         const int32_t row = block_row(p, table_block(p, u, key), key);
@@ -333,8 +343,6 @@ __device__ void run_prefetch(const Ctx& c, const TreeLaunch& p, PairParts parts,
           for (int i = 0; i < NP; ++i) tma_prefetch_2d(tb, i * 64, row);
         }
       }
-      // Not faster than the products: tile t's first panels have been read.
-      if (!c.wait_warp(KE, tiles & 1)) return;
     }
   }
 }
@@ -652,6 +660,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   int* abort_flag = reinterpret_cast<int*>(smem + OFF_MISC + 4);
+  int* begun = reinterpret_cast<int*>(smem + OFF_MISC + 8);   // tiles that the K producer has begun, less one
   const uint32_t rank = cluster_ctarank();
   const int worker = blockIdx.x >> 1;
   const Ctx c{smem_addr(smem), abort_flag, p.t.status, p.wait_limit_ns, rank};
@@ -661,6 +670,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     for (int i = 0; i < 2; ++i) mbar_init(c.bar(XB + i), 2);      // the two warps of 32 rows
     mbar_init(c.bar(PR), 8);                                        // every softmax warp, of both CTAs
     *abort_flag = 0;
+    *begun = -1;
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
@@ -686,13 +696,13 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const PairParts parts(p.t, start, count);
   if (warp == 0) {
-    run_producer_qk(c, p, parts, &tm_q, &tm_c, &tm_b, &tm_3);
+    run_producer_qk(c, p, parts, &tm_q, &tm_c, &tm_b, &tm_3, begun);
   } else if (warp == 2) {
     run_producer_v(c, p, parts, &tm_c, &tm_b, &tm_2, smem);
   } else if (warp == 1) {
     if (rank == 0) run_mma(c, p, parts, tmem);
   } else if (warp == 3) {
-    run_prefetch(c, p, parts, &tm_b, &tm_3);
+    run_prefetch(c, p, parts, &tm_b, &tm_3, begun);
   } else {
     run_softmax(c, p, parts, tmem, ws + WS_SLOTS + (size_t)worker * 2 * SLOT_BYTES, smem);
   }

@@ -82,7 +82,7 @@ cudaError_t launch_tree_join(const TreeLaunch& p, int rows, cudaStream_t stream)
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 0;
   switch (rows) {
     case 128: return cudaLaunchKernelEx(&cfg, tree_join_kernel<128>, p);
     case 64: return cudaLaunchKernelEx(&cfg, tree_join_kernel<64>, p);
