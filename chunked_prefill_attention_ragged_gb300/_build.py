@@ -37,7 +37,6 @@ SOURCES = [
     "tables_kernel.cu",
     "tree_kernels.cu",
     "tree_attn_kernel.cu",
-    "tree_few_kernel.cu",
     "tree_join_kernel.cu",
 ]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]

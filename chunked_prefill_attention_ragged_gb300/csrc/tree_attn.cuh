@@ -6,9 +6,12 @@
 
 namespace mla {
 
+constexpr int TREE_ROWS = 128;   // (node, head) pairs per unit
+constexpr int TREE_KEYS = 128;   // keys per tile
+
 struct TreeLaunch {
   TreeParams t;
-  int workers;
+  int workers;         // clusters of two CTAs
   int32_t oob_row;     // a row coordinate past the cache: the copy fills it with zeros
   int block_shift;     // log2 of the block size, or -1
   int piece_rows;      // rows of one box of the block map (0: gather4 only)
@@ -21,10 +24,6 @@ struct TreeLaunch {
 };
 
 // Workspace: one record per worker, two slots per worker.
-// Where a worker's piece starts.
-struct StartRec {
-  int req, unit, tile, pad;
-};
 // The unit that the boundary before a worker cuts, if it is the unit's first such boundary: parts
 // k = 0 .. parts - 1 belong to workers w - 1 + k, each that worker's first part (slot 0) except that
 // part 0 may be a later one (slot0).
@@ -37,8 +36,8 @@ struct JoinRec {
 constexpr int MAX_WORKERS = 256;
 constexpr size_t WS_SLOTS = MAX_WORKERS * sizeof(JoinRec);
 // A slot: the rows' O (fp32), then their (m in log2 units, l).
-__host__ __device__ constexpr size_t slot_ml(int rows) { return (size_t)rows * 512 * 4; }
-__host__ __device__ constexpr size_t slot_bytes(int rows) { return slot_ml(rows) + (size_t)rows * 2 * 4; }
+constexpr size_t SLOT_ML = (size_t)TREE_ROWS * 512 * 4;
+constexpr size_t SLOT_BYTES = SLOT_ML + TREE_ROWS * 2 * 4;
 
 // One lane's look at a barrier, whose result can be used later; for wait_warp's `seen`.
 __device__ __forceinline__ uint32_t look_warp(uint32_t bar, uint32_t parity) {
@@ -107,23 +106,35 @@ struct Req {
   int units, tiles;
 };
 
-// ROWS pairs a unit, KEYS keys a tile.
-template <int ROWS, int KEYS>
-__device__ __forceinline__ Req load_req(const TreeParams& p, int r, bool report) {
+struct ReqWords {
+  int q0, q1, len;
+};
+__device__ __forceinline__ ReqWords load_words(const TreeParams& p, int r) {
+  return {__ldg(p.qo_indptr + r), __ldg(p.qo_indptr + r + 1), __ldg(p.kv_lens + r)};
+}
+__device__ __forceinline__ Req make_req(const TreeParams& p, const ReqWords& w, bool report) {
   Req q;
-  const int q0 = __ldg(p.qo_indptr + r), q1 = __ldg(p.qo_indptr + r + 1), len = __ldg(p.kv_lens + r);
   const int64_t reach = (int64_t)p.max_blocks * p.block_size;
-  const bool rows_ok = q0 >= 0 && q1 >= q0 && q1 <= p.total_rows;
-  const bool len_ok = len >= 0 && len <= reach;
+  const bool rows_ok = w.q0 >= 0 && w.q1 >= w.q0 && w.q1 <= p.total_rows;
+  const bool len_ok = w.len >= 0 && w.len <= reach;
   if (report && p.status && (!rows_ok || !len_ok)) atomicOr(p.status, MLA_DEVSTAT_BAD_INDEX);
-  q.q0 = q0;
-  q.nodes = rows_ok ? q1 - q0 : 0;
-  q.ctx = (int64_t)len - q.nodes;
-  q.kv = len_ok ? len : (len < 0 ? 0 : (int)reach);
-  q.units = (int)(((int64_t)q.nodes * p.num_heads + ROWS - 1) / ROWS);
-  q.tiles = q.units ? max(1, (q.kv + KEYS - 1) / KEYS) : 0;
+  q.q0 = w.q0;
+  q.nodes = rows_ok ? w.q1 - w.q0 : 0;
+  q.ctx = (int64_t)w.len - q.nodes;
+  q.kv = len_ok ? w.len : (w.len < 0 ? 0 : (int)reach);
+  q.units = (int)(((int64_t)q.nodes * p.num_heads + TREE_ROWS - 1) / TREE_ROWS);
+  q.tiles = q.units ? max(1, (q.kv + TREE_KEYS - 1) / TREE_KEYS) : 0;
   return q;
 }
+__device__ __forceinline__ Req load_req(const TreeParams& p, int r, bool report) {
+  return make_req(p, load_words(p, r), report);
+}
+
+// Where a worker's piece starts.
+struct StartRec {
+  int req, unit, tile;
+  Req q;
+};
 
 // A part of a worker's piece: tiles [lo, hi) of one unit.
 struct Part {
@@ -136,29 +147,26 @@ struct Part {
   int slot;            // 0: the worker's first part, 1: a later one (its last, if not whole)
 };
 
-template <int ROWS, int KEYS>
 struct Parts {
   const TreeParams& p;
   int64_t left;
   int r, unit, tile, index;
   Req q;
   __device__ Parts(const TreeParams& tp, const StartRec& s, int64_t count)
-      : p(tp), left(count), r(s.req), unit(s.unit), tile(s.tile), index(0) {
-    if (left > 0) q = load_req<ROWS, KEYS>(p, r, false);
-  }
+      : p(tp), left(count), r(s.req), unit(s.unit), tile(s.tile), index(0), q(s.q) {}
   __device__ bool next(Part* out) {
     if (left <= 0) return false;
     while (unit >= q.units) {   // to the next request that has rows
       if (++r >= p.batch) return false;   // (lengths changed under the kernel: out of bounds is not read)
       unit = 0;
-      q = load_req<ROWS, KEYS>(p, r, false);
+      q = load_req(p, r, false);
     }
     const int n = (int)min((int64_t)(q.tiles - tile), left);
     out->q = q;
     out->r = r;
-    const int64_t first = (int64_t)unit * ROWS;
+    const int64_t first = (int64_t)unit * TREE_ROWS;
     out->pair0 = (int64_t)q.q0 * p.num_heads + first;
-    out->npairs = (int)min((int64_t)ROWS, (int64_t)q.nodes * p.num_heads - first);
+    out->npairs = (int)min((int64_t)TREE_ROWS, (int64_t)q.nodes * p.num_heads - first);
     out->lo = tile;
     out->hi = tile + n;
     out->whole = n == q.tiles;
@@ -172,23 +180,20 @@ struct Parts {
 };
 
 // Where 64 keys from `key0` on are, spread over the lanes: first the blocks as the table has them
-// (the loads are under way while the caller does other things), then the rows to copy.  Whole
-// pieces (by_block) come by boxes, lane k holding piece k; else lanes 0-15 hold keys 4 lane .. + 3
-// each.  A key past the readable ones, or in a block that the table does not name, is the row past
-// the cache (read as zeros), the latter flagged.
+// (the loads are under way while the caller does other things), then the rows to copy.  With block
+// sizes of 8, 16, 32 or multiples of 64 they come by boxes, lane k holding piece k; else lanes 0-15
+// hold keys 4 lane .. + 3 each.  A key past the readable ones, or in a block that the table does not
+// name, is the row past the cache (read as zeros), the latter flagged; in the piece in which the
+// readable keys end, what lies behind them comes along.
 constexpr int32_t PAST_END = -0x7fffffff - 1;
 struct KeyBlocks {
   int32_t b[4];
 };
 struct KeyRows {
-  bool by_block;
   int32_t r[4];
 };
 __device__ __forceinline__ int block_of(const TreeLaunch& p, int key) {
   return p.block_shift >= 0 ? key >> p.block_shift : key / p.t.block_size;
-}
-__device__ __forceinline__ bool whole_piece(const TreeLaunch& p, const Part& u, int64_t key0) {
-  return p.piece_rows > 0 && key0 + 64 <= u.q.kv;
 }
 __device__ __forceinline__ int32_t table_block(const TreeLaunch& p, const Part& u, int64_t key) {
   return key < u.q.kv ? __ldg(p.t.block_table + (int64_t)u.r * p.t.max_blocks + block_of(p, (int)key)) : PAST_END;
@@ -202,7 +207,7 @@ __device__ __forceinline__ int32_t block_row(const TreeLaunch& p, int32_t blk, i
 }
 __device__ __forceinline__ KeyBlocks find_blocks(const TreeLaunch& p, const Part& u, int64_t key0, int lane) {
   KeyBlocks k{{PAST_END, PAST_END, PAST_END, PAST_END}};
-  if (whole_piece(p, u, key0)) {
+  if (p.piece_rows > 0) {
     if (lane * p.piece_rows < 64) k.b[0] = table_block(p, u, key0 + lane * p.piece_rows);
   } else if (lane < 16) {
 #pragma unroll
@@ -213,8 +218,7 @@ __device__ __forceinline__ KeyBlocks find_blocks(const TreeLaunch& p, const Part
 __device__ __forceinline__ KeyRows find_rows(const TreeLaunch& p, const Part& u, const KeyBlocks& k, int64_t key0,
                                              int lane) {
   KeyRows w;
-  w.by_block = whole_piece(p, u, key0);
-  if (w.by_block) {
+  if (p.piece_rows > 0) {
     w.r[0] = block_row(p, k.b[0], key0 + lane * p.piece_rows);
   } else {
 #pragma unroll
@@ -248,17 +252,17 @@ __device__ __forceinline__ uint64_t visible(const TreeParams& p, const Part& u, 
 }
 
 // Where worker w's piece starts and how long it is, and what is to be joined at its start; every
-// thread of the CTA calls.
-template <int ROWS, int KEYS, int NTHREADS>
-__device__ __forceinline__ void find_piece(const TreeParams& p, int worker, int workers, bool report, StartRec* start,
-                                           int64_t* count, JoinRec* join) {
+// thread of the CTA calls, with the words of request threadIdx.x, loaded before.
+template <int NTHREADS>
+__device__ __forceinline__ void find_piece(const TreeParams& p, const ReqWords& own, int worker, int workers,
+                                           bool report, StartRec* start, int64_t* count, JoinRec* join) {
   __shared__ int64_t warp_sum[NTHREADS / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.batch + NTHREADS - 1) / NTHREADS;
   const int r0 = min(tid * per, p.batch), r1 = min(r0 + per, p.batch);
   int64_t mine = 0;
   for (int r = r0; r < r1; ++r) {
-    const Req q = load_req<ROWS, KEYS>(p, r, report);
+    const Req q = per == 1 ? make_req(p, own, report) : load_req(p, r, report);
     mine += (int64_t)q.units * q.tiles;
   }
   int64_t incl = mine;
@@ -282,18 +286,18 @@ __device__ __forceinline__ void find_piece(const TreeParams& p, int worker, int 
   if (lo < hi && lo >= before && lo < before + mine) {
     int64_t sum = before;
     for (int r = r0; r < r1; ++r) {
-      const Req q = load_req<ROWS, KEYS>(p, r, false);
+      const Req q = per == 1 ? make_req(p, own, false) : load_req(p, r, false);
       const int64_t k = (int64_t)q.units * q.tiles;
       if (lo < sum + k) {
         const int unit = (int)((lo - sum) / q.tiles), tile = (int)((lo - sum) % q.tiles);
-        *start = StartRec{r, unit, tile, 0};
+        *start = StartRec{r, unit, tile, q};
         JoinRec j{0, 0, 0, 0, {}};
         const int64_t first = lo - tile, prev = worker > 0 ? at(worker - 1) : 0;   // the unit's first tile
         if (tile > 0 && prev <= first) {
           // The last worker with a part: at(w) < first + tiles, i.e. total * w / n < first + tiles.
           const int last = (int)min((int64_t)(n - 1), ((first + q.tiles) * n - 1) / total);
-          j.pair0 = (int64_t)q.q0 * p.num_heads + (int64_t)unit * ROWS;
-          j.npairs = (int)min((int64_t)ROWS, (int64_t)q.nodes * p.num_heads - (int64_t)unit * ROWS);
+          j.pair0 = (int64_t)q.q0 * p.num_heads + (int64_t)unit * TREE_ROWS;
+          j.npairs = (int)min((int64_t)TREE_ROWS, (int64_t)q.nodes * p.num_heads - (int64_t)unit * TREE_ROWS);
           j.parts = last - worker + 2;
           j.slot0 = prev < first ? 1 : 0;
         }
@@ -318,14 +322,8 @@ __device__ __forceinline__ int32_t piece_rows(const TreeLaunch& p, const Part& u
   return lane < n && key < u.q.kv ? block_row(p, table_block(p, u, key), key) : p.oob_row;
 }
 
-// tree_join_kernel.cu: joins the parts of units of `rows` pairs and tiles of `keys` keys
-// (128 x 128, or 16, 32 or 64 x 64) that several workers left.
-cudaError_t launch_tree_join(const TreeLaunch& p, int rows, cudaStream_t stream);
-
-// tree_few_kernel.cu: units of 16, 32 or 64 pairs.  Workers (0 on error), and the launch.
-int tree_few_workers();
-cudaError_t launch_tree_few(const TreeLaunch& p, int rows, const CUtensorMap& tq, const CUtensorMap& tc,
-                            const CUtensorMap& tb, const CUtensorMap& t2, cudaStream_t stream);
+// tree_join_kernel.cu: joins the parts of units that several workers left.
+cudaError_t launch_tree_join(const TreeLaunch& p, cudaStream_t stream);
 
 constexpr uint64_t TREE_DRAIN_LIMIT_NS = 200000000ull;   // own copies and products after an abort
 constexpr float TREE_RESCALE_THRESHOLD = 8.0f;           // log2 units

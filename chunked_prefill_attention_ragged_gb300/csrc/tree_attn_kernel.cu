@@ -49,8 +49,7 @@
 namespace mla {
 namespace {
 
-constexpr int ROWS = 128;               // pairs per unit, 64 in each CTA
-constexpr int KEYS = 128;               // keys per tile
+constexpr int ROWS = TREE_ROWS, KEYS = TREE_KEYS;   // 64 rows in each CTA
 constexpr int QP = 64 * 128;            // a [64 rows, 64 columns] panel: 8 KB
 constexpr int NP = 9;                   // 64-column panels of 576
 constexpr int KGROUPS = 3;              // K panels arrive in groups of three
@@ -87,8 +86,6 @@ __device__ __forceinline__ constexpr uint32_t TM_O(int chunk) { return (uint32_t
 __device__ __forceinline__ constexpr uint32_t TM_S(int b) { return 256u + (uint32_t)b * 64u; }
 constexpr uint32_t IDESC_QK = idesc_bf16_f32(ROWS, KEYS, false, false);
 constexpr uint32_t IDESC_PV = idesc_bf16_f32(ROWS, 256, false, true);
-constexpr size_t SLOT_BYTES = slot_bytes(ROWS), SLOT_ML = slot_ml(ROWS);
-using PairParts = Parts<ROWS, KEYS>;
 
 struct Ctx {
   uint32_t sbase;
@@ -111,14 +108,14 @@ struct Ctx {
 };
 
 // 64 keys x panels [panel0, panel0 + n) to n consecutive 8 KB panels at dst, completing on `bar`
-// (of the even CTA).
+// (a shared::cluster address).  Not for maps of several panels.
 __device__ __forceinline__ void copy_panels(const TreeLaunch& p, const KeyRows& k, uint32_t dst, uint32_t bar,
                                             const CUtensorMap* tc, const CUtensorMap* tb, int panel0, int n,
                                             int lane) {
 #pragma unroll 1
   for (int i = 0; i < n; ++i) {
     const int col = (panel0 + i) * 64;
-    if (k.by_block) {
+    if (p.piece_rows > 0) {
       if (lane * p.piece_rows < 64) tma_load_2d_pair(dst + i * QP + lane * p.piece_rows * 128, tb, bar, col, k.r[0]);
     } else if (lane < 16) {
       tma_gather4_pair(dst + i * QP + lane * 4 * 128, tc, bar, col, k.r[0], k.r[1], k.r[2], k.r[3]);
@@ -141,7 +138,7 @@ __device__ __forceinline__ void settle() {
   }
 }
 
-__device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, PairParts parts, const CUtensorMap* tq,
+__device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, Parts parts, const CUtensorMap* tq,
                                 const CUtensorMap* tc, const CUtensorMap* tb, const CUtensorMap* t3,
                                 volatile int* begun) {
   const int lane = threadIdx.x & 31;
@@ -150,12 +147,13 @@ __device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, PairParts par
   bool ok = true;
   Part u;
   while (ok && parts.next(&u)) {
+    KeyBlocks blocks{};
+    if (!p.grouped) blocks = find_blocks(p, u, (int64_t)u.lo * KEYS + 64 * c.rank, lane);
     if (lane == 0) {
       if (units > 0) ok = c.wait(QE, (units - 1) & 1);
       if (ok) {
         expect_both(c, QF, NP * QP);
-        for (int i = 0; i < NP; ++i)
-          tma_load_2d_pair(c.sbase + OFF_Q + i * QP, tq, qf, i * 64, (int32_t)(u.pair0 + 64 * c.rank));
+        tma_load_3d_pair(c.sbase + OFF_Q, tq, qf, 0, (int32_t)(u.pair0 + 64 * c.rank), 0);
       }
     }
     ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -181,7 +179,8 @@ __device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, PairParts par
           }
         }
       } else {
-        const KeyRows k = find_rows(p, u, find_blocks(p, u, key0, lane), key0, lane);
+        const KeyRows k = find_rows(p, u, blocks, key0, lane);
+        if (t + 1 < u.hi) blocks = find_blocks(p, u, key0 + KEYS, lane);
 #pragma unroll 1
         for (int g = 0; g < KGROUPS; ++g) {
           if (lane == 0) {
@@ -211,7 +210,7 @@ __device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, PairParts par
   }
 }
 
-__device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, PairParts parts, const CUtensorMap* tc,
+__device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, Parts parts, const CUtensorMap* tc,
                                const CUtensorMap* tb, const CUtensorMap* t2, uint8_t* smem) {
   const int lane = threadIdx.x & 31;
   const uint32_t vf = mapa_shared(c.bar(VF), 0);
@@ -221,6 +220,11 @@ __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, PairParts part
   Part u;
   while (ok && parts.next(&u)) {
     int32_t ahead0 = 0, ahead1 = 0;   // rows of 32 tiles' first and second halves
+    KeyBlocks b0{}, b1{};
+    if (!p.grouped) {
+      b0 = find_blocks(p, u, (int64_t)u.lo * KEYS, lane);
+      b1 = find_blocks(p, u, (int64_t)u.lo * KEYS + 64, lane);
+    }
 #pragma unroll 1
     for (int t = u.lo; t < u.hi && ok; ++t, ++tiles) {
       const int j = (t - u.lo) & 31;
@@ -230,8 +234,10 @@ __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, PairParts part
         ahead1 = piece_rows(p, u, key0 + 64, KEYS, u.hi - t, lane);
       }
       const int32_t row0 = __shfl_sync(0xffffffffu, ahead0, j), row1 = __shfl_sync(0xffffffffu, ahead1, j);
-      const int64_t valid = u.q.kv - key0;   // keys of the tile
-      if (p.grouped && (valid >= KEYS || valid == 64 || valid <= 0)) {   // one lane, four copies
+      // The half in which the keys end brings along what lies behind them.
+      const int64_t valid = u.q.kv - key0;
+      const bool ends = p.piece_rows > 0 && valid > 0 && valid < KEYS && valid != 64;
+      if (p.grouped && !ends) {   // one lane, four copies
         if (lane == 0) {
 #pragma unroll 1
           for (int i = 0; i < 4; ++i) {   // chunk i / 2, key half i % 2
@@ -243,33 +249,42 @@ __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, PairParts part
             ++issued;
           }
         }
-      } else if (p.grouped) {
-        // The tile in which the keys end.  In that half the rows behind the last key came along: they
-        // are made zero (their P is 0, but 0 times what is there need not be).  Each CTA sees to its
-        // own, then the even one says that the half is there.
+      } else {
+        KeyRows k0{}, k1{};
+        if (!p.grouped) {
+          k0 = find_rows(p, u, b0, key0, lane);
+          k1 = find_rows(p, u, b1, key0 + 64, lane);
+          if (t + 1 < u.hi) {
+            b0 = find_blocks(p, u, key0 + KEYS, lane);
+            b1 = find_blocks(p, u, key0 + KEYS + 64, lane);
+          }
+        }
+        // Those rows are made zero (their P is 0, but 0 times what is there need not be).  Each CTA
+        // sees to its own, then the even one says that the half is there.
         const int cut = valid < 64 ? 0 : 1, first = (int)(valid & 63);
 #pragma unroll 1
         for (int i = 0; i < 4 && ok; ++i) {
           const uint32_t dst = c.sbase + OFF_V + i * 2 * QP;
           const int panel = 4 * (i >> 1) + 2 * (int)c.rank;
-          const bool mend = (i & 1) == cut;
+          const bool mend = ends && (i & 1) == cut;
           if (lane == 0) {
             if (tiles > 0) ok = c.wait(VE + i, (tiles - 1) & 1);
             if (ok) {
-              if (mend) {
-                mbar_arrive_expect_tx(c.bar(LB), 2 * QP);
-                tma_load_3d(dst, t2, c.bar(LB), 0, i & 1 ? row1 : row0, panel);
-                ok = c.wait(LB, cuts & 1);
-                ++cuts;
-              } else {
-                expect_both(c, VF + i, 2 * QP);
-                tma_load_3d_pair(dst, t2, vf + 8 * i, 0, i & 1 ? row1 : row0, panel);
-              }
-              ++issued;
+              if (mend) mbar_arrive_expect_tx(c.bar(LB), 2 * QP);
+              else expect_both(c, VF + i, 2 * QP);
             }
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!mend || !ok) continue;
+          if (!ok) break;
+          const uint32_t bar = mend ? mapa_shared(c.bar(LB), c.rank) : vf + 8 * i;
+          if (!p.grouped) copy_panels(p, i & 1 ? k1 : k0, dst, bar, tc, tb, panel, 2, lane);
+          else if (lane == 0) tma_load_3d_pair(dst, t2, bar, 0, i & 1 ? row1 : row0, panel);
+          ++issued;
+          if (!mend) continue;
+          if (lane == 0) ok = c.wait(LB, cuts & 1);
+          ++cuts;
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
           uint8_t* at = smem + OFF_V + i * 2 * QP;
           for (int k = lane; k < (64 - first) * 16; k += 32)
             *reinterpret_cast<uint4*>(at + (k & 8 ? QP : 0) + (first + (k >> 4)) * 128 + (k & 7) * 16) =
@@ -282,22 +297,7 @@ __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, PairParts part
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
         }
-        ++zeros;
-      } else {
-        const KeyRows k0 = find_rows(p, u, find_blocks(p, u, key0, lane), key0, lane);
-        const KeyRows k1 = find_rows(p, u, find_blocks(p, u, key0 + 64, lane), key0 + 64, lane);
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-          if (lane == 0) {
-            if (tiles > 0) ok = c.wait(VE + i, (tiles - 1) & 1);
-            if (ok) expect_both(c, VF + i, 2 * QP);
-          }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) break;
-          copy_panels(p, i & 1 ? k1 : k0, c.sbase + OFF_V + i * 2 * QP, vf + 8 * i, tc, tb,
-                      4 * (i >> 1) + 2 * (int)c.rank, 2, lane);
-          ++issued;
-        }
+        if (ends) ++zeros;
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
     }
@@ -317,7 +317,7 @@ __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, PairParts part
 // leave a load less than a tile's time, which DRAM does not keep to: with the rows in L2 it does.
 // It follows the K producer's count of tiles, which only grows (on a barrier's phases a warp that
 // fell two tiles behind would wait for one that never comes), and gives up quietly.
-__device__ void run_prefetch(const Ctx& c, const TreeLaunch& p, PairParts parts, const CUtensorMap* tb,
+__device__ void run_prefetch(const Ctx& c, const TreeLaunch& p, Parts parts, const CUtensorMap* tb,
                              const CUtensorMap* t3, const volatile int* begun) {
   if (p.piece_rows == 0) return;
   const int lane = threadIdx.x & 31, pieces = 64 / p.piece_rows;
@@ -375,7 +375,7 @@ __device__ __forceinline__ void commit_both(uint32_t bar) {
       : "memory");
 }
 
-__device__ void run_mma(const Ctx& c, const TreeLaunch& p, PairParts parts, uint32_t tmem) {
+__device__ void run_mma(const Ctx& c, const TreeLaunch& p, Parts parts, uint32_t tmem) {
   const uint64_t q_desc = sdesc_sw128(c.sbase + OFF_Q, 16, 1024);
   const uint64_t k_desc = sdesc_sw128(c.sbase + OFF_K, 16, 1024);
   const uint64_t v_desc = sdesc_sw128(c.sbase + OFF_V, QP, 1024);
@@ -467,7 +467,7 @@ __device__ __forceinline__ void st_shared_v4(uint32_t a, uint32_t x, uint32_t y,
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-__device__ void run_softmax(const Ctx& c, const TreeLaunch& p, PairParts parts, uint32_t tmem, char* ws_slots, uint8_t* smem) {
+__device__ void run_softmax(const Ctx& c, const TreeLaunch& p, Parts parts, uint32_t tmem, char* ws_slots, uint8_t* smem) {
   const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3;
   const int half = q4 >> 1, rg = q4 & 1;             // key / column half, group of 32 rows
   const int row = 32 * rg + lane;                    // of the CTA's 64
@@ -664,7 +664,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   const uint32_t rank = cluster_ctarank();
   const int worker = blockIdx.x >> 1;
   const Ctx c{smem_addr(smem), abort_flag, p.t.status, p.wait_limit_ns, rank};
-  launch_dependents();   // the join kernel, which waits for this one to end
+  ReqWords words{0, 0, 0};   // (on their way while the barriers are made)
+  if ((int)threadIdx.x < p.t.batch) words = load_words(p.t, threadIdx.x);
   if (threadIdx.x == 0) {
     for (int i = 0; i < NBAR; ++i) mbar_init(c.bar(i), 1);
     for (int i = 0; i < 2; ++i) mbar_init(c.bar(XB + i), 2);      // the two warps of 32 rows
@@ -686,15 +687,16 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     tmem_alloc_pair(smem_addr(tmem_slot), TMEM_COLS);
     tmem_relinquish_pair();
   }
-  find_piece<ROWS, KEYS, NTHREADS>(p.t, worker, p.workers, blockIdx.x == 0, &start, &count, &join);
+  __syncwarp();
+  tc_fence_before();
+  cluster_arrive();   // both CTAs' barriers exist, TMEM is there: waited for below
+  find_piece<NTHREADS>(p.t, words, worker, p.workers, blockIdx.x == 0, &start, &count, &join);
   char* ws = static_cast<char*>(p.t.workspace);
   if (threadIdx.x == 0 && rank == 0) reinterpret_cast<JoinRec*>(ws)[worker] = join;
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync();   // both CTAs' barriers exist before any remote arrival
+  cluster_wait();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  const PairParts parts(p.t, start, count);
+  const Parts parts(p.t, start, count);
   if (warp == 0) {
     run_producer_qk(c, p, parts, &tm_q, &tm_c, &tm_b, &tm_3, begun);
   } else if (warp == 2) {
@@ -757,30 +759,23 @@ int max_workers() {
 }  // namespace
 
 int64_t tree_workspace_bytes() {
-  const size_t n = max_workers(), few = tree_few_workers();
-  if (n == 0 || few == 0) return 0;
-  const size_t a = n * 2 * SLOT_BYTES, b = few * 2 * slot_bytes(64);
-  return (int64_t)(WS_SLOTS + (a > b ? a : b));
+  const int n = max_workers();
+  return n > 0 ? (int64_t)(WS_SLOTS + (size_t)n * 2 * SLOT_BYTES) : 0;
 }
 
 cudaError_t launch_tree_attention(const TreeParams& t, cudaStream_t stream) {
   TreeLaunch p;
   p.t = t;
-  // Units of about as many pairs as a request has, by the average (the lengths themselves are on
-  // the device; any unit size is right for any request).
-  const int64_t pairs = t.total_rows * t.num_heads;
-  const int few = pairs <= 16 * (int64_t)t.batch ? 16 : pairs <= 32 * (int64_t)t.batch ? 32
-                  : pairs <= 64 * (int64_t)t.batch ? 64 : 0;
-  p.workers = few ? tree_few_workers() : max_workers();
+  p.workers = max_workers();
   if (p.workers <= 0) return cudaErrorInvalidConfiguration;
   const bool any = t.max_blocks > 0;   // some cache row may be read
   const int bs = t.block_size;
   const uint64_t slots = any ? (uint64_t)t.num_blocks * (uint64_t)bs : 1;
   CUtensorMap tq, tc, tb, t2, t3;
   {
-    const uint64_t dims[2] = {576, (uint64_t)t.total_rows * (uint64_t)t.num_heads}, strides[1] = {576 * 2};
-    const uint32_t box[2] = {64, few ? (uint32_t)few : 64u};
-    if (make_tensor_map_bf16(&tq, t.q, 2, dims, strides, box) != MLA_OK) return cudaErrorInvalidValue;
+    const uint64_t dims[3] = {64, (uint64_t)t.total_rows * (uint64_t)t.num_heads, NP}, strides[2] = {576 * 2, 64 * 2};
+    const uint32_t box[3] = {64, 64, NP};   // 64 rows, panel by panel
+    if (make_tensor_map_bf16(&tq, t.q, 3, dims, strides, box) != MLA_OK) return cudaErrorInvalidValue;
   }
   const void* rows = any ? static_cast<const void*>(t.cache) : t.q;   // a map needs a valid base
   {
@@ -806,7 +801,7 @@ cudaError_t launch_tree_attention(const TreeParams& t, cudaStream_t stream) {
     const uint64_t dims[3] = {64, slots, NP}, strides[2] = {576 * 2, 64 * 2};
     const uint32_t box2[3] = {64, 64, 2}, box3[3] = {64, 64, 3};
     if (make_tensor_map_bf16(&t2, rows, 3, dims, strides, box2) != MLA_OK) return cudaErrorInvalidValue;
-    if (!few && make_tensor_map_bf16(&t3, rows, 3, dims, strides, box3) != MLA_OK) return cudaErrorInvalidValue;
+    if (make_tensor_map_bf16(&t3, rows, 3, dims, strides, box3) != MLA_OK) return cudaErrorInvalidValue;
   }
   p.oob_row = (int32_t)slots;
   p.o_align32 = (reinterpret_cast<uintptr_t>(t.o) & 31u) == 0;
@@ -818,16 +813,10 @@ cudaError_t launch_tree_attention(const TreeParams& t, cudaStream_t stream) {
   const uint64_t forced = forced_timeout_ns();
   p.force_timeout = forced != 0;
   p.wait_limit_ns = forced ? forced : kWaitLimitNs;
-  cudaError_t e;
-  if (few) {
-    e = launch_tree_few(p, few, tq, tc, tb, t2, stream);
-  } else {
-    cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = pair_config(attr, p.workers, stream);
-    e = cudaLaunchKernelEx(&cfg, tree_attn_kernel, tq, tc, tb, t2, t3, p);
-  }
-  if (e != cudaSuccess) return e;
-  return launch_tree_join(p, few ? few : ROWS, stream);
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = pair_config(attr, p.workers, stream);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_attn_kernel, tq, tc, tb, t2, t3, p);
+  return e != cudaSuccess ? e : launch_tree_join(p, stream);
 }
 
 }  // namespace mla

@@ -11,9 +11,7 @@ namespace {
 // lane.  Bound by latency: record, (m, l), O, result, each waits for the one before.
 constexpr int JOIN_WARPS = 8;
 
-template <int ROWS>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) tree_join_kernel(const __grid_constant__ TreeLaunch p) {
-  wait_for_previous();   // launched early: everything read here comes from the kernel before
   const char* ws = static_cast<const char*>(p.t.workspace);
   const int b = blockIdx.x + 1;   // the boundary before worker b
   const JoinRec j = reinterpret_cast<const JoinRec*>(ws)[b];
@@ -22,11 +20,11 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) tree_join_kernel(const __grid
   if (row >= j.npairs || j.parts == 0) return;
   const int64_t pair = j.pair0 + row;
   const int n = j.parts;
-  const char* slots = ws + WS_SLOTS + (size_t)2 * (b - 1) * slot_bytes(ROWS);
-  auto slot = [&](int k) { return slots + (size_t)(2 * k + (k == 0 ? j.slot0 : 0)) * slot_bytes(ROWS); };
+  const char* slots = ws + WS_SLOTS + (size_t)2 * (b - 1) * SLOT_BYTES;
+  auto slot = [&](int k) { return slots + (size_t)(2 * k + (k == 0 ? j.slot0 : 0)) * SLOT_BYTES; };
   const float NEG_INF = -__int_as_float(0x7f800000);
   float m = NEG_INF;
-  for (int k = lane; k < n; k += 32) m = fmaxf(m, reinterpret_cast<const float2*>(slot(k) + slot_ml(ROWS))[row].x);
+  for (int k = lane; k < n; k += 32) m = fmaxf(m, reinterpret_cast<const float2*>(slot(k) + SLOT_ML)[row].x);
 #pragma unroll
   for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
   const float mref = m == NEG_INF ? 0.f : m;
@@ -37,7 +35,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) tree_join_kernel(const __grid
   for (int k0 = 0; k0 < n; k0 += 32) {
     float w = 0.f, wl = 0.f;
     if (k0 + lane < n) {
-      const float2 ml = reinterpret_cast<const float2*>(slot(k0 + lane) + slot_ml(ROWS))[row];
+      const float2 ml = reinterpret_cast<const float2*>(slot(k0 + lane) + SLOT_ML)[row];
       w = ex2_approx(ml.x - mref);
       wl = w * ml.y;
     }
@@ -71,25 +69,12 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) tree_join_kernel(const __grid
 
 }  // namespace
 
-cudaError_t launch_tree_join(const TreeLaunch& p, int rows, cudaStream_t stream) {
+cudaError_t launch_tree_join(const TreeLaunch& p, cudaStream_t stream) {
   if (p.workers < 2) return cudaSuccess;
-  const dim3 grid(p.workers - 1, (rows + JOIN_WARPS - 1) / JOIN_WARPS), block(JOIN_WARPS * 32);
-  cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.stream = stream;
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 0;
-  switch (rows) {
-    case 128: return cudaLaunchKernelEx(&cfg, tree_join_kernel<128>, p);
-    case 64: return cudaLaunchKernelEx(&cfg, tree_join_kernel<64>, p);
-    case 32: return cudaLaunchKernelEx(&cfg, tree_join_kernel<32>, p);
-    case 16: return cudaLaunchKernelEx(&cfg, tree_join_kernel<16>, p);
-    default: return cudaErrorInvalidValue;
-  }
+  // (Launched early, to wait for the other kernel's end on the GPU, it made calls up to 4 us longer:
+  // its CTAs take room and issue slots from that kernel's.)
+  tree_join_kernel<<<dim3(p.workers - 1, TREE_ROWS / JOIN_WARPS), JOIN_WARPS * 32, 0, stream>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace mla
