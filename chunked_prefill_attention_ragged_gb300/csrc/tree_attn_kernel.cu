@@ -30,7 +30,8 @@
 //   warp 0     Q and K producer: Q once per unit; K in three groups of three 64-column panels
 //   warp 1     even CTA: issues every product
 //   warp 2     V producer: two 256-column chunks (128 of the columns here), by halves of the keys
-//   warp 3     TMEM allocation; brings the next tile's rows into L2
+//   warp 3     TMEM allocation; brings the next tile's rows into L2, or, where K comes in many small
+//              copies, loads its last group
 //   warps 4-7  softmax: two threads per pair (the two halves of the keys and of O's columns)
 // Order of products: S(t + 1) before P V(t), so that the tensor cores work on the next tile while
 // the softmax does this one.  Key rows come by whole boxes of 64 where the block size is a multiple
@@ -70,8 +71,8 @@ enum Bar {
   SF = VE + 4,         // [buffer] S done
   PR = SF + 2,         // P written (and the S buffer read) by every softmax warp of both CTAs
   OD,                  // P V done
-  LB,                  // a partial piece of V landed (in this CTA)
-  ZB,                  // [chunk] the odd CTA's partial piece is ready
+  LB,                  // [chunk] the half of V to mend landed (in this CTA)
+  ZB = LB + 2,         // [chunk] the odd CTA has mended its own
   XB = ZB + 2,         // [row half] maxima exchanged between the two warps of 32 rows
   FIN = XB + 2,        // every product drained
   NEVER,               // nothing arrives here: the time-out test mode waits on it
@@ -123,6 +124,19 @@ __device__ __forceinline__ void copy_panels(const TreeLaunch& p, const KeyRows& 
   }
 }
 
+// 64 keys x panels panel0 and panel0 + 1 as a product's values: piece by piece, each with both its
+// panels (r rows of 128 bytes, then the other panel's r rows).
+__device__ __forceinline__ void copy_values(const TreeLaunch& p, const KeyRows& k, uint32_t dst, uint32_t bar,
+                                            const CUtensorMap* tc, const CUtensorMap* t2, int panel0, int lane) {
+  if (p.piece_rows > 0) {
+    if (lane * p.piece_rows < 64) tma_load_3d_pair(dst + lane * p.piece_rows * 256, t2, bar, 0, k.r[0], panel0);
+  } else if (lane < 16) {
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i)
+      tma_gather4_pair(dst + i * QP + lane * 4 * 128, tc, bar, (panel0 + i) * 64, k.r[0], k.r[1], k.r[2], k.r[3]);
+  }
+}
+
 // ------------------------------------------------------------------ producers
 // The copies of both CTAs complete on the even CTA's barriers, where the products wait for them;
 // its producers announce the bytes of both.  The buffers hold one tile: what a product has read
@@ -143,6 +157,7 @@ __device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, Parts parts, 
                                 volatile int* begun) {
   const int lane = threadIdx.x & 31;
   const uint32_t qf = mapa_shared(c.bar(QF), 0), kf = mapa_shared(c.bar(KF), 0);
+  const int groups = p.grouped ? KGROUPS : KGROUPS - 1;   // (see run_producer_k_last)
   int tiles = 0, units = 0, issued = 0;   // tiles begun, parts, K groups
   bool ok = true;
   Part u;
@@ -182,7 +197,7 @@ __device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, Parts parts, 
         const KeyRows k = find_rows(p, u, blocks, key0, lane);
         if (t + 1 < u.hi) blocks = find_blocks(p, u, key0 + KEYS, lane);
 #pragma unroll 1
-        for (int g = 0; g < KGROUPS; ++g) {
+        for (int g = 0; g < groups; ++g) {
           if (lane == 0) {
             if (tiles > 0) ok = c.wait(KE + g, (tiles - 1) & 1);
             if (ok) expect_both(c, KF + g, 3 * QP);
@@ -200,8 +215,8 @@ __device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, Parts parts, 
   if (lane == 0) {
     if (c.rank == 0) {
       if (units) c.drain(QF, (units - 1) & 1);
-      for (int g = 0; g < KGROUPS; ++g) {
-        const int n = (issued + KGROUPS - 1 - g) / KGROUPS;
+      for (int g = 0; g < groups; ++g) {
+        const int n = (issued + groups - 1 - g) / groups;
         if (n) c.drain(KF + g, (n - 1) & 1);
       }
     } else if (!ok) {
@@ -210,12 +225,43 @@ __device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, Parts parts, 
   }
 }
 
+// Warp 3 where K comes in many small copies: its last group.
+__device__ void run_producer_k_last(const Ctx& c, const TreeLaunch& p, Parts parts, const CUtensorMap* tc,
+                                    const CUtensorMap* tb) {
+  const int lane = threadIdx.x & 31, g = KGROUPS - 1;
+  const uint32_t kf = mapa_shared(c.bar(KF), 0);
+  int tiles = 0, issued = 0;
+  bool ok = true;
+  Part u;
+  while (ok && parts.next(&u)) {
+    int64_t key0 = (int64_t)u.lo * KEYS + 64 * c.rank;
+    KeyBlocks blocks = find_blocks(p, u, key0, lane);
+#pragma unroll 1
+    for (int t = u.lo; t < u.hi && ok; ++t, ++tiles, key0 += KEYS) {
+      const KeyRows k = find_rows(p, u, blocks, key0, lane);
+      if (t + 1 < u.hi) blocks = find_blocks(p, u, key0 + KEYS, lane);
+      if (lane == 0) {
+        if (tiles > 0) ok = c.wait(KE + g, (tiles - 1) & 1);
+        if (ok) expect_both(c, KF + g, 3 * QP);
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      copy_panels(p, k, c.sbase + OFF_K + 3 * g * QP, kf + 8 * g, tc, tb, 3 * g, 3, lane);
+      ++issued;
+    }
+  }
+  if (lane == 0) {
+    if (c.rank == 0 && issued) c.drain(KF + g, (issued - 1) & 1);
+    if (!ok) settle();
+  }
+}
+
 __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, Parts parts, const CUtensorMap* tc,
-                               const CUtensorMap* tb, const CUtensorMap* t2, uint8_t* smem) {
+                               const CUtensorMap* t2, uint8_t* smem) {
   const int lane = threadIdx.x & 31;
   const uint32_t vf = mapa_shared(c.bar(VF), 0);
   int tiles = 0, issued = 0;
-  int cuts = 0, zeros = 0;   // partial pieces, and tiles that have them
+  int mends = 0;   // tiles that have a half to mend
   bool ok = true;
   Part u;
   while (ok && parts.next(&u)) {
@@ -250,7 +296,7 @@ __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, Parts parts, c
           }
         }
       } else {
-        KeyRows k0{}, k1{};
+        KeyRows k0{{row0, 0, 0, 0}}, k1{{row1, 0, 0, 0}};
         if (!p.grouped) {
           k0 = find_rows(p, u, b0, key0, lane);
           k1 = find_rows(p, u, b1, key0 + 64, lane);
@@ -259,45 +305,46 @@ __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, Parts parts, c
             b1 = find_blocks(p, u, key0 + KEYS + 64, lane);
           }
         }
-        // Those rows are made zero (their P is 0, but 0 times what is there need not be).  Each CTA
-        // sees to its own, then the even one says that the half is there.
-        const int cut = valid < 64 ? 0 : 1, first = (int)(valid & 63);
+        const int cut = !ends ? 2 : valid < 64 ? 0 : 1;   // the half to mend
 #pragma unroll 1
-        for (int i = 0; i < 4 && ok; ++i) {
-          const uint32_t dst = c.sbase + OFF_V + i * 2 * QP;
-          const int panel = 4 * (i >> 1) + 2 * (int)c.rank;
-          const bool mend = ends && (i & 1) == cut;
+        for (int i = 0; i < 4; ++i) {
           if (lane == 0) {
             if (tiles > 0) ok = c.wait(VE + i, (tiles - 1) & 1);
             if (ok) {
-              if (mend) mbar_arrive_expect_tx(c.bar(LB), 2 * QP);
+              if ((i & 1) == cut) mbar_arrive_expect_tx(c.bar(LB + (i >> 1)), 2 * QP);
               else expect_both(c, VF + i, 2 * QP);
             }
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) break;
-          const uint32_t bar = mend ? mapa_shared(c.bar(LB), c.rank) : vf + 8 * i;
-          if (!p.grouped) copy_panels(p, i & 1 ? k1 : k0, dst, bar, tc, tb, panel, 2, lane);
-          else if (lane == 0) tma_load_3d_pair(dst, t2, bar, 0, i & 1 ? row1 : row0, panel);
+          copy_values(p, i & 1 ? k1 : k0, c.sbase + OFF_V + i * 2 * QP,
+                      (i & 1) == cut ? mapa_shared(c.bar(LB + (i >> 1)), c.rank) : vf + 8 * i, tc, t2,
+                      4 * (i >> 1) + 2 * (int)c.rank, lane);
           ++issued;
-          if (!mend) continue;
-          if (lane == 0) ok = c.wait(LB, cuts & 1);
-          ++cuts;
+        }
+        // What came along behind the last key is made zero (its P is 0, but 0 times what is there need
+        // not be).  Each CTA sees to its own, then the even one says that the half is there.
+#pragma unroll 1
+        for (int j2 = 0; j2 < 2 && ends && ok; ++j2) {
+          if (lane == 0) ok = c.wait(LB + j2, mends & 1);
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) break;
-          uint8_t* at = smem + OFF_V + i * 2 * QP;
-          for (int k = lane; k < (64 - first) * 16; k += 32)
-            *reinterpret_cast<uint4*>(at + (k & 8 ? QP : 0) + (first + (k >> 4)) * 128 + (k & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
+          uint8_t* at = smem + OFF_V + (2 * j2 + cut) * 2 * QP;
+          const int low = p.piece_rows - 1;   // (a power of two less one)
+          for (int k = lane; k < (64 - (int)(valid & 63)) * 16; k += 32) {
+            const int row = (int)(valid & 63) + (k >> 4);
+            *reinterpret_cast<uint4*>(at + (2 * (row & ~low) + (k & 8 ? low + 1 : 0) + (row & low)) * 128 +
+                                      (k & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
           fence_async_shared();
           __syncwarp();
           if (lane == 0) {
-            if (c.rank != 0) mbar_arrive_remote(mapa_shared(c.bar(ZB + (i >> 1)), 0));
-            else if ((ok = c.wait(ZB + (i >> 1), zeros & 1))) mbar_arrive(c.bar(VF + i));
+            if (c.rank != 0) mbar_arrive_remote(mapa_shared(c.bar(ZB + j2), 0));
+            else if ((ok = c.wait(ZB + j2, mends & 1))) mbar_arrive(c.bar(VF + 2 * j2 + cut));
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
         }
-        if (ends) ++zeros;
+        if (ends) ++mends;
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
     }
@@ -313,35 +360,29 @@ __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, Parts parts, c
   }
 }
 
-// Warp 3: this CTA's keys of the tile after the one being loaded, into L2.  The one-tile buffers
-// leave a load less than a tile's time, which DRAM does not keep to: with the rows in L2 it does.
-// It follows the K producer's count of tiles, which only grows (on a barrier's phases a warp that
-// fell two tiles behind would wait for one that never comes), and gives up quietly.
-__device__ void run_prefetch(const Ctx& c, const TreeLaunch& p, Parts parts, const CUtensorMap* tb,
-                             const CUtensorMap* t3, const volatile int* begun) {
-  if (p.piece_rows == 0) return;
-  const int lane = threadIdx.x & 31, pieces = 64 / p.piece_rows;
+// Warp 3 where K comes in whole boxes: this CTA's keys of the tile after the one being loaded, into
+// L2.  The one-tile buffers leave a load less than a tile's time, which DRAM does not keep to: with
+// the rows in L2 it does.  It follows the K producer's count of tiles, which only grows (on a
+// barrier's phases a warp that fell two tiles behind would wait for one that never comes), and gives
+// up quietly.
+__device__ void run_prefetch(const Ctx& c, const TreeLaunch& p, Parts parts, const CUtensorMap* t3,
+                             const volatile int* begun) {
+  const int lane = threadIdx.x & 31;
   int tiles = 0;
   Part u;
   while (parts.next(&u)) {
     for (int t = u.lo; t < u.hi; ++t, ++tiles) {
-      const int64_t key0 = (int64_t)(t + 1) * KEYS + 64 * c.rank;
+      const int64_t key = (int64_t)(t + 1) * KEYS + 64 * c.rank;
       const uint64_t t0 = global_timer_ns();
       while (*begun < tiles) {   // tile t is not being loaded yet
         __nanosleep(200);
         if (*c.abort_flag || global_timer_ns() - t0 > p.wait_limit_ns) return;
       }
       __syncwarp();
-      if (t + 1 < u.hi && key0 + 64 <= u.q.kv && lane < pieces) {
-        const int64_t key = key0 + lane * p.piece_rows;
+      if (t + 1 < u.hi && key + 64 <= u.q.kv && lane == 0) {
         const int32_t row = block_row(p, table_block(p, u, key), key);
-        if (p.grouped) {
 #pragma unroll 1
-          for (int g = 0; g < KGROUPS; ++g) tma_prefetch_3d(t3, 0, row, 3 * g);
-        } else {
-#pragma unroll 1
-          for (int i = 0; i < NP; ++i) tma_prefetch_2d(tb, i * 64, row);
-        }
+        for (int g = 0; g < KGROUPS; ++g) tma_prefetch_3d(t3, 0, row, 3 * g);
       }
     }
   }
@@ -378,7 +419,13 @@ __device__ __forceinline__ void commit_both(uint32_t bar) {
 __device__ void run_mma(const Ctx& c, const TreeLaunch& p, Parts parts, uint32_t tmem) {
   const uint64_t q_desc = sdesc_sw128(c.sbase + OFF_Q, 16, 1024);
   const uint64_t k_desc = sdesc_sw128(c.sbase + OFF_K, 16, 1024);
-  const uint64_t v_desc = sdesc_sw128(c.sbase + OFF_V, QP, 1024);
+  // Values lie in pieces of r keys, each with both its panels: 16 keys of a product are part of one
+  // piece, a whole one or two.
+  const int r = p.piece_rows > 0 ? p.piece_rows : 64;
+  const uint64_t v_desc = sdesc_sw128(c.sbase + OFF_V, r * 128, r == 8 ? 2048 : 1024);
+  uint32_t v_step[4];
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) v_step[kk] = (uint32_t)((kk * 16 / r) * 2 * r + kk * 16 % r) * 128 >> 4;
   const uint64_t p_desc = sdesc_sw128(c.sbase + OFF_P, 16, 1024);
   bool ok = true;
   if (p.force_timeout) ok = c.wait_warp(NEVER, 0);
@@ -420,9 +467,9 @@ __device__ void run_mma(const Ctx& c, const TreeLaunch& p, Parts parts, uint32_t
     ++st;
     return true;
   };
-  auto pv_products = [&](bool first_tile, bool s_next) {
+  auto pv_products = [&](uint32_t add, bool s_next) {   // add: 0 for a part's first tile
     const int t = pv;
-    const uint32_t more = __shfl_sync(0xffffffffu, first_tile ? 0u : 1u, 0);
+    const uint32_t more = __shfl_sync(0xffffffffu, add, 0);
     uint32_t seen = seen_v;
     if (!c.wait_warp(PR, t & 1, seen_p)) return false;
     seen_p = seen_v = 0;
@@ -435,7 +482,7 @@ __device__ void run_mma(const Ctx& c, const TreeLaunch& p, Parts parts, uint32_t
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
         const uint64_t po = (uint64_t)(((i & 1) * QP + kk * 32) >> 4);
-        const uint64_t vo = (uint64_t)((i * 2 * QP + kk * 16 * 128) >> 4);
+        const uint64_t vo = (uint64_t)(i * 2 * QP >> 4) + v_step[kk];
         issue(tmem + TM_O(i >> 1), p_desc + po, v_desc + vo, IDESC_PV, kk > 0 ? 1u : (i & 1) ? 1u : more);
       }
       commit_both(c.bar(VE + i));
@@ -452,10 +499,10 @@ __device__ void run_mma(const Ctx& c, const TreeLaunch& p, Parts parts, uint32_t
     for (int t = 0; t < n && ok; ++t) {
       // S's buffer held P V(pv - 2)'s scores, read before that tile's P was ready.
       ok = s_products(t == n - 1);
-      if (ok && t > 0) ok = pv_products(t == 1, t < n - 1);
+      if (ok && t > 0) ok = pv_products(t > 1 ? 1u : 0u, t < n - 1);
     }
-    // (The next part's Q is only loaded now that S is done: P V does not wait for it.)
-    if (ok) ok = pv_products(n == 1, false);
+    // (The next part's Q and keys come later than this one's last P: its S first was no faster.)
+    if (ok) ok = pv_products(n > 1 ? 1u : 0u, false);
   }
   commit_both(c.bar(FIN));
   c.drain(FIN, 0);
@@ -677,11 +724,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_c);
-    if (p.piece_rows > 0) tma_prefetch_desc(&tm_b);
-    if (p.grouped) {
-      tma_prefetch_desc(&tm_2);
-      tma_prefetch_desc(&tm_3);
-    }
+    if (p.piece_rows > 0) tma_prefetch_desc(&tm_2);
+    tma_prefetch_desc(p.grouped ? &tm_3 : &tm_b);
   }
   if (warp == 3) {   // one warp of each CTA of the pair, together
     tmem_alloc_pair(smem_addr(tmem_slot), TMEM_COLS);
@@ -700,11 +744,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   if (warp == 0) {
     run_producer_qk(c, p, parts, &tm_q, &tm_c, &tm_b, &tm_3, begun);
   } else if (warp == 2) {
-    run_producer_v(c, p, parts, &tm_c, &tm_b, &tm_2, smem);
+    run_producer_v(c, p, parts, &tm_c, &tm_2, smem);
   } else if (warp == 1) {
     if (rank == 0) run_mma(c, p, parts, tmem);
   } else if (warp == 3) {
-    run_prefetch(c, p, parts, &tm_b, &tm_3, begun);
+    if (p.grouped) run_prefetch(c, p, parts, &tm_3, begun);
+    else run_producer_k_last(c, p, parts, &tm_c, &tm_b);
   } else {
     run_softmax(c, p, parts, tmem, ws + WS_SLOTS + (size_t)worker * 2 * SLOT_BYTES, smem);
   }
@@ -797,11 +842,12 @@ cudaError_t launch_tree_attention(const TreeParams& t, cudaStream_t stream) {
     const uint32_t box[2] = {64, (uint32_t)p.piece_rows};
     if (make_tensor_map_bf16(&tb, rows, 2, dims, strides, box) != MLA_OK) return cudaErrorInvalidValue;
   }
-  if (p.grouped) {
+  if (p.piece_rows > 0) {
     const uint64_t dims[3] = {64, slots, NP}, strides[2] = {576 * 2, 64 * 2};
-    const uint32_t box2[3] = {64, 64, 2}, box3[3] = {64, 64, 3};
-    if (make_tensor_map_bf16(&t2, rows, 3, dims, strides, box2) != MLA_OK) return cudaErrorInvalidValue;
-    if (make_tensor_map_bf16(&t3, rows, 3, dims, strides, box3) != MLA_OK) return cudaErrorInvalidValue;
+    const uint32_t box2[3] = {64, (uint32_t)p.piece_rows, 2}, box3[3] = {64, 64, 3};
+    if (make_tensor_map_bf16(&t2, rows, 3, dims, strides, box2) != MLA_OK ||
+        (p.grouped && make_tensor_map_bf16(&t3, rows, 3, dims, strides, box3) != MLA_OK))
+      return cudaErrorInvalidValue;
   }
   p.oob_row = (int32_t)slots;
   p.o_align32 = (reinterpret_cast<uintptr_t>(t.o) & 31u) == 0;
