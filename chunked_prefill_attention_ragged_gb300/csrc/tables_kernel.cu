@@ -7,13 +7,17 @@
 // (the slot rule of vLLM "vllm/models/deepseek_v4/sparse_mla.py",
 // _build_c128a_topk_metadata_kernel, decode branch; slot -1 marks a token without a place).
 //
-// Everything is decided by exclusive prefix sums over the requests of (new tokens, blocks to
-// give back, blocks to take), so the result does not depend on the order in which threads run.
-// The sums are made by every CTA for itself (at most 8192 requests, a few per thread); then
-// give back | take | slot map are three phases over flat lists of blocks or tokens, whose
-// request is found by binary search in shared memory.  The phases are separated by barriers of
-// one cluster, so that one launch does it all: what bounds the call is its latency (about
-// 20 bytes per request and 8 per token).
+// Everything is decided by exclusive prefix sums over the requests of (new tokens, blocks given
+// back, blocks to take), so that the result does not depend on the order in which threads run.  With
+// R blocks given back and the stack's height c before, the k-th block taken is the one at stack index
+// c + R - 1 - k, where block k of those given back goes: so for k < R it is that block itself, which
+// moves from one table row to the other without the stack between, and every block is one thread's.
+//
+// Two forms.  Up to 4096 tokens to map, one CTA does it all: sums, blocks, slots, with its own
+// barriers between (what bounds it is latency: about 20 bytes per request and 8 per token).  More,
+// and one kernel moves the blocks and a second one writes the lengths and the slots, each CTA of
+// both making the sums for itself (at most 8192 requests, a few per thread): the map of 530 thousand
+// tokens took 77 us from eight CTAs and 9 us from a grid.
 #include <climits>
 
 #include "internal.h"
@@ -22,8 +26,9 @@
 namespace mla {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kClusterCtas = 8;
+constexpr int kMaxThreads = 1024;
+constexpr int64_t kOneCtaTokens = 4096;
+constexpr int kSlotThreads = 512, kSlotsPerThread = 4;
 
 struct Sums {
   int64_t tok;
@@ -51,50 +56,47 @@ __device__ __forceinline__ int owner(const int* start, int n, int x) {
   return lo;
 }
 
-// One cluster (kCluster) or one CTA.
-template <bool kCluster>
-__global__ void __launch_bounds__(kThreads) tables_kernel(const TablesParams p) {
-  extern __shared__ int smem[];
-  const int b = p.batch, stride = b + 1;
-  int* s_tok = smem;                  // exclusive sums, [b + 1]
-  int* s_rel = s_tok + stride;
-  int* s_need = s_rel + stride;
-  int* s_held = s_need + stride;      // blocks held before, and after
-  int* s_after = s_held + stride;
-  __shared__ Sums warp_sum[kThreads / 32];
-  __shared__ int s_taken;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = kCluster ? (int)cluster_ctarank() : 0;
-  const int nthr = kCluster ? kThreads * kClusterCtas : kThreads;
-  const int gtid = rank * kThreads + tid;
-  auto sync_all = [] {
-    if constexpr (kCluster) cluster_sync(); else __syncthreads();
-  };
-  const int base_raw = p.free_count[0];
-  const int base = min(max(base_raw, 0), p.free_capacity);
-  if (gtid == 0 && base != base_raw) flag(p.status, MLA_DEVSTAT_BAD_INDEX);
+// The sums in shared memory (exclusive, [batch + 1] each), and what a request holds before and after.
+struct Shared {
+  int *tok, *rel, *need, *held, *after;
+  int taken;      // blocks taken: the needs of the requests that are served, a prefix of those that need any
+  int released;
+  int base;       // height of the stack before
+  int64_t top;    // height with everything given back
+};
 
-  // Exclusive sums: a thread's consecutive requests, then its warp, then the CTA.
-  const int per = (b + kThreads - 1) / kThreads;
+__device__ void make_sums(const TablesParams& p, int* smem, bool report, Shared* out) {
+  __shared__ Sums warp_sum[kMaxThreads / 32];
+  __shared__ int s_taken;
+  const int b = p.batch, stride = b + 1, threads = blockDim.x;
+  Shared s;
+  s.tok = smem;
+  s.rel = s.tok + stride;
+  s.need = s.rel + stride;
+  s.held = s.need + stride;
+  s.after = s.held + stride;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int count = p.free_count[0];
+  const int per = (b + threads - 1) / threads;
   const int r0 = min(tid * per, b), r1 = min(r0 + per, b);
   Sums mine{0, 0, 0};
   bool bad = false;
   for (int r = r0; r < r1; ++r) {
-    int s = p.seq_lens[r], m = p.new_lens[r], h = p.num_held[r];
-    bad |= s < 0 || m < 0 || h < 0 || h > p.max_blocks;
-    s = max(s, 0);
+    int l = p.seq_lens[r], m = p.new_lens[r], h = p.num_held[r];
+    bad |= l < 0 || m < 0 || h < 0 || h > p.max_blocks;
+    l = max(l, 0);
     m = max(m, 0);
     h = min(max(h, 0), p.max_blocks);
-    const int64_t target = ((int64_t)s + m + p.block_size - 1) / p.block_size;
+    const int64_t target = ((int64_t)l + m + p.block_size - 1) / p.block_size;
     const bool fits = target <= p.max_blocks;
     bad |= !fits;
     const int want = fits ? (int)target : h;   // a request too long for its row changes nothing
-    s_tok[r] = m;
-    s_held[r] = h;
-    s_after[r] = want;
+    s.tok[r] = m;
+    s.held[r] = h;
+    s.after[r] = want;
     mine = mine + Sums{m, max(h - want, 0), max(want - h, 0)};
   }
-  if (bad) flag(p.status, MLA_DEVSTAT_BAD_INDEX);
+  if (report && bad) flag(p.status, MLA_DEVSTAT_BAD_INDEX);
   Sums incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -105,119 +107,223 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesParams p) 
   if (tid == 0) s_taken = 0;
   __syncthreads();
   Sums before{0, 0, 0}, total{0, 0, 0};
-  for (int w = 0; w < kThreads / 32; ++w) {
+  for (int w = 0; w < threads / 32; ++w) {
     if (w < warp) before = before + warp_sum[w];
     total = total + warp_sum[w];
   }
   Sums run{before.tok + incl.tok - mine.tok, before.rel + incl.rel - mine.rel, before.need + incl.need - mine.need};
-  const int released = total.rel;
-  const int64_t top = (int64_t)base + released;   // stack height once everything is given back
+  s.released = total.rel;
+  s.base = min(max(count, 0), p.free_capacity);
+  s.top = (int64_t)s.base + s.released;
   int taken = 0;
   bool short_of = false;
   for (int r = r0; r < r1; ++r) {
-    const int m = s_tok[r], h = s_held[r], want = s_after[r];
+    const int m = s.tok[r], h = s.held[r], want = s.after[r];
     const int rel = max(h - want, 0), need = max(want - h, 0);
-    s_tok[r] = (int)min(run.tok, (int64_t)INT_MAX);
-    s_rel[r] = run.rel;
-    s_need[r] = run.need;
+    s.tok[r] = (int)min(run.tok, (int64_t)INT_MAX);
+    s.rel[r] = run.rel;
+    s.need[r] = run.need;
     run = run + Sums{m, rel, need};
     // First come, first served: a request is served when all up to it can be.
     if (need > 0) {
-      if (run.need <= top) taken = run.need;
-      else { s_after[r] = h; short_of = true; }
+      if (run.need <= s.top) taken = run.need;
+      else { s.after[r] = h; short_of = true; }
     }
   }
   if (tid == 0) {
-    s_tok[b] = (int)min(total.tok, (int64_t)INT_MAX);
-    s_rel[b] = total.rel;
-    s_need[b] = total.need;
-    if (total.tok > INT_MAX || (p.slot_mapping && total.tok > p.num_tokens)) flag(p.status, MLA_DEVSTAT_BAD_INDEX);
+    s.tok[b] = (int)min(total.tok, (int64_t)INT_MAX);
+    s.rel[b] = total.rel;
+    s.need[b] = total.need;
+    if (report && (count != s.base || total.tok > INT_MAX || (p.slot_mapping && total.tok > p.num_tokens)))
+      flag(p.status, MLA_DEVSTAT_BAD_INDEX);
   }
-  if (short_of) flag(p.status, MLA_DEVSTAT_NO_BLOCKS);
+  if (report && short_of) flag(p.status, MLA_DEVSTAT_NO_BLOCKS);
   if (taken) atomicMax(&s_taken, taken);
-  sync_all();   // every CTA has read the old state; the sums are in place
-  taken = s_taken;
+  __syncthreads();
+  s.taken = s_taken;
+  *out = s;
+}
 
-  // Give back: block k of the list goes where the k-th take from the top will look, so that
-  // what a step reserved and gave back leaves the stack as it was.
-  for (int k = gtid; k < released; k += nthr) {
-    const int r = owner(s_rel, b, k);
-    int32_t* entry = p.block_table + (int64_t)r * p.max_blocks + s_after[r] + (k - s_rel[r]);
-    const int64_t at = top - 1 - k;
-    const int blk = *entry;
-    *entry = -1;
-    if (at < p.free_capacity) p.free_blocks[at] = blk;
-    else flag(p.status, MLA_DEVSTAT_BAD_INDEX);
+// Block k of those given back or taken, for k = first, first + step, ...: out of its row, into the
+// row that takes it or onto the stack; or off the stack into the row.
+__device__ __forceinline__ void move_blocks(const TablesParams& p, const Shared& s, int first, int step) {
+  constexpr int kAtOnce = 4;   // loads under way together
+  const int n = max(s.released, s.taken);
+  for (int k0 = first; k0 < n; k0 += kAtOnce * step) {
+    int32_t* entry[kAtOnce];
+    int blk[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int k = k0 + i * step;
+      const int64_t at = s.top - 1 - k;
+      entry[i] = nullptr;
+      blk[i] = -1;
+      if (k < s.released) {
+        const int r = owner(s.rel, p.batch, k);
+        entry[i] = p.block_table + (int64_t)r * p.max_blocks + s.after[r] + (k - s.rel[r]);
+        blk[i] = *entry[i];
+      } else if (k < n && at < p.free_capacity) {
+        blk[i] = p.free_blocks[at];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int k = k0 + i * step;
+      const int64_t at = s.top - 1 - k;
+      if (k >= n) break;
+      if (entry[i]) *entry[i] = -1;
+      if (k < s.taken) {
+        if (blk[i] < 0) {
+          flag(p.status, MLA_DEVSTAT_BAD_INDEX);
+          blk[i] = -1;
+        }
+        const int r = owner(s.need, p.batch, k);
+        p.block_table[(int64_t)r * p.max_blocks + s.held[r] + (k - s.need[r])] = blk[i];
+      } else if (at < p.free_capacity) {
+        p.free_blocks[at] = blk[i];
+      } else {
+        flag(p.status, MLA_DEVSTAT_BAD_INDEX);   // the stack is full
+      }
+    }
   }
-  for (int r = gtid; r <= b; r += nthr) {
-    if (p.qo_indptr) p.qo_indptr[r] = s_tok[r];
-    if (r < b) {
-      p.num_held[r] = s_after[r];
+}
+
+__device__ __forceinline__ void write_lengths(const TablesParams& p, const Shared& s, int first, int step) {
+  for (int r = first; r <= p.batch; r += step) {
+    if (p.qo_indptr) p.qo_indptr[r] = s.tok[r];
+    if (r < p.batch) {
+      p.num_held[r] = s.after[r];
       if (p.kv_lens) {
         const int64_t len = (int64_t)max(p.seq_lens[r], 0) + max(p.new_lens[r], 0);
         p.kv_lens[r] = (int)min(len, (int64_t)INT_MAX);
       }
     }
   }
-  if (gtid == 0) p.free_count[0] = (int)min(top - taken, (int64_t)p.free_capacity);
-  sync_all();
+  if (first == 0) p.free_count[0] = (int)min(s.top - s.taken, (int64_t)p.free_capacity);
+}
 
-  for (int k = gtid; k < taken; k += nthr) {
-    const int r = owner(s_need, b, k);
-    const int64_t at = top - 1 - k;
-    int blk = at < p.free_capacity ? p.free_blocks[at] : -1;
-    if (blk < 0) {
-      flag(p.status, MLA_DEVSTAT_BAD_INDEX);
-      blk = -1;
-    }
-    p.block_table[(int64_t)r * p.max_blocks + s_held[r] + (k - s_need[r])] = blk;
-  }
-  if (!p.slot_mapping) return;
-  sync_all();
-
-  const int live = s_tok[b];
-  for (int64_t t = gtid; t < p.num_tokens; t += nthr) {
+// Slots of tokens t .. t + n - 1.
+__device__ __forceinline__ void write_slots(const TablesParams& p, const int* tok, int64_t t, int n) {
+  const int live = tok[p.batch];
+  int r = t < live ? owner(tok, p.batch, (int)t) : p.batch;
+  int64_t seen = -1, base = -1;   // block index last looked up, its first slot
+  for (int i = 0; i < n; ++i, ++t) {
+    if (t >= p.num_tokens) return;
     int64_t slot = -1;
     if (t < live) {
-      const int r = owner(s_tok, b, (int)t);
-      const int64_t pos = (int64_t)max(p.seq_lens[r], 0) + (t - s_tok[r]);
+      while (t >= tok[r + 1]) {   // (ends: t < tok[batch])
+        ++r;
+        seen = -1;
+      }
+      const int64_t pos = (int64_t)max(p.seq_lens[r], 0) + (t - tok[r]);
       const int64_t bi = pos / p.block_size;
-      const int blk = bi < p.max_blocks ? p.block_table[(int64_t)r * p.max_blocks + bi] : -1;
-      if (blk >= 0) slot = (int64_t)blk * p.block_size + (pos - bi * p.block_size);
+      if (bi != seen) {
+        seen = bi;
+        const int blk = bi < p.max_blocks ? p.block_table[(int64_t)r * p.max_blocks + bi] : -1;
+        base = blk >= 0 ? (int64_t)blk * p.block_size : -1;
+      }
+      if (base >= 0) slot = base + (pos - bi * p.block_size);
     }
     p.slot_mapping[t] = slot;
   }
 }
 
+__global__ void __launch_bounds__(kMaxThreads) tables_kernel(const TablesParams p) {
+  extern __shared__ int smem[];
+  Shared s;
+  make_sums(p, smem, true, &s);
+  move_blocks(p, s, threadIdx.x, blockDim.x);
+  write_lengths(p, s, threadIdx.x, blockDim.x);
+  if (!p.slot_mapping) return;
+  __syncthreads();
+  for (int64_t t = threadIdx.x; t < p.num_tokens; t += blockDim.x) write_slots(p, s.tok, t, 1);
+}
+
+// The old lengths stay until the second kernel: every CTA reads them.
+__global__ void __launch_bounds__(kMaxThreads) tables_blocks_kernel(const TablesParams p) {
+  extern __shared__ int smem[];
+  Shared s;
+  make_sums(p, smem, blockIdx.x == 0, &s);
+  move_blocks(p, s, blockIdx.x * blockDim.x + threadIdx.x, gridDim.x * blockDim.x);
+}
+
+// CTA 0 alone reads and writes what a request holds; the others only sum the new tokens.
+__global__ void __launch_bounds__(kSlotThreads) tables_slots_kernel(const TablesParams p) {
+  extern __shared__ int smem[];
+  if (blockIdx.x == 0) {
+    Shared s;
+    make_sums(p, smem, false, &s);
+    write_lengths(p, s, threadIdx.x, kSlotThreads);
+  } else {
+    __shared__ int64_t warp_sum[kSlotThreads / 32];
+    const int b = p.batch, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (b + kSlotThreads - 1) / kSlotThreads;
+    const int r0 = min(tid * per, b), r1 = min(r0 + per, b);
+    int64_t mine = 0;
+    for (int r = r0; r < r1; ++r) {
+      const int m = max(p.new_lens[r], 0);
+      smem[r] = m;
+      mine += m;
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int64_t run = incl - mine, total = 0;
+    for (int w = 0; w < kSlotThreads / 32; ++w) {
+      if (w < warp) run += warp_sum[w];
+      total += warp_sum[w];
+    }
+    for (int r = r0; r < r1; ++r) {
+      const int m = smem[r];
+      smem[r] = (int)min(run, (int64_t)INT_MAX);
+      run += m;
+    }
+    if (tid == 0) smem[b] = (int)min(total, (int64_t)INT_MAX);
+    __syncthreads();
+  }
+  // (Neighbouring threads have neighbouring tokens, a thread every kSlotThreads-th.)
+  const int64_t t0 = (int64_t)blockIdx.x * kSlotThreads * kSlotsPerThread + threadIdx.x;
+#pragma unroll
+  for (int i = 0; i < kSlotsPerThread; ++i) write_slots(p, smem, t0 + i * kSlotThreads, 1);
+}
+
+int sums_bytes(int batch) { return 5 * (batch + 1) * (int)sizeof(int); }
+
 }  // namespace
 
 cudaError_t launch_tables(const TablesParams& p, cudaStream_t stream) {
-  const int smem = 5 * (p.batch + 1) * (int)sizeof(int);
+  const int smem = sums_bytes(p.batch);
   static PerDeviceOnce configured;
   cudaError_t e = configured.run([] {
-    const int most = 5 * (kMaxTableBatch + 1) * (int)sizeof(int);
-    cudaError_t r = cudaFuncSetAttribute(tables_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (r != cudaSuccess) return r;
-    return cudaFuncSetAttribute(tables_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    const int most = sums_bytes(kMaxTableBatch);
+    const void* kernels[3] = {(const void*)tables_kernel, (const void*)tables_blocks_kernel,
+                              (const void*)tables_slots_kernel};
+    for (const void* k : kernels) {
+      const cudaError_t r = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+      if (r != cudaSuccess) return r;
+    }
+    return cudaSuccess;
   });
   if (e != cudaSuccess) return e;
-  if (p.num_tokens <= 4096) {
-    tables_kernel<false><<<1, kThreads, smem, stream>>>(p);
+  if (p.num_tokens <= kOneCtaTokens) {
+    // A small CTA starts a microsecond sooner; with room for many blocks many may have to move (8320
+    // given back: 62 us with 128 threads).
+    const int64_t room = (int64_t)p.batch * p.max_blocks;
+    const int threads = room <= 1024 && p.num_tokens <= 512 && p.batch <= 128 ? 128 : kMaxThreads;
+    tables_kernel<<<1, threads, smem, stream>>>(p);
     return cudaGetLastError();
   }
-  cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kClusterCtas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kClusterCtas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tables_kernel<true>, p);
+  tables_blocks_kernel<<<8, kMaxThreads, smem, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int64_t per_cta = (int64_t)kSlotThreads * kSlotsPerThread;
+  tables_slots_kernel<<<(unsigned)((p.num_tokens + per_cta - 1) / per_cta), kSlotThreads, smem, stream>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace mla

@@ -3,9 +3,12 @@
 //
 // tree_mask: a drafted node sees itself and its ancestors.  With parent(i) < i,
 //   M(i) = {i} u M(parent(i)),  depth(i) = 1 + depth(parent(i)),  M(-1) = {}, depth(-1) = -1,
-// written as bits, and its token position, context length + depth.  Each node is one thread
-// that walks up its own chain: no thread waits for another, and a chain is as long as the
-// tree is deep.
+// written as bits, and its token position, context length + depth.  For up to 256 nodes by doubling,
+// one CTA per tree: with J the 2^k-th ancestor and M the nearest 2^k of them (itself the first),
+//   M'(i) = M(i) u M(J(i)),  J'(i) = J(J(i)),
+// log2(depth) steps in shared memory; the depth is the number of bits less one.  (One thread per node
+// walking up its chain took 11 us for 256 trees of up to 100 nodes, this 6.)  Larger trees: each node
+// walks up, four words of its row at a time.
 //
 // tree_commit: row (s + path[i]) of the request moves to row (s + i), for i = 0 .. count - 1
 // with path strictly increasing, so path[j] >= j.  A thread owns 16 bytes of the row in one
@@ -20,6 +23,7 @@ namespace {
 
 constexpr int kMaskThreads = 128;
 constexpr int kMaskWords = 4;   // words of a row collected per walk
+constexpr int kSmallTree = 64 * kMaskWords;
 
 __device__ __forceinline__ void flag(int32_t* status) {
   if (status) atomicOr(status, MLA_DEVSTAT_BAD_INDEX);
@@ -38,6 +42,42 @@ tree_mask_kernel(const int32_t* __restrict__ parents, const int32_t* __restrict_
   const int n = (int)(q1 - q0);
   const int base = kv_lens ? kv_lens[r] - n : 0;
   const int32_t* par = parents + q0;
+  if (n <= kSmallTree) {
+    __shared__ uint64_t m[2][kSmallTree][kMaskWords];
+    __shared__ int16_t j[2][kSmallTree];
+    const int used = (n + 63) >> 6;   // words that hold bits
+    bool bad = false;
+    for (int i = threadIdx.x; i < n; i += kMaskThreads) {
+      const int up = __ldg(par + i);
+      const bool ok = up >= -1 && up < i;
+      bad |= !ok || i >= 64 * (int64_t)words;
+      j[0][i] = (int16_t)(ok ? up : -1);
+      for (int w = 0; w < used; ++w) m[0][i][w] = (i >> 6) == w ? 1ull << (i & 63) : 0ull;
+    }
+    if (bad) flag(status);
+    int at = 0;
+    bool more = true;
+    while (__syncthreads_or(more)) {   // halves what is left of the longest chain: at most 9 times
+      more = false;
+      for (int i = threadIdx.x; i < n; i += kMaskThreads) {
+        const int up = j[at][i], far = up >= 0 ? j[at][up] : -1;
+        for (int w = 0; w < used; ++w) m[at ^ 1][i][w] = m[at][i][w] | (up >= 0 ? m[at][up][w] : 0ull);
+        j[at ^ 1][i] = (int16_t)far;
+        more |= far >= 0;
+      }
+      at ^= 1;
+    }
+    for (int i = threadIdx.x; i < n; i += kMaskThreads) {
+      int depth = -1;
+      for (int w = 0; w < used; ++w) depth += __popcll(m[at][i][w]);
+      if (positions) positions[q0 + i] = base + depth;
+    }
+    for (int k = threadIdx.x; k < n * words; k += kMaskThreads) {   // (words <= 1024: fits)
+      const int i = k / words, w = k - i * words;
+      mask[q0 * words + k] = w < used ? (int64_t)m[at][i][w] : 0;
+    }
+    return;
+  }
   for (int i = threadIdx.x; i < n; i += kMaskThreads) {
     bool bad = i >= 64 * (int64_t)words;
     int depth = 0;
@@ -75,13 +115,16 @@ tree_commit_kernel(const CommitParams p) {
   __shared__ int64_t src[kCommitRows], dst[kCommitRows];   // flat slots; -1: leave this row
   __shared__ int stop;
   const int r = blockIdx.y, tid = threadIdx.x;
+  const int32_t* path = p.paths + (int64_t)r * p.max_accept;
+  // The first rows' path entries come with the count, not after it.
+  const bool mine = tid < kCommitRows && tid < p.max_accept;
+  const int first_node = mine ? path[tid] : 0, first_before = mine && tid > 0 ? path[tid - 1] : -1;
   int count = p.counts[r];
   if (count < 0 || count > p.max_accept) {
     if (tid == 0 && blockIdx.x == 0) flag(p.status);
     count = min(max(count, 0), p.max_accept);
   }
   const int64_t base = p.seq_lens[r];
-  const int32_t* path = p.paths + (int64_t)r * p.max_accept;
   const int chunks = p.row_chunks;
   const int64_t item = (int64_t)blockIdx.x * kCommitThreads + tid;
   const bool live = item < (int64_t)p.num_layers * chunks;
@@ -92,8 +135,8 @@ tree_commit_kernel(const CommitParams p) {
     if (tid == 0) stop = here;
     __syncthreads();
     if (tid < here) {
-      const int i = i0 + tid, node = path[i];
-      if (node < 0 || base < 0 || (i > 0 && path[i - 1] >= node)) atomicMin(&stop, tid);
+      const int i = i0 + tid, node = i0 ? path[i] : first_node, before = i0 ? path[i - 1] : first_before;
+      if (node < 0 || base < 0 || before >= node) atomicMin(&stop, tid);
       auto slot = [&](int64_t pos) -> int64_t {
         const int64_t bi = pos / p.block_size;
         if (pos < 0 || bi >= p.max_blocks) return -1;
