@@ -646,9 +646,10 @@ def mla_tree_mask(parents, qo_indptr, mask_words: int, kv_lens=None, mask=None, 
     context length when kv_lens is given)."""
     T, dev, st, handle = _here(stream, parents, "parents")
     int32, int64 = T.int32, T.int64
-    t, b, w = parents.shape[0], qo_indptr.shape[0] - 1, int(mask_words)
-    if parents.dim() != 1 or qo_indptr.dim() != 1 or b < 0 or w < 1:
+    w = int(mask_words)
+    if parents.dim() != 1 or qo_indptr.dim() != 1 or qo_indptr.shape[0] < 1 or w < 1:
         raise ValueError("parents must be [T], qo_indptr [B+1] and mask_words at least 1")
+    t, b = parents.shape[0], qo_indptr.shape[0] - 1
     if mask is None:
         mask = _new(T, (t, w), int64, parents.device, st)
     if positions is None:

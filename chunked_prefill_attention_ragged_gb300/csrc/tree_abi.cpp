@@ -32,6 +32,10 @@ int mla_block_table_update(const int32_t* seq_lens, const int32_t* new_lens, int
     return MLA_ERR_INVALID_ARG;
   if (batch > 0 && (!seq_lens || !new_lens || !num_held || (max_blocks_per_req > 0 && !block_table)))
     return MLA_ERR_INVALID_ARG;
+  // The lengths are read again after the outputs of their size are written.
+  if (batch > 0 && (kv_lens == seq_lens || kv_lens == new_lens || qo_indptr == seq_lens || qo_indptr == new_lens ||
+                    num_held == seq_lens || num_held == new_lens))
+    return MLA_ERR_INVALID_ARG;
   TablesParams p;
   p.seq_lens = seq_lens;
   p.new_lens = new_lens;
@@ -67,7 +71,7 @@ int mla_tree_mask(const int32_t* parents, const int32_t* qo_indptr, const int32_
 
 int mla_tree_workspace(int64_t total_rows, int num_heads, int64_t* bytes) {
   if (!bytes || total_rows < 0 || num_heads < 1 || num_heads > 65535) return MLA_ERR_INVALID_ARG;
-  if (total_rows * num_heads > kMaxTreePairs) return MLA_ERR_UNSUPPORTED;
+  if (total_rows > kMaxTreePairs || total_rows * num_heads > kMaxTreePairs) return MLA_ERR_UNSUPPORTED;
   const int64_t n = tree_workspace_bytes();
   if (n <= 0) return MLA_ERR_CUDA;
   *bytes = n;

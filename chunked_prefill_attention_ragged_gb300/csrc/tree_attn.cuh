@@ -196,7 +196,9 @@ __device__ __forceinline__ int block_of(const TreeLaunch& p, int key) {
   return p.block_shift >= 0 ? key >> p.block_shift : key / p.t.block_size;
 }
 __device__ __forceinline__ int32_t table_block(const TreeLaunch& p, const Part& u, int64_t key) {
-  return key < u.q.kv ? __ldg(p.t.block_table + (int64_t)u.r * p.t.max_blocks + block_of(p, (int)key)) : PAST_END;
+  if (key >= u.q.kv) return PAST_END;
+  const int32_t blk = __ldg(p.t.block_table + (int64_t)u.r * p.t.max_blocks + block_of(p, (int)key));
+  return blk == PAST_END ? -1 : blk;   // (so named in the table, it is a bad id like any other)
 }
 __device__ __forceinline__ int32_t block_row(const TreeLaunch& p, int32_t blk, int64_t key) {
   if (blk < 0 || (int64_t)blk >= p.t.num_blocks) {

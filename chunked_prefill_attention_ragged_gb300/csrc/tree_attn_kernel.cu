@@ -3,11 +3,6 @@
 // (node i, head h) of a request with n nodes and kv cached positions sees the positions below
 // kv - n and those of the nodes that its mask bits name.
 //
-// What is computed follows sglang issue #3849 ("[DeepseekR1] How ragged prefill manage
-// kv_cache?"): every head attends to the compressed cache rows (512 latent + 64 rope, one KV
-// head), and the slot rule of vLLM "vllm/models/deepseek_v4/sparse_mla.py"
-// (_build_c128a_topk_metadata_kernel, decode branch).
-//
 // Mathematics.  A unit is 128 consecutive (node, head) pairs of one request.  Over tiles of 128
 // keys, with scores s in log2 units and a reference m per pair that follows the running maximum,
 //   P = 2^(s - m),  l += sum P,  O += P V;  when a maximum passes m + 8: O, l *= 2^(m - m').
@@ -649,7 +644,7 @@ __device__ void run_softmax(const Ctx& c, const TreeLaunch& p, Parts parts, uint
     const float l_row = l + l_other;
     if (!c.wait_warp(OD, (g - 1) & 1)) break;
     tc_fence_after();
-    const bool empty = !(l_row > 0.f);
+    const bool empty = l_row == 0.f;   // (a NaN is passed on)
     const float inv = u.whole ? (empty ? 0.f : 1.f / l_row) : 1.f;
     const float2 inv2 = make_float2(inv, inv);
     char* slot = ws_slots + (size_t)u.slot * SLOT_BYTES;

@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) tree_join_kernel(const __grid
       }
     }
   }
-  const bool empty = !(l > 0.f);
+  const bool empty = l == 0.f;
   const float inv = empty ? 0.f : 1.f / l;
   uint2* d = reinterpret_cast<uint2*>(p.t.o + pair * 512) + lane;
 #pragma unroll

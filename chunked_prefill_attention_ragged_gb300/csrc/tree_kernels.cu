@@ -3,12 +3,13 @@
 //
 // tree_mask: a drafted node sees itself and its ancestors.  With parent(i) < i,
 //   M(i) = {i} u M(parent(i)),  depth(i) = 1 + depth(parent(i)),  M(-1) = {}, depth(-1) = -1,
-// written as bits, and its token position, context length + depth.  For up to 256 nodes by doubling,
-// one CTA per tree: with J the 2^k-th ancestor and M the nearest 2^k of them (itself the first),
+// written as bits, and its token position, context length + depth.  One CTA per tree, 256 nodes at a
+// time, by doubling: with J the 2^k-th ancestor and M the nearest 2^k of them (itself the first),
 //   M'(i) = M(i) u M(J(i)),  J'(i) = J(J(i)),
-// log2(depth) steps in shared memory; the depth is the number of bits less one.  (One thread per node
-// walking up its chain took 11 us for 256 trees of up to 100 nodes, this 6.)  Larger trees: each node
-// walks up, four words of its row at a time.
+// log2(depth) steps in shared memory, as far as the ancestors are of the same 256; what is above the
+// lowest of those is the finished row of its parent.  The depth is the number of bits less one.  Bound
+// by latency (two loads, the steps, a store: 5 us, and 6 for 256 trees of up to 100 nodes, where one
+// thread per node walking up its chain took 11); the work grows with nodes * mask_words only.
 //
 // tree_commit: row (s + path[i]) of the request moves to row (s + i), for i = 0 .. count - 1
 // with path strictly increasing, so path[j] >= j.  A thread owns 16 bytes of the row in one
@@ -22,8 +23,8 @@ namespace mla {
 namespace {
 
 constexpr int kMaskThreads = 128;
-constexpr int kMaskWords = 4;   // words of a row collected per walk
-constexpr int kSmallTree = 64 * kMaskWords;
+constexpr int kNodeWords = 4;
+constexpr int kNodes = 64 * kNodeWords;   // nodes at a time
 
 __device__ __forceinline__ void flag(int32_t* status) {
   if (status) atomicOr(status, MLA_DEVSTAT_BAD_INDEX);
@@ -31,8 +32,7 @@ __device__ __forceinline__ void flag(int32_t* status) {
 
 __global__ void __launch_bounds__(kMaskThreads)
 tree_mask_kernel(const int32_t* __restrict__ parents, const int32_t* __restrict__ qo_indptr,
-                 const int32_t* __restrict__ kv_lens, int64_t total_rows, int words, int64_t* __restrict__ mask,
-                 int32_t* __restrict__ positions, int32_t* status) {
+                 const int32_t* __restrict__ kv_lens, int64_t total_rows, int words, int64_t* mask, int32_t* positions, int32_t* status) {
   const int r = blockIdx.x;
   const int64_t q0 = qo_indptr[r], q1 = qo_indptr[r + 1];
   if (q0 < 0 || q1 < q0 || q1 > total_rows) {
@@ -42,16 +42,21 @@ tree_mask_kernel(const int32_t* __restrict__ parents, const int32_t* __restrict_
   const int n = (int)(q1 - q0);
   const int base = kv_lens ? kv_lens[r] - n : 0;
   const int32_t* par = parents + q0;
-  if (n <= kSmallTree) {
-    __shared__ uint64_t m[2][kSmallTree][kMaskWords];
-    __shared__ int16_t j[2][kSmallTree];
-    const int used = (n + 63) >> 6;   // words that hold bits
+  __shared__ uint64_t m[2][kNodes][kNodeWords];
+  __shared__ int16_t j[2][kNodes];      // ancestor inside the group, -1: none
+  __shared__ int32_t above[kNodes];     // parent before the group, -1: none
+  for (int i0 = 0; i0 < n; i0 += kNodes) {
+    const int here = min(kNodes, n - i0), used = (here + 63) >> 6, w0 = i0 >> 6;
     bool bad = false;
-    for (int i = threadIdx.x; i < n; i += kMaskThreads) {
-      const int up = __ldg(par + i);
-      const bool ok = up >= -1 && up < i;
-      bad |= !ok || i >= 64 * (int64_t)words;
-      j[0][i] = (int16_t)(ok ? up : -1);
+    for (int i = threadIdx.x; i < here; i += kMaskThreads) {
+      int up = __ldg(par + i0 + i);
+      if (up < -1 || up >= i0 + i) {
+        bad = true;
+        up = -1;
+      }
+      bad |= i0 + i >= 64 * (int64_t)words;
+      j[0][i] = (int16_t)(up >= i0 ? up - i0 : -1);
+      above[i] = up >= i0 ? -1 : up;
       for (int w = 0; w < used; ++w) m[0][i][w] = (i >> 6) == w ? 1ull << (i & 63) : 0ull;
     }
     if (bad) flag(status);
@@ -59,7 +64,7 @@ tree_mask_kernel(const int32_t* __restrict__ parents, const int32_t* __restrict_
     bool more = true;
     while (__syncthreads_or(more)) {   // halves what is left of the longest chain: at most 9 times
       more = false;
-      for (int i = threadIdx.x; i < n; i += kMaskThreads) {
+      for (int i = threadIdx.x; i < here; i += kMaskThreads) {
         const int up = j[at][i], far = up >= 0 ? j[at][up] : -1;
         for (int w = 0; w < used; ++w) m[at ^ 1][i][w] = m[at][i][w] | (up >= 0 ? m[at][up][w] : 0ull);
         j[at ^ 1][i] = (int16_t)far;
@@ -67,42 +72,31 @@ tree_mask_kernel(const int32_t* __restrict__ parents, const int32_t* __restrict_
       }
       at ^= 1;
     }
-    for (int i = threadIdx.x; i < n; i += kMaskThreads) {
-      int depth = -1;
-      for (int w = 0; w < used; ++w) depth += __popcll(m[at][i][w]);
-      if (positions) positions[q0 + i] = base + depth;
-    }
-    for (int k = threadIdx.x; k < n * words; k += kMaskThreads) {   // (words <= 1024: fits)
-      const int i = k / words, w = k - i * words;
-      mask[q0 * words + k] = w < used ? (int64_t)m[at][i][w] : 0;
-    }
-    return;
-  }
-  for (int i = threadIdx.x; i < n; i += kMaskThreads) {
-    bool bad = i >= 64 * (int64_t)words;
-    int depth = 0;
-    for (int w0 = 0; w0 < words; w0 += kMaskWords) {
-      uint64_t bits[kMaskWords] = {0, 0, 0, 0};
-      int up = i;
-      depth = -1;
-      while (up >= 0) {   // strictly downwards: ends
-        ++depth;
-#pragma unroll
-        for (int k = 0; k < kMaskWords; ++k)
-          if ((up >> 6) == w0 + k) bits[k] |= 1ull << (up & 63);
-        const int next = __ldg(par + up);
-        if (next < -1 || next >= up) {
-          bad = true;
-          break;
-        }
-        up = next;
+    // The chain leaves the group behind its lowest node here.
+    for (int i = threadIdx.x; i < here; i += kMaskThreads) {
+      int len = 0, top = -1;
+      for (int w = 0; w < used; ++w) {
+        const uint64_t bits = m[at][i][w];
+        len += __popcll(bits);
+        if (top < 0 && bits) top = 64 * w + __ffsll((long long)bits) - 1;
       }
-#pragma unroll
-      for (int k = 0; k < kMaskWords; ++k)
-        if (w0 + k < words) mask[(q0 + i) * words + w0 + k] = (int64_t)bits[k];
+      const int up = above[top];
+      j[at ^ 1][i] = (int16_t)top;
+      if (positions) positions[q0 + i0 + i] = (up >= 0 ? positions[q0 + up] : base - 1) + len;
     }
-    if (positions) positions[q0 + i] = base + depth;
-    if (bad) flag(status);
+    __syncthreads();
+    for (int k = threadIdx.x; k < here * words; k += kMaskThreads) {   // (words <= 1024: fits)
+      const int i = k / words, w = k - i * words;
+      uint64_t bits = 0;
+      if (w >= w0) {
+        if (w - w0 < used) bits = m[at][i][w - w0];
+      } else {
+        const int up = above[j[at ^ 1][i]];
+        if (up >= 0) bits = (uint64_t)mask[(q0 + up) * words + w];   // (written by this CTA, groups ago)
+      }
+      mask[(q0 + i0) * words + k] = (int64_t)bits;
+    }
+    __syncthreads();
   }
 }
 

@@ -377,7 +377,6 @@ MLA_API int mla_absorbed_run(mla_plan_t plan, const void* q_abs, const void* cac
  * to consecutive positions (mla_tree_commit).  One node per request is
  * ordinary decoding.  Every length is read on the device, so that a captured
  * graph of the step can be replayed as the requests grow.
- * [vLLM-V4] slot rule; [sglang] 512 latent + 64 rope per cache row.
  * ====================================================================== */
 /*
  * Fit the block tables to the requests' lengths, and map new tokens to slots.
@@ -401,7 +400,8 @@ MLA_API int mla_absorbed_run(mla_plan_t plan, const void* q_abs, const void* cac
  * negative length, num_held or free_count outside its range (clamped), a request that needs
  * more than max_blocks_per_req blocks (it keeps what it holds), a full stack (the block is
  * lost), a negative block id taken from the stack, or more new tokens than num_tokens.
- * Limits: batch <= 8192, batch * max_blocks_per_req < 2^31.  One launch; allocates nothing.
+ * Limits: batch <= 8192, batch * max_blocks_per_req < 2^31.  One or two launches; allocates nothing.
+ * kv_lens, qo_indptr and num_held are not the arrays of seq_lens or new_lens.
  * Calls that share a stack must be ordered by the caller.
  */
 MLA_API int mla_block_table_update(const int32_t* seq_lens, const int32_t* new_lens, int batch, int block_size,
@@ -454,7 +454,9 @@ MLA_API int mla_tree_workspace(int64_t total_rows, int num_heads, int64_t* bytes
  *   workspace  : DEVICE, 32-byte aligned, at least mla_tree_workspace bytes, not in use by
  *                another call that may run at the same time; its contents do not matter
  *   status     : DEVICE int32 word or NULL
- * A row that sees no key gets O = 0, LSE = -inf.  Positions at or past kv_len are never read.
+ * A row that sees no key gets O = 0, LSE = -inf; a NaN in a row of q_abs makes that row NaN.
+ * Positions at or past kv_len never count (rows behind the last key may be read inside its
+ * block; what is in them does not matter).  The cap's logits are off by at most 2^-20 c.
  * Cache rows below kv_len are to be finite: an infinity or NaN in a row that a node does not
  * see may still reach the other rows of its request.  MLA_DEVSTAT_BAD_INDEX is OR-ed in for a
  * block id outside [0, num_blocks) (its rows read as zeros), kv_len outside

@@ -1,12 +1,10 @@
 """The speculative-decoding step over a paged cache, in plain Python and float64 -- test
 infrastructure only.
 
-Sources: vLLM "vllm/models/deepseek_v4/sparse_mla.py", _build_c128a_topk_metadata_kernel
-(decode branch): slot of position p = block_table[r, p // block_size] * block_size +
-p % block_size, -1 for a token without a place; sglang issue #3849: a cache row is 512 latent
-+ 64 rope values, and under absorption every head attends to the rows themselves.  The rest is
-the definition, written out: blocks are counted by rounding lengths up, a drafted node sees the
-context, itself and its ancestors.
+The definitions, written out: position p of a request is in slot block_table[r, p // block_size] *
+block_size + p % block_size, -1 for a token without a place; blocks are counted by rounding lengths
+up; a cache row is 512 latent + 64 rope values, and every head attends to the rows themselves; a
+drafted node sees the context, itself and its ancestors.
 """
 import numpy as np
 

@@ -97,13 +97,50 @@ def test_slots_past_32_bits():
     assert got[2].tolist() == [4000 * (1 << 20) + k for k in (5, 6, 7)]
 
 
+def test_block_table_update_many_tokens_bad_values():
+    """As above where the slots come from a grid: a request that does not fit its row, a stack that is
+    full, more new tokens than slots."""
+    bs, new = 16, [3000, 900, 2500, 0]
+    table = np.full((4, 200), -1)
+    table[3, :2] = [7, 8]
+    got = run_tables([0, 4000, 0, 0], new, table, [0, 0, 0, 2], list(range(100, 500)), bs, 500, sum(new) + 3005)
+    assert got[6] == BAD_INDEX and got[4].tolist() == [188, 0, 157, 0]
+    want = np.concatenate([[7, 8], np.arange(499, 99, -1)])   # (the ones given back go first)
+    assert got[3][0, :188].tolist() == want[:188].tolist() and got[3][2, :157].tolist() == want[188:345].tolist()
+    pos = np.arange(3000)
+    assert np.array_equal(got[2][:3000], want[pos // bs] * bs + pos % bs) and (got[2][3000:3900] == -1).all()
+    assert (got[2][-5:] == -1).all()
+    got = run_tables([0], [0], [[3, 4]], [2], [1], bs, 2, 9000)     # two blocks come back, one finds room
+    assert got[6] == BAD_INDEX and got[5] == [1, 4] and (got[2] == -1).all()
+    got = run_tables([0], [12000], [[-1] * 800], [0], list(range(800)), bs, 800, 9000)
+    assert got[6] == BAD_INDEX and got[0].tolist() == [0, 12000]
+    assert got[2][-1] == (799 - 8999 // bs) * bs + 8999 % bs
+
+
+def test_block_table_update_of_two_streams():
+    import chunked_prefill_attention_ragged_gb300 as mla
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    for k, s in enumerate(streams):
+        with torch.cuda.stream(s):
+            args = [i32([5, 9]), i32([k + 1, 6000 * k]), i32([[-1] * 400] * 2), i32([0, 0]), i32(np.arange(800)), i32([800])]
+        s.synchronize()
+        outs.append((args, [mla.mla_block_table_update(*args, 16, 6002 + 3000 * k, stream=s) for _ in range(3)][-1]))
+    torch.cuda.synchronize()
+    for k, (args, (qo, kv, slots)) in enumerate(outs):
+        assert qo.tolist() == [0, k + 1, k + 1 + 6000 * k] and kv.tolist() == [6 + k, 9 + 6000 * k]
+        need = 1 + -(-(9 + 6000 * k) // 16)
+        assert args[5].tolist() == [800 - need] and slots[0] == 799 * 16 + 5 and (slots[k + 1 + 6000 * k:] == -1).all()
+
+
 # ---------------------------------------------------------------------------------- tree mask
 def random_parents(rng, n, reach):
     return np.array([-1 if i == 0 else int(rng.integers(max(-1, i - reach), i)) for i in range(n)], dtype=np.int64)
 
 
 @pytest.mark.parametrize("nodes,words,reach", [([1], 1, 1), ([64, 0, 1, 63], 1, 3), ([65, 200, 7], 4, 5), ([300], 5, 1),
-                                               ([3, 130], 3, 200), ([2] * 70, 1, 2), ([600], 10, 4)])
+                                               ([3, 130], 3, 200), ([2] * 70, 1, 2), ([600], 10, 4),
+                                               ([256, 257, 5, 511], 9, 400), ([1500, 1], 24, 1), ([700, 40], 30, 700)])
 def test_tree_mask(nodes, words, reach):
     import chunked_prefill_attention_ragged_gb300 as mla
     rng = np.random.default_rng(sum(nodes) + words)
@@ -127,6 +164,18 @@ def test_tree_mask(nodes, words, reach):
             np.testing.assert_array_equal(p.tensor[qo[r]:qo[r + 1]].cpu().numpy(), depth + base)
         assert (m.tensor[qo[-1]:] == -5).all() and (p.tensor[qo[-1]:] == -6).all()
     assert int(st) == 0
+
+
+def test_tree_mask_of_a_long_chain():
+    """Node i sees 0 .. i: 20000 of them, in time that grows with the size of the mask."""
+    import chunked_prefill_attention_ragged_gb300 as mla
+    n, words, st = 20000, 313, new_status()
+    mask, pos = mla.mla_tree_mask(i32(np.arange(n) - 1), i32([0, n]), words, status=st)
+    assert int(st) == 0 and torch.equal(pos, torch.arange(n, dtype=torch.int32, device="cuda"))
+    i, w = torch.arange(n, device="cuda")[:, None], torch.arange(words, device="cuda")[None]
+    ones = (i + 1 - 64 * w).clamp(0, 64)   # bits set in the word, from the lowest on
+    want = torch.where(ones == 64, -1, (torch.ones_like(ones) << ones.clamp(max=63)) - 1)
+    assert torch.equal(mask, want)
 
 
 def test_tree_mask_bad_input():
@@ -339,10 +388,66 @@ def test_tree_attention_does_not_read_past_the_lengths(heads):
     assert np.array_equal(bits_of(before[0]), bits_of(after[0])) and torch.equal(before[1], after[1])
 
 
+@pytest.mark.parametrize("bs", [1, 8, 16, 24, 32, 128])
+def test_tree_attention_ends_inside_a_block(bs):
+    """NaN behind the last key, at every kind of end and block size."""
+    kv = [1, 7, 8, 9, 31, 33, 63, 65, 97, 120, 127, 129, 160, 191, 193, 250]
+    p = Problem(18, [1] * len(kv), kv, 6, bs, False)
+    own = np.zeros(p.b.cache.shape[:2], dtype=bool)
+    for r, k in enumerate(kv):
+        pos = np.arange(k)
+        own[p.b.block_table[r, pos // bs], pos % bs] = True
+    p.b.cache[~own] = 0x7FC0
+    o, lse, st = p.run()
+    assert st == 0
+    p.check(o, lse)
+
+
+@pytest.mark.parametrize("ctx", [60, 20000])   # in one piece, and joined
+def test_tree_attention_passes_nan_on_in_its_row_only(ctx):
+    p = Problem(19, [3, 2], [ctx, 70], 4, 64, True)
+    p.b.q_abs[1, 2, 570] = 0x7FC0
+    o, lse, st = p.run()
+    assert st == 0 and torch.isnan(o[1, 2].float()).all() and bool(torch.isnan(lse[1, 2]))
+    q = p.b.q_abs.copy()
+    q[1, 2] = p.b.q_abs[1, 1]
+    p.b.q_abs = q
+    o2, lse2, _ = p.run()
+    keep = torch.ones_like(lse, dtype=torch.bool)
+    keep[1, 2] = False
+    assert torch.equal(o[keep], o2[keep]) and torch.equal(lse[keep], lse2[keep])
+
+
+def test_tree_attention_nodes_past_the_mask_are_not_seen():
+    p = Problem(21, [70, 3], [100, 40], 2, 64, True)
+    assert p.words == 2
+    p.seen = [s * (np.arange(s.shape[1]) < 64) for s in p.seen]
+    want = p.run()
+    p.seen = [s[:, :64] for s in p.seen]
+    p.words = 1
+    got = p.run()
+    assert np.array_equal(bits_of(got[0]), bits_of(want[0])) and torch.equal(got[1], want[1])
+    p.seen = [np.pad(s, ((0, 0), (0, max(0, len(s) - s.shape[1])))) for s in p.seen]
+    p.check(got[0], got[1])
+
+
+@pytest.mark.parametrize("ctx", [70, 20000])
+def test_tree_attention_output_on_16_bytes(ctx):
+    import chunked_prefill_attention_ragged_gb300 as mla
+    p = Problem(22, [2], [ctx], 5, 64, True)
+    o, lse, _ = p.run()
+    o2 = torch.full((10 * 512 + 16,), 3.0, dtype=torch.bfloat16, device="cuda")
+    b = p.b
+    mla.mla_tree_attention(to_dev_bf16(b.q_abs), to_dev_bf16(b.cache), to_dev(b.block_table), i32(b.qo_indptr),
+                           i32(p.kv), p.mask(), sm_scale=b.sm_scale, o=o2[8:-8].view(2, 5, 512))
+    assert np.array_equal(bits_of(o2[8:-8].view(2, 5, 512)), bits_of(o))
+    assert (o2[:8] == 3.0).all() and (o2[-8:] == 3.0).all()
+
+
 @pytest.mark.parametrize("heads", [8, 100])
 def test_tree_attention_bad_blocks_read_as_zeros(heads):
     p = Problem(9, [2, 2], [300, 150], heads, 64, True)
-    p.b.block_table[0, 1] = 10 ** 6
+    p.b.block_table[0, 1] = -2 ** 31 if heads > 8 else 10 ** 6
     p.b.block_table[1, 0] = -1
     o, lse, st = p.run()
     assert st == BAD_INDEX
@@ -370,6 +475,27 @@ def test_tree_attention_bad_lengths_are_clamped_or_skipped():
                                     i32([0, 2, 4, 9]), i32(p.kv), p.mask(), sm_scale=p.b.sm_scale, o=o, status=st)
     assert int(st) == BAD_INDEX and (o[4:] == 3.0).all()
     p.check(o, lse, [0, 1])
+
+
+def test_tree_attention_more_requests_than_threads():
+    """Several requests to a thread in the search for a worker's piece, empty ones among them."""
+    rng = np.random.default_rng(4)
+    nodes, kv = rng.integers(0, 3, 700), rng.integers(0, 200, 700)
+    p = Problem(15, nodes.tolist(), kv.tolist(), 3, 16, False)
+    o, lse, st = p.run(pad=1)
+    assert st == 0
+    p.check(o, lse, list(range(0, 700, 13)) + [699])
+
+
+def test_tree_attention_forced_timeout(monkeypatch):
+    """One wait that nothing satisfies gives up and is reported; the next call is right again."""
+    p = Problem(16, [3, 2], [500, 40], 16, 64, True)
+    monkeypatch.setenv("MLA_TEST_FORCE_TIMEOUT_NS", "2000000")
+    assert p.run()[2] == 1
+    monkeypatch.delenv("MLA_TEST_FORCE_TIMEOUT_NS")
+    o, lse, st = p.run()
+    assert st == 0
+    p.check(o, lse)
 
 
 def test_tree_attention_no_lse_and_own_workspace():

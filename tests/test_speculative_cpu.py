@@ -8,7 +8,7 @@ A = 4096   # an aligned address that is never followed
 
 
 def tables(**kw):
-    a = dict(seq=A, new=A, batch=2, bs=64, table=A, m=4, held=A, free=A, cap=8, count=A, qo=A, kv=A, slots=A, n=3,
+    a = dict(seq=3 * A, new=4 * A, batch=2, bs=64, table=A, m=4, held=A, free=A, cap=8, count=A, qo=A, kv=A, slots=A, n=3,
              status=None)
     a.update(kw)
     return mla.library().mla_block_table_update(a["seq"], a["new"], a["batch"], a["bs"], a["table"], a["m"], a["held"],
@@ -22,6 +22,7 @@ def tables(**kw):
     (dict(seq=None), -1), (dict(new=None), -1), (dict(table=None), -1), (dict(held=None), -1), (dict(free=None), -1),
     (dict(count=None), -1), (dict(slots=None), -1), (dict(slots=A + 4), -1), (dict(seq=A + 2), -1),
     (dict(status=A + 1), -1),
+    (dict(kv=A, seq=A, new=2 * A), -1), (dict(qo=A, new=A, seq=2 * A), -1), (dict(held=A, seq=A, new=2 * A), -1),
 ])
 def test_block_table_update_refuses(kw, rc):
     assert tables(**kw) == rc
@@ -95,6 +96,8 @@ def test_workspace_refuses():
         mla.mla_tree_workspace(-1, 16)
     with pytest.raises(mla.MlaError):
         mla.mla_tree_workspace(1 << 40, 16)
+    with pytest.raises(mla.MlaError):
+        mla.mla_tree_workspace(1 << 62, 16)   # (times the heads: 0 in 64 bits)
 
 
 def test_python_wants_cuda_tensors():
