@@ -35,7 +35,9 @@ struct JoinRec {
 };
 constexpr int MAX_WORKERS = 256;
 constexpr size_t WS_SLOTS = MAX_WORKERS * sizeof(JoinRec);
-// A slot: the rows' O (fp32), then their (m in log2 units, l).
+// A slot: O (fp32) as 64 groups of eight columns, each [128 rows][8], so that a warp, whose threads
+// have a row each, writes and reads 1 KB at a time; then the rows' (m in log2 units, l).
+__device__ __forceinline__ size_t slot_at(int row, int col) { return ((size_t)(col >> 3) * TREE_ROWS + row) * 32; }
 constexpr size_t SLOT_ML = (size_t)TREE_ROWS * 512 * 4;
 constexpr size_t SLOT_BYTES = SLOT_ML + TREE_ROWS * 2 * 4;
 

@@ -672,9 +672,9 @@ __device__ void run_softmax(const Ctx& c, const TreeLaunch& p, Parts parts, uint
             reinterpret_cast<uint4*>(d)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
         }
       } else {
-        float* d = reinterpret_cast<float*>(slot) + (size_t)pr0 * 512 + col;
+        char* d = slot + slot_at(pr0, col);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) st_global_v8(d + 8 * k, ov + 8 * k);
+        for (int k = 0; k < 8; ++k) st_global_v8(d + slot_at(0, 8 * k), ov + 8 * k);
       }
     }
     if (live && half == 0) {
