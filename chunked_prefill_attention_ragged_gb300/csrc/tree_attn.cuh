@@ -14,8 +14,6 @@ struct TreeLaunch {
   int workers;         // clusters of two CTAs
   int32_t oob_row;     // a row coordinate past the cache: the copy fills it with zeros
   int block_shift;     // log2 of the block size, or -1
-  int piece_rows;      // rows of one box of the block map (0: gather4 only)
-  int grouped;         // 64-row boxes over several panels (the three-dimensional maps)
   int o_align32;
   int has_cap;
   float scale_log2, cap_log2, cap_ex2_scale;
@@ -183,8 +181,8 @@ struct Parts {
 
 // Where 64 keys from `key0` on are, spread over the lanes: first the blocks as the table has them
 // (the loads are under way while the caller does other things), then the rows to copy.  With block
-// sizes of 8, 16, 32 or multiples of 64 they come by boxes, lane k holding piece k; else lanes 0-15
-// hold keys 4 lane .. + 3 each.  A key past the readable ones, or in a block that the table does not
+// sizes of 8, 16, 32 or multiples of 64 they come by boxes of `step` keys, lane k holding box k; else
+// (step 0) lanes 0-15 hold keys 4 lane .. + 3 each.  A key past the readable ones, or in a block that the table does not
 // name, is the row past the cache (read as zeros), the latter flagged; in the piece in which the
 // readable keys end, what lies behind them comes along.
 constexpr int32_t PAST_END = -0x7fffffff - 1;
@@ -209,10 +207,10 @@ __device__ __forceinline__ int32_t block_row(const TreeLaunch& p, int32_t blk, i
   }
   return (int32_t)((int64_t)blk * p.t.block_size + ((int)key - block_of(p, (int)key) * p.t.block_size));
 }
-__device__ __forceinline__ KeyBlocks find_blocks(const TreeLaunch& p, const Part& u, int64_t key0, int lane) {
+__device__ __forceinline__ KeyBlocks find_blocks(const TreeLaunch& p, const Part& u, int64_t key0, int step, int lane) {
   KeyBlocks k{{PAST_END, PAST_END, PAST_END, PAST_END}};
-  if (p.piece_rows > 0) {
-    if (lane * p.piece_rows < 64) k.b[0] = table_block(p, u, key0 + lane * p.piece_rows);
+  if (step > 0) {
+    if (lane * step < 64) k.b[0] = table_block(p, u, key0 + lane * step);
   } else if (lane < 16) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) k.b[j] = table_block(p, u, key0 + 4 * lane + j);
@@ -220,10 +218,10 @@ __device__ __forceinline__ KeyBlocks find_blocks(const TreeLaunch& p, const Part
   return k;
 }
 __device__ __forceinline__ KeyRows find_rows(const TreeLaunch& p, const Part& u, const KeyBlocks& k, int64_t key0,
-                                             int lane) {
+                                             int step, int lane) {
   KeyRows w;
-  if (p.piece_rows > 0) {
-    w.r[0] = block_row(p, k.b[0], key0 + lane * p.piece_rows);
+  if (step > 0) {
+    w.r[0] = block_row(p, k.b[0], key0 + lane * step);
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) w.r[j] = block_row(p, k.b[j], key0 + 4 * lane + j);

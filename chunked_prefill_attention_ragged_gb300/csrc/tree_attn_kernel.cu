@@ -20,18 +20,19 @@
 // 0-63 hold the first half of a product's columns for the 64 rows, lanes 64-127 the second),
 // which leaves room for two S buffers.  A single CTA with 128 rows has no room for S beside O and
 // would compute S once per half of the values.  Per CTA in shared memory: its Q rows (64 x 576),
-// its 64 of the tile's 128 keys as the half of S's B operand, the tile's 128 keys x its half of
-// the value columns as the half of P V's B operand, and P (64 x 128).
+// its 64 of the tile's 128 keys as the half of S's B operand, the tile's 128 keys x 256 of the value
+// columns as the half of P V's B operand (two products of 128 columns of each CTA), and P (64 x 128).
 //   warp 0     Q and K producer: Q once per unit; K in three groups of three 64-column panels
 //   warp 1     even CTA: issues every product
-//   warp 2     V producer: two 256-column chunks (128 of the columns here), by halves of the keys
-//   warp 3     TMEM allocation; brings the next tile's rows into L2, or, where K comes in many small
-//              copies, loads its last group
+//   warp 2     V producer: the CTA's columns, by halves of the keys
+//   warp 3     TMEM allocation; brings the next tile's rows into L2, or, where K comes by gather4,
+//              loads its last group
 //   warps 4-7  softmax: two threads per pair (the two halves of the keys and of O's columns)
 // Order of products: S(t + 1) before P V(t), so that the tensor cores work on the next tile while
 // the softmax does this one.  Key rows come by whole boxes of 64 where the block size is a multiple
-// of that (in the piece where the keys end, what lies behind them is made zero), else by smaller
-// boxes or by gather4 with rows past the end read as zeros.
+// of that, by smaller boxes where it is 8, 16 or 32 (in the piece where the keys end, what lies behind
+// them is made zero), else by gather4 with rows past the end read as zeros.  The kernel is compiled
+// for each: with strides of the operands read from registers the products' issue took 3% longer.
 // Every wait is bounded: on time-out the CTA records MLA_DEVSTAT_TIMEOUT, drains its copies and
 // products, frees TMEM and returns.
 #include <cuda_bf16.h>
@@ -48,12 +49,13 @@ namespace {
 constexpr int ROWS = TREE_ROWS, KEYS = TREE_KEYS;   // 64 rows in each CTA
 constexpr int QP = 64 * 128;            // a [64 rows, 64 columns] panel: 8 KB
 constexpr int NP = 9;                   // 64-column panels of 576
-constexpr int KGROUPS = 3;              // K panels arrive in groups of three
-constexpr int V_CHUNK = 4 * QP;         // [2 key halves][2 panels][64 keys][64 columns] of one value chunk
+constexpr int KGROUPS = 3;              // K panels arrive in groups of three, or
+constexpr int K_ROWS8 = NP * 8 * 128;   // eight rows at a time: [panel][8 rows] of each
+constexpr int V_HALF = 4 * QP;          // 64 keys x the CTA's 256 value columns
 constexpr int OFF_Q = 0;
 constexpr int OFF_K = OFF_Q + NP * QP;
 constexpr int OFF_V = OFF_K + NP * QP;
-constexpr int OFF_P = OFF_V + 2 * V_CHUNK;
+constexpr int OFF_P = OFF_V + 2 * V_HALF;
 constexpr int OFF_XCHG = OFF_P + 2 * QP;            // [2 tiles][2 halves][64 rows] maxima
 constexpr int OFF_BAR = OFF_XCHG + 2 * 2 * 64 * 4;
 enum Bar {
@@ -61,14 +63,14 @@ enum Bar {
   QE,                  // the unit's last S done: Q may be replaced
   KF,                  // [group] K panels landed
   KE = KF + KGROUPS,   // [group] their products done
-  VF = KE + KGROUPS,   // [chunk, key half] V landed
-  VE = VF + 4,         // [chunk, key half] its products done
-  SF = VE + 4,         // [buffer] S done
+  VF = KE + KGROUPS,   // [key half] V landed
+  VE = VF + 2,         // [key half] its products done
+  SF = VE + 2,         // [buffer] S done
   PR = SF + 2,         // P written (and the S buffer read) by every softmax warp of both CTAs
   OD,                  // P V done
-  LB,                  // [chunk] the half of V to mend landed (in this CTA)
-  ZB = LB + 2,         // [chunk] the odd CTA has mended its own
-  XB = ZB + 2,         // [row half] maxima exchanged between the two warps of 32 rows
+  LB,                  // the half of V to mend landed (in this CTA)
+  ZB,                  // the odd CTA has mended its own
+  XB,                  // [row half] maxima exchanged between the two warps of 32 rows
   FIN = XB + 2,        // every product drained
   NEVER,               // nothing arrives here: the time-out test mode waits on it
   NBAR
@@ -103,33 +105,14 @@ struct Ctx {
   }
 };
 
-// 64 keys x panels [panel0, panel0 + n) to n consecutive 8 KB panels at dst, completing on `bar`
-// (a shared::cluster address).  Not for maps of several panels.
-__device__ __forceinline__ void copy_panels(const TreeLaunch& p, const KeyRows& k, uint32_t dst, uint32_t bar,
-                                            const CUtensorMap* tc, const CUtensorMap* tb, int panel0, int n,
-                                            int lane) {
+// Where the block size is no multiple of 64: 64 keys by four rows at a time, panels [panel0, panel0 + n)
+// to n consecutive 8 KB panels at dst, completing on `bar` (a shared::cluster address).
+__device__ __forceinline__ void gather_panels(const KeyRows& k, uint32_t dst, uint32_t bar, const CUtensorMap* tc,
+                                              int panel0, int n, int lane) {
+  if (lane >= 16) return;
 #pragma unroll 1
-  for (int i = 0; i < n; ++i) {
-    const int col = (panel0 + i) * 64;
-    if (p.piece_rows > 0) {
-      if (lane * p.piece_rows < 64) tma_load_2d_pair(dst + i * QP + lane * p.piece_rows * 128, tb, bar, col, k.r[0]);
-    } else if (lane < 16) {
-      tma_gather4_pair(dst + i * QP + lane * 4 * 128, tc, bar, col, k.r[0], k.r[1], k.r[2], k.r[3]);
-    }
-  }
-}
-
-// 64 keys x panels panel0 and panel0 + 1 as a product's values: piece by piece, each with both its
-// panels (r rows of 128 bytes, then the other panel's r rows).
-__device__ __forceinline__ void copy_values(const TreeLaunch& p, const KeyRows& k, uint32_t dst, uint32_t bar,
-                                            const CUtensorMap* tc, const CUtensorMap* t2, int panel0, int lane) {
-  if (p.piece_rows > 0) {
-    if (lane * p.piece_rows < 64) tma_load_3d_pair(dst + lane * p.piece_rows * 256, t2, bar, 0, k.r[0], panel0);
-  } else if (lane < 16) {
-#pragma unroll 1
-    for (int i = 0; i < 2; ++i)
-      tma_gather4_pair(dst + i * QP + lane * 4 * 128, tc, bar, (panel0 + i) * 64, k.r[0], k.r[1], k.r[2], k.r[3]);
-  }
+  for (int i = 0; i < n; ++i)
+    tma_gather4_pair(dst + i * QP + lane * 4 * 128, tc, bar, (panel0 + i) * 64, k.r[0], k.r[1], k.r[2], k.r[3]);
 }
 
 // ------------------------------------------------------------------ producers
@@ -147,18 +130,21 @@ __device__ __forceinline__ void settle() {
   }
 }
 
+template <int R>
 __device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, Parts parts, const CUtensorMap* tq,
-                                const CUtensorMap* tc, const CUtensorMap* tb, const CUtensorMap* t3,
-                                volatile int* begun) {
+                                const CUtensorMap* tc, const CUtensorMap* tk, volatile int* begun) {
   const int lane = threadIdx.x & 31;
   const uint32_t qf = mapa_shared(c.bar(QF), 0), kf = mapa_shared(c.bar(KF), 0);
-  const int groups = p.grouped ? KGROUPS : KGROUPS - 1;   // (see run_producer_k_last)
+  // Whole boxes come in three groups, small ones as one ((R == 64 ? KGROUPS : 1)); gather4's last group is another
+  // warp's.
+  const int groups = R > 0 ? (R == 64 ? KGROUPS : 1) : KGROUPS - 1;
+  const int step = R > 0 ? 8 : 0;
   int tiles = 0, units = 0, issued = 0;   // tiles begun, parts, K groups
   bool ok = true;
   Part u;
   while (ok && parts.next(&u)) {
     KeyBlocks blocks{};
-    if (!p.grouped) blocks = find_blocks(p, u, (int64_t)u.lo * KEYS + 64 * c.rank, lane);
+    if (!(R == 64)) blocks = find_blocks(p, u, (int64_t)u.lo * KEYS + 64 * c.rank, step, lane);
     if (lane == 0) {
       if (units > 0) ok = c.wait(QE, (units - 1) & 1);
       if (ok) {
@@ -174,32 +160,36 @@ __device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, Parts parts, 
     for (int t = u.lo; t < u.hi && ok; ++t, ++tiles) {
       const int i = (t - u.lo) & 31;
       const int64_t key0 = (int64_t)t * KEYS + 64 * c.rank;
-      if (i == 0 && p.grouped) ahead = piece_rows(p, u, key0, KEYS, u.hi - t, lane);
+      if (i == 0 && (R == 64)) ahead = piece_rows(p, u, key0, KEYS, u.hi - t, lane);
       const int32_t row = __shfl_sync(0xffffffffu, ahead, i);
       if (lane == 0) *begun = tiles;
-      if (p.grouped) {   // one lane, three copies
+      if ((R == 64)) {   // one lane, three copies
         if (lane == 0) {
 #pragma unroll 1
           for (int g = 0; g < KGROUPS; ++g) {
             if (tiles > 0) ok = c.wait(KE + g, (tiles - 1) & 1);
             if (!ok) break;
             expect_both(c, KF + g, 3 * QP);
-            tma_load_3d_pair(c.sbase + OFF_K + 3 * g * QP, t3, kf + 8 * g, 0, row, 3 * g);
+            tma_load_3d_pair(c.sbase + OFF_K + 3 * g * QP, tk, kf + 8 * g, 0, row, 3 * g);
             ++issued;
           }
         }
       } else {
-        const KeyRows k = find_rows(p, u, blocks, key0, lane);
-        if (t + 1 < u.hi) blocks = find_blocks(p, u, key0 + KEYS, lane);
+        const KeyRows k = find_rows(p, u, blocks, key0, step, lane);
+        if (t + 1 < u.hi) blocks = find_blocks(p, u, key0 + KEYS, step, lane);
 #pragma unroll 1
         for (int g = 0; g < groups; ++g) {
           if (lane == 0) {
             if (tiles > 0) ok = c.wait(KE + g, (tiles - 1) & 1);
-            if (ok) expect_both(c, KF + g, 3 * QP);
+            if (ok) expect_both(c, KF + g, (R > 0 ? NP : 3) * QP);
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) break;
-          copy_panels(p, k, c.sbase + OFF_K + 3 * g * QP, kf + 8 * g, tc, tb, 3 * g, 3, lane);
+          if (R > 0) {
+            if (lane < 8) tma_load_3d_pair(c.sbase + OFF_K + lane * K_ROWS8, tk, kf, 0, k.r[0], 0);
+          } else {
+            gather_panels(k, c.sbase + OFF_K + 3 * g * QP, kf + 8 * g, tc, 3 * g, 3, lane);
+          }
           ++issued;
         }
       }
@@ -220,9 +210,8 @@ __device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, Parts parts, 
   }
 }
 
-// Warp 3 where K comes in many small copies: its last group.
-__device__ void run_producer_k_last(const Ctx& c, const TreeLaunch& p, Parts parts, const CUtensorMap* tc,
-                                    const CUtensorMap* tb) {
+// Warp 3 where K comes by gather4: its last group.
+__device__ void run_producer_k_last(const Ctx& c, const TreeLaunch& p, Parts parts, const CUtensorMap* tc) {
   const int lane = threadIdx.x & 31, g = KGROUPS - 1;
   const uint32_t kf = mapa_shared(c.bar(KF), 0);
   int tiles = 0, issued = 0;
@@ -230,18 +219,18 @@ __device__ void run_producer_k_last(const Ctx& c, const TreeLaunch& p, Parts par
   Part u;
   while (ok && parts.next(&u)) {
     int64_t key0 = (int64_t)u.lo * KEYS + 64 * c.rank;
-    KeyBlocks blocks = find_blocks(p, u, key0, lane);
+    KeyBlocks blocks = find_blocks(p, u, key0, 0, lane);
 #pragma unroll 1
     for (int t = u.lo; t < u.hi && ok; ++t, ++tiles, key0 += KEYS) {
-      const KeyRows k = find_rows(p, u, blocks, key0, lane);
-      if (t + 1 < u.hi) blocks = find_blocks(p, u, key0 + KEYS, lane);
+      const KeyRows k = find_rows(p, u, blocks, key0, 0, lane);
+      if (t + 1 < u.hi) blocks = find_blocks(p, u, key0 + KEYS, 0, lane);
       if (lane == 0) {
         if (tiles > 0) ok = c.wait(KE + g, (tiles - 1) & 1);
         if (ok) expect_both(c, KF + g, 3 * QP);
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
-      copy_panels(p, k, c.sbase + OFF_K + 3 * g * QP, kf + 8 * g, tc, tb, 3 * g, 3, lane);
+      gather_panels(k, c.sbase + OFF_K + 3 * g * QP, kf + 8 * g, tc, 3 * g, 3, lane);
       ++issued;
     }
   }
@@ -251,9 +240,10 @@ __device__ void run_producer_k_last(const Ctx& c, const TreeLaunch& p, Parts par
   }
 }
 
+template <int R>
 __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, Parts parts, const CUtensorMap* tc,
-                               const CUtensorMap* t2, uint8_t* smem) {
-  const int lane = threadIdx.x & 31;
+                               const CUtensorMap* tv, uint8_t* smem) {
+  const int lane = threadIdx.x & 31, panel0 = 4 * (int)c.rank;
   const uint32_t vf = mapa_shared(c.bar(VF), 0);
   int tiles = 0, issued = 0;
   int mends = 0;   // tiles that have a half to mend
@@ -262,92 +252,94 @@ __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, Parts parts, c
   while (ok && parts.next(&u)) {
     int32_t ahead0 = 0, ahead1 = 0;   // rows of 32 tiles' first and second halves
     KeyBlocks b0{}, b1{};
-    if (!p.grouped) {
-      b0 = find_blocks(p, u, (int64_t)u.lo * KEYS, lane);
-      b1 = find_blocks(p, u, (int64_t)u.lo * KEYS + 64, lane);
+    if (!(R == 64)) {
+      b0 = find_blocks(p, u, (int64_t)u.lo * KEYS, R, lane);
+      b1 = find_blocks(p, u, (int64_t)u.lo * KEYS + 64, R, lane);
     }
 #pragma unroll 1
     for (int t = u.lo; t < u.hi && ok; ++t, ++tiles) {
       const int j = (t - u.lo) & 31;
       const int64_t key0 = (int64_t)t * KEYS;
-      if (j == 0 && p.grouped) {
+      if (j == 0 && (R == 64)) {
         ahead0 = piece_rows(p, u, key0, KEYS, u.hi - t, lane);
         ahead1 = piece_rows(p, u, key0 + 64, KEYS, u.hi - t, lane);
       }
       const int32_t row0 = __shfl_sync(0xffffffffu, ahead0, j), row1 = __shfl_sync(0xffffffffu, ahead1, j);
       // The half in which the keys end brings along what lies behind them.
       const int64_t valid = u.q.kv - key0;
-      const bool ends = p.piece_rows > 0 && valid > 0 && valid < KEYS && valid != 64;
-      if (p.grouped && !ends) {   // one lane, four copies
+      const bool ends = R > 0 && valid > 0 && valid < KEYS && valid != 64;
+      if ((R == 64) && !ends) {   // one lane, two copies
         if (lane == 0) {
 #pragma unroll 1
-          for (int i = 0; i < 4; ++i) {   // chunk i / 2, key half i % 2
+          for (int i = 0; i < 2; ++i) {
             if (tiles > 0) ok = c.wait(VE + i, (tiles - 1) & 1);
             if (!ok) break;
-            expect_both(c, VF + i, 2 * QP);
-            tma_load_3d_pair(c.sbase + OFF_V + i * 2 * QP, t2, vf + 8 * i, 0, i & 1 ? row1 : row0,
-                             4 * (i >> 1) + 2 * (int)c.rank);
+            expect_both(c, VF + i, V_HALF);
+            tma_load_3d_pair(c.sbase + OFF_V + i * V_HALF, tv, vf + 8 * i, 0, i ? row1 : row0, panel0);
             ++issued;
           }
         }
       } else {
         KeyRows k0{{row0, 0, 0, 0}}, k1{{row1, 0, 0, 0}};
-        if (!p.grouped) {
-          k0 = find_rows(p, u, b0, key0, lane);
-          k1 = find_rows(p, u, b1, key0 + 64, lane);
+        if (!(R == 64)) {
+          k0 = find_rows(p, u, b0, key0, R, lane);
+          k1 = find_rows(p, u, b1, key0 + 64, R, lane);
           if (t + 1 < u.hi) {
-            b0 = find_blocks(p, u, key0 + KEYS, lane);
-            b1 = find_blocks(p, u, key0 + KEYS + 64, lane);
+            b0 = find_blocks(p, u, key0 + KEYS, R, lane);
+            b1 = find_blocks(p, u, key0 + KEYS + 64, R, lane);
           }
         }
         const int cut = !ends ? 2 : valid < 64 ? 0 : 1;   // the half to mend
 #pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
           if (lane == 0) {
             if (tiles > 0) ok = c.wait(VE + i, (tiles - 1) & 1);
             if (ok) {
-              if ((i & 1) == cut) mbar_arrive_expect_tx(c.bar(LB + (i >> 1)), 2 * QP);
-              else expect_both(c, VF + i, 2 * QP);
+              if (i == cut) mbar_arrive_expect_tx(c.bar(LB), V_HALF);
+              else expect_both(c, VF + i, V_HALF);
             }
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) break;
-          copy_values(p, i & 1 ? k1 : k0, c.sbase + OFF_V + i * 2 * QP,
-                      (i & 1) == cut ? mapa_shared(c.bar(LB + (i >> 1)), c.rank) : vf + 8 * i, tc, t2,
-                      4 * (i >> 1) + 2 * (int)c.rank, lane);
+          const KeyRows& k = i ? k1 : k0;
+          const uint32_t dst = c.sbase + OFF_V + i * V_HALF, bar = i == cut ? mapa_shared(c.bar(LB), c.rank) : vf + 8 * i;
+          if (R > 0) {
+            if (lane * R < 64) tma_load_3d_pair(dst + lane * R * 512, tv, bar, 0, k.r[0], panel0);
+          } else {
+            gather_panels(k, dst, bar, tc, panel0, 4, lane);
+          }
           ++issued;
         }
         // What came along behind the last key is made zero (its P is 0, but 0 times what is there need
         // not be).  Each CTA sees to its own, then the even one says that the half is there.
-#pragma unroll 1
-        for (int j2 = 0; j2 < 2 && ends && ok; ++j2) {
-          if (lane == 0) ok = c.wait(LB + j2, mends & 1);
+        if (ends && ok) {
+          if (lane == 0) ok = c.wait(LB, mends & 1);
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) break;
-          uint8_t* at = smem + OFF_V + (2 * j2 + cut) * 2 * QP;
-          const int low = p.piece_rows - 1;   // (a power of two less one)
-          for (int k = lane; k < (64 - (int)(valid & 63)) * 16; k += 32) {
-            const int row = (int)(valid & 63) + (k >> 4);
-            *reinterpret_cast<uint4*>(at + (2 * (row & ~low) + (k & 8 ? low + 1 : 0) + (row & low)) * 128 +
-                                      (k & 7) * 16) = make_uint4(0, 0, 0, 0);
+          uint8_t* at = smem + OFF_V + cut * V_HALF;
+          const int low = R - 1;   // (a power of two less one)
+          for (int k = lane; k < (64 - (int)(valid & 63)) * 32; k += 32) {
+            const int row = (int)(valid & 63) + (k >> 5), panel = (k >> 3) & 3;
+            *reinterpret_cast<uint4*>(at + (4 * (row & ~low) + panel * (low + 1) + (row & low)) * 128 + (k & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
           }
           fence_async_shared();
           __syncwarp();
           if (lane == 0) {
-            if (c.rank != 0) mbar_arrive_remote(mapa_shared(c.bar(ZB + j2), 0));
-            else if ((ok = c.wait(ZB + j2, mends & 1))) mbar_arrive(c.bar(VF + 2 * j2 + cut));
+            if (c.rank != 0) mbar_arrive_remote(mapa_shared(c.bar(ZB), 0));
+            else if ((ok = c.wait(ZB, mends & 1))) mbar_arrive(c.bar(VF + cut));
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
+          ++mends;
         }
-        if (ends) ++mends;
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
     }
   }
   if (lane == 0) {
     if (c.rank == 0) {
-      for (int i = 0; i < 4; ++i) {
-        const int n = (issued + 3 - i) / 4;
+      for (int i = 0; i < 2; ++i) {
+        const int n = (issued + 1 - i) / 2;
         if (n) c.drain(VF + i, (n - 1) & 1);
       }
     }
@@ -411,16 +403,18 @@ __device__ __forceinline__ void commit_both(uint32_t bar) {
       : "memory");
 }
 
+template <int R>
 __device__ void run_mma(const Ctx& c, const TreeLaunch& p, Parts parts, uint32_t tmem) {
   const uint64_t q_desc = sdesc_sw128(c.sbase + OFF_Q, 16, 1024);
-  const uint64_t k_desc = sdesc_sw128(c.sbase + OFF_K, 16, 1024);
-  // Values lie in pieces of r keys, each with both its panels: 16 keys of a product are part of one
+  // K lies in panels of 64 rows, or eight rows at a time with all their panels.
+  constexpr bool rows8 = R > 0 && R < 64;
+  const uint64_t k_desc = sdesc_sw128(c.sbase + OFF_K, 16, rows8 ? K_ROWS8 : 1024);
+  constexpr uint32_t k_panel = (rows8 ? 1024 : QP) >> 4;
+  // Values lie in pieces of r keys, each with its four panels: 16 keys of a product are part of one
   // piece, a whole one or two.
-  const int r = p.piece_rows > 0 ? p.piece_rows : 64;
-  const uint64_t v_desc = sdesc_sw128(c.sbase + OFF_V, r * 128, r == 8 ? 2048 : 1024);
-  uint32_t v_step[4];
-#pragma unroll
-  for (int kk = 0; kk < 4; ++kk) v_step[kk] = (uint32_t)((kk * 16 / r) * 2 * r + kk * 16 % r) * 128 >> 4;
+  constexpr int r = R > 0 ? R : 64;
+  const uint64_t v_desc = sdesc_sw128(c.sbase + OFF_V, r * 128, r == 8 ? 4096 : 1024);
+  constexpr uint32_t v_chunk = (uint32_t)(2 * r * 128) >> 4;
   const uint64_t p_desc = sdesc_sw128(c.sbase + OFF_P, 16, 1024);
   bool ok = true;
   if (p.force_timeout) ok = c.wait_warp(NEVER, 0);
@@ -439,10 +433,10 @@ __device__ void run_mma(const Ctx& c, const TreeLaunch& p, Parts parts, uint32_t
     seen_k = 0;
 #pragma unroll 1
     for (int g = 0; g < KGROUPS; ++g) {
-      if (!c.wait_warp(KF + g, st & 1, seen)) return false;
+      if ((g == 0 || !rows8) && !c.wait_warp(KF + g, st & 1, seen)) return false;
       tc_fence_after();
       if (g + 1 < KGROUPS) {
-        seen = c.look(KF + g + 1, st & 1);
+        if (!rows8) seen = c.look(KF + g + 1, st & 1);
       } else {   // the P V that follows
         seen_p = c.look(PR, pv & 1);
         seen_v = c.look(VF, pv & 1);
@@ -451,12 +445,13 @@ __device__ void run_mma(const Ctx& c, const TreeLaunch& p, Parts parts, uint32_t
       for (int i = 3 * g; i < 3 * g + 3; ++i) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-          const uint64_t off = (uint64_t)((i * QP + kk * 32) >> 4);
-          issue(d, q_desc + off, k_desc + off, IDESC_QK, kk > 0 ? 1u : i > 0 ? 1u : 0u);
+          const uint64_t qo = (uint64_t)((i * QP + kk * 32) >> 4), ko = (uint64_t)(i * k_panel + (kk * 32 >> 4));
+          issue(d, q_desc + qo, k_desc + ko, IDESC_QK, kk > 0 ? 1u : i > 0 ? 1u : 0u);
         }
       }
-      commit_both(c.bar(KE + g));
+      if (!rows8) commit_both(c.bar(KE + g));
     }
+    if (rows8) commit_both(c.bar(KE));
     commit_both(c.bar(SF + b));
     if (last) commit_both(c.bar(QE));
     ++st;
@@ -469,16 +464,19 @@ __device__ void run_mma(const Ctx& c, const TreeLaunch& p, Parts parts, uint32_t
     if (!c.wait_warp(PR, t & 1, seen_p)) return false;
     seen_p = seen_v = 0;
 #pragma unroll 1
-    for (int i = 0; i < 4; ++i) {   // chunk i / 2, key half i % 2
+    for (int i = 0; i < 2; ++i) {   // halves of the keys
       if (!c.wait_warp(VF + i, t & 1, seen)) return false;
       tc_fence_after();
-      if (i < 3) seen = c.look(VF + i + 1, t & 1);
+      if (i == 0) seen = c.look(VF + 1, t & 1);
       else if (s_next) seen_k = c.look(KF, st & 1);
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        const uint64_t po = (uint64_t)(((i & 1) * QP + kk * 32) >> 4);
-        const uint64_t vo = (uint64_t)(i * 2 * QP >> 4) + v_step[kk];
-        issue(tmem + TM_O(i >> 1), p_desc + po, v_desc + vo, IDESC_PV, kk > 0 ? 1u : (i & 1) ? 1u : more);
+      for (int ch = 0; ch < 2; ++ch) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint64_t po = (uint64_t)((i * QP + kk * 32) >> 4);
+          const uint64_t vo = (uint64_t)(i * V_HALF >> 4) + ch * v_chunk + (((kk * 16 / r) * 4 * r + kk * 16 % r) * 128 >> 4);
+          issue(tmem + TM_O(ch), p_desc + po, v_desc + vo, IDESC_PV, kk > 0 ? 1u : i ? 1u : more);
+        }
       }
       commit_both(c.bar(VE + i));
     }
@@ -650,8 +648,8 @@ __device__ void run_softmax(const Ctx& c, const TreeLaunch& p, Parts parts, uint
     char* slot = ws_slots + (size_t)u.slot * SLOT_BYTES;
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
-      // TMEM columns 64 q ..: value columns 256 (q / 2) + 128 half + 64 (q % 2) ..
-      const int col = 256 * (q >> 1) + 128 * half + 64 * (q & 1);
+      // TMEM columns 64 q ..: the values of CTA `half`, chunk q / 2 of 128
+      const int col = 256 * half + 64 * q;
       uint32_t ov[64];
       tmem_ld64_sync(lane_addr + q * 64, ov);
       if (!live) continue;
@@ -690,10 +688,12 @@ __device__ void run_softmax(const Ctx& c, const TreeLaunch& p, Parts parts, uint
   }
 }
 
+// R: rows of a box of the cache (8, 16, 32, 64), 0: by gather4.
+template <int R>
 __global__ void __launch_bounds__(NTHREADS, 1)
 tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_c,
-                 const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_2,
-                 const __grid_constant__ CUtensorMap tm_3, const __grid_constant__ TreeLaunch p) {
+                 const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                 const __grid_constant__ TreeLaunch p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ StartRec start;
   __shared__ int64_t count;
@@ -718,9 +718,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tm_q);
-    tma_prefetch_desc(&tm_c);
-    if (p.piece_rows > 0) tma_prefetch_desc(&tm_2);
-    tma_prefetch_desc(p.grouped ? &tm_3 : &tm_b);
+    tma_prefetch_desc(R > 0 ? &tm_k : &tm_c);
+    if (R > 0) tma_prefetch_desc(&tm_v);
   }
   if (warp == 3) {   // one warp of each CTA of the pair, together
     tmem_alloc_pair(smem_addr(tmem_slot), TMEM_COLS);
@@ -737,14 +736,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const Parts parts(p.t, start, count);
   if (warp == 0) {
-    run_producer_qk(c, p, parts, &tm_q, &tm_c, &tm_b, &tm_3, begun);
+    run_producer_qk<R>(c, p, parts, &tm_q, &tm_c, &tm_k, begun);
   } else if (warp == 2) {
-    run_producer_v(c, p, parts, &tm_c, &tm_2, smem);
+    run_producer_v<R>(c, p, parts, &tm_c, &tm_v, smem);
   } else if (warp == 1) {
-    if (rank == 0) run_mma(c, p, parts, tmem);
+    if (rank == 0) run_mma<R>(c, p, parts, tmem);
   } else if (warp == 3) {
-    if (p.grouped) run_prefetch(c, p, parts, &tm_3, begun);
-    else run_producer_k_last(c, p, parts, &tm_c, &tm_b);
+    if constexpr (R == 64) run_prefetch(c, p, parts, &tm_k, begun);
+    else if constexpr (R == 0) run_producer_k_last(c, p, parts, &tm_c);
   } else {
     run_softmax(c, p, parts, tmem, ws + WS_SLOTS + (size_t)worker * 2 * SLOT_BYTES, smem);
   }
@@ -776,18 +775,32 @@ cudaLaunchConfig_t pair_config(cudaLaunchAttribute* attr, int workers, cudaStrea
   return cfg;
 }
 
+using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap, const TreeLaunch);
+Kernel kernel_of(int box_rows) {
+  switch (box_rows) {
+    case 8: return tree_attn_kernel<8>;
+    case 16: return tree_attn_kernel<16>;
+    case 32: return tree_attn_kernel<32>;
+    case 64: return tree_attn_kernel<64>;
+    default: return tree_attn_kernel<0>;
+  }
+}
+
 // Clusters that run at once on the current device (0 on error).
 int max_workers() {
   static PerDeviceOnce configured;
   static int workers[PerDeviceOnce::kMaxDevices] = {};
   const cudaError_t e = configured.run([] {
-    cudaError_t r = cudaFuncSetAttribute(tree_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    cudaError_t r = cudaSuccess;
+    for (int rows : {0, 8, 16, 32, 64})
+      if (r == cudaSuccess)
+        r = cudaFuncSetAttribute(kernel_of(rows), cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     int dev = 0, n = 0;
     if (r == cudaSuccess) r = cudaGetDevice(&dev);
     if (r != cudaSuccess) return r;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = pair_config(attr, 1, nullptr);
-    r = cudaOccupancyMaxActiveClusters(&n, tree_attn_kernel, &cfg);
+    r = cudaOccupancyMaxActiveClusters(&n, kernel_of(64), &cfg);
     if (r == cudaSuccess) workers[dev] = n < MAX_WORKERS ? n : MAX_WORKERS;
     return r;
   });
@@ -811,38 +824,35 @@ cudaError_t launch_tree_attention(const TreeParams& t, cudaStream_t stream) {
   const bool any = t.max_blocks > 0;   // some cache row may be read
   const int bs = t.block_size;
   const uint64_t slots = any ? (uint64_t)t.num_blocks * (uint64_t)bs : 1;
-  CUtensorMap tq, tc, tb, t2, t3;
+  CUtensorMap tq, tc, tk, tv;
   {
     const uint64_t dims[3] = {64, (uint64_t)t.total_rows * (uint64_t)t.num_heads, NP}, strides[2] = {576 * 2, 64 * 2};
     const uint32_t box[3] = {64, 64, NP};   // 64 rows, panel by panel
     if (make_tensor_map_bf16(&tq, t.q, 3, dims, strides, box) != MLA_OK) return cudaErrorInvalidValue;
   }
   const void* rows = any ? static_cast<const void*>(t.cache) : t.q;   // a map needs a valid base
-  {
-    const uint64_t dims[2] = {576, slots}, strides[1] = {576 * 2};
-    const uint32_t box[2] = {64, 1};   // one row high: rows are fetched four at a time by gather4
-    if (make_tensor_map_bf16(&tc, rows, 2, dims, strides, box) != MLA_OK) return cudaErrorInvalidValue;
-  }
   // Boxes for 64-key pieces: one when the block size is a multiple of 64, 64 / block_size when
   // it is 8, 16 or 32 (8 rows keep a box on the swizzle's 1024-byte period); several panels in
-  // one box by a map of the rows as {64 columns, rows, 9 column groups}.
-  p.piece_rows = !any ? 0 : (bs % 64 == 0) ? 64 : (bs % 8 == 0 && 64 % bs == 0) ? bs : 0;
-  p.grouped = p.piece_rows == 64;
+  // one box by a map of the rows as {64 columns, rows, 9 column groups}.  Small blocks' keys come eight
+  // rows at a time with all nine panels (8 copies where {64 columns, 16 rows} took 36), their values
+  // with four.
+  const int box_rows = !any ? 0 : (bs % 64 == 0) ? 64 : (bs % 8 == 0 && 64 % bs == 0) ? bs : 0;
   p.block_shift = -1;
   for (int i = 0; i < 31; ++i)
     if (bs == 1 << i) p.block_shift = i;
-  tb = t2 = t3 = tc;
-  if (p.piece_rows > 0) {
-    const uint64_t dims[2] = {576, slots}, strides[1] = {576 * 2};
-    const uint32_t box[2] = {64, (uint32_t)p.piece_rows};
-    if (make_tensor_map_bf16(&tb, rows, 2, dims, strides, box) != MLA_OK) return cudaErrorInvalidValue;
-  }
-  if (p.piece_rows > 0) {
+  if (box_rows > 0) {
     const uint64_t dims[3] = {64, slots, NP}, strides[2] = {576 * 2, 64 * 2};
-    const uint32_t box2[3] = {64, (uint32_t)p.piece_rows, 2}, box3[3] = {64, 64, 3};
-    if (make_tensor_map_bf16(&t2, rows, 3, dims, strides, box2) != MLA_OK ||
-        (p.grouped && make_tensor_map_bf16(&t3, rows, 3, dims, strides, box3) != MLA_OK))
+    const uint32_t box_k[3] = {64, box_rows == 64 ? 64u : 8u, box_rows == 64 ? 3u : (uint32_t)NP};
+    const uint32_t box_v[3] = {64, (uint32_t)box_rows, 4};
+    if (make_tensor_map_bf16(&tk, rows, 3, dims, strides, box_k) != MLA_OK ||
+        make_tensor_map_bf16(&tv, rows, 3, dims, strides, box_v) != MLA_OK)
       return cudaErrorInvalidValue;
+    tc = tk;   // (not used)
+  } else {
+    const uint64_t dims[2] = {576, slots}, strides[1] = {576 * 2};
+    const uint32_t box[2] = {64, 1};   // one row high: rows are fetched four at a time by gather4
+    if (make_tensor_map_bf16(&tc, rows, 2, dims, strides, box) != MLA_OK) return cudaErrorInvalidValue;
+    tk = tv = tc;
   }
   p.oob_row = (int32_t)slots;
   p.o_align32 = (reinterpret_cast<uintptr_t>(t.o) & 31u) == 0;
@@ -856,7 +866,7 @@ cudaError_t launch_tree_attention(const TreeParams& t, cudaStream_t stream) {
   p.wait_limit_ns = forced ? forced : kWaitLimitNs;
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = pair_config(attr, p.workers, stream);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_attn_kernel, tq, tc, tb, t2, t3, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel_of(box_rows), tq, tc, tk, tv, p);
   return e != cudaSuccess ? e : launch_tree_join(p, stream);
 }
 
