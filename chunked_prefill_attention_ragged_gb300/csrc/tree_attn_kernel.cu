@@ -135,16 +135,15 @@ __device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, Parts parts, 
                                 const CUtensorMap* tc, const CUtensorMap* tk, volatile int* begun) {
   const int lane = threadIdx.x & 31;
   const uint32_t qf = mapa_shared(c.bar(QF), 0), kf = mapa_shared(c.bar(KF), 0);
-  // Whole boxes come in three groups, small ones as one ((R == 64 ? KGROUPS : 1)); gather4's last group is another
-  // warp's.
-  const int groups = R > 0 ? (R == 64 ? KGROUPS : 1) : KGROUPS - 1;
-  const int step = R > 0 ? 8 : 0;
+  // Whole boxes come in three groups, small ones as one; gather4's last group is another warp's.
+  constexpr int groups = R == 64 ? KGROUPS : R > 0 ? 1 : KGROUPS - 1;
+  constexpr int step = R > 0 ? 8 : 0;
   int tiles = 0, units = 0, issued = 0;   // tiles begun, parts, K groups
   bool ok = true;
   Part u;
   while (ok && parts.next(&u)) {
     KeyBlocks blocks{};
-    if (!(R == 64)) blocks = find_blocks(p, u, (int64_t)u.lo * KEYS + 64 * c.rank, step, lane);
+    if (R != 64) blocks = find_blocks(p, u, (int64_t)u.lo * KEYS + 64 * c.rank, step, lane);
     if (lane == 0) {
       if (units > 0) ok = c.wait(QE, (units - 1) & 1);
       if (ok) {
@@ -160,10 +159,10 @@ __device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, Parts parts, 
     for (int t = u.lo; t < u.hi && ok; ++t, ++tiles) {
       const int i = (t - u.lo) & 31;
       const int64_t key0 = (int64_t)t * KEYS + 64 * c.rank;
-      if (i == 0 && (R == 64)) ahead = piece_rows(p, u, key0, KEYS, u.hi - t, lane);
+      if (i == 0 && R == 64) ahead = piece_rows(p, u, key0, KEYS, u.hi - t, lane);
       const int32_t row = __shfl_sync(0xffffffffu, ahead, i);
       if (lane == 0) *begun = tiles;
-      if ((R == 64)) {   // one lane, three copies
+      if (R == 64) {   // one lane, three copies
         if (lane == 0) {
 #pragma unroll 1
           for (int g = 0; g < KGROUPS; ++g) {
@@ -252,7 +251,7 @@ __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, Parts parts, c
   while (ok && parts.next(&u)) {
     int32_t ahead0 = 0, ahead1 = 0;   // rows of 32 tiles' first and second halves
     KeyBlocks b0{}, b1{};
-    if (!(R == 64)) {
+    if (R != 64) {
       b0 = find_blocks(p, u, (int64_t)u.lo * KEYS, R, lane);
       b1 = find_blocks(p, u, (int64_t)u.lo * KEYS + 64, R, lane);
     }
@@ -260,7 +259,7 @@ __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, Parts parts, c
     for (int t = u.lo; t < u.hi && ok; ++t, ++tiles) {
       const int j = (t - u.lo) & 31;
       const int64_t key0 = (int64_t)t * KEYS;
-      if (j == 0 && (R == 64)) {
+      if (j == 0 && R == 64) {
         ahead0 = piece_rows(p, u, key0, KEYS, u.hi - t, lane);
         ahead1 = piece_rows(p, u, key0 + 64, KEYS, u.hi - t, lane);
       }
@@ -268,7 +267,7 @@ __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, Parts parts, c
       // The half in which the keys end brings along what lies behind them.
       const int64_t valid = u.q.kv - key0;
       const bool ends = R > 0 && valid > 0 && valid < KEYS && valid != 64;
-      if ((R == 64) && !ends) {   // one lane, two copies
+      if (R == 64 && !ends) {   // one lane, two copies
         if (lane == 0) {
 #pragma unroll 1
           for (int i = 0; i < 2; ++i) {
@@ -281,7 +280,7 @@ __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, Parts parts, c
         }
       } else {
         KeyRows k0{{row0, 0, 0, 0}}, k1{{row1, 0, 0, 0}};
-        if (!(R == 64)) {
+        if (R != 64) {
           k0 = find_rows(p, u, b0, key0, R, lane);
           k1 = find_rows(p, u, b1, key0 + 64, R, lane);
           if (t + 1 < u.hi) {
@@ -347,29 +346,30 @@ __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, Parts parts, c
   }
 }
 
-// Warp 3 where K comes in whole boxes: this CTA's keys of the tile after the one being loaded, into
+// Warp 3 where K comes by boxes: this CTA's keys of the tile after the one being loaded, into
 // L2.  The one-tile buffers leave a load less than a tile's time, which DRAM does not keep to: with
 // the rows in L2 it does.  It follows the K producer's count of tiles, which only grows (on a
 // barrier's phases a warp that fell two tiles behind would wait for one that never comes), and gives
 // up quietly.
-__device__ void run_prefetch(const Ctx& c, const TreeLaunch& p, Parts parts, const CUtensorMap* t3,
+template <int R>
+__device__ void run_prefetch(const Ctx& c, const TreeLaunch& p, Parts parts, const CUtensorMap* tk,
                              const volatile int* begun) {
   const int lane = threadIdx.x & 31;
   int tiles = 0;
   Part u;
   while (parts.next(&u)) {
     for (int t = u.lo; t < u.hi; ++t, ++tiles) {
-      const int64_t key = (int64_t)(t + 1) * KEYS + 64 * c.rank;
+      const int64_t key = (int64_t)(t + 1) * KEYS + 64 * c.rank + (R < 64 ? 8 * lane : 0);
       const uint64_t t0 = global_timer_ns();
       while (*begun < tiles) {   // tile t is not being loaded yet
         __nanosleep(200);
         if (*c.abort_flag || global_timer_ns() - t0 > p.wait_limit_ns) return;
       }
       __syncwarp();
-      if (t + 1 < u.hi && key + 64 <= u.q.kv && lane == 0) {
+      if (t + 1 < u.hi && lane < (R < 64 ? 8 : 1) && key + (R < 64 ? 8 : 64) <= u.q.kv) {
         const int32_t row = block_row(p, table_block(p, u, key), key);
 #pragma unroll 1
-        for (int g = 0; g < KGROUPS; ++g) tma_prefetch_3d(t3, 0, row, 3 * g);
+        for (int g = 0; g < (R < 64 ? 1 : KGROUPS); ++g) tma_prefetch_3d(tk, 0, row, 3 * g);
       }
     }
   }
@@ -742,8 +742,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   } else if (warp == 1) {
     if (rank == 0) run_mma<R>(c, p, parts, tmem);
   } else if (warp == 3) {
-    if constexpr (R == 64) run_prefetch(c, p, parts, &tm_k, begun);
-    else if constexpr (R == 0) run_producer_k_last(c, p, parts, &tm_c);
+    if constexpr (R > 0) run_prefetch<R>(c, p, parts, &tm_k, begun);
+    else run_producer_k_last(c, p, parts, &tm_c);
   } else {
     run_softmax(c, p, parts, tmem, ws + WS_SLOTS + (size_t)worker * 2 * SLOT_BYTES, smem);
   }
