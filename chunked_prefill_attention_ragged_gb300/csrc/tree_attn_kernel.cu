@@ -309,15 +309,16 @@ __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, Parts parts, c
           }
           ++issued;
         }
-        // What came along behind the last key is made zero (its P is 0, but 0 times what is there need
-        // not be).  Each CTA sees to its own, then the even one says that the half is there.
+        // What came along behind the last key, as far as products read (16 keys at a time), is made zero
+        // (its P is 0, but 0 times what is there need not be).  Each CTA sees to its own, then the even
+        // one says that the half is there.
         if (ends && ok) {
           if (lane == 0) ok = c.wait(LB, mends & 1);
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) break;
           uint8_t* at = smem + OFF_V + cut * V_HALF;
           const int low = R - 1;   // (a power of two less one)
-          for (int k = lane; k < (64 - (int)(valid & 63)) * 32; k += 32) {
+          for (int k = lane; k < (-(int)valid & 15) * 32; k += 32) {
             const int row = (int)(valid & 63) + (k >> 5), panel = (k >> 3) & 3;
             *reinterpret_cast<uint4*>(at + (4 * (row & ~low) + panel * (low + 1) + (row & low)) * 128 + (k & 7) * 16) =
                 make_uint4(0, 0, 0, 0);
@@ -366,7 +367,7 @@ __device__ void run_prefetch(const Ctx& c, const TreeLaunch& p, Parts parts, con
         if (*c.abort_flag || global_timer_ns() - t0 > p.wait_limit_ns) return;
       }
       __syncwarp();
-      if (t + 1 < u.hi && lane < (R < 64 ? 8 : 1) && key + (R < 64 ? 8 : 64) <= u.q.kv) {
+      if (t + 1 < u.hi && lane < (R < 64 ? 8 : 1) && key < u.q.kv) {
         const int32_t row = block_row(p, table_block(p, u, key), key);
 #pragma unroll 1
         for (int g = 0; g < (R < 64 ? 1 : KGROUPS); ++g) tma_prefetch_3d(tk, 0, row, 3 * g);
@@ -457,7 +458,8 @@ __device__ void run_mma(const Ctx& c, const TreeLaunch& p, Parts parts, uint32_t
     ++st;
     return true;
   };
-  auto pv_products = [&](uint32_t add, bool s_next) {   // add: 0 for a part's first tile
+  // add: 0 for a part's first tile; keys: up to which of the tile's
+  auto pv_products = [&](uint32_t add, int keys, bool s_next) {
     const int t = pv;
     const uint32_t more = __shfl_sync(0xffffffffu, add, 0);
     uint32_t seen = seen_v;
@@ -473,6 +475,7 @@ __device__ void run_mma(const Ctx& c, const TreeLaunch& p, Parts parts, uint32_t
       for (int ch = 0; ch < 2; ++ch) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
+          if (kk > 0 && 64 * i + 16 * kk >= keys) break;
           const uint64_t po = (uint64_t)((i * QP + kk * 32) >> 4);
           const uint64_t vo = (uint64_t)(i * V_HALF >> 4) + ch * v_chunk + (((kk * 16 / r) * 4 * r + kk * 16 % r) * 128 >> 4);
           issue(tmem + TM_O(ch), p_desc + po, v_desc + vo, IDESC_PV, kk > 0 ? 1u : i ? 1u : more);
@@ -492,10 +495,11 @@ __device__ void run_mma(const Ctx& c, const TreeLaunch& p, Parts parts, uint32_t
     for (int t = 0; t < n && ok; ++t) {
       // S's buffer held P V(pv - 2)'s scores, read before that tile's P was ready.
       ok = s_products(t == n - 1);
-      if (ok && t > 0) ok = pv_products(t > 1 ? 1u : 0u, t < n - 1);
+      if (ok && t > 0) ok = pv_products(t > 1 ? 1u : 0u, KEYS, t < n - 1);
     }
     // (The next part's Q and keys come later than this one's last P: its S first was no faster.)
-    if (ok) ok = pv_products(n > 1 ? 1u : 0u, false);
+    const int keys = __shfl_sync(0xffffffffu, (int)min((int64_t)KEYS, u.q.kv - (int64_t)(u.hi - 1) * KEYS), 0);
+    if (ok) ok = pv_products(n > 1 ? 1u : 0u, keys, false);
   }
   commit_both(c.bar(FIN));
   c.drain(FIN, 0);
