@@ -253,6 +253,11 @@ __device__ __forceinline__ uint64_t visible(const TreeParams& p, const Part& u, 
   return v;
 }
 
+// Quotients whose terms nearly always have 32 bits: the long division is a call of its own.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {   // 0 <= a, 0 < b
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // Where worker w's piece starts and how long it is, and what is to be joined at its start; every
 // thread of the CTA calls, with the words of request threadIdx.x, loaded before.
 template <int NTHREADS>
@@ -281,7 +286,9 @@ __device__ __forceinline__ void find_piece(const TreeParams& p, const ReqWords& 
     total += warp_sum[w];
   }
   const int n = (int)min((int64_t)workers, total);   // a tile is worth a worker
-  auto at = [&](int w) { return total * w / n; };
+  // The first `more` workers have a tile more than the others.
+  const int64_t each = n > 0 ? quotient(total, n) : 0, more = total - each * n;
+  auto at = [&](int w) { return each * w + min((int64_t)w, more); };
   const int64_t lo = worker < n ? at(worker) : total, hi = worker < n ? at(worker + 1) : total;
   if (tid == 0) *count = hi - lo;
   if (tid == 0 && lo >= hi) *join = JoinRec{0, 0, 0, 0, {}};
@@ -291,13 +298,14 @@ __device__ __forceinline__ void find_piece(const TreeParams& p, const ReqWords& 
       const Req q = per == 1 ? make_req(p, own, false) : load_req(p, r, false);
       const int64_t k = (int64_t)q.units * q.tiles;
       if (lo < sum + k) {
-        const int unit = (int)((lo - sum) / q.tiles), tile = (int)((lo - sum) % q.tiles);
+        const int unit = (int)quotient(lo - sum, q.tiles), tile = (int)(lo - sum - (int64_t)unit * q.tiles);
         *start = StartRec{r, unit, tile, q};
         JoinRec j{0, 0, 0, 0, {}};
         const int64_t first = lo - tile, prev = worker > 0 ? at(worker - 1) : 0;   // the unit's first tile
         if (tile > 0 && prev <= first) {
-          // The last worker with a part: at(w) < first + tiles, i.e. total * w / n < first + tiles.
-          const int last = (int)min((int64_t)(n - 1), ((first + q.tiles) * n - 1) / total);
+          // The last worker with a part is the one that has the unit's last tile.
+          const int64_t end = first + q.tiles - 1, big = more * (each + 1);
+          const int last = (int)(end < big ? quotient(end, each + 1) : more + quotient(end - big, each));
           j.pair0 = (int64_t)q.q0 * p.num_heads + (int64_t)unit * TREE_ROWS;
           j.npairs = (int)min((int64_t)TREE_ROWS, (int64_t)q.nodes * p.num_heads - (int64_t)unit * TREE_ROWS);
           j.parts = last - worker + 2;

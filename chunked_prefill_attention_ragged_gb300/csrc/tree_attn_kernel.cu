@@ -712,12 +712,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   const Ctx c{smem_addr(smem), abort_flag, p.t.status, p.wait_limit_ns, rank};
   ReqWords words{0, 0, 0};   // (on their way while the barriers are made)
   if ((int)threadIdx.x < p.t.batch) words = load_words(p.t, threadIdx.x);
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < NBAR; ++i) mbar_init(c.bar(i), 1);
-    for (int i = 0; i < 2; ++i) mbar_init(c.bar(XB + i), 2);      // the two warps of 32 rows
-    mbar_init(c.bar(PR), 8);                                        // every softmax warp, of both CTAs
-    *abort_flag = 0;
-    *begun = -1;
+  if (warp == 1) {
+    // P: every softmax warp of both CTAs; maxima: the two warps of 32 rows.
+    static_assert(NBAR <= 32, "a lane each");
+    if (lane < NBAR) mbar_init(c.bar(lane), lane == PR ? 8 : lane == XB || lane == XB + 1 ? 2 : 1);
+    if (lane == 0) {
+      *abort_flag = 0;
+      *begun = -1;
+    }
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
@@ -731,7 +733,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   }
   __syncwarp();
   tc_fence_before();
-  cluster_arrive();   // both CTAs' barriers exist, TMEM is there: waited for below
+  // Both CTAs' barriers exist, TMEM is there: waited for below.  (A release waits for the lengths' loads.)
+  if (warp == 3) cluster_arrive();
+  else cluster_arrive_relaxed();
   find_piece<NTHREADS>(p.t, words, worker, p.workers, blockIdx.x == 0, &start, &count, &join);
   char* ws = static_cast<char*>(p.t.workspace);
   if (threadIdx.x == 0 && rank == 0) reinterpret_cast<JoinRec*>(ws)[worker] = join;
