@@ -461,7 +461,8 @@ MLA_API int mla_tree_workspace(int64_t total_rows, int num_heads, int64_t* bytes
  * see may still reach the other rows of its request.  MLA_DEVSTAT_BAD_INDEX is OR-ed in for a
  * block id outside [0, num_blocks) (its rows read as zeros), kv_len outside
  * [0, max_blocks_per_req * block_size] (clamped), or a request whose rows are not inside
- * total_rows (skipped); MLA_DEVSTAT_TIMEOUT when a pipeline wait gave up.
+ * total_rows (skipped); MLA_DEVSTAT_TIMEOUT when a pipeline wait gave up (after 2 s, or in the test
+ * mode of MLA_TEST_FORCE_TIMEOUT_NS, see mla_prefill_plan, which is read at every call here).
  * Needs num_blocks * block_size < 2^31 - 1 and total_rows * num_heads <= 2^31 - 256.
  * Allocates nothing, does not synchronise; results do not depend on timing.
  */
