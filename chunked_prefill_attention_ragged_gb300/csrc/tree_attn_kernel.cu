@@ -30,8 +30,8 @@
 //   warps 4-7  softmax: two threads per pair (the two halves of the keys and of O's columns)
 // Order of products: S(t + 1) before P V(t), so that the tensor cores work on the next tile while
 // the softmax does this one.  Key rows come by whole boxes of 64 where the block size is a multiple
-// of that, by smaller boxes where it is 8, 16 or 32 (in the piece where the keys end, what lies behind
-// them is made zero), else by gather4 with rows past the end read as zeros.  The kernel is compiled
+// of that, by boxes of 32, 16 or 8 where it is one of these (in the piece where the keys end, what lies
+// behind them is made zero), else by gather4 with rows past the end read as zeros.  The kernel is compiled
 // for each: with strides of the operands read from registers the products' issue took 3% longer.
 // What bounds it: for one node a request HBM (64 requests over 4096 positions, 16 heads: 66.5 us with the
 // join, 6 TB/s while tiles run); for many the products and what feeds them (32 x 16 nodes over 8192, 128
@@ -844,12 +844,13 @@ cudaError_t launch_tree_attention(const TreeParams& t, cudaStream_t stream) {
     if (make_tensor_map_bf16(&tq, t.q, 3, dims, strides, box) != MLA_OK) return cudaErrorInvalidValue;
   }
   const void* rows = any ? static_cast<const void*>(t.cache) : t.q;   // a map needs a valid base
-  // Boxes for 64-key pieces: one when the block size is a multiple of 64, 64 / block_size when
-  // it is 8, 16 or 32 (8 rows keep a box on the swizzle's 1024-byte period); several panels in
-  // one box by a map of the rows as {64 columns, rows, 9 column groups}.  Small blocks' keys come eight
+  // Boxes for 64-key pieces: of as many rows, 64 to 8, as the block size is a multiple of (8 rows keep a
+  // box on the swizzle's 1024-byte period; by gather4 blocks of 24, 48 and 96 took 235 us where they
+  // take 85, 16 requests of 4 nodes, 128 heads, over 4096); several panels in
+  // one box by a map of the rows as {64 columns, rows, 9 column groups}.  Smaller boxes' keys come eight
   // rows at a time with all nine panels (8 copies where {64 columns, 16 rows} took 36), their values
   // with four.
-  const int box_rows = !any ? 0 : (bs % 64 == 0) ? 64 : (bs % 8 == 0 && 64 % bs == 0) ? bs : 0;
+  const int box_rows = !any ? 0 : bs % 64 == 0 ? 64 : bs % 32 == 0 ? 32 : bs % 16 == 0 ? 16 : bs % 8 == 0 ? 8 : 0;
   p.block_shift = -1;
   for (int i = 0; i < 31; ++i)
     if (bs == 1 << i) p.block_shift = i;

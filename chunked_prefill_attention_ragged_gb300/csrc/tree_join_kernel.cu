@@ -7,10 +7,11 @@ namespace mla {
 namespace {
 
 // A CTA has 32 rows of a unit that a boundary between two workers cuts (the unit's first such
-// boundary) and 128 of the columns, a thread a row and 16 columns: two 32-byte groups of a part, whose
+// boundary) and 64 of the columns, a thread a row and 16 columns: two 32-byte groups of a part, whose
 // rows lie one behind the other.  Bound by latency: record, (m, l), result, each waits for the one
-// before, with O's loads under way beside the weights'.
-constexpr int JOIN_WARPS = 8, JOIN_COLS = 16;
+// before, with O's loads under way beside the weights'; 6-8 us of a call with the launch.  (128 columns
+// a CTA took a call over 16 parts a unit from 72.0 to 73.4 us, 32 columns a thread to 76.8.)
+constexpr int JOIN_WARPS = 4, JOIN_COLS = 16;
 
 __global__ void __launch_bounds__(JOIN_WARPS * 32) tree_join_kernel(const __grid_constant__ TreeLaunch p) {
   const char* ws = static_cast<const char*>(p.t.workspace);

@@ -388,7 +388,7 @@ def test_tree_attention_does_not_read_past_the_lengths(heads):
     assert np.array_equal(bits_of(before[0]), bits_of(after[0])) and torch.equal(before[1], after[1])
 
 
-@pytest.mark.parametrize("bs", [1, 8, 16, 24, 32, 128])
+@pytest.mark.parametrize("bs", [1, 8, 16, 24, 32, 48, 96, 128])
 def test_tree_attention_ends_inside_a_block(bs):
     """NaN behind the last key, at every kind of end and block size."""
     kv = [1, 7, 8, 9, 31, 33, 63, 65, 97, 120, 127, 129, 160, 191, 193, 250]
