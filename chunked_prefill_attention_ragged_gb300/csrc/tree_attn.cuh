@@ -179,19 +179,11 @@ struct Parts {
   }
 };
 
-// Where 64 keys from `key0` on are, spread over the lanes: first the blocks as the table has them
-// (the loads are under way while the caller does other things), then the rows to copy.  With block
-// sizes of 8, 16, 32 or multiples of 64 they come by boxes of `step` keys, lane k holding box k; else
-// (step 0) lanes 0-15 hold keys 4 lane .. + 3 each.  A key past the readable ones, or in a block that the table does not
-// name, is the row past the cache (read as zeros), the latter flagged; in the piece in which the
-// readable keys end, what lies behind them comes along.
+// From key positions to cache rows: first the block as the table has it (its load is under way while
+// the caller does other things), then the row to copy.  A key past the readable ones, or in a block
+// that the table does not name, is the row past the cache (read as zeros), the latter flagged; of a box
+// in which the readable keys end, what lies behind them comes along.
 constexpr int32_t PAST_END = -0x7fffffff - 1;
-struct KeyBlocks {
-  int32_t b[4];
-};
-struct KeyRows {
-  int32_t r[4];
-};
 __device__ __forceinline__ int block_of(const TreeLaunch& p, int key) {
   return p.block_shift >= 0 ? key >> p.block_shift : key / p.t.block_size;
 }
@@ -207,26 +199,22 @@ __device__ __forceinline__ int32_t block_row(const TreeLaunch& p, int32_t blk, i
   }
   return (int32_t)((int64_t)blk * p.t.block_size + ((int)key - block_of(p, (int)key) * p.t.block_size));
 }
-__device__ __forceinline__ KeyBlocks find_blocks(const TreeLaunch& p, const Part& u, int64_t key0, int step, int lane) {
-  KeyBlocks k{{PAST_END, PAST_END, PAST_END, PAST_END}};
-  if (step > 0) {
-    if (lane * step < 64) k.b[0] = table_block(p, u, key0 + lane * step);
-  } else if (lane < 16) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) k.b[j] = table_block(p, u, key0 + 4 * lane + j);
-  }
-  return k;
+// 64 keys from key0 on by boxes of `step` keys, lane k with box k.
+__device__ __forceinline__ int32_t box_block(const TreeLaunch& p, const Part& u, int64_t key0, int step, int lane) {
+  return lane * step < 64 ? table_block(p, u, key0 + lane * step) : PAST_END;
 }
-__device__ __forceinline__ KeyRows find_rows(const TreeLaunch& p, const Part& u, const KeyBlocks& k, int64_t key0,
-                                             int step, int lane) {
-  KeyRows w;
-  if (step > 0) {
-    w.r[0] = block_row(p, k.b[0], key0 + lane * step);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w.r[j] = block_row(p, k.b[j], key0 + 4 * lane + j);
-  }
-  return w;
+// And row by row, a lane keys lane and 32 + lane.
+struct KeyBlocks {
+  int32_t b[2];
+};
+struct KeyRows {
+  int32_t r[2];
+};
+__device__ __forceinline__ KeyBlocks find_blocks(const TreeLaunch& p, const Part& u, int64_t key0, int lane) {
+  return {{table_block(p, u, key0 + lane), table_block(p, u, key0 + 32 + lane)}};
+}
+__device__ __forceinline__ KeyRows find_rows(const TreeLaunch& p, const KeyBlocks& k, int64_t key0, int lane) {
+  return {{block_row(p, k.b[0], key0 + lane), block_row(p, k.b[1], key0 + 32 + lane)}};
 }
 
 // Visibility of 64 keys from position pos0 on for node i (row t of the batch), bit k for key k.

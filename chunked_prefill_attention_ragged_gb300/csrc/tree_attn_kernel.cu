@@ -25,14 +25,14 @@
 //   warp 0     Q and K producer: Q once per unit; K in three groups of three 64-column panels
 //   warp 1     even CTA: issues every product
 //   warp 2     V producer: the CTA's columns, by halves of the keys
-//   warp 3     TMEM allocation; brings the next tile's rows into L2, or, where K comes by gather4,
-//              loads its last group
+//   warp 3     TMEM allocation; brings the next tile's rows into L2, or, where rows are copied
+//              one by one, loads K's last group
 //   warps 4-7  softmax: two threads per pair (the two halves of the keys and of O's columns)
 // Order of products: S(t + 1) before P V(t), so that the tensor cores work on the next tile while
 // the softmax does this one.  Key rows come by whole boxes of 64 where the block size is a multiple
 // of that, by boxes of 32, 16 or 8 where it is one of these (in the piece where the keys end, what lies
-// behind them is made zero), else by gather4 with rows past the end read as zeros.  The kernel is compiled
-// for each: with strides of the operands read from registers the products' issue took 3% longer.
+// behind them is made zero), else row by row by the producers' own lanes.  The kernel is compiled for
+// each: with strides of the operands read from registers the products' issue took 3% longer.
 // What bounds it: for one node a request HBM (64 requests over 4096 positions, 16 heads: 66.5 us with the
 // join, 6 TB/s while tiles run); for many the products and what feeds them (32 x 16 nodes over 8192, 128
 // heads: 785-815 us, 0.77-0.80 of the measured tensor rate: a tile is 2176 clocks of products, 392 KB
@@ -110,14 +110,23 @@ struct Ctx {
   }
 };
 
-// Where the block size is no multiple of 64: 64 keys by four rows at a time, panels [panel0, panel0 + n)
-// to n consecutive 8 KB panels at dst, completing on `bar` (a shared::cluster address).
-__device__ __forceinline__ void gather_panels(const KeyRows& k, uint32_t dst, uint32_t bar, const CUtensorMap* tc,
-                                              int panel0, int n, int lane) {
-  if (lane >= 16) return;
-#pragma unroll 1
-  for (int i = 0; i < n; ++i)
-    tma_gather4_pair(dst + i * QP + lane * 4 * 128, tc, bar, (panel0 + i) * 64, k.r[0], k.r[1], k.r[2], k.r[3]);
+// Where the block size is no multiple of 8: 64 keys' rows, PANELS panels from panel0 on, to consecutive
+// 8 KB panels at dst (in the swizzle that a box would have), 16 bytes a thread: eight lanes a row.  Rows
+// that are not there are zeros.
+template <int PANELS>
+__device__ __forceinline__ void copy_rows(const TreeLaunch& p, const KeyRows& k, uint32_t dst, int panel0, int lane) {
+  const int ch = lane & 7;
+  const __nv_bfloat16* cache = (p.t.cache ? p.t.cache : p.t.q) + panel0 * 64 + ch * 8;
+#pragma unroll 2
+  for (int j = 0; j < 16; ++j) {
+    const int key = 4 * j + (lane >> 3);
+    const int32_t row = __shfl_sync(0xffffffffu, j < 8 ? k.r[0] : k.r[1], key & 31);
+    const bool there = row != p.oob_row;
+    const __nv_bfloat16* src = cache + (there ? (int64_t)row * 576 : 0);
+    const uint32_t d = dst + key * 128 + ((ch ^ (key & 7)) << 4);
+#pragma unroll
+    for (int i = 0; i < PANELS; ++i) cp_async16(d + i * QP, src + i * 64, there ? 16 : 0);
+  }
 }
 
 // ------------------------------------------------------------------ producers
@@ -137,18 +146,16 @@ __device__ __forceinline__ void settle() {
 
 template <int R>
 __device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, Parts parts, const CUtensorMap* tq,
-                                const CUtensorMap* tc, const CUtensorMap* tk, volatile int* begun) {
+                                const CUtensorMap* tk, volatile int* begun) {
   const int lane = threadIdx.x & 31;
   const uint32_t qf = mapa_shared(c.bar(QF), 0), kf = mapa_shared(c.bar(KF), 0);
-  // Whole boxes come in three groups, small ones as one; gather4's last group is another warp's.
-  constexpr int groups = R == 64 ? KGROUPS : R > 0 ? 1 : KGROUPS - 1;
-  constexpr int step = R > 0 ? 8 : 0;
+  constexpr int groups = R == 64 ? KGROUPS : 1;   // smaller boxes come as one
   int tiles = 0, units = 0, issued = 0;   // tiles begun, parts, K groups
   bool ok = true;
   Part u;
   while (ok && parts.next(&u)) {
-    KeyBlocks blocks{};
-    if (R != 64) blocks = find_blocks(p, u, (int64_t)u.lo * KEYS + 64 * c.rank, step, lane);
+    int32_t block = 0;
+    if (R != 64) block = box_block(p, u, (int64_t)u.lo * KEYS + 64 * c.rank, 8, lane);
     if (lane == 0) {
       if (units > 0) ok = c.wait(QE, (units - 1) & 1);
       if (ok) {
@@ -179,23 +186,16 @@ __device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, Parts parts, 
           }
         }
       } else {
-        const KeyRows k = find_rows(p, u, blocks, key0, step, lane);
-        if (t + 1 < u.hi) blocks = find_blocks(p, u, key0 + KEYS, step, lane);
-#pragma unroll 1
-        for (int g = 0; g < groups; ++g) {
-          if (lane == 0) {
-            if (tiles > 0) ok = c.wait(KE + g, (tiles - 1) & 1);
-            if (ok) expect_both(c, KF + g, (R > 0 ? NP : 3) * QP);
-          }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) break;
-          if (R > 0) {
-            if (lane < 8) tma_load_3d_pair(c.sbase + OFF_K + lane * K_ROWS8, tk, kf, 0, k.r[0], 0);
-          } else {
-            gather_panels(k, c.sbase + OFF_K + 3 * g * QP, kf + 8 * g, tc, 3 * g, 3, lane);
-          }
-          ++issued;
+        const int32_t box = block_row(p, block, key0 + 8 * lane);
+        if (t + 1 < u.hi) block = box_block(p, u, key0 + KEYS, 8, lane);
+        if (lane == 0) {
+          if (tiles > 0) ok = c.wait(KE, (tiles - 1) & 1);
+          if (ok) expect_both(c, KF, NP * QP);
         }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        if (lane < 8) tma_load_3d_pair(c.sbase + OFF_K + lane * K_ROWS8, tk, kf, 0, box, 0);
+        ++issued;
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
     }
@@ -214,39 +214,80 @@ __device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, Parts parts, 
   }
 }
 
-// Warp 3 where K comes by gather4: its last group.
-__device__ void run_producer_k_last(const Ctx& c, const TreeLaunch& p, Parts parts, const CUtensorMap* tc) {
-  const int lane = threadIdx.x & 31, g = KGROUPS - 1;
-  const uint32_t kf = mapa_shared(c.bar(KF), 0);
-  int tiles = 0, issued = 0;
+// Where the block size is no multiple of 8, K (groups first .. first + n - 1, and Q beside group 0) or V
+// (n = 2 halves) row by row: the lanes' own copies, handed to the even CTA's barriers when they have
+// landed.  Bound by the threads' path from L2, 30 bytes a clock and SM: 16 requests of 4 nodes, 128 heads,
+// over 4096 take 168 us with blocks of 1 or 4, 203 by gather4 (four rows of a panel a copy), 69 by boxes
+// of 64.
+template <bool V>
+__device__ void run_rows(const Ctx& c, const TreeLaunch& p, Parts parts, const CUtensorMap* tq, int first, int n) {
+  const int lane = threadIdx.x & 31;
+  const bool with_q = !V && first == 0;
+  const int full = V ? VF : KF + first, empty = V ? VE : KE + first;
+  const uint32_t dst = c.sbase + (V ? OFF_V : OFF_K + 3 * first * QP);
+  int tiles = 0, units = 0;
   bool ok = true;
   Part u;
   while (ok && parts.next(&u)) {
-    int64_t key0 = (int64_t)u.lo * KEYS + 64 * c.rank;
-    KeyBlocks blocks = find_blocks(p, u, key0, 0, lane);
-#pragma unroll 1
-    for (int t = u.lo; t < u.hi && ok; ++t, ++tiles, key0 += KEYS) {
-      const KeyRows k = find_rows(p, u, blocks, key0, 0, lane);
-      if (t + 1 < u.hi) blocks = find_blocks(p, u, key0 + KEYS, 0, lane);
+    int64_t key0 = (int64_t)u.lo * KEYS + (V ? 0 : 64 * c.rank);
+    KeyBlocks b0 = find_blocks(p, u, key0, lane), b1{};
+    if (V) b1 = find_blocks(p, u, key0 + 64, lane);
+    if (with_q) {
       if (lane == 0) {
-        if (tiles > 0) ok = c.wait(KE + g, (tiles - 1) & 1);
-        if (ok) expect_both(c, KF + g, 3 * QP);
+        if (units > 0) ok = c.wait(QE, (units - 1) & 1);
+        if (ok) {
+          expect_both(c, QF, NP * QP);
+          tma_load_3d_pair(c.sbase + OFF_Q, tq, mapa_shared(c.bar(QF), 0), 0, (int32_t)(u.pair0 + 64 * c.rank), 0);
+        }
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
-      gather_panels(k, c.sbase + OFF_K + 3 * g * QP, kf + 8 * g, tc, 3 * g, 3, lane);
-      ++issued;
+      ++units;
+    }
+#pragma unroll 1
+    for (int t = u.lo; t < u.hi && ok; ++t, ++tiles, key0 += KEYS) {
+      const KeyRows k0 = find_rows(p, b0, key0, lane);
+      KeyRows k1{};
+      if (V) k1 = find_rows(p, b1, key0 + 64, lane);
+      if (t + 1 < u.hi) {
+        b0 = find_blocks(p, u, key0 + KEYS, lane);
+        if (V) b1 = find_blocks(p, u, key0 + KEYS + 64, lane);
+      }
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        if (lane == 0 && tiles > 0) ok = c.wait(empty + i, (tiles - 1) & 1);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        __syncwarp();   // (what lane 0 acquired, for the others' writes)
+        if (V) copy_rows<4>(p, i ? k1 : k0, dst + i * V_HALF, 4 * (int)c.rank, lane);
+        else copy_rows<3>(p, k0, dst + 3 * i * QP, 3 * (first + i), lane);
+        cp_async_commit();
+      }
+#pragma unroll 1
+      for (int i = 0; i < n && ok; ++i) {
+        if (i + 1 < n) cp_async_wait<1>();
+        else cp_async_wait<0>();
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          if (c.rank) mbar_arrive_remote(mapa_shared(c.bar(full + i), 0));
+          else mbar_arrive(c.bar(full + i));
+        }
+      }
     }
   }
-  if (lane == 0) {
-    if (c.rank == 0 && issued) c.drain(KF + g, (issued - 1) & 1);
-    if (!ok) settle();
+  cp_async_wait<0>();
+  if (lane == 0 && with_q) {
+    if (c.rank == 0) {
+      if (units) c.drain(QF, (units - 1) & 1);
+    } else if (!ok) {
+      settle();
+    }
   }
 }
 
 template <int R>
-__device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, Parts parts, const CUtensorMap* tc,
-                               const CUtensorMap* tv, uint8_t* smem) {
+__device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, Parts parts, const CUtensorMap* tv, uint8_t* smem) {
   const int lane = threadIdx.x & 31, panel0 = 4 * (int)c.rank;
   const uint32_t vf = mapa_shared(c.bar(VF), 0);
   int tiles = 0, issued = 0;
@@ -255,10 +296,10 @@ __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, Parts parts, c
   Part u;
   while (ok && parts.next(&u)) {
     int32_t ahead0 = 0, ahead1 = 0;   // rows of 32 tiles' first and second halves
-    KeyBlocks b0{}, b1{};
+    int32_t b0 = 0, b1 = 0;
     if (R != 64) {
-      b0 = find_blocks(p, u, (int64_t)u.lo * KEYS, R, lane);
-      b1 = find_blocks(p, u, (int64_t)u.lo * KEYS + 64, R, lane);
+      b0 = box_block(p, u, (int64_t)u.lo * KEYS, R, lane);
+      b1 = box_block(p, u, (int64_t)u.lo * KEYS + 64, R, lane);
     }
 #pragma unroll 1
     for (int t = u.lo; t < u.hi && ok; ++t, ++tiles) {
@@ -268,10 +309,10 @@ __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, Parts parts, c
         ahead0 = piece_rows(p, u, key0, KEYS, u.hi - t, lane);
         ahead1 = piece_rows(p, u, key0 + 64, KEYS, u.hi - t, lane);
       }
-      const int32_t row0 = __shfl_sync(0xffffffffu, ahead0, j), row1 = __shfl_sync(0xffffffffu, ahead1, j);
+      int32_t row0 = __shfl_sync(0xffffffffu, ahead0, j), row1 = __shfl_sync(0xffffffffu, ahead1, j);
       // The half in which the keys end brings along what lies behind them.
       const int64_t valid = u.q.kv - key0;
-      const bool ends = R > 0 && valid > 0 && valid < KEYS && valid != 64;
+      const bool ends = valid > 0 && valid < KEYS && valid != 64;
       if (R == 64 && !ends) {   // one lane, two copies
         if (lane == 0) {
 #pragma unroll 1
@@ -284,13 +325,12 @@ __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, Parts parts, c
           }
         }
       } else {
-        KeyRows k0{{row0, 0, 0, 0}}, k1{{row1, 0, 0, 0}};
         if (R != 64) {
-          k0 = find_rows(p, u, b0, key0, R, lane);
-          k1 = find_rows(p, u, b1, key0 + 64, R, lane);
+          row0 = block_row(p, b0, key0 + lane * R);
+          row1 = block_row(p, b1, key0 + 64 + lane * R);
           if (t + 1 < u.hi) {
-            b0 = find_blocks(p, u, key0 + KEYS, R, lane);
-            b1 = find_blocks(p, u, key0 + KEYS + 64, R, lane);
+            b0 = box_block(p, u, key0 + KEYS, R, lane);
+            b1 = box_block(p, u, key0 + KEYS + 64, R, lane);
           }
         }
         const int cut = !ends ? 2 : valid < 64 ? 0 : 1;   // the half to mend
@@ -305,13 +345,8 @@ __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, Parts parts, c
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) break;
-          const KeyRows& k = i ? k1 : k0;
           const uint32_t dst = c.sbase + OFF_V + i * V_HALF, bar = i == cut ? mapa_shared(c.bar(LB), c.rank) : vf + 8 * i;
-          if (R > 0) {
-            if (lane * R < 64) tma_load_3d_pair(dst + lane * R * 512, tv, bar, 0, k.r[0], panel0);
-          } else {
-            gather_panels(k, dst, bar, tc, panel0, 4, lane);
-          }
+          if (lane * R < 64) tma_load_3d_pair(dst + lane * R * 512, tv, bar, 0, i ? row1 : row0, panel0);
           ++issued;
         }
         // What came along behind the last key, as far as products read (16 keys at a time), is made zero
@@ -697,12 +732,11 @@ __device__ void run_softmax(const Ctx& c, const TreeLaunch& p, Parts parts, uint
   }
 }
 
-// R: rows of a box of the cache (8, 16, 32, 64), 0: by gather4.
+// R: rows of a box of the cache (8, 16, 32, 64), 0: row by row.
 template <int R>
 __global__ void __launch_bounds__(NTHREADS, 1)
-tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_c,
-                 const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                 const __grid_constant__ TreeLaunch p) {
+tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeLaunch p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ StartRec start;
   __shared__ int64_t count;
@@ -718,9 +752,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   ReqWords words{0, 0, 0};   // (on their way while the barriers are made)
   if ((int)threadIdx.x < p.t.batch) words = load_words(p.t, threadIdx.x);
   if (warp == 1) {
-    // P: every softmax warp of both CTAs; maxima: the two warps of 32 rows.
+    // P: every softmax warp of both CTAs; maxima: the two warps of 32 rows; rows: a warp of each CTA.
     static_assert(NBAR <= 32, "a lane each");
-    if (lane < NBAR) mbar_init(c.bar(lane), lane == PR ? 8 : lane == XB || lane == XB + 1 ? 2 : 1);
+    const bool rows = R == 0 && ((lane >= KF && lane < KF + KGROUPS) || (lane >= VF && lane < VF + 2));
+    if (lane < NBAR) mbar_init(c.bar(lane), lane == PR ? 8 : lane == XB || lane == XB + 1 || rows ? 2 : 1);
     if (lane == 0) {
       *abort_flag = 0;
       *begun = -1;
@@ -729,8 +764,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tm_q);
-    tma_prefetch_desc(R > 0 ? &tm_k : &tm_c);
-    if (R > 0) tma_prefetch_desc(&tm_v);
+    if (R > 0) {
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
   }
   if (warp == 3) {   // one warp of each CTA of the pair, together
     tmem_alloc_pair(smem_addr(tmem_slot), TMEM_COLS);
@@ -749,14 +786,16 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const Parts parts(p.t, start, count);
   if (warp == 0) {
-    run_producer_qk<R>(c, p, parts, &tm_q, &tm_c, &tm_k, begun);
+    if constexpr (R > 0) run_producer_qk<R>(c, p, parts, &tm_q, &tm_k, begun);
+    else run_rows<false>(c, p, parts, &tm_q, 0, KGROUPS - 1);
   } else if (warp == 2) {
-    run_producer_v<R>(c, p, parts, &tm_c, &tm_v, smem);
+    if constexpr (R > 0) run_producer_v<R>(c, p, parts, &tm_v, smem);
+    else run_rows<true>(c, p, parts, &tm_q, 0, 2);
   } else if (warp == 1) {
     if (rank == 0) run_mma<R>(c, p, parts, tmem);
   } else if (warp == 3) {
     if constexpr (R > 0) run_prefetch<R>(c, p, parts, &tm_k, begun);
-    else run_producer_k_last(c, p, parts, &tm_c);
+    else run_rows<false>(c, p, parts, &tm_q, KGROUPS - 1, 1);
   } else {
     run_softmax(c, p, parts, tmem, ws + WS_SLOTS + (size_t)worker * 2 * SLOT_BYTES, smem);
   }
@@ -788,7 +827,7 @@ cudaLaunchConfig_t pair_config(cudaLaunchAttribute* attr, int workers, cudaStrea
   return cfg;
 }
 
-using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap, const TreeLaunch);
+using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const TreeLaunch);
 Kernel kernel_of(int box_rows) {
   switch (box_rows) {
     case 8: return tree_attn_kernel<8>;
@@ -837,13 +876,12 @@ cudaError_t launch_tree_attention(const TreeParams& t, cudaStream_t stream) {
   const bool any = t.max_blocks > 0;   // some cache row may be read
   const int bs = t.block_size;
   const uint64_t slots = any ? (uint64_t)t.num_blocks * (uint64_t)bs : 1;
-  CUtensorMap tq, tc, tk, tv;
+  CUtensorMap tq, tk, tv;
   {
     const uint64_t dims[3] = {64, (uint64_t)t.total_rows * (uint64_t)t.num_heads, NP}, strides[2] = {576 * 2, 64 * 2};
     const uint32_t box[3] = {64, 64, NP};   // 64 rows, panel by panel
     if (make_tensor_map_bf16(&tq, t.q, 3, dims, strides, box) != MLA_OK) return cudaErrorInvalidValue;
   }
-  const void* rows = any ? static_cast<const void*>(t.cache) : t.q;   // a map needs a valid base
   // Boxes for 64-key pieces: of as many rows, 64 to 8, as the block size is a multiple of (8 rows keep a
   // box on the swizzle's 1024-byte period; by gather4 blocks of 24, 48 and 96 took 235 us where they
   // take 85, 16 requests of 4 nodes, 128 heads, over 4096); several panels in
@@ -858,15 +896,11 @@ cudaError_t launch_tree_attention(const TreeParams& t, cudaStream_t stream) {
     const uint64_t dims[3] = {64, slots, NP}, strides[2] = {576 * 2, 64 * 2};
     const uint32_t box_k[3] = {64, box_rows == 64 ? 64u : 8u, box_rows == 64 ? 3u : (uint32_t)NP};
     const uint32_t box_v[3] = {64, (uint32_t)box_rows, 4};
-    if (make_tensor_map_bf16(&tk, rows, 3, dims, strides, box_k) != MLA_OK ||
-        make_tensor_map_bf16(&tv, rows, 3, dims, strides, box_v) != MLA_OK)
+    if (make_tensor_map_bf16(&tk, t.cache, 3, dims, strides, box_k) != MLA_OK ||
+        make_tensor_map_bf16(&tv, t.cache, 3, dims, strides, box_v) != MLA_OK)
       return cudaErrorInvalidValue;
-    tc = tk;   // (not used)
   } else {
-    const uint64_t dims[2] = {576, slots}, strides[1] = {576 * 2};
-    const uint32_t box[2] = {64, 1};   // one row high: rows are fetched four at a time by gather4
-    if (make_tensor_map_bf16(&tc, rows, 2, dims, strides, box) != MLA_OK) return cudaErrorInvalidValue;
-    tk = tv = tc;
+    tk = tv = tq;   // (not used)
   }
   p.oob_row = (int32_t)slots;
   p.o_align32 = (reinterpret_cast<uintptr_t>(t.o) & 31u) == 0;
@@ -880,7 +914,7 @@ cudaError_t launch_tree_attention(const TreeParams& t, cudaStream_t stream) {
   p.wait_limit_ns = forced ? forced : kWaitLimitNs;
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = pair_config(attr, p.workers, stream);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel_of(box_rows), tq, tc, tk, tv, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel_of(box_rows), tq, tk, tv, p);
   return e != cudaSuccess ? e : launch_tree_join(p, stream);
 }
 

@@ -321,6 +321,7 @@ ATTENTION = [
     ("wide_block_128", [2, 2], [400, 128], 48, 128, True, 0.0),
     ("wide_few_keys", [20, 9, 12], [4, 0, 12], 8, 64, True, 0.0),
     ("wide_softcap", [4, 3], [200, 513], 32, 64, True, 30.0),
+    ("block_5", [3, 9, 2], [1000, 131, 2], 20, 5, True, 0.0),
 ]
 
 
@@ -487,9 +488,10 @@ def test_tree_attention_more_requests_than_threads():
     p.check(o, lse, list(range(0, 700, 13)) + [699])
 
 
-def test_tree_attention_forced_timeout(monkeypatch):
+@pytest.mark.parametrize("bs", [1, 16, 64])
+def test_tree_attention_forced_timeout(monkeypatch, bs):
     """One wait that nothing satisfies gives up and is reported; the next call is right again."""
-    p = Problem(16, [3, 2], [500, 40], 16, 64, True)
+    p = Problem(16, [3, 2], [500, 40], 16, bs, True)
     monkeypatch.setenv("MLA_TEST_FORCE_TIMEOUT_NS", "2000000")
     assert p.run()[2] == 1
     monkeypatch.delenv("MLA_TEST_FORCE_TIMEOUT_NS")
