@@ -171,6 +171,9 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
+// For a kernel that may be launched before the one before it in its stream has ended.
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ------------------------------------------------------------------ copies by the threads
 // 16 bytes, of which `bytes` (0 or 16) are read and the others zero.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
