@@ -243,17 +243,21 @@ __global__ void __launch_bounds__(kMaxThreads) tables_kernel(const TablesParams 
 // The old lengths stay until the second kernel: every CTA reads them.
 __global__ void __launch_bounds__(kMaxThreads) tables_blocks_kernel(const TablesParams p) {
   extern __shared__ int smem[];
+  grid_launch_dependents();
   Shared s;
   make_sums(p, smem, blockIdx.x == 0, &s);
   move_blocks(p, s, blockIdx.x * blockDim.x + threadIdx.x, gridDim.x * blockDim.x);
 }
 
-// CTA 0 alone reads and writes what a request holds; the others only sum the new tokens.
+// CTA 0 alone reads and writes what a request holds; the others only sum the new tokens.  The sums are
+// made while the first kernel moves the blocks (it changes nothing that they are made of), then its end is
+// waited for.
 __global__ void __launch_bounds__(kSlotThreads) tables_slots_kernel(const TablesParams p) {
   extern __shared__ int smem[];
   if (blockIdx.x == 0) {
     Shared s;
     make_sums(p, smem, false, &s);
+    grid_dependency_wait();
     write_lengths(p, s, threadIdx.x, kSlotThreads);
   } else {
     __shared__ int64_t warp_sum[kSlotThreads / 32];
@@ -286,6 +290,7 @@ __global__ void __launch_bounds__(kSlotThreads) tables_slots_kernel(const Tables
     }
     if (tid == 0) smem[b] = (int)min(total, (int64_t)INT_MAX);
     __syncthreads();
+    grid_dependency_wait();
   }
   // (Neighbouring threads have neighbouring tokens, a thread every kSlotThreads-th.)
   const int64_t t0 = (int64_t)blockIdx.x * kSlotThreads * kSlotsPerThread + threadIdx.x;
@@ -323,8 +328,17 @@ cudaError_t launch_tables(const TablesParams& p, cudaStream_t stream) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int64_t per_cta = (int64_t)kSlotThreads * kSlotsPerThread;
-  tables_slots_kernel<<<(unsigned)((p.num_tokens + per_cta - 1) / per_cta), kSlotThreads, smem, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((p.num_tokens + per_cta - 1) / per_cta));
+  cfg.blockDim = dim3(kSlotThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tables_slots_kernel, p);
 }
 
 }  // namespace mla
