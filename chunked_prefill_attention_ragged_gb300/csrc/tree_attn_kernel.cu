@@ -33,9 +33,9 @@
 // of that, by boxes of 32, 16 or 8 where it is one of these (in the piece where the keys end, what lies
 // behind them is made zero), else row by row by the producers' own lanes.  The kernel is compiled for
 // each: with strides of the operands read from registers the products' issue took 3% longer.
-// What bounds it: for one node a request HBM (64 requests over 4096 positions, 16 heads: 66.5 us with the
+// What bounds it: for one node a request HBM (64 requests over 4096 positions, 16 heads: 65 us with the
 // join, 6 TB/s while tiles run); for many the products and what feeds them (32 x 16 nodes over 8192, 128
-// heads: 785-815 us, 0.77-0.80 of the measured tensor rate: a tile is 2176 clocks of products, 392 KB
+// heads: 772-815 us, 0.77-0.81 of the measured tensor rate: a tile is 2176 clocks of products, 392 KB
 // through shared memory and 272 KB from L2, and takes 2700-2950).  Calls of few tiles cost 14 us: 3.5 to
 // the first copy, a tile, the state and the join.
 // Every wait is bounded: on time-out the CTA records MLA_DEVSTAT_TIMEOUT, drains its copies and
