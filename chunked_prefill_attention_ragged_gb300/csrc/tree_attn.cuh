@@ -16,7 +16,7 @@ struct TreeLaunch {
   int block_shift;     // log2 of the block size, or -1
   int o_align32;
   int has_cap;
-  float scale_log2, cap_log2, cap_ex2_scale;
+  float scale_log2, cap_log2, cap_inv;
   uint64_t wait_limit_ns;
   int force_timeout;
 };

@@ -456,7 +456,7 @@ MLA_API int mla_tree_workspace(int64_t total_rows, int num_heads, int64_t* bytes
  *   status     : DEVICE int32 word or NULL
  * A row that sees no key gets O = 0, LSE = -inf; a NaN in a row of q_abs makes that row NaN.
  * Positions at or past kv_len never count (rows behind the last key may be read inside its
- * block; what is in them does not matter).  The cap's logits are off by at most 2^-20 c.
+ * block; what is in them does not matter). 
  * Cache rows below kv_len are to be finite: an infinity or NaN in a row that a node does not
  * see may still reach the other rows of its request.  MLA_DEVSTAT_BAD_INDEX is OR-ed in for a
  * block id outside [0, num_blocks) (its rows read as zeros), kv_len outside

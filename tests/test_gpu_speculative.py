@@ -117,6 +117,34 @@ def test_block_table_update_many_tokens_bad_values():
     assert got[2][-1] == (799 - 8999 // bs) * bs + 8999 % bs
 
 
+@pytest.mark.parametrize("num_tokens", [300, 9000])
+def test_block_table_update_replayed(num_tokens):
+    """One captured call, lengths changed between replays: against the oracle each time."""
+    import chunked_prefill_attention_ragged_gb300 as mla
+    rng = np.random.default_rng(num_tokens)
+    batch, bs, width, total = 20, 16, 120, 900
+    seq, new, table, held = i32([0] * batch), i32([0] * batch), i32(np.full((batch, width), -1)), i32([0] * batch)
+    free, count, st = i32(rng.permutation(total)), i32([total]), new_status()
+    mla.mla_block_table_update(seq, new, table, held, free, count, bs, num_tokens, status=st)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        qo, kv, slots = mla.mla_block_table_update(seq, new, table, held, free, count, bs, num_tokens, status=st)
+    h_table, h_held, h_stack = np.full((batch, width), -1), [0] * batch, free.cpu().numpy().tolist()
+    for _ in range(6):
+        s, m = rng.integers(0, 1000, batch), rng.integers(0, num_tokens // batch, batch)
+        seq.copy_(i32(s))
+        new.copy_(i32(m))
+        g.replay()
+        torch.cuda.synchronize()
+        want = update_block_table(s, m, h_table, h_held, h_stack, bs, total, num_tokens)
+        h_table, h_held, h_stack = want[3], want[4], want[5]
+        for k, got in enumerate((qo, kv, slots, table, held)):
+            np.testing.assert_array_equal(got.cpu().numpy(), want[k])
+        assert free.cpu().numpy()[:int(count)].tolist() == list(h_stack)
+        st.zero_()
+
+
 def test_block_table_update_of_two_streams():
     import chunked_prefill_attention_ragged_gb300 as mla
     streams = [torch.cuda.Stream() for _ in range(2)]
@@ -322,6 +350,8 @@ ATTENTION = [
     ("wide_few_keys", [20, 9, 12], [4, 0, 12], 8, 64, True, 0.0),
     ("wide_softcap", [4, 3], [200, 513], 32, 64, True, 30.0),
     ("block_5", [3, 9, 2], [1000, 131, 2], 20, 5, True, 0.0),
+    ("softcap_256", [4, 3], [200, 513], 16, 64, True, 256.0),
+    ("softcap_300", [4, 3], [200, 513], 16, 64, True, 300.0),
 ]
 
 
@@ -353,6 +383,26 @@ def test_tree_attention_split_and_unsplit(batch, ctx, nodes, heads):
     assert st == 0
     some = sorted({0, batch // 2, batch - 1})
     p.check(o, lse, some, None if heads <= 16 else [0, heads // 2, heads - 1])
+
+
+@pytest.mark.parametrize("spread", [1.0, 3000.0])   # logits far below the cap, and up to it
+def test_tree_attention_large_cap(spread):
+    """As good as without a cap: the bounds have no term for it (a relative error of 2^-20 of a logit,
+    three operations' worth, is inside what they allow for 576 products)."""
+    cap = 20000.0
+    p = Problem(34, [3, 2], [400, 90], 8, 64, True, cap=cap, spread=spread, sm_scale=0.07)
+    o, lse, st = p.run()
+    assert st == 0
+    b = p.b
+    o, lse = f64_of_bf16(o), lse.double().cpu().numpy()
+    for r in range(2):
+        rows = slice(int(b.qo_indptr[r]), int(b.qo_indptr[r + 1]))
+        q, kv = bf16_bits_to_f64(b.q_abs[rows]), bf16_bits_to_f64(p.rows(r))
+        want_o, want_l = tree_attention(q, kv, p.seen[r], sm_scale=0.07, logits_soft_cap=cap)
+        tol_o, tol_l = bounds(q, kv, p.seen[r], want_o, sm_scale=0.07, cap=0)
+        top = np.abs(want_l).max() * 2.0 ** -19   # the exponential form, where logits come near the cap
+        assert (np.abs(o[rows] - want_o) <= tol_o + 2 * top * np.abs(kv[:, :512]).max()).all()
+        assert (np.abs(lse[rows] - want_l) <= tol_l + top).all()
 
 
 def test_tree_attention_mask_rows_without_any_node():
@@ -729,3 +779,48 @@ def test_serving_steps_replayed_from_one_graph():
         graph.replay()
         torch.cuda.synchronize()
         s.step_oracle_and_check()
+
+
+# ----------------------------------------------------------------------------------- refusals
+def test_python_refusals():
+    import chunked_prefill_attention_ragged_gb300 as mla
+    p = Problem(40, [3, 2], [100, 40], 4, 64, True)
+    b = p.b
+    q, cache, table, qo, kv, mask = (to_dev_bf16(b.q_abs), to_dev_bf16(b.cache), to_dev(b.block_table),
+                                     i32(b.qo_indptr), i32(p.kv), p.mask())
+
+    def attention(**kw):
+        a = dict(q=q, cache=cache, table=table, qo=qo, kv=kv, mask=mask, extra={})
+        a.update(kw)
+        mla.mla_tree_attention(a["q"], a["cache"], a["table"], a["qo"], a["kv"], a["mask"], sm_scale=0.1, **a["extra"])
+
+    attention()
+    for kw, err in [(dict(q=q.float()), TypeError), (dict(q=q.transpose(0, 1)), ValueError), (dict(q=q[:, :, :512]), ValueError),
+                    (dict(cache=cache.half()), TypeError), (dict(cache=cache[:, ::2]), ValueError),
+                    (dict(table=table.long()), TypeError), (dict(table=table[0]), ValueError),
+                    (dict(qo=qo[:-1]), ValueError), (dict(kv=kv.cpu()), TypeError), (dict(mask=mask[:-1]), ValueError),
+                    (dict(mask=mask.int()), TypeError), (dict(extra=dict(o=torch.empty_like(q))), ValueError),
+                    (dict(extra=dict(lse=torch.zeros(5, 5, device="cuda"))), ValueError),
+                    (dict(extra=dict(workspace=torch.zeros(1 << 20, device="cuda"))), TypeError),
+                    (dict(extra=dict(status=torch.zeros(1, device="cuda"))), TypeError),
+                    (dict(extra=dict(logits_soft_cap=float("nan"))), mla.MlaError)]:
+        with pytest.raises(err):
+            attention(**kw)
+    with pytest.raises(ValueError):
+        mla.mla_tree_mask(i32([[-1]]), i32([0, 1]), 1)
+    with pytest.raises(ValueError):
+        mla.mla_tree_mask(i32([-1]), i32([0, 1]), 0)
+    with pytest.raises(ValueError):
+        mla.mla_tree_mask(i32([-1]), i32([0, 1]), 1, mask=torch.zeros(1, 2, dtype=torch.int64, device="cuda"))
+    seq = i32([3])
+    with pytest.raises(mla.MlaError):   # in place over the lengths that are read again
+        mla.mla_block_table_update(seq, i32([1]), i32([[-1]]), i32([0]), i32([0]), i32([1]), 4, 1, kv_lens=seq)
+    with pytest.raises(ValueError):
+        mla.mla_block_table_update(seq, i32([1, 2]), i32([[-1]]), i32([0]), i32([0]), i32([1]), 4)
+    with pytest.raises(mla.MlaError):
+        mla.mla_block_table_update(seq, i32([1]), i32([[-1]]), i32([0]), i32([0]), i32([1]), 0)
+    with pytest.raises(ValueError):
+        mla.mla_tree_commit(cache[0], table, kv, i32([[0], [0]]), i32([0, 0]))
+    with pytest.raises(mla.MlaError):   # rows of no multiple of 16 bytes
+        mla.mla_tree_commit(torch.zeros(2, 4, 12, dtype=torch.bfloat16, device="cuda"), table, kv, i32([[0], [0]]), i32([0, 0]))
+    torch.cuda.synchronize()
