@@ -56,8 +56,8 @@ namespace {
 constexpr int ROWS = TREE_ROWS, KEYS = TREE_KEYS;   // 64 rows in each CTA
 constexpr int QP = 64 * 128;            // a [64 rows, 64 columns] panel: 8 KB
 constexpr int NP = 9;                   // 64-column panels of 576
-constexpr int KGROUPS = 3;              // K panels arrive in groups of three, or
-constexpr int K_ROWS8 = NP * 8 * 128;   // eight rows at a time: [panel][8 rows] of each
+constexpr int KGROUPS = 3;              // K panels arrive in groups of three,
+constexpr int K_ROWS8 = 3 * 8 * 128;    // by small boxes eight rows at a time: [panel][8 rows] of each
 constexpr int V_HALF = 4 * QP;          // 64 keys x the CTA's 256 value columns
 constexpr int OFF_Q = 0;
 constexpr int OFF_K = OFF_Q + NP * QP;
@@ -151,7 +151,6 @@ __device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, Parts parts, 
                                 const CUtensorMap* tk, volatile int* begun) {
   const int lane = threadIdx.x & 31;
   const uint32_t qf = mapa_shared(c.bar(QF), 0), kf = mapa_shared(c.bar(KF), 0);
-  constexpr int groups = R == 64 ? KGROUPS : 1;   // smaller boxes come as one
   int tiles = 0, units = 0, issued = 0;   // tiles begun, parts, K groups
   bool ok = true;
   Part u;
@@ -190,14 +189,17 @@ __device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, Parts parts, 
       } else {
         const int32_t box = block_row(p, block, key0 + 8 * lane);
         if (t + 1 < u.hi) block = box_block(p, u, key0 + KEYS, 8, lane);
-        if (lane == 0) {
-          if (tiles > 0) ok = c.wait(KE, (tiles - 1) & 1);
-          if (ok) expect_both(c, KF, NP * QP);
+#pragma unroll 1
+        for (int g = 0; g < KGROUPS; ++g) {
+          if (lane == 0) {
+            if (tiles > 0) ok = c.wait(KE + g, (tiles - 1) & 1);
+            if (ok) expect_both(c, KF + g, 3 * QP);
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          if (lane < 8) tma_load_3d_pair(c.sbase + OFF_K + 3 * g * QP + lane * K_ROWS8, tk, kf + 8 * g, 0, box, 3 * g);
+          ++issued;
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        if (lane < 8) tma_load_3d_pair(c.sbase + OFF_K + lane * K_ROWS8, tk, kf, 0, box, 0);
-        ++issued;
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
     }
@@ -206,8 +208,8 @@ __device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, Parts parts, 
   if (lane == 0) {
     if (c.rank == 0) {
       if (units) c.drain(QF, (units - 1) & 1);
-      for (int g = 0; g < groups; ++g) {
-        const int n = (issued + groups - 1 - g) / groups;
+      for (int g = 0; g < KGROUPS; ++g) {
+        const int n = (issued + KGROUPS - 1 - g) / KGROUPS;
         if (n) c.drain(KF + g, (n - 1) & 1);
       }
     } else if (!ok) {
@@ -412,7 +414,7 @@ __device__ void run_prefetch(const Ctx& c, const TreeLaunch& p, Parts parts, con
       if (t + 1 < u.hi && lane < (R < 64 ? 8 : 1) && key < u.q.kv) {
         const int32_t row = block_row(p, table_block(p, u, key), key);
 #pragma unroll 1
-        for (int g = 0; g < (R < 64 ? 1 : KGROUPS); ++g) tma_prefetch_3d(tk, 0, row, 3 * g);
+        for (int g = 0; g < KGROUPS; ++g) tma_prefetch_3d(tk, 0, row, 3 * g);
       }
     }
   }
@@ -449,10 +451,10 @@ __device__ __forceinline__ void commit_both(uint32_t bar) {
 template <int R>
 __device__ void run_mma(const Ctx& c, const TreeLaunch& p, Parts parts, uint32_t tmem) {
   const uint64_t q_desc = sdesc_sw128(c.sbase + OFF_Q, 16, 1024);
-  // K lies in panels of 64 rows, or eight rows at a time with all their panels.
+  // A group of K lies in panels of 64 rows, or eight rows at a time with their three panels.
   constexpr bool rows8 = R > 0 && R < 64;
+  constexpr uint32_t K_PANEL = rows8 ? 1024 : QP;
   const uint64_t k_desc = sdesc_sw128(c.sbase + OFF_K, 16, rows8 ? K_ROWS8 : 1024);
-  constexpr uint32_t k_panel = (rows8 ? 1024 : QP) >> 4;
   // Values lie in pieces of r keys, each with its four panels: 16 keys of a product are part of one
   // piece, a whole one or two.
   constexpr int r = R > 0 ? R : 64;
@@ -476,25 +478,24 @@ __device__ void run_mma(const Ctx& c, const TreeLaunch& p, Parts parts, uint32_t
     seen_k = 0;
 #pragma unroll 1
     for (int g = 0; g < KGROUPS; ++g) {
-      if ((g == 0 || !rows8) && !c.wait_warp(KF + g, st & 1, seen)) return false;
+      if (!c.wait_warp(KF + g, st & 1, seen)) return false;
       tc_fence_after();
       if (g + 1 < KGROUPS) {
-        if (!rows8) seen = c.look(KF + g + 1, st & 1);
+        seen = c.look(KF + g + 1, st & 1);
       } else {   // the P V that follows
         seen_p = c.look(PR, pv & 1);
         seen_v = c.look(VF, pv & 1);
       }
 #pragma unroll 1
-      for (int i = 3 * g; i < 3 * g + 3; ++i) {
+      for (int i = 0; i < 3; ++i) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-          const uint64_t qo = (uint64_t)((i * QP + kk * 32) >> 4), ko = (uint64_t)(i * k_panel + (kk * 32 >> 4));
-          issue(d, q_desc + qo, k_desc + ko, IDESC_QK, kk > 0 ? 1u : i > 0 ? 1u : 0u);
+          const uint32_t qo = (uint32_t)((3 * g + i) * QP + kk * 32) >> 4, ko = (uint32_t)(3 * g * QP + i * K_PANEL + kk * 32) >> 4;
+          issue(d, q_desc + qo, k_desc + ko, IDESC_QK, kk > 0 ? 1u : g + i > 0 ? 1u : 0u);
         }
       }
-      if (!rows8) commit_both(c.bar(KE + g));
+      commit_both(c.bar(KE + g));
     }
-    if (rows8) commit_both(c.bar(KE));
     commit_both(c.bar(SF + b));
     if (last) commit_both(c.bar(QE));
     ++st;
@@ -899,15 +900,15 @@ cudaError_t launch_tree_attention(const TreeParams& t, cudaStream_t stream) {
   // box on the swizzle's 1024-byte period; by gather4 blocks of 24, 48 and 96 took 235 us where they
   // take 85, 16 requests of 4 nodes, 128 heads, over 4096); several panels in
   // one box by a map of the rows as {64 columns, rows, 9 column groups}.  Smaller boxes' keys come eight
-  // rows at a time with all nine panels (8 copies where {64 columns, 16 rows} took 36), their values
-  // with four.
+  // rows at a time with three panels (all nine at once: 8 copies instead of 24, but products wait for
+  // all of them: 86 us instead of 82 for blocks of 24), their values with four.
   const int box_rows = !any ? 0 : bs % 64 == 0 ? 64 : bs % 32 == 0 ? 32 : bs % 16 == 0 ? 16 : bs % 8 == 0 ? 8 : 0;
   p.block_shift = -1;
   for (int i = 0; i < 31; ++i)
     if (bs == 1 << i) p.block_shift = i;
   if (box_rows > 0) {
     const uint64_t dims[3] = {64, slots, NP}, strides[2] = {576 * 2, 64 * 2};
-    const uint32_t box_k[3] = {64, box_rows == 64 ? 64u : 8u, box_rows == 64 ? 3u : (uint32_t)NP};
+    const uint32_t box_k[3] = {64, box_rows == 64 ? 64u : 8u, 3};
     const uint32_t box_v[3] = {64, (uint32_t)box_rows, 4};
     if (make_tensor_map_bf16(&tk, t.cache, 3, dims, strides, box_k) != MLA_OK ||
         make_tensor_map_bf16(&tv, t.cache, 3, dims, strides, box_v) != MLA_OK)
