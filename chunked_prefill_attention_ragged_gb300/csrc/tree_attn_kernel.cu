@@ -898,7 +898,7 @@ cudaError_t launch_tree_attention(const TreeParams& t, cudaStream_t stream) {
   }
   // Boxes for 64-key pieces: of as many rows, 64 to 8, as the block size is a multiple of (8 rows keep a
   // box on the swizzle's 1024-byte period; by gather4 blocks of 24, 48 and 96 took 235 us where they
-  // take 85, 16 requests of 4 nodes, 128 heads, over 4096); several panels in
+  // take 82, 16 requests of 4 nodes, 128 heads, over 4096); several panels in
   // one box by a map of the rows as {64 columns, rows, 9 column groups}.  Smaller boxes' keys come eight
   // rows at a time with three panels (all nine at once: 8 copies instead of 24, but products wait for
   // all of them: 86 us instead of 82 for blocks of 24), their values with four.
