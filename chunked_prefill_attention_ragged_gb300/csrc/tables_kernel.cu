@@ -12,6 +12,10 @@
 // c + R - 1 - k, where block k of those given back goes: so for k < R it is that block itself, which
 // moves from one table row to the other without the stack between, and every block is one thread's.
 //
+// Entries of a row behind those in use may hold anything.  A request that is not served would reach them:
+// as far as it would have needed them they are made -1, so that neither its slots here nor the calls that
+// read the table next (a commit writes by it) touch a block that it does not hold.
+//
 // Two forms.  Up to 8192 tokens to map, one CTA does it all: sums, blocks, slots, with its own
 // barriers between (what bounds it is latency: about 20 bytes per request and 8 per token).  More,
 // and one kernel moves the blocks and a second one writes the lengths and the slots, each CTA of
@@ -64,7 +68,13 @@ struct Shared {
   int released;
   int base;       // height of the stack before
   int64_t top;    // height with everything given back
+  bool refused;   // some request is not served
 };
+
+// Blocks that a request of l cached and m new tokens needs.
+__device__ __forceinline__ int64_t blocks_of(const TablesParams& p, int l, int m) {
+  return ((int64_t)max(l, 0) + max(m, 0) + p.block_size - 1) / p.block_size;
+}
 
 __device__ void make_sums(const TablesParams& p, int* smem, bool report, Shared* out) {
   __shared__ Sums warp_sum[kMaxThreads / 32];
@@ -81,16 +91,17 @@ __device__ void make_sums(const TablesParams& p, int* smem, bool report, Shared*
   const int per = (b + threads - 1) / threads;
   const int r0 = min(tid * per, b), r1 = min(r0 + per, b);
   Sums mine{0, 0, 0};
-  bool bad = false;
+  bool bad = false, refused = false;
   for (int r = r0; r < r1; ++r) {
     int l = p.seq_lens[r], m = p.new_lens[r], h = p.num_held[r];
     bad |= l < 0 || m < 0 || h < 0 || h > p.max_blocks;
     l = max(l, 0);
     m = max(m, 0);
     h = min(max(h, 0), p.max_blocks);
-    const int64_t target = ((int64_t)l + m + p.block_size - 1) / p.block_size;
+    const int64_t target = blocks_of(p, l, m);
     const bool fits = target <= p.max_blocks;
     bad |= !fits;
+    refused |= !fits;
     const int want = fits ? (int)target : h;   // a request too long for its row changes nothing
     s.tok[r] = m;
     s.held[r] = h;
@@ -140,9 +151,17 @@ __device__ void make_sums(const TablesParams& p, int* smem, bool report, Shared*
   }
   if (report && short_of) flag(p.status, MLA_DEVSTAT_NO_BLOCKS);
   if (taken) atomicMax(&s_taken, taken);
-  __syncthreads();
+  s.refused = __syncthreads_or(refused || short_of) != 0;
   s.taken = s_taken;
   *out = s;
+}
+
+// The entries that a request which is not served would have needed beyond those it holds; a warp a row.
+__device__ __forceinline__ void clear_refused(const TablesParams& p, const Shared& s, int first, int step) {
+  for (int r = first >> 5; r < p.batch; r += step >> 5) {
+    const int held = s.after[r], end = (int)min(blocks_of(p, p.seq_lens[r], p.new_lens[r]), (int64_t)p.max_blocks);
+    for (int j = held + (threadIdx.x & 31); j < end; j += 32) p.block_table[(int64_t)r * p.max_blocks + j] = -1;
+  }
 }
 
 // Block k of those given back or taken, for k = first, first + step, ...: out of its row, into the
@@ -234,6 +253,7 @@ __global__ void __launch_bounds__(kMaxThreads) tables_kernel(const TablesParams 
   Shared s;
   make_sums(p, smem, true, &s);
   move_blocks(p, s, threadIdx.x, blockDim.x);
+  if (s.refused) clear_refused(p, s, threadIdx.x, blockDim.x);
   write_lengths(p, s, threadIdx.x, blockDim.x);
   if (!p.slot_mapping) return;
   __syncthreads();
@@ -247,6 +267,7 @@ __global__ void __launch_bounds__(kMaxThreads) tables_blocks_kernel(const Tables
   Shared s;
   make_sums(p, smem, blockIdx.x == 0, &s);
   move_blocks(p, s, blockIdx.x * blockDim.x + threadIdx.x, gridDim.x * blockDim.x);
+  if (s.refused) clear_refused(p, s, blockIdx.x * blockDim.x + threadIdx.x, gridDim.x * blockDim.x);
 }
 
 // CTA 0 alone reads and writes what a request holds; the others only sum the new tokens.  The sums are

@@ -395,11 +395,13 @@ MLA_API int mla_absorbed_run(mla_plan_t plan, const void* q_abs, const void* cac
  * Row r ends up with ceil((seq_lens[r] + new_lens[r]) / block_size) entries: surplus blocks go
  * back on the stack first (entries become -1), then missing ones are taken, request by request.
  * A request is served when all requests up to it can be: otherwise it keeps what it holds, and
- * MLA_DEVSTAT_NO_BLOCKS is OR-ed into status.  Reserving blocks and giving the same ones back
- * restores the stack.  seq = new = 0 releases a row.  MLA_DEVSTAT_BAD_INDEX is OR-ed in for a
- * negative length, num_held or free_count outside its range (clamped), a request that needs
- * more than max_blocks_per_req blocks (it keeps what it holds), a full stack (the block is
- * lost), a negative block id taken from the stack, or more new tokens than num_tokens.
+ * MLA_DEVSTAT_NO_BLOCKS is OR-ed into status.  Entries of a row behind those in use may hold
+ * anything; those that a request which is not served would have needed become -1.  Reserving
+ * blocks and giving the same ones back restores the stack.  seq = new = 0 releases a row.
+ * MLA_DEVSTAT_BAD_INDEX is OR-ed in for a negative length, num_held or free_count outside its
+ * range (clamped), a request that needs more than max_blocks_per_req blocks (it is not served), a
+ * full stack (the block is lost), a negative block id taken from the stack, or more new tokens
+ * than num_tokens.
  * Limits: batch <= 8192, batch * max_blocks_per_req < 2^31.  One or two launches; allocates nothing.
  * kv_lens, qo_indptr and num_held are not the arrays of seq_lens or new_lens.
  * Calls that share a stack must be ordered by the caller.

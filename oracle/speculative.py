@@ -15,7 +15,9 @@ LORA = 512
 
 def update_block_table(seq, new, table, held, stack, block_size, capacity, num_tokens):
     """Returns (qo_indptr, kv_lens, slots, table, held, stack, short) for lists of lengths,
-    table [B, M], held [B] and the stack of free blocks (last = next to be taken)."""
+    table [B, M], held [B] and the stack of free blocks (last = next to be taken).  Entries of a row
+    behind those in use may hold anything; a request that is not served names no block in those that
+    it would have needed."""
     table, held, stack = np.array(table, dtype=np.int64), list(map(int, held)), list(map(int, stack))
     batch, width = table.shape
     want = [-(-(int(seq[r]) + int(new[r])) // block_size) for r in range(batch)]
@@ -29,11 +31,15 @@ def update_block_table(seq, new, table, held, stack, block_size, capacity, num_t
     left, short = len(stack), False
     for r in range(batch):
         need = want[r] - held[r]
-        if want[r] > width or need <= 0:
+        if need <= 0:
+            continue
+        if want[r] > width:
+            table[r, held[r]:] = -1
             continue
         left -= need                      # a request that cannot be served leaves none for later ones
         if left < 0:
             short = True
+            table[r, held[r]:want[r]] = -1
             continue
         for j in range(held[r], want[r]):
             table[r, j] = stack.pop()
@@ -43,7 +49,7 @@ def update_block_table(seq, new, table, held, stack, block_size, capacity, num_t
         qo.append(qo[-1] + int(new[r]))
         for i in range(int(new[r])):
             p = int(seq[r]) + i
-            blk = int(table[r, p // block_size]) if p // block_size < width else -1
+            blk = int(table[r, p // block_size]) if p // block_size < held[r] else -1
             slots.append(blk * block_size + p % block_size if blk >= 0 else -1)
     slots = (slots + [-1] * num_tokens)[:num_tokens]
     return (np.array(qo), np.array([int(a) + int(b) for a, b in zip(seq, new)]), np.array(slots, dtype=np.int64),
