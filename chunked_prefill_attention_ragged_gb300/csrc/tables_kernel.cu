@@ -200,6 +200,7 @@ __device__ __forceinline__ void move_blocks(const TablesParams& p, const Shared&
         const int r = owner(s.need, p.batch, (int)k);
         p.block_table[(int64_t)r * p.max_blocks + s.held[r] + (k - s.need[r])] = blk[i];
       } else if (at < p.free_capacity) {
+        if (blk[i] < 0) flag(p.status, MLA_DEVSTAT_BAD_INDEX);   // (where it came from: now, not when it is taken)
         p.free_blocks[at] = blk[i];
       } else {
         flag(p.status, MLA_DEVSTAT_BAD_INDEX);   // the stack is full

@@ -41,3 +41,14 @@ def test_anything_behind_the_entries_in_use(batch, most, bs, grid):
     assert got[5] == want[5]
     unfit = bool((-(-(seq + new) // bs) > width).any())
     assert got[6] == (NO_BLOCKS if want[6] else 0) | (BAD_INDEX if unfit or int(new.sum()) > n else 0)
+
+
+@pytest.mark.parametrize("num_tokens", [0, 9000])
+def test_a_row_that_gives_back_no_block_is_reported(num_tokens):
+    """An entry in use without a block (its id was negative on the stack, or the caller's own) is reported by
+    the call that gives it back, also when it goes to another row at once."""
+    got = run_tables([0, 0], [0, 0], [[3, -1], [4, 5]], [2, 2], [], 4, 4, num_tokens)
+    assert got[6] == BAD_INDEX and got[4].tolist() == [0, 0]
+    assert got[5] == [5, 4, -1, 3] and (got[3] == -1).all()
+    got = run_tables([0, 0], [0, 4], [[-1], [-1]], [1, 0], [9], 4, 4, num_tokens)
+    assert got[6] & BAD_INDEX and got[3].tolist() == [[-1], [-1]] and got[5] == [9]
