@@ -98,6 +98,7 @@ __device__ void make_sums(const TablesParams& p, int* smem, bool report, Shared*
     l = max(l, 0);
     m = max(m, 0);
     h = min(max(h, 0), p.max_blocks);
+    bad |= (int64_t)l + m > INT_MAX;   // (kv_lens says INT_MAX)
     const int64_t target = blocks_of(p, l, m);
     const bool fits = target <= p.max_blocks;
     bad |= !fits;

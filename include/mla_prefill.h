@@ -398,10 +398,11 @@ MLA_API int mla_absorbed_run(mla_plan_t plan, const void* q_abs, const void* cac
  * MLA_DEVSTAT_NO_BLOCKS is OR-ed into status.  Entries of a row behind those in use may hold
  * anything; those that a request which is not served would have needed become -1.  Reserving
  * blocks and giving the same ones back restores the stack.  seq = new = 0 releases a row.
- * MLA_DEVSTAT_BAD_INDEX is OR-ed in for a negative length, num_held or free_count outside its
- * range (clamped), a request that needs more than max_blocks_per_req blocks (it is not served), a
- * full stack (the block is lost), a negative block id taken from the stack or given back (it goes on
- * the stack all the same), or more new tokens than num_tokens.
+ * MLA_DEVSTAT_BAD_INDEX is OR-ed in for a negative length or one that passes 2^31 - 1 with its
+ * new tokens, num_held or free_count outside its range (all clamped), a request that needs more
+ * than max_blocks_per_req blocks (it is not served), a full stack (the block is lost), a negative
+ * block id taken from the stack or given back (it goes on the stack all the same), or more new
+ * tokens than num_tokens.
  * Limits: batch <= 8192, batch * max_blocks_per_req < 2^31.  One or two launches; allocates nothing.
  * kv_lens, qo_indptr and num_held are not the arrays of seq_lens or new_lens.
  * Calls that share a stack must be ordered by the caller.

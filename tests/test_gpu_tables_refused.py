@@ -52,3 +52,14 @@ def test_a_row_that_gives_back_no_block_is_reported(num_tokens):
     assert got[5] == [5, 4, -1, 3] and (got[3] == -1).all()
     got = run_tables([0, 0], [0, 4], [[-1], [-1]], [1, 0], [9], 4, 4, num_tokens)
     assert got[6] & BAD_INDEX and got[3].tolist() == [[-1], [-1]] and got[5] == [9]
+
+
+@pytest.mark.parametrize("num_tokens", [5, 9000])
+def test_lengths_past_32_bits(num_tokens):
+    """Blocks of 2^20 tokens: the row has room for a length that kv_lens cannot say."""
+    got = run_tables([2 ** 31 - 4], [5], [[7] * 2049], [2048], [8], 1 << 20, 4, num_tokens)
+    assert got[6] == BAD_INDEX and got[1].tolist() == [2 ** 31 - 1]
+    assert got[4].tolist() == [2049] and got[3][0, 2048] == 8
+    assert got[2][:5].tolist() == [8 * 2 ** 20 + k for k in (-4, -3, -2, -1, 0)]   # the end of 7, the first of 8
+    got = run_tables([2 ** 31 - 4], [3], [[7] * 2049], [2048], [8], 1 << 20, 4, num_tokens)
+    assert got[6] == 0 and got[1].tolist() == [2 ** 31 - 1]
