@@ -10,6 +10,10 @@ namespace {
 
 inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
+inline bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && a_bytes > 0 && b_bytes > 0 && (x < y ? y - x < (uintptr_t)a_bytes : x - y < (uintptr_t)b_bytes);
+}
 inline int done(cudaError_t e) { return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA; }
 
 }  // namespace
@@ -32,10 +36,14 @@ int mla_block_table_update(const int32_t* seq_lens, const int32_t* new_lens, int
     return MLA_ERR_INVALID_ARG;
   if (batch > 0 && (!seq_lens || !new_lens || !num_held || (max_blocks_per_req > 0 && !block_table)))
     return MLA_ERR_INVALID_ARG;
-  // The lengths are read again after the outputs of their size are written.
-  if (batch > 0 && (kv_lens == seq_lens || kv_lens == new_lens || qo_indptr == seq_lens || qo_indptr == new_lens ||
-                    num_held == seq_lens || num_held == new_lens))
-    return MLA_ERR_INVALID_ARG;
+  // The lengths are read again after outputs are written.
+  struct Written { const void* at; int64_t bytes; };
+  const int64_t b = batch;
+  const Written written[] = {{block_table, 4 * b * max_blocks_per_req}, {num_held, 4 * b},
+                             {free_blocks, 4 * (int64_t)free_capacity}, {free_count, 4},
+                             {qo_indptr, 4 * (b + 1)}, {kv_lens, 4 * b}, {slot_mapping, 8 * num_tokens}, {status, 4}};
+  for (const Written& w : written)
+    if (overlap(seq_lens, 4 * b, w.at, w.bytes) || overlap(new_lens, 4 * b, w.at, w.bytes)) return MLA_ERR_INVALID_ARG;
   TablesParams p;
   p.seq_lens = seq_lens;
   p.new_lens = new_lens;

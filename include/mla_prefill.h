@@ -404,7 +404,7 @@ MLA_API int mla_absorbed_run(mla_plan_t plan, const void* q_abs, const void* cac
  * block id taken from the stack or given back (it goes on the stack all the same), or more new
  * tokens than num_tokens.
  * Limits: batch <= 8192, batch * max_blocks_per_req < 2^31.  One or two launches; allocates nothing.
- * kv_lens, qo_indptr and num_held are not the arrays of seq_lens or new_lens.
+ * Nothing that is written overlaps seq_lens or new_lens (MLA_ERR_INVALID_ARG).
  * Calls that share a stack must be ordered by the caller.
  */
 MLA_API int mla_block_table_update(const int32_t* seq_lens, const int32_t* new_lens, int batch, int block_size,

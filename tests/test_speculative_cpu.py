@@ -111,3 +111,14 @@ def test_python_wants_cuda_tensors():
         mla.mla_tree_attention(torch.zeros(1, 1, 576), torch.zeros(1, 1, 576), t, i, i, sm_scale=1.0)
     with pytest.raises(TypeError):
         mla.mla_tree_commit(torch.zeros(1, 1, 576), t, i, t, i)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(seq=A + 4, kv=A), dict(seq=A, kv=A + 4), dict(new=A + 8, qo=A), dict(seq=A - 4, held=A), dict(new=A + 20, slots=A),
+    dict(new=A + 28, table=A), dict(seq=A + 28, free=A), dict(new=A, count=A + 4), dict(seq=A, status=A + 4),
+])
+def test_block_table_update_refuses_overlap(kw):
+    """The lengths beside, not the same as, what is written: elsewhere everything is apart."""
+    a = dict(seq=3 * A, new=4 * A, table=5 * A, held=6 * A, free=7 * A, count=8 * A, qo=9 * A, kv=10 * A, slots=11 * A)
+    a.update(kw)
+    assert tables(**a) == -1
