@@ -567,6 +567,14 @@ def _arg(t, dtype, dev, name, shape=None):
     return t.data_ptr()
 
 
+def _status_arg(t, dtype, dev):
+    """Address of a status word; one without an element would pass for none."""
+    at = _arg(t, dtype, dev, "status")
+    if at is not None and t.numel() == 0:
+        raise ValueError("status must have an element")
+    return at
+
+
 class _Torch:
     """What these calls use of torch, looked up once (the module is imported by the first call)."""
 
@@ -635,7 +643,7 @@ def mla_block_table_update(seq_lens, new_lens, block_table, num_held, free_block
         _arg(free_blocks, int32, dev, "free_blocks"), free_blocks.shape[0],
         _arg(free_count, int32, dev, "free_count", (1,)), _arg(qo_indptr, int32, dev, "qo_indptr", (b + 1,)),
         _arg(kv_lens, int32, dev, "kv_lens", (b,)), _arg(slot_mapping, int64, dev, "slot_mapping", (n,)), n,
-        _arg(status, int32, dev, "status"), handle), "mla_block_table_update")
+        _status_arg(status, int32, dev), handle), "mla_block_table_update")
     return qo_indptr, kv_lens, slot_mapping
 
 
@@ -657,7 +665,7 @@ def mla_tree_mask(parents, qo_indptr, mask_words: int, kv_lens=None, mask=None, 
     _check((_lib or library()).mla_tree_mask(
         _arg(parents, int32, dev, "parents"), _arg(qo_indptr, int32, dev, "qo_indptr"),
         _arg(kv_lens, int32, dev, "kv_lens", (b,)), b, t, w, _arg(mask, int64, dev, "mask", (t, w)),
-        _arg(positions, int32, dev, "positions", (t,)), _arg(status, int32, dev, "status"), handle), "mla_tree_mask")
+        _arg(positions, int32, dev, "positions", (t,)), _status_arg(status, int32, dev), handle), "mla_tree_mask")
     return mask, positions
 
 
@@ -708,7 +716,7 @@ def mla_tree_attention(q_abs, cache, block_table, qo_indptr, kv_lens, tree_mask=
         _arg(kv_lens, int32, dev, "kv_lens", (b,)), _arg(tree_mask, T.int64, dev, "tree_mask"), words, b, t, h,
         float(sm_scale), float(logits_soft_cap), _arg(o, bfloat16, dev, "o", (t, h, 512)),
         _arg(lse, float32, dev, "lse", (t, h)), _arg(workspace, uint8, dev, "workspace"), workspace.numel(),
-        _arg(status, int32, dev, "status"), handle), "mla_tree_attention")
+        _status_arg(status, int32, dev), handle), "mla_tree_attention")
     return o, lse
 
 
@@ -728,5 +736,5 @@ def mla_tree_commit(cache, block_table, seq_lens, accepted, accepted_counts, sta
         _arg(cache, bfloat16, dev, "cache"), layers, nb * bs * e, nb, bs, e,
         _arg(block_table, int32, dev, "block_table"), m, _arg(seq_lens, int32, dev, "seq_lens", (b,)),
         _arg(accepted, int32, dev, "accepted", (b, a)), _arg(accepted_counts, int32, dev, "accepted_counts", (b,)),
-        b, a, _arg(status, int32, dev, "status"), handle), "mla_tree_commit")
+        b, a, _status_arg(status, int32, dev), handle), "mla_tree_commit")
     return cache
