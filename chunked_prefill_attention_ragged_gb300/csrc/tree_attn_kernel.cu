@@ -593,30 +593,45 @@ __device__ void run_softmax(const Ctx& c, const TreeLaunch& p, Parts parts, uint
       tc_fence_after();
       float sv[64];
       tmem_ld64_sync(lane_addr + TM_S(sb), reinterpret_cast<uint32_t*>(sv));
-      // c * tanh(y) in log2 units, y = sm_scale * x / c, from tanh(y) = 1 - 2 / (e^(2y) + 1).  That is good to
-      // 2^-20 of 1 and so not for a small y, as logits under a large cap are: above 256 there is the series
-      // instead for |y| < 1/4 (its next term is 2^-21 of y there).  (Always so, 9 x up to 37 nodes under a
-      // cap of 30 took 41.5 us instead of 40.2.)
-      if (p.has_cap == 1) {
-        const float2 k2 = make_float2(2.8853900817779268f * p.cap_inv, 2.8853900817779268f * p.cap_inv);
-        const float2 one = make_float2(1.f, 1.f);
-        const float2 m2c = make_float2(-2.f * p.cap_log2, -2.f * p.cap_log2);
-        const float2 c2 = make_float2(p.cap_log2, p.cap_log2);
+      // c * tanh(y) in log2 units, y = x / c with the logit x.  For |y| < 1/4 x times the series of tanh(y) / y,
+      // whose next term is 2^-21; from there on c (1 - 2 / (e^(2y) + 1)), which is good to 2^-22 of c and so to
+      // 2^-20 of the result, where below it would lose the logit's low bits (all of them under a large cap).
+      // Most logits are far below their cap, so the second is worked out only for the 16 keys of a warp's rows
+      // in which some logit needs it.  (9 x up to 37 nodes under a cap of 30: 40.6 us, 39.4 with the second form
+      // alone; both for all keys and a choice: 41.2; tanh(y) / y as a quotient of polynomials: 41.0.)
+      if (p.has_cap) {
+        const float2 inv2 = make_float2(p.cap_inv, p.cap_inv), scale2 = make_float2(p.scale_log2, p.scale_log2);
+        const float2 e2 = make_float2(2.8853900817779268f, 2.8853900817779268f), one = make_float2(1.f, 1.f);
+        const float2 cap2 = make_float2(p.cap_log2, p.cap_log2), m2c = make_float2(-2.f * p.cap_log2, -2.f * p.cap_log2);
+        const float2 s1 = make_float2(-1.f / 3.f, -1.f / 3.f), s2 = make_float2(2.f / 15.f, 2.f / 15.f);
+        const float2 s3 = make_float2(-17.f / 315.f, -17.f / 315.f);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const float2 a = fmul2(make_float2(sv[2 * k], sv[2 * k + 1]), k2);
-          const float2 d = fadd2(make_float2(ex2_approx(a.x), ex2_approx(a.y)), one);
-          const float2 r = ffma2(make_float2(rcp_approx(d.x), rcp_approx(d.y)), m2c, c2);
-          sv[2 * k] = r.x;
-          sv[2 * k + 1] = r.y;
-        }
-      } else if (p.has_cap) {
+        for (int j = 0; j < 64; j += 16) {
+          float2 y[8], r[8];
+          float top = 0.f;
 #pragma unroll
-        for (int k = 0; k < 64; ++k) {
-          const float y = sv[k] * p.cap_inv, z = y * y;
-          const float a = 1.f - 2.f * rcp_approx(ex2_approx(2.8853900817779268f * y) + 1.f);
-          const float b = y + y * z * (-1.f / 3.f + z * (2.f / 15.f - z * (17.f / 315.f)));
-          sv[k] = p.cap_log2 * (z < 0.0625f ? b : a);
+          for (int k = 0; k < 8; ++k) {
+            const float2 x = make_float2(sv[j + 2 * k], sv[j + 2 * k + 1]);
+            y[k] = fmul2(x, inv2);
+            const float2 z = fmul2(y[k], y[k]);
+            r[k] = fmul2(fmul2(x, scale2), ffma2(z, ffma2(z, ffma2(z, s3, s2), s1), one));
+            top = fmax3(top, z.x, z.y);   // (passes over a NaN, which r has)
+          }
+          if (__any_sync(0xffffffffu, top >= 0.0625f)) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float2 a = fmul2(y[k], e2);
+              const float2 d = fadd2(make_float2(ex2_approx(a.x), ex2_approx(a.y)), one);
+              const float2 far = ffma2(make_float2(rcp_approx(d.x), rcp_approx(d.y)), m2c, cap2);
+              if (fabsf(y[k].x) >= 0.25f) r[k].x = far.x;
+              if (fabsf(y[k].y) >= 0.25f) r[k].y = far.y;
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            sv[j + 2 * k] = r[k].x;
+            sv[j + 2 * k + 1] = r[k].y;
+          }
         }
       }
       const int64_t pos0 = (int64_t)t * KEYS + 64 * half;
@@ -919,7 +934,7 @@ cudaError_t launch_tree_attention(const TreeParams& t, cudaStream_t stream) {
   p.oob_row = (int32_t)slots;
   p.o_align32 = (reinterpret_cast<uintptr_t>(t.o) & 31u) == 0;
   const float LOG2E = 1.4426950408889634f;
-  p.has_cap = t.soft_cap > 256.f ? 2 : t.soft_cap > 0.f ? 1 : 0;
+  p.has_cap = t.soft_cap > 0.f;
   p.scale_log2 = t.sm_scale * LOG2E;
   p.cap_log2 = p.has_cap ? t.soft_cap * LOG2E : 0.f;
   p.cap_inv = p.has_cap ? std::fmin(t.sm_scale / t.soft_cap, 1e38f) : 0.f;
