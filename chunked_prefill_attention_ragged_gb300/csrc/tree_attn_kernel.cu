@@ -725,8 +725,7 @@ __device__ void run_softmax(const Ctx& c, const TreeLaunch& p, Parts parts, uint
       const int col = 256 * half + 64 * q;
       uint32_t ov[64];
       tmem_ld64_sync(lane_addr + q * 64, ov);
-      if (!live) continue;
-      if (u.whole) {
+      if (live && u.whole) {
         uint32_t w[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
@@ -742,11 +741,12 @@ __device__ void run_softmax(const Ctx& c, const TreeLaunch& p, Parts parts, uint
           for (int k = 0; k < 8; ++k)
             reinterpret_cast<uint4*>(d)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
         }
-      } else {
+      } else if (live) {
         char* d = slot + slot_at(pr0, col);
 #pragma unroll
         for (int k = 0; k < 8; ++k) st_global_v8(d + slot_at(0, 8 * k), ov + 8 * k);
       }
+      __syncwarp();   // (the next load is one instruction of the whole warp)
     }
     if (live && half == 0) {
       if (u.whole) {
@@ -810,6 +810,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   find_piece<NTHREADS>(p.t, words, worker, p.workers, blockIdx.x == 0, &start, &count, &join);
   char* ws = static_cast<char*>(p.t.workspace);
   if (threadIdx.x == 0 && rank == 0) reinterpret_cast<JoinRec*>(ws)[worker] = join;
+  __syncwarp();
   cluster_wait();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
