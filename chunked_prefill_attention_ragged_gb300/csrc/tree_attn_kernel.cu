@@ -75,9 +75,9 @@ enum Bar {
   SF = VE + 2,         // [buffer] S done
   PR = SF + 2,         // P written (and the S buffer read) by every softmax warp of both CTAs
   OD,                  // P V done
-  LB,                  // the half of V to mend landed (in this CTA)
-  ZB,                  // the odd CTA has mended its own
-  XB,                  // [row half] maxima exchanged between the two warps of 32 rows
+  LB,                  // [key half] V to be mended landed (in this CTA)
+  ZB = LB + 2,         // [key half] the odd CTA has mended its own
+  XB = ZB + 2,         // [row half] maxima exchanged between the two warps of 32 rows
   FIN = XB + 2,        // every product drained
   NEVER,               // nothing arrives here: the time-out test mode waits on it
   NBAR
@@ -218,6 +218,56 @@ __device__ void run_producer_qk(const Ctx& c, const TreeLaunch& p, Parts parts, 
   }
 }
 
+__device__ __forceinline__ void st_shared_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// From which key on there are nodes that some row of the unit may not see (kv: none; a single new token sees
+// itself).
+__device__ __forceinline__ int64_t first_unseen(const TreeLaunch& p, const Part& u) {
+  return u.q.nodes < 2 && !p.t.mask ? u.q.kv : min(max(u.q.ctx, (int64_t)0), (int64_t)u.q.kv);
+}
+
+// A weight of 0 times a NaN or an infinity is NaN, and products take every row of the tile: in rows [from, to) of
+// 64 of V, those of nodes, a NaN becomes 0 (whoever sees it has a NaN score, the row being its key too) and an
+// infinity the largest finite value.  Rows lie in pieces of `low` + 1, each with its four panels; a lane has 16
+// bytes of a row.  The rows are looked through by their largest magnitude, a NaN above all, and only gone over
+// again if that is not finite.  (Not inline, to keep the producer's loop short.  A row at a time with a branch in
+// it took 9 x up to 37 nodes from 40.9 to 43.8 us, this way 41.5; calls of single tokens do not come here.)
+__device__ __noinline__ void mend_nodes(uint32_t at, int from, int to, int low) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t base = at + (lane >> 3) * (low + 1) * 128 + (lane & 7) * 16;
+  auto addr = [&](int row) { return base + (4 * (row & ~low) + (row & low)) * 128; };
+  auto load = [&](int row, uint32_t* v) {
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr(row)) : "memory");
+  };
+  auto most = [](uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  };
+  auto odd = [](uint32_t w) { return (((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u) != 0; };   // an exponent of all ones
+  uint32_t top[4] = {0u, 0u, 0u, 0u};
+  for (int row = from; row < to; row += 4) {
+    uint32_t v[4][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) load(min(row + k, to - 1), v[k]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) top[w] = most(top[w], v[k][w]);
+  }
+  if (!(odd(top[0]) || odd(top[1]) || odd(top[2]) || odd(top[3]))) return;
+  auto half = [](uint32_t h) { return (h & 0x7fffu) > 0x7f80u ? 0u : (h & 0x7fffu) == 0x7f80u ? h - 1 : h; };
+  for (int row = from; row < to; ++row) {
+    uint32_t v[4];
+    load(row, v);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) v[w] = half(v[w] & 0xffffu) | half(v[w] >> 16) << 16;
+    st_shared_v4(addr(row), v[0], v[1], v[2], v[3]);
+  }
+}
+
 // Where the block size is no multiple of 8, K (groups first .. first + n - 1, and Q beside group 0) or V
 // (n = 2 halves) row by row: the lanes' own copies, handed to the even CTA's barriers when they have
 // landed.  Bound by the threads' path from L2, 30 bytes a clock and SM: 16 requests of 4 nodes, 128 heads,
@@ -236,6 +286,7 @@ __device__ void run_rows(const Ctx& c, const TreeLaunch& p, Parts parts, const C
     int64_t key0 = (int64_t)u.lo * KEYS + (V ? 0 : 64 * c.rank);
     KeyBlocks b0 = find_blocks(p, u, key0, lane), b1{};
     if (V) b1 = find_blocks(p, u, key0 + 64, lane);
+    const int64_t unseen = V ? first_unseen(p, u) : 0;
     if (with_q) {
       if (lane == 0) {
         if (units > 0) ok = c.wait(QE, (units - 1) & 1);
@@ -271,6 +322,11 @@ __device__ void run_rows(const Ctx& c, const TreeLaunch& p, Parts parts, const C
       for (int i = 0; i < n && ok; ++i) {
         if (i + 1 < n) cp_async_wait<1>();
         else cp_async_wait<0>();
+        const int64_t a = key0 + 64 * i;
+        if (V && a + 64 > unseen && max(a, unseen) < u.q.kv) {
+          __syncwarp();   // (a row's pieces are other lanes' copies)
+          mend_nodes(dst + i * V_HALF, (int)max(unseen - a, (int64_t)0), (int)min(u.q.kv - a, (int64_t)64), 63);
+        }
         fence_async_shared();
         __syncwarp();
         if (lane == 0) {
@@ -295,10 +351,11 @@ __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, Parts parts, c
   const int lane = threadIdx.x & 31, panel0 = 4 * (int)c.rank;
   const uint32_t vf = mapa_shared(c.bar(VF), 0);
   int tiles = 0, issued = 0;
-  int mends = 0;   // tiles that have a half to mend
+  int mends[2] = {0, 0};   // halves mended so far
   bool ok = true;
   Part u;
   while (ok && parts.next(&u)) {
+    const int64_t unseen = first_unseen(p, u);
     int32_t ahead0 = 0, ahead1 = 0;   // rows of 32 tiles' first and second halves
     int32_t b0 = 0, b1 = 0;
     if (R != 64) {
@@ -314,10 +371,7 @@ __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, Parts parts, c
         ahead1 = piece_rows(p, u, key0 + 64, KEYS, u.hi - t, lane);
       }
       int32_t row0 = __shfl_sync(0xffffffffu, ahead0, j), row1 = __shfl_sync(0xffffffffu, ahead1, j);
-      // The half in which the keys end brings along what lies behind them.
-      const int64_t valid = u.q.kv - key0;
-      const bool ends = valid > 0 && valid < KEYS && valid != 64;
-      if (R == 64 && !ends) {   // one lane, two copies
+      if (R == 64 && key0 + KEYS <= unseen) {   // one lane, two copies
         if (lane == 0) {
 #pragma unroll 1
           for (int i = 0; i < 2; ++i) {
@@ -337,44 +391,57 @@ __device__ void run_producer_v(const Ctx& c, const TreeLaunch& p, Parts parts, c
             b1 = box_block(p, u, key0 + KEYS + 64, R, lane);
           }
         }
-        const int cut = !ends ? 2 : valid < 64 ? 0 : 1;   // the half to mend
+        // The half in which the keys end brings along what lies behind them, one with nodes what some may not see.
+        const int64_t valid = u.q.kv - key0;
+        const int cut = valid <= 0 || valid >= KEYS || valid == 64 ? 2 : valid < 64 ? 0 : 1;
+        auto nodes_in = [&](int i) { return unseen < u.q.kv && key0 + 64 * i + 64 > unseen && 64 * i < valid; };
+        const bool dirty0 = cut == 0 || nodes_in(0), dirty1 = cut == 1 || nodes_in(1);
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
+          const bool dirty = i ? dirty1 : dirty0;
           if (lane == 0) {
             if (tiles > 0) ok = c.wait(VE + i, (tiles - 1) & 1);
             if (ok) {
-              if (i == cut) mbar_arrive_expect_tx(c.bar(LB), V_HALF);
+              if (dirty) mbar_arrive_expect_tx(c.bar(LB + i), V_HALF);
               else expect_both(c, VF + i, V_HALF);
             }
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) break;
-          const uint32_t dst = c.sbase + OFF_V + i * V_HALF, bar = i == cut ? mapa_shared(c.bar(LB), c.rank) : vf + 8 * i;
+          const uint32_t dst = c.sbase + OFF_V + i * V_HALF, bar = dirty ? mapa_shared(c.bar(LB + i), c.rank) : vf + 8 * i;
           if (lane * R < 64) tma_load_3d_pair(dst + lane * R * 512, tv, bar, 0, i ? row1 : row0, panel0);
           ++issued;
         }
         // What came along behind the last key, as far as products read (16 keys at a time), is made zero
-        // (its P is 0, but 0 times what is there need not be).  Each CTA sees to its own, then the even
-        // one says that the half is there.
-        if (ends && ok) {
-          if (lane == 0) ok = c.wait(LB, mends & 1);
+        // (its P is 0, but 0 times what is there need not be), and nodes' rows finite.  Each CTA sees to its
+        // own, then the even one says that the half is there.
+#pragma unroll 1
+        for (int i = 0; i < 2 && ok; ++i) {
+          if (!(i ? dirty1 : dirty0)) continue;
+          const uint32_t phase = (i ? mends[1]++ : mends[0]++) & 1;
+          if (lane == 0) ok = c.wait(LB + i, phase);
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) break;
-          uint8_t* at = smem + OFF_V + cut * V_HALF;
+          __syncwarp();   // (what lane 0 acquired, for the others' reads)
+          uint8_t* at = smem + OFF_V + i * V_HALF;
           const int low = R - 1;   // (a power of two less one)
-          for (int k = lane; k < (-(int)valid & 15) * 32; k += 32) {
-            const int row = (int)(valid & 63) + (k >> 5), panel = (k >> 3) & 3;
-            *reinterpret_cast<uint4*>(at + (4 * (row & ~low) + panel * (low + 1) + (row & low)) * 128 + (k & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
+          if (i == cut) {
+            for (int k = lane; k < (-(int)valid & 15) * 32; k += 32) {
+              const int row = (int)(valid & 63) + (k >> 5), panel = (k >> 3) & 3;
+              *reinterpret_cast<uint4*>(at + (4 * (row & ~low) + panel * (low + 1) + (row & low)) * 128 + (k & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+            }
           }
+          if (nodes_in(i))
+            mend_nodes(c.sbase + OFF_V + i * V_HALF, (int)max(unseen - key0 - 64 * i, (int64_t)0),
+                       (int)min(valid - 64 * i, (int64_t)64), low);
           fence_async_shared();
           __syncwarp();
           if (lane == 0) {
-            if (c.rank != 0) mbar_arrive_remote(mapa_shared(c.bar(ZB), 0));
-            else if ((ok = c.wait(ZB, mends & 1))) mbar_arrive(c.bar(VF + cut));
+            if (c.rank != 0) mbar_arrive_remote(mapa_shared(c.bar(ZB + i), 0));
+            else if ((ok = c.wait(ZB + i, phase))) mbar_arrive(c.bar(VF + i));
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
-          ++mends;
         }
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -550,10 +617,6 @@ __device__ void run_mma(const Ctx& c, const TreeLaunch& p, Parts parts, uint32_t
 }
 
 // ------------------------------------------------------------------ softmax (warps 4-7)
-__device__ __forceinline__ void st_shared_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
-
 __device__ void run_softmax(const Ctx& c, const TreeLaunch& p, Parts parts, uint32_t tmem, char* ws_slots, uint8_t* smem) {
   const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3;
   const int half = q4 >> 1, rg = q4 & 1;             // key / column half, group of 32 rows

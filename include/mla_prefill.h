@@ -459,9 +459,10 @@ MLA_API int mla_tree_workspace(int64_t total_rows, int num_heads, int64_t* bytes
  *   status     : DEVICE int32 word or NULL
  * A row that sees no key gets O = 0, LSE = -inf; a NaN in a row of q_abs makes that row NaN.
  * Positions at or past kv_len never count (rows behind the last key may be read inside its
- * block; what is in them does not matter). 
- * Cache rows below kv_len are to be finite: an infinity or NaN in a row that a node does not
- * see may still reach the other rows of its request.  MLA_DEVSTAT_BAD_INDEX is OR-ed in for a
+ * block; what is in them does not matter).  Nor does what is in the cached row of a node that a
+ * row does not see, NaN and infinities included; a node that sees a NaN is NaN, and where a soft
+ * cap leaves an infinity a finite weight it counts as the largest finite value.
+ * MLA_DEVSTAT_BAD_INDEX is OR-ed in for a
  * block id outside [0, num_blocks) (its rows read as zeros), kv_len outside
  * [0, max_blocks_per_req * block_size] (clamped), or a request whose rows are not inside
  * total_rows (skipped); MLA_DEVSTAT_TIMEOUT when a pipeline wait gave up (after 2 s, or in the test
