@@ -396,8 +396,12 @@ MLA_API int mla_absorbed_run(mla_plan_t plan, const void* q_abs, const void* cac
  * back on the stack first (entries become -1), then missing ones are taken, request by request.
  * A request is served when all requests up to it can be: otherwise it keeps what it holds, and
  * MLA_DEVSTAT_NO_BLOCKS is OR-ed into status.  Entries of a row behind those in use may hold
- * anything; those that a request which is not served would have needed become -1.  Reserving
- * blocks and giving the same ones back restores the stack.  seq = new = 0 releases a row.
+ * anything; those that a request which is not served would have needed become -1.  It is still
+ * counted in qo_indptr and kv_lens, and num_held[r] * block_size < kv_lens[r] tells it from the
+ * others: what the step's other calls give for it means nothing (its missing rows are neither
+ * stored nor moved, and read as zeros) and is dropped; the other requests are not touched by it.
+ * Block ids are not compared with a cache here; the calls that read it report one past its end.
+ * Reserving blocks and giving the same ones back restores the stack.  seq = new = 0 releases a row.
  * MLA_DEVSTAT_BAD_INDEX is OR-ed in for a negative length or one that passes 2^31 - 1 with its
  * new tokens, num_held or free_count outside its range (all clamped), a request that needs more
  * than max_blocks_per_req blocks (it is not served), a full stack (the block is lost), a negative
