@@ -569,8 +569,10 @@ def _arg(t, dtype, dev, name, shape=None):
 
 def _status_arg(t, dtype, dev):
     """Address of a status word; one without an element would pass for none."""
+    if t is None:
+        return None
     at = _arg(t, dtype, dev, "status")
-    if at is not None and t.numel() == 0:
+    if t.numel() == 0:
         raise ValueError("status must have an element")
     return at
 
