@@ -33,11 +33,18 @@
 // of that, by boxes of 32, 16 or 8 where it is one of these (in the piece where the keys end, what lies
 // behind them is made zero), else row by row by the producers' own lanes.  The kernel is compiled for
 // each: with strides of the operands read from registers the products' issue took 3% longer.
-// What bounds it: for one node a request HBM (64 requests over 4096 positions, 16 heads: 65 us with the
-// join, 6 TB/s while tiles run); for many the products and what feeds them (32 x 16 nodes over 8192, 128
-// heads: 772-815 us, 0.77-0.81 of the measured tensor rate: a tile is 2176 clocks of products, 392 KB
-// through shared memory and 272 KB from L2, and takes 2700-2950).  Calls of few tiles cost 14 us: 3.5 to
-// the first copy, a tile, the state and the join.
+// What bounds it: for one node a request HBM (64 requests over 4096 positions, 16 heads: 66 us with the
+// join, a copy's rate while tiles run; 8 us pass before the first scores are there); for many the products
+// and what feeds them (32 x 16 nodes over 8192, 128 heads: 772-815 us in replayed graphs, 0.77-0.81 of the
+// measured tensor rate, and 900-930 in calls back to back, when the power cap lowers the clock: 0.74-0.76 of
+// the rate that then holds.  A tile is 2176 clocks of products, 392 KB through shared memory and 272 KB from
+// L2, and takes 2700-2950).  Calls of few tiles cost 14 us: 2.3 to the first copy, a tile, the state and the
+// join.
+//
+// Roundings: scores, maxima, sums, O and the parts are fp32.  P is rounded to bf16, as products with bf16 values
+// have to have it: each weight is off by up to 2^-8 of itself, O by up to 2^-8 sum P |V| / l, in practice
+// less than its own rounding to bf16 adds (both: 0.0017 to 0.0020 of O's norm, O's alone 0.0017).  The sum l, and with it the LSE, is
+// of the unrounded weights.
 // Every wait is bounded: on time-out the CTA records MLA_DEVSTAT_TIMEOUT, drains its copies and
 // products, frees TMEM and returns.
 #include <cmath>

@@ -456,7 +456,8 @@ MLA_API int mla_tree_workspace(int64_t total_rows, int num_heads, int64_t* bytes
  *                are set, its own only if set; a node past 64 * mask_words is not seen.  NULL
  *                (mask_words 0): node i sees nodes 0 .. i, a chain
  *   sm_scale   : finite and > 0; logits_soft_cap: <= 0 none, c > 0: c * tanh(x / c)
- *   o_lat      : bf16 [total_rows, num_heads, 512]  (written)
+ *   o_lat      : bf16 [total_rows, num_heads, 512]  (written).  Weights are rounded to bf16 for
+ *                their product with the values; everything else is fp32
  *   lse        : fp32 [total_rows, num_heads], natural log, or NULL  (written)
  *   workspace  : DEVICE, 32-byte aligned, at least mla_tree_workspace bytes, not in use by
  *                another call that may run at the same time; its contents do not matter
