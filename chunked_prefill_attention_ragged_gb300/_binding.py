@@ -59,6 +59,14 @@ _SIGNATURES = {
     "mla_tree_workspace": (_c_int, [_c_i64, _c_int, _i64p]),
     "mla_tree_attention": (_c_int, [_c_vp, _c_vp, _c_i64, _c_int, _c_vp, _c_int, _c_vp, _c_vp, _c_vp, _c_int, _c_int,
                                     _c_i64, _c_int, _c_f, _c_f, _c_vp, _c_vp, _c_vp, _c_i64, _c_vp, _c_vp]),
+    "mla_tree_attention_fp4": (_c_int, [_c_vp, _c_vp, _c_i64, _c_int, _c_vp, _c_int, _c_vp, _c_vp, _c_vp, _c_int, _c_int,
+                                        _c_i64, _c_int, _c_f, _c_f, _c_vp, _c_vp, _c_vp, _c_i64, _c_vp, _c_vp]),
+    "mla_tree_verify": (_c_int, [_c_vp, _c_vp, _c_int, _c_i64, _c_vp, _c_vp, _c_vp, _c_int, _c_i64, _c_vp, _c_vp, _c_vp,
+                                 _c_int, _c_vp, _c_vp, _c_vp, _c_vp]),
+    "mla_cache_append": (_c_int, [_c_vp, _c_int, _c_i64, _c_int, _c_vp, _c_i64, _c_vp, _c_f, _c_vp, _c_vp, _c_i64, _c_int,
+                                  _c_vp, _c_i64, _c_vp, _c_i64, _c_i64, _c_int, _c_vp, _c_i64, _c_i64, _c_vp, _c_vp]),
+    "mla_gather_latent_fp4": (_c_int, [_c_vp, _c_i64, _c_int, _c_int, _c_vp, _c_int, _c_vp, _c_vp, _c_int, _c_i64,
+                                       _c_vp, _c_vp, _c_vp]),
     "mla_tree_commit": (_c_int, [_c_vp, _c_int, _c_i64, _c_i64, _c_int, _c_int, _c_vp, _c_int, _c_vp, _c_vp, _c_vp,
                                  _c_int, _c_int, _c_vp, _c_vp]),
 }
@@ -681,18 +689,12 @@ def mla_tree_workspace(total_rows: int, num_heads: int) -> int:
     return int(n.value)
 
 
-def mla_tree_attention(q_abs, cache, block_table, qo_indptr, kv_lens, tree_mask=None, *, sm_scale: float,
-                       logits_soft_cap: float = 0.0, o=None, lse=None, return_lse: bool = True, workspace=None,
-                       status=None, stream=None):
-    """Drafted nodes (or single new tokens) over the paged latent cache: q_abs [T, H, 576],
-    cache [NB, BS, 576] bf16, block_table [B, M], qo_indptr [B+1], kv_lens [B] int32 (all on the
-    device), tree_mask [T, W] int64 from mla_tree_mask (None: each node sees those before it)
-    -> (o_lat [T, H, 512] bf16, lse [T, H] fp32 or None).  The workspace (uint8) is allocated
-    for the call when not given; one that is given must not serve two calls at a time."""
+def _tree_attention(name, kind, width, q_abs, cache, block_table, qo_indptr, kv_lens, tree_mask, sm_scale,
+                    logits_soft_cap, o, lse, return_lse, workspace, status, stream):
     T, dev, st, handle = _here(stream, q_abs, "q_abs")
     int32, bfloat16, float32, uint8 = T.int32, T.bf16, T.f32, T.uint8
-    if q_abs.dim() != 3 or q_abs.shape[2] != 576 or cache.dim() != 3 or cache.shape[2] != 576:
-        raise ValueError("q_abs must be [T, H, 576] and cache [NB, BS, 576]")
+    if q_abs.dim() != 3 or q_abs.shape[2] != 576 or cache.dim() != 3 or cache.shape[2] != width:
+        raise ValueError(f"q_abs must be [T, H, 576] and cache [NB, BS, {width}]")
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, M]")
     t, h, _ = q_abs.shape
@@ -712,14 +714,66 @@ def mla_tree_attention(q_abs, cache, block_table, qo_indptr, kv_lens, tree_mask=
         if n is None:
             n = _workspace_bytes[dev] = mla_tree_workspace(t, h)
         workspace = _new(T, (n,), uint8, device, st)
-    _check((_lib or library()).mla_tree_attention(
-        _arg(q_abs, bfloat16, dev, "q_abs"), _arg(cache, bfloat16, dev, "cache"), cache.shape[0], cache.shape[1],
+    _check(getattr(_lib or library(), name)(
+        _arg(q_abs, bfloat16, dev, "q_abs"), _arg(cache, getattr(T, kind), dev, "cache"), cache.shape[0], cache.shape[1],
         _arg(block_table, int32, dev, "block_table"), m, _arg(qo_indptr, int32, dev, "qo_indptr", (b + 1,)),
         _arg(kv_lens, int32, dev, "kv_lens", (b,)), _arg(tree_mask, T.int64, dev, "tree_mask"), words, b, t, h,
         float(sm_scale), float(logits_soft_cap), _arg(o, bfloat16, dev, "o", (t, h, 512)),
         _arg(lse, float32, dev, "lse", (t, h)), _arg(workspace, uint8, dev, "workspace"), workspace.numel(),
-        _status_arg(status, int32, dev), handle), "mla_tree_attention")
+        _status_arg(status, int32, dev), handle), name)
     return o, lse
+
+
+def mla_tree_attention(q_abs, cache, block_table, qo_indptr, kv_lens, tree_mask=None, *, sm_scale: float,
+                       logits_soft_cap: float = 0.0, o=None, lse=None, return_lse: bool = True, workspace=None,
+                       status=None, stream=None):
+    """Drafted nodes (or single new tokens) over the paged latent cache: q_abs [T, H, 576],
+    cache [NB, BS, 576] bf16, block_table [B, M], qo_indptr [B+1], kv_lens [B] int32 (all on the
+    device), tree_mask [T, W] int64 from mla_tree_mask (None: each node sees those before it)
+    -> (o_lat [T, H, 512] bf16, lse [T, H] fp32 or None).  The workspace (uint8) is allocated
+    for the call when not given; one that is given must not serve two calls at a time."""
+    return _tree_attention("mla_tree_attention", "bf16", 576, q_abs, cache, block_table, qo_indptr, kv_lens, tree_mask,
+                           sm_scale, logits_soft_cap, o, lse, return_lse, workspace, status, stream)
+
+
+def mla_tree_attention_fp4(q_abs, cache, block_table, qo_indptr, kv_lens, tree_mask=None, *, sm_scale: float,
+                           logits_soft_cap: float = 0.0, o=None, lse=None, return_lse: bool = True, workspace=None,
+                           status=None, stream=None):
+    """mla_tree_attention over a cache of 4-bit entries, uint8 [NB, BS, 400]; the rest as there."""
+    return _tree_attention("mla_tree_attention_fp4", "uint8", 400, q_abs, cache, block_table, qo_indptr, kv_lens,
+                           tree_mask, sm_scale, logits_soft_cap, o, lse, return_lse, workspace, status, stream)
+
+
+def mla_tree_verify(target_probs, tokens, qo_indptr, uniforms, final_uniforms, max_accepted: int, parents=None,
+                    draft_probs=None, accepted=None, accepted_counts=None, next_tokens=None, status=None, stream=None):
+    """Which drafted nodes are kept: target_probs [T, V] (fp32 or bf16) after each node, tokens [T],
+    parents [T] (None: chains), qo_indptr [B+1] int32, uniforms [T] and final_uniforms [B] fp32 in
+    [0, 1), draft_probs [T, V] like target_probs if the nodes were drawn from them (None: given)
+    -> (accepted [B, max_accepted] int32, -1 behind each path, accepted_counts [B], next_tokens [B])."""
+    T, dev, st, handle = _here(stream, target_probs, "target_probs")
+    int32, f32 = T.int32, T.f32
+    if target_probs.dim() != 2 or tokens.dim() != 1 or final_uniforms.dim() != 1:
+        raise ValueError("target_probs must be [T, V], tokens [T] and final_uniforms [B]")
+    t, vocab = target_probs.shape
+    b, n, device, kind = final_uniforms.shape[0], int(max_accepted), target_probs.device, target_probs.dtype
+    if kind is not f32 and kind is not T.bf16:
+        raise TypeError(f"target_probs must be torch.float32 or torch.bfloat16, got {kind}")
+    if n < 1:
+        raise ValueError("max_accepted must be at least 1")
+    if accepted is None:
+        accepted = _new(T, (b, n), int32, device, st)
+    if accepted_counts is None:
+        accepted_counts = _new(T, (b,), int32, device, st)
+    if next_tokens is None:
+        next_tokens = _new(T, (b,), int32, device, st)
+    _check((_lib or library()).mla_tree_verify(
+        _arg(target_probs, kind, dev, "target_probs"), _arg(draft_probs, kind, dev, "draft_probs", (t, vocab)),
+        0 if kind is f32 else 1, vocab, _arg(tokens, int32, dev, "tokens", (t,)), _arg(parents, int32, dev, "parents", (t,)),
+        _arg(qo_indptr, int32, dev, "qo_indptr", (b + 1,)), b, t, _arg(uniforms, f32, dev, "uniforms", (t,)),
+        _arg(final_uniforms, f32, dev, "final_uniforms"), _arg(accepted, int32, dev, "accepted", (b, n)), n,
+        _arg(accepted_counts, int32, dev, "accepted_counts", (b,)), _arg(next_tokens, int32, dev, "next_tokens", (b,)),
+        _status_arg(status, int32, dev), handle), "mla_tree_verify")
+    return accepted, accepted_counts, next_tokens
 
 
 def mla_tree_commit(cache, block_table, seq_lens, accepted, accepted_counts, status=None, stream=None):
@@ -740,3 +794,76 @@ def mla_tree_commit(cache, block_table, seq_lens, accepted, accepted_counts, sta
         _arg(accepted, int32, dev, "accepted", (b, a)), _arg(accepted_counts, int32, dev, "accepted_counts", (b,)),
         b, a, _status_arg(status, int32, dev), handle), "mla_tree_commit")
     return cache
+
+
+# ---------------------------------------------------------------------------- entries of several formats
+def _view(t, dtype, dev, name):
+    """Address of a tensor whose last dimension is contiguous, on the current device."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype or t.get_device() != dev:
+        _bad_tensor(t, dtype, dev, name)
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return t.data_ptr()
+
+
+def mla_cache_append(cache, latent, slot_mapping, positions, cos_sin, norm_weight=None, norm_eps: float = 1e-6,
+                     interleaved: bool = True, q_rope=None, q_out=None, status=None, stream=None):
+    """New tokens into the paged cache, [NB, BS, 576] bf16, [NB, BS, 648] uint8 (fp8) or [NB, BS, 400]
+    uint8 (fp4): latent [T, 576] bf16 (rows may be strided, its rope not rotated), slot_mapping [T]
+    int64 (negative: padding), positions [T] int32, cos_sin [P, 64] fp32 (32 cosines, 32 sines),
+    norm_weight [512] bf16 or None.  q_rope [T, H, 64] bf16 (a strided view, e.g. q[..., 128:]) is
+    rotated into q_out (another view, e.g. q_abs[..., 512:]; None: in place).  Returns the cache."""
+    T, dev, _, handle = _here(stream, cache, "cache")
+    bf16 = T.bf16
+    if cache.dim() != 3 or latent.dim() != 2 or latent.shape[1] != 576 or cos_sin.dim() != 2:
+        raise ValueError("cache must be [NB, BS, E], latent [T, 576] and cos_sin [P, 64]")
+    nb, bs, e = cache.shape
+    if cache.dtype is bf16:
+        entry = 0 if e == 576 else None
+    else:
+        entry = {648: 1, 400: 2}.get(e)
+    if entry is None:
+        raise ValueError("cache must be [NB, BS, 576] bf16 or [NB, BS, 648 or 400] uint8")
+    t = latent.shape[0]
+    h, q = 0, (None, 0, 0, 0, None, 0, 0)
+    if q_rope is not None:
+        if q_out is None:
+            q_out = q_rope
+        if q_rope.dim() != 3 or q_rope.shape[0] != t or q_rope.shape[2] != 64 or q_out.shape != q_rope.shape:
+            raise ValueError(f"q_rope and q_out must be [{t}, H, 64]")
+        h = q_rope.shape[1]
+        if h and t:
+            q = (_view(q_rope, bf16, dev, "q_rope"), q_rope.stride(0), q_rope.stride(1), h,
+                 _view(q_out, bf16, dev, "q_out"), q_out.stride(0), q_out.stride(1))
+    elif q_out is not None:
+        raise ValueError("q_out without q_rope")
+    _check((_lib or library()).mla_cache_append(
+        _arg(cache, bf16 if entry == 0 else T.uint8, dev, "cache"), entry, nb, bs, _view(latent, bf16, dev, "latent"),
+        latent.stride(0) if t > 1 else 576, _arg(norm_weight, bf16, dev, "norm_weight", (512,)), float(norm_eps),
+        _arg(positions, T.int32, dev, "positions", (t,)), _arg(cos_sin, T.f32, dev, "cos_sin", (cos_sin.shape[0], 64)),
+        cos_sin.shape[0], int(bool(interleaved)), _arg(slot_mapping, T.int64, dev, "slot_mapping", (t,)), t, *q,
+        _status_arg(status, T.int32, dev), handle), "mla_cache_append")
+    return cache
+
+
+def mla_gather_latent_fp4(cache, block_table, cu_seq_lens, chunk_starts, total_tokens: int, out=None, status=None,
+                          stream=None):
+    """One prefix chunk out of a 4-bit paged cache (uint8 [NB, BS, 400]), dequantized to
+    bf16 [total_tokens, 576]."""
+    T, dev, st, handle = _here(stream, cache, "cache")
+    if cache.dim() != 3 or cache.shape[2] != 400 or block_table.dim() != 2:
+        raise ValueError("cache must be [NB, BS, 400] and block_table [B, M]")
+    nb, bs, e = cache.shape
+    t, (batch, width) = int(total_tokens), block_table.shape
+    if out is None:
+        out = _new(T, (t, 576), T.bf16, cache.device, st)
+    i32 = T.int32
+    _check((_lib or library()).mla_gather_latent_fp4(
+        _arg(cache, T.uint8, dev, "cache"), nb, bs, e, _arg(block_table, i32, dev, "block_table"), width,
+        _arg(cu_seq_lens, i32, dev, "cu_seq_lens", (batch + 1,)), _arg(chunk_starts, i32, dev, "chunk_starts", (batch,)),
+        batch, t, _arg(out, T.bf16, dev, "out", (t, 576)), _status_arg(status, i32, dev), handle),
+        "mla_gather_latent_fp4")
+    return out

@@ -38,6 +38,11 @@ SOURCES = [
     "tree_kernels.cu",
     "tree_attn_kernel.cu",
     "tree_join_kernel.cu",
+    "verify_kernel.cu",
+    "entry_abi.cpp",
+    "append_kernel.cu",
+    "fp4_gather_kernel.cu",
+    "tree_attn_fp4_kernel.cu",
 ]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

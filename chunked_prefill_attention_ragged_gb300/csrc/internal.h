@@ -175,6 +175,53 @@ struct CommitParams {
 };
 cudaError_t launch_tree_commit(const CommitParams& p, int batch, cudaStream_t stream);
 
+struct VerifyParams {
+  const void *target, *draft;           // [total_rows, vocab] fp32 or bf16; draft may be null
+  int64_t vocab;
+  const int32_t *tokens, *parents;      // [total_rows]; parents may be null: a chain
+  const int32_t* qo;                    // [batch + 1]
+  int64_t total_rows;
+  const float *uniforms, *final_uniforms;   // [total_rows], [batch]
+  int32_t* accepted;                    // [batch, max_accepted]
+  int max_accepted;
+  int32_t *counts, *next;               // [batch]
+  int32_t* status;
+  int wide, ranks;                      // set by launch_verify: 16-byte loads, CTAs of a request
+};
+constexpr int64_t kMaxVocab = 1 << 24;
+int verify_ranks(int64_t vocab);
+cudaError_t launch_verify(VerifyParams p, int batch, bool bf16, cudaStream_t stream);
+
+// ---- latent cache entries of several formats ---------------------------------------
+struct AppendParams {
+  uint8_t* cache;                       // slot s at cache + s * entry bytes
+  int64_t num_slots;
+  const __nv_bfloat16* latent;          // [num_tokens] rows of 576
+  int64_t latent_stride;
+  const __nv_bfloat16* norm_weight;     // [512] or null
+  float norm_eps;
+  const int32_t* positions;             // [num_tokens]
+  const float* cos_sin;                 // [max_positions, 64]
+  int64_t max_positions;
+  int interleaved;
+  const int64_t* slots;                 // [num_tokens]
+  int64_t num_tokens;
+  const __nv_bfloat16* q_rope;          // may be q_out
+  int64_t q_token, q_head;
+  int num_heads;
+  __nv_bfloat16* q_out;
+  int64_t q_out_token, q_out_head;
+  int32_t* status;
+};
+cudaError_t launch_append(const AppendParams& p, int format, cudaStream_t stream);
+
+cudaError_t launch_gather_fp4(const void* cache, int64_t num_blocks, int block_size, const int32_t* block_table,
+                              int max_blocks_per_req, const int32_t* cu_seq_lens, const int32_t* chunk_starts,
+                              int batch, int64_t total_tokens, void* out, int32_t* status, cudaStream_t stream);
+
+// As launch_tree_attention, over 400-byte entries (TreeParams.cache is their address).
+cudaError_t launch_tree_attention_fp4(const TreeParams& p, cudaStream_t stream);
+
 // MLA_PLAN_CTA_PAIRS: 1 when "1" (plan prefills on CTA pairs), 0 when "0", -1 otherwise.
 int cta_pair_mode();
 

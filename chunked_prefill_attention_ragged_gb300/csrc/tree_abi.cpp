@@ -16,6 +16,54 @@ inline bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_byt
 }
 inline int done(cudaError_t e) { return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA; }
 
+// The checks of both tree attentions; `launch` gets the parameters.
+int tree_attention(const void* q_abs, const void* cache, int64_t num_blocks, int block_size,
+                   const int32_t* block_table, int max_blocks_per_req, const int32_t* qo_indptr,
+                   const int32_t* kv_lens, const int64_t* tree_mask, int mask_words, int batch, int64_t total_rows,
+                   int num_heads, float sm_scale, float logits_soft_cap, void* o_lat, float* lse, void* workspace,
+                   int64_t workspace_bytes, int32_t* status, void* stream,
+                   cudaError_t (*launch)(const TreeParams&, cudaStream_t)) {
+  if (batch < 0 || total_rows < 0 || num_blocks < 0 || block_size < 1 || max_blocks_per_req < 0 || num_heads < 1 ||
+      num_heads > 65535 || !std::isfinite(sm_scale) || !(sm_scale > 0.f) || !std::isfinite(logits_soft_cap))
+    return MLA_ERR_INVALID_ARG;
+  if (tree_mask ? (mask_words < 1) : (mask_words != 0)) return MLA_ERR_INVALID_ARG;
+  // Slots are TMA row coordinates (int32), and one past the last slot marks a missing row;
+  // so are the (row, head) pairs.
+  if (total_rows > kMaxTreePairs || total_rows * num_heads > kMaxTreePairs || mask_words > kMaxMaskWords ||
+      num_blocks > 0x7fffffff || num_blocks * (int64_t)block_size >= 0x7fffffff ||
+      (int64_t)max_blocks_per_req * block_size > 0x7fffff00)
+    return MLA_ERR_UNSUPPORTED;
+  if (!aligned(q_abs, 16) || !aligned(cache, 16) || !aligned(o_lat, 16) || !aligned(workspace, 32) ||
+      !aligned(block_table, 4) || !aligned(qo_indptr, 4) || !aligned(kv_lens, 4) || !aligned(tree_mask, 8) ||
+      !aligned(lse, 4) || !aligned(status, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (batch == 0 || total_rows == 0) return MLA_OK;
+  if (!q_abs || !o_lat || !qo_indptr || !kv_lens || !workspace) return MLA_ERR_INVALID_ARG;
+  if (max_blocks_per_req > 0 && num_blocks > 0 && (!cache || !block_table)) return MLA_ERR_INVALID_ARG;
+  if (workspace_bytes < tree_workspace_bytes()) return MLA_ERR_INVALID_ARG;
+  TreeParams p;
+  p.q = static_cast<const __nv_bfloat16*>(q_abs);
+  p.cache = static_cast<const __nv_bfloat16*>(cache);
+  p.num_blocks = num_blocks;
+  p.block_size = block_size;
+  p.block_table = block_table;
+  p.max_blocks = num_blocks > 0 ? max_blocks_per_req : 0;
+  p.qo_indptr = qo_indptr;
+  p.kv_lens = kv_lens;
+  p.mask = tree_mask;
+  p.mask_words = mask_words;
+  p.batch = batch;
+  p.total_rows = total_rows;
+  p.num_heads = num_heads;
+  p.sm_scale = sm_scale;
+  p.soft_cap = logits_soft_cap > 0.f ? logits_soft_cap : 0.f;
+  p.o = static_cast<__nv_bfloat16*>(o_lat);
+  p.lse = lse;
+  p.workspace = workspace;
+  p.status = status;
+  return done(launch(p, as_stream(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -91,45 +139,53 @@ int mla_tree_attention(const void* q_abs, const void* cache, int64_t num_blocks,
                        const int32_t* kv_lens, const int64_t* tree_mask, int mask_words, int batch, int64_t total_rows,
                        int num_heads, float sm_scale, float logits_soft_cap, void* o_lat, float* lse, void* workspace,
                        int64_t workspace_bytes, int32_t* status, void* stream) {
-  if (batch < 0 || total_rows < 0 || num_blocks < 0 || block_size < 1 || max_blocks_per_req < 0 || num_heads < 1 ||
-      num_heads > 65535 || !std::isfinite(sm_scale) || !(sm_scale > 0.f) || !std::isfinite(logits_soft_cap))
+  return tree_attention(q_abs, cache, num_blocks, block_size, block_table, max_blocks_per_req, qo_indptr, kv_lens,
+                        tree_mask, mask_words, batch, total_rows, num_heads, sm_scale, logits_soft_cap, o_lat, lse, workspace,
+                        workspace_bytes, status, stream, launch_tree_attention);
+}
+
+int mla_tree_attention_fp4(const void* q_abs, const void* cache, int64_t num_blocks, int block_size,
+                           const int32_t* block_table, int max_blocks_per_req, const int32_t* qo_indptr,
+                           const int32_t* kv_lens, const int64_t* tree_mask, int mask_words, int batch, int64_t total_rows,
+                           int num_heads, float sm_scale, float logits_soft_cap, void* o_lat, float* lse, void* workspace,
+                           int64_t workspace_bytes, int32_t* status, void* stream) {
+  return tree_attention(q_abs, cache, num_blocks, block_size, block_table, max_blocks_per_req, qo_indptr, kv_lens,
+                        tree_mask, mask_words, batch, total_rows, num_heads, sm_scale, logits_soft_cap, o_lat, lse, workspace,
+                        workspace_bytes, status, stream, launch_tree_attention_fp4);
+}
+
+int mla_tree_verify(const void* target_probs, const void* draft_probs, int prob_type, int64_t vocab,
+                    const int32_t* tokens, const int32_t* parents, const int32_t* qo_indptr, int batch,
+                    int64_t total_rows, const float* uniforms, const float* final_uniforms, int32_t* accepted,
+                    int max_accepted, int32_t* accepted_counts, int32_t* next_tokens, int32_t* status, void* stream) {
+  if (prob_type < 0 || prob_type > 1 || vocab < 1 || batch < 0 || total_rows < 0 || max_accepted < 1)
     return MLA_ERR_INVALID_ARG;
-  if (tree_mask ? (mask_words < 1) : (mask_words != 0)) return MLA_ERR_INVALID_ARG;
-  // Slots are TMA row coordinates (int32), and one past the last slot marks a missing row;
-  // so are the (row, head) pairs.
-  if (total_rows > kMaxTreePairs || total_rows * num_heads > kMaxTreePairs || mask_words > kMaxMaskWords ||
-      num_blocks > 0x7fffffff || num_blocks * (int64_t)block_size >= 0x7fffffff ||
-      (int64_t)max_blocks_per_req * block_size > 0x7fffff00)
+  if (vocab > kMaxVocab || total_rows > 0x7fffffff || (int64_t)batch * verify_ranks(vocab) > 0x7fffffff)
     return MLA_ERR_UNSUPPORTED;
-  if (!aligned(q_abs, 16) || !aligned(cache, 16) || !aligned(o_lat, 16) || !aligned(workspace, 32) ||
-      !aligned(block_table, 4) || !aligned(qo_indptr, 4) || !aligned(kv_lens, 4) || !aligned(tree_mask, 8) ||
-      !aligned(lse, 4) || !aligned(status, 4))
+  const uintptr_t element = prob_type == 0 ? 4 : 2;
+  if (!aligned(target_probs, element) || !aligned(draft_probs, element) || !aligned(tokens, 4) ||
+      !aligned(parents, 4) || !aligned(qo_indptr, 4) || !aligned(uniforms, 4) || !aligned(final_uniforms, 4) ||
+      !aligned(accepted, 4) || !aligned(accepted_counts, 4) || !aligned(next_tokens, 4) || !aligned(status, 4))
     return MLA_ERR_INVALID_ARG;
-  if (batch == 0 || total_rows == 0) return MLA_OK;
-  if (!q_abs || !o_lat || !qo_indptr || !kv_lens || !workspace) return MLA_ERR_INVALID_ARG;
-  if (max_blocks_per_req > 0 && num_blocks > 0 && (!cache || !block_table)) return MLA_ERR_INVALID_ARG;
-  if (workspace_bytes < tree_workspace_bytes()) return MLA_ERR_INVALID_ARG;
-  TreeParams p;
-  p.q = static_cast<const __nv_bfloat16*>(q_abs);
-  p.cache = static_cast<const __nv_bfloat16*>(cache);
-  p.num_blocks = num_blocks;
-  p.block_size = block_size;
-  p.block_table = block_table;
-  p.max_blocks = num_blocks > 0 ? max_blocks_per_req : 0;
-  p.qo_indptr = qo_indptr;
-  p.kv_lens = kv_lens;
-  p.mask = tree_mask;
-  p.mask_words = mask_words;
-  p.batch = batch;
-  p.total_rows = total_rows;
-  p.num_heads = num_heads;
-  p.sm_scale = sm_scale;
-  p.soft_cap = logits_soft_cap > 0.f ? logits_soft_cap : 0.f;
-  p.o = static_cast<__nv_bfloat16*>(o_lat);
-  p.lse = lse;
-  p.workspace = workspace;
-  p.status = status;
-  return done(launch_tree_attention(p, as_stream(stream)));
+  if (batch == 0) return MLA_OK;
+  if (!qo_indptr || !final_uniforms || !accepted || !accepted_counts || !next_tokens) return MLA_ERR_INVALID_ARG;
+  if (total_rows > 0 && (!target_probs || !tokens || !uniforms)) return MLA_ERR_INVALID_ARG;
+  VerifyParams v = {};
+  v.target = target_probs;
+  v.draft = draft_probs;
+  v.vocab = vocab;
+  v.tokens = tokens;
+  v.parents = parents;
+  v.qo = qo_indptr;
+  v.total_rows = total_rows;
+  v.uniforms = uniforms;
+  v.final_uniforms = final_uniforms;
+  v.accepted = accepted;
+  v.max_accepted = max_accepted;
+  v.counts = accepted_counts;
+  v.next = next_tokens;
+  v.status = status;
+  return done(launch_verify(v, batch, prob_type == 1, as_stream(stream)));
 }
 
 int mla_tree_commit(void* cache, int num_layers, int64_t layer_stride, int64_t num_blocks, int block_size,

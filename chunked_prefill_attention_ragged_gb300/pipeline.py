@@ -20,7 +20,8 @@ of every chunk's latent rows (one launch, large enough to run near HBM
 bandwidth) feeds mla_up_proj; with fuse_merge=False the attention writes its
 own O/LSE and mla_merge_state merges them.  With cache_fp8=True the cache holds
 648-byte fp8 entries (vLLM sparse_mla.py's fp8_ds_mla layout, see
-mla_gather_latent_fp8): one dequantizing gather of every chunk feeds
+mla_gather_latent_fp8), with cache_fp4=True 400-byte 4-bit ones
+(mla_gather_latent_fp4): one dequantizing gather of every chunk feeds
 mla_up_proj.  Chunking bounds the decompressed
 K/V (per chunk tokens x heads x 640 bytes).  Every step is a kernel of
 libmla_prefill.so; this class only owns buffers and orders the calls on one
@@ -30,7 +31,7 @@ from __future__ import annotations
 
 import numpy as np
 
-from ._binding import (mla_gather_latent, mla_gather_latent_fp8, mla_merge_state, mla_prefill_plan,
+from ._binding import (mla_gather_latent, mla_gather_latent_fp4, mla_gather_latent_fp8, mla_merge_state, mla_prefill_plan,
                        mla_prefill_run_shared_rope, mla_up_proj, mla_up_proj_paged, mla_up_proj_paged_split)
 
 
@@ -43,8 +44,10 @@ class ChunkedPrefill:
 
     def __init__(self, qo_indptr, cu_seq_lens, chunk_starts, num_heads: int, *, sm_scale: float,
                  logits_soft_cap: float = 0.0, device="cuda", stream=None, fuse_merge: bool = True,
-                 paged_up_proj: bool = True, cache_fp8: bool = False):
+                 paged_up_proj: bool = True, cache_fp8: bool = False, cache_fp4: bool = False):
         import torch
+        if cache_fp8 and cache_fp4:
+            raise ValueError("a cache has entries of one format: cache_fp8 or cache_fp4")
         self.num_heads = num_heads
         qo = np.asarray(qo_indptr, dtype=np.int32)
         cu = np.atleast_2d(np.asarray(cu_seq_lens, dtype=np.int32))
@@ -79,8 +82,8 @@ class ChunkedPrefill:
         t_max = max(self.chunk_tokens, default=0)
         h = num_heads
         bf = torch.bfloat16
-        self.cache_fp8 = bool(cache_fp8)
-        self.paged_up_proj = bool(paged_up_proj) and not self.cache_fp8
+        self.cache_fp8, self.cache_fp4 = bool(cache_fp8), bool(cache_fp4)
+        self.paged_up_proj = bool(paged_up_proj) and not (self.cache_fp8 or self.cache_fp4)
         self.latent = None if self.paged_up_proj else torch.empty((max(self.total_prefix, 1), 576), dtype=bf,
                                                                    device=device)
         # K of a chunk: [T, H, 192], or with the shared rope K_nope [T, H, 128] + rope [T, 64]
@@ -118,13 +121,14 @@ class ChunkedPrefill:
         if self.latent is None:
             self.latent = torch.empty((max(self.total_prefix, 1), 576), dtype=torch.bfloat16, device=cache.device)
         if self.total_prefix:
-            gather = mla_gather_latent_fp8 if self.cache_fp8 else mla_gather_latent
+            gather = (mla_gather_latent_fp8 if self.cache_fp8 else mla_gather_latent_fp4 if self.cache_fp4
+                      else mla_gather_latent)
             gather(cache, self.chunk_table(block_table), self.cu_all_dev, self.starts_all_dev, self.total_prefix,
                    self.latent[:self.total_prefix], self.status, stream)
         return self.latent
 
     def run(self, q, k, v, cache, block_table, w_kvb, o=None, lse=None, stream=None):
-        """q/k/v: new tokens; cache [NB, BS, 576] bf16 (or [NB, BS, 648] uint8 with cache_fp8);
+        """q/k/v: new tokens; cache [NB, BS, 576] bf16 (or [NB, BS, 648] uint8 with cache_fp8, [NB, BS, 400] with cache_fp4);
         block_table [B, M] int32 (device)."""
         o, lse = self.main.run(q, k, v, o, lse, True, stream)
         if not self.paged_up_proj:

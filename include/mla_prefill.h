@@ -503,6 +503,124 @@ MLA_API int mla_tree_commit(void* cache, int num_layers, int64_t layer_stride, i
                             const int32_t* seq_lens, const int32_t* accepted, const int32_t* accepted_counts,
                             int batch, int max_accepted, int32_t* status, void* stream);
 
+/*
+ * Which drafted nodes are kept, and the token that follows: a tree of drafts against the target's
+ * probabilities, from given random numbers, so that what is kept is distributed as the target is.
+ *   target_probs : [total_rows, vocab], the target's distribution after each node; fp32
+ *                  (prob_type 0) or bf16 (1)
+ *   draft_probs  : as target_probs, or NULL: the distribution that the children of each node were
+ *                  drawn from, independently of one another.  NULL: children were given, not drawn
+ *                  (the draft's best continuations, a lookup)
+ *   tokens       : DEVICE int32 [total_rows], each node's token
+ *   parents      : DEVICE int32 [total_rows], as for mla_tree_mask, or NULL: node i's is i - 1
+ *   qo_indptr    : DEVICE int32 [batch+1] (qo_indptr[0] = 0)
+ *   uniforms     : DEVICE fp32 [total_rows], a number in [0, 1) for each node's test
+ *   final_uniforms : DEVICE fp32 [batch], one for the token that follows
+ *   accepted     : DEVICE int32 [batch, max_accepted], as mla_tree_commit takes it, -1 behind the
+ *                  path  (written)
+ *   accepted_counts : DEVICE int32 [batch]  (written)
+ *   next_tokens  : DEVICE int32 [batch]     (written)
+ *   status       : DEVICE int32 word or NULL
+ * Node 0 is the token that the step before ended with: it is kept.  At a kept node c with target p
+ * and draft q, its children are tested in the order of their indices; the first that passes is kept
+ * and the walk goes on there.  With a = 0, F = 1 before the first of them, a child with token x
+ * passes if u q(x) F < max(p(x) - a q(x), 0); if not, a becomes a + F and F the sum over the
+ * vocabulary of max(p - a q, 0).  Given children: u F < p(x), p(x) as it is now; if not, F loses
+ * p(x), and p(x) becomes 0.  When no child is left (or the path has max_accepted nodes: then as if c
+ * had none), next is the least token whose sum of what is left of p, with those below it, passes
+ * final_uniform times the sum of all; where nothing is left of it, p itself counts.
+ * Other nodes whose parent is -1 are never kept.  A request without nodes gets count 0, next -1; so
+ * does next where p has no mass.  Probabilities are taken into [0, 1], a NaN as 0; a row's sum must be
+ * below 2048.  Sums are kept in 64-bit fixed point (2^-52): they do not depend on any order.
+ * MLA_DEVSTAT_BAD_INDEX is OR-ed in for a token outside the vocabulary or a parent that is not below its
+ * node (such a node counts as if it was not there, node 0's own apart), or a request whose rows are not
+ * inside total_rows (as one without nodes).
+ * vocab <= 2^24, vocab * total_rows any; all arrays aligned to their elements.  One launch; allocates
+ * nothing.
+ */
+MLA_API int mla_tree_verify(const void* target_probs, const void* draft_probs, int prob_type, int64_t vocab,
+                            const int32_t* tokens, const int32_t* parents, const int32_t* qo_indptr, int batch,
+                            int64_t total_rows, const float* uniforms, const float* final_uniforms, int32_t* accepted,
+                            int max_accepted, int32_t* accepted_counts, int32_t* next_tokens, int32_t* status,
+                            void* stream);
+
+/* ======================================================================
+ * A latent cache of 4-bit entries, and new tokens into a cache of any entry.  [sglang] the cache
+ * keeps 512 latent + 64 rope per token; [vLLM-V4] the fp8 entry has the latent in 8 bits with
+ * power-of-two scales and the rope in bf16: the 4-bit entry is the same with e2m1 codes.
+ * ====================================================================== */
+/*
+ * An fp4 entry has 400 bytes: bytes [0, 256) 512 latent values in e2m1 (sign, two exponent bits, a
+ * mantissa bit: 0, 1/2, 1, 3/2, 2, 3, 4, 6 and their negatives), eight in each 32-bit little-endian
+ * word, values 8 w + 0, 2, 4, 6 of word w in bits 0-3, 4-7, 8-11, 12-15 and values 8 w + 1, 3, 5, 7 in
+ * bits 16-31 likewise; [256, 384) the rope as 64 bf16; [384, 400) scale bytes, scale g =
+ * 2^(byte_g - 127) covering latent values [32 g, 32 g + 32) (byte 255 is NaN).
+ */
+#define MLA_ENTRY_BF16 0   /* 1152 bytes */
+#define MLA_ENTRY_FP8  1   /*  648 bytes, see mla_gather_latent_fp8 */
+#define MLA_ENTRY_FP4  2   /*  400 bytes */
+
+/*
+ * New tokens' rows into the paged cache: the latent normalised, the rope rotated by the token's
+ * position, both rounded (or quantized) once and stored by slot; the queries' rope on the way.
+ *   cache        : [num_blocks, block_size] entries of entry_format, written in place
+ *   latent       : bf16, token t's row (512 latent then 64 rope, not rotated) at latent + t *
+ *                  latent_stride (elements; >= 576 and a multiple of 8)
+ *   norm_weight  : bf16 [512] or NULL: the latent x becomes x / sqrt(mean(x^2) + norm_eps) * weight
+ *   positions    : DEVICE int32 [num_tokens], as mla_tree_mask writes them
+ *   cos_sin      : fp32 [max_positions, 64]: 32 cosines, then 32 sines, of a position's angles
+ *   interleaved  : nonzero: angle i turns values 2 i and 2 i + 1, zero: values i and i + 32:
+ *                  (x, y) becomes (x cos - y sin, y cos + x sin)
+ *   slot_mapping : DEVICE int64 [num_tokens], as for mla_cache_write
+ *   q_rope       : bf16 or NULL (num_heads 0): token t's, head h's 64 values at q_rope + t *
+ *                  q_token_stride + h * q_head_stride (elements, multiples of 8), not rotated
+ *   q_out        : bf16, strides likewise: the rotated values; the same memory as q_rope (with its
+ *                  strides) or none of it.  E.g. q_rope = q + 128 of q [T, H, 192], q_out = q_abs +
+ *                  512 of q_abs [T, H, 576]   (written)
+ *   status       : DEVICE int32 word or NULL
+ * A token with a negative slot is padding: nothing of it is read or written, not its queries either.
+ * MLA_DEVSTAT_BAD_INDEX is OR-ed in for a slot past the cache or a position outside
+ * [0, max_positions); nothing of such a token is written.  Where two tokens name one slot, what is
+ * left there may be part of each.
+ * fp8 and fp4: a group's scale (64 and 32 values) is the least power of two, not below 2^-127, times
+ * which 448 (fp8) or 7 (fp4, whose largest value 6 is the nearest to it) reaches the group's largest
+ * magnitude; values / scale are rounded to nearest, ties to even.  A group with a NaN or an infinity,
+ * or in fp4 one that would need a scale above 2^125, gets scale byte 255 and zeros, and reads as NaN.
+ * One launch; allocates nothing.
+ */
+MLA_API int mla_cache_append(void* cache, int entry_format, int64_t num_blocks, int block_size, const void* latent,
+                             int64_t latent_stride, const void* norm_weight, float norm_eps, const int32_t* positions,
+                             const float* cos_sin, int64_t max_positions, int interleaved,
+                             const int64_t* slot_mapping, int64_t num_tokens, const void* q_rope,
+                             int64_t q_token_stride, int64_t q_head_stride, int num_heads, void* q_out,
+                             int64_t q_out_token_stride, int64_t q_out_head_stride, int32_t* status, void* stream);
+
+/*
+ * Paged gather of an fp4 latent cache, dequantized: as mla_gather_latent_fp8, with
+ *   cache        : uint8 [num_blocks, block_size, entry_bytes], entry_bytes must be 400
+ *                  (MLA_ERR_UNSUPPORTED otherwise), 16-byte aligned
+ *   out          : bf16 [total_tokens, 576]: e2m1 times scale, rounded to bf16 (exact unless above its
+ *                  largest value, then infinite), and the rope bits copied
+ */
+MLA_API int mla_gather_latent_fp4(const void* cache, int64_t num_blocks, int block_size, int entry_bytes,
+                                  const int32_t* block_table, int max_blocks_per_req, const int32_t* cu_seq_lens,
+                                  const int32_t* chunk_starts, int batch, int64_t total_tokens, void* out,
+                                  int32_t* status, void* stream);
+
+/*
+ * Attention of drafted nodes, or single new tokens, over an fp4 latent cache: mla_tree_attention with
+ *   cache        : uint8 [num_blocks, block_size, 400], 16-byte aligned
+ * and everything else as there, its workspace (mla_tree_workspace) too.  Keys and values are the
+ * dequantized rows, which bf16 holds exactly.  A cached row with a scale byte above 252 counts as NaN
+ * for the rows that see it (mla_cache_append writes none but 255).
+ */
+MLA_API int mla_tree_attention_fp4(const void* q_abs, const void* cache, int64_t num_blocks, int block_size,
+                                   const int32_t* block_table, int max_blocks_per_req, const int32_t* qo_indptr,
+                                   const int32_t* kv_lens, const int64_t* tree_mask, int mask_words, int batch,
+                                   int64_t total_rows, int num_heads, float sm_scale, float logits_soft_cap,
+                                   void* o_lat, float* lse, void* workspace, int64_t workspace_bytes,
+                                   int32_t* status, void* stream);
+
 /* ======================================================================
  * LSE merge of two partial attention states.  [vLLM-FI]
  * run_prefill_context_chunk always returns LSE so chunk results can merge.

@@ -27,7 +27,10 @@ computes, written from the pages' definitions:
   * absorbed-weight attention (multi-query over the 576-wide compressed rows,
     sglang issue #3849's forward_absorb; explicit sm_scale per TVM PR #17674);
   * the speculative-decoding step: block tables and slots from lengths, tree
-    visibility, tree attention over the cache rows, accepted rows moved.
+    visibility, tree attention over the cache rows, accepted rows moved, drafts
+    verified against the target's probabilities;
+  * the 4-bit latent cache entry, its gather, and the append of new tokens
+    (norm, rotation, quantization) to a cache of any entry.
 
 Only ``tests/``, ``__graft_entry__.smoke()`` and the CPU-baseline leg of
 ``bench.py`` may import this package.  It shares no code with the CUDA path
@@ -44,7 +47,9 @@ chunked pipeline (split/merge identity), absorbed attention (the
 absorption identity against the MHA oracle over decompressed K/V, brute force),
 fp8 entries (hand-decoded codes, every
 e4m3 code against the library's float8 type, exact products), speculative step
-(hand-written tables and trees, chains against absorbed attention, brute force).  No function is "parity unpinned".
+(hand-written tables and trees, chains against absorbed attention, brute force, verified
+nodes against the target's distribution), 4-bit entries (hand-written words, every code, scales
+by definition).  No function is "parity unpinned".
 """
 from .bf16 import bf16_bits_to_f64, round_f64_to_bf16
 from .attention import allowed_mask, attend_request, ragged_attention
@@ -56,8 +61,10 @@ from .chunked import chunked_prefill_attention
 from .absorbed import absorb_query, absorbed_attention, absorbed_output_to_mha
 from .fp8_cache import (dequant_fp8_entries, e4m3_to_f64, f64_to_bf16_bits, gather_latent_fp8,
                         ue8m0_to_f64)
+from .fp4_cache import (e2m1_to_f64, fp4_codes, fp4_values, gather_latent_fp4, normalise, pack_fp4, pack_fp8, quantize,
+                        rotate)
 from .speculative import (pack_bits, tree_attention, tree_commit, tree_visibility,
-                          update_block_table)
+                          update_block_table, verify_children, verify_tree)
 
 __all__ = [
     "bf16_bits_to_f64", "round_f64_to_bf16", "allowed_mask", "attend_request",
@@ -65,4 +72,6 @@ __all__ = [
     "chunked_prefill_attention", "dequant_fp8_entries", "e4m3_to_f64", "f64_to_bf16_bits",
     "gather_latent_fp8", "ue8m0_to_f64", "absorb_query", "absorbed_attention", "absorbed_output_to_mha",
     "pack_bits", "tree_attention", "tree_commit", "tree_visibility", "update_block_table",
+    "e2m1_to_f64", "fp4_codes", "fp4_values", "gather_latent_fp4", "normalise", "pack_fp4", "pack_fp8", "quantize",
+    "rotate", "verify_children", "verify_tree",
 ]

@@ -110,3 +110,44 @@ def tree_commit(cache, table, seq, paths, counts):
             a, b = int(seq[r]) + int(paths[r][i]), int(seq[r]) + i
             out[:, table[r][b // bs], b % bs] = cache[:, table[r][a // bs], a % bs]
     return out
+
+
+def verify_children(p, tokens, q=None):
+    """One node of a verified tree: the children's tokens in order against the target row p (and the
+    row q that they were drawn from; None: given).  Returns (the uniform below which each passes, given
+    that those before it were refused; what is left of p when all are refused)."""
+    p = np.asarray(p, dtype=np.float64)
+    left, mass, times, below = p.copy(), 1.0, 0.0, []
+    for x in tokens:
+        px, qx = left[x], 1.0 if q is None else float(q[x])
+        below.append(0.0 if px <= 0 else float("inf") if qx * mass <= 0 else px / (qx * mass))
+        if q is None:
+            mass -= px
+            left[x] = 0.0
+        else:
+            times += mass
+            left = np.maximum(p - times * np.asarray(q, dtype=np.float64), 0.0)
+            mass = left.sum()
+    return below, left
+
+
+def verify_tree(target, tokens, parents, uniforms, final_uniform, max_accepted, draft=None):
+    """(kept path, the token that follows) of one request: target [n, V], tokens and parents [n]."""
+    path = [0]
+    while True:
+        at = path[-1]
+        p = np.asarray(target[at], dtype=np.float64)
+        children = [j for j in range(at + 1, len(tokens)) if parents[j] == at and 0 <= tokens[j] < len(p)]
+        if len(path) >= max_accepted:
+            children = []
+        below, left = verify_children(p, [int(tokens[j]) for j in children], None if draft is None else draft[at])
+        passed = [j for j, b in zip(children, below) if uniforms[j] < b]
+        if passed:
+            path.append(passed[0])
+            continue
+        if not left.sum() > 0:
+            left = p
+        if not left.sum() > 0:
+            return path, -1
+        sums = np.cumsum(left)
+        return path, int(np.searchsorted(sums, float(final_uniform) * sums[-1], side="right"))
