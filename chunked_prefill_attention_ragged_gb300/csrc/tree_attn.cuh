@@ -1,6 +1,8 @@
 // What the kernels of tree attention share: the requests as they see them, the split of the
 // work among workers, the way from key positions to cache rows, visibility, and waits.
 #pragma once
+#include <cmath>
+
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -20,6 +22,28 @@ struct TreeLaunch {
   uint64_t wait_limit_ns;
   int force_timeout;
 };
+
+// What both kernels' launches have in common.
+inline TreeLaunch tree_launch(const TreeParams& t, int workers) {
+  TreeLaunch p = {};
+  p.t = t;
+  p.workers = workers;
+  const int bs = t.block_size;
+  p.oob_row = (int32_t)(t.max_blocks > 0 ? (uint64_t)t.num_blocks * (uint64_t)bs : 1);
+  p.block_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (bs == 1 << i) p.block_shift = i;
+  p.o_align32 = (reinterpret_cast<uintptr_t>(t.o) & 31u) == 0;
+  const float LOG2E = 1.4426950408889634f;
+  p.has_cap = t.soft_cap > 0.f;
+  p.scale_log2 = t.sm_scale * LOG2E;
+  p.cap_log2 = p.has_cap ? t.soft_cap * LOG2E : 0.f;
+  p.cap_inv = p.has_cap ? std::fmin(t.sm_scale / t.soft_cap, 1e38f) : 0.f;
+  const uint64_t forced = forced_timeout_ns();
+  p.force_timeout = forced != 0;
+  p.wait_limit_ns = forced ? forced : kWaitLimitNs;
+  return p;
+}
 
 // Workspace: one record per worker, two slots per worker.
 // The unit that the boundary before a worker cuts, if it is the unit's first such boundary: parts

@@ -1,108 +1,404 @@
-// Tree attention over a cache of 4-bit entries (include/mla_prefill.h): a plain kernel, one warp for each
-// (node, head) pair, which goes over the keys once with the running maximum and sum of its softmax.
-#include <cuda_bf16.h>
+// Tree attention over a cache of 4-bit entries: the mathematics, the split of the work, the products and the
+// softmax of tree_attn_kernel.cu (a cluster of two CTAs runs a unit of 128 pairs with cta_group::2 products),
+// over keys and values that are made bf16 on their way into shared memory.
+//
+// Eight warps make them: four the CTA's 64 keys of a tile as the half of S's B operand, four the tile's 128
+// keys x 256 of the value columns.  A lane has a row and one 32-value group (16 bytes, one scale) of each
+// panel: it loads a tile's bytes into registers while the products read the tile before, waits until a panel
+// is free, and writes 64 bytes of it in the swizzle that the products expect.  Eight lanes of a store have
+// eight rows, and so eight different bank groups.  Entries go straight from L2 to registers: there is no
+// room for them in shared memory beside Q (72 KB), a tile (136 KB) and P.
+//   warp 0     Q producer
+//   warp 1     even CTA: issues every product
+//   warp 2     brings rows of the tiles to come into L2
+//   warp 3     TMEM allocation
+//   warps 4-7  softmax
+//   warps 8-11 keys, 12-15 values
+// A code becomes bf16 by moving its bits to a bf16's low exponent bits and one product by 2^126 times the
+// scale, exact; scales above 2, where that factor has no bf16, take two products (a tile in which a warp
+// meets one).  A row with a scale byte above 252 has NaN in its rope, which only S sees, and zeros for values,
+// so that it cannot reach rows that do not see it.  Rows that are not there are zeros.
+#include <algorithm>
 
 #include "fp4.cuh"
 #include "internal.h"
-#include "tree_attn.cuh"
+#include "tree_core.cuh"
 
 namespace mla {
 namespace {
 
-constexpr int WARPS = 8;
+constexpr int NTHREADS = 512;
+constexpr int LAUNCH_REGS = 128;
+constexpr int REGS_CTRL = 96, REGS_SOFTMAX = 208, REGS_ROWS = 104;
+static_assert(REGS_CTRL + REGS_SOFTMAX + 2 * REGS_ROWS <= 4 * LAUNCH_REGS, "register split exceeds the launch allocation");
+constexpr int AHEAD = 2;   // tiles between the one being made and the one brought into L2
 
-__device__ __forceinline__ void unpack8(const uint4& v, float* x) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Where a key's entry lies: its table's block, looked up a tile ahead, then its address (null: zeros).
+__device__ __forceinline__ const uint8_t* entry_of(const TreeLaunch& p, int32_t blk, int64_t key) {
+  const int32_t row = block_row(p, blk, key);
+  return row == p.oob_row ? nullptr : reinterpret_cast<const uint8_t*>(p.t.cache) + (int64_t)row * FP4_ENTRY;
+}
+__device__ __forceinline__ uint4 load16(const uint8_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+__device__ __forceinline__ uint32_t byte_of(uint32_t w, int i) { return (w >> (8 * i)) & 0xffu; }
+// Bytes of a word above 252 (in their top bits), and above 128.
+__device__ __forceinline__ uint32_t above252(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x03030303u) & w & 0x80808080u; }
+__device__ __forceinline__ uint32_t above128(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x7f7f7f7fu) & w & 0x80808080u; }
+
+// A group's 32 values to four 16-byte pieces at `at` + the swizzled offsets.  `b`: its scale byte.
+template <bool BIG>
+__device__ __forceinline__ void put_group(uint32_t at, const uint32_t* off, const uint4& w, uint32_t b) {
+  const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+  const bool none = b > FP4_MAX_SCALE;
+  uint32_t m, s = 0;
+  if (BIG) {
+    m = 0x7e807e80u;   // 2^126
+    s = none ? 0u : scale_bf16x2(b);
+  } else {
+    m = (b + 126) << 7;
+    m = none ? 0u : m | m << 16;
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    uint32_t r[4];
+    fp4_fields(words[i], r);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      r[k] = mul_bf16x2(r[k], m);
+      if (BIG) r[k] = mul_bf16x2(r[k], s);
+    }
+    st_shared_v4(at + off[i], r[0], r[1], r[2], r[3]);
   }
 }
 
-__global__ void __launch_bounds__(WARPS * 32) tree_attn_fp4_kernel(const __grid_constant__ TreeParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t pair = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5);
-  const int64_t row = pair / p.num_heads;
-  if (pair >= p.total_rows * p.num_heads) return;
-  int r = 0;
-  for (; r < p.batch; ++r) {   // the request that has the row
-    const Req q = load_req(p, r, pair == 0);
-    if (pair > 0 && row >= q.q0 && row < q.q0 + q.nodes) break;
+// A warp's part of what it writes is there: handed to the products' proxy, told to the even CTA.
+__device__ __forceinline__ void tell(const Ctx& c, int b, int lane) {
+  fence_async_shared();
+  __syncwarp();
+  if (lane == 0) {
+    if (c.rank) mbar_arrive_remote(mapa_shared(c.bar(b), 0));
+    else mbar_arrive(c.bar(b));
   }
-  if (pair == 0)
-    for (r = 0; r < p.batch; ++r) {
-      const Req q = load_req(p, r, false);
-      if (row >= q.q0 && row < q.q0 + q.nodes) break;
-    }
-  if (r == p.batch) return;
-  const Req req = load_req(p, r, false);
+}
+
+// Warps 8-11: a lane has row 16 w + lane % 16 of the CTA's 64, and the first or second half of each panel.
+__device__ void run_keys(const Ctx& c, const TreeLaunch& p, Parts parts, volatile int* begun) {
+  const int lane = threadIdx.x & 31, w4 = (threadIdx.x >> 5) & 3, half = lane >> 4;
+  const int row = 16 * w4 + (lane & 15);
+  uint32_t off[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) off[i] = row * 128 + (((4 * half + i) ^ (row & 7)) << 4);
+  const uint32_t dst = c.sbase + OFF_K;
+  int tiles = 0;
+  bool ok = true;
   Part u;
-  u.q = req;
-  u.r = r;
-  const int node = (int)(row - req.q0);
-  const uint8_t* cache = reinterpret_cast<const uint8_t*>(p.cache);
-  const uint4* qv = reinterpret_cast<const uint4*>(p.q + pair * 576);
-  float q[2][8], qr[8] = {}, acc[2][8] = {};
-  unpack8(qv[lane], q[0]);
-  unpack8(qv[32 + lane], q[1]);
-  if (lane < 8) unpack8(qv[64 + lane], qr);
-  const float NEG_INF = -__int_as_float(0x7f800000);
-  float m = NEG_INF, l = 0.f;
-  uint64_t bits = 0;
-  for (int key = 0; key < req.kv; ++key) {
-    if ((key & 63) == 0) bits = visible(p, u, node, key);
-    if (!((bits >> (key & 63)) & 1)) continue;
-    const int64_t b = __ldg(p.block_table + (int64_t)r * p.max_blocks + key / p.block_size);
-    const bool there = b >= 0 && b < p.num_blocks;
-    if (!there && lane == 0 && p.status) atomicOr(p.status, MLA_DEVSTAT_BAD_INDEX);
-    float c[2][8] = {}, s = 0.f;
-    if (there) {
-      const uint8_t* e = cache + (b * p.block_size + key % p.block_size) * FP4_ENTRY;
-      float rope[8] = {};
-      uint32_t most = 0;
+  while (ok && parts.next(&u)) {
+    int64_t key = (int64_t)u.lo * KEYS + 64 * c.rank + row;
+    const uint8_t* e = entry_of(p, table_block(p, u, key), key);
+    uint4 code[8], rope[4], sc;
+    auto load = [&]() {
+      if (e) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t sc = __ldg(e + FP4_SCALES + 8 * h + (lane >> 2));
-        most = max(most, sc);
-        unpack8(fp4_values(__ldg(reinterpret_cast<const uint32_t*>(e) + 32 * h + lane), scale_bf16x2(sc)), c[h]);
+        for (int i = 0; i < 8; ++i) code[i] = load16(e + 32 * i + 16 * half);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rope[i] = load16(e + FP4_ROPE + 64 * half + 16 * i);
+        sc = load16(e + FP4_SCALES);
+      } else {
+        sc = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) code[i] = sc;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rope[i] = sc;
       }
-      if (lane < 8) unpack8(__ldg(reinterpret_cast<const uint4*>(e + FP4_ROPE) + lane), rope);
+    };
+    load();
+    int32_t blk = u.lo + 1 < u.hi ? table_block(p, u, key + KEYS) : PAST_END;
+    for (int t = u.lo; t < u.hi; ++t, ++tiles) {
+      if (w4 == 0 && lane == 0) *begun = tiles;
+      if (above252(sc.x) | above252(sc.y) | above252(sc.z) | above252(sc.w)) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s += q[0][i] * c[0][i] + q[1][i] * c[1][i] + qr[i] * rope[i];
+        for (int i = 0; i < 4; ++i) rope[i] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+      }
+      const bool big = __any_sync(0xffffffffu, (above128(sc.x) | above128(sc.y) | above128(sc.z) | above128(sc.w)) != 0);
+      const uint32_t s4[4] = {sc.x >> (8 * half), sc.y >> (8 * half), sc.z >> (8 * half), sc.w >> (8 * half)};
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-      if (__any_sync(0xffffffffu, most > FP4_MAX_SCALE)) s = __int_as_float(0x7fc00000);
+      for (int g = 0; g < KGROUPS; ++g) {
+        if (tiles > 0 && !c.wait_warp(KE + g, (tiles - 1) & 1)) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int i = 3 * g; i < 3 * g + 3 && i < 8; ++i) {
+          const uint32_t b = byte_of(s4[i >> 1], 2 * (i & 1));
+          if (big) put_group<true>(dst + i * QP, off, code[i], b);
+          else put_group<false>(dst + i * QP, off, code[i], b);
+        }
+        if (g == KGROUPS - 1) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) st_shared_v4(dst + 8 * QP + off[i], rope[i].x, rope[i].y, rope[i].z, rope[i].w);
+        }
+        tell(c, KF + g, lane);
+      }
+      if (!ok) break;
+      key += KEYS;
+      if (t + 1 < u.hi) {
+        e = entry_of(p, blk, key);
+        load();
+        if (t + 2 < u.hi) blk = table_block(p, u, key + KEYS);
+      }
     }
-    s *= p.sm_scale;
-    if (p.soft_cap > 0.f) s = p.soft_cap * tanhf(s / p.soft_cap);
-    const float mn = s > m ? s : m;   // (a NaN passes into the sums)
-    const float old = m == NEG_INF ? 0.f : expf(m - mn), w = expf(s - mn);
-    m = mn;
-    l = l * old + w;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[h][i] = acc[h][i] * old + w * c[h][i];
   }
-  const bool empty = m == NEG_INF && l == 0.f;
-  uint4* o = reinterpret_cast<uint4*>(p.o + pair * 512);
+}
+
+// Warps 12-15: rows 16 w + lane % 16 of both halves of the tile's keys, the CTA's four panels of values.
+__device__ void run_values(const Ctx& c, const TreeLaunch& p, Parts parts) {
+  const int lane = threadIdx.x & 31, w4 = (threadIdx.x >> 5) & 3, half = lane >> 4;
+  const int row = 16 * w4 + (lane & 15);
+  uint32_t off[4];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t w[4];
+  for (int i = 0; i < 4; ++i) off[i] = row * 128 + (((4 * half + i) ^ (row & 7)) << 4);
+  const uint32_t dst = c.sbase + OFF_V;
+  const int codes = 128 * (int)c.rank + 16 * half, scales = FP4_SCALES + 8 * (int)c.rank;
+  int tiles = 0;
+  bool ok = true;
+  Part u;
+  while (ok && parts.next(&u)) {
+    int64_t key = (int64_t)u.lo * KEYS + row;
+    uint4 code[2][4];
+    uint2 sc[2];
+    int32_t blk[2] = {table_block(p, u, key), table_block(p, u, key + 64)};
+    auto load = [&](int i, int64_t k) {
+      const uint8_t* e = entry_of(p, blk[i], k);
+      if (e) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = empty ? 0u : pack_bf16x2(acc[h][2 * i] / l, acc[h][2 * i + 1] / l);
-    o[32 * h + lane] = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int j = 0; j < 4; ++j) code[i][j] = load16(e + codes + 32 * j);
+        sc[i] = __ldg(reinterpret_cast<const uint2*>(e + scales));
+      } else {
+        sc[i] = make_uint2(0, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) code[i][j] = make_uint4(0, 0, 0, 0);
+      }
+    };
+    load(0, key);
+    load(1, key + 64);
+    if (u.lo + 1 < u.hi) {
+      blk[0] = table_block(p, u, key + KEYS);
+      blk[1] = table_block(p, u, key + KEYS + 64);
+    }
+    for (int t = u.lo; t < u.hi; ++t, ++tiles, key += KEYS) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (tiles > 0 && !c.wait_warp(VE + i, (tiles - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        const bool big = __any_sync(0xffffffffu, (above128(sc[i].x) | above128(sc[i].y)) != 0);
+        const uint32_t s2[2] = {sc[i].x >> (8 * half), sc[i].y >> (8 * half)};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t b = byte_of(s2[j >> 1], 2 * (j & 1));
+          if (big) put_group<true>(dst + i * V_HALF + j * QP, off, code[i][j], b);
+          else put_group<false>(dst + i * V_HALF + j * QP, off, code[i][j], b);
+        }
+        tell(c, VF + i, lane);
+        if (t + 1 < u.hi) load(i, key + KEYS + 64 * i);
+      }
+      if (!ok) break;
+      if (t + 2 < u.hi) {
+        blk[0] = table_block(p, u, key + 2 * KEYS);
+        blk[1] = table_block(p, u, key + 2 * KEYS + 64);
+      }
+    }
   }
-  if (lane == 0 && p.lse) p.lse[pair] = empty ? NEG_INF : m + logf(l);
+}
+
+__device__ void run_queries(const Ctx& c, Parts parts, const CUtensorMap* tq) {
+  const int lane = threadIdx.x & 31;
+  int units = 0;
+  bool ok = true;
+  Part u;
+  while (ok && parts.next(&u)) {
+    if (lane == 0) {
+      if (units > 0) ok = c.wait(QE, (units - 1) & 1);
+      if (ok) {
+        expect_both(c, QF, NP * QP);
+        tma_load_3d_pair(c.sbase + OFF_Q, tq, mapa_shared(c.bar(QF), 0), 0, (int32_t)(u.pair0 + 64 * c.rank), 0);
+      }
+    }
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    if (ok) ++units;
+  }
+  if (lane == 0) {
+    if (c.rank == 0) {
+      if (units) c.drain(QF, (units - 1) & 1);
+    } else if (!ok) {
+      settle();
+    }
+  }
+}
+
+// Warp 2: this CTA's keys of the tiles to come into L2, a lane an entry.  It follows the keys' count of
+// tiles and gives up quietly.
+__device__ void run_prefetch(const Ctx& c, const TreeLaunch& p, Parts parts, const volatile int* begun) {
+  const int lane = threadIdx.x & 31;
+  int tiles = 0;
+  Part u;
+  while (parts.next(&u)) {
+    for (int t = u.lo; t < u.hi; ++t, ++tiles) {
+      const uint64_t t0 = global_timer_ns();
+      while (*begun < tiles) {
+        __nanosleep(200);
+        if (*c.abort_flag || global_timer_ns() - t0 > p.wait_limit_ns) return;
+      }
+      __syncwarp();
+      if (t + AHEAD < u.hi) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int64_t key = (int64_t)(t + AHEAD) * KEYS + 64 * c.rank + 32 * i + lane;
+          if (key < u.q.kv) {
+            const uint8_t* e = entry_of(p, table_block(p, u, key), key);
+            if (e) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(e), "r"(FP4_ENTRY) : "memory");
+          }
+        }
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(NTHREADS, 1)
+tree_attn_fp4_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ TreeLaunch p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ StartRec start;
+  __shared__ int64_t count;
+  __shared__ JoinRec join;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
+  int* abort_flag = reinterpret_cast<int*>(smem + OFF_MISC + 4);
+  int* begun = reinterpret_cast<int*>(smem + OFF_MISC + 8);   // tiles that the keys' first warp has begun, less one
+  const uint32_t rank = cluster_ctarank();
+  const int worker = blockIdx.x >> 1;
+  const Ctx c{smem_addr(smem), abort_flag, p.t.status, p.wait_limit_ns, rank};
+  ReqWords words{0, 0, 0};   // (on their way while the barriers are made)
+  if ((int)threadIdx.x < p.t.batch) words = load_words(p.t, threadIdx.x);
+  if (warp == 1) {
+    // P: every softmax warp of both CTAs; maxima: the two warps of 32 rows; keys and values: four warps of each.
+    static_assert(NBAR <= 32, "a lane each");
+    const bool rows = (lane >= KF && lane < KF + KGROUPS) || (lane >= VF && lane < VF + 2);
+    if (lane < NBAR) mbar_init(c.bar(lane), lane == PR || rows ? 8 : lane == XB || lane == XB + 1 ? 2 : 1);
+    if (lane == 0) {
+      *abort_flag = 0;
+      *begun = -1;
+    }
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) tma_prefetch_desc(&tm_q);
+  if (warp == 3) {   // one warp of each CTA of the pair, together
+    tmem_alloc_pair(smem_addr(tmem_slot), TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  __syncwarp();
+  tc_fence_before();
+  if (warp == 3) cluster_arrive();   // (see tree_attn_kernel)
+  else cluster_arrive_relaxed();
+  find_piece<NTHREADS>(p.t, words, worker, p.workers, blockIdx.x == 0, &start, &count, &join);
+  char* ws = static_cast<char*>(p.t.workspace);
+  if (threadIdx.x == 0 && rank == 0) reinterpret_cast<JoinRec*>(ws)[worker] = join;
+  __syncwarp();
+  cluster_wait();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  const Parts parts(p.t, start, count);
+  if (warp < 4) {
+    setmaxnreg_dec<REGS_CTRL>();
+    if (warp == 0) run_queries(c, parts, &tm_q);
+    else if (warp == 1 && rank == 0) run_mma<64>(c, p, parts, tmem);
+    else if (warp == 2) run_prefetch(c, p, parts, begun);
+  } else if (warp < 8) {
+    setmaxnreg_inc<REGS_SOFTMAX>();
+    run_softmax(c, p, parts, tmem, ws + WS_SLOTS + (size_t)worker * 2 * SLOT_BYTES, smem);
+  } else {
+    setmaxnreg_dec<REGS_ROWS>();
+    if (warp < 12) run_keys(c, p, parts, begun);
+    else run_values(c, p, parts);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  // Neither CTA leaves (freeing shared memory and TMEM) while the even CTA's products may still
+  // read or write the other's.
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 3) {
+    __syncwarp();
+    tmem_dealloc_pair(tmem, TMEM_COLS);
+  }
+}
+
+cudaLaunchConfig_t pair_config(cudaLaunchAttribute* attr, int workers, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * workers, 1, 1);
+  cfg.blockDim = dim3(NTHREADS, 1, 1);
+  cfg.dynamicSmemBytes = SMEM;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+// Clusters that run at once on the current device (0 on error), no more than the workspace has room for.
+int max_workers() {
+  static PerDeviceOnce configured;
+  static int workers[PerDeviceOnce::kMaxDevices] = {};
+  const cudaError_t e = configured.run([] {
+    cudaError_t r = cudaFuncSetAttribute(tree_attn_fp4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (r != cudaSuccess) return r;
+    // The split of the registers takes for granted that every thread starts with LAUNCH_REGS.
+    cudaFuncAttributes attrs;
+    r = cudaFuncGetAttributes(&attrs, tree_attn_fp4_kernel);
+    if (r != cudaSuccess) return r;
+    if (attrs.numRegs != LAUNCH_REGS) return cudaErrorInvalidConfiguration;
+    int dev = 0, n = 0;
+    r = cudaGetDevice(&dev);
+    if (r != cudaSuccess) return r;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = pair_config(attr, 1, nullptr);
+    r = cudaOccupancyMaxActiveClusters(&n, tree_attn_fp4_kernel, &cfg);
+    if (r != cudaSuccess) return r;
+    const int64_t room = (tree_workspace_bytes() - (int64_t)WS_SLOTS) / (int64_t)(2 * SLOT_BYTES);
+    workers[dev] = (int)std::min<int64_t>(n, std::min<int64_t>(room, MAX_WORKERS));
+    return r;
+  });
+  int dev = 0;
+  if (e != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) return 0;
+  return workers[dev];
 }
 
 }  // namespace
 
-cudaError_t launch_tree_attention_fp4(const TreeParams& p, cudaStream_t stream) {
-  const int64_t pairs = p.total_rows * p.num_heads;
-  tree_attn_fp4_kernel<<<(unsigned)((pairs + WARPS - 1) / WARPS), WARPS * 32, 0, stream>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_tree_attention_fp4(const TreeParams& t, cudaStream_t stream) {
+  const TreeLaunch p = tree_launch(t, max_workers());
+  if (p.workers <= 0) return cudaErrorInvalidConfiguration;
+  CUtensorMap tq;
+  const uint64_t dims[3] = {64, (uint64_t)t.total_rows * (uint64_t)t.num_heads, NP}, strides[2] = {576 * 2, 64 * 2};
+  const uint32_t box[3] = {64, 64, NP};   // 64 rows, panel by panel
+  if (make_tensor_map_bf16(&tq, t.q, 3, dims, strides, box) != MLA_OK) return cudaErrorInvalidValue;
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = pair_config(attr, p.workers, stream);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_attn_fp4_kernel, tq, p);
+  return e != cudaSuccess ? e : launch_tree_join(p, stream);
 }
 
 }  // namespace mla
