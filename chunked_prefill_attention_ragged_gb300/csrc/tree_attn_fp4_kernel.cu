@@ -4,14 +4,14 @@
 //
 // Eight warps make them: four the CTA's 64 keys of a tile as the half of S's B operand, four the tile's 128
 // keys x 256 of the value columns.  A lane has a row and one 32-value group (16 bytes, one scale) of each
-// panel: it loads a tile's bytes into registers while the products read the tile before, waits until a panel
-// is free, and writes 64 bytes of it in the swizzle that the products expect.  Eight lanes of a store have
+// panel: it loads them into registers while the products read the tile before, waits until four panels
+// are free, and writes 64 bytes of each in the swizzle that the products expect.  Eight lanes of a store have
 // eight rows, and so eight different bank groups.  Entries go straight from L2 to registers: there is no
 // room for them in shared memory beside Q (72 KB), a tile (136 KB) and P.
 //   warp 0     Q producer
 //   warp 1     even CTA: issues every product
 //   warp 2     brings rows of the tiles to come into L2
-//   warp 3     TMEM allocation
+//   warp 3     TMEM allocation; ropes
 //   warps 4-7  softmax
 //   warps 8-11 keys, 12-15 values
 // A code becomes bf16 by moving its bits to a bf16's low exponent bits and one product by 2^126 times the
@@ -29,7 +29,7 @@ namespace {
 
 constexpr int NTHREADS = 512;
 constexpr int LAUNCH_REGS = 128;
-constexpr int REGS_CTRL = 96, REGS_SOFTMAX = 208, REGS_ROWS = 104;
+constexpr int REGS_CTRL = 88, REGS_SOFTMAX = 216, REGS_ROWS = 104;
 static_assert(REGS_CTRL + REGS_SOFTMAX + 2 * REGS_ROWS <= 4 * LAUNCH_REGS, "register split exceeds the launch allocation");
 constexpr int AHEAD = 2;   // tiles between the one being made and the one brought into L2
 
@@ -53,30 +53,25 @@ __device__ __forceinline__ uint32_t byte_of(uint32_t w, int i) { return (w >> (8
 __device__ __forceinline__ uint32_t above252(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x03030303u) & w & 0x80808080u; }
 __device__ __forceinline__ uint32_t above128(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x7f7f7f7fu) & w & 0x80808080u; }
 
-// A group's 32 values to four 16-byte pieces at `at` + the swizzled offsets.  `b`: its scale byte.
-template <bool BIG>
-__device__ __forceinline__ void put_group(uint32_t at, const uint32_t* off, const uint4& w, uint32_t b) {
+// A group's 32 values to four 16-byte pieces at `at` + the swizzled offsets.  Each code is multiplied by `m`
+// and, where the scales are `big`, by `m2`.
+__device__ __forceinline__ void put_group(uint32_t at, const uint32_t* off, const uint4& w, bool big, uint32_t m, uint32_t m2) {
   const uint32_t words[4] = {w.x, w.y, w.z, w.w};
-  const bool none = b > FP4_MAX_SCALE;
-  uint32_t m, s = 0;
-  if (BIG) {
-    m = 0x7e807e80u;   // 2^126
-    s = none ? 0u : scale_bf16x2(b);
-  } else {
-    m = (b + 126) << 7;
-    m = none ? 0u : m | m << 16;
-  }
+  uint32_t r[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t r[4];
-    fp4_fields(words[i], r);
+    fp4_fields(words[i], r[i]);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      r[k] = mul_bf16x2(r[k], m);
-      if (BIG) r[k] = mul_bf16x2(r[k], s);
-    }
-    st_shared_v4(at + off[i], r[0], r[1], r[2], r[3]);
+    for (int k = 0; k < 4; ++k) r[i][k] = mul_bf16x2(r[i][k], m);
   }
+  if (big) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) r[i][k] = mul_bf16x2(r[i][k], m2);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) st_shared_v4(at + off[i], r[i][0], r[i][1], r[i][2], r[i][3]);
 }
 
 // A warp's part of what it writes is there: handed to the products' proxy, told to the even CTA.
@@ -89,133 +84,133 @@ __device__ __forceinline__ void tell(const Ctx& c, int b, int lane) {
   }
 }
 
-// Warps 8-11: a lane has row 16 w + lane % 16 of the CTA's 64, and the first or second half of each panel.
-__device__ void run_keys(const Ctx& c, const TreeLaunch& p, Parts parts, volatile int* begun) {
+// What the eight warps do is a line of stages, two for each tile: four panels of 64 rows each.  Keys (warps
+// 8-11): panels 0-3 and 4-7 of the CTA's 64 keys; values (warps 12-15): the CTA's four panels, of the tile's
+// first and second 64 keys.  A warp has 16 rows, a lane one of them and half of each panel.  The bytes of the
+// stage after next are loaded when a stage is done: most of a tile's time before they are needed.  One loop
+// for both, and short: straight code for a tile of each did not stay in the instruction cache (see below).
+struct Stage {
+  uint4 code[4];
+  uint2 scale;
+};
+__device__ __forceinline__ void load_stage(const uint8_t* e, int at_code, int at_scale, Stage* s) {
+  if (e) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s->code[j] = load16(e + at_code + 32 * j);
+    s->scale = __ldg(reinterpret_cast<const uint2*>(e + at_scale));
+  } else {
+    s->scale = make_uint2(0, 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s->code[j] = make_uint4(0, 0, 0, 0);
+  }
+}
+__device__ void run_rows(const Ctx& c, const TreeLaunch& p, Parts parts, bool values, volatile int* begun) {
   const int lane = threadIdx.x & 31, w4 = (threadIdx.x >> 5) & 3, half = lane >> 4;
   const int row = 16 * w4 + (lane & 15);
   uint32_t off[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) off[i] = row * 128 + (((4 * half + i) ^ (row & 7)) << 4);
-  const uint32_t dst = c.sbase + OFF_K;
+  const uint32_t dst = c.sbase + (values ? OFF_V : OFF_K);
+  const int full = values ? VF : KF, empty = values ? VE : KE;
+  // The key of stage 0 and how much further stage 1's is; where a stage's bytes lie in an entry, likewise.
+  const int first = values ? row : 64 * (int)c.rank + row, second = values ? 64 : 0;
+  const int part = values ? (int)c.rank : 0, step = values ? 0 : 1;
   int tiles = 0;
   bool ok = true;
   Part u;
   while (ok && parts.next(&u)) {
-    int64_t key = (int64_t)u.lo * KEYS + 64 * c.rank + row;
-    const uint8_t* e = entry_of(p, table_block(p, u, key), key);
-    uint4 code[8], rope[4], sc;
-    auto load = [&]() {
-      if (e) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) code[i] = load16(e + 32 * i + 16 * half);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) rope[i] = load16(e + FP4_ROPE + 64 * half + 16 * i);
-        sc = load16(e + FP4_SCALES);
-      } else {
-        sc = make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) code[i] = sc;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) rope[i] = sc;
-      }
+    const int64_t key0 = (int64_t)u.lo * KEYS + first, end = (int64_t)u.hi * KEYS;
+    auto find = [&](int64_t key) { return key < end ? table_block(p, u, key) : PAST_END; };
+    auto get = [&](int32_t blk, int64_t key, int s, Stage* to) {
+      load_stage(entry_of(p, blk, key), 128 * (part + step * s) + 16 * half, FP4_SCALES + 8 * (part + step * s), to);
     };
-    load();
-    int32_t blk = u.lo + 1 < u.hi ? table_block(p, u, key + KEYS) : PAST_END;
-    for (int t = u.lo; t < u.hi; ++t, ++tiles) {
-      if (w4 == 0 && lane == 0) *begun = tiles;
-      if (above252(sc.x) | above252(sc.y) | above252(sc.z) | above252(sc.w)) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) rope[i] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+    Stage now, next;
+    get(find(key0), key0, 0, &now);
+    get(find(key0 + second), key0 + second, 1, &next);
+    // blocks of the two stages after those
+    int32_t blk0 = find(key0 + KEYS), blk1 = find(key0 + second + KEYS);
+    int64_t key = key0 + KEYS;
+#pragma unroll 1
+    for (int n = 0; n < 2 * (u.hi - u.lo); ++n) {
+      const int s = n & 1;
+      if (s == 0 && !values && w4 == 0 && lane == 0) *begun = tiles;
+      __syncwarp();
+      if (tiles > 0 && !c.wait_warp(empty + s, (tiles - 1) & 1)) {
+        ok = false;
+        break;
       }
-      const bool big = __any_sync(0xffffffffu, (above128(sc.x) | above128(sc.y) | above128(sc.z) | above128(sc.w)) != 0);
-      const uint32_t s4[4] = {sc.x >> (8 * half), sc.y >> (8 * half), sc.z >> (8 * half), sc.w >> (8 * half)};
+      const bool big = __any_sync(0xffffffffu, (above128(now.scale.x) | above128(now.scale.y)) != 0);
+      const uint32_t at = dst + s * 4 * QP;
 #pragma unroll
-      for (int g = 0; g < KGROUPS; ++g) {
-        if (tiles > 0 && !c.wait_warp(KE + g, (tiles - 1) & 1)) {
-          ok = false;
-          break;
-        }
-#pragma unroll
-        for (int i = 3 * g; i < 3 * g + 3 && i < 8; ++i) {
-          const uint32_t b = byte_of(s4[i >> 1], 2 * (i & 1));
-          if (big) put_group<true>(dst + i * QP, off, code[i], b);
-          else put_group<false>(dst + i * QP, off, code[i], b);
-        }
-        if (g == KGROUPS - 1) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) st_shared_v4(dst + 8 * QP + off[i], rope[i].x, rope[i].y, rope[i].z, rope[i].w);
-        }
-        tell(c, KF + g, lane);
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t b = byte_of((j < 2 ? now.scale.x : now.scale.y) >> (8 * half), 2 * (j & 1));
+        // 2^126 times the scale, or one after the other; values of a row that is NaN are zeros
+        uint32_t m = big ? 0x7e80u : (b + 126) << 7;
+        if (b > FP4_MAX_SCALE) m = 0;
+        put_group(at + j * QP, off, now.code[j], big, m | m << 16, scale_bf16x2(b > FP4_MAX_SCALE ? 0 : b));
       }
-      if (!ok) break;
-      key += KEYS;
-      if (t + 1 < u.hi) {
-        e = entry_of(p, blk, key);
-        load();
-        if (t + 2 < u.hi) blk = table_block(p, u, key + KEYS);
+      tell(c, full + s, lane);
+      now = next;
+      const int64_t k = key + (s ? second : 0);
+      get(s ? blk1 : blk0, k, s, &next);
+      if (s == 0) {
+        blk0 = find(k + KEYS);
+      } else {
+        blk1 = find(k + KEYS);
+        key += KEYS;
+        ++tiles;
       }
     }
   }
 }
 
-// Warps 12-15: rows 16 w + lane % 16 of both halves of the tile's keys, the CTA's four panels of values.
-__device__ void run_values(const Ctx& c, const TreeLaunch& p, Parts parts) {
-  const int lane = threadIdx.x & 31, w4 = (threadIdx.x >> 5) & 3, half = lane >> 4;
-  const int row = 16 * w4 + (lane & 15);
-  uint32_t off[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) off[i] = row * 128 + (((4 * half + i) ^ (row & 7)) << 4);
-  const uint32_t dst = c.sbase + OFF_V;
-  const int codes = 128 * (int)c.rank + 16 * half, scales = FP4_SCALES + 8 * (int)c.rank;
+// Warp 3: the ropes of the CTA's 64 keys, K's last panel.  Lane i has 16 bytes of rows 4 j + i / 8; a row with
+// a scale byte above 252 gets NaN.
+__device__ void run_ropes(const Ctx& c, const TreeLaunch& p, Parts parts) {
+  const int lane = threadIdx.x & 31, ch = lane & 7;
+  const uint32_t dst = c.sbase + OFF_K + 8 * QP;
   int tiles = 0;
   bool ok = true;
   Part u;
   while (ok && parts.next(&u)) {
-    int64_t key = (int64_t)u.lo * KEYS + row;
-    uint4 code[2][4];
-    uint2 sc[2];
-    int32_t blk[2] = {table_block(p, u, key), table_block(p, u, key + 64)};
-    auto load = [&](int i, int64_t k) {
-      const uint8_t* e = entry_of(p, blk[i], k);
-      if (e) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) code[i][j] = load16(e + codes + 32 * j);
-        sc[i] = __ldg(reinterpret_cast<const uint2*>(e + scales));
-      } else {
-        sc[i] = make_uint2(0, 0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) code[i][j] = make_uint4(0, 0, 0, 0);
-      }
-    };
-    load(0, key);
-    load(1, key + 64);
-    if (u.lo + 1 < u.hi) {
-      blk[0] = table_block(p, u, key + KEYS);
-      blk[1] = table_block(p, u, key + KEYS + 64);
-    }
-    for (int t = u.lo; t < u.hi; ++t, ++tiles, key += KEYS) {
+    int64_t key0 = (int64_t)u.lo * KEYS + 64 * c.rank;
+    KeyBlocks b = find_blocks(p, u, key0, lane);
+#pragma unroll 1
+    for (int t = u.lo; t < u.hi; ++t, ++tiles, key0 += KEYS) {
+      const KeyRows k = find_rows(p, b, key0, lane);
+      if (t + 1 < u.hi) b = find_blocks(p, u, key0 + KEYS, lane);
+      // which of a lane's two rows are NaN
+      uint32_t bad[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        if (tiles > 0 && !c.wait_warp(VE + i, (tiles - 1) & 1)) {
-          ok = false;
-          break;
-        }
-        const bool big = __any_sync(0xffffffffu, (above128(sc[i].x) | above128(sc[i].y)) != 0);
-        const uint32_t s2[2] = {sc[i].x >> (8 * half), sc[i].y >> (8 * half)};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t b = byte_of(s2[j >> 1], 2 * (j & 1));
-          if (big) put_group<true>(dst + i * V_HALF + j * QP, off, code[i][j], b);
-          else put_group<false>(dst + i * V_HALF + j * QP, off, code[i][j], b);
-        }
-        tell(c, VF + i, lane);
-        if (t + 1 < u.hi) load(i, key + KEYS + 64 * i);
+        uint4 s = make_uint4(0, 0, 0, 0);
+        if (k.r[i] != p.oob_row) s = load16(reinterpret_cast<const uint8_t*>(p.t.cache) + (int64_t)k.r[i] * FP4_ENTRY + FP4_SCALES);
+        bad[i] = __ballot_sync(0xffffffffu, (above252(s.x) | above252(s.y) | above252(s.z) | above252(s.w)) != 0);
       }
-      if (!ok) break;
-      if (t + 2 < u.hi) {
-        blk[0] = table_block(p, u, key + 2 * KEYS);
-        blk[1] = table_block(p, u, key + 2 * KEYS + 64);
+      if (tiles > 0 && !c.wait_warp(KE + 2, (tiles - 1) & 1)) {
+        ok = false;
+        break;
       }
+#pragma unroll 2
+      for (int j = 0; j < 16; ++j) {
+        const int key = 4 * j + (lane >> 3);
+        const int32_t row = __shfl_sync(0xffffffffu, j < 8 ? k.r[0] : k.r[1], key & 31);
+        const bool there = row != p.oob_row;
+        const uint8_t* src = (there ? reinterpret_cast<const uint8_t*>(p.t.cache) + (int64_t)row * FP4_ENTRY + FP4_ROPE
+                                    : reinterpret_cast<const uint8_t*>(p.t.q)) + ch * 16;
+        cp_async16(dst + key * 128 + ((ch ^ (key & 7)) << 4), src, there ? 16 : 0);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      if (bad[0] | bad[1]) {
+        __syncwarp();   // (a row's pieces are other lanes' copies)
+        for (int j = 0; j < 16; ++j) {
+          const int key = 4 * j + (lane >> 3);
+          if ((bad[j >> 3] >> (key & 31)) & 1)
+            st_shared_v4(dst + key * 128 + ch * 16, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+        }
+      }
+      tell(c, KF + 2, lane);
     }
   }
 }
@@ -290,10 +285,11 @@ tree_attn_fp4_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   ReqWords words{0, 0, 0};   // (on their way while the barriers are made)
   if ((int)threadIdx.x < p.t.batch) words = load_words(p.t, threadIdx.x);
   if (warp == 1) {
-    // P: every softmax warp of both CTAs; maxima: the two warps of 32 rows; keys and values: four warps of each.
+    // P: every softmax warp of both CTAs; maxima: the two warps of 32 rows; keys and values: four warps of
+    // each CTA; ropes: one.
     static_assert(NBAR <= 32, "a lane each");
-    const bool rows = (lane >= KF && lane < KF + KGROUPS) || (lane >= VF && lane < VF + 2);
-    if (lane < NBAR) mbar_init(c.bar(lane), lane == PR || rows ? 8 : lane == XB || lane == XB + 1 ? 2 : 1);
+    const bool rows = lane == KF || lane == KF + 1 || lane == VF || lane == VF + 1;
+    if (lane < NBAR) mbar_init(c.bar(lane), lane == PR || rows ? 8 : lane == KF + 2 || lane == XB || lane == XB + 1 ? 2 : 1);
     if (lane == 0) {
       *abort_flag = 0;
       *begun = -1;
@@ -320,15 +316,15 @@ tree_attn_fp4_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   if (warp < 4) {
     setmaxnreg_dec<REGS_CTRL>();
     if (warp == 0) run_queries(c, parts, &tm_q);
-    else if (warp == 1 && rank == 0) run_mma<64>(c, p, parts, tmem);
+    else if (warp == 1 && rank == 0) run_mma<FP4>(c, p, parts, tmem);
     else if (warp == 2) run_prefetch(c, p, parts, begun);
+    else if (warp == 3) run_ropes(c, p, parts);
   } else if (warp < 8) {
     setmaxnreg_inc<REGS_SOFTMAX>();
     run_softmax(c, p, parts, tmem, ws + WS_SLOTS + (size_t)worker * 2 * SLOT_BYTES, smem);
   } else {
     setmaxnreg_dec<REGS_ROWS>();
-    if (warp < 12) run_keys(c, p, parts, begun);
-    else run_values(c, p, parts);
+    run_rows(c, p, parts, warp >= 12, begun);
   }
   __syncwarp();
   tc_fence_before();

@@ -116,16 +116,20 @@ __device__ __forceinline__ void commit_both(uint32_t bar) {
       : "memory");
 }
 
+// R: rows of a box (tree_attn_kernel), or FP4 (tree_attn_fp4_kernel): K's groups are then two of four panels and
+// the rope's panel.
+constexpr int FP4 = 4;
 template <int R>
 __device__ void run_mma(const Ctx& c, const TreeLaunch& p, Parts parts, uint32_t tmem) {
   const uint64_t q_desc = sdesc_sw128(c.sbase + OFF_Q, 16, 1024);
   // A group of K lies in panels of 64 rows, or eight rows at a time with their three panels.
-  constexpr bool rows8 = R > 0 && R < 64;
+  constexpr bool rows8 = R == 8 || R == 16 || R == 32;
   constexpr uint32_t K_PANEL = rows8 ? 1024 : QP;
   const uint64_t k_desc = sdesc_sw128(c.sbase + OFF_K, 16, rows8 ? K_ROWS8 : 1024);
   // Values lie in pieces of r keys, each with its four panels: 16 keys of a product are part of one
   // piece, a whole one or two.
-  constexpr int r = R > 0 ? R : 64;
+  constexpr int r = rows8 ? R : 64;
+  constexpr int GP = R == FP4 ? 4 : 3;   // panels of a group of K
   const uint64_t v_desc = sdesc_sw128(c.sbase + OFF_V, r * 128, r == 8 ? 4096 : 1024);
   constexpr uint32_t v_chunk = (uint32_t)(2 * r * 128) >> 4;
   const uint64_t p_desc = sdesc_sw128(c.sbase + OFF_P, 16, 1024);
@@ -155,10 +159,10 @@ __device__ void run_mma(const Ctx& c, const TreeLaunch& p, Parts parts, uint32_t
         seen_v = c.look(VF, pv & 1);
       }
 #pragma unroll 1
-      for (int i = 0; i < 3; ++i) {
+      for (int i = 0; i < GP && GP * g + i < NP; ++i) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-          const uint32_t qo = (uint32_t)((3 * g + i) * QP + kk * 32) >> 4, ko = (uint32_t)(3 * g * QP + i * K_PANEL + kk * 32) >> 4;
+          const uint32_t qo = (uint32_t)((GP * g + i) * QP + kk * 32) >> 4, ko = (uint32_t)(GP * g * QP + i * K_PANEL + kk * 32) >> 4;
           issue(d, q_desc + qo, k_desc + ko, IDESC_QK, kk > 0 ? 1u : g + i > 0 ? 1u : 0u);
         }
       }
