@@ -3,10 +3,9 @@
 // over keys and values that are made bf16 on their way into shared memory.
 //
 // Eight warps make them: four the CTA's 64 keys of a tile as the half of S's B operand, four the tile's 128
-// keys x 256 of the value columns.  A lane has a row and one 32-value group (16 bytes, one scale) of each
-// panel: it loads them into registers while the products read the tile before, waits until four panels
-// are free, and writes 64 bytes of each in the swizzle that the products expect.  Eight lanes of a store have
-// eight rows, and so eight different bank groups.  Entries go straight from L2 to registers: there is no
+// keys x 256 of the value columns.  A lane has four 32-value groups (16 bytes,
+// one scale) at a time: it loads them into registers while the products read the tile before, waits until four
+// panels are free, and writes 64 bytes of each in the swizzle that the products expect.  Entries go straight from L2 to registers: there is no
 // room for them in shared memory beside Q (72 KB), a tile (136 KB) and P.
 //   warp 0     Q producer
 //   warp 1     even CTA: issues every product
@@ -42,20 +41,14 @@ __device__ __forceinline__ void setmaxnreg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Where a key's entry lies: its table's block, looked up a tile ahead, then its address (null: zeros).
-__device__ __forceinline__ const uint8_t* entry_of(const TreeLaunch& p, int32_t blk, int64_t key) {
-  const int32_t row = block_row(p, blk, key);
-  return row == p.oob_row ? nullptr : reinterpret_cast<const uint8_t*>(p.t.cache) + (int64_t)row * FP4_ENTRY;
-}
 __device__ __forceinline__ uint4 load16(const uint8_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
-__device__ __forceinline__ uint32_t byte_of(uint32_t w, int i) { return (w >> (8 * i)) & 0xffu; }
-// Bytes of a word above 252 (in their top bits), and above 128.
+// Bytes of a word above 252 (in their top bits).
 __device__ __forceinline__ uint32_t above252(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x03030303u) & w & 0x80808080u; }
-__device__ __forceinline__ uint32_t above128(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x7f7f7f7fu) & w & 0x80808080u; }
 
-// A group's 32 values to four 16-byte pieces at `at` + the swizzled offsets.  Each code is multiplied by `m`
-// and, where the scales are `big`, by `m2`.
-__device__ __forceinline__ void put_group(uint32_t at, const uint32_t* off, const uint4& w, bool big, uint32_t m, uint32_t m2) {
+// A group's 32 values to four 16-byte pieces.  Each code is multiplied by `m` and, where the scales are `big`,
+// by `m2`.
+__device__ __forceinline__ void put_group(const uint32_t* at, uint32_t flip, uint32_t more, const uint4& w, bool big, uint32_t m,
+                                          uint32_t m2) {
   const uint32_t words[4] = {w.x, w.y, w.z, w.w};
   uint32_t r[4][4];
 #pragma unroll
@@ -71,7 +64,7 @@ __device__ __forceinline__ void put_group(uint32_t at, const uint32_t* off, cons
       for (int k = 0; k < 4; ++k) r[i][k] = mul_bf16x2(r[i][k], m2);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) st_shared_v4(at + off[i], r[i][0], r[i][1], r[i][2], r[i][3]);
+  for (int i = 0; i < 4; ++i) st_shared_v4((at[i] ^ flip) + more, r[i][0], r[i][1], r[i][2], r[i][3]);
 }
 
 // A warp's part of what it writes is there: handed to the products' proxy, told to the even CTA.
@@ -86,50 +79,58 @@ __device__ __forceinline__ void tell(const Ctx& c, int b, int lane) {
 
 // What the eight warps do is a line of stages, two for each tile: four panels of 64 rows each.  Keys (warps
 // 8-11): panels 0-3 and 4-7 of the CTA's 64 keys; values (warps 12-15): the CTA's four panels, of the tile's
-// first and second 64 keys.  A warp has 16 rows, a lane one of them and half of each panel.  The bytes of the
-// stage after next are loaded when a stage is done: most of a tile's time before they are needed.  One loop
+// first and second 64 keys.  A warp has 16 rows.  The bytes of the stage after next are loaded when a stage is done: most of a tile's time before they are needed.  One loop
 // for both, and short: straight code for a tile of each did not stay in the instruction cache (see below).
+//
+// Lane (panel, row % 4, half) = (l / 8, l / 2 % 4, l % 2) has a piece of rows 4 j + row % 4 of the warp's, j < 4:
+// a load takes 128 bytes of four rows, and eight lanes of a store have eight different bank groups.
 struct Stage {
   uint4 code[4];
-  uint2 scale;
+  uint32_t scale[4];
 };
-__device__ __forceinline__ void load_stage(const uint8_t* e, int at_code, int at_scale, Stage* s) {
-  if (e) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) s->code[j] = load16(e + at_code + 32 * j);
-    s->scale = __ldg(reinterpret_cast<const uint2*>(e + at_scale));
-  } else {
-    s->scale = make_uint2(0, 0);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) s->code[j] = make_uint4(0, 0, 0, 0);
-  }
-}
 __device__ void run_rows(const Ctx& c, const TreeLaunch& p, Parts parts, bool values, volatile int* begun) {
-  const int lane = threadIdx.x & 31, w4 = (threadIdx.x >> 5) & 3, half = lane >> 4;
-  const int row = 16 * w4 + (lane & 15);
-  uint32_t off[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) off[i] = row * 128 + (((4 * half + i) ^ (row & 7)) << 4);
+  const int lane = threadIdx.x & 31, w4 = (threadIdx.x >> 5) & 3, r4 = (lane >> 1) & 3;
+  const int group = 2 * (lane >> 3) + (lane & 1);   // of the stage's eight
   const uint32_t dst = c.sbase + (values ? OFF_V : OFF_K);
+  uint32_t at[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) at[i] = dst + (lane >> 3) * QP + (16 * w4 + r4) * 128 + (((4 * (lane & 1) + i) ^ r4) << 4);
   const int full = values ? VF : KF, empty = values ? VE : KE;
-  // The key of stage 0 and how much further stage 1's is; where a stage's bytes lie in an entry, likewise.
-  const int first = values ? row : 64 * (int)c.rank + row, second = values ? 64 : 0;
+  // The key of stage 0 that this lane looks up (lanes 0-15: the warp's rows), how much further stage 1's is,
+  // and where a stage's bytes lie in an entry.
+  const int first = (values ? 0 : 64 * (int)c.rank) + 16 * w4 + (lane & 15), second = values ? 64 : 0;
   const int part = values ? (int)c.rank : 0, step = values ? 0 : 1;
+  const uint8_t* cache = reinterpret_cast<const uint8_t*>(p.t.cache);
   int tiles = 0;
   bool ok = true;
   Part u;
   while (ok && parts.next(&u)) {
-    const int64_t key0 = (int64_t)u.lo * KEYS + first, end = (int64_t)u.hi * KEYS;
-    auto find = [&](int64_t key) { return key < end ? table_block(p, u, key) : PAST_END; };
-    auto get = [&](int32_t blk, int64_t key, int s, Stage* to) {
-      load_stage(entry_of(p, blk, key), 128 * (part + step * s) + 16 * half, FP4_SCALES + 8 * (part + step * s), to);
+    const int64_t end = min((int64_t)u.hi * KEYS, (int64_t)u.q.kv);
+    // A block as the table has it: looked at a tile later, so that nothing waits for it here.
+    auto find = [&](int64_t key) {
+      return key < end ? __ldg(p.t.block_table + (int64_t)u.r * p.t.max_blocks + block_of(p, (int)key)) : 0;
     };
+    auto get = [&](int32_t blk, int64_t key, int s, Stage* to) {
+      const int32_t mine = key < end ? block_row(p, blk == PAST_END ? -1 : blk, key) : p.oob_row;
+      const int at_code = 128 * (part + step * s) + 16 * group, at_scale = FP4_SCALES + 8 * (part + step * s) + group;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int32_t row = __shfl_sync(0xffffffffu, mine, 4 * j + r4);
+        to->code[j] = make_uint4(0, 0, 0, 0);
+        to->scale[j] = 0;
+        if (row != p.oob_row) {
+          const uint8_t* e = cache + (int64_t)row * FP4_ENTRY;
+          to->code[j] = load16(e + at_code);
+          to->scale[j] = __ldg(e + at_scale);
+        }
+      }
+    };
+    int64_t key = (int64_t)u.lo * KEYS + first;
     Stage now, next;
-    get(find(key0), key0, 0, &now);
-    get(find(key0 + second), key0 + second, 1, &next);
-    // blocks of the two stages after those
-    int32_t blk0 = find(key0 + KEYS), blk1 = find(key0 + second + KEYS);
-    int64_t key = key0 + KEYS;
+    get(find(key), key, 0, &now);
+    get(find(key + second), key + second, 1, &next);
+    key += KEYS;
+    int32_t blk0 = find(key), blk1 = find(key + second);   // of the two stages after those
 #pragma unroll 1
     for (int n = 0; n < 2 * (u.hi - u.lo); ++n) {
       const int s = n & 1;
@@ -139,15 +140,16 @@ __device__ void run_rows(const Ctx& c, const TreeLaunch& p, Parts parts, bool va
         ok = false;
         break;
       }
-      const bool big = __any_sync(0xffffffffu, (above128(now.scale.x) | above128(now.scale.y)) != 0);
-      const uint32_t at = dst + s * 4 * QP;
+      const uint32_t most = max(max(now.scale[0], now.scale[1]), max(now.scale[2], now.scale[3]));
+      const bool big = __any_sync(0xffffffffu, most > 128);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t b = byte_of((j < 2 ? now.scale.x : now.scale.y) >> (8 * half), 2 * (j & 1));
+        const uint32_t b = now.scale[j];
         // 2^126 times the scale, or one after the other; values of a row that is NaN are zeros
         uint32_t m = big ? 0x7e80u : (b + 126) << 7;
         if (b > FP4_MAX_SCALE) m = 0;
-        put_group(at + j * QP, off, now.code[j], big, m | m << 16, scale_bf16x2(b > FP4_MAX_SCALE ? 0 : b));
+        put_group(at, (j & 1) << 6, s * 4 * QP + j * 512, now.code[j], big, m | m << 16,
+                  scale_bf16x2(b > FP4_MAX_SCALE ? 0 : b));
       }
       tell(c, full + s, lane);
       now = next;
@@ -259,8 +261,10 @@ __device__ void run_prefetch(const Ctx& c, const TreeLaunch& p, Parts parts, con
         for (int i = 0; i < 2; ++i) {
           const int64_t key = (int64_t)(t + AHEAD) * KEYS + 64 * c.rank + 32 * i + lane;
           if (key < u.q.kv) {
-            const uint8_t* e = entry_of(p, table_block(p, u, key), key);
-            if (e) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(e), "r"(FP4_ENTRY) : "memory");
+            const int32_t row = block_row(p, table_block(p, u, key), key);
+            const uint8_t* e = reinterpret_cast<const uint8_t*>(p.t.cache) + (int64_t)row * FP4_ENTRY;
+            if (row != p.oob_row)
+              asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(e), "r"(FP4_ENTRY) : "memory");
           }
         }
       }
