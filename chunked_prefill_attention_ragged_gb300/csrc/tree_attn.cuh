@@ -8,12 +8,13 @@
 
 namespace mla {
 
-constexpr int TREE_ROWS = 128;   // (node, head) pairs per unit
-constexpr int TREE_KEYS = 128;   // keys per tile
+// (node, head) pairs per unit and keys per tile, unless a kernel says otherwise (the ROWS and KEYS below).
+constexpr int TREE_ROWS = 128;
+constexpr int TREE_KEYS = 128;
 
 struct TreeLaunch {
   TreeParams t;
-  int workers;         // clusters of two CTAs
+  int workers;         // clusters of two CTAs, or CTAs
   int32_t oob_row;     // a row coordinate past the cache: the copy fills it with zeros
   int block_shift;     // log2 of the block size, or -1
   int o_align32;
@@ -136,6 +137,7 @@ struct ReqWords {
 __device__ __forceinline__ ReqWords load_words(const TreeParams& p, int r) {
   return {__ldg(p.qo_indptr + r), __ldg(p.qo_indptr + r + 1), __ldg(p.kv_lens + r)};
 }
+template <int ROWS = TREE_ROWS, int KEYS = TREE_KEYS>
 __device__ __forceinline__ Req make_req(const TreeParams& p, const ReqWords& w, bool report) {
   Req q;
   const int64_t reach = (int64_t)p.max_blocks * p.block_size;
@@ -146,12 +148,13 @@ __device__ __forceinline__ Req make_req(const TreeParams& p, const ReqWords& w, 
   q.nodes = rows_ok ? w.q1 - w.q0 : 0;
   q.ctx = (int64_t)w.len - q.nodes;
   q.kv = len_ok ? w.len : (w.len < 0 ? 0 : (int)reach);
-  q.units = (int)(((int64_t)q.nodes * p.num_heads + TREE_ROWS - 1) / TREE_ROWS);
-  q.tiles = q.units ? max(1, (q.kv + TREE_KEYS - 1) / TREE_KEYS) : 0;
+  q.units = (int)(((int64_t)q.nodes * p.num_heads + ROWS - 1) / ROWS);
+  q.tiles = q.units ? max(1, (int)(((int64_t)q.kv + KEYS - 1) / KEYS)) : 0;
   return q;
 }
+template <int ROWS = TREE_ROWS, int KEYS = TREE_KEYS>
 __device__ __forceinline__ Req load_req(const TreeParams& p, int r, bool report) {
-  return make_req(p, load_words(p, r), report);
+  return make_req<ROWS, KEYS>(p, load_words(p, r), report);
 }
 
 // Where a worker's piece starts.
@@ -171,26 +174,27 @@ struct Part {
   int slot;            // 0: the worker's first part, 1: a later one (its last, if not whole)
 };
 
-struct Parts {
+template <int ROWS, int KEYS>
+struct PartsOf {
   const TreeParams& p;
   int64_t left;
   int r, unit, tile, index;
   Req q;
-  __device__ Parts(const TreeParams& tp, const StartRec& s, int64_t count)
+  __device__ PartsOf(const TreeParams& tp, const StartRec& s, int64_t count)
       : p(tp), left(count), r(s.req), unit(s.unit), tile(s.tile), index(0), q(s.q) {}
   __device__ bool next(Part* out) {
     if (left <= 0) return false;
     while (unit >= q.units) {   // to the next request that has rows
       if (++r >= p.batch) return false;   // (lengths changed under the kernel: out of bounds is not read)
       unit = 0;
-      q = load_req(p, r, false);
+      q = load_req<ROWS, KEYS>(p, r, false);
     }
     const int n = (int)min((int64_t)(q.tiles - tile), left);
     out->q = q;
     out->r = r;
-    const int64_t first = (int64_t)unit * TREE_ROWS;
+    const int64_t first = (int64_t)unit * ROWS;
     out->pair0 = (int64_t)q.q0 * p.num_heads + first;
-    out->npairs = (int)min((int64_t)TREE_ROWS, (int64_t)q.nodes * p.num_heads - first);
+    out->npairs = (int)min((int64_t)ROWS, (int64_t)q.nodes * p.num_heads - first);
     out->lo = tile;
     out->hi = tile + n;
     out->whole = n == q.tiles;
@@ -202,6 +206,7 @@ struct Parts {
     return true;
   }
 };
+using Parts = PartsOf<TREE_ROWS, TREE_KEYS>;
 
 // From key positions to cache rows: first the block as the table has it (its load is under way while
 // the caller does other things), then the row to copy.  A key past the readable ones, or in a block
@@ -272,7 +277,7 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {   // 0 <= a,
 
 // Where worker w's piece starts and how long it is, and what is to be joined at its start; every
 // thread of the CTA calls, with the words of request threadIdx.x, loaded before.
-template <int NTHREADS>
+template <int NTHREADS, int ROWS = TREE_ROWS, int KEYS = TREE_KEYS>
 __device__ __forceinline__ void find_piece(const TreeParams& p, const ReqWords& own, int worker, int workers,
                                            bool report, StartRec* start, int64_t* count, JoinRec* join) {
   __shared__ int64_t warp_sum[NTHREADS / 32];
@@ -281,7 +286,7 @@ __device__ __forceinline__ void find_piece(const TreeParams& p, const ReqWords& 
   const int r0 = min(tid * per, p.batch), r1 = min(r0 + per, p.batch);
   int64_t mine = 0;
   for (int r = r0; r < r1; ++r) {
-    const Req q = per == 1 ? make_req(p, own, report) : load_req(p, r, report);
+    const Req q = per == 1 ? make_req<ROWS, KEYS>(p, own, report) : load_req<ROWS, KEYS>(p, r, report);
     mine += (int64_t)q.units * q.tiles;
   }
   int64_t incl = mine;
@@ -307,7 +312,7 @@ __device__ __forceinline__ void find_piece(const TreeParams& p, const ReqWords& 
   if (lo < hi && lo >= before && lo < before + mine) {
     int64_t sum = before;
     for (int r = r0; r < r1; ++r) {
-      const Req q = per == 1 ? make_req(p, own, false) : load_req(p, r, false);
+      const Req q = per == 1 ? make_req<ROWS, KEYS>(p, own, false) : load_req<ROWS, KEYS>(p, r, false);
       const int64_t k = (int64_t)q.units * q.tiles;
       if (lo < sum + k) {
         const int unit = (int)quotient(lo - sum, q.tiles), tile = (int)(lo - sum - (int64_t)unit * q.tiles);
@@ -318,8 +323,8 @@ __device__ __forceinline__ void find_piece(const TreeParams& p, const ReqWords& 
           // The last worker with a part is the one that has the unit's last tile.
           const int64_t end = first + q.tiles - 1, big = more * (each + 1);
           const int last = (int)(end < big ? quotient(end, each + 1) : more + quotient(end - big, each));
-          j.pair0 = (int64_t)q.q0 * p.num_heads + (int64_t)unit * TREE_ROWS;
-          j.npairs = (int)min((int64_t)TREE_ROWS, (int64_t)q.nodes * p.num_heads - (int64_t)unit * TREE_ROWS);
+          j.pair0 = (int64_t)q.q0 * p.num_heads + (int64_t)unit * ROWS;
+          j.npairs = (int)min((int64_t)ROWS, (int64_t)q.nodes * p.num_heads - (int64_t)unit * ROWS);
           j.parts = last - worker + 2;
           j.slot0 = prev < first ? 1 : 0;
         }
@@ -346,6 +351,9 @@ __device__ __forceinline__ int32_t piece_rows(const TreeLaunch& p, const Part& u
 
 // tree_join_kernel.cu: joins the parts of units that several workers left.
 cudaError_t launch_tree_join(const TreeLaunch& p, cudaStream_t stream);
+// The same for units of few pairs: a slot is O (fp32) row by row, then the rows' (m in log2 units, l).
+__host__ __device__ constexpr size_t few_slot_bytes(int rows) { return (size_t)rows * (512 * 4 + 8); }
+cudaError_t launch_tree_join_few(const TreeLaunch& p, int rows, cudaStream_t stream);
 
 constexpr uint64_t TREE_DRAIN_LIMIT_NS = 200000000ull;   // own copies and products after an abort
 constexpr float TREE_RESCALE_THRESHOLD = 8.0f;           // log2 units

@@ -389,6 +389,8 @@ int max_workers() {
 }  // namespace
 
 cudaError_t launch_tree_attention_fp4(const TreeParams& t, cudaStream_t stream) {
+  const int64_t pairs = (t.total_rows * t.num_heads + t.batch - 1) / t.batch;   // of a request, on average
+  if (pairs <= 32) return launch_tree_attention_fp4_few(t, (int)pairs, stream);
   const TreeLaunch p = tree_launch(t, max_workers());
   if (p.workers <= 0) return cudaErrorInvalidConfiguration;
   CUtensorMap tq;
