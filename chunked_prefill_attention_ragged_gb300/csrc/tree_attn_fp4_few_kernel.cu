@@ -12,8 +12,10 @@
 //
 // Tiles are shared out among the SMs as in tree_attn_kernel.cu (equal pieces of the line of all tiles, parts
 // joined by a second kernel).  Two tile buffers: one is made while the other is multiplied.
-//   warp 0  Q producer    1  issues the products    2  brings rows to come into L2    3  TMEM; ropes
-//   warps 4-7  softmax and output    8-15  codes to bf16: eight rows each
+//   warp 0  copies entries into a ring in shared memory     1  issues S    2  issues P V    3  TMEM; Q; brings
+//   entries to come into L2    warps 4-7  softmax and output    8-15  entries to bf16
+// S and P V have a warp each: from one warp, which has to take them in a fixed order, P V waited for the next
+// tile's keys or S for this tile's softmax (64 x 1 over 8192 at 16 heads: 184 us).
 // Where P V's accumulator lies: columns 128 i .. of the latent in TMEM columns N i .., lane = column.
 #include <algorithm>
 
@@ -32,29 +34,34 @@ constexpr int REGS_CTRL = 96, REGS_SOFTMAX = 208, REGS_ROWS = 104;
 static_assert(REGS_CTRL + REGS_SOFTMAX + 2 * REGS_ROWS <= 4 * LAUNCH_REGS, "register split exceeds the launch allocation");
 constexpr int PANEL = KEYS * 128;        // 64 keys x 64 columns
 constexpr int TILE = 9 * PANEL;
+constexpr int HALF = KEYS / 2 * FP4_ENTRY;   // half a tile's entries
 constexpr int AHEAD = 4;                 // tiles between the one being made and the one brought into L2
 constexpr uint32_t TMEM_COLS = 256;
 
 template <int N>
 struct Off {
-  static constexpr int TILES = 0, Q = 2 * TILE, P = Q + 9 * N * 128, FLAG = P + 2 * N * 128;
+  static constexpr int SLOTS = N == 16 ? 4 : 2;   // of the ring, half a tile's entries each
+  static constexpr int TILES = 0, Q = 2 * TILE, P = Q + 9 * N * 128, RING = P + 2 * N * 128;
+  static constexpr int FLAG = RING + SLOTS * HALF;
   static constexpr int MAXIMA = FLAG + 2 * 4 * 4, SUMS = MAXIMA + 4 * N * 4, BAR = SUMS + 4 * N * 4;
-  static constexpr int MISC = BAR + 16 * 8, SMEM = MISC + 64 + 1024;
+  static constexpr int THERE = BAR + 24 * 8, MISC = THERE + SLOTS * 4, SMEM = MISC + 64 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
 enum Bar {
   QF = 0,       // Q landed
   QE,           // the part's last S done: Q may be replaced
-  CF,           // [buffer][half] panels 0-3, panels 4-8 made
-  TE = CF + 4,  // [buffer] P V done: the tile, P's buffer and, for the next rescale, O are free
+  CF,           // [buffer] tile made
+  TE = CF + 2,  // [buffer] P V done: the tile, P's buffer and, for the next rescale, O are free
   SF = TE + 2,  // [buffer] S done
   PR = SF + 2,  // [buffer] P written (and the S buffer read) by the four softmax warps
   XB = PR + 2,  // exchange among them
-  FIN,          // every product drained
-  NEVER,        // nothing arrives here: the time-out test mode waits on it
+  EF,           // [slot] entries landed
+  EE = EF + 4,  // [slot] entries read
+  FIN = EE + 4, // [S, P V] every product drained
+  NEVER = FIN + 2,   // nothing arrives here: the time-out test mode waits on it
   NBAR
 };
-static_assert(NBAR <= 16, "barriers");
+static_assert(NBAR <= 24, "barriers");
 
 template <int R>
 __device__ __forceinline__ void setmaxnreg_dec() {
@@ -86,13 +93,9 @@ struct Ctx {
 template <int N>
 using PartsN = PartsOf<N, KEYS>;
 
-__device__ __forceinline__ uint4 load16(const uint8_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 __device__ __forceinline__ void st_shared_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
-// Bytes of a word above 252 (in their top bits).
-__device__ __forceinline__ uint32_t above252(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x03030303u) & w & 0x80808080u; }
-
 // A warp's part of what it writes is there: handed to the products' proxy.
 template <int N>
 __device__ __forceinline__ void tell(const Ctx<N>& c, int b, int lane) {
@@ -101,154 +104,160 @@ __device__ __forceinline__ void tell(const Ctx<N>& c, int b, int lane) {
   if (lane == 0) mbar_arrive(c.bar(b));
 }
 
-// Four groups of 32 values of a row piece (see tree_attn_fp4_kernel.cu: one product by 2^126 times the scale,
-// or two where the scales are `big`).
-__device__ __forceinline__ void put_group(const uint32_t* at, uint32_t flip, uint32_t more, const uint4& w, bool big, uint32_t m,
-                                          uint32_t m2) {
-  const uint32_t words[4] = {w.x, w.y, w.z, w.w};
-  uint32_t r[4][4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    fp4_fields(words[i], r[i]);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) r[i][k] = mul_bf16x2(r[i][k], m);
-  }
-  if (big) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) r[i][k] = mul_bf16x2(r[i][k], m2);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) st_shared_v4((at[i] ^ flip) + more, r[i][0], r[i][1], r[i][2], r[i][3]);
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
 }
 
-// Warps 8-15.  Lane (panel % 4, row % 4, half) = (l / 8, l / 2 % 4, l % 2); piece j: row 4 (j % 2) + row % 4 of
-// the warp's eight, panel 4 (j / 2) + panel % 4.  The bytes of the tile after next are loaded when a tile is done.
-struct Pieces {
-  uint4 code[4];
-  uint32_t scale[4];
-};
+// Warp 0: half a tile's entries at a time, in runs of rows that lie side by side (`run`: as many of 32 as the
+// block size is a multiple of, 8 at least, or 1), a lane a row.
 template <int N>
-__device__ void run_rows(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts, volatile int* begun) {
-  const int lane = threadIdx.x & 31, w8 = (threadIdx.x >> 5) - 8, r4 = (lane >> 1) & 3;
-  const int group = 2 * (lane >> 3) + (lane & 1);   // of the half's eight
-  uint32_t at[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    at[i] = c.sbase + Off<N>::TILES + (lane >> 3) * PANEL + (8 * w8 + r4) * 128 + (((4 * (lane & 1) + i) ^ r4) << 4);
+__device__ void run_copies(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts, uint8_t* smem, volatile int* begun) {
+  constexpr int SLOTS = Off<N>::SLOTS;
+  const int lane = threadIdx.x & 31, bs = p.t.block_size;
+  const int run = bs % 32 == 0 ? 32 : bs % 16 == 0 ? 16 : bs % 8 == 0 ? 8 : 1;
+  volatile uint32_t* there = reinterpret_cast<volatile uint32_t*>(smem + Off<N>::THERE);   // which rows exist
   const uint8_t* cache = reinterpret_cast<const uint8_t*>(p.t.cache);
-  int g = 0;
+  uint32_t put = 0;
   bool ok = true;
   Part u;
   while (ok && parts.next(&u)) {
     const int64_t end = min((int64_t)u.hi * KEYS, (int64_t)u.q.kv);
-    auto find = [&](int64_t key) {
-      return key < end ? __ldg(p.t.block_table + (int64_t)u.r * p.t.max_blocks + block_of(p, (int)key)) : 0;
+    // A block as the table has it: looked at two steps later, so that nothing waits for it here.
+    auto find = [&](int64_t k) {
+      return k < end ? __ldg(p.t.block_table + (int64_t)u.r * p.t.max_blocks + block_of(p, (int)k)) : 0;
     };
-    auto get = [&](int32_t blk, int64_t key, Pieces* to) {
-      const int32_t mine = key < end ? block_row(p, blk == PAST_END ? -1 : blk, key) : p.oob_row;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int32_t row = __shfl_sync(0xffffffffu, mine, 4 * (j & 1) + r4);
-        to->code[j] = make_uint4(0, 0, 0, 0);
-        to->scale[j] = 0;
-        if (row != p.oob_row) {
-          const uint8_t* e = cache + (int64_t)row * FP4_ENTRY;
-          to->code[j] = load16(e + 128 * (j >> 1) + 16 * group);
-          to->scale[j] = __ldg(e + FP4_SCALES + 8 * (j >> 1) + group);
-        }
-      }
-    };
-    int64_t key = (int64_t)u.lo * KEYS + 8 * w8 + (lane & 7);   // the row that this lane looks up
-    Pieces now, next;
-    get(find(key), key, &now);
-    get(find(key + KEYS), key + KEYS, &next);
-    int32_t blk = find(key + 2 * KEYS);
+    int64_t key = (int64_t)u.lo * KEYS + lane;
+    int32_t blk0 = find(key), blk1 = find(key + 32);
 #pragma unroll 1
-    for (int t = u.lo; t < u.hi; ++t, ++g) {
-      if (w8 == 0 && lane == 0) *begun = g;
-      __syncwarp();
-      const int b = g & 1;
-      if (g > 1 && !c.wait_warp(TE + b, ((g >> 1) - 1) & 1)) {
+    for (int n = 0; n < 2 * (u.hi - u.lo); ++n, key += 32, ++put) {
+      const int32_t row = key < end ? block_row(p, blk0 == PAST_END ? -1 : blk0, key) : p.oob_row;
+      blk0 = blk1;
+      blk1 = find(key + 64);
+      const uint32_t have = __ballot_sync(0xffffffffu, row != p.oob_row);
+      const uint32_t slot = put % SLOTS, dst = c.sbase + Off<N>::RING + slot * HALF;
+      if (put >= SLOTS && !c.wait_warp(EE + slot, (put / SLOTS - 1) & 1)) {
         ok = false;
         break;
       }
-      const uint32_t most = max(max(now.scale[0], now.scale[1]), max(now.scale[2], now.scale[3]));
-      const bool big = __any_sync(0xffffffffu, most > 128);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t s = now.scale[j];
-        uint32_t m = big ? 0x7e80u : (s + 126) << 7;   // 2^126 times the scale, or one after the other
-        if (s > FP4_MAX_SCALE) m = 0;                  // values of a row that is NaN are zeros
-        put_group(at, (j & 1) << 6, b * TILE + (j >> 1) * 4 * PANEL + (j & 1) * 512, now.code[j], big, m | m << 16,
-                  scale_bf16x2(s > FP4_MAX_SCALE ? 0 : s));
-        if (j & 1) tell(c, CF + 2 * b + (j >> 1), lane);
+      if (lane == 0) {
+        *begun = put >> 1;
+        there[slot] = have;
+        if (have) mbar_arrive_expect_tx(c.bar(EF + slot), __popc(have) * FP4_ENTRY);
+        else mbar_arrive(c.bar(EF + slot));
       }
-      now = next;
-      get(blk, key + 2 * KEYS, &next);
-      key += KEYS;
-      blk = find(key + 2 * KEYS);
+      __syncwarp();
+      const uint32_t mine = __popc((have >> lane) & (run == 32 ? 0xffffffffu : (1u << run) - 1));   // (the first of a run)
+      if ((lane & (run - 1)) == 0 && (have >> lane & 1))
+        bulk_load(dst + lane * FP4_ENTRY, cache + (int64_t)row * FP4_ENTRY, mine * FP4_ENTRY, c.bar(EF + slot));
+      __syncwarp();
     }
   }
+  // Let every copy started here land before the CTA can exit.
+  if (lane == 0)
+    for (uint32_t k = put > SLOTS ? put - SLOTS : 0; k < put; ++k) c.drain(EF + k % SLOTS, (k / SLOTS) & 1);
 }
 
-// Warp 3: the ropes, a tile's last panel.  Lane i has 16 bytes of rows 4 j + i / 8; a row with a scale byte
-// above 252 gets NaN.
+// Warps 8-15: four rows of a half tile each.  A lane has two pieces, a piece being 32 values (16 bytes of codes,
+// one scale): lane (panel % 4, row, half) = (l / 8, l / 2 % 4, l % 2) has that of panels panel % 4 and 4 + panel % 4;
+// eight lanes of a store have eight different bank groups.  And 16 bytes of a rope, lane (row, piece) = (l / 8, l % 8).
+// The loop is kept short: with a tile's loads in registers a tile ahead, its code took three times as long beside
+// the other warps' (it does not stay in the instruction cache).
 template <int N>
-__device__ void run_ropes(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts) {
-  const int lane = threadIdx.x & 31, ch = lane & 7;
-  const uint8_t* cache = reinterpret_cast<const uint8_t*>(p.t.cache);
-  int g = 0;
+__device__ void run_rows(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts, uint8_t* smem) {
+  constexpr int SLOTS = Off<N>::SLOTS;
+  const int lane = threadIdx.x & 31, w8 = (threadIdx.x >> 5) - 8, r4 = (lane >> 1) & 3, rr = lane >> 3;
+  const int group = 2 * (lane >> 3) + (lane & 1);   // of a panel group's eight
+  uint32_t at[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    at[i] = c.sbase + Off<N>::TILES + (lane >> 3) * PANEL + (4 * w8 + r4) * 128 + (((4 * (lane & 1) + i) ^ (4 * (w8 & 1) + r4)) << 4);
+  const uint32_t rope_at = c.sbase + Off<N>::TILES + 8 * PANEL + (4 * w8 + rr) * 128 + (((lane & 7) ^ (4 * (w8 & 1) + rr)) << 4);
+  const uint32_t from = c.sbase + Off<N>::RING + 4 * w8 * FP4_ENTRY;
+  const volatile uint32_t* there = reinterpret_cast<const volatile uint32_t*>(smem + Off<N>::THERE);
+  uint32_t got = 0;
   bool ok = true;
   Part u;
   while (ok && parts.next(&u)) {
-    int64_t key0 = (int64_t)u.lo * KEYS;
-    KeyBlocks blocks = find_blocks(p, u, key0, lane);
 #pragma unroll 1
-    for (int t = u.lo; t < u.hi; ++t, ++g, key0 += KEYS) {
-      const int b = g & 1;
-      const uint32_t dst = c.sbase + Off<N>::TILES + b * TILE + 8 * PANEL;
-      const KeyRows k = find_rows(p, blocks, key0, lane);
-      if (t + 1 < u.hi) blocks = find_blocks(p, u, key0 + KEYS, lane);
-      uint32_t bad[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint4 s = make_uint4(0, 0, 0, 0);
-        if (k.r[i] != p.oob_row) s = load16(cache + (int64_t)k.r[i] * FP4_ENTRY + FP4_SCALES);
-        bad[i] = __ballot_sync(0xffffffffu, (above252(s.x) | above252(s.y) | above252(s.z) | above252(s.w)) != 0);
-      }
-      if (g > 1 && !c.wait_warp(TE + b, ((g >> 1) - 1) & 1)) {
+    for (int n = 0; n < 2 * (u.hi - u.lo); ++n, ++got) {
+      const int h = n & 1, g = (int)(got >> 1), b = g & 1;
+      const uint32_t slot = got % SLOTS, e = from + slot * HALF;
+      if (!c.wait_warp(EF + slot, (got / SLOTS) & 1)) {
         ok = false;
         break;
       }
-#pragma unroll 4
-      for (int j = 0; j < 16; ++j) {
-        const int key = 4 * j + (lane >> 3);
-        const int32_t row = __shfl_sync(0xffffffffu, j < 8 ? k.r[0] : k.r[1], key & 31);
-        const bool there = row != p.oob_row;
-        const uint8_t* src = there ? cache + (int64_t)row * FP4_ENTRY + FP4_ROPE + ch * 16 : reinterpret_cast<const uint8_t*>(p.t.q);
-        cp_async16(dst + key * 128 + ((ch ^ (key & 7)) << 4), src, there ? 16 : 0);
-      }
-      cp_async_commit();
-      cp_async_wait<0>();
-      if (bad[0] | bad[1]) {
-        __syncwarp();   // (a row's pieces are other lanes' copies)
-        for (int j = 0; j < 16; ++j) {
-          const int key = 4 * j + (lane >> 3);
-          if ((bad[j >> 3] >> (key & 31)) & 1)
-            st_shared_v4(dst + key * 128 + ch * 16, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+      uint4 code[2] = {ld_shared_v4(e + r4 * FP4_ENTRY + 16 * group), ld_shared_v4(e + r4 * FP4_ENTRY + 128 + 16 * group)};
+      uint32_t scale[2] = {ld_shared_u8(e + r4 * FP4_ENTRY + FP4_SCALES + group), ld_shared_u8(e + r4 * FP4_ENTRY + FP4_SCALES + 8 + group)};
+      uint4 rope = ld_shared_v4(e + rr * FP4_ENTRY + FP4_ROPE + (lane & 7) * 16);
+      const uint32_t have = (there[slot] >> (4 * w8)) & 15u;
+      if (have != 15u) {   // rows that are not there are zeros
+        if (!(have >> r4 & 1)) {
+          code[0] = code[1] = make_uint4(0, 0, 0, 0);
+          scale[0] = scale[1] = 0;
         }
+        if (!(have >> rr & 1)) rope = make_uint4(0, 0, 0, 0);
       }
-      tell(c, CF + 2 * b + 1, lane);
+      const uint32_t most = max(scale[0], scale[1]);
+      // (a vote that needs every lane's loads: the slot may be copied into again)
+      const bool big = __any_sync(0xffffffffu, most > 128);
+      if (lane == 0) mbar_arrive(c.bar(EE + slot));
+      if (big) {   // a row with a scale byte above 252 is NaN: in its rope, while its values are zeros
+        const uint32_t nans = __ballot_sync(0xffffffffu, most > FP4_MAX_SCALE);
+        if (nans & (0x03030303u << (2 * rr))) rope = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+      }
+      if (h == 0 && g > 1 && !c.wait_warp(TE + b, ((g >> 1) - 1) & 1)) {
+        ok = false;
+        break;
+      }
+      const uint32_t to = b * TILE + h * (KEYS / 2) * 128;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        // One product by 2^126 times the scale, or, where a scale is above 2, two.
+        const uint32_t s = scale[k], words[4] = {code[k].x, code[k].y, code[k].z, code[k].w};
+        uint32_t m = big ? 0x7e80u : (s + 126) << 7;
+        if (big && s > FP4_MAX_SCALE) m = 0;
+        m |= m << 16;
+        uint32_t r[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          fp4_fields(words[i], r[i]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) r[i][q] = mul_bf16x2(r[i][q], m);
+        }
+        if (big) {
+          const uint32_t m2 = scale_bf16x2(s > FP4_MAX_SCALE ? 0 : s);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) r[i][q] = mul_bf16x2(r[i][q], m2);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st_shared_v4(at[i] + to + k * 4 * PANEL, r[i][0], r[i][1], r[i][2], r[i][3]);
+      }
+      st_shared_v4(rope_at + to, rope.x, rope.y, rope.z, rope.w);
+      if (h == 1) tell(c, CF + b, lane);
     }
   }
 }
 
+// Warp 3: Q of each part, and entries of tiles to come into L2, a lane an entry; for the latter it follows the copies'
+// count of tiles and gives up quietly.
 template <int N>
-__device__ void run_queries(const Ctx<N>& c, PartsN<N> parts, const CUtensorMap* tq) {
+__device__ void run_queries(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts, const CUtensorMap* tq, const volatile int* begun) {
   const int lane = threadIdx.x & 31;
-  int units = 0;
+  int units = 0, g = 0;
   bool ok = true;
   Part u;
   while (ok && parts.next(&u)) {
@@ -260,43 +269,33 @@ __device__ void run_queries(const Ctx<N>& c, PartsN<N> parts, const CUtensorMap*
       }
     }
     ok = __shfl_sync(0xffffffffu, ok, 0);
-    if (ok) ++units;
+    if (!ok) break;
+    ++units;
+    // (a part's first tiles, beyond those that are copied at once, together)
+    for (int t = u.lo + 2; t < u.hi; ++t) {
+      const uint64_t t0 = global_timer_ns();
+      while (*begun < g + t - u.lo - AHEAD && ok) {
+        __nanosleep(200);
+        if (*c.abort_flag || global_timer_ns() - t0 > p.wait_limit_ns) ok = false;
+      }
+      if (!__all_sync(0xffffffffu, ok)) break;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int64_t key = (int64_t)t * KEYS + 32 * i + lane;
+        if (key < u.q.kv) {
+          const int32_t row = block_row(p, table_block(p, u, key), key);
+          const uint8_t* e = reinterpret_cast<const uint8_t*>(p.t.cache) + (int64_t)row * FP4_ENTRY;
+          if (row != p.oob_row) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(e), "r"(FP4_ENTRY) : "memory");
+        }
+      }
+    }
+    ok = __all_sync(0xffffffffu, ok);
+    g += u.hi - u.lo;
   }
   if (lane == 0 && units) c.drain(QF, (units - 1) & 1);   // (the copy lands before the CTA exits)
 }
 
-// Warp 2: keys of the tiles to come into L2, a lane an entry; it follows the rows' count and gives up quietly.
-template <int N>
-__device__ void run_prefetch(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts, const volatile int* begun) {
-  const int lane = threadIdx.x & 31;
-  int g = 0;
-  Part u;
-  while (parts.next(&u)) {
-    for (int t = u.lo; t < u.hi; ++t, ++g) {
-      const uint64_t t0 = global_timer_ns();
-      while (*begun < g) {
-        __nanosleep(100);
-        if (*c.abort_flag || global_timer_ns() - t0 > p.wait_limit_ns) return;
-      }
-      __syncwarp();
-      // (a part's first tiles, beyond those that the rows' warps load themselves, all at once)
-      for (int a = t == u.lo ? 2 : AHEAD; a <= AHEAD; ++a) {
-        if (t + a >= u.hi) break;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int64_t key = (int64_t)(t + a) * KEYS + 32 * i + lane;
-          if (key < u.q.kv) {
-            const int32_t row = block_row(p, table_block(p, u, key), key);
-            const uint8_t* e = reinterpret_cast<const uint8_t*>(p.t.cache) + (int64_t)row * FP4_ENTRY;
-            if (row != p.oob_row) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(e), "r"(FP4_ENTRY) : "memory");
-          }
-        }
-      }
-    }
-  }
-}
-
-// ------------------------------------------------------------------ products (warp 1)
+// ------------------------------------------------------------------ products (warps 1 and 2)
 // (see tree_core.cuh: a converged warp, one elected lane, operands the same in all lanes)
 __device__ __forceinline__ void issue(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -317,70 +316,71 @@ __device__ __forceinline__ void commit(uint32_t bar) {
 }
 
 template <int N>
-__device__ void run_mma(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts, uint32_t tmem) {
-  constexpr uint32_t IDESC_S = idesc_bf16_f32(KEYS, N, false, false), IDESC_O = idesc_bf16_f32(128, N, true, false);
+__device__ void run_scores(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts, uint32_t tmem) {
+  constexpr uint32_t IDESC = idesc_bf16_f32(KEYS, N, false, false);
   const uint64_t k_desc = sdesc_sw128(c.sbase + Off<N>::TILES, 16, 1024);
-  const uint64_t v_desc = sdesc_sw128(c.sbase + Off<N>::TILES, PANEL, 1024);
   const uint64_t q_desc = sdesc_sw128(c.sbase + Off<N>::Q, 16, 1024);
-  const uint64_t p_desc = sdesc_sw128(c.sbase + Off<N>::P, 16, 1024);
   bool ok = true;
   if (p.force_timeout) ok = c.wait_warp(NEVER, 0);
-  int st = 0, pv = 0, units = 0;
-  auto s_products = [&](bool last) {
-    const int b = st & 1;
-    const uint32_t d = __shfl_sync(0xffffffffu, tmem + 4 * N + b * N, 0), phase = (st >> 1) & 1;
-    const uint32_t tile = __shfl_sync(0xffffffffu, (uint32_t)(b * TILE) >> 4, 0);
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      if (!c.wait_warp(CF + 2 * b + h, phase)) return false;
-      tc_fence_after();
-#pragma unroll 1
-      for (int i = 4 * h; i < (h ? 9 : 4); ++i) {
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          issue(d, k_desc + tile + ((uint32_t)(i * PANEL + kk * 32) >> 4), q_desc + ((uint32_t)(i * N * 128 + kk * 32) >> 4),
-                IDESC_S, kk > 0 ? 1u : i > 0 ? 1u : 0u);
-      }
-    }
-    commit(c.bar(SF + b));
-    if (last) commit(c.bar(QE));
-    ++st;
-    return true;
-  };
-  auto pv_products = [&](uint32_t add, int keys) {
-    const int b = pv & 1;
-    const uint32_t more = __shfl_sync(0xffffffffu, add, 0);
-    const uint32_t tile = __shfl_sync(0xffffffffu, (uint32_t)(b * TILE) >> 4, 0), pb = __shfl_sync(0xffffffffu, (uint32_t)(b * N * 128) >> 4, 0);
-    if (!c.wait_warp(PR + b, (pv >> 1) & 1)) return false;
-    tc_fence_after();
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        if (kk > 0 && 16 * kk >= keys) break;
-        issue(tmem + i * N, v_desc + tile + ((uint32_t)(2 * i * PANEL + kk * 2048) >> 4), p_desc + pb + ((uint32_t)(kk * 32) >> 4),
-              IDESC_O, kk > 0 ? 1u : more);
-      }
-    }
-    commit(c.bar(TE + b));
-    ++pv;
-    return true;
-  };
+  int g = 0, units = 0;
   Part u;
   while (ok && parts.next(&u)) {
     const int n = __shfl_sync(0xffffffffu, u.hi - u.lo, 0);
     ok = c.wait_warp(QF, units & 1);
     ++units;
-    for (int t = 0; t < n && ok; ++t) {
-      // S's buffer held P V(pv - 2)'s scores, read before that tile's P was ready.
-      ok = s_products(t == n - 1);
-      if (ok && t > 0) ok = pv_products(t > 1 ? 1u : 0u, KEYS);
+    for (int t = 0; t < n && ok; ++t, ++g) {
+      const int b = g & 1;
+      const uint32_t d = __shfl_sync(0xffffffffu, tmem + 4 * N + b * N, 0);
+      const uint32_t tile = __shfl_sync(0xffffffffu, (uint32_t)(b * TILE) >> 4, 0);
+      // S's buffer: the scores of the tile before last were read before its P was ready, and its tile, which this one
+      // replaced, was free after that.
+      if (!(ok = c.wait_warp(CF + b, (g >> 1) & 1))) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int i = 0; i < 9; ++i) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          issue(d, k_desc + tile + ((uint32_t)(i * PANEL + kk * 32) >> 4), q_desc + ((uint32_t)(i * N * 128 + kk * 32) >> 4),
+                IDESC, kk > 0 ? 1u : i > 0 ? 1u : 0u);
+      }
+      commit(c.bar(SF + b));
+      if (t == n - 1) commit(c.bar(QE));
     }
-    const int keys = __shfl_sync(0xffffffffu, (int)min((int64_t)KEYS, u.q.kv - (int64_t)(u.hi - 1) * KEYS), 0);
-    if (ok) ok = pv_products(n > 1 ? 1u : 0u, keys);
   }
   commit(c.bar(FIN));
   c.drain(FIN, 0);
+  __syncwarp();
+}
+
+template <int N>
+__device__ void run_values(const Ctx<N>& c, PartsN<N> parts, uint32_t tmem) {
+  constexpr uint32_t IDESC = idesc_bf16_f32(128, N, true, false);
+  const uint64_t v_desc = sdesc_sw128(c.sbase + Off<N>::TILES, PANEL, 1024);
+  const uint64_t p_desc = sdesc_sw128(c.sbase + Off<N>::P, 16, 1024);
+  bool ok = true;
+  int g = 0;
+  Part u;
+  while (ok && parts.next(&u)) {
+    const int n = __shfl_sync(0xffffffffu, u.hi - u.lo, 0);
+    for (int t = 0; t < n; ++t, ++g) {
+      const int b = g & 1;
+      const uint32_t more = __shfl_sync(0xffffffffu, t > 0 ? 1u : 0u, 0);
+      const uint32_t tile = __shfl_sync(0xffffffffu, (uint32_t)(b * TILE) >> 4, 0), pb = __shfl_sync(0xffffffffu, (uint32_t)(b * N * 128) >> 4, 0);
+      // (P was made of S, and S of the tile: it is there)
+      if (!(ok = c.wait_warp(PR + b, (g >> 1) & 1))) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          issue(tmem + i * N, v_desc + tile + ((uint32_t)(2 * i * PANEL + kk * 2048) >> 4), p_desc + pb + ((uint32_t)(kk * 32) >> 4),
+                IDESC, kk > 0 ? 1u : more);
+      }
+      commit(c.bar(TE + b));
+    }
+  }
+  commit(c.bar(FIN + 1));
+  c.drain(FIN + 1, 0);
   __syncwarp();
 }
 
@@ -579,15 +579,15 @@ tree_attn_fp4_few_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Off<N>::MISC);
   int* abort_flag = reinterpret_cast<int*>(smem + Off<N>::MISC + 4);
-  int* begun = reinterpret_cast<int*>(smem + Off<N>::MISC + 8);   // tiles that the rows' first warp has begun, less one
+  int* begun = reinterpret_cast<int*>(smem + Off<N>::MISC + 8);   // tiles whose copies have begun, less one
   const int worker = blockIdx.x;
   const Ctx<N> c{smem_addr(smem), abort_flag, p.t.status, p.wait_limit_ns};
   ReqWords words{0, 0, 0};   // (on their way while the barriers are made)
   if ((int)threadIdx.x < p.t.batch) words = load_words(p.t, threadIdx.x);
   if (warp == 1) {
-    // Codes: eight warps, ropes beside the second half; P and exchanges: four.
-    const bool half0 = lane == CF || lane == CF + 2, half1 = lane == CF + 1 || lane == CF + 3;
-    if (lane < NBAR) mbar_init(c.bar(lane), half0 ? 8 : half1 ? 9 : lane == PR || lane == PR + 1 || lane == XB ? 4 : 1);
+    // A tile, and entries read: eight warps; P and exchanges: four.
+    const bool eight = lane == CF || lane == CF + 1 || (lane >= EE && lane < EE + 4);
+    if (lane < NBAR) mbar_init(c.bar(lane), eight ? 8 : lane == PR || lane == PR + 1 || lane == XB ? 4 : 1);
     if (lane == 0) {
       *abort_flag = 0;
       *begun = -1;
@@ -610,16 +610,16 @@ tree_attn_fp4_few_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
   const PartsN<N> parts(p.t, start, count);
   if (warp < 4) {
     setmaxnreg_dec<REGS_CTRL>();
-    if (warp == 0) run_queries<N>(c, parts, &tm_q);
-    else if (warp == 1) run_mma<N>(c, p, parts, tmem);
-    else if (warp == 2) run_prefetch<N>(c, p, parts, begun);
-    else run_ropes<N>(c, p, parts);
+    if (warp == 0) run_copies<N>(c, p, parts, smem, begun);
+    else if (warp == 1) run_scores<N>(c, p, parts, tmem);
+    else if (warp == 2) run_values<N>(c, parts, tmem);
+    else run_queries<N>(c, p, parts, &tm_q, begun);
   } else if (warp < 8) {
     setmaxnreg_inc<REGS_SOFTMAX>();
     run_softmax<N>(c, p, parts, tmem, ws + WS_SLOTS + (size_t)worker * 2 * few_slot_bytes(N), smem);
   } else {
     setmaxnreg_dec<REGS_ROWS>();
-    run_rows<N>(c, p, parts, begun);
+    run_rows<N>(c, p, parts, smem);
   }
   __syncwarp();
   tc_fence_before();
