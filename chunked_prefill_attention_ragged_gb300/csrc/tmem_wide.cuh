@@ -4,6 +4,28 @@
 
 namespace mla {
 
+// tcgen05.ld 32x32b.x8 followed by wait::ld in one asm statement, so no use of the
+// destination registers can be scheduled before the data has landed.
+__device__ __forceinline__ void tmem_ld8_sync(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+
+// tcgen05.st 32x32b.x8 followed by wait::st in one asm statement, so the source
+// registers stay untouched until the store has been performed.
+__device__ __forceinline__ void tmem_st8_sync(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\t"
+      "tcgen05.wait::st.sync.aligned;"
+      :
+      : "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
 // tcgen05.ld 32x32b.x16 followed by wait::ld in one asm statement, so no use of the
 // destination registers can be scheduled before the data has landed.
 __device__ __forceinline__ void tmem_ld16_sync(uint32_t taddr, uint32_t* r) {

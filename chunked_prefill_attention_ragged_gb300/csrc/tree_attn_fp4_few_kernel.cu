@@ -13,7 +13,7 @@
 // Tiles are shared out among the SMs as in tree_attn_kernel.cu (equal pieces of the line of all tiles, parts
 // joined by a second kernel).  Two tile buffers: one is made while the other is multiplied.
 //   warp 0  copies entries into a ring in shared memory     1  issues S    2  issues P V    3  TMEM; Q; brings
-//   entries to come into L2    warps 4-7  softmax and output    8-15  entries to bf16
+//   entries to come into L2    warps 4-11  softmax and output    12-19  entries to bf16
 // S and P V have a warp each: from one warp, which has to take them in a fixed order, P V waited for the next
 // tile's keys or S for this tile's softmax (64 x 1 over 8192 at 16 heads: 184 us).
 // Where P V's accumulator lies: columns 128 i .. of the latent in TMEM columns N i .., lane = column.
@@ -28,10 +28,7 @@ namespace mla {
 namespace {
 
 constexpr int KEYS = 64;
-constexpr int NTHREADS = 512;
-constexpr int LAUNCH_REGS = 128;
-constexpr int REGS_CTRL = 96, REGS_SOFTMAX = 208, REGS_ROWS = 104;
-static_assert(REGS_CTRL + REGS_SOFTMAX + 2 * REGS_ROWS <= 4 * LAUNCH_REGS, "register split exceeds the launch allocation");
+constexpr int NTHREADS = 640;
 constexpr int PANEL = KEYS * 128;        // 64 keys x 64 columns
 constexpr int TILE = 9 * PANEL;
 constexpr int HALF = KEYS / 2 * FP4_ENTRY;   // half a tile's entries
@@ -42,8 +39,7 @@ template <int N>
 struct Off {
   static constexpr int SLOTS = N == 16 ? 4 : 2;   // of the ring, half a tile's entries each
   static constexpr int TILES = 0, Q = 2 * TILE, P = Q + 9 * N * 128, RING = P + 2 * N * 128;
-  static constexpr int FLAG = RING + SLOTS * HALF;
-  static constexpr int MAXIMA = FLAG + 2 * 4 * 4, SUMS = MAXIMA + 4 * N * 4, BAR = SUMS + 4 * N * 4;
+  static constexpr int MAXIMA = RING + SLOTS * HALF, SUMS = MAXIMA + 4 * N * 4, BAR = SUMS + 4 * N * 4;
   static constexpr int THERE = BAR + 24 * 8, MISC = THERE + SLOTS * 4, SMEM = MISC + 64 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
@@ -53,24 +49,14 @@ enum Bar {
   CF,           // [buffer] tile made
   TE = CF + 2,  // [buffer] P V done: the tile, P's buffer and, for the next rescale, O are free
   SF = TE + 2,  // [buffer] S done
-  PR = SF + 2,  // [buffer] P written (and the S buffer read) by the four softmax warps
-  XB = PR + 2,  // exchange among them
-  EF,           // [slot] entries landed
+  PR = SF + 2,  // [buffer] P written (and the S buffer read) by the softmax warps
+  EF = PR + 2,  // [slot] entries landed
   EE = EF + 4,  // [slot] entries read
   FIN = EE + 4, // [S, P V] every product drained
   NEVER = FIN + 2,   // nothing arrives here: the time-out test mode waits on it
   NBAR
 };
 static_assert(NBAR <= 24, "barriers");
-
-template <int R>
-__device__ __forceinline__ void setmaxnreg_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
-}
-template <int R>
-__device__ __forceinline__ void setmaxnreg_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
-}
 
 template <int N>
 struct Ctx {
@@ -169,7 +155,7 @@ __device__ void run_copies(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts
     for (uint32_t k = put > SLOTS ? put - SLOTS : 0; k < put; ++k) c.drain(EF + k % SLOTS, (k / SLOTS) & 1);
 }
 
-// Warps 8-15: four rows of a half tile each.  A lane has two pieces, a piece being 32 values (16 bytes of codes,
+// Warps 12-19: four rows of a half tile each.  A lane has two pieces, a piece being 32 values (16 bytes of codes,
 // one scale): lane (panel % 4, row, half) = (l / 8, l / 2 % 4, l % 2) has that of panels panel % 4 and 4 + panel % 4;
 // eight lanes of a store have eight different bank groups.  And 16 bytes of a rope, lane (row, piece) = (l / 8, l % 8).
 // The loop is kept short: with a tile's loads in registers a tile ahead, its code took three times as long beside
@@ -177,7 +163,7 @@ __device__ void run_copies(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts
 template <int N>
 __device__ void run_rows(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts, uint8_t* smem) {
   constexpr int SLOTS = Off<N>::SLOTS;
-  const int lane = threadIdx.x & 31, w8 = (threadIdx.x >> 5) - 8, r4 = (lane >> 1) & 3, rr = lane >> 3;
+  const int lane = threadIdx.x & 31, w8 = (threadIdx.x >> 5) - 12, r4 = (lane >> 1) & 3, rr = lane >> 3;
   const int group = 2 * (lane >> 3) + (lane & 1);   // of a panel group's eight
   uint32_t at[4];
 #pragma unroll
@@ -384,21 +370,16 @@ __device__ void run_values(const Ctx<N>& c, PartsN<N> parts, uint32_t tmem) {
   __syncwarp();
 }
 
-// ------------------------------------------------------------------ softmax (warps 4-7)
-template <int N>
-__device__ __forceinline__ void tmem_load(uint32_t at, float* x);
-template <>
-__device__ __forceinline__ void tmem_load<32>(uint32_t at, float* x) {
-  tmem_ld32_sync(at, reinterpret_cast<uint32_t*>(x));
+// ------------------------------------------------------------------ softmax (warps 4-11)
+template <int W>
+__device__ __forceinline__ void tmem_load(uint32_t at, float* x) {
+  if constexpr (W == 16) tmem_ld16_sync(at, reinterpret_cast<uint32_t*>(x));
+  else tmem_ld8_sync(at, reinterpret_cast<uint32_t*>(x));
 }
-template <>
-__device__ __forceinline__ void tmem_load<16>(uint32_t at, float* x) {
-  tmem_ld16_sync(at, reinterpret_cast<uint32_t*>(x));
-}
-template <int N>
+template <int W>
 __device__ __forceinline__ void tmem_store(uint32_t at, const float* x) {
-  if constexpr (N == 32) tmem_st32_sync(at, reinterpret_cast<const uint32_t*>(x));
-  else tmem_st16_sync(at, reinterpret_cast<const uint32_t*>(x));
+  if constexpr (W == 16) tmem_st16_sync(at, reinterpret_cast<const uint32_t*>(x));
+  else tmem_st8_sync(at, reinterpret_cast<const uint32_t*>(x));
 }
 __device__ __forceinline__ float warp_max(float x) {   // (passes over a NaN)
   float r;
@@ -414,50 +395,64 @@ __device__ __forceinline__ float capped(const TreeLaunch& p, float x) {
   return r;
 }
 
+// A barrier of one half of the softmax warps, and whether any of their threads says yes.
+__device__ __forceinline__ bool meet(int id, bool yes) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"((uint32_t)yes), "r"(id)
+      : "memory");
+  return r != 0;
+}
+
+// Half the pairs for each four warps.  These meet at barriers that have no time limit, so a warp whose wait gave up
+// goes through the rest of its tiles without waiting: nobody is left alone at one.
 template <int N>
 __device__ void run_softmax(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts, uint32_t tmem, char* ws_slots, uint8_t* smem) {
-  const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3;
+  constexpr int W = N / 2;   // pairs of a warp
+  const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3, side = (threadIdx.x >> 7) - 1, i0 = side * W;
+  const int barrier = 1 + side;
   // M = 64: rows 16 q4 .. of S^T lie in lanes 0-15 of this warp's quarter of TMEM.
   const bool mine = lane < 16;
   const int row = 16 * q4 + (lane & 15);
-  const uint32_t lane_addr = tmem + ((uint32_t)(q4 * 32) << 16);
-  volatile int* flags = reinterpret_cast<volatile int*>(smem + Off<N>::FLAG);
-  volatile float* maxima = reinterpret_cast<volatile float*>(smem + Off<N>::MAXIMA);
-  volatile float* sums = reinterpret_cast<volatile float*>(smem + Off<N>::SUMS);
-  const uint32_t p_at = c.sbase + Off<N>::P + (row & 7) * 2;
+  const uint32_t lane_addr = tmem + ((uint32_t)(q4 * 32) << 16) + i0;
+  volatile float* maxima = reinterpret_cast<volatile float*>(smem + Off<N>::MAXIMA) + i0;
+  volatile float* sums = reinterpret_cast<volatile float*>(smem + Off<N>::SUMS) + i0;
+  const uint32_t p_at = c.sbase + Off<N>::P + i0 * 128 + (row & 7) * 2;
   const float NEG_INF = -__int_as_float(0x7f800000);
   const float sc = p.has_cap ? 1.f : p.scale_log2;
   bool ok = true;
-  int g = 0, xs = 0;   // tiles and exchanges so far
-  auto meet = [&]() {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(c.bar(XB));
-    return c.wait_warp(XB, xs++ & 1);
-  };
+  int g = 0;   // tiles so far
+  auto wait = [&](int b, uint32_t parity) { ok = ok && c.wait_warp(b, parity); };
   Part u;
-  while (ok && parts.next(&u)) {
-    float m[N], l[N];   // m: the same in every thread
+  while (parts.next(&u)) {
+    float m[W], l[W];   // m: the same in every thread
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+    for (int i = 0; i < W; ++i) {
       m[i] = NEG_INF;
       l[i] = 0.f;
     }
-    const int64_t first = u.pair0 - (int64_t)u.q.q0 * p.t.num_heads;   // the unit's first pair in its request
+    const int64_t first = u.pair0 - (int64_t)u.q.q0 * p.t.num_heads + i0;   // this warp's first pair in its request
+#pragma unroll 1
     for (int t = u.lo; t < u.hi; ++t, ++g) {
       const int b = g & 1;
-      if (!c.wait_warp(SF + b, (g >> 1) & 1)) { ok = false; break; }
+      wait(SF + b, (g >> 1) & 1);
       tc_fence_after();
-      float s[N];
-      tmem_load<N>(lane_addr + 4 * N + b * N, s);
+      float s[W];
+      tmem_load<W>(lane_addr + 4 * N + b * N, s);
       if (p.has_cap) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) s[i] = capped(p, s[i]);
+        for (int i = 0; i < W; ++i) s[i] = capped(p, s[i]);
       }
       const int64_t pos = (int64_t)t * KEYS + row;
       if ((int64_t)t * KEYS + KEYS > min(u.q.ctx, (int64_t)u.q.kv)) {   // nodes, or the end of the keys
         const int64_t j = pos - u.q.ctx;   // node index of the key
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
+        for (int i = 0; i < W; ++i) {
           bool seen = pos < u.q.kv;
           if (seen && j >= 0) {
             // (a row without a pair computes on something harmless: the last node's mask)
@@ -468,31 +463,26 @@ __device__ void run_softmax(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> part
           if (!seen) s[i] = NEG_INF;
         }
       }
-      bool over = false;
+      bool over = t == u.lo;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
+      for (int i = 0; i < W; ++i) {
         s[i] = mine ? s[i] * sc : NEG_INF;
         over |= s[i] > m[i] + TREE_RESCALE_THRESHOLD;
       }
-      const bool begin = t == u.lo;
-      over = __any_sync(0xffffffffu, over);
-      if (lane == 0) flags[(xs & 1) * 4 + q4] = over;
-      const int x = xs & 1;
-      if (!meet()) { ok = false; break; }
-      if (begin || (flags[4 * x] | flags[4 * x + 1] | flags[4 * x + 2] | flags[4 * x + 3])) {
+      if (meet(barrier, over)) {
         // Maxima move: of every pair over the tile's keys.
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
+        for (int i = 0; i < W; ++i) {
           const float v = warp_max(s[i]);
           if (lane == 0) maxima[q4 * N + i] = v;
         }
-        if (!meet()) { ok = false; break; }
-        // O is rescaled behind the last product into it.
-        if (!begin && !c.wait_warp(TE + (b ^ 1), ((g - 1) >> 1) & 1)) { ok = false; break; }
+        meet(barrier, false);
+        const bool begin = t == u.lo;
+        if (!begin) wait(TE + (b ^ 1), ((g - 1) >> 1) & 1);   // O is rescaled behind the last product into it
         tc_fence_after();
-        float alpha[N];
+        float alpha[W];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
+        for (int i = 0; i < W; ++i) {
           const float top = fmaxf(fmaxf(maxima[i], maxima[N + i]), fmaxf(maxima[2 * N + i], maxima[3 * N + i]));
           const bool moves = begin || top > m[i] + TREE_RESCALE_THRESHOLD;
           alpha[i] = moves && !begin ? ex2_approx(m[i] - top) : 1.f;
@@ -502,18 +492,17 @@ __device__ void run_softmax(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> part
         if (!begin) {
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
-            float o[N];
-            tmem_load<N>(lane_addr + q * N, o);
+            float o[W];
+            tmem_load<W>(lane_addr + q * N, o);
 #pragma unroll
-            for (int i = 0; i < N; ++i) o[i] *= alpha[i];
-            tmem_store<N>(lane_addr + q * N, o);
+            for (int i = 0; i < W; ++i) o[i] *= alpha[i];
+            tmem_store<W>(lane_addr + q * N, o);
           }
         }
       }
-      // P's buffer was read by the tile before last's product.
-      if (g > 1 && !c.wait_warp(TE + b, ((g >> 1) - 1) & 1)) { ok = false; break; }
+      if (g > 1) wait(TE + b, ((g >> 1) - 1) & 1);   // P's buffer was read by the tile before last's product
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
+      for (int i = 0; i < W; ++i) {
         const float e = ex2_approx(s[i] - (m[i] == NEG_INF ? 0.f : m[i]));
         l[i] += e;   // (of the unrounded weights; 0 in the lanes without a key)
         if (mine) {
@@ -526,45 +515,46 @@ __device__ void run_softmax(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> part
       __syncwarp();
       if (lane == 0) mbar_arrive(c.bar(PR + b));
     }
-    if (!ok) break;
     // The part's end: the rows' sums, then O out of TMEM once the last product is done.
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+    for (int i = 0; i < W; ++i) {
 #pragma unroll
       for (int d = 8; d > 0; d >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
       if (lane == 0) sums[q4 * N + i] = l[i];
     }
-    if (!meet()) break;
-    if (!c.wait_warp(TE + ((g - 1) & 1), ((g - 1) >> 1) & 1)) break;
+    meet(barrier, false);
+    wait(TE + ((g - 1) & 1), ((g - 1) >> 1) & 1);
     tc_fence_after();
+    const int live = ok ? min(max(u.npairs - i0, 0), W) : 0;   // pairs to write
     char* slot = ws_slots + (size_t)u.slot * few_slot_bytes(N);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+    for (int i = 0; i < W; ++i) {
       l[i] = (sums[i] + sums[N + i]) + (sums[2 * N + i] + sums[3 * N + i]);
-      if (q4 == 0 && lane == i && i < u.npairs) {
+      if (q4 == 0 && lane == i && i < live) {
         if (u.whole) {
           const bool empty = l[i] == 0.f;   // (a NaN is passed on)
-          if (p.t.lse) p.t.lse[u.pair0 + i] = empty ? NEG_INF : (m[i] + log2f(l[i])) * 0.6931471805599453f;
+          if (p.t.lse) p.t.lse[u.pair0 + i0 + i] = empty ? NEG_INF : (m[i] + log2f(l[i])) * 0.6931471805599453f;
         } else {
-          reinterpret_cast<float2*>(slot + (size_t)N * 512 * 4)[i] = make_float2(m[i], l[i]);
+          reinterpret_cast<float2*>(slot + (size_t)N * 512 * 4)[i0 + i] = make_float2(m[i], l[i]);
         }
       }
       if (u.whole) l[i] = l[i] == 0.f ? 0.f : 1.f / l[i];
     }
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
-      float o[N];
-      tmem_load<N>(lane_addr + q * N, o);
+      float o[W];
+      tmem_load<W>(lane_addr + q * N, o);
       const int col = 128 * q + 32 * q4 + lane;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (i >= u.npairs) break;
-        if (u.whole) p.t.o[(u.pair0 + i) * 512 + col] = __float2bfloat16_rn(l[i] == 0.f ? 0.f : o[i] * l[i]);
-        else reinterpret_cast<float*>(slot)[i * 512 + col] = o[i];
+      for (int i = 0; i < W; ++i) {
+        if (i >= live) break;
+        if (u.whole) p.t.o[(u.pair0 + i0 + i) * 512 + col] = __float2bfloat16_rn(l[i] == 0.f ? 0.f : o[i] * l[i]);
+        else reinterpret_cast<float*>(slot)[(i0 + i) * 512 + col] = o[i];
       }
       __syncwarp();   // (the next load is one instruction of the whole warp)
     }
     tc_fence_before();   // O has been read: the next part's first P-ready lets it be overwritten
+    meet(barrier, false);   // (and the sums, before they are written again)
   }
 }
 
@@ -585,9 +575,9 @@ tree_attn_fp4_few_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
   ReqWords words{0, 0, 0};   // (on their way while the barriers are made)
   if ((int)threadIdx.x < p.t.batch) words = load_words(p.t, threadIdx.x);
   if (warp == 1) {
-    // A tile, and entries read: eight warps; P and exchanges: four.
-    const bool eight = lane == CF || lane == CF + 1 || (lane >= EE && lane < EE + 4);
-    if (lane < NBAR) mbar_init(c.bar(lane), eight ? 8 : lane == PR || lane == PR + 1 || lane == XB ? 4 : 1);
+    // A tile, entries read, P: eight warps.
+    const bool eight = lane == CF || lane == CF + 1 || lane == PR || lane == PR + 1 || (lane >= EE && lane < EE + 4);
+    if (lane < NBAR) mbar_init(c.bar(lane), eight ? 8 : 1);
     if (lane == 0) {
       *abort_flag = 0;
       *begun = -1;
@@ -609,16 +599,13 @@ tree_attn_fp4_few_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const PartsN<N> parts(p.t, start, count);
   if (warp < 4) {
-    setmaxnreg_dec<REGS_CTRL>();
     if (warp == 0) run_copies<N>(c, p, parts, smem, begun);
     else if (warp == 1) run_scores<N>(c, p, parts, tmem);
     else if (warp == 2) run_values<N>(c, parts, tmem);
     else run_queries<N>(c, p, parts, &tm_q, begun);
-  } else if (warp < 8) {
-    setmaxnreg_inc<REGS_SOFTMAX>();
+  } else if (warp < 12) {
     run_softmax<N>(c, p, parts, tmem, ws + WS_SLOTS + (size_t)worker * 2 * few_slot_bytes(N), smem);
   } else {
-    setmaxnreg_dec<REGS_ROWS>();
     run_rows<N>(c, p, parts, smem);
   }
   __syncwarp();
@@ -639,11 +626,6 @@ int max_workers() {
   const cudaError_t e = configured.run([] {
     cudaError_t r = cudaFuncSetAttribute(tree_attn_fp4_few_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Off<N>::SMEM);
     if (r != cudaSuccess) return r;
-    // The split of the registers takes for granted that every thread starts with LAUNCH_REGS.
-    cudaFuncAttributes attrs;
-    r = cudaFuncGetAttributes(&attrs, tree_attn_fp4_few_kernel<N>);
-    if (r != cudaSuccess) return r;
-    if (attrs.numRegs != LAUNCH_REGS) return cudaErrorInvalidConfiguration;
     int dev = 0;
     r = cudaGetDevice(&dev);
     if (r != cudaSuccess) return r;

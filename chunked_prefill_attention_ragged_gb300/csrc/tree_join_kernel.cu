@@ -63,39 +63,74 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) tree_join_kernel(const __grid
   if (col == 0 && p.t.lse) p.t.lse[pair] = empty ? NEG_INF : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-// Where units have few pairs (slots row by row): a CTA has a row of a cut unit, a thread four of its columns
-// and every fourth part; the parts' weights come first.  A request alone on the GPU leaves a part for every
-// SM: with all of them in one thread's loop the loads' latencies, eight at a time, took longer than all else.
+// Where units have few pairs (slots row by row): threads have four columns of a row of a cut unit.  Of few parts
+// (a boundary between two workers mostly cuts a unit in two or three) a CTA joins four rows; of many (a request
+// alone on the GPU leaves a part for every SM) its four groups of 128 threads take every fourth part of one row.
 constexpr int FEW_GROUPS = 4, FEW_THREADS = FEW_GROUPS * 128;
+constexpr int FEW_PARTS = 16;
 
 __global__ void __launch_bounds__(FEW_THREADS) tree_join_few_kernel(const __grid_constant__ TreeLaunch p, int rows) {
   __shared__ float weight[MAX_WORKERS];
   __shared__ float2 part[FEW_THREADS / 32];
   __shared__ float4 sum[FEW_GROUPS - 1][128];
   const char* ws = static_cast<const char*>(p.t.workspace);
-  const int b = blockIdx.x + 1, row = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+  const int b = blockIdx.x + 1, tid = threadIdx.x, lane = tid & 31, group = tid >> 7, col = 4 * (tid & 127);
   grid_dependency_wait();   // (the other kernel has ended, what it wrote is there)
   const JoinRec j = reinterpret_cast<const JoinRec*>(ws)[b];
-  if (row >= j.npairs || j.parts == 0) return;
   const int n = j.parts;
   const size_t bytes = few_slot_bytes(rows);
   const char* slots = ws + WS_SLOTS + (size_t)2 * (b - 1) * bytes;
   auto slot = [&](int k) { return slots + (size_t)(2 * k + (k == 0 ? j.slot0 : 0)) * bytes; };
+  auto state = [&](int k, int row) { return reinterpret_cast<const float2*>(slot(k) + (size_t)rows * 512 * 4)[row]; };
+  auto values = [&](int k, int row) { return *reinterpret_cast<const float4*>(slot(k) + ((size_t)row * 512 + col) * 4); };
   const float NEG_INF = -__int_as_float(0x7f800000);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float m = NEG_INF, l = 0.f;
+  auto add = [&](float f, const float4& x) {
+    o.x += f * x.x;
+    o.y += f * x.y;
+    o.z += f * x.z;
+    o.w += f * x.w;
+  };
+  auto write = [&](int row) {
+    const bool empty = l == 0.f;   // (a NaN is passed on)
+    const float inv = empty ? 0.f : 1.f / l;
+    const int64_t pair = j.pair0 + row;
+    *reinterpret_cast<uint2*>(p.t.o + pair * 512 + col) =
+        empty ? make_uint2(0u, 0u) : make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (col == 0 && p.t.lse) p.t.lse[pair] = empty ? NEG_INF : (m + log2f(l)) * 0.6931471805599453f;
+  };
+  if (n <= FEW_PARTS) {
+    const int row = FEW_GROUPS * blockIdx.y + group;
+    if (n == 0 || row >= j.npairs) return;
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) m = fmaxf(m, state(k, row).x);
+    const float mref = m == NEG_INF ? 0.f : m;
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const float2 ml = state(k, row);
+      const float f = ex2_approx(ml.x - mref);
+      l += f * ml.y;
+      add(f, values(k, row));
+    }
+    write(row);
+    return;
+  }
+  const int row = blockIdx.y;
+  if (row >= j.npairs) return;
   // The parts' maximum, and the sum of their weighted sums (n <= 256: a thread a part).
   float2 ml = make_float2(NEG_INF, 0.f);
-  if (tid < n) ml = reinterpret_cast<const float2*>(slot(tid) + (size_t)rows * 512 * 4)[row];
-  float m = ml.x;
+  if (tid < n) ml = state(tid, row);
+  m = ml.x;
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
   if (lane == 0) part[tid >> 5].x = m;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < FEW_THREADS / 32; ++w) m = fmaxf(m, part[w].x);
-  const float mref = m == NEG_INF ? 0.f : m;
-  const float w = tid < n ? ex2_approx(ml.x - mref) : 0.f;
+  const float w = tid < n ? ex2_approx(ml.x - (m == NEG_INF ? 0.f : m)) : 0.f;
   if (tid < n) weight[tid] = w;
-  float l = tid < n ? w * ml.y : 0.f;
+  l = tid < n ? w * ml.y : 0.f;
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
   if (lane == 0) part[tid >> 5].y = l;
@@ -103,34 +138,14 @@ __global__ void __launch_bounds__(FEW_THREADS) tree_join_few_kernel(const __grid
   l = 0.f;
 #pragma unroll
   for (int i = 0; i < FEW_THREADS / 32; ++i) l += part[i].y;
-  const int col = 4 * (tid & 127), group = tid >> 7;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-  for (int k = group; k < n; k += FEW_GROUPS) {
-    const float4 x = *reinterpret_cast<const float4*>(slot(k) + ((size_t)row * 512 + col) * 4);
-    const float f = weight[k];
-    o.x += f * x.x;
-    o.y += f * x.y;
-    o.z += f * x.z;
-    o.w += f * x.w;
-  }
+  for (int k = group; k < n; k += FEW_GROUPS) add(weight[k], values(k, row));
   if (group > 0) sum[group - 1][tid & 127] = o;
   __syncthreads();
   if (group > 0) return;
 #pragma unroll
-  for (int i = 0; i < FEW_GROUPS - 1; ++i) {
-    const float4 x = sum[i][tid];
-    o.x += x.x;
-    o.y += x.y;
-    o.z += x.z;
-    o.w += x.w;
-  }
-  const bool empty = l == 0.f;   // (a NaN is passed on)
-  const float inv = empty ? 0.f : 1.f / l;
-  const int64_t pair = j.pair0 + row;
-  *reinterpret_cast<uint2*>(p.t.o + pair * 512 + col) =
-      empty ? make_uint2(0u, 0u) : make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-  if (tid == 0 && p.t.lse) p.t.lse[pair] = empty ? NEG_INF : (m + log2f(l)) * 0.6931471805599453f;
+  for (int i = 0; i < FEW_GROUPS - 1; ++i) add(1.f, sum[i][tid]);
+  write(row);
 }
 
 }  // namespace
