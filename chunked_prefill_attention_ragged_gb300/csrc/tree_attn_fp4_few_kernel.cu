@@ -12,8 +12,8 @@
 //
 // Tiles are shared out among the SMs as in tree_attn_kernel.cu (equal pieces of the line of all tiles, parts
 // joined by a second kernel).  Two tile buffers: one is made while the other is multiplied.
-//   warp 0  copies entries into a ring in shared memory     1  issues S    2  issues P V    3  TMEM; Q; brings
-//   entries to come into L2    warps 4-11  softmax and output    12-19  entries to bf16
+//   warp 0  copies entries into a ring in shared memory     1  issues S    2  issues P V    3  TMEM; Q
+//   warps 4-11  softmax and output    12-19  entries to bf16
 // S and P V have a warp each: from one warp, which has to take them in a fixed order, P V waited for the next
 // tile's keys or S for this tile's softmax (64 x 1 over 8192 at 16 heads: 184 us).
 // Where P V's accumulator lies: columns 128 i .. of the latent in TMEM columns N i .., lane = column.
@@ -32,27 +32,26 @@ constexpr int NTHREADS = 640;
 constexpr int PANEL = KEYS * 128;        // 64 keys x 64 columns
 constexpr int TILE = 9 * PANEL;
 constexpr int HALF = KEYS / 2 * FP4_ENTRY;   // half a tile's entries
-constexpr int AHEAD = 4;                 // tiles between the one being made and the one brought into L2
 constexpr uint32_t TMEM_COLS = 256;
 
 template <int N>
 struct Off {
-  static constexpr int SLOTS = N == 16 ? 4 : 2;   // of the ring, half a tile's entries each
+  static constexpr int SLOTS = N == 16 ? 2 : 1;   // of the ring, a tile's entries each
   static constexpr int TILES = 0, Q = 2 * TILE, P = Q + 9 * N * 128, RING = P + 2 * N * 128;
-  static constexpr int MAXIMA = RING + SLOTS * HALF, SUMS = MAXIMA + 4 * N * 4, BAR = SUMS + 4 * N * 4;
-  static constexpr int THERE = BAR + 24 * 8, MISC = THERE + SLOTS * 4, SMEM = MISC + 64 + 1024;
+  static constexpr int MAXIMA = RING + SLOTS * KEYS * FP4_ENTRY, SUMS = MAXIMA + 4 * N * 4, BAR = SUMS + 4 * N * 4;
+  static constexpr int THERE = BAR + 24 * 8, MISC = THERE + SLOTS * 8, SMEM = MISC + 64 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
 enum Bar {
   QF = 0,       // Q landed
   QE,           // the part's last S done: Q may be replaced
-  CF,           // [buffer] tile made
-  TE = CF + 2,  // [buffer] P V done: the tile, P's buffer and, for the next rescale, O are free
+  CF,           // [buffer][half] panels 0-3, panels 4-8 made
+  TE = CF + 4,  // [buffer] P V done: the tile, P's buffer and, for the next rescale, O are free
   SF = TE + 2,  // [buffer] S done
   PR = SF + 2,  // [buffer] P written (and the S buffer read) by the softmax warps
   EF = PR + 2,  // [slot] entries landed
-  EE = EF + 4,  // [slot] entries read
-  FIN = EE + 4, // [S, P V] every product drained
+  EE = EF + 2,  // [slot] entries read
+  FIN = EE + 2, // [S, P V] every product drained
   NEVER = FIN + 2,   // nothing arrives here: the time-out test mode waits on it
   NBAR
 };
@@ -107,9 +106,10 @@ __device__ __forceinline__ uint32_t ld_shared_u8(uint32_t a) {
 }
 
 // Warp 0: half a tile's entries at a time, in runs of rows that lie side by side (`run`: as many of 32 as the
-// block size is a multiple of, 8 at least, or 1), a lane a row.
+// block size is a multiple of, 8 at least, or 1), a lane a row.  Where the ring holds one tile only, the next one's
+// entries are brought into L2 meanwhile.
 template <int N>
-__device__ void run_copies(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts, uint8_t* smem, volatile int* begun) {
+__device__ void run_copies(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts, uint8_t* smem) {
   constexpr int SLOTS = Off<N>::SLOTS;
   const int lane = threadIdx.x & 31, bs = p.t.block_size;
   const int run = bs % 32 == 0 ? 32 : bs % 16 == 0 ? 16 : bs % 8 == 0 ? 8 : 1;
@@ -120,26 +120,33 @@ __device__ void run_copies(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts
   Part u;
   while (ok && parts.next(&u)) {
     const int64_t end = min((int64_t)u.hi * KEYS, (int64_t)u.q.kv);
-    // A block as the table has it: looked at two steps later, so that nothing waits for it here.
+    // A block as the table has it: looked at two steps later at the least, so that nothing waits for it here.
     auto find = [&](int64_t k) {
       return k < end ? __ldg(p.t.block_table + (int64_t)u.r * p.t.max_blocks + block_of(p, (int)k)) : 0;
     };
     int64_t key = (int64_t)u.lo * KEYS + lane;
-    int32_t blk0 = find(key), blk1 = find(key + 32);
+    auto row_of = [&](int32_t blk, int64_t k) { return k < end ? block_row(p, blk == PAST_END ? -1 : blk, k) : p.oob_row; };
+    int32_t blk0 = find(key), blk1 = find(key + 32), blk2 = find(key + 64), blk3 = find(key + 96);
 #pragma unroll 1
     for (int n = 0; n < 2 * (u.hi - u.lo); ++n, key += 32, ++put) {
-      const int32_t row = key < end ? block_row(p, blk0 == PAST_END ? -1 : blk0, key) : p.oob_row;
+      const int32_t row = row_of(blk0, key);
       blk0 = blk1;
-      blk1 = find(key + 64);
+      blk1 = blk2;
+      blk2 = blk3;
+      blk3 = find(key + 128);
+      if (SLOTS == 1) {
+        const int32_t later = row_of(blk1, key + 64);
+        if (later != p.oob_row)
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(cache + (int64_t)later * FP4_ENTRY), "r"(FP4_ENTRY) : "memory");
+      }
       const uint32_t have = __ballot_sync(0xffffffffu, row != p.oob_row);
-      const uint32_t slot = put % SLOTS, dst = c.sbase + Off<N>::RING + slot * HALF;
-      if (put >= SLOTS && !c.wait_warp(EE + slot, (put / SLOTS - 1) & 1)) {
+      const uint32_t g = put >> 1, slot = g % SLOTS, half = 2 * slot + (put & 1), dst = c.sbase + Off<N>::RING + half * HALF;
+      if ((put & 1) == 0 && g >= SLOTS && !c.wait_warp(EE + slot, (g / SLOTS - 1) & 1)) {
         ok = false;
         break;
       }
       if (lane == 0) {
-        *begun = put >> 1;
-        there[slot] = have;
+        there[half] = have;
         if (have) mbar_arrive_expect_tx(c.bar(EF + slot), __popc(have) * FP4_ENTRY);
         else mbar_arrive(c.bar(EF + slot));
       }
@@ -151,67 +158,68 @@ __device__ void run_copies(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts
     }
   }
   // Let every copy started here land before the CTA can exit.
+  // (A wait gives up between tiles only, with both halves of those before copied.)
   if (lane == 0)
-    for (uint32_t k = put > SLOTS ? put - SLOTS : 0; k < put; ++k) c.drain(EF + k % SLOTS, (k / SLOTS) & 1);
+    for (uint32_t n = put >> 1, g = n > SLOTS ? n - SLOTS : 0; g < n; ++g) c.drain(EF + g % SLOTS, (g / SLOTS) & 1);
 }
 
-// Warps 12-19: four rows of a half tile each.  A lane has two pieces, a piece being 32 values (16 bytes of codes,
-// one scale): lane (panel % 4, row, half) = (l / 8, l / 2 % 4, l % 2) has that of panels panel % 4 and 4 + panel % 4;
-// eight lanes of a store have eight different bank groups.  And 16 bytes of a rope, lane (row, piece) = (l / 8, l % 8).
+// Warps 12-19: eight rows of a tile each, first panels 0-3, then 4-8, so that S begins with the first half.  A lane
+// has two pieces of a half, a piece being 32 values (16 bytes of codes, one scale): lane (panel % 4, row % 4, half
+// panel) = (l / 8, l / 2 % 4, l % 2), rows row % 4 and 4 + row % 4; eight lanes of a store have eight different
+// bank groups.  And 16 bytes of two ropes, lane (row % 4, piece) = (l / 8, l % 8).
 // The loop is kept short: with a tile's loads in registers a tile ahead, its code took three times as long beside
 // the other warps' (it does not stay in the instruction cache).
 template <int N>
 __device__ void run_rows(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts, uint8_t* smem) {
   constexpr int SLOTS = Off<N>::SLOTS;
   const int lane = threadIdx.x & 31, w8 = (threadIdx.x >> 5) - 12, r4 = (lane >> 1) & 3, rr = lane >> 3;
-  const int group = 2 * (lane >> 3) + (lane & 1);   // of a panel group's eight
+  const int group = 2 * (lane >> 3) + (lane & 1);   // of a half's eight
   uint32_t at[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    at[i] = c.sbase + Off<N>::TILES + (lane >> 3) * PANEL + (4 * w8 + r4) * 128 + (((4 * (lane & 1) + i) ^ (4 * (w8 & 1) + r4)) << 4);
-  const uint32_t rope_at = c.sbase + Off<N>::TILES + 8 * PANEL + (4 * w8 + rr) * 128 + (((lane & 7) ^ (4 * (w8 & 1) + rr)) << 4);
-  const uint32_t from = c.sbase + Off<N>::RING + 4 * w8 * FP4_ENTRY;
-  const volatile uint32_t* there = reinterpret_cast<const volatile uint32_t*>(smem + Off<N>::THERE);
-  uint32_t got = 0;
+    at[i] = c.sbase + Off<N>::TILES + (lane >> 3) * PANEL + (8 * w8 + r4) * 128 + (((4 * (lane & 1) + i) ^ r4) << 4);
+  const uint32_t rope_at = c.sbase + Off<N>::TILES + 8 * PANEL + (8 * w8 + rr) * 128 + (((lane & 7) ^ rr) << 4);
+  const uint32_t from = c.sbase + Off<N>::RING + (8 * w8 + r4) * FP4_ENTRY;
+  const uint32_t rope_from = c.sbase + Off<N>::RING + (8 * w8 + rr) * FP4_ENTRY + FP4_ROPE + (lane & 7) * 16;
+  const volatile uint8_t* there = smem + Off<N>::THERE + w8;   // which of the warp's rows exist
+  int g = 0;
+  uint32_t nans[2] = {0, 0};
   bool ok = true;
   Part u;
   while (ok && parts.next(&u)) {
 #pragma unroll 1
-    for (int n = 0; n < 2 * (u.hi - u.lo); ++n, ++got) {
-      const int h = n & 1, g = (int)(got >> 1), b = g & 1;
-      const uint32_t slot = got % SLOTS, e = from + slot * HALF;
-      if (!c.wait_warp(EF + slot, (got / SLOTS) & 1)) {
-        ok = false;
-        break;
-      }
-      uint4 code[2] = {ld_shared_v4(e + r4 * FP4_ENTRY + 16 * group), ld_shared_v4(e + r4 * FP4_ENTRY + 128 + 16 * group)};
-      uint32_t scale[2] = {ld_shared_u8(e + r4 * FP4_ENTRY + FP4_SCALES + group), ld_shared_u8(e + r4 * FP4_ENTRY + FP4_SCALES + 8 + group)};
-      uint4 rope = ld_shared_v4(e + rr * FP4_ENTRY + FP4_ROPE + (lane & 7) * 16);
-      const uint32_t have = (there[slot] >> (4 * w8)) & 15u;
-      if (have != 15u) {   // rows that are not there are zeros
-        if (!(have >> r4 & 1)) {
-          code[0] = code[1] = make_uint4(0, 0, 0, 0);
-          scale[0] = scale[1] = 0;
+    for (int n = 0; n < 2 * (u.hi - u.lo); ++n) {
+      const int k = n & 1, b = g & 1;
+      const uint32_t slot = (uint32_t)g % SLOTS, e = from + slot * 2 * HALF;
+      if (k == 0) {
+        if (!c.wait_warp(EF + slot, ((uint32_t)g / SLOTS) & 1) || (g > 1 && !c.wait_warp(TE + b, ((g >> 1) - 1) & 1))) {
+          ok = false;
+          break;
         }
-        if (!(have >> rr & 1)) rope = make_uint4(0, 0, 0, 0);
       }
-      const uint32_t most = max(scale[0], scale[1]);
-      // (a vote that needs every lane's loads: the slot may be copied into again)
-      const bool big = __any_sync(0xffffffffu, most > 128);
-      if (lane == 0) mbar_arrive(c.bar(EE + slot));
-      if (big) {   // a row with a scale byte above 252 is NaN: in its rope, while its values are zeros
-        const uint32_t nans = __ballot_sync(0xffffffffu, most > FP4_MAX_SCALE);
-        if (nans & (0x03030303u << (2 * rr))) rope = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
-      }
-      if (h == 0 && g > 1 && !c.wait_warp(TE + b, ((g >> 1) - 1) & 1)) {
-        ok = false;
-        break;
-      }
-      const uint32_t to = b * TILE + h * (KEYS / 2) * 128;
+      uint4 code[2] = {ld_shared_v4(e + 128 * k + 16 * group), ld_shared_v4(e + 4 * FP4_ENTRY + 128 * k + 16 * group)};
+      uint32_t scale[2] = {ld_shared_u8(e + FP4_SCALES + 8 * k + group), ld_shared_u8(e + 4 * FP4_ENTRY + FP4_SCALES + 8 * k + group)};
+      const uint32_t have = there[8 * slot];
+      if (have != 255u) {   // rows that are not there are zeros
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+        for (int h = 0; h < 2; ++h)
+          if (!(have >> (4 * h + r4) & 1)) {
+            code[h] = make_uint4(0, 0, 0, 0);
+            scale[h] = 0;
+          }
+      }
+      const bool big = __any_sync(0xffffffffu, max(scale[0], scale[1]) > 128);
+      // A row with a scale byte above 252 is NaN: in its rope, while its values are zeros.
+      if (k == 0) nans[0] = nans[1] = 0;
+      if (big) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) nans[h] |= __ballot_sync(0xffffffffu, scale[h] > FP4_MAX_SCALE);
+      }
+      const uint32_t to = b * TILE + k * 4 * PANEL;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
         // One product by 2^126 times the scale, or, where a scale is above 2, two.
-        const uint32_t s = scale[k], words[4] = {code[k].x, code[k].y, code[k].z, code[k].w};
+        const uint32_t s = scale[h], words[4] = {code[h].x, code[h].y, code[h].z, code[h].w};
         uint32_t m = big ? 0x7e80u : (s + 126) << 7;
         if (big && s > FP4_MAX_SCALE) m = 0;
         m |= m << 16;
@@ -230,20 +238,31 @@ __device__ void run_rows(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts, 
             for (int q = 0; q < 4; ++q) r[i][q] = mul_bf16x2(r[i][q], m2);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) st_shared_v4(at[i] + to + k * 4 * PANEL, r[i][0], r[i][1], r[i][2], r[i][3]);
+        for (int i = 0; i < 4; ++i) st_shared_v4((at[i] ^ (h << 6)) + to + h * 512, r[i][0], r[i][1], r[i][2], r[i][3]);
       }
-      st_shared_v4(rope_at + to, rope.x, rope.y, rope.z, rope.w);
-      if (h == 1) tell(c, CF + b, lane);
+      if (k == 1) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint4 rope = ld_shared_v4(rope_from + slot * 2 * HALF + h * 4 * FP4_ENTRY);
+          if (!(have >> (4 * h + rr) & 1)) rope = make_uint4(0, 0, 0, 0);
+          if (nans[h] & (0x03030303u << (2 * rr))) rope = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+          st_shared_v4((rope_at ^ (h << 6)) + b * TILE + h * 512, rope.x, rope.y, rope.z, rope.w);
+        }
+      }
+      tell(c, CF + 2 * b + k, lane);
+      if (k == 1) {
+        if (lane == 0) mbar_arrive(c.bar(EE + slot));   // (every lane's loads were waited for before its stores)
+        ++g;
+      }
     }
   }
 }
 
-// Warp 3: Q of each part, and entries of tiles to come into L2, a lane an entry; for the latter it follows the copies'
-// count of tiles and gives up quietly.
+// Warp 3: Q of each part.
 template <int N>
-__device__ void run_queries(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts, const CUtensorMap* tq, const volatile int* begun) {
+__device__ void run_queries(const Ctx<N>& c, PartsN<N> parts, const CUtensorMap* tq) {
   const int lane = threadIdx.x & 31;
-  int units = 0, g = 0;
+  int units = 0;
   bool ok = true;
   Part u;
   while (ok && parts.next(&u)) {
@@ -255,28 +274,7 @@ __device__ void run_queries(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> part
       }
     }
     ok = __shfl_sync(0xffffffffu, ok, 0);
-    if (!ok) break;
-    ++units;
-    // (a part's first tiles, beyond those that are copied at once, together)
-    for (int t = u.lo + 2; t < u.hi; ++t) {
-      const uint64_t t0 = global_timer_ns();
-      while (*begun < g + t - u.lo - AHEAD && ok) {
-        __nanosleep(200);
-        if (*c.abort_flag || global_timer_ns() - t0 > p.wait_limit_ns) ok = false;
-      }
-      if (!__all_sync(0xffffffffu, ok)) break;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int64_t key = (int64_t)t * KEYS + 32 * i + lane;
-        if (key < u.q.kv) {
-          const int32_t row = block_row(p, table_block(p, u, key), key);
-          const uint8_t* e = reinterpret_cast<const uint8_t*>(p.t.cache) + (int64_t)row * FP4_ENTRY;
-          if (row != p.oob_row) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(e), "r"(FP4_ENTRY) : "memory");
-        }
-      }
-    }
-    ok = __all_sync(0xffffffffu, ok);
-    g += u.hi - u.lo;
+    if (ok) ++units;
   }
   if (lane == 0 && units) c.drain(QF, (units - 1) & 1);   // (the copy lands before the CTA exits)
 }
@@ -320,15 +318,18 @@ __device__ void run_scores(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts
       const uint32_t tile = __shfl_sync(0xffffffffu, (uint32_t)(b * TILE) >> 4, 0);
       // S's buffer: the scores of the tile before last were read before its P was ready, and its tile, which this one
       // replaced, was free after that.
-      if (!(ok = c.wait_warp(CF + b, (g >> 1) & 1))) break;
-      tc_fence_after();
 #pragma unroll 1
       for (int i = 0; i < 9; ++i) {
+        if ((i & 3) == 0 && i < 8) {
+          if (!(ok = c.wait_warp(CF + 2 * b + (i >> 2), (g >> 1) & 1))) break;
+          tc_fence_after();
+        }
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           issue(d, k_desc + tile + ((uint32_t)(i * PANEL + kk * 32) >> 4), q_desc + ((uint32_t)(i * N * 128 + kk * 32) >> 4),
                 IDESC, kk > 0 ? 1u : i > 0 ? 1u : 0u);
       }
+      if (!ok) break;
       commit(c.bar(SF + b));
       if (t == n - 1) commit(c.bar(QE));
     }
@@ -569,19 +570,15 @@ tree_attn_fp4_few_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Off<N>::MISC);
   int* abort_flag = reinterpret_cast<int*>(smem + Off<N>::MISC + 4);
-  int* begun = reinterpret_cast<int*>(smem + Off<N>::MISC + 8);   // tiles whose copies have begun, less one
   const int worker = blockIdx.x;
   const Ctx<N> c{smem_addr(smem), abort_flag, p.t.status, p.wait_limit_ns};
   ReqWords words{0, 0, 0};   // (on their way while the barriers are made)
   if ((int)threadIdx.x < p.t.batch) words = load_words(p.t, threadIdx.x);
   if (warp == 1) {
-    // A tile, entries read, P: eight warps.
-    const bool eight = lane == CF || lane == CF + 1 || lane == PR || lane == PR + 1 || (lane >= EE && lane < EE + 4);
-    if (lane < NBAR) mbar_init(c.bar(lane), eight ? 8 : 1);
-    if (lane == 0) {
-      *abort_flag = 0;
-      *begun = -1;
-    }
+    // A half tile, entries read, P: eight warps; entries: both halves.
+    const bool eight = (lane >= CF && lane < CF + 4) || lane == PR || lane == PR + 1 || lane == EE || lane == EE + 1;
+    if (lane < NBAR) mbar_init(c.bar(lane), eight ? 8 : lane == EF || lane == EF + 1 ? 2 : 1);
+    if (lane == 0) *abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) tma_prefetch_desc(&tm_q);
@@ -599,10 +596,10 @@ tree_attn_fp4_few_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const PartsN<N> parts(p.t, start, count);
   if (warp < 4) {
-    if (warp == 0) run_copies<N>(c, p, parts, smem, begun);
+    if (warp == 0) run_copies<N>(c, p, parts, smem);
     else if (warp == 1) run_scores<N>(c, p, parts, tmem);
     else if (warp == 2) run_values<N>(c, parts, tmem);
-    else run_queries<N>(c, p, parts, &tm_q, begun);
+    else run_queries<N>(c, parts, &tm_q);
   } else if (warp < 12) {
     run_softmax<N>(c, p, parts, tmem, ws + WS_SLOTS + (size_t)worker * 2 * few_slot_bytes(N), smem);
   } else {
