@@ -81,6 +81,22 @@ using PartsN = PartsOf<N, KEYS>;
 __device__ __forceinline__ void st_shared_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
+// A barrier of `THREADS` threads, and whether any of them says yes.  Warps that wait for the same thing leave the
+// looking to one of them and meet it here: sixteen warps that look all the time take a third of the issue slots.
+template <int THREADS>
+__device__ __forceinline__ bool meet(int id, bool yes) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"((uint32_t)yes), "r"(id), "n"(THREADS)
+      : "memory");
+  return r != 0;
+}
+
 // A warp's part of what it writes is there: handed to the products' proxy.
 template <int N>
 __device__ __forceinline__ void tell(const Ctx<N>& c, int b, int lane) {
@@ -192,7 +208,8 @@ __device__ void run_rows(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts, 
       const int k = n & 1, b = g & 1;
       const uint32_t slot = (uint32_t)g % SLOTS, e = from + slot * 2 * HALF;
       if (k == 0) {
-        if (!c.wait_warp(EF + slot, ((uint32_t)g / SLOTS) & 1) || (g > 1 && !c.wait_warp(TE + b, ((g >> 1) - 1) & 1))) {
+        if (w8 == 0) ok = c.wait_warp(EF + slot, ((uint32_t)g / SLOTS) & 1) && (g < 2 || c.wait_warp(TE + b, ((g >> 1) - 1) & 1));
+        if (meet<256>(3, !ok)) {
           ok = false;
           break;
         }
@@ -396,22 +413,8 @@ __device__ __forceinline__ float capped(const TreeLaunch& p, float x) {
   return r;
 }
 
-// A barrier of one half of the softmax warps, and whether any of their threads says yes.
-__device__ __forceinline__ bool meet(int id, bool yes) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}\n"
-      : "=r"(r)
-      : "r"((uint32_t)yes), "r"(id)
-      : "memory");
-  return r != 0;
-}
-
-// Half the pairs for each four warps.  These meet at barriers that have no time limit, so a warp whose wait gave up
-// goes through the rest of its tiles without waiting: nobody is left alone at one.
+// Half the pairs for each four warps.  These meet at barriers, which have no time limit, so where a wait gave up
+// they go through the rest of their tiles without waiting: nobody is left alone at one.
 template <int N>
 __device__ void run_softmax(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts, uint32_t tmem, char* ws_slots, uint8_t* smem) {
   constexpr int W = N / 2;   // pairs of a warp
@@ -441,7 +444,8 @@ __device__ void run_softmax(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> part
 #pragma unroll 1
     for (int t = u.lo; t < u.hi; ++t, ++g) {
       const int b = g & 1;
-      wait(SF + b, (g >> 1) & 1);
+      if (q4 == 0) wait(SF + b, (g >> 1) & 1);
+      if (meet<128>(barrier, !ok)) ok = false;
       tc_fence_after();
       float s[W];
       tmem_load<W>(lane_addr + 4 * N + b * N, s);
@@ -470,14 +474,14 @@ __device__ void run_softmax(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> part
         s[i] = mine ? s[i] * sc : NEG_INF;
         over |= s[i] > m[i] + TREE_RESCALE_THRESHOLD;
       }
-      if (meet(barrier, over)) {
+      if (meet<128>(barrier, over)) {
         // Maxima move: of every pair over the tile's keys.
 #pragma unroll
         for (int i = 0; i < W; ++i) {
           const float v = warp_max(s[i]);
           if (lane == 0) maxima[q4 * N + i] = v;
         }
-        meet(barrier, false);
+        meet<128>(barrier, false);
         const bool begin = t == u.lo;
         if (!begin) wait(TE + (b ^ 1), ((g - 1) >> 1) & 1);   // O is rescaled behind the last product into it
         tc_fence_after();
@@ -501,7 +505,7 @@ __device__ void run_softmax(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> part
           }
         }
       }
-      if (g > 1) wait(TE + b, ((g >> 1) - 1) & 1);   // P's buffer was read by the tile before last's product
+      // (P's buffer was read by the tile before last's product: this tile's rows waited for that.)
 #pragma unroll
       for (int i = 0; i < W; ++i) {
         const float e = ex2_approx(s[i] - (m[i] == NEG_INF ? 0.f : m[i]));
@@ -523,7 +527,7 @@ __device__ void run_softmax(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> part
       for (int d = 8; d > 0; d >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
       if (lane == 0) sums[q4 * N + i] = l[i];
     }
-    meet(barrier, false);
+    meet<128>(barrier, false);
     wait(TE + ((g - 1) & 1), ((g - 1) >> 1) & 1);
     tc_fence_after();
     const int live = ok ? min(max(u.npairs - i0, 0), W) : 0;   // pairs to write
@@ -555,7 +559,7 @@ __device__ void run_softmax(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> part
       __syncwarp();   // (the next load is one instruction of the whole warp)
     }
     tc_fence_before();   // O has been read: the next part's first P-ready lets it be overwritten
-    meet(barrier, false);   // (and the sums, before they are written again)
+    meet<128>(barrier, false);   // (and the sums, before they are written again)
   }
 }
 
