@@ -199,77 +199,85 @@ __device__ void run_rows(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts, 
   const uint32_t rope_from = c.sbase + Off<N>::RING + (8 * w8 + rr) * FP4_ENTRY + FP4_ROPE + (lane & 7) * 16;
   const volatile uint8_t* there = smem + Off<N>::THERE + w8;   // which of the warp's rows exist
   int g = 0;
-  uint32_t nans[2] = {0, 0};
   bool ok = true;
   Part u;
   while (ok && parts.next(&u)) {
 #pragma unroll 1
-    for (int n = 0; n < 2 * (u.hi - u.lo); ++n) {
-      const int k = n & 1, b = g & 1;
+    for (int t = u.lo; t < u.hi; ++t, ++g) {
+      const int b = g & 1;
       const uint32_t slot = (uint32_t)g % SLOTS, e = from + slot * 2 * HALF;
-      if (k == 0) {
-        if (w8 == 0) ok = c.wait_warp(EF + slot, ((uint32_t)g / SLOTS) & 1) && (g < 2 || c.wait_warp(TE + b, ((g >> 1) - 1) & 1));
-        if (meet<256>(3, !ok)) {
-          ok = false;
-          break;
-        }
+      if (w8 == 0) ok = c.wait_warp(EF + slot, ((uint32_t)g / SLOTS) & 1) && (g < 2 || c.wait_warp(TE + b, ((g >> 1) - 1) & 1));
+      if (meet<256>(3, !ok)) {
+        ok = false;
+        break;
       }
-      uint4 code[2] = {ld_shared_v4(e + 128 * k + 16 * group), ld_shared_v4(e + 4 * FP4_ENTRY + 128 * k + 16 * group)};
-      uint32_t scale[2] = {ld_shared_u8(e + FP4_SCALES + 8 * k + group), ld_shared_u8(e + 4 * FP4_ENTRY + FP4_SCALES + 8 * k + group)};
+      // All of the tile's loads at once: their latency, under the other warps' stores, is a third of a half's time.
+      uint4 code[2][2], rope[2];   // [half][row]
+      uint32_t scale[2][2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          code[k][h] = ld_shared_v4(e + h * 4 * FP4_ENTRY + 128 * k + 16 * group);
+          scale[k][h] = ld_shared_u8(e + h * 4 * FP4_ENTRY + FP4_SCALES + 8 * k + group);
+        }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) rope[h] = ld_shared_v4(rope_from + slot * 2 * HALF + h * 4 * FP4_ENTRY);
       const uint32_t have = there[8 * slot];
       if (have != 255u) {   // rows that are not there are zeros
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h) {
           if (!(have >> (4 * h + r4) & 1)) {
-            code[h] = make_uint4(0, 0, 0, 0);
-            scale[h] = 0;
+            code[0][h] = code[1][h] = make_uint4(0, 0, 0, 0);
+            scale[0][h] = scale[1][h] = 0;
           }
-      }
-      const bool big = __any_sync(0xffffffffu, max(scale[0], scale[1]) > 128);
-      // A row with a scale byte above 252 is NaN: in its rope, while its values are zeros.
-      if (k == 0) nans[0] = nans[1] = 0;
-      if (big) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) nans[h] |= __ballot_sync(0xffffffffu, scale[h] > FP4_MAX_SCALE);
-      }
-      const uint32_t to = b * TILE + k * 4 * PANEL;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        // One product by 2^126 times the scale, or, where a scale is above 2, two.
-        const uint32_t s = scale[h], words[4] = {code[h].x, code[h].y, code[h].z, code[h].w};
-        uint32_t m = big ? 0x7e80u : (s + 126) << 7;
-        if (big && s > FP4_MAX_SCALE) m = 0;
-        m |= m << 16;
-        uint32_t r[4][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          fp4_fields(words[i], r[i]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) r[i][q] = mul_bf16x2(r[i][q], m);
+          if (!(have >> (4 * h + rr) & 1)) rope[h] = make_uint4(0, 0, 0, 0);
         }
-        if (big) {
-          const uint32_t m2 = scale_bf16x2(s > FP4_MAX_SCALE ? 0 : s);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) r[i][q] = mul_bf16x2(r[i][q], m2);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) st_shared_v4((at[i] ^ (h << 6)) + to + h * 512, r[i][0], r[i][1], r[i][2], r[i][3]);
       }
-      if (k == 1) {
+      const uint32_t most[2] = {max(scale[0][0], scale[1][0]), max(scale[0][1], scale[1][1])};
+      const bool big = __any_sync(0xffffffffu, max(most[0], most[1]) > 128);
+      if (big) {   // a row with a scale byte above 252 is NaN: in its rope, while its values are zeros
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint4 rope = ld_shared_v4(rope_from + slot * 2 * HALF + h * 4 * FP4_ENTRY);
-          if (!(have >> (4 * h + rr) & 1)) rope = make_uint4(0, 0, 0, 0);
-          if (nans[h] & (0x03030303u << (2 * rr))) rope = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
-          st_shared_v4((rope_at ^ (h << 6)) + b * TILE + h * 512, rope.x, rope.y, rope.z, rope.w);
+          const uint32_t nans = __ballot_sync(0xffffffffu, most[h] > FP4_MAX_SCALE);
+          if (nans & (0x03030303u << (2 * rr))) rope[h] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
         }
       }
-      tell(c, CF + 2 * b + k, lane);
-      if (k == 1) {
-        if (lane == 0) mbar_arrive(c.bar(EE + slot));   // (every lane's loads were waited for before its stores)
-        ++g;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) st_shared_v4((rope_at ^ (h << 6)) + b * TILE + h * 512, rope[h].x, rope[h].y, rope[h].z, rope[h].w);
+      // (Every lane's loads have arrived: the codes', before the scales' that the vote needed, and the ropes'.)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(c.bar(EE + slot));
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t to = b * TILE + k * 4 * PANEL;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // One product by 2^126 times the scale, or, where a scale is above 2, two.
+          const uint32_t s = scale[0][h], words[4] = {code[0][h].x, code[0][h].y, code[0][h].z, code[0][h].w};
+          uint32_t m = big ? 0x7e80u : (s + 126) << 7;
+          if (big && s > FP4_MAX_SCALE) m = 0;
+          m |= m << 16;
+          uint32_t r[4][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            fp4_fields(words[i], r[i]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) r[i][q] = mul_bf16x2(r[i][q], m);
+          }
+          if (big) {
+            const uint32_t m2 = scale_bf16x2(s > FP4_MAX_SCALE ? 0 : s);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) r[i][q] = mul_bf16x2(r[i][q], m2);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) st_shared_v4((at[i] ^ (h << 6)) + to + h * 512, r[i][0], r[i][1], r[i][2], r[i][3]);
+          code[0][h] = code[1][h];
+          scale[0][h] = scale[1][h];
+        }
+        tell(c, CF + 2 * b + k, lane);
       }
     }
   }
