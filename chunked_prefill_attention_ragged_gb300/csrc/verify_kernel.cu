@@ -277,8 +277,11 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const __grid_constant__
   if (warp == 0) walk();
   __syncthreads();
   // A child that does not pass takes one sweep, so there are less than n of them.
+  int swept = -1;   // the node that the sums are of (with what the last child left of it)
+  uint64_t all = 0;
   for (int i = 0; i < n && !ask.pick; ++i) {
-    const uint64_t all = sweep(ask.node, ask.a, false);
+    swept = ask.node;
+    all = sweep(ask.node, ask.a, false);
     if (warp == 0) {
       mass = (double)all * UNIT;
       __syncwarp();
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const __grid_constant__
   const T* p = target + (q0 + (int64_t)last.node) * V;
   double times = last.a;
   bool given = last.given;
-  uint64_t all = sweep(last.node, times, given);
+  if (swept != last.node) all = sweep(last.node, times, given);   // (its last child's refusal asked for them already)
   if (all == 0 && (times != 0.0 || given)) {   // nothing is left: p itself
     times = 0.0;
     given = false;
