@@ -7,9 +7,11 @@
 // residual is p without their tokens, and needs none.  The next token is drawn by inverse sums from what
 // is left at the last kept node.
 //
-// Sums are integers in units of 2^-52: exact whatever their order, so that the token does not depend on
-// how the row is split.  (p - a q)+ is made by two fp32 multiply-adds with a in two fp32 parts: off by
-// 2^-24 of p at most, at random; a itself is good to 2^-48.
+// Sums are integers in units of 2^-43: exact whatever their order, so that the token does not depend on
+// how the row is split; an entry is off by half a unit at most, at random.  An entry's integer comes from two
+// additions of constants, whose results' low bits it is (a conversion of fp32 to 64 bits takes eight times as long
+// here).  (p - a q)+ is made by two fp32 multiply-adds with a in two fp32 parts: off by 2^-24 of p at most, at
+// random; a itself is good to 2^-48.
 //
 // One launch; a cluster of up to eight CTAs has a request, each a slice of the vocabulary.  Every CTA walks
 // the tree by itself (its few numbers are loaded at once, for all nodes) and comes to the same end; only
@@ -25,22 +27,38 @@
 namespace mla {
 namespace {
 
-constexpr int THREADS = 512, NWARPS = THREADS / 32;
+constexpr int THREADS = 256, NWARPS = THREADS / 32;
+constexpr int BLOCKS = 4;                  // of an SM: 64 requests' clusters of eight are all there at once
 constexpr int GROUP = 512;                 // entries of one sum
 constexpr int LOADED = 512;                // nodes whose numbers are held in shared memory
 constexpr int MAX_CLUSTER = 8;
-constexpr int SLICE = 16384;               // entries for which another CTA is worth its barriers
+constexpr int SLICE = 4096;                // entries for which another CTA is worth its barriers
 constexpr unsigned ALL = 0xffffffffu;
-constexpr double UNIT = 1.0 / 4503599627370496.0;   // 2^-52
+constexpr double UNIT = 1.0 / 8796093022208.0;   // 2^-43
 
-__device__ __forceinline__ float probability(float x) { return fminf(fmaxf(x, 0.f), 1.f); }   // (a NaN: 0)
+__device__ __forceinline__ float probability(float x) { return __saturatef(x); }   // (a NaN: 0)
 __device__ __forceinline__ float at(const float* p) { return probability(__ldg(p)); }
 __device__ __forceinline__ float at(const __nv_bfloat16* p) { return probability(__bfloat162float(*p)); }
 
-__device__ __forceinline__ uint64_t fixed(float x) { return __float2ull_rn(x * 4503599627370496.f); }   // x >= 0
+// x in [0, 1] as two integers, of units of 2^-20 (rounded) and of the rest in units of 2^-43: x + 8 has its last bit
+// at 2^-20, the rest + 1.5 * 2^-20 at 2^-43.  Sums of up to 2^8 of them are exact in 32 bits each.
+struct Fixed {
+  uint32_t high, low;
+  __device__ void add(float x) {
+    const float t = x + 8.f, u = (x - (t - 8.f)) + 1.5f / 1048576.f;
+    high += __float_as_uint(t) - __float_as_uint(8.f);
+    low += __float_as_uint(u) - __float_as_uint(1.5f / 1048576.f);
+  }
+  __device__ uint64_t value() const { return ((uint64_t)high << 23) + (uint64_t)(int64_t)(int32_t)low; }
+};
+__device__ __forceinline__ uint64_t fixed(float x) {
+  Fixed f{0, 0};
+  f.add(x);
+  return f.value();
+}
 // What is left of p after `a` times q, a = hi + lo.
 __device__ __forceinline__ float left_of(float p, float q, float hi, float lo) {
-  return fmaxf(fmaf(-lo, q, fmaf(-hi, q, p)), 0.f);
+  return __saturatef(fmaf(-lo, q, fmaf(-hi, q, p)));
 }
 
 // Sixteen bytes of a row as values.
@@ -82,36 +100,42 @@ template <class T>
 __device__ __forceinline__ uint64_t group_sum(const T* p, const T* q, int64_t first, int64_t vocab, bool wide, float hi, float lo,
                                               int lane) {
   constexpr int EACH = 16 / sizeof(T), STEPS = GROUP / 32 / EACH;
-  uint64_t s = 0;
+  Fixed s{0, 0};
   if (wide) {
-    uint4 a[STEPS], b[STEPS];
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-      const int64_t e = first + (32 * i + lane) * EACH;
-      const bool there = e < vocab;   // (all of the sixteen bytes: the vocabulary is a multiple of them)
-      a[i] = there ? __ldg(reinterpret_cast<const uint4*>(p + e)) : make_uint4(0, 0, 0, 0);
-      b[i] = there && q ? __ldg(reinterpret_cast<const uint4*>(q + e)) : make_uint4(0, 0, 0, 0);
-    }
+    for (int i = 0; i < STEPS; i += 2) {   // (two steps' loads at a time: more registers would halve the CTAs of an SM)
+      uint4 a[2], b[2];
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-      float x[EACH], y[EACH];
-      unpack(a[i], x, p);
-      unpack(b[i], y, p);
+      for (int k = 0; k < 2; ++k) {
+        const int64_t e = first + (32 * (i + k) + lane) * EACH;
+        const bool there = e < vocab;   // (all of the sixteen bytes: the vocabulary is a multiple of them)
+        a[k] = there ? __ldg(reinterpret_cast<const uint4*>(p + e)) : make_uint4(0, 0, 0, 0);
+        b[k] = there && q ? __ldg(reinterpret_cast<const uint4*>(q + e)) : make_uint4(0, 0, 0, 0);
+      }
 #pragma unroll
-      for (int k = 0; k < EACH; ++k) s += fixed(left_of(x[k], y[k], hi, lo));
+      for (int k = 0; k < 2; ++k) {
+        float x[EACH], y[EACH];
+        unpack(a[k], x, p);
+        unpack(b[k], y, p);
+#pragma unroll
+        for (int j = 0; j < EACH; ++j) s.add(left_of(x[j], y[j], hi, lo));
+      }
     }
   } else {
-    float x[GROUP / 32], y[GROUP / 32];
 #pragma unroll
-    for (int i = 0; i < GROUP / 32; ++i) {
-      const int64_t e = first + 32 * i + lane;
-      x[i] = e < vocab ? at(p + e) : 0.f;
-      y[i] = e < vocab && q ? at(q + e) : 0.f;
+    for (int i = 0; i < GROUP / 32; i += 8) {
+      float x[8], y[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int64_t e = first + 32 * (i + k) + lane;
+        x[k] = e < vocab ? at(p + e) : 0.f;
+        y[k] = e < vocab && q ? at(q + e) : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s.add(left_of(x[k], y[k], hi, lo));
     }
-#pragma unroll
-    for (int i = 0; i < GROUP / 32; ++i) s += fixed(left_of(x[i], y[i], hi, lo));
   }
-  return warp_sum(s);
+  return warp_sum(s.value());
 }
 
 // What the walk asks of all threads: a sum over the vocabulary, or the search in it, at a node with `a` times
@@ -126,7 +150,7 @@ struct Node {
 };
 
 template <class T>
-__global__ void __launch_bounds__(THREADS) verify_kernel(const __grid_constant__ VerifyParams v) {
+__global__ void __launch_bounds__(THREADS, BLOCKS) verify_kernel(const __grid_constant__ VerifyParams v) {
   extern __shared__ uint64_t sums[];              // of the slice's groups
   __shared__ int parent_s[LOADED], token_s[LOADED];
   __shared__ float u_s[LOADED], p_s[LOADED], q_s[LOADED];
@@ -333,11 +357,11 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const __grid_constant__
       const T* q = times != 0.0 ? draft + (q0 + (int64_t)last.node) * V : nullptr;
       const float hi = (float)times, lo = (float)(times - (double)hi);
       const int64_t e0 = g * GROUP + lane * (GROUP / 32);
-      uint64_t f[GROUP / 32], sum = 0;
+      float f[GROUP / 32];
 #pragma unroll
       for (int i = 0; i < GROUP / 32; ++i) {
         const int64_t e = e0 + i;
-        f[i] = e < V ? fixed(left_of(at(p + e), q ? at(q + e) : 0.f, hi, lo)) : 0ull;
+        f[i] = e < V ? left_of(at(p + e), q ? at(q + e) : 0.f, hi, lo) : 0.f;
       }
       if (given) {
         for (int j = last.node + 1; j < n; ++j) {
@@ -345,11 +369,13 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const __grid_constant__
           if (d.parent != last.node || d.token < e0 || d.token >= e0 + GROUP / 32) continue;
 #pragma unroll
           for (int i = 0; i < GROUP / 32; ++i)
-            if (e0 + i == d.token) f[i] = 0;
+            if (e0 + i == d.token) f[i] = 0.f;
         }
       }
+      Fixed mine_f{0, 0};
 #pragma unroll
-      for (int i = 0; i < GROUP / 32; ++i) sum += f[i];
+      for (int i = 0; i < GROUP / 32; ++i) mine_f.add(f[i]);
+      const uint64_t sum = mine_f.value();
       __syncwarp();
       const uint64_t s = warp_scan(sum, lane) + done;
       const unsigned m = __ballot_sync(ALL, s > goal);
@@ -358,7 +384,7 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const __grid_constant__
         int k = 0;
 #pragma unroll
         for (int i = 0; i < GROUP / 32; ++i) {
-          at_now += f[i];
+          at_now += fixed(f[i]);
           if (at_now <= goal) k = i + 1;
         }
         v.next[r] = (int32_t)(e0 + k);
