@@ -123,6 +123,22 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatil
   return ok;
 }
 
+// A barrier of `THREADS` threads, and whether any of them says yes.  Warps that wait for the same thing leave the
+// looking to one of them and meet it here: sixteen warps that look all the time take a third of the issue slots.
+template <int THREADS>
+__device__ __forceinline__ bool meet(int id, bool yes) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"((uint32_t)yes), "r"(id), "n"(THREADS)
+      : "memory");
+  return r != 0;
+}
+
 // One request as the kernel sees it.
 struct Req {
   int q0, nodes;       // rows; 0 nodes when the request is empty or refused

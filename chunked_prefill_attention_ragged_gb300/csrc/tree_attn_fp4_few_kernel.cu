@@ -23,6 +23,7 @@
 #include "internal.h"
 #include "tmem_wide.cuh"
 #include "tree_attn.cuh"
+#include "tree_issue.cuh"
 
 namespace mla {
 namespace {
@@ -77,25 +78,6 @@ struct Ctx {
 };
 template <int N>
 using PartsN = PartsOf<N, KEYS>;
-
-__device__ __forceinline__ void st_shared_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
-// A barrier of `THREADS` threads, and whether any of them says yes.  Warps that wait for the same thing leave the
-// looking to one of them and meet it here: sixteen warps that look all the time take a third of the issue slots.
-template <int THREADS>
-__device__ __forceinline__ bool meet(int id, bool yes) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}\n"
-      : "=r"(r)
-      : "r"((uint32_t)yes), "r"(id), "n"(THREADS)
-      : "memory");
-  return r != 0;
-}
 
 // A warp's part of what it writes is there: handed to the products' proxy.
 template <int N>
@@ -305,7 +287,7 @@ __device__ void run_queries(const Ctx<N>& c, PartsN<N> parts, const CUtensorMap*
 }
 
 // ------------------------------------------------------------------ products (warps 1 and 2)
-// (see tree_core.cuh: a converged warp, one elected lane, operands the same in all lanes)
+// (see issue_pair: a converged warp, one elected lane, operands the same in all lanes)
 __device__ __forceinline__ void issue(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\t"
@@ -413,7 +395,7 @@ __device__ __forceinline__ float warp_max(float x) {   // (passes over a NaN)
   return r;
 }
 
-// c * tanh(x / c) in log2 units; as in run_softmax of tree_core.cuh (there is why).
+// c * tanh(x / c) in log2 units; as cap_scores (there is why).
 __device__ __forceinline__ float capped(const TreeLaunch& p, float x) {
   const float y = x * p.cap_inv, z = y * y;
   float r = x * p.scale_log2 * fmaf(z, fmaf(z, fmaf(z, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);

@@ -1,18 +1,23 @@
-// Tree attention over a cache of 4-bit entries: the mathematics, the split of the work, the products and the
-// softmax of tree_attn_kernel.cu (a cluster of two CTAs runs a unit of 128 pairs with cta_group::2 products),
-// over keys and values that are made bf16 on their way into shared memory.
+// Tree attention over a cache of 4-bit entries: the mathematics and the split of the work of tree_attn_kernel.cu (a
+// cluster of two CTAs runs a unit of 128 pairs with cta_group::2 products of M = 128, 64 pairs in each CTA), over
+// keys and values that are made bf16 on their way into shared memory.
 //
-// Eight warps make them: four the CTA's 64 keys of a tile as the half of S's B operand, four the tile's 128
-// keys x 256 of the value columns.  A lane has four 32-value groups (16 bytes,
-// one scale) at a time: it loads them into registers while the products read the tile before, waits until four
-// panels are free, and writes 64 bytes of each in the swizzle that the products expect.  Entries go straight from L2 to registers: there is no
-// room for them in shared memory beside Q (72 KB), a tile (136 KB) and P.
-//   warp 0     Q producer
-//   warp 1     even CTA: issues every product
-//   warp 2     brings rows of the tiles to come into L2
-//   warp 3     TMEM allocation; ropes
-//   warps 4-7  softmax
-//   warps 8-11 keys, 12-15 values
+// Each CTA makes its half of a tile's keys once, as its half of S's B operand.  A key's first 512 values are its
+// value too: its columns 0-255 are values of the even CTA and 256-511 of the odd one, in the swizzle that they have as
+// keys, so that bulk copies take them there from shared memory to shared memory.  (Both made from the entries, as keys by
+// four warps and as values by four more: twice the conversions; 32 x 16 over 8192 at 128 heads 1545 us, 9 x up to
+// 37 nodes at 16 heads 54 us; copied: 1493 and 48.)  Entries go straight from L2 to registers: there is no room for them
+// in shared memory beside Q (72 KB), two tiles (136 KB) and P (16 KB).
+//   warp 0      Q producer
+//   warp 1      even CTA: issues every product; odd CTA: tells that its copies landed
+//   warp 2      copies of the values
+//   warp 3      TMEM allocation; ropes; brings entries into L2
+//   warps 4-11  softmax: four threads per pair (quarters of the keys and of O's columns)
+//   warps 12-19 keys
+// A tile has 64 keys, so that there are two: with one of 128 its making, S, P V and the copies took turns (2207 us).
+// A product of 64 keys takes as long as one of 128 (30 clocks: Q's rows are read from shared memory for each), which
+// makes 1600 clocks of products a tile; a tile takes 3300, of which the warps that make keys work 2600: what they wait
+// for is shared memory's queue, behind 264 KB a tile that products and copies take from it.
 // A code becomes bf16 by moving its bits to a bf16's low exponent bits and one product by 2^126 times the
 // scale, exact; scales above 2, where that factor has no bf16, take two products (a tile in which a warp
 // meets one).  A row with a scale byte above 252 has NaN in its rope, which only S sees, and zeros for values,
@@ -21,53 +26,93 @@
 
 #include "fp4.cuh"
 #include "internal.h"
-#include "tree_core.cuh"
+#include "tmem_wide.cuh"
+#include "tree_attn.cuh"
+#include "tree_issue.cuh"
 
 namespace mla {
 namespace {
 
-constexpr int NTHREADS = 512;
-constexpr int LAUNCH_REGS = 128;
-constexpr int REGS_CTRL = 88, REGS_SOFTMAX = 216, REGS_ROWS = 104;
-static_assert(REGS_CTRL + REGS_SOFTMAX + 2 * REGS_ROWS <= 4 * LAUNCH_REGS, "register split exceeds the launch allocation");
-constexpr int AHEAD = 2;   // tiles between the one being made and the one brought into L2
+constexpr int ROWS = 128, KEYS = 64;
+constexpr int NTHREADS = 640;
+constexpr int AHEAD = 4;                // tiles between the one being made and the one brought into L2
+constexpr int NP = 9;                   // 64-column panels of 576
+constexpr int QP = 64 * 128;            // a panel of Q, P or V: 64 rows
+constexpr int KP = KEYS / 2 * 128;      // a panel of K: the CTA's half of the keys
+constexpr int V_HALF = 4 * KP;          // of V: four panels of the keys of one CTA
+constexpr int K_TILE = NP * KP, V_TILE = 2 * V_HALF;
+constexpr int OFF_Q = 0;
+constexpr int OFF_K = OFF_Q + NP * QP;              // two tiles
+constexpr int OFF_V = OFF_K + 2 * K_TILE;           // two tiles: 64 keys x the CTA's 256 value columns
+constexpr int OFF_P = OFF_V + 2 * V_TILE;           // two tiles
+constexpr int OFF_XCHG = OFF_P + 2 * QP;            // [4 threads][64 rows] maxima
+constexpr int OFF_BAR = OFF_XCHG + 4 * 64 * 4;
+enum Bar {
+  QF = 0,       // Q landed
+  QE,           // the unit's last S done: Q may be replaced
+  KF,           // [buffer] keys made (of both CTAs), for the products
+  KL = KF + 2,  // [buffer] the CTA's own, but for the ropes, for their copies
+  KE = KL + 2,  // [buffer] S done with them, and both CTAs' copies
+  VF = KE + 2,  // [buffer] the CTA's values landed
+  VR = VF + 2,  // [buffer] (even CTA) the odd one's did
+  VE = VR + 2,  // [buffer] P V done: values, P and, for the next rescale, O are free
+  SF = VE + 2,  // [buffer] S done (in both CTAs)
+  PR = SF + 2,  // [buffer] P written (and the S buffer read) by every softmax warp of both CTAs
+  FIN = PR + 2, // every product drained
+  NEVER,        // nothing arrives here: the time-out test mode waits on it
+  NBAR
+};
+constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+constexpr int SMEM = OFF_MISC + 64 + 1024;   // + slack for 1024-byte alignment
+static_assert(SMEM + 512 <= 227 * 1024, "shared memory budget");
+constexpr uint32_t TMEM_COLS = 512;
+__device__ __forceinline__ constexpr uint32_t TM_S(int b) { return 256u + (uint32_t)b * (KEYS / 2); }
+constexpr uint32_t IDESC_QK = idesc_bf16_f32(ROWS, KEYS, false, false);
+constexpr uint32_t IDESC_PV = idesc_bf16_f32(ROWS, 256, false, true);
+using PartsK = PartsOf<ROWS, KEYS>;
 
-template <int N>
-__device__ __forceinline__ void setmaxnreg_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void setmaxnreg_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
+struct Ctx {
+  uint32_t sbase;
+  volatile int* abort_flag;
+  int* status;
+  uint64_t wait_limit_ns;
+  uint32_t rank;
+  __device__ uint32_t bar(int i) const { return sbase + OFF_BAR + 8 * i; }
+  __device__ bool wait(int b, uint32_t parity) const {
+    return mbar_wait_bounded(bar(b), parity, abort_flag, status, MLA_DEVSTAT_TIMEOUT, wait_limit_ns);
+  }
+  __device__ bool wait_warp(int b, uint32_t parity) const {
+    return mla::wait_warp(bar(b), parity, abort_flag, status, wait_limit_ns);
+  }
+  __device__ void drain(int b, uint32_t parity) const {
+    int dummy = 0;
+    mbar_wait_bounded(bar(b), parity, &dummy, status, MLA_DEVSTAT_TIMEOUT, TREE_DRAIN_LIMIT_NS, true);
+  }
+};
 
-__device__ __forceinline__ uint4 load16(const uint8_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+// Zeros, or the load: without a copy of its registers, which would wait for it.
+__device__ __forceinline__ uint4 load16_if(bool there, const uint8_t* p) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}\n"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"((uint32_t)there));
+  return v;
+}
+__device__ __forceinline__ uint32_t load1_if(bool there, const uint8_t* p) {
+  uint32_t v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.nc.u8 %0, [%1];\n\t}\n"
+      : "=&r"(v)
+      : "l"(p), "r"((uint32_t)there));
+  return v;
+}
 // Bytes of a word above 252 (in their top bits).
 __device__ __forceinline__ uint32_t above252(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x03030303u) & w & 0x80808080u; }
 
-// A group's 32 values to four 16-byte pieces.  Each code is multiplied by `m` and, where the scales are `big`,
-// by `m2`.
-__device__ __forceinline__ void put_group(const uint32_t* at, uint32_t flip, uint32_t more, const uint4& w, bool big, uint32_t m,
-                                          uint32_t m2) {
-  const uint32_t words[4] = {w.x, w.y, w.z, w.w};
-  uint32_t r[4][4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    fp4_fields(words[i], r[i]);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) r[i][k] = mul_bf16x2(r[i][k], m);
-  }
-  if (big) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) r[i][k] = mul_bf16x2(r[i][k], m2);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) st_shared_v4((at[i] ^ flip) + more, r[i][0], r[i][1], r[i][2], r[i][3]);
-}
-
-// A warp's part of what it writes is there: handed to the products' proxy, told to the even CTA.
+// A warp's part of what it writes is there: handed to the asynchronous proxy, told to the even CTA.
 __device__ __forceinline__ void tell(const Ctx& c, int b, int lane) {
   fence_async_shared();
   __syncwarp();
@@ -77,31 +122,23 @@ __device__ __forceinline__ void tell(const Ctx& c, int b, int lane) {
   }
 }
 
-// What the eight warps do is a line of stages, two for each tile: four panels of 64 rows each.  Keys (warps
-// 8-11): panels 0-3 and 4-7 of the CTA's 64 keys; values (warps 12-15): the CTA's four panels, of the tile's
-// first and second 64 keys.  A warp has 16 rows.  The bytes of the stage after next are loaded when a stage is done: most of a tile's time before they are needed.  One loop
-// for both, and short: straight code for a tile of each did not stay in the instruction cache (see below).
-//
-// Lane (panel, row % 4, half) = (l / 8, l / 2 % 4, l % 2) has a piece of rows 4 j + row % 4 of the warp's, j < 4:
-// a load takes 128 bytes of four rows, and eight lanes of a store have eight different bank groups.
-struct Stage {
-  uint4 code[4];
-  uint32_t scale[4];
+// Warps 12-19: four of the CTA's 32 keys each.  Lane (panel % 4, row, half panel) = (l / 8, l / 2 % 4, l % 2) makes
+// two pieces of 32 columns, of panel % 4 and panel % 4 + 4.  A load takes 128 bytes of four rows, and eight lanes of a
+// store have eight different bank groups.
+struct Pieces {
+  uint4 code[2];
+  uint32_t scale[2];
 };
-__device__ void run_rows(const Ctx& c, const TreeLaunch& p, Parts parts, bool values, volatile int* begun) {
-  const int lane = threadIdx.x & 31, w4 = (threadIdx.x >> 5) & 3, r4 = (lane >> 1) & 3;
-  const int group = 2 * (lane >> 3) + (lane & 1);   // of the stage's eight
-  const uint32_t dst = c.sbase + (values ? OFF_V : OFF_K);
-  uint32_t at[4];
+__device__ void run_rows(const Ctx& c, const TreeLaunch& p, PartsK parts) {
+  const int lane = threadIdx.x & 31, w8 = (threadIdx.x >> 5) & 7, r4 = (lane >> 1) & 3;
+  const int group = 2 * (lane >> 3) + (lane & 1);   // of four panels' eight
+  const int row8 = 4 * (w8 & 1) + r4;               // row % 8: the swizzle
+  uint32_t chunk[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) at[i] = dst + (lane >> 3) * QP + (16 * w4 + r4) * 128 + (((4 * (lane & 1) + i) ^ r4) << 4);
-  const int full = values ? VF : KF, empty = values ? VE : KE;
-  // The key of stage 0 that this lane looks up (lanes 0-15: the warp's rows), how much further stage 1's is,
-  // and where a stage's bytes lie in an entry.
-  const int first = (values ? 0 : 64 * (int)c.rank) + 16 * w4 + (lane & 15), second = values ? 64 : 0;
-  const int part = values ? (int)c.rank : 0, step = values ? 0 : 1;
+  for (int i = 0; i < 4; ++i) chunk[i] = ((4 * (lane & 1) + i) ^ row8) << 4;
+  const uint32_t keys_at = c.sbase + OFF_K + (lane >> 3) * KP + (4 * w8 + r4) * 128;
   const uint8_t* cache = reinterpret_cast<const uint8_t*>(p.t.cache);
-  int tiles = 0;
+  int g = 0;
   bool ok = true;
   Part u;
   while (ok && parts.next(&u)) {
@@ -110,114 +147,183 @@ __device__ void run_rows(const Ctx& c, const TreeLaunch& p, Parts parts, bool va
     auto find = [&](int64_t key) {
       return key < end ? __ldg(p.t.block_table + (int64_t)u.r * p.t.max_blocks + block_of(p, (int)key)) : 0;
     };
-    auto get = [&](int32_t blk, int64_t key, int s, Stage* to) {
-      const int32_t mine = key < end ? block_row(p, blk == PAST_END ? -1 : blk, key) : p.oob_row;
-      const int at_code = 128 * (part + step * s) + 16 * group, at_scale = FP4_SCALES + 8 * (part + step * s) + group;
+    auto get = [&](int32_t blk, int64_t key, Pieces* to) {
+      const int32_t row = key < end ? block_row(p, blk == PAST_END ? -1 : blk, key) : p.oob_row;
+      const bool there = row != p.oob_row;
+      const uint8_t* e = cache + (int64_t)row * FP4_ENTRY;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int32_t row = __shfl_sync(0xffffffffu, mine, 4 * j + r4);
-        to->code[j] = make_uint4(0, 0, 0, 0);
-        to->scale[j] = 0;
-        if (row != p.oob_row) {
-          const uint8_t* e = cache + (int64_t)row * FP4_ENTRY;
-          to->code[j] = load16(e + at_code);
-          to->scale[j] = __ldg(e + at_scale);
-        }
+      for (int j = 0; j < 2; ++j) {
+        to->code[j] = load16_if(there, e + 16 * group + 128 * j);
+        to->scale[j] = load1_if(there, e + FP4_SCALES + group + 8 * j);
       }
     };
-    int64_t key = (int64_t)u.lo * KEYS + first;
-    Stage now, next;
-    get(find(key), key, 0, &now);
-    get(find(key + second), key + second, 1, &next);
-    key += KEYS;
-    int32_t blk0 = find(key), blk1 = find(key + second);   // of the two stages after those
+    int64_t key = (int64_t)u.lo * KEYS + KEYS / 2 * (int)c.rank + 4 * w8 + r4;
+    Pieces now;
+    get(find(key), key, &now);
+    int32_t blk = find(key + KEYS);
 #pragma unroll 1
-    for (int n = 0; n < 2 * (u.hi - u.lo); ++n) {
-      const int s = n & 1;
-      if (s == 0 && !values && w4 == 0 && lane == 0) *begun = tiles;
+    for (int t = u.lo; t < u.hi; ++t, ++g) {
+      const int b = g & 1;
+      const bool big = __any_sync(0xffffffffu, max(now.scale[0], now.scale[1]) > 128);
+      uint32_t r[2][16];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        // 2^126 times the scale, or one after the other; values of a row that is NaN are zeros
+        const uint32_t s = now.scale[j], words[4] = {now.code[j].x, now.code[j].y, now.code[j].z, now.code[j].w};
+        uint32_t m = big ? 0x7e80u : (s + 126) << 7;
+        if (big && s > FP4_MAX_SCALE) m = 0;
+        m |= m << 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          fp4_fields(words[i], r[j] + 4 * i);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) r[j][4 * i + k] = mul_bf16x2(r[j][4 * i + k], m);
+        }
+        if (big) {
+          const uint32_t m2 = scale_bf16x2(s > FP4_MAX_SCALE ? 0 : s);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) r[j][k] = mul_bf16x2(r[j][k], m2);
+        }
+      }
+      key += KEYS;
+      get(blk, key, &now);
+      blk = find(key + KEYS);
       __syncwarp();
-      if (tiles > 0 && !c.wait_warp(empty + s, (tiles - 1) & 1)) {
+      if (w8 == 0 && g > 1) ok = c.wait_warp(KE + b, ((g >> 1) - 1) & 1);
+      if (meet<256>(3, !ok)) {
         ok = false;
         break;
       }
-      const uint32_t most = max(max(now.scale[0], now.scale[1]), max(now.scale[2], now.scale[3]));
-      const bool big = __any_sync(0xffffffffu, most > 128);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t b = now.scale[j];
-        // 2^126 times the scale, or one after the other; values of a row that is NaN are zeros
-        uint32_t m = big ? 0x7e80u : (b + 126) << 7;
-        if (b > FP4_MAX_SCALE) m = 0;
-        put_group(at, (j & 1) << 6, s * 4 * QP + j * 512, now.code[j], big, m | m << 16,
-                  scale_bf16x2(b > FP4_MAX_SCALE ? 0 : b));
-      }
-      tell(c, full + s, lane);
-      now = next;
-      const int64_t k = key + (s ? second : 0);
-      get(s ? blk1 : blk0, k, s, &next);
-      if (s == 0) {
-        blk0 = find(k + KEYS);
-      } else {
-        blk1 = find(k + KEYS);
-        key += KEYS;
-        ++tiles;
-      }
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          st_shared_v4(keys_at + b * K_TILE + 4 * j * KP + chunk[i], r[j][4 * i], r[j][4 * i + 1], r[j][4 * i + 2], r[j][4 * i + 3]);
+      tell(c, KF + b, lane);
+      if (lane == 0) mbar_arrive(c.bar(KL + b));
     }
   }
 }
 
-// Warp 3: the ropes of the CTA's 64 keys, K's last panel.  Lane i has 16 bytes of rows 4 j + i / 8; a row with
-// a scale byte above 252 gets NaN.
-__device__ void run_ropes(const Ctx& c, const TreeLaunch& p, Parts parts) {
-  const int lane = threadIdx.x & 31, ch = lane & 7;
-  const uint32_t dst = c.sbase + OFF_K + 8 * QP;
-  int tiles = 0;
+// Warp 2: a key's first 256 columns are values of the even CTA, the others of the odd one, in the swizzle that they have
+// as keys: they are copied from shared memory to shared memory, 32 rows of a panel at a time.
+__device__ void run_copies(const Ctx& c, PartsK parts) {
+  const int lane = threadIdx.x & 31, to_cta = lane & 1;
+  const uint32_t from = c.sbase + OFF_K + to_cta * V_HALF;
+  const uint32_t to = mapa_shared(c.sbase + OFF_V + c.rank * V_HALF, to_cta);
+  const uint32_t full = mapa_shared(c.bar(VF), to_cta);
+  int g = 0;
   bool ok = true;
   Part u;
   while (ok && parts.next(&u)) {
-    int64_t key0 = (int64_t)u.lo * KEYS + 64 * c.rank;
-    KeyBlocks b = find_blocks(p, u, key0, lane);
 #pragma unroll 1
-    for (int t = u.lo; t < u.hi; ++t, ++tiles, key0 += KEYS) {
-      const KeyRows k = find_rows(p, b, key0, lane);
-      if (t + 1 < u.hi) b = find_blocks(p, u, key0 + KEYS, lane);
-      // which of a lane's two rows are NaN
-      uint32_t bad[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint4 s = make_uint4(0, 0, 0, 0);
-        if (k.r[i] != p.oob_row) s = load16(reinterpret_cast<const uint8_t*>(p.t.cache) + (int64_t)k.r[i] * FP4_ENTRY + FP4_SCALES);
-        bad[i] = __ballot_sync(0xffffffffu, (above252(s.x) | above252(s.y) | above252(s.z) | above252(s.w)) != 0);
+    for (int t = u.lo; t < u.hi; ++t, ++g) {
+      const int b = g & 1;
+      ok = (g < 2 || c.wait_warp(VE + b, ((g >> 1) - 1) & 1)) && c.wait_warp(KL + b, (g >> 1) & 1);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(c.bar(VF + b), V_TILE);
+      if (lane < 2)
+        asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to + b * V_TILE),
+                     "r"(from + b * K_TILE), "r"(V_HALF), "r"(full + 8 * b)
+                     : "memory");
+      __syncwarp();
+      if (c.rank == 0 && g > 0) {   // the even CTA's last ones landed
+        ok = c.wait_warp(VF + (b ^ 1), ((g - 1) >> 1) & 1);
+        if (!ok) break;
+        if (lane < 2) mbar_arrive_remote(mapa_shared(c.bar(KE + (b ^ 1)), lane));
+        __syncwarp();
       }
-      if (tiles > 0 && !c.wait_warp(KE + 2, (tiles - 1) & 1)) {
-        ok = false;
-        break;
-      }
-#pragma unroll 2
-      for (int j = 0; j < 16; ++j) {
-        const int key = 4 * j + (lane >> 3);
-        const int32_t row = __shfl_sync(0xffffffffu, j < 8 ? k.r[0] : k.r[1], key & 31);
-        const bool there = row != p.oob_row;
-        const uint8_t* src = (there ? reinterpret_cast<const uint8_t*>(p.t.cache) + (int64_t)row * FP4_ENTRY + FP4_ROPE
-                                    : reinterpret_cast<const uint8_t*>(p.t.q)) + ch * 16;
-        cp_async16(dst + key * 128 + ((ch ^ (key & 7)) << 4), src, there ? 16 : 0);
-      }
-      cp_async_commit();
-      cp_async_wait<0>();
-      if (bad[0] | bad[1]) {
-        __syncwarp();   // (a row's pieces are other lanes' copies)
-        for (int j = 0; j < 16; ++j) {
-          const int key = 4 * j + (lane >> 3);
-          if ((bad[j >> 3] >> (key & 31)) & 1)
-            st_shared_v4(dst + key * 128 + ch * 16, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
-        }
-      }
-      tell(c, KF + 2, lane);
+    }
+  }
+  if (!ok) {   // the copies under way land before a CTA can exit: they have this long
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < TREE_DRAIN_LIMIT_NS) {
     }
   }
 }
 
-__device__ void run_queries(const Ctx& c, Parts parts, const CUtensorMap* tq) {
+// The odd CTA's warp 1: its copies landed.
+__device__ void run_relay(const Ctx& c, PartsK parts) {
+  const uint32_t there = mapa_shared(c.bar(VR), 0);
+  int g = 0;
+  bool ok = true;
+  Part u;
+  while (ok && parts.next(&u)) {
+#pragma unroll 1
+    for (int t = u.lo; t < u.hi && ok; ++t, ++g) {
+      ok = c.wait_warp(VF + (g & 1), (g >> 1) & 1);
+      if (ok && (threadIdx.x & 31) == 0) mbar_arrive_remote(there + 8 * (g & 1));
+      if (ok && (threadIdx.x & 31) < 2) mbar_arrive_remote(mapa_shared(c.bar(KE + (g & 1)), threadIdx.x & 31));
+      __syncwarp();
+    }
+  }
+}
+
+// Warp 3: the ropes of the CTA's 32 keys, K's last panel, and the entries of the tiles to come into L2.  Lane i has
+// 16 bytes of rows 4 j + i / 8, loaded a tile ahead; a row with a scale byte above 252 gets NaN.
+__device__ void run_ropes(const Ctx& c, const TreeLaunch& p, PartsK parts) {
+  const int lane = threadIdx.x & 31, ch = lane & 7, r0 = lane >> 3;
+  const uint8_t* cache = reinterpret_cast<const uint8_t*>(p.t.cache);
+  int g = 0;
+  bool ok = true;
+  Part u;
+  while (ok && parts.next(&u)) {
+    const int64_t end = min((int64_t)u.hi * KEYS, (int64_t)u.q.kv);
+    int64_t key = (int64_t)u.lo * KEYS + KEYS / 2 * c.rank + lane;
+    auto find = [&](int64_t k) {
+      return k < end ? __ldg(p.t.block_table + (int64_t)u.r * p.t.max_blocks + block_of(p, (int)k)) : 0;
+    };
+    auto row_of = [&](int32_t blk, int64_t k) {
+      const int32_t row = k < end ? block_row(p, blk == PAST_END ? -1 : blk, k) : p.oob_row;
+      if (row != p.oob_row) {
+        const uint8_t* e = cache + (int64_t)row * FP4_ENTRY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm volatile("prefetch.global.L2 [%0];" ::"l"(e + 128 * i) : "memory");
+      }
+      return row;
+    };
+    uint4 rope[8], s;
+    auto load = [&](int32_t rows) {
+      s = load16_if(rows != p.oob_row, cache + (int64_t)rows * FP4_ENTRY + FP4_SCALES);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int32_t row = __shfl_sync(0xffffffffu, rows, 4 * j + r0);
+        rope[j] = load16_if(row != p.oob_row, cache + (int64_t)row * FP4_ENTRY + FP4_ROPE + ch * 16);
+      }
+    };
+    int32_t blk[AHEAD + 1], row[AHEAD];   // row[i]: of the tile i + 1 ahead
+#pragma unroll
+    for (int i = 0; i <= AHEAD; ++i) blk[i] = find(key + i * KEYS);
+    load(row_of(blk[0], key));
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) row[i] = row_of(blk[i + 1], key + (i + 1) * KEYS);
+    int32_t last = find(key + (AHEAD + 1) * KEYS);
+#pragma unroll 1
+    for (int t = u.lo; t < u.hi; ++t, ++g, key += KEYS) {
+      const int b = g & 1;
+      const uint32_t dst = c.sbase + OFF_K + b * K_TILE + 8 * KP + r0 * 128;
+      if (g > 1 && !c.wait_warp(KE + b, ((g >> 1) - 1) & 1)) {
+        ok = false;
+        break;
+      }
+      const uint32_t bad = __ballot_sync(0xffffffffu, (above252(s.x) | above252(s.y) | above252(s.z) | above252(s.w)) != 0);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if ((bad >> (4 * j + r0)) & 1) rope[j] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+        st_shared_v4(dst + j * 512 + ((ch ^ (4 * (j & 1) + r0)) << 4), rope[j].x, rope[j].y, rope[j].z, rope[j].w);
+      }
+      tell(c, KF + b, lane);
+      const int32_t rows = row[0];
+#pragma unroll
+      for (int i = 0; i + 1 < AHEAD; ++i) row[i] = row[i + 1];
+      row[AHEAD - 1] = row_of(last, key + (AHEAD + 1) * KEYS);
+      load(rows);
+      last = find(key + (AHEAD + 2) * KEYS);
+    }
+  }
+}
+
+__device__ void run_queries(const Ctx& c, PartsK parts, const CUtensorMap* tq) {
   const int lane = threadIdx.x & 31;
   int units = 0;
   bool ok = true;
@@ -226,49 +332,238 @@ __device__ void run_queries(const Ctx& c, Parts parts, const CUtensorMap* tq) {
     if (lane == 0) {
       if (units > 0) ok = c.wait(QE, (units - 1) & 1);
       if (ok) {
-        expect_both(c, QF, NP * QP);
+        // (both CTAs' copies complete on the even one's barrier, where the products wait)
+        if (c.rank == 0) mbar_arrive_expect_tx(c.bar(QF), 2 * NP * QP);
         tma_load_3d_pair(c.sbase + OFF_Q, tq, mapa_shared(c.bar(QF), 0), 0, (int32_t)(u.pair0 + 64 * c.rank), 0);
       }
     }
     ok = __shfl_sync(0xffffffffu, ok, 0);
     if (ok) ++units;
   }
-  if (lane == 0) {
+  if (lane == 0) {   // the copies land before the CTA can exit
     if (c.rank == 0) {
       if (units) c.drain(QF, (units - 1) & 1);
-    } else if (!ok) {
-      settle();
+    } else if (!ok) {   // the odd CTA cannot see its own: they have this long
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < TREE_DRAIN_LIMIT_NS) {
+      }
     }
   }
 }
 
-// Warp 2: this CTA's keys of the tiles to come into L2, a lane an entry.  It follows the keys' count of
-// tiles and gives up quietly.
-__device__ void run_prefetch(const Ctx& c, const TreeLaunch& p, Parts parts, const volatile int* begun) {
-  const int lane = threadIdx.x & 31;
-  int tiles = 0;
+// ------------------------------------------------------------------ products (even CTA, warp 1)
+__device__ void run_mma(const Ctx& c, const TreeLaunch& p, PartsK parts, uint32_t tmem) {
+  const uint64_t q_desc = sdesc_sw128(c.sbase + OFF_Q, 16, 1024);
+  const uint64_t k_desc = sdesc_sw128(c.sbase + OFF_K, 16, 1024);
+  const uint64_t v_desc = sdesc_sw128(c.sbase + OFF_V, KP, 1024);
+  const uint64_t p_desc = sdesc_sw128(c.sbase + OFF_P, 16, 1024);
+  bool ok = true;
+  if (p.force_timeout) ok = c.wait_warp(NEVER, 0);
+  int st = 0, pv = 0, units = 0;
+  auto s_products = [&](bool last) {
+    const int b = st & 1;
+    const uint32_t d = __shfl_sync(0xffffffffu, tmem + TM_S(b), 0), tile = __shfl_sync(0xffffffffu, (uint32_t)(b * K_TILE) >> 4, 0);
+    if (!c.wait_warp(KF + b, (st >> 1) & 1)) return false;
+    tc_fence_after();
+#pragma unroll 1
+    for (int i = 0; i < NP; ++i) {
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        issue_pair(d, q_desc + ((uint32_t)(i * QP + kk * 32) >> 4), k_desc + tile + ((uint32_t)(i * KP + kk * 32) >> 4), IDESC_QK,
+                   kk > 0 ? 1u : i > 0 ? 1u : 0u);
+    }
+    commit_both(c.bar(KE + b));
+    commit_both(c.bar(SF + b));
+    if (last) commit_both(c.bar(QE));
+    ++st;
+    return true;
+  };
+  auto pv_products = [&](uint32_t add) {
+    const int b = pv & 1;
+    const uint32_t more = __shfl_sync(0xffffffffu, add, 0);
+    const uint32_t tile = __shfl_sync(0xffffffffu, (uint32_t)(b * V_TILE) >> 4, 0), pt = __shfl_sync(0xffffffffu, (uint32_t)(b * QP) >> 4, 0);
+    if (!c.wait_warp(PR + b, (pv >> 1) & 1) || !c.wait_warp(VF + b, (pv >> 1) & 1) || !c.wait_warp(VR + b, (pv >> 1) & 1)) return false;
+    tc_fence_after();
+#pragma unroll 1
+    for (int ch = 0; ch < 2; ++ch) {
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        issue_pair(tmem + ch * 128, p_desc + pt + ((uint32_t)(kk * 32) >> 4), v_desc + tile + ((uint32_t)(2 * ch * KP + (kk >> 1) * V_HALF + (kk & 1) * 2048) >> 4),
+                   IDESC_PV, kk > 0 ? 1u : more);
+    }
+    commit_both(c.bar(VE + b));
+    ++pv;
+    return true;
+  };
+  Part u;
+  while (ok && parts.next(&u)) {
+    const int n = __shfl_sync(0xffffffffu, u.hi - u.lo, 0);
+    ok = c.wait_warp(QF, units & 1);
+    ++units;
+    for (int t = 0; t < n && ok; ++t) {
+      // S's buffer held the scores of the tile before last, read before that tile's P was ready: its P V is behind us.
+      ok = s_products(t == n - 1);
+      if (ok && t > 0) ok = pv_products(t > 1 ? 1u : 0u);
+    }
+    if (ok) ok = pv_products(n > 1 ? 1u : 0u);
+  }
+  commit_both(c.bar(FIN));
+  c.drain(FIN, 0);
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------ softmax (warps 4-11)
+// Four threads a row: (half, quarter) have keys 32 half + 16 quarter .. and columns 256 half + 128 quarter ...  One of
+// the eight warps looks for S and the others meet it; as these meetings have no time limit, where a wait gave up the
+// warps go through the rest of their tiles without waiting.
+__device__ void run_softmax(const Ctx& c, const TreeLaunch& p, PartsK parts, uint32_t tmem, char* ws_slots, uint8_t* smem) {
+  const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3, sub = ((threadIdx.x >> 5) - 4) >> 2;
+  const int half = q4 >> 1, rg = q4 & 1;             // key / column half, group of 32 rows
+  const int row = 32 * rg + lane;                    // of the CTA's 64
+  const uint32_t lane_addr = tmem + ((uint32_t)(q4 * 32) << 16);
+  float* xchg = reinterpret_cast<float*>(smem + OFF_XCHG);
+  const uint32_t p_row = c.sbase + OFF_P + row * 128;
+  const float NEG_INF = -__int_as_float(0x7f800000);
+  const float sc = p.has_cap ? 1.f : p.scale_log2;
+  const float2 sc2 = make_float2(sc, sc);
+  bool ok = true;
+  int g = 0;
+  auto wait = [&](int b, uint32_t parity) { ok = ok && c.wait_warp(b, parity); };
+  // The four threads' values of a row; a meeting of the row group's warps lies between two exchanges.
+  auto exchange = [&](float mine) {
+    xchg[(2 * half + sub) * 64 + row] = mine;
+    meet<128>(5 + rg, false);
+    return make_float4(xchg[row], xchg[64 + row], xchg[128 + row], xchg[192 + row]);
+  };
   Part u;
   while (parts.next(&u)) {
-    for (int t = u.lo; t < u.hi; ++t, ++tiles) {
-      const uint64_t t0 = global_timer_ns();
-      while (*begun < tiles) {
-        __nanosleep(200);
-        if (*c.abort_flag || global_timer_ns() - t0 > p.wait_limit_ns) return;
-      }
-      __syncwarp();
-      if (t + AHEAD < u.hi) {
+    const int pr0 = 64 * (int)c.rank + row;          // pair inside the unit
+    const int64_t pair = u.pair0 + pr0;
+    // A row without a pair computes on something harmless: the last node's mask.
+    const int node = min((int)((pair - (int64_t)u.q.q0 * p.t.num_heads) / p.t.num_heads), u.q.nodes - 1);
+    float m_used = NEG_INF, l = 0.f;
+#pragma unroll 1
+    for (int t = u.lo; t < u.hi; ++t, ++g) {
+      const int b = g & 1;
+      if (q4 == 0 && sub == 0) wait(SF + b, (g >> 1) & 1);
+      if (meet<256>(2, !ok)) ok = false;
+      tc_fence_after();
+      float sv[16];
+      tmem_ld16_sync(lane_addr + TM_S(b) + 16 * sub, reinterpret_cast<uint32_t*>(sv));
+      if (p.has_cap) cap_scores<16>(p, sv);
+      const int64_t pos0 = (int64_t)t * KEYS + 32 * half + 16 * sub;
+      if (pos0 + 16 > min(u.q.ctx, (int64_t)u.q.kv)) {   // nodes, or the end of the keys
+        const uint32_t v = (uint32_t)visible(p.t, u, node, pos0);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int64_t key = (int64_t)(t + AHEAD) * KEYS + 64 * c.rank + 32 * i + lane;
-          if (key < u.q.kv) {
-            const int32_t row = block_row(p, table_block(p, u, key), key);
-            const uint8_t* e = reinterpret_cast<const uint8_t*>(p.t.cache) + (int64_t)row * FP4_ENTRY;
-            if (row != p.oob_row)
-              asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(e), "r"(FP4_ENTRY) : "memory");
-          }
+        for (int k = 0; k < 16; ++k)
+          if (!((v >> k) & 1)) sv[k] = NEG_INF;
+      }
+      float mx[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        mx[k] = fmax3(fmax3(sv[8 * k], sv[8 * k + 1], sv[8 * k + 2]),
+                      fmax3(sv[8 * k + 3], sv[8 * k + 4], sv[8 * k + 5]), fmaxf(sv[8 * k + 6], sv[8 * k + 7]));
+      const float mt = fmaxf(mx[0], mx[1]) * sc;
+      // The row's maximum is asked for in a part's first tile and where some row's has grown by more than the threshold;
+      // elsewhere the reference stays, and no probability is above 2^threshold.
+      float m_new = m_used;
+      bool rescale = false;
+      const bool first = t == u.lo;
+      if (meet<128>(5 + rg, first || mt > m_used + TREE_RESCALE_THRESHOLD)) {
+        const float4 x = exchange(mt);
+        const float top = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w));
+        if (first) {
+          m_new = top;
+        } else if (top > m_used + TREE_RESCALE_THRESHOLD) {
+          m_new = top;
+          rescale = true;
         }
       }
+      const float msub = (m_new == NEG_INF) ? 0.f : m_new;
+      const float2 neg_m = make_float2(-msub, -msub);
+      float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      uint32_t pr[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float2 a = ffma2(make_float2(sv[2 * k], sv[2 * k + 1]), sc2, neg_m);
+        const float2 e = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+        acc[k & 1] = fadd2(acc[k & 1], e);
+        pr[k] = pack_bf16x2(e.x, e.y);   // the operand type; the sum is of the unrounded values
+      }
+      const float2 s01 = fadd2(acc[0], acc[1]);
+      const float alpha = rescale ? ex2_approx(m_used - m_new) : 1.f;
+      l = l * alpha + (s01.x + s01.y);
+      // (P's buffer was read by the tile before last's product, issued before this tile's S)
+      if (__any_sync(0xffffffffu, rescale)) {        // O behind the last one's; tcgen05.ld/st are warp-collective
+        wait(VE + (b ^ 1), ((g - 1) >> 1) & 1);
+        tc_fence_after();
+        const float2 a2 = make_float2(alpha, alpha);
+#pragma unroll 1
+        for (int q = 0; q < 8; ++q) {
+          const uint32_t at = lane_addr + 128 * sub + q * 16;
+          tmem_ld16_sync(at, reinterpret_cast<uint32_t*>(sv));
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float2 r = fmul2(make_float2(sv[2 * k], sv[2 * k + 1]), a2);
+            sv[2 * k] = r.x;
+            sv[2 * k + 1] = r.y;
+          }
+          tmem_st16_sync(at, reinterpret_cast<uint32_t*>(sv));
+        }
+      }
+      m_used = m_new;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        st_shared_v4(p_row + b * QP + (((4 * half + 2 * sub + k) ^ (row & 7)) << 4), pr[4 * k], pr[4 * k + 1], pr[4 * k + 2], pr[4 * k + 3]);
+      tc_fence_before();
+      tell(c, PR + b, lane);
     }
+    // The part's end: the row's sum, then O out of TMEM once the last product is done.
+    meet<128>(5 + rg, false);
+    const float4 ls = exchange(l);
+    const float l_row = (ls.x + ls.y) + (ls.z + ls.w);
+    wait(VE + ((g - 1) & 1), ((g - 1) >> 1) & 1);
+    tc_fence_after();
+    const bool live = ok && pr0 < u.npairs, empty = l_row == 0.f;   // (a NaN is passed on)
+    const float inv = u.whole ? (empty ? 0.f : 1.f / l_row) : 1.f;
+    const float2 inv2 = make_float2(inv, inv);
+    char* slot = ws_slots + (size_t)u.slot * SLOT_BYTES;
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+      const int col = 256 * half + 128 * sub + 32 * q;   // TMEM columns 128 sub + 32 q ..: the values of CTA `half`
+      uint32_t ov[32];
+      tmem_ld32_sync(lane_addr + 128 * sub + q * 32, ov);
+      if (live && u.whole) {
+        uint32_t w[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float2 r = fmul2(make_float2(__uint_as_float(ov[2 * k]), __uint_as_float(ov[2 * k + 1])), inv2);
+          w[k] = empty ? 0u : pack_bf16x2(r.x, r.y);
+        }
+        __nv_bfloat16* d = p.t.o + pair * 512 + col;
+        if (p.o_align32) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) st_global_v8(d + 16 * k, w + 8 * k);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            reinterpret_cast<uint4*>(d)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        }
+      } else if (live) {
+        char* d = slot + slot_at(pr0, col);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) st_global_v8(d + slot_at(0, 8 * k), ov + 8 * k);
+      }
+      __syncwarp();   // (the next load is one instruction of the whole warp)
+    }
+    if (live && half == 0 && sub == 0) {
+      if (u.whole) {
+        if (p.t.lse) p.t.lse[pair] = empty ? NEG_INF : (m_used + log2f(l_row)) * 0.6931471805599453f;
+      } else {
+        reinterpret_cast<float2*>(slot + SLOT_ML)[pr0] = make_float2(m_used, l_row);
+      }
+    }
+    tc_fence_before();   // O has been read: the next part's first P-ready lets it be overwritten
   }
 }
 
@@ -282,22 +577,18 @@ tree_attn_fp4_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   int* abort_flag = reinterpret_cast<int*>(smem + OFF_MISC + 4);
-  int* begun = reinterpret_cast<int*>(smem + OFF_MISC + 8);   // tiles that the keys' first warp has begun, less one
   const uint32_t rank = cluster_ctarank();
   const int worker = blockIdx.x >> 1;
   const Ctx c{smem_addr(smem), abort_flag, p.t.status, p.wait_limit_ns, rank};
   ReqWords words{0, 0, 0};   // (on their way while the barriers are made)
   if ((int)threadIdx.x < p.t.batch) words = load_words(p.t, threadIdx.x);
   if (warp == 1) {
-    // P: every softmax warp of both CTAs; maxima: the two warps of 32 rows; keys and values: four warps of
-    // each CTA; ropes: one.
+    // P: every softmax warp of both CTAs; keys: eight warps of each CTA and the ropes'.
     static_assert(NBAR <= 32, "a lane each");
-    const bool rows = lane == KF || lane == KF + 1 || lane == VF || lane == VF + 1;
-    if (lane < NBAR) mbar_init(c.bar(lane), lane == PR || rows ? 8 : lane == KF + 2 || lane == XB || lane == XB + 1 ? 2 : 1);
-    if (lane == 0) {
-      *abort_flag = 0;
-      *begun = -1;
-    }
+    const bool keys = lane == KF || lane == KF + 1, local = lane == KL || lane == KL + 1, probs = lane == PR || lane == PR + 1;
+    const bool free = lane == KE || lane == KE + 1;
+    if (lane < NBAR) mbar_init(c.bar(lane), keys ? 18 : probs ? 16 : local ? 8 : free ? 3 : 1);
+    if (lane == 0) *abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) tma_prefetch_desc(&tm_q);
@@ -309,26 +600,24 @@ tree_attn_fp4_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   tc_fence_before();
   if (warp == 3) cluster_arrive();   // (see tree_attn_kernel)
   else cluster_arrive_relaxed();
-  find_piece<NTHREADS>(p.t, words, worker, p.workers, blockIdx.x == 0, &start, &count, &join);
+  find_piece<NTHREADS, ROWS, KEYS>(p.t, words, worker, p.workers, blockIdx.x == 0, &start, &count, &join);
   char* ws = static_cast<char*>(p.t.workspace);
   if (threadIdx.x == 0 && rank == 0) reinterpret_cast<JoinRec*>(ws)[worker] = join;
   __syncwarp();
   cluster_wait();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  const Parts parts(p.t, start, count);
+  const PartsK parts(p.t, start, count);
   if (warp < 4) {
-    setmaxnreg_dec<REGS_CTRL>();
     if (warp == 0) run_queries(c, parts, &tm_q);
-    else if (warp == 1 && rank == 0) run_mma<FP4>(c, p, parts, tmem);
-    else if (warp == 2) run_prefetch(c, p, parts, begun);
-    else if (warp == 3) run_ropes(c, p, parts);
-  } else if (warp < 8) {
-    setmaxnreg_inc<REGS_SOFTMAX>();
+    else if (warp == 1 && rank == 0) run_mma(c, p, parts, tmem);
+    else if (warp == 1) run_relay(c, parts);
+    else if (warp == 2) run_copies(c, parts);
+    else run_ropes(c, p, parts);
+  } else if (warp < 12) {
     run_softmax(c, p, parts, tmem, ws + WS_SLOTS + (size_t)worker * 2 * SLOT_BYTES, smem);
   } else {
-    setmaxnreg_dec<REGS_ROWS>();
-    run_rows(c, p, parts, warp >= 12, begun);
+    run_rows(c, p, parts);
   }
   __syncwarp();
   tc_fence_before();
@@ -365,11 +654,6 @@ int max_workers() {
   const cudaError_t e = configured.run([] {
     cudaError_t r = cudaFuncSetAttribute(tree_attn_fp4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (r != cudaSuccess) return r;
-    // The split of the registers takes for granted that every thread starts with LAUNCH_REGS.
-    cudaFuncAttributes attrs;
-    r = cudaFuncGetAttributes(&attrs, tree_attn_fp4_kernel);
-    if (r != cudaSuccess) return r;
-    if (attrs.numRegs != LAUNCH_REGS) return cudaErrorInvalidConfiguration;
     int dev = 0, n = 0;
     r = cudaGetDevice(&dev);
     if (r != cudaSuccess) return r;
