@@ -221,8 +221,8 @@ cudaError_t launch_gather_fp4(const void* cache, int64_t num_blocks, int block_s
 
 // As launch_tree_attention, over 400-byte entries (TreeParams.cache is their address).
 cudaError_t launch_tree_attention_fp4(const TreeParams& p, cudaStream_t stream);
-// Its kernel for units of up to 32 pairs; `pairs`: about how many a request has.
-cudaError_t launch_tree_attention_fp4_few(const TreeParams& p, int pairs, cudaStream_t stream);
+// Its kernel for units of 16 pairs.
+cudaError_t launch_tree_attention_fp4_few(const TreeParams& p, cudaStream_t stream);
 
 // MLA_PLAN_CTA_PAIRS: 1 when "1" (plan prefills on CTA pairs), 0 when "0", -1 otherwise.
 int cta_pair_mode();

@@ -1,8 +1,8 @@
 // Tree attention over a cache of 4-bit entries for few (node, head) pairs a request: a decoding step of one
-// token and up to 16 or 32 heads.
+// token and up to 16 heads.
 //
-// The 128 x 128 products of tree_attn_fp4_kernel make every key bf16 twice, in two CTAs, and are mostly
-// padding when a request has 16 pairs.  Here one CTA has a unit of N = 16 or 32 pairs and the transposed
+// The 128-pair units of tree_attn_fp4_kernel are mostly padding when a request has 16 pairs.  Here one CTA has a unit of
+// N = 16 pairs and the transposed
 // products: with a tile of 64 keys C (64 x 576) made bf16 once in shared memory,
 //   S^T = C Q^T             (M = 64 keys, N pairs, K = 576)
 //   O^T += C[:, :512]^T P^T  (M = 128 columns four times, N pairs, K = 64 keys),
@@ -28,16 +28,15 @@
 namespace mla {
 namespace {
 
-constexpr int KEYS = 64;
+constexpr int N = 16, KEYS = 64;   // pairs of a unit, keys of a tile
 constexpr int NTHREADS = 640;
 constexpr int PANEL = KEYS * 128;        // 64 keys x 64 columns
 constexpr int TILE = 9 * PANEL;
 constexpr int HALF = KEYS / 2 * FP4_ENTRY;   // half a tile's entries
 constexpr uint32_t TMEM_COLS = 256;
 
-template <int N>
 struct Off {
-  static constexpr int SLOTS = N == 16 ? 2 : 1;   // of the ring, a tile's entries each
+  static constexpr int SLOTS = 2;   // of the ring, a tile's entries each
   static constexpr int TILES = 0, Q = 2 * TILE, P = Q + 9 * N * 128, RING = P + 2 * N * 128;
   static constexpr int MAXIMA = RING + SLOTS * KEYS * FP4_ENTRY, SUMS = MAXIMA + 4 * N * 4, BAR = SUMS + 4 * N * 4;
   static constexpr int THERE = BAR + 24 * 8, MISC = THERE + SLOTS * 8, SMEM = MISC + 64 + 1024;
@@ -58,13 +57,12 @@ enum Bar {
 };
 static_assert(NBAR <= 24, "barriers");
 
-template <int N>
 struct Ctx {
   uint32_t sbase;
   volatile int* abort_flag;
   int* status;
   uint64_t wait_limit_ns;
-  __device__ uint32_t bar(int i) const { return sbase + Off<N>::BAR + 8 * i; }
+  __device__ uint32_t bar(int i) const { return sbase + Off::BAR + 8 * i; }
   __device__ bool wait(int b, uint32_t parity) const {
     return mbar_wait_bounded(bar(b), parity, abort_flag, status, MLA_DEVSTAT_TIMEOUT, wait_limit_ns);
   }
@@ -76,12 +74,10 @@ struct Ctx {
     mbar_wait_bounded(bar(b), parity, &dummy, status, MLA_DEVSTAT_TIMEOUT, TREE_DRAIN_LIMIT_NS);
   }
 };
-template <int N>
 using PartsN = PartsOf<N, KEYS>;
 
 // A warp's part of what it writes is there: handed to the products' proxy.
-template <int N>
-__device__ __forceinline__ void tell(const Ctx<N>& c, int b, int lane) {
+__device__ __forceinline__ void tell(const Ctx& c, int b, int lane) {
   fence_async_shared();
   __syncwarp();
   if (lane == 0) mbar_arrive(c.bar(b));
@@ -106,12 +102,11 @@ __device__ __forceinline__ uint32_t ld_shared_u8(uint32_t a) {
 // Warp 0: half a tile's entries at a time, in runs of rows that lie side by side (`run`: as many of 32 as the
 // block size is a multiple of, 8 at least, or 1), a lane a row.  Where the ring holds one tile only, the next one's
 // entries are brought into L2 meanwhile.
-template <int N>
-__device__ void run_copies(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts, uint8_t* smem) {
-  constexpr int SLOTS = Off<N>::SLOTS;
+__device__ void run_copies(const Ctx& c, const TreeLaunch& p, PartsN parts, uint8_t* smem) {
+  constexpr int SLOTS = Off::SLOTS;
   const int lane = threadIdx.x & 31, bs = p.t.block_size;
   const int run = bs % 32 == 0 ? 32 : bs % 16 == 0 ? 16 : bs % 8 == 0 ? 8 : 1;
-  volatile uint32_t* there = reinterpret_cast<volatile uint32_t*>(smem + Off<N>::THERE);   // which rows exist
+  volatile uint32_t* there = reinterpret_cast<volatile uint32_t*>(smem + Off::THERE);   // which rows exist
   const uint8_t* cache = reinterpret_cast<const uint8_t*>(p.t.cache);
   uint32_t put = 0;
   bool ok = true;
@@ -138,7 +133,7 @@ __device__ void run_copies(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts
           asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(cache + (int64_t)later * FP4_ENTRY), "r"(FP4_ENTRY) : "memory");
       }
       const uint32_t have = __ballot_sync(0xffffffffu, row != p.oob_row);
-      const uint32_t g = put >> 1, slot = g % SLOTS, half = 2 * slot + (put & 1), dst = c.sbase + Off<N>::RING + half * HALF;
+      const uint32_t g = put >> 1, slot = g % SLOTS, half = 2 * slot + (put & 1), dst = c.sbase + Off::RING + half * HALF;
       if ((put & 1) == 0 && g >= SLOTS && !c.wait_warp(EE + slot, (g / SLOTS - 1) & 1)) {
         ok = false;
         break;
@@ -167,19 +162,18 @@ __device__ void run_copies(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts
 // bank groups.  And 16 bytes of two ropes, lane (row % 4, piece) = (l / 8, l % 8).
 // The loop is kept short: with a tile's loads in registers a tile ahead, its code took three times as long beside
 // the other warps' (it does not stay in the instruction cache).
-template <int N>
-__device__ void run_rows(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts, uint8_t* smem) {
-  constexpr int SLOTS = Off<N>::SLOTS;
+__device__ void run_rows(const Ctx& c, const TreeLaunch& p, PartsN parts, uint8_t* smem) {
+  constexpr int SLOTS = Off::SLOTS;
   const int lane = threadIdx.x & 31, w8 = (threadIdx.x >> 5) - 12, r4 = (lane >> 1) & 3, rr = lane >> 3;
   const int group = 2 * (lane >> 3) + (lane & 1);   // of a half's eight
   uint32_t at[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    at[i] = c.sbase + Off<N>::TILES + (lane >> 3) * PANEL + (8 * w8 + r4) * 128 + (((4 * (lane & 1) + i) ^ r4) << 4);
-  const uint32_t rope_at = c.sbase + Off<N>::TILES + 8 * PANEL + (8 * w8 + rr) * 128 + (((lane & 7) ^ rr) << 4);
-  const uint32_t from = c.sbase + Off<N>::RING + (8 * w8 + r4) * FP4_ENTRY;
-  const uint32_t rope_from = c.sbase + Off<N>::RING + (8 * w8 + rr) * FP4_ENTRY + FP4_ROPE + (lane & 7) * 16;
-  const volatile uint8_t* there = smem + Off<N>::THERE + w8;   // which of the warp's rows exist
+    at[i] = c.sbase + Off::TILES + (lane >> 3) * PANEL + (8 * w8 + r4) * 128 + (((4 * (lane & 1) + i) ^ r4) << 4);
+  const uint32_t rope_at = c.sbase + Off::TILES + 8 * PANEL + (8 * w8 + rr) * 128 + (((lane & 7) ^ rr) << 4);
+  const uint32_t from = c.sbase + Off::RING + (8 * w8 + r4) * FP4_ENTRY;
+  const uint32_t rope_from = c.sbase + Off::RING + (8 * w8 + rr) * FP4_ENTRY + FP4_ROPE + (lane & 7) * 16;
+  const volatile uint8_t* there = smem + Off::THERE + w8;   // which of the warp's rows exist
   int g = 0;
   bool ok = true;
   Part u;
@@ -266,8 +260,7 @@ __device__ void run_rows(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts, 
 }
 
 // Warp 3: Q of each part.
-template <int N>
-__device__ void run_queries(const Ctx<N>& c, PartsN<N> parts, const CUtensorMap* tq) {
+__device__ void run_queries(const Ctx& c, PartsN parts, const CUtensorMap* tq) {
   const int lane = threadIdx.x & 31;
   int units = 0;
   bool ok = true;
@@ -277,7 +270,7 @@ __device__ void run_queries(const Ctx<N>& c, PartsN<N> parts, const CUtensorMap*
       if (units > 0) ok = c.wait(QE, (units - 1) & 1);
       if (ok) {
         mbar_arrive_expect_tx(c.bar(QF), 9 * N * 128);
-        tma_load_3d(c.sbase + Off<N>::Q, tq, c.bar(QF), 0, (int32_t)u.pair0, 0);
+        tma_load_3d(c.sbase + Off::Q, tq, c.bar(QF), 0, (int32_t)u.pair0, 0);
       }
     }
     ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -306,11 +299,10 @@ __device__ __forceinline__ void commit(uint32_t bar) {
       : "memory");
 }
 
-template <int N>
-__device__ void run_scores(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts, uint32_t tmem) {
+__device__ void run_scores(const Ctx& c, const TreeLaunch& p, PartsN parts, uint32_t tmem) {
   constexpr uint32_t IDESC = idesc_bf16_f32(KEYS, N, false, false);
-  const uint64_t k_desc = sdesc_sw128(c.sbase + Off<N>::TILES, 16, 1024);
-  const uint64_t q_desc = sdesc_sw128(c.sbase + Off<N>::Q, 16, 1024);
+  const uint64_t k_desc = sdesc_sw128(c.sbase + Off::TILES, 16, 1024);
+  const uint64_t q_desc = sdesc_sw128(c.sbase + Off::Q, 16, 1024);
   bool ok = true;
   if (p.force_timeout) ok = c.wait_warp(NEVER, 0);
   int g = 0, units = 0;
@@ -346,11 +338,10 @@ __device__ void run_scores(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts
   __syncwarp();
 }
 
-template <int N>
-__device__ void run_values(const Ctx<N>& c, PartsN<N> parts, uint32_t tmem) {
+__device__ void run_values(const Ctx& c, PartsN parts, uint32_t tmem) {
   constexpr uint32_t IDESC = idesc_bf16_f32(128, N, true, false);
-  const uint64_t v_desc = sdesc_sw128(c.sbase + Off<N>::TILES, PANEL, 1024);
-  const uint64_t p_desc = sdesc_sw128(c.sbase + Off<N>::P, 16, 1024);
+  const uint64_t v_desc = sdesc_sw128(c.sbase + Off::TILES, PANEL, 1024);
+  const uint64_t p_desc = sdesc_sw128(c.sbase + Off::P, 16, 1024);
   bool ok = true;
   int g = 0;
   Part u;
@@ -379,16 +370,6 @@ __device__ void run_values(const Ctx<N>& c, PartsN<N> parts, uint32_t tmem) {
 }
 
 // ------------------------------------------------------------------ softmax (warps 4-11)
-template <int W>
-__device__ __forceinline__ void tmem_load(uint32_t at, float* x) {
-  if constexpr (W == 16) tmem_ld16_sync(at, reinterpret_cast<uint32_t*>(x));
-  else tmem_ld8_sync(at, reinterpret_cast<uint32_t*>(x));
-}
-template <int W>
-__device__ __forceinline__ void tmem_store(uint32_t at, const float* x) {
-  if constexpr (W == 16) tmem_st16_sync(at, reinterpret_cast<const uint32_t*>(x));
-  else tmem_st8_sync(at, reinterpret_cast<const uint32_t*>(x));
-}
 __device__ __forceinline__ float warp_max(float x) {   // (passes over a NaN)
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
@@ -405,8 +386,7 @@ __device__ __forceinline__ float capped(const TreeLaunch& p, float x) {
 
 // Half the pairs for each four warps.  These meet at barriers, which have no time limit, so where a wait gave up
 // they go through the rest of their tiles without waiting: nobody is left alone at one.
-template <int N>
-__device__ void run_softmax(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> parts, uint32_t tmem, char* ws_slots, uint8_t* smem) {
+__device__ void run_softmax(const Ctx& c, const TreeLaunch& p, PartsN parts, uint32_t tmem, char* ws_slots, uint8_t* smem) {
   constexpr int W = N / 2;   // pairs of a warp
   const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3, side = (threadIdx.x >> 7) - 1, i0 = side * W;
   const int barrier = 1 + side;
@@ -414,9 +394,9 @@ __device__ void run_softmax(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> part
   const bool mine = lane < 16;
   const int row = 16 * q4 + (lane & 15);
   const uint32_t lane_addr = tmem + ((uint32_t)(q4 * 32) << 16) + i0;
-  volatile float* maxima = reinterpret_cast<volatile float*>(smem + Off<N>::MAXIMA) + i0;
-  volatile float* sums = reinterpret_cast<volatile float*>(smem + Off<N>::SUMS) + i0;
-  const uint32_t p_at = c.sbase + Off<N>::P + i0 * 128 + (row & 7) * 2;
+  volatile float* maxima = reinterpret_cast<volatile float*>(smem + Off::MAXIMA) + i0;
+  volatile float* sums = reinterpret_cast<volatile float*>(smem + Off::SUMS) + i0;
+  const uint32_t p_at = c.sbase + Off::P + i0 * 128 + (row & 7) * 2;
   const float NEG_INF = -__int_as_float(0x7f800000);
   const float sc = p.has_cap ? 1.f : p.scale_log2;
   bool ok = true;
@@ -438,7 +418,7 @@ __device__ void run_softmax(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> part
       if (meet<128>(barrier, !ok)) ok = false;
       tc_fence_after();
       float s[W];
-      tmem_load<W>(lane_addr + 4 * N + b * N, s);
+      tmem_ld8_sync(lane_addr + 4 * N + b * N, reinterpret_cast<uint32_t*>(s));
       if (p.has_cap) {
 #pragma unroll
         for (int i = 0; i < W; ++i) s[i] = capped(p, s[i]);
@@ -488,10 +468,10 @@ __device__ void run_softmax(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> part
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
             float o[W];
-            tmem_load<W>(lane_addr + q * N, o);
+            tmem_ld8_sync(lane_addr + q * N, reinterpret_cast<uint32_t*>(o));
 #pragma unroll
             for (int i = 0; i < W; ++i) o[i] *= alpha[i];
-            tmem_store<W>(lane_addr + q * N, o);
+            tmem_st8_sync(lane_addr + q * N, reinterpret_cast<const uint32_t*>(o));
           }
         }
       }
@@ -538,7 +518,7 @@ __device__ void run_softmax(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> part
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
       float o[W];
-      tmem_load<W>(lane_addr + q * N, o);
+      tmem_ld8_sync(lane_addr + q * N, reinterpret_cast<uint32_t*>(o));
       const int col = 128 * q + 32 * q4 + lane;
 #pragma unroll
       for (int i = 0; i < W; ++i) {
@@ -553,7 +533,6 @@ __device__ void run_softmax(const Ctx<N>& c, const TreeLaunch& p, PartsN<N> part
   }
 }
 
-template <int N>
 __global__ void __launch_bounds__(NTHREADS, 1)
 tree_attn_fp4_few_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ TreeLaunch p) {
   extern __shared__ uint8_t smem_raw[];
@@ -562,10 +541,10 @@ tree_attn_fp4_few_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
   __shared__ JoinRec join;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Off<N>::MISC);
-  int* abort_flag = reinterpret_cast<int*>(smem + Off<N>::MISC + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Off::MISC);
+  int* abort_flag = reinterpret_cast<int*>(smem + Off::MISC + 4);
   const int worker = blockIdx.x;
-  const Ctx<N> c{smem_addr(smem), abort_flag, p.t.status, p.wait_limit_ns};
+  const Ctx c{smem_addr(smem), abort_flag, p.t.status, p.wait_limit_ns};
   ReqWords words{0, 0, 0};   // (on their way while the barriers are made)
   if ((int)threadIdx.x < p.t.batch) words = load_words(p.t, threadIdx.x);
   if (warp == 1) {
@@ -588,16 +567,16 @@ tree_attn_fp4_few_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
   if (threadIdx.x == 0) reinterpret_cast<JoinRec*>(ws)[worker] = join;
   __syncwarp();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  const PartsN<N> parts(p.t, start, count);
+  const PartsN parts(p.t, start, count);
   if (warp < 4) {
-    if (warp == 0) run_copies<N>(c, p, parts, smem);
-    else if (warp == 1) run_scores<N>(c, p, parts, tmem);
-    else if (warp == 2) run_values<N>(c, parts, tmem);
-    else run_queries<N>(c, parts, &tm_q);
+    if (warp == 0) run_copies(c, p, parts, smem);
+    else if (warp == 1) run_scores(c, p, parts, tmem);
+    else if (warp == 2) run_values(c, parts, tmem);
+    else run_queries(c, parts, &tm_q);
   } else if (warp < 12) {
-    run_softmax<N>(c, p, parts, tmem, ws + WS_SLOTS + (size_t)worker * 2 * few_slot_bytes(N), smem);
+    run_softmax(c, p, parts, tmem, ws + WS_SLOTS + (size_t)worker * 2 * few_slot_bytes(N), smem);
   } else {
-    run_rows<N>(c, p, parts, smem);
+    run_rows(c, p, parts, smem);
   }
   __syncwarp();
   tc_fence_before();
@@ -610,12 +589,11 @@ tree_attn_fp4_few_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
 }
 
 // CTAs that run at once on the current device (0 on error), no more than the workspace has room for.
-template <int N>
 int max_workers() {
   static PerDeviceOnce configured;
   static int workers[PerDeviceOnce::kMaxDevices] = {};
   const cudaError_t e = configured.run([] {
-    cudaError_t r = cudaFuncSetAttribute(tree_attn_fp4_few_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Off<N>::SMEM);
+    cudaError_t r = cudaFuncSetAttribute(tree_attn_fp4_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Off::SMEM);
     if (r != cudaSuccess) return r;
     int dev = 0;
     r = cudaGetDevice(&dev);
@@ -629,23 +607,22 @@ int max_workers() {
   return workers[dev];
 }
 
-template <int N>
-cudaError_t launch(const TreeParams& t, cudaStream_t stream) {
-  const TreeLaunch p = tree_launch(t, max_workers<N>());
+}  // namespace
+
+cudaError_t launch_tree_attention_fp4_few(const TreeParams& t, cudaStream_t stream) {
+  const TreeLaunch p = tree_launch(t, max_workers());
   if (p.workers <= 0) return cudaErrorInvalidConfiguration;
   CUtensorMap tq;
   const uint64_t dims[3] = {64, (uint64_t)t.total_rows * (uint64_t)t.num_heads, 9}, strides[2] = {576 * 2, 64 * 2};
   const uint32_t box[3] = {64, N, 9};   // N rows, panel by panel
   if (make_tensor_map_bf16(&tq, t.q, 3, dims, strides, box) != MLA_OK) return cudaErrorInvalidValue;
-  tree_attn_fp4_few_kernel<N><<<p.workers, NTHREADS, Off<N>::SMEM, stream>>>(tq, p);
-  const cudaError_t e = cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.workers);
+  cfg.blockDim = dim3(NTHREADS);
+  cfg.dynamicSmemBytes = Off::SMEM;
+  cfg.stream = stream;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_attn_fp4_few_kernel, tq, p);
   return e != cudaSuccess ? e : launch_tree_join_few(p, N, stream);
-}
-
-}  // namespace
-
-cudaError_t launch_tree_attention_fp4_few(const TreeParams& t, int pairs, cudaStream_t stream) {
-  return pairs <= 16 ? launch<16>(t, stream) : launch<32>(t, stream);
 }
 
 }  // namespace mla
