@@ -6,7 +6,7 @@
 // value too: its columns 0-255 are values of the even CTA and 256-511 of the odd one, in the swizzle that they have as
 // keys, so that bulk copies take them there from shared memory to shared memory.  (Both made from the entries, as keys by
 // four warps and as values by four more: twice the conversions; 32 x 16 over 8192 at 128 heads 1545 us, 9 x up to
-// 37 nodes at 16 heads 54 us; copied: 1493 and 48.)  Entries go straight from L2 to registers: there is no room for them
+// 37 nodes at 16 heads 54 us, against 1468 and 48.)  Entries go straight from L2 to registers: there is no room for them
 // in shared memory beside Q (72 KB), two tiles (136 KB) and P (16 KB).
 //   warp 0      Q producer
 //   warp 1      even CTA: issues every product; odd CTA: tells that its copies landed
@@ -15,9 +15,12 @@
 //   warps 4-11  softmax: four threads per pair (quarters of the keys and of O's columns)
 //   warps 12-19 keys
 // A tile has 64 keys, so that there are two: with one of 128 its making, S, P V and the copies took turns (2207 us).
-// A product of 64 keys takes as long as one of 128 (30 clocks: Q's rows are read from shared memory for each), which
-// makes 1600 clocks of products a tile; a tile takes 3300, of which the warps that make keys work 2600: what they wait
-// for is shared memory's queue, behind 264 KB a tile that products and copies take from it.
+// Either S of the next tile or P V of this one is issued, whichever has its operands first (S always first: 1481 us).
+// What bounds it (32 x 16 over 8192 at 128 heads, 1468 us in replayed graphs, 0.43 of the measured tensor rate): a tile takes
+// 3100 clocks, of which the products take 1850 (a product of 64 keys takes as long as one of 128, 30 clocks: Q's rows are
+// read from shared memory for each) and wait 1200 for their operands: keys wait for the copies out of their buffer, which
+// wait for the P V of the tile before last.  No unit is busy more than half of the time; another two tiles would have
+// to fit into shared memory.  Twice the warps that make keys: 1425 us, but 49.8 us instead of 48.2 for 9 x up to 37 nodes.
 // A code becomes bf16 by moving its bits to a bf16's low exponent bits and one product by 2^126 times the
 // scale, exact; scales above 2, where that factor has no bf16, take two products (a tile in which a warp
 // meets one).  A row with a scale byte above 252 has NaN in its rope, which only S sees, and zeros for values,
@@ -83,6 +86,22 @@ struct Ctx {
   }
   __device__ bool wait_warp(int b, uint32_t parity) const {
     return mla::wait_warp(bar(b), parity, abort_flag, status, wait_limit_ns);
+  }
+  // Whether a phase is complete: one lane looks, all see what it acquired.
+  __device__ bool look(int b, uint32_t parity) const {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, 0, 0;\n\t"
+        "@e mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(r)
+        : "r"(bar(b)), "r"(parity)
+        : "memory");
+    const bool yes = __any_sync(0xffffffffu, r != 0);
+    __syncwarp();
+    return yes;
   }
   __device__ void drain(int b, uint32_t parity) const {
     int dummy = 0;
@@ -363,7 +382,6 @@ __device__ void run_mma(const Ctx& c, const TreeLaunch& p, PartsK parts, uint32_
   auto s_products = [&](bool last) {
     const int b = st & 1;
     const uint32_t d = __shfl_sync(0xffffffffu, tmem + TM_S(b), 0), tile = __shfl_sync(0xffffffffu, (uint32_t)(b * K_TILE) >> 4, 0);
-    if (!c.wait_warp(KF + b, (st >> 1) & 1)) return false;
     tc_fence_after();
 #pragma unroll 1
     for (int i = 0; i < NP; ++i) {
@@ -376,13 +394,11 @@ __device__ void run_mma(const Ctx& c, const TreeLaunch& p, PartsK parts, uint32_
     commit_both(c.bar(SF + b));
     if (last) commit_both(c.bar(QE));
     ++st;
-    return true;
   };
   auto pv_products = [&](uint32_t add) {
     const int b = pv & 1;
     const uint32_t more = __shfl_sync(0xffffffffu, add, 0);
     const uint32_t tile = __shfl_sync(0xffffffffu, (uint32_t)(b * V_TILE) >> 4, 0), pt = __shfl_sync(0xffffffffu, (uint32_t)(b * QP) >> 4, 0);
-    if (!c.wait_warp(PR + b, (pv >> 1) & 1) || !c.wait_warp(VF + b, (pv >> 1) & 1) || !c.wait_warp(VR + b, (pv >> 1) & 1)) return false;
     tc_fence_after();
 #pragma unroll 1
     for (int ch = 0; ch < 2; ++ch) {
@@ -393,19 +409,36 @@ __device__ void run_mma(const Ctx& c, const TreeLaunch& p, PartsK parts, uint32_
     }
     commit_both(c.bar(VE + b));
     ++pv;
-    return true;
   };
   Part u;
   while (ok && parts.next(&u)) {
     const int n = __shfl_sync(0xffffffffu, u.hi - u.lo, 0);
     ok = c.wait_warp(QF, units & 1);
     ++units;
-    for (int t = 0; t < n && ok; ++t) {
-      // S's buffer held the scores of the tile before last, read before that tile's P was ready: its P V is behind us.
-      ok = s_products(t == n - 1);
-      if (ok && t > 0) ok = pv_products(t > 1 ? 1u : 0u);
+    // S's buffer holds the scores of the tile before last, read before that tile's P was ready: its P V has to be behind.
+    const int s_end = st + n, pv_begin = pv;
+    uint64_t since = 0;
+    for (uint32_t it = 0; ok && pv < s_end; ++it) {
+      const int bp = pv & 1, bs = st & 1;
+      if (pv < st && c.look(PR + bp, (pv >> 1) & 1) && c.look(VF + bp, (pv >> 1) & 1) && c.look(VR + bp, (pv >> 1) & 1)) {
+        pv_products(pv > pv_begin ? 1u : 0u);
+        it = 0;
+      } else if (st < s_end && st - pv < 2 && c.look(KF + bs, (st >> 1) & 1)) {
+        s_products(st == s_end - 1);
+        it = 0;
+      } else if ((it & 63) == 63) {
+        const uint64_t now = global_timer_ns();
+        if (it == 63) since = now;
+        const bool late = now - since > c.wait_limit_ns;
+        if (__any_sync(0xffffffffu, late || *c.abort_flag)) {
+          if (late) {
+            *c.abort_flag = 1;
+            if (c.status) atomicOr(c.status, MLA_DEVSTAT_TIMEOUT);
+          }
+          ok = false;
+        }
+      }
     }
-    if (ok) ok = pv_products(n > 1 ? 1u : 0u);
   }
   commit_both(c.bar(FIN));
   c.drain(FIN, 0);

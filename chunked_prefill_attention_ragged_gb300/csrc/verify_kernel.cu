@@ -18,8 +18,8 @@
 // sums over the vocabulary, and the search in them, are shared out.  A warp sums 512 entries at a time and
 // leaves each such sum in shared memory, so that the search looks at the sums and one group of entries.
 // What bounds it: for few requests latencies, one behind the other (the nodes, the row's slice, the cluster's
-// sum, the group); for many the reading of the last nodes' rows.  (Replayed graphs: 1 request of 5 given nodes over 129,280
-// entries 8.5 us; 64 of 16 drawn ones 28.5 us, of which the rows that are read, 67 MB, take 10 at a copy's rate: a node's
+// sum, the group); for many the reading of the last nodes' rows.  (Replayed graphs: 1 request of 5 given nodes over 32,003
+// entries 8.5 us; 64 of up to 16 drawn ones over 131,072 28.5 us, of which the rows that are read, 67 MB, take 10 at a copy's rate: a node's
 // refusals are one pass over its rows each, and the next pass starts from the last one's sum.)
 #include <cuda_bf16.h>
 
