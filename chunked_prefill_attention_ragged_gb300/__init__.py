@@ -15,14 +15,14 @@ from ._binding import (EXPORTED, AbsorbedPlan, MlaError, PrefillPlan, error_stri
                        mla_prefill_plan, mla_prefill_run, mla_prefill_run_merge, mla_prefill_run_noalloc,
                        mla_prefill_run_shared_rope, mla_prefill_status, mla_tree_attention,
                        mla_tree_attention_fp4, mla_tree_commit,
-                       mla_tree_mask, mla_tree_verify, mla_tree_workspace, mla_up_proj, mla_up_proj_paged,
-                       mla_up_proj_paged_split)
+                       mla_tree_mask, mla_tree_verify, mla_tree_workspace, mla_tree_workspace_fp4, mla_up_proj,
+                       mla_up_proj_paged, mla_up_proj_paged_split)
 
 __all__ = [
     "EXPORTED", "AbsorbedPlan", "MlaError", "PrefillPlan", "error_string", "library", "library_path",
     "mla_absorbed_plan", "mla_absorbed_run", "mla_block_table_update",
     "mla_tree_attention", "mla_tree_attention_fp4", "mla_tree_commit", "mla_tree_mask", "mla_tree_verify",
-    "mla_tree_workspace",
+    "mla_tree_workspace", "mla_tree_workspace_fp4",
     "mla_cache_append", "mla_cache_write", "mla_gather_latent", "mla_gather_latent_fp4", "mla_gather_latent_fp8", "mla_merge_state", "mla_plan_destroy", "mla_plan_units_host",
     "mla_prefill_plan", "mla_prefill_run", "mla_prefill_run_merge", "mla_prefill_run_noalloc", "mla_prefill_status",
     "mla_up_proj",

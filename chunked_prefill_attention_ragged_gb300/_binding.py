@@ -57,6 +57,7 @@ _SIGNATURES = {
                                         _c_vp, _c_vp, _c_vp, _c_i64, _c_vp, _c_vp]),
     "mla_tree_mask": (_c_int, [_c_vp, _c_vp, _c_vp, _c_int, _c_i64, _c_int, _c_vp, _c_vp, _c_vp, _c_vp]),
     "mla_tree_workspace": (_c_int, [_c_i64, _c_int, _i64p]),
+    "mla_tree_workspace_fp4": (_c_int, [_c_i64, _c_int, _c_int, _c_i64, _c_int, _i64p]),
     "mla_tree_attention": (_c_int, [_c_vp, _c_vp, _c_i64, _c_int, _c_vp, _c_int, _c_vp, _c_vp, _c_vp, _c_int, _c_int,
                                     _c_i64, _c_int, _c_f, _c_f, _c_vp, _c_vp, _c_vp, _c_i64, _c_vp, _c_vp]),
     "mla_tree_attention_fp4": (_c_int, [_c_vp, _c_vp, _c_i64, _c_int, _c_vp, _c_int, _c_vp, _c_vp, _c_vp, _c_int, _c_int,
@@ -689,6 +690,15 @@ def mla_tree_workspace(total_rows: int, num_heads: int) -> int:
     return int(n.value)
 
 
+def mla_tree_workspace_fp4(total_rows: int, num_heads: int, batch: int, num_blocks: int, block_size: int) -> int:
+    """Bytes of workspace with which mla_tree_attention_fp4 is fastest on the current device (it does
+    with those of mla_tree_workspace): with many pairs a request, room for the cache's rows in bf16."""
+    n = ctypes.c_int64()
+    _check((_lib or library()).mla_tree_workspace_fp4(int(total_rows), int(num_heads), int(batch), int(num_blocks),
+                                                      int(block_size), ctypes.byref(n)), "mla_tree_workspace_fp4")
+    return n.value
+
+
 def _tree_attention(name, kind, width, q_abs, cache, block_table, qo_indptr, kv_lens, tree_mask, sm_scale,
                     logits_soft_cap, o, lse, return_lse, workspace, status, stream):
     T, dev, st, handle = _here(stream, q_abs, "q_abs")
@@ -713,6 +723,8 @@ def _tree_attention(name, kind, width, q_abs, cache, block_table, qo_indptr, kv_
         n = _workspace_bytes.get(dev)
         if n is None:
             n = _workspace_bytes[dev] = mla_tree_workspace(t, h)
+        if kind == "uint8" and t * h > 128 * b:   # (for fewer pairs it is the same)
+            n = mla_tree_workspace_fp4(t, h, b, cache.shape[0], cache.shape[1])
         workspace = _new(T, (n,), uint8, device, st)
     _check(getattr(_lib or library(), name)(
         _arg(q_abs, bfloat16, dev, "q_abs"), _arg(cache, getattr(T, kind), dev, "cache"), cache.shape[0], cache.shape[1],
@@ -739,7 +751,9 @@ def mla_tree_attention(q_abs, cache, block_table, qo_indptr, kv_lens, tree_mask=
 def mla_tree_attention_fp4(q_abs, cache, block_table, qo_indptr, kv_lens, tree_mask=None, *, sm_scale: float,
                            logits_soft_cap: float = 0.0, o=None, lse=None, return_lse: bool = True, workspace=None,
                            status=None, stream=None):
-    """mla_tree_attention over a cache of 4-bit entries, uint8 [NB, BS, 400]; the rest as there."""
+    """mla_tree_attention over a cache of 4-bit entries, uint8 [NB, BS, 400]; the rest as there.  With many
+    pairs a request the workspace that is allocated has room for the cache's rows in bf16 (see
+    mla_tree_workspace_fp4); one of mla_tree_workspace bytes may be given instead."""
     return _tree_attention("mla_tree_attention_fp4", "uint8", 400, q_abs, cache, block_table, qo_indptr, kv_lens,
                            tree_mask, sm_scale, logits_soft_cap, o, lse, return_lse, workspace, status, stream)
 

@@ -44,6 +44,7 @@ SOURCES = [
     "fp4_gather_kernel.cu",
     "tree_attn_fp4_kernel.cu",
     "tree_attn_fp4_few_kernel.cu",
+    "tree_expand_kernel.cu",
 ]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

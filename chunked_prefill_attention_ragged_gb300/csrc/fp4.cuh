@@ -16,6 +16,9 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// Bytes of a word of scales above that (in their top bits).
+__device__ __forceinline__ uint32_t above252(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x03030303u) & w & 0x80808080u; }
+
 // bf16 of a scale byte, 2^(b - 127), in both halves: b is a bf16's exponent field; 0 stands for the
 // subnormal 2^-127, 255 for NaN.
 __device__ __forceinline__ uint32_t scale_bf16x2(uint32_t b) {

@@ -156,6 +156,7 @@ struct TreeParams {
   __nv_bfloat16* o;                     // [total_rows, H, 512]
   float* lse;                           // [total_rows, H] or null
   void* workspace;
+  int64_t workspace_bytes;
   int32_t* status;
 };
 int64_t tree_workspace_bytes();         // on the current device; 0 on error
@@ -221,6 +222,9 @@ cudaError_t launch_gather_fp4(const void* cache, int64_t num_blocks, int block_s
 
 // As launch_tree_attention, over 400-byte entries (TreeParams.cache is their address).
 cudaError_t launch_tree_attention_fp4(const TreeParams& p, cudaStream_t stream);
+// Bytes of workspace with which it may make the cached rows bf16 first (where that pays; else what any call needs).
+int64_t tree_workspace_fp4_bytes(int64_t total_rows, int num_heads, int batch, int64_t num_blocks, int block_size);
+cudaError_t launch_tree_expand(const TreeParams& p, void* rows, cudaStream_t stream);
 // Its kernel for units of 16 pairs.
 cudaError_t launch_tree_attention_fp4_few(const TreeParams& p, cudaStream_t stream);
 

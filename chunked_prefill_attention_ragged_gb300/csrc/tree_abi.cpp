@@ -60,6 +60,7 @@ int tree_attention(const void* q_abs, const void* cache, int64_t num_blocks, int
   p.o = static_cast<__nv_bfloat16*>(o_lat);
   p.lse = lse;
   p.workspace = workspace;
+  p.workspace_bytes = workspace_bytes;
   p.status = status;
   return done(launch(p, as_stream(stream)));
 }
@@ -129,6 +130,19 @@ int mla_tree_workspace(int64_t total_rows, int num_heads, int64_t* bytes) {
   if (!bytes || total_rows < 0 || num_heads < 1 || num_heads > 65535) return MLA_ERR_INVALID_ARG;
   if (total_rows > kMaxTreePairs || total_rows * num_heads > kMaxTreePairs) return MLA_ERR_UNSUPPORTED;
   const int64_t n = tree_workspace_bytes();
+  if (n <= 0) return MLA_ERR_CUDA;
+  *bytes = n;
+  return MLA_OK;
+}
+
+int mla_tree_workspace_fp4(int64_t total_rows, int num_heads, int batch, int64_t num_blocks, int block_size,
+                           int64_t* bytes) {
+  if (!bytes || total_rows < 0 || num_heads < 1 || num_heads > 65535 || batch < 0 || num_blocks < 0 || block_size < 1)
+    return MLA_ERR_INVALID_ARG;
+  if (total_rows > kMaxTreePairs || total_rows * num_heads > kMaxTreePairs || num_blocks > 0x7fffffff ||
+      num_blocks * (int64_t)block_size >= 0x7fffffff)
+    return MLA_ERR_UNSUPPORTED;
+  const int64_t n = tree_workspace_fp4_bytes(total_rows, num_heads, batch, num_blocks, block_size);
   if (n <= 0) return MLA_ERR_CUDA;
   *bytes = n;
   return MLA_OK;

@@ -128,8 +128,6 @@ __device__ __forceinline__ uint32_t load1_if(bool there, const uint8_t* p) {
       : "l"(p), "r"((uint32_t)there));
   return v;
 }
-// Bytes of a word above 252 (in their top bits).
-__device__ __forceinline__ uint32_t above252(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x03030303u) & w & 0x80808080u; }
 
 // A warp's part of what it writes is there: handed to the asynchronous proxy, told to the even CTA.
 __device__ __forceinline__ void tell(const Ctx& c, int b, int lane) {
@@ -703,14 +701,38 @@ int max_workers() {
   return workers[dev];
 }
 
+int64_t pairs_of_a_request(int64_t total_rows, int num_heads, int batch) {   // on average
+  return (total_rows * num_heads + batch - 1) / std::max(batch, 1);
+}
+// Where the bf16 rows are, in a workspace that has room for them.
+int64_t expanded_at() { return (tree_workspace_bytes() + 1023) & ~int64_t(1023); }
 }  // namespace
 
+// From 384 pairs a request on, three units and more read each row, and making them bf16 once, for the kernel over bf16
+// caches, is faster than making each unit's keys again.  (Replayed graphs, without and with: 64 x 3 over 2048 at 128
+// heads 164 us and EX1, 32 x 4 over 8192 386 and EX2, 32 x 16 over 8192 1469 and EX3, 1 x 16 over 8192 65 and EX4; 32 x 2
+// over 8192, 256 pairs: 203 and 209.)  It takes 1152 bytes for each slot of the cache: above 4 GB of them it is left.
+constexpr int64_t EXPAND_PAIRS = 384, EXPAND_BYTES = int64_t(4) << 30;
+int64_t tree_workspace_fp4_bytes(int64_t total_rows, int num_heads, int batch, int64_t num_blocks, int block_size) {
+  const int64_t rows = num_blocks * block_size * (576 * 2), base = tree_workspace_bytes();
+  const bool pays = batch > 0 && batch <= 65535 &&
+                    pairs_of_a_request(total_rows, num_heads, batch) >= EXPAND_PAIRS && rows > 0 && rows <= EXPAND_BYTES;
+  return base > 0 && pays ? expanded_at() + rows : base;
+}
+
 cudaError_t launch_tree_attention_fp4(const TreeParams& t, cudaStream_t stream) {
+  const int64_t with_rows = tree_workspace_fp4_bytes(t.total_rows, t.num_heads, t.batch, t.num_blocks, t.block_size);
+  if (with_rows > tree_workspace_bytes() && t.workspace_bytes >= with_rows && t.max_blocks > 0) {
+    TreeParams expanded = t;
+    void* rows = static_cast<char*>(t.workspace) + expanded_at();
+    expanded.cache = static_cast<const __nv_bfloat16*>(rows);
+    const cudaError_t e = launch_tree_expand(t, rows, stream);
+    return e != cudaSuccess ? e : launch_tree_attention(expanded, stream);
+  }
   // Requests of up to 16 pairs, on average, have units of 16.  (Replayed graphs, this kernel and that one: 64 x 1 over
   // 8192 at 16 heads 200 and 110 us, 1 x 1 over 700 15.4 and 16.4, over 8192 40 and 19; 16 x 1 over 700 20 and 22.5;
   // units of 32 for 64 x 1 over 8192 at 32 heads: 202 and 197, 8 x 1 over 20000 73 and 77, 1 x 1 over 700 15 and 25.)
-  const int64_t pairs = (t.total_rows * t.num_heads + t.batch - 1) / t.batch;
-  if (pairs <= 16) return launch_tree_attention_fp4_few(t, stream);
+  if (pairs_of_a_request(t.total_rows, t.num_heads, t.batch) <= 16) return launch_tree_attention_fp4_few(t, stream);
   const TreeLaunch p = tree_launch(t, max_workers());
   if (p.workers <= 0) return cudaErrorInvalidConfiguration;
   CUtensorMap tq;

@@ -1,4 +1,6 @@
 """Refusals of the 4-bit cache's, the append's and the verification's entry points, without a GPU."""
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -87,6 +89,20 @@ def verify(**kw):
 ])
 def test_verify_refuses(kw, rc):
     assert verify(**kw) == rc
+
+
+@pytest.mark.parametrize("kw,rc", [
+    (dict(rows=-1), -1), (dict(heads=0), -1), (dict(heads=65536), -1), (dict(batch=-1), -1), (dict(nb=-1), -1), (dict(bs=0), -1),
+    (dict(rows=1 << 40), -3), (dict(nb=1 << 31), -3), (dict(nb=1 << 26, bs=64), -3),
+])
+def test_workspace_refuses(kw, rc):
+    a = dict(rows=96, heads=128, batch=4, nb=10, bs=64)
+    a.update(kw)
+    lib, n = mla.library(), ctypes.c_int64(7)
+    assert lib.mla_tree_workspace_fp4(a["rows"], a["heads"], a["batch"], a["nb"], a["bs"], ctypes.byref(n)) == rc and n.value == 7
+    assert lib.mla_tree_workspace_fp4(4, 16, 1, 1, 1, None) == -1
+    with pytest.raises(mla.MlaError):
+        mla.mla_tree_workspace_fp4(a["rows"], a["heads"], a["batch"], a["nb"], a["bs"])
 
 
 def test_python_wants_cuda_tensors():
