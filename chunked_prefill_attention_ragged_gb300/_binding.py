@@ -723,7 +723,7 @@ def _tree_attention(name, kind, width, q_abs, cache, block_table, qo_indptr, kv_
         n = _workspace_bytes.get(dev)
         if n is None:
             n = _workspace_bytes[dev] = mla_tree_workspace(t, h)
-        if kind == "uint8" and t * h > 128 * b:   # (for fewer pairs it is the same)
+        if kind == "uint8" and t * h > 128 * b:   # (for fewer it is the same)
             n = mla_tree_workspace_fp4(t, h, b, cache.shape[0], cache.shape[1])
         workspace = _new(T, (n,), uint8, device, st)
     _check(getattr(_lib or library(), name)(

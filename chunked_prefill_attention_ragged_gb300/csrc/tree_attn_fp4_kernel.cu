@@ -21,6 +21,7 @@
 // read from shared memory for each) and wait 1200 for their operands: keys wait for the copies out of their buffer, which
 // wait for the P V of the tile before last.  No unit is busy more than half of the time; another two tiles would have
 // to fit into shared memory.  Twice the warps that make keys: 1425 us, but 49.8 us instead of 48.2 for 9 x up to 37 nodes.
+// Calls with more than a unit a request mostly come here without room for bf16 rows (see launch_tree_attention_fp4).
 // A code becomes bf16 by moving its bits to a bf16's low exponent bits and one product by 2^126 times the
 // scale, exact; scales above 2, where that factor has no bf16, take two products (a tile in which a warp
 // meets one).  A row with a scale byte above 252 has NaN in its rope, which only S sees, and zeros for values,
@@ -708,15 +709,16 @@ int64_t pairs_of_a_request(int64_t total_rows, int num_heads, int batch) {   // 
 int64_t expanded_at() { return (tree_workspace_bytes() + 1023) & ~int64_t(1023); }
 }  // namespace
 
-// From 384 pairs a request on, three units and more read each row, and making them bf16 once, for the kernel over bf16
-// caches, is faster than making each unit's keys again.  (Replayed graphs, without and with: 64 x 3 over 2048 at 128
-// heads 164 us and EX1, 32 x 4 over 8192 386 and EX2, 32 x 16 over 8192 1469 and EX3, 1 x 16 over 8192 65 and EX4; 32 x 2
-// over 8192, 256 pairs: 203 and 209.)  It takes 1152 bytes for each slot of the cache: above 4 GB of them it is left.
-constexpr int64_t EXPAND_PAIRS = 384, EXPAND_BYTES = int64_t(4) << 30;
+// With more pairs a request than a unit has, each row is read by two units and more, and making them bf16 once, for the
+// kernel over bf16 caches, is faster than making each unit's keys again.  (Replayed graphs, without and with: 32 x 3 over
+// 8192 at 64 heads, 192 pairs, 201 us and 183, 32 x 2 at 128 202 and 186, 32 x 4 384 and 281, 32 x 16 1469 and 838; 1 x 2
+// over 8192 at 128 heads 35 and 36, 1 x 16 64 and 40; of one unit, 32 x 1 over 8192 at 128 heads 110 and 140.)  It takes
+// 1152 bytes for each slot of the cache: above 4 GB of them it is left.
+constexpr int64_t EXPAND_BYTES = int64_t(4) << 30;
 int64_t tree_workspace_fp4_bytes(int64_t total_rows, int num_heads, int batch, int64_t num_blocks, int block_size) {
   const int64_t rows = num_blocks * block_size * (576 * 2), base = tree_workspace_bytes();
   const bool pays = batch > 0 && batch <= 65535 &&
-                    pairs_of_a_request(total_rows, num_heads, batch) >= EXPAND_PAIRS && rows > 0 && rows <= EXPAND_BYTES;
+                    pairs_of_a_request(total_rows, num_heads, batch) > ROWS && rows > 0 && rows <= EXPAND_BYTES;
   return base > 0 && pays ? expanded_at() + rows : base;
 }
 

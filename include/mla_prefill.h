@@ -607,8 +607,11 @@ MLA_API int mla_gather_latent_fp4(const void* cache, int64_t num_blocks, int blo
                                   const int32_t* chunk_starts, int batch, int64_t total_tokens, void* out,
                                   int32_t* status, void* stream);
 
-/* Bytes of workspace with which mla_tree_attention_fp4 is fastest on the current device: mla_tree_workspace's, and,
- * where it pays (many pairs a request), 1152 for each of the cache's slots, while those are below 4 GB. */
+/*
+ * Bytes of workspace with which mla_tree_attention_fp4 is fastest on the current device: those of
+ * mla_tree_workspace and, for more than 128 (node, head) pairs a request (on average; up to 65535
+ * requests), 1152 for each of the cache's slots, where these are no more than 4 GB.
+ */
 MLA_API int mla_tree_workspace_fp4(int64_t total_rows, int num_heads, int batch, int64_t num_blocks, int block_size,
                                    int64_t* bytes);
 
@@ -616,9 +619,10 @@ MLA_API int mla_tree_workspace_fp4(int64_t total_rows, int num_heads, int batch,
  * Attention of drafted nodes, or single new tokens, over an fp4 latent cache: mla_tree_attention with
  *   cache        : uint8 [num_blocks, block_size, 400], 16-byte aligned
  * and everything else as there.  A workspace of mla_tree_workspace bytes serves every call; with one of
- * mla_tree_workspace_fp4 bytes a call of many pairs a request first makes the rows that it reads bf16
- * there, and is up to 1.7 times as fast.  Keys and values are the dequantized rows, which bf16 holds exactly.  A cached row with a scale byte above 252 counts as NaN
- * for the rows that see it (mla_cache_append writes none but 255).
+ * mla_tree_workspace_fp4 bytes a call of more than 128 pairs a request first makes the rows that it reads bf16
+ * there, and is up to 1.8 times as fast.  Keys and values are the dequantized rows, which bf16 holds
+ * exactly.  A cached row with a scale byte above 252 counts as NaN for the rows that see it
+ * (mla_cache_append writes none but 255).
  */
 MLA_API int mla_tree_attention_fp4(const void* q_abs, const void* cache, int64_t num_blocks, int block_size,
                                    const int32_t* block_table, int max_blocks_per_req, const int32_t* qo_indptr,

@@ -46,6 +46,14 @@ def test_against_the_oracle(name, nodes, kv, heads, bs, tree, cap):
         p.check(o, lse)
 
 
+@pytest.mark.parametrize("batch,ctx,nodes,heads", [(2, 9000, 5, 128), (40, 900, 4, 128), (1, 20000, 9, 16), (90, 200, 10, 16)])
+def test_units_in_many_pieces(batch, ctx, nodes, heads):
+    p = Problem4(45 + batch, [nodes] * batch, [ctx + 13 * (r % 7) + nodes for r in range(batch)], heads, 64, True)
+    for o, lse, st in both(p):
+        assert st == 0
+        p.check(o, lse, sorted({0, batch // 2, batch - 1}), None if heads <= 16 else [0, heads // 2, heads - 1])
+
+
 def test_rows_that_are_nan():
     """A scale byte above 252 in a context row makes its request NaN, in a node's row those that see the node."""
     p = Problem4(42, [24, 24, 24], [90, 200, 100], 16, 16, True)
@@ -113,8 +121,8 @@ def test_sizes():
     import chunked_prefill_attention_ragged_gb300 as mla
     base = mla.mla_tree_workspace(64, 128)
     f = mla.mla_tree_workspace_fp4
-    assert f(64, 128, 32, 100, 64) == base                       # 256 pairs a request
+    assert f(32, 128, 32, 100, 64) == base                       # 128 pairs a request: a unit
     assert f(96, 128, 32, 0, 64) == base and f(0, 128, 0, 10, 64) == base
-    large = f(96, 128, 32, 100, 64)
+    large = f(33, 128, 32, 100, 64)
     assert base + 6400 * 1152 <= large <= base + 6400 * 1152 + 1024
     assert f(96, 128, 32, 1 << 16, 64) == base                   # 4.8 GB of rows
