@@ -179,6 +179,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) verify_kernel(const __grid_co
     }
     return;
   }
+  if (rank == 0 && tid == 0) v.next[r] = -1;   // (whoever finds a token writes it behind a cluster's barrier)
   auto load = [&](int j, bool report) {
     Node d;
     d.parent = v.parents ? __ldg(v.parents + q0 + j) : j - 1;
@@ -328,10 +329,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) verify_kernel(const __grid_co
   if (warp == 0 && rank == 0) {
     if (lane == 0) path[0] = 0;
     for (int i = length + lane; i < v.max_accepted; i += 32) path[i] = -1;
-    if (lane == 0) {
-      v.counts[r] = length;
-      if (all == 0) v.next[r] = -1;
-    }
+    if (lane == 0) v.counts[r] = length;
   }
   if (warp == 0 && all > 0) {
     const double u = fminf(fmaxf(__ldg(v.final_uniforms + r), 0.f), 1.f);

@@ -117,6 +117,22 @@ def test_chosen_without_a_workspace_and_replayed():
         assert torch.equal(x, o2) and torch.equal(y, lse2)
 
 
+@pytest.mark.parametrize("nodes,heads,rows", [(16, 64, True), (16, 64, False), (1, 128, False), (1, 16, False)])
+def test_a_wait_that_gives_up(monkeypatch, nodes, heads, rows):
+    """In the test mode each of the kernels reports that a wait ran out, and the next call is as ever."""
+    import chunked_prefill_attention_ragged_gb300 as mla
+    p = Problem4(46, [nodes], [300], heads, 64, True)
+    nb, bs = p.b.cache.shape[:2]
+    n = mla.mla_tree_workspace_fp4(nodes, heads, 1, nb, bs) if rows else mla.mla_tree_workspace(nodes, heads)
+    work = torch.empty(n, dtype=torch.uint8, device="cuda")
+    monkeypatch.setenv("MLA_TEST_FORCE_TIMEOUT_NS", "2000000")
+    assert p.run(workspace=work)[2] == 1
+    monkeypatch.delenv("MLA_TEST_FORCE_TIMEOUT_NS")
+    o, lse, st = p.run(workspace=work)
+    assert st == 0
+    p.check(o, lse)
+
+
 def test_sizes():
     import chunked_prefill_attention_ragged_gb300 as mla
     base = mla.mla_tree_workspace(64, 128)

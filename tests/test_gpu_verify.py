@@ -158,6 +158,17 @@ def test_probabilities_out_of_range():
     assert p.run(1)[2].tolist() == [20]
 
 
+def test_rows_that_are_no_probabilities():
+    """Sums far past one: some token of the vocabulary, or -1; what was in the output does not stay."""
+    d = Drafts(31, [4, 3], 70001, tree=True, drawn=False)
+    d.target = np.full_like(d.target, 1e30)
+    for value in (1e30, np.nan):
+        d.target[:] = value
+        acc, cnt, nxt, st = d.run(3)
+        assert st == 0 and ((nxt >= -1) & (nxt < 70001)).all() and ((cnt >= 1) & (cnt <= 3)).all() and (acc[:, 0] == 0).all()
+    assert (nxt == -1).all()
+
+
 def test_bad_tokens_parents_and_rows():
     p = Drafts(12, [6, 4], 100, True, True, close=0.0)
     p.u[:] = 0
