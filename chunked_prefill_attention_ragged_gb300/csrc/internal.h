@@ -160,7 +160,8 @@ struct TreeParams {
   int32_t* status;
 };
 int64_t tree_workspace_bytes();         // on the current device; 0 on error
-cudaError_t launch_tree_attention(const TreeParams& p, cudaStream_t stream);
+// rows_on_their_way: the launch before it in the stream makes the cache's rows.
+cudaError_t launch_tree_attention(const TreeParams& p, cudaStream_t stream, bool rows_on_their_way);
 
 struct CommitParams {
   uint4* cache;                         // layer l, slot s, chunk c: cache[l * layer_chunks + s * row_chunks + c]

@@ -155,7 +155,7 @@ int mla_tree_attention(const void* q_abs, const void* cache, int64_t num_blocks,
                        int64_t workspace_bytes, int32_t* status, void* stream) {
   return tree_attention(q_abs, cache, num_blocks, block_size, block_table, max_blocks_per_req, qo_indptr, kv_lens,
                         tree_mask, mask_words, batch, total_rows, num_heads, sm_scale, logits_soft_cap, o_lat, lse, workspace,
-                        workspace_bytes, status, stream, launch_tree_attention);
+                        workspace_bytes, status, stream, [](const TreeParams& t, cudaStream_t st) { return launch_tree_attention(t, st, false); });
 }
 
 int mla_tree_attention_fp4(const void* q_abs, const void* cache, int64_t num_blocks, int block_size,

@@ -729,7 +729,7 @@ cudaError_t launch_tree_attention_fp4(const TreeParams& t, cudaStream_t stream) 
     void* rows = static_cast<char*>(t.workspace) + expanded_at();
     expanded.cache = static_cast<const __nv_bfloat16*>(rows);
     const cudaError_t e = launch_tree_expand(t, rows, stream);
-    return e != cudaSuccess ? e : launch_tree_attention(expanded, stream);
+    return e != cudaSuccess ? e : launch_tree_attention(expanded, stream, true);
   }
   // Requests of up to 16 pairs, on average, have units of 16.  (Replayed graphs, this kernel and that one: 64 x 1 over
   // 8192 at 16 heads 200 and 110 us, 1 x 1 over 700 15.4 and 16.4, over 8192 40 and 19; 16 x 1 over 700 20 and 22.5;

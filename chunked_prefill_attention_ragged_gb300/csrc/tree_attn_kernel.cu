@@ -812,6 +812,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   __syncwarp();
   cluster_wait();
   tc_fence_after();
+  grid_dependency_wait();   // (rows that a kernel before this one makes are there)
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const Parts parts(p.t, start, count);
   if (warp == 0) {
@@ -897,7 +898,7 @@ int64_t tree_workspace_bytes() {
   return n > 0 ? (int64_t)(WS_SLOTS + (size_t)n * 2 * SLOT_BYTES) : 0;
 }
 
-cudaError_t launch_tree_attention(const TreeParams& t, cudaStream_t stream) {
+cudaError_t launch_tree_attention(const TreeParams& t, cudaStream_t stream, bool rows_on_their_way) {
   const TreeLaunch p = tree_launch(t, max_workers());
   if (p.workers <= 0) return cudaErrorInvalidConfiguration;
   const bool any = t.max_blocks > 0;   // some cache row may be read
@@ -926,8 +927,13 @@ cudaError_t launch_tree_attention(const TreeParams& t, cudaStream_t stream) {
   } else {
     tk = tv = tq;   // (not used)
   }
-  cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = pair_config(attr, p.workers, stream);
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = pair_config(attr, p.workers, stream);
+  if (rows_on_their_way) {   // the start beside the end of the kernel that makes them
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 2;
+  }
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel_of(box_rows), tq, tk, tv, p);
   return e != cudaSuccess ? e : launch_tree_join(p, stream);
 }
