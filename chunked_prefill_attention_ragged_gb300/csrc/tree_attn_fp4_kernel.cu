@@ -16,11 +16,12 @@
 //   warps 12-19 keys
 // A tile has 64 keys, so that there are two: with one of 128 its making, S, P V and the copies took turns (2207 us).
 // Either S of the next tile or P V of this one is issued, whichever has its operands first (S always first: 1481 us).
-// What bounds it (32 x 16 over 8192 at 128 heads, 1468 us in replayed graphs, 0.43 of the measured tensor rate): a tile takes
-// 3100 clocks, of which the products take 1850 (a product of 64 keys takes as long as one of 128, 30 clocks: Q's rows are
-// read from shared memory for each) and wait 1200 for their operands: keys wait for the copies out of their buffer, which
-// wait for the P V of the tile before last.  No unit is busy more than half of the time; another two tiles would have
-// to fit into shared memory.  Twice the warps that make keys: 1425 us, but 49.8 us instead of 48.2 for 9 x up to 37 nodes.
+// What bounds it (32 x 1 over ragged contexts at 128 heads, 102 us in replayed graphs; 32 x 16 over 8192 1468, 0.42 of the
+// measured tensor rate): a tile takes 3100 clocks, in which 300 KB pass through shared memory (S 108: Q's rows are read for
+// each product, so that one of 64 keys takes as long as one of 128, 30 clocks; copies 64, P V 48, keys 36 in), 2350 clocks
+// of it.  With a stage left out in turn the first case takes: copies of an eighth 85 us, stores of a quarter of the keys
+// 91, no loads 93, a third of S 93, no arithmetic on codes 95, a quarter of P V 100, no exponentials 102.
+// Twice the warps that make keys: 1425 us, but 49.8 us instead of 48.2 for 9 x up to 37 nodes.
 // Calls with more than a unit a request mostly come here without room for bf16 rows (see launch_tree_attention_fp4).
 // A code becomes bf16 by moving its bits to a bf16's low exponent bits and one product by 2^126 times the
 // scale, exact; scales above 2, where that factor has no bf16, take two products (a tile in which a warp
