@@ -57,10 +57,9 @@ enum Bar {
   QE,           // the unit's last S done: Q may be replaced
   KF,           // [buffer] keys made (of both CTAs), for the products
   KL = KF + 2,  // [buffer] the CTA's own, but for the ropes, for their copies
-  KE = KL + 2,  // [buffer] S done with them, and both CTAs' copies
-  VF = KE + 2,  // [buffer] the CTA's values landed
+  VF = KL + 2,  // [buffer] the peer's half of the CTA's values landed
   VR = VF + 2,  // [buffer] (even CTA) the odd one's did
-  VE = VR + 2,  // [buffer] P V done: values, P and, for the next rescale, O are free
+  VE = VR + 2,  // [buffer] P V done: keys, values, P and, for the next rescale, O are free
   SF = VE + 2,  // [buffer] S done (in both CTAs)
   PR = SF + 2,  // [buffer] P written (and the S buffer read) by every softmax warp of both CTAs
   FIN = PR + 2, // every product drained
@@ -155,6 +154,7 @@ __device__ void run_rows(const Ctx& c, const TreeLaunch& p, PartsK parts) {
   uint32_t chunk[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) chunk[i] = ((4 * (lane & 1) + i) ^ row8) << 4;
+  const uint32_t values_at = c.sbase + OFF_V + c.rank * V_HALF + (lane >> 3) * KP + (4 * w8 + r4) * 128;
   const uint32_t keys_at = c.sbase + OFF_K + (lane >> 3) * KP + (4 * w8 + r4) * 128;
   const uint8_t* cache = reinterpret_cast<const uint8_t*>(p.t.cache);
   int g = 0;
@@ -208,7 +208,7 @@ __device__ void run_rows(const Ctx& c, const TreeLaunch& p, PartsK parts) {
       get(blk, key, &now);
       blk = find(key + KEYS);
       __syncwarp();
-      if (w8 == 0 && g > 1) ok = c.wait_warp(KE + b, ((g >> 1) - 1) & 1);
+      if (w8 == 0 && g > 1) ok = c.wait_warp(VE + b, ((g >> 1) - 1) & 1);
       if (meet<256>(3, !ok)) {
         ok = false;
         break;
@@ -218,19 +218,26 @@ __device__ void run_rows(const Ctx& c, const TreeLaunch& p, PartsK parts) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           st_shared_v4(keys_at + b * K_TILE + 4 * j * KP + chunk[i], r[j][4 * i], r[j][4 * i + 1], r[j][4 * i + 2], r[j][4 * i + 3]);
+      const uint32_t to = values_at + b * V_TILE;   // the columns that are the CTA's values
+      if (c.rank == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st_shared_v4(to + chunk[i], r[0][4 * i], r[0][4 * i + 1], r[0][4 * i + 2], r[0][4 * i + 3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st_shared_v4(to + chunk[i], r[1][4 * i], r[1][4 * i + 1], r[1][4 * i + 2], r[1][4 * i + 3]);
+      }
       tell(c, KF + b, lane);
       if (lane == 0) mbar_arrive(c.bar(KL + b));
     }
   }
 }
 
-// Warp 2: a key's first 256 columns are values of the even CTA, the others of the odd one, in the swizzle that they have
-// as keys: they are copied from shared memory to shared memory, 32 rows of a panel at a time.
+// Warp 2: the columns that are values of the other CTA go there as they are, from shared memory to shared memory.
+// (That keys are made says that P V of the tile before last is done, and with it that the other CTA's buffer is free.)
 __device__ void run_copies(const Ctx& c, PartsK parts) {
-  const int lane = threadIdx.x & 31, to_cta = lane & 1;
-  const uint32_t from = c.sbase + OFF_K + to_cta * V_HALF;
-  const uint32_t to = mapa_shared(c.sbase + OFF_V + c.rank * V_HALF, to_cta);
-  const uint32_t full = mapa_shared(c.bar(VF), to_cta);
+  const int lane = threadIdx.x & 31;
+  const uint32_t other = c.rank ^ 1, from = c.sbase + OFF_K + other * V_HALF;
+  const uint32_t to = mapa_shared(c.sbase + OFF_V + c.rank * V_HALF, other), full = mapa_shared(c.bar(VF), other);
   int g = 0;
   bool ok = true;
   Part u;
@@ -238,20 +245,15 @@ __device__ void run_copies(const Ctx& c, PartsK parts) {
 #pragma unroll 1
     for (int t = u.lo; t < u.hi; ++t, ++g) {
       const int b = g & 1;
-      ok = (g < 2 || c.wait_warp(VE + b, ((g >> 1) - 1) & 1)) && c.wait_warp(KL + b, (g >> 1) & 1);
+      ok = c.wait_warp(KL + b, (g >> 1) & 1);
       if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(c.bar(VF + b), V_TILE);
-      if (lane < 2)
+      if (lane == 0) {
+        mbar_arrive_expect_tx(c.bar(VF + b), V_HALF);
         asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to + b * V_TILE),
                      "r"(from + b * K_TILE), "r"(V_HALF), "r"(full + 8 * b)
                      : "memory");
-      __syncwarp();
-      if (c.rank == 0 && g > 0) {   // the even CTA's last ones landed
-        ok = c.wait_warp(VF + (b ^ 1), ((g - 1) >> 1) & 1);
-        if (!ok) break;
-        if (lane < 2) mbar_arrive_remote(mapa_shared(c.bar(KE + (b ^ 1)), lane));
-        __syncwarp();
       }
+      __syncwarp();
     }
   }
   if (!ok) {   // the copies under way land before a CTA can exit: they have this long
@@ -261,7 +263,7 @@ __device__ void run_copies(const Ctx& c, PartsK parts) {
   }
 }
 
-// The odd CTA's warp 1: its copies landed.
+// The odd CTA's warp 1: what it got landed.
 __device__ void run_relay(const Ctx& c, PartsK parts) {
   const uint32_t there = mapa_shared(c.bar(VR), 0);
   int g = 0;
@@ -272,7 +274,6 @@ __device__ void run_relay(const Ctx& c, PartsK parts) {
     for (int t = u.lo; t < u.hi && ok; ++t, ++g) {
       ok = c.wait_warp(VF + (g & 1), (g >> 1) & 1);
       if (ok && (threadIdx.x & 31) == 0) mbar_arrive_remote(there + 8 * (g & 1));
-      if (ok && (threadIdx.x & 31) < 2) mbar_arrive_remote(mapa_shared(c.bar(KE + (g & 1)), threadIdx.x & 31));
       __syncwarp();
     }
   }
@@ -321,7 +322,7 @@ __device__ void run_ropes(const Ctx& c, const TreeLaunch& p, PartsK parts) {
     for (int t = u.lo; t < u.hi; ++t, ++g, key += KEYS) {
       const int b = g & 1;
       const uint32_t dst = c.sbase + OFF_K + b * K_TILE + 8 * KP + r0 * 128;
-      if (g > 1 && !c.wait_warp(KE + b, ((g >> 1) - 1) & 1)) {
+      if (g > 1 && !c.wait_warp(VE + b, ((g >> 1) - 1) & 1)) {
         ok = false;
         break;
       }
@@ -390,7 +391,6 @@ __device__ void run_mma(const Ctx& c, const TreeLaunch& p, PartsK parts, uint32_
         issue_pair(d, q_desc + ((uint32_t)(i * QP + kk * 32) >> 4), k_desc + tile + ((uint32_t)(i * KP + kk * 32) >> 4), IDESC_QK,
                    kk > 0 ? 1u : i > 0 ? 1u : 0u);
     }
-    commit_both(c.bar(KE + b));
     commit_both(c.bar(SF + b));
     if (last) commit_both(c.bar(QE));
     ++st;
@@ -619,8 +619,7 @@ tree_attn_fp4_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     // P: every softmax warp of both CTAs; keys: eight warps of each CTA and the ropes'.
     static_assert(NBAR <= 32, "a lane each");
     const bool keys = lane == KF || lane == KF + 1, local = lane == KL || lane == KL + 1, probs = lane == PR || lane == PR + 1;
-    const bool free = lane == KE || lane == KE + 1;
-    if (lane < NBAR) mbar_init(c.bar(lane), keys ? 18 : probs ? 16 : local ? 8 : free ? 3 : 1);
+    if (lane < NBAR) mbar_init(c.bar(lane), keys ? 18 : probs ? 16 : local ? 8 : 1);
     if (lane == 0) *abort_flag = 0;
     fence_barrier_init();
   }
