@@ -4,24 +4,25 @@
 //
 // Each CTA makes its half of a tile's keys once, as its half of S's B operand.  A key's first 512 values are its
 // value too: its columns 0-255 are values of the even CTA and 256-511 of the odd one, in the swizzle that they have as
-// keys, so that bulk copies take them there from shared memory to shared memory.  (Both made from the entries, as keys by
-// four warps and as values by four more: twice the conversions; 32 x 16 over 8192 at 128 heads 1545 us, 9 x up to
-// 37 nodes at 16 heads 54 us, against 1468 and 48.)  Entries go straight from L2 to registers: there is no room for them
-// in shared memory beside Q (72 KB), two tiles (136 KB) and P (16 KB).
+// keys.  The columns that are the CTA's own values are stored twice, the others go from its keys to the other CTA by bulk
+// copies from shared memory to shared memory.  (Keys and values made from the entries by four warps each, twice the
+// conversions: 32 x 1 over ragged contexts at 128 heads 106 us, 32 x 16 over 8192 1545; all values copied 102 and 1468; so
+// 99 and 1408.  Stores to the other CTA, with a release at cluster scope: 166 and 2707.)  Entries go straight from L2 to
+// registers: there is no room for them in shared memory beside Q (72 KB), two tiles (136 KB) and P (16 KB).
 //   warp 0      Q producer
-//   warp 1      even CTA: issues every product; odd CTA: tells that its copies landed
-//   warp 2      copies of the values
+//   warp 1      even CTA: issues every product; odd CTA: tells that the copies to it landed
+//   warp 2      copies to the other CTA
 //   warp 3      TMEM allocation; ropes; brings entries into L2
 //   warps 4-11  softmax: four threads per pair (quarters of the keys and of O's columns)
 //   warps 12-19 keys
-// A tile has 64 keys, so that there are two: with one of 128 its making, S, P V and the copies took turns (2207 us).
-// Either S of the next tile or P V of this one is issued, whichever has its operands first (S always first: 1481 us).
-// What bounds it (32 x 1 over ragged contexts at 128 heads, 102 us in replayed graphs; 32 x 16 over 8192 1468, 0.42 of the
-// measured tensor rate): a tile takes 3100 clocks, in which 300 KB pass through shared memory (S 108: Q's rows are read for
-// each product, so that one of 64 keys takes as long as one of 128, 30 clocks; copies 64, P V 48, keys 36 in), 2350 clocks
-// of it.  With a stage left out in turn the first case takes: copies of an eighth 85 us, stores of a quarter of the keys
-// 91, no loads 93, a third of S 93, no arithmetic on codes 95, a quarter of P V 100, no exponentials 102.
-// Twice the warps that make keys: 1425 us, but 49.8 us instead of 48.2 for 9 x up to 37 nodes.
+// A tile has 64 keys, so that there are two: with one of 128 its making, S, P V and the copies took turns (149 and 2207 us).
+// Either S of the next tile or P V of this one is issued, whichever has its operands first (S always first: 1.5% more).
+// What bounds it (32 x 1 over ragged contexts at 128 heads, 99 us in replayed graphs; 32 x 16 over 8192 1408, 0.44 of the
+// measured tensor rate): a tile takes 3000 clocks, half of its way through the roles (two are in flight), in which 270 KB
+// pass through shared memory (S 108: Q's rows are read for each product, so that one of 64 keys takes as long as one of
+// 128, 30 clocks).  With a stage left out in turn the first case takes: a third of S 89 us, copies of an eighth 92, no loads
+// 92, stores of a quarter of the keys 95, a quarter of P V 97, no arithmetic on codes 99; without any of them 69, waits and
+// barriers alone.  Sixteen warps that make keys, or every warp looking at its barrier itself: no faster.
 // Calls with more than a unit a request mostly come here without room for bf16 rows (see launch_tree_attention_fp4).
 // A code becomes bf16 by moving its bits to a bf16's low exponent bits and one product by 2^126 times the
 // scale, exact; scales above 2, where that factor has no bf16, take two products (a tile in which a warp
@@ -711,7 +712,7 @@ int64_t expanded_at() { return (tree_workspace_bytes() + 1023) & ~int64_t(1023);
 
 // With more pairs a request than a unit has, each row is read by two units and more, and making them bf16 once, for the
 // kernel over bf16 caches, is faster than making each unit's keys again.  (Replayed graphs, without and with: 32 x 3 over
-// 8192 at 64 heads, 192 pairs, 201 us and 183, 32 x 2 at 128 202 and 186, 32 x 4 384 and 281, 32 x 16 1469 and 838; 1 x 2
+// 8192 at 64 heads, 192 pairs, 201 us and 183, 32 x 2 at 128 202 and 186, 32 x 4 384 and 281, 32 x 16 1408 and 812; 1 x 2
 // over 8192 at 128 heads 35 and 36, 1 x 16 64 and 40; of one unit, 32 x 1 over 8192 at 128 heads 110 and 140.)  It takes
 // 1152 bytes for each slot of the cache: above 4 GB of them it is left.
 constexpr int64_t EXPAND_BYTES = int64_t(4) << 30;
