@@ -75,7 +75,8 @@ enum Bar {
   SF = VE + MAX_STAGES, // [S buffer] S = Q K^T done
   SE = SF + NSB,        // [S buffer] P V done reading P: S may be overwritten
   OD = SE + NSB,        // [tile parity] O += P V done
-  FINQ = OD + 2,        // all MMAs of the S issuer drained before TMEM is released
+  FINQ = OD + 2,        // all MMAs of the S issuer drained before TMEM is released (a pair's odd CTA: every
+                        // commit of the even one has arrived)
   FINP,                 // the same for the P V issuer
   PR,                   // [S buffer][half row] P written by that half's four softmax warps
                         // (of both CTAs of a pair): keys 0-63 / 64-127 of the tile
@@ -347,7 +348,7 @@ __device__ void run_mma_qk(const Ctx<kPair>& c, const PrefillParams& p, uint32_t
     kv_g += n;
   }
   // Every MMA issued by this thread must finish before TMEM is released.
-  c.commit(FINQ);
+  c.commit_both(FINQ);
   c.drain(FINQ, 0);
 }
 
@@ -393,7 +394,7 @@ __device__ void run_mma_pv(const Ctx<kPair>& c, const PrefillParams& p, uint32_t
       c.commit_both(OD + (g & 1));
     }
   }
-  c.commit(FINP);
+  c.commit_both(FINP);
   c.drain(FINP, 0);
 }
 
@@ -849,8 +850,13 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
   tc_fence_before();
   __syncthreads();
   // In a pair, neither CTA leaves (freeing its shared memory and TMEM) while the even
-  // CTA's products may still read or write the other's.
-  if constexpr (kPair) cluster_sync();
+  // CTA's products may still read or write the other's, or their commits arrive in it (in the
+  // odd one the last of those on barriers that nothing there waits for).
+  if constexpr (kPair) {
+    if (rank == 1 && lane == 0 && (warp == 1 || warp == 3)) c.drain(warp == 1 ? FINQ : FINP, 0);
+    __syncwarp();
+    cluster_sync();
+  }
   tc_fence_after();
   if (warp == 1) {
     __syncwarp();

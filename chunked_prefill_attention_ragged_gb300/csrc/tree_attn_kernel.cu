@@ -833,7 +833,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   tc_fence_before();
   __syncthreads();
   // Neither CTA leaves (freeing shared memory and TMEM) while the even CTA's products may still
-  // read or write the other's.
+  // read or write the other's.  The commits of those products arrive in the odd CTA's shared memory too, the last of
+  // them on barriers that nothing there waits for: the last commit of all is waited for here.
+  if (warp == 1 && rank == 1) {
+    if (lane == 0) c.drain(FIN, 0);
+    __syncwarp();
+  }
   cluster_sync();
   tc_fence_after();
   if (warp == 3) {
