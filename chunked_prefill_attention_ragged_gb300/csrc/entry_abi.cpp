@@ -1,5 +1,6 @@
 // C ABI of the entry points for latent cache entries of several formats (declared in
 // include/mla_prefill.h): argument checks and launches.
+#include <algorithm>
 #include <cmath>
 
 #include "internal.h"
@@ -11,6 +12,59 @@ namespace {
 inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 inline int done(cudaError_t e) { return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA; }
+
+// Bytes as a grid of pieces: piece (i, j), i < n[0], j < n[1], is [at + i s[0] + j s[1], + width).
+struct Pieces {
+  const void* at;
+  int64_t n[2], s[2], width;
+};
+inline Pieces bytes(const void* at, int64_t n) { return {at, {1, 1}, {0, 0}, n}; }
+
+inline int64_t div_down(int64_t a, int64_t b) { return a / b - (a % b < 0); }
+// Whether lo < c + k s < hi for some k in [first, last]; s >= 0.
+bool reaches(int64_t c, int64_t s, int64_t first, int64_t last, int64_t lo, int64_t hi) {
+  if (s == 0) return first <= last && lo < c && c < hi;
+  return std::max(first, div_down(lo - c, s) + 1) <= std::min(last, div_down(hi - c - 1, s));
+}
+
+// Whether two grids share a byte.  Exact where they have a stride in common (rows of one matrix, or of the same number of
+// heads) and few pieces lie close to one another; other grids do if the ranges that they lie in do.
+constexpr int64_t MOST_STEPS = 1 << 18;
+bool overlap(Pieces a, Pieces b) {
+  for (int k = 0; k < 2; ++k) {   // the stride of a single piece is any
+    if (a.n[k] == 1) a.s[k] = b.s[k];
+    if (b.n[k] == 1) b.s[k] = a.s[k];
+  }
+  if (!a.at || !b.at || a.width <= 0 || b.width <= 0 || a.n[0] <= 0 || a.n[1] <= 0 || b.n[0] <= 0 || b.n[1] <= 0) return false;
+  auto reach = [](const Pieces& p, int k) { return (p.n[k] - 1) * p.s[k]; };
+  const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(b.at) - reinterpret_cast<uintptr_t>(a.at));
+  if (d >= reach(a, 0) + reach(a, 1) + a.width || -d >= reach(b, 0) + reach(b, 1) + b.width) return false;
+  const bool same[2] = {a.s[0] == b.s[0], a.s[1] == b.s[1]};
+  if (!same[0] && !same[1]) return true;
+  // Pieces k apart in a dimension e with a common stride; in the other one each of a's against all of b's, or, where that
+  // stride is common too, one against all differences.
+  int e = same[0] ? 0 : 1;
+  if (same[0] && same[1] && a.n[1] + b.n[1] < a.n[0] + b.n[0]) e = 1;   // (the fewer steps)
+  const int o = 1 - e;
+  const int64_t far_a = reach(a, o) + a.width, far_b = reach(b, o) + b.width, s = a.s[e];
+  int64_t first = -(a.n[e] - 1), last = b.n[e] - 1;
+  if (s > 0) {
+    first = std::max(first, div_down(-far_b - d, s) + 1);
+    last = std::min(last, div_down(far_a - d - 1, s));
+  } else {
+    first = last = 0;
+  }
+  if (last >= first && (last - first + 1) * (same[o] ? 1 : a.n[o]) > MOST_STEPS) return true;
+  for (int64_t k = first; k <= last; ++k) {
+    if (same[o]) {
+      if (reaches(d + k * s, a.s[o], -(a.n[o] - 1), b.n[o] - 1, -b.width, a.width)) return true;
+    } else {
+      for (int64_t i = 0; i < a.n[o]; ++i)
+        if (reaches(d + k * s - i * a.s[o], b.s[o], 0, b.n[o] - 1, -b.width, a.width)) return true;
+    }
+  }
+  return false;
+}
 
 }  // namespace
 
@@ -42,9 +96,6 @@ int mla_cache_append(void* cache, int entry_format, int64_t num_blocks, int bloc
   if (!latent || !positions || !slot_mapping || (max_positions > 0 && !cos_sin) || (num_blocks > 0 && !cache) ||
       (num_heads > 0 && (!q_rope || !q_out)))
     return MLA_ERR_INVALID_ARG;
-  // Each value is read before it is written only where the two are the same.
-  if (num_heads > 0 && q_rope == q_out && (q_token_stride != q_out_token_stride || q_head_stride != q_out_head_stride))
-    return MLA_ERR_INVALID_ARG;
   // No two of the rows that are written share memory.
   if (num_heads > 0) {
     const int64_t heads = (num_heads - 1) * q_out_head_stride + 64, tokens = (num_tokens - 1) * q_out_token_stride + 64;
@@ -52,6 +103,20 @@ int mla_cache_append(void* cache, int entry_format, int64_t num_blocks, int bloc
         (num_heads > 1 && num_tokens > 1 && q_out_token_stride < heads && q_out_head_stride < tokens))
       return MLA_ERR_INVALID_ARG;
   }
+  // What is written is read by nobody and written by nobody else; but the queries may be rotated in place, where each
+  // value is read before it is written.
+  const int64_t entry = entry_format == MLA_ENTRY_BF16 ? 1152 : entry_format == MLA_ENTRY_FP8 ? 648 : 400;
+  const Pieces rows = bytes(cache, num_blocks * block_size * entry), state = bytes(status, 4);
+  const Pieces out = {num_heads > 0 ? q_out : nullptr, {num_tokens, num_heads}, {2 * q_out_token_stride, 2 * q_out_head_stride}, 128};
+  const Pieces in = {num_heads > 0 ? q_rope : nullptr, {num_tokens, num_heads}, {2 * q_token_stride, 2 * q_head_stride}, 128};
+  const Pieces read[] = {{latent, {num_tokens, 1}, {2 * latent_stride, 0}, 1152}, bytes(norm_weight, 1024),
+                         bytes(positions, 4 * num_tokens), bytes(cos_sin, 256 * std::min(max_positions, INT64_MAX >> 16)), bytes(slot_mapping, 8 * num_tokens)};
+  for (const Pieces& r : read)
+    if (overlap(rows, r) || overlap(out, r) || overlap(state, r)) return MLA_ERR_INVALID_ARG;
+  if (overlap(rows, in) || overlap(rows, out) || overlap(rows, state) || overlap(state, in) || overlap(state, out))
+    return MLA_ERR_INVALID_ARG;
+  const bool in_place = q_rope == q_out && q_token_stride == q_out_token_stride && q_head_stride == q_out_head_stride;
+  if (!in_place && overlap(in, out)) return MLA_ERR_INVALID_ARG;
   AppendParams p;
   p.cache = static_cast<uint8_t*>(cache);
   p.num_slots = num_blocks * block_size;

@@ -578,6 +578,9 @@ MLA_API int mla_tree_verify(const void* target_probs, const void* draft_probs, i
  *                  strides) or none of it.  E.g. q_rope = q + 128 of q [T, H, 192], q_out = q_abs +
  *                  512 of q_abs [T, H, 576]   (written)
  *   status       : DEVICE int32 word or NULL
+ * Apart from that nothing that is written shares memory with what is read or written: MLA_ERR_INVALID_ARG.
+ * (Views into one buffer are looked at piece by piece where they have a stride in common, others by the
+ * ranges that they lie in.)
  * A token with a negative slot is padding: nothing of it is read or written, not its queries either.
  * MLA_DEVSTAT_BAD_INDEX is OR-ed in for a slot past the cache or a position outside
  * [0, max_positions); nothing of such a token is written.  Where two tokens name one slot, what is
