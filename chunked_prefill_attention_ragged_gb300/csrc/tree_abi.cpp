@@ -184,6 +184,18 @@ int mla_tree_verify(const void* target_probs, const void* draft_probs, int prob_
   if (batch == 0) return MLA_OK;
   if (!qo_indptr || !final_uniforms || !accepted || !accepted_counts || !next_tokens) return MLA_ERR_INVALID_ARG;
   if (total_rows > 0 && (!target_probs || !tokens || !uniforms)) return MLA_ERR_INVALID_ARG;
+  // Paths are written while other CTAs of the request still read, and by more than one of them.
+  struct Bytes { const void* at; int64_t n; };
+  const int64_t b = batch, probs = total_rows * vocab * (int64_t)element;
+  const Bytes written[] = {{accepted, 4 * b * max_accepted}, {accepted_counts, 4 * b}, {next_tokens, 4 * b}, {status, 4}};
+  const Bytes read[] = {{target_probs, probs}, {draft_probs, probs}, {tokens, 4 * total_rows}, {parents, 4 * total_rows},
+                        {qo_indptr, 4 * (b + 1)}, {uniforms, 4 * total_rows}, {final_uniforms, 4 * b}};
+  for (const Bytes& w : written) {
+    for (const Bytes& r : read)
+      if (overlap(w.at, w.n, r.at, r.n)) return MLA_ERR_INVALID_ARG;
+    for (const Bytes* o = written; o != &w; ++o)
+      if (overlap(w.at, w.n, o->at, o->n)) return MLA_ERR_INVALID_ARG;
+  }
   VerifyParams v = {};
   v.target = target_probs;
   v.draft = draft_probs;

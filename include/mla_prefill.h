@@ -535,8 +535,8 @@ MLA_API int mla_tree_commit(void* cache, int num_layers, int64_t layer_stride, i
  * MLA_DEVSTAT_BAD_INDEX is OR-ed in for a token outside the vocabulary or a parent that is not below its
  * node (such a node counts as if it was not there, node 0's own apart), or a request whose rows are not
  * inside total_rows (as one without nodes).
- * vocab <= 2^24, vocab * total_rows any; all arrays aligned to their elements.  One launch; allocates
- * nothing.
+ * vocab <= 2^24, vocab * total_rows any; all arrays aligned to their elements; none that is written may
+ * share memory with another (MLA_ERR_INVALID_ARG).  One launch; allocates nothing.
  */
 MLA_API int mla_tree_verify(const void* target_probs, const void* draft_probs, int prob_type, int64_t vocab,
                             const int32_t* tokens, const int32_t* parents, const int32_t* qo_indptr, int batch,
