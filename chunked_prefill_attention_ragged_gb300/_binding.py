@@ -593,7 +593,7 @@ class _Torch:
         import torch
         self.int32, self.int64, self.uint8 = torch.int32, torch.int64, torch.uint8
         self.bf16, self.f32 = torch.bfloat16, torch.float32
-        self.empty = torch.empty
+        self.empty, self.out_of_memory = torch.empty, torch.OutOfMemoryError
         self.device, self.raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
@@ -724,8 +724,12 @@ def _tree_attention(name, kind, width, q_abs, cache, block_table, qo_indptr, kv_
         if n is None:
             n = _workspace_bytes[dev] = mla_tree_workspace(t, h)
         if kind == "uint8" and t * h > 128 * b:   # (for fewer it is the same)
-            n = mla_tree_workspace_fp4(t, h, b, cache.shape[0], cache.shape[1])
-        workspace = _new(T, (n,), uint8, device, st)
+            try:
+                workspace = _new(T, (mla_tree_workspace_fp4(t, h, b, cache.shape[0], cache.shape[1]),), uint8, device, st)
+            except T.out_of_memory:   # the rows in bf16 are 2.9 times the cache: without room for them the call is slower
+                pass
+        if workspace is None:
+            workspace = _new(T, (n,), uint8, device, st)
     _check(getattr(_lib or library(), name)(
         _arg(q_abs, bfloat16, dev, "q_abs"), _arg(cache, getattr(T, kind), dev, "cache"), cache.shape[0], cache.shape[1],
         _arg(block_table, int32, dev, "block_table"), m, _arg(qo_indptr, int32, dev, "qo_indptr", (b + 1,)),
@@ -753,7 +757,7 @@ def mla_tree_attention_fp4(q_abs, cache, block_table, qo_indptr, kv_lens, tree_m
                            status=None, stream=None):
     """mla_tree_attention over a cache of 4-bit entries, uint8 [NB, BS, 400]; the rest as there.  With many
     pairs a request the workspace that is allocated has room for the cache's rows in bf16 (see
-    mla_tree_workspace_fp4); one of mla_tree_workspace bytes may be given instead."""
+    mla_tree_workspace_fp4) unless memory is short; one of mla_tree_workspace bytes may be given instead."""
     return _tree_attention("mla_tree_attention_fp4", "uint8", 400, q_abs, cache, block_table, qo_indptr, kv_lens,
                            tree_mask, sm_scale, logits_soft_cap, o, lse, return_lse, workspace, status, stream)
 
