@@ -854,8 +854,9 @@ def mla_cache_append(cache, latent, slot_mapping, positions, cos_sin, norm_weigh
             raise ValueError(f"q_rope and q_out must be [{t}, H, 64]")
         h = q_rope.shape[1]
         if h and t:
-            q = (_view(q_rope, bf16, dev, "q_rope"), q_rope.stride(0), q_rope.stride(1), h,
-                 _view(q_out, bf16, dev, "q_out"), q_out.stride(0), q_out.stride(1))
+            # (torch gives a dimension of one element any stride)
+            at = lambda x: (x.stride(0) if t > 1 else 64 * h, x.stride(1) if h > 1 else 64)  # noqa: E731
+            q = (_view(q_rope, bf16, dev, "q_rope"), *at(q_rope), h, _view(q_out, bf16, dev, "q_out"), *at(q_out))
     elif q_out is not None:
         raise ValueError("q_out without q_rope")
     _check((_lib or library()).mla_cache_append(
