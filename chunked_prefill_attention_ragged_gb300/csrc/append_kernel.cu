@@ -101,6 +101,16 @@ __device__ __forceinline__ float larger(float a, float b) {
   return a;
 }
 
+// The sum of the squares of a row: each lane has sixteen of its values.
+__device__ __forceinline__ float squares(const float (*x)[8]) {
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s += x[0][i] * x[0][i] + x[1][i] * x[1][i];
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(ALL, s, d);
+  return s;
+}
+
 template <int FORMAT>
 __global__ void __launch_bounds__(WARPS * 32) append_kernel(const __grid_constant__ AppendParams p) {
   const int lane = threadIdx.x & 31;
@@ -144,12 +154,19 @@ __global__ void __launch_bounds__(WARPS * 32) append_kernel(const __grid_constan
     float g[2][8];
     unpack(__ldg(w + lane), g[0]);
     unpack(__ldg(w + 32 + lane), g[1]);
-    float s = 0.f;
+    float s = squares(x), eps = p.norm_eps;   // (the same in every lane)
+    // Squares that leave fp32's range: the row by a power of two, which the quotient takes out again.
+    if (s > 0x1p120f || s * (1.f / 512.f) + eps < 0x1p-60f) {
+      const float f = s > 1.f ? 0x1p-70f : 0x1p80f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s += x[0][i] * x[0][i] + x[1][i] * x[1][i];
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(ALL, s, d);
-    const float r = 1.f / sqrtf(s * (1.f / 512.f) + p.norm_eps);
+      for (int i = 0; i < 8; ++i) {
+        x[0][i] *= f;
+        x[1][i] *= f;
+      }
+      s = squares(x);
+      eps = eps * f * f;   // (the square of the larger f has no fp32)
+    }
+    const float r = 1.f / sqrtf(s * (1.f / 512.f) + eps);
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
