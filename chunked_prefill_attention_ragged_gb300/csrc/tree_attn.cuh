@@ -368,8 +368,9 @@ __device__ __forceinline__ int32_t piece_rows(const TreeLaunch& p, const Part& u
 // tree_join_kernel.cu: joins the parts of units that several workers left.
 cudaError_t launch_tree_join(const TreeLaunch& p, cudaStream_t stream);
 // The same for units of few pairs: a slot is O (fp32) row by row, then the rows' (m in log2 units, l).
-__host__ __device__ constexpr size_t few_slot_bytes(int rows) { return (size_t)rows * (512 * 4 + 8); }
-cudaError_t launch_tree_join_few(const TreeLaunch& p, int rows, cudaStream_t stream);
+constexpr int TREE_FEW = 16;   // pairs of such a unit
+constexpr size_t FEW_SLOT_ML = (size_t)TREE_FEW * 512 * 4, FEW_SLOT_BYTES = FEW_SLOT_ML + TREE_FEW * 8;
+cudaError_t launch_tree_join_few(const TreeLaunch& p, cudaStream_t stream);
 
 constexpr uint64_t TREE_DRAIN_LIMIT_NS = 200000000ull;   // own copies and products after an abort
 constexpr float TREE_RESCALE_THRESHOLD = 8.0f;           // log2 units

@@ -34,7 +34,7 @@
 namespace mla {
 namespace {
 
-constexpr int N = 16, KEYS = 64;   // pairs of a unit, keys of a tile
+constexpr int N = TREE_FEW, KEYS = 64;   // pairs of a unit, keys of a tile
 constexpr int NTHREADS = 640;
 constexpr int PANEL = KEYS * 128;        // 64 keys x 64 columns
 constexpr int TILE = 9 * PANEL;
@@ -106,8 +106,7 @@ __device__ __forceinline__ uint32_t ld_shared_u8(uint32_t a) {
 }
 
 // Warp 0: half a tile's entries at a time, in runs of rows that lie side by side (`run`: as many of 32 as the
-// block size is a multiple of, 8 at least, or 1), a lane a row.  Where the ring holds one tile only, the next one's
-// entries are brought into L2 meanwhile.
+// block size is a multiple of, 8 at least, or 1), a lane a row.
 __device__ void run_copies(const Ctx& c, const TreeLaunch& p, PartsN parts, uint8_t* smem) {
   constexpr int SLOTS = Off::SLOTS;
   const int lane = threadIdx.x & 31, bs = p.t.block_size;
@@ -124,20 +123,14 @@ __device__ void run_copies(const Ctx& c, const TreeLaunch& p, PartsN parts, uint
       return k < end ? __ldg(p.t.block_table + (int64_t)u.r * p.t.max_blocks + block_of(p, (int)k)) : 0;
     };
     int64_t key = (int64_t)u.lo * KEYS + lane;
-    auto row_of = [&](int32_t blk, int64_t k) { return k < end ? block_row(p, blk == PAST_END ? -1 : blk, k) : p.oob_row; };
     int32_t blk0 = find(key), blk1 = find(key + 32), blk2 = find(key + 64), blk3 = find(key + 96);
 #pragma unroll 1
     for (int n = 0; n < 2 * (u.hi - u.lo); ++n, key += 32, ++put) {
-      const int32_t row = row_of(blk0, key);
+      const int32_t row = key < end ? block_row(p, blk0 == PAST_END ? -1 : blk0, key) : p.oob_row;
       blk0 = blk1;
       blk1 = blk2;
       blk2 = blk3;
       blk3 = find(key + 128);
-      if (SLOTS == 1) {
-        const int32_t later = row_of(blk1, key + 64);
-        if (later != p.oob_row)
-          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(cache + (int64_t)later * FP4_ENTRY), "r"(FP4_ENTRY) : "memory");
-      }
       const uint32_t have = __ballot_sync(0xffffffffu, row != p.oob_row);
       const uint32_t g = put >> 1, slot = g % SLOTS, half = 2 * slot + (put & 1), dst = c.sbase + Off::RING + half * HALF;
       if ((put & 1) == 0 && g >= SLOTS && !c.wait_warp(EE + slot, (g / SLOTS - 1) & 1)) {
@@ -507,7 +500,7 @@ __device__ void run_softmax(const Ctx& c, const TreeLaunch& p, PartsN parts, uin
     wait(TE + ((g - 1) & 1), ((g - 1) >> 1) & 1);
     tc_fence_after();
     const int live = ok ? min(max(u.npairs - i0, 0), W) : 0;   // pairs to write
-    char* slot = ws_slots + (size_t)u.slot * few_slot_bytes(N);
+    char* slot = ws_slots + (size_t)u.slot * FEW_SLOT_BYTES;
 #pragma unroll
     for (int i = 0; i < W; ++i) {
       l[i] = (sums[i] + sums[N + i]) + (sums[2 * N + i] + sums[3 * N + i]);
@@ -516,7 +509,7 @@ __device__ void run_softmax(const Ctx& c, const TreeLaunch& p, PartsN parts, uin
           const bool empty = l[i] == 0.f;   // (a NaN is passed on)
           if (p.t.lse) p.t.lse[u.pair0 + i0 + i] = empty ? NEG_INF : (m[i] + log2f(l[i])) * 0.6931471805599453f;
         } else {
-          reinterpret_cast<float2*>(slot + (size_t)N * 512 * 4)[i0 + i] = make_float2(m[i], l[i]);
+          reinterpret_cast<float2*>(slot + FEW_SLOT_ML)[i0 + i] = make_float2(m[i], l[i]);
         }
       }
       if (u.whole) l[i] = l[i] == 0.f ? 0.f : 1.f / l[i];
@@ -580,7 +573,7 @@ tree_attn_fp4_few_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_
     else if (warp == 2) run_values(c, parts, tmem);
     else run_queries(c, parts, &tm_q);
   } else if (warp < 12) {
-    run_softmax(c, p, parts, tmem, ws + WS_SLOTS + (size_t)worker * 2 * few_slot_bytes(N), smem);
+    run_softmax(c, p, parts, tmem, ws + WS_SLOTS + (size_t)worker * 2 * FEW_SLOT_BYTES, smem);
   } else {
     run_rows(c, p, parts, smem);
   }
@@ -604,7 +597,7 @@ int max_workers() {
     int dev = 0;
     r = cudaGetDevice(&dev);
     if (r != cudaSuccess) return r;
-    const int64_t room = (tree_workspace_bytes() - (int64_t)WS_SLOTS) / (int64_t)(2 * few_slot_bytes(N));
+    const int64_t room = (tree_workspace_bytes() - (int64_t)WS_SLOTS) / (int64_t)(2 * FEW_SLOT_BYTES);
     workers[dev] = (int)std::min<int64_t>(device_sm_count(), std::min<int64_t>(room, MAX_WORKERS));
     return r;
   });
@@ -628,7 +621,7 @@ cudaError_t launch_tree_attention_fp4_few(const TreeParams& t, cudaStream_t stre
   cfg.dynamicSmemBytes = Off::SMEM;
   cfg.stream = stream;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_attn_fp4_few_kernel, tq, p);
-  return e != cudaSuccess ? e : launch_tree_join_few(p, N, stream);
+  return e != cudaSuccess ? e : launch_tree_join_few(p, stream);
 }
 
 }  // namespace mla

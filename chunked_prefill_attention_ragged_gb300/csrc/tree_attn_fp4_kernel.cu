@@ -740,7 +740,7 @@ cudaError_t launch_tree_attention_fp4(const TreeParams& t, cudaStream_t stream) 
   // Requests of up to 16 pairs, on average, have units of 16.  (Replayed graphs, this kernel and that one: 64 x 1 over
   // 8192 at 16 heads 200 and 110 us, 1 x 1 over 700 15.4 and 16.4, over 8192 40 and 19; 16 x 1 over 700 20 and 22.5;
   // units of 32 for 64 x 1 over 8192 at 32 heads: 202 and 197, 8 x 1 over 20000 73 and 77, 1 x 1 over 700 15 and 25.)
-  if (pairs_of_a_request(t.total_rows, t.num_heads, t.batch) <= 16) return launch_tree_attention_fp4_few(t, stream);
+  if (pairs_of_a_request(t.total_rows, t.num_heads, t.batch) <= TREE_FEW) return launch_tree_attention_fp4_few(t, stream);
   const TreeLaunch p = tree_launch(t, max_workers());
   if (p.workers <= 0) return cudaErrorInvalidConfiguration;
   CUtensorMap tq;

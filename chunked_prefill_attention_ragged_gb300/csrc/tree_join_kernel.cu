@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) tree_join_kernel(const __grid
 // 2 us.  (In replayed graphs, the whole call at 16 heads: 2 requests over 8192 23.5 us, 34.6 with GROUPS = 1 and 27.1 with
 // GROUPS = 4 at every boundary; 8 over 8192 30.5, 33.8 and 32.0; 16 over 8192 42.7 with GROUPS = 1, 43.9 with 4.)
 template <int GROUPS>
-__global__ void __launch_bounds__(GROUPS * 128) tree_join_few_kernel(const __grid_constant__ TreeLaunch p, int rows) {
+__global__ void __launch_bounds__(GROUPS * 128) tree_join_few_kernel(const __grid_constant__ TreeLaunch p) {
   constexpr int THREADS = GROUPS * 128;
   __shared__ float weight[GROUPS > 1 ? MAX_WORKERS : 1];
   __shared__ float2 part[THREADS / 32];
@@ -97,10 +97,9 @@ __global__ void __launch_bounds__(GROUPS * 128) tree_join_few_kernel(const __gri
   const JoinRec j = recs[b];
   const int n = j.parts;
   if (n == 0 || row >= j.npairs) return;
-  const size_t bytes = few_slot_bytes(rows);
-  const char* slots = ws + WS_SLOTS + (size_t)2 * (b - 1) * bytes;
-  auto slot = [&](int k) { return slots + (size_t)(2 * k + (k == 0 ? j.slot0 : 0)) * bytes; };
-  auto state = [&](int k) { return reinterpret_cast<const float2*>(slot(k) + (size_t)rows * 512 * 4)[row]; };
+  const char* slots = ws + WS_SLOTS + (size_t)2 * (b - 1) * FEW_SLOT_BYTES;
+  auto slot = [&](int k) { return slots + (size_t)(2 * k + (k == 0 ? j.slot0 : 0)) * FEW_SLOT_BYTES; };
+  auto state = [&](int k) { return reinterpret_cast<const float2*>(slot(k) + FEW_SLOT_ML)[row]; };
   auto values = [&](int k) { return *reinterpret_cast<const float4*>(slot(k) + ((size_t)row * 512 + col) * 4); };
   const float NEG_INF = -__int_as_float(0x7f800000);
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -161,20 +160,20 @@ __global__ void __launch_bounds__(GROUPS * 128) tree_join_few_kernel(const __gri
 
 }  // namespace
 
-cudaError_t launch_tree_join_few(const TreeLaunch& p, int rows, cudaStream_t stream) {
+cudaError_t launch_tree_join_few(const TreeLaunch& p, cudaStream_t stream) {
   if (p.workers < 2) return cudaSuccess;
-  const int64_t units = (p.t.total_rows * p.t.num_heads + (int64_t)p.t.batch * (rows - 1)) / rows;   // at most
+  const int64_t units = (p.t.total_rows * p.t.num_heads + (int64_t)p.t.batch * (TREE_FEW - 1)) / TREE_FEW;   // at most
   const bool wide = units * 8 <= p.workers;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = wide ? dim3((unsigned)units, rows) : dim3(p.workers - 1, rows);
+  cfg.gridDim = wide ? dim3((unsigned)units, TREE_FEW) : dim3(p.workers - 1, TREE_FEW);
   cfg.blockDim = dim3(wide ? 512 : 128);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return wide ? cudaLaunchKernelEx(&cfg, tree_join_few_kernel<4>, p, rows) : cudaLaunchKernelEx(&cfg, tree_join_few_kernel<1>, p, rows);
+  return wide ? cudaLaunchKernelEx(&cfg, tree_join_few_kernel<4>, p) : cudaLaunchKernelEx(&cfg, tree_join_few_kernel<1>, p);
 }
 
 cudaError_t launch_tree_join(const TreeLaunch& p, cudaStream_t stream) {

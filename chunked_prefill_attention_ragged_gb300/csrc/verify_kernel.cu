@@ -144,7 +144,7 @@ __device__ __forceinline__ uint64_t group_sum(const T* p, const T* q, int64_t fi
 // its draft (or its given children) taken off.
 struct Ask {
   int pick, given, node;
-  double a, sum;
+  double a;
 };
 struct Node {
   int parent, token;   // parent -1: never kept
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) verify_kernel(const __grid_co
         sum = true;
       }
     }
-    if (lane == 0) ask = Ask{pick, pick && !full && !draft, cur, a, 0.0};
+    if (lane == 0) ask = Ask{pick, pick && !full && !draft, cur, a};
   };
   int sweeps = 0;
   uint64_t before = 0;   // what the slices before this one have
