@@ -817,10 +817,11 @@ def mla_tree_commit(cache, block_table, seq_lens, accepted, accepted_counts, sta
 # ---------------------------------------------------------------------------- entries of several formats
 def _view(t, dtype, dev, name):
     """Address of a tensor whose last dimension is contiguous, on the current device."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype or t.get_device() != dev:
+    try:
+        ok = t.dtype is dtype and t.get_device() == dev and dev >= 0
+    except AttributeError:
+        ok = False
+    if not ok:
         _bad_tensor(t, dtype, dev, name)
     if t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
