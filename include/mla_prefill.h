@@ -531,7 +531,7 @@ MLA_API int mla_tree_commit(void* cache, int num_layers, int64_t layer_stride, i
  * final_uniform times the sum of all; where nothing is left of it, p itself counts.
  * Other nodes whose parent is -1 are never kept.  A request without nodes gets count 0, next -1; so
  * does next where p has no mass.  Probabilities are taken into [0, 1], a NaN as 0; a row's sum must be
- * below 2048.  Sums are kept in 64-bit fixed point (2^-43): they do not depend on any order.
+ * below 2^21.  Sums are kept in 64-bit fixed point (2^-43): they do not depend on any order.
  * MLA_DEVSTAT_BAD_INDEX is OR-ed in for a token outside the vocabulary or a parent that is not below its
  * node (such a node counts as if it was not there, node 0's own apart), or a request whose rows are not
  * inside total_rows (as one without nodes).
