@@ -7,10 +7,11 @@
 // one load in fp4, 8 in fp8, so that its largest magnitude takes two or three shuffles), or 32 heads of its
 // queries: eight lanes a head, four heads a load, eight loads under way.  Both kinds are blocks of one
 // grid, so that a decoding step of few tokens has all its latencies side by side.  (Replayed graphs: 8192 bf16 tokens
-// with 128 heads 50 us, 290 MB at 5.8 TB/s, 0.85 of a copy's rate; 10,245 fp8 tokens 8 us, 18.4 MB that stay in L2;
-// 64 fp4 tokens with 16 heads 3 us, the three loads that follow one another.)
+// with 128 heads 50 us, 290 MB at 5.8 TB/s, 0.86 of a copy's rate; up to 2049 fp8 tokens of 5 requests and the gather of
+// them 8 us, data that stay in L2; 64 fp4 tokens with 16 heads 3 us, the three loads that follow one another.)
 //
-// Roundings: sums, norm and rotation are fp32; each stored value is rounded once.
+// Roundings: sums, norm and rotation are fp32; each stored value is rounded once.  Squares may leave fp32's range where
+// values do not: such a row is scaled by a power of two first.
 #include <cuda_bf16.h>
 
 #include "fp4.cuh"

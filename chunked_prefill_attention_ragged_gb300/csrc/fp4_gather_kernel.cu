@@ -3,8 +3,9 @@
 //
 // Memory bound: 400 bytes read, 1152 written a row.  A warp has a row: lane l words l and 32 + l of the codes (128
 // contiguous bytes a load, 512 a store), whose scales are bytes l / 4 and 8 + l / 4, and lanes 0-7 copy 16 bytes of rope.
-// As many warps as rows: a row's latencies, slot then entry, lie beside other rows'.  (4 x 8192 rows 12.1 us in replayed
-// graphs, 4.2 TB/s, 3 x 500 2.7; one wave of warps, two rows in flight each: 12.3 and 3.4, four rows: 14.3 and 4.6.)
+// As many warps as rows: a row's latencies, slot then entry, lie beside other rows'.  (4 x 8192 rows 11.6 us in replayed
+// graphs, 4.4 TB/s, 3 x 500 2.3; as first measured, 12.1 and 2.7, one wave of warps with two rows in flight each took 12.3
+// and 3.4, four rows 14.3 and 4.6.)
 #include "fp4.cuh"
 #include "internal.h"
 #include "paged.cuh"

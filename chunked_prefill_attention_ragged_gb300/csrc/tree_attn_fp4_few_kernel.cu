@@ -17,7 +17,8 @@
 // S and P V have a warp each: from one warp, which has to take them in a fixed order, P V waited for the next
 // tile's keys or S for this tile's softmax (64 x 1 over 8192 at 16 heads: 184 us).
 // Where P V's accumulator lies: columns 128 i .. of the latent in TMEM columns N i .., lane = column.
-// What bounds it (64 x 1 over 8192 at 16 heads, 111 us in replayed graphs, 1.9 TB/s of entries): 3640 clocks a tile, of
+// What bounds it (64 x 1 over 8192 at 16 heads, 110 us in replayed graphs, 1.9 TB/s of entries; bf16 entries, 2.9 times the
+// bytes, 107-109): 3640 clocks a tile, of
 // which the warps that make keys work 3000; 277 KB pass through shared memory (entries in and out, keys in, and read by both
 // products), 2160 clocks of it.  With a stage left out in turn the call takes: a quarter of the stores of keys 98 us, no loads
 // of codes 101, no arithmetic on them 103, a quarter of S 106, of P V 109, no exponentials 111, entries from L2 111.

@@ -17,8 +17,9 @@
 //   warps 12-19 keys
 // A tile has 64 keys, so that there are two: with one of 128 its making, S, P V and the copies took turns (149 and 2207 us).
 // Either S of the next tile or P V of this one is issued, whichever has its operands first (S always first: 1.5% more).
-// What bounds it (32 x 1 over ragged contexts at 128 heads, 99 us in replayed graphs; 32 x 16 over 8192 1408, 0.44 of the
-// measured tensor rate): a tile takes 3000 clocks, half of its way through the roles (two are in flight), in which 270 KB
+// What bounds it (32 x 1 over ragged contexts at 128 heads, 98.4 us in replayed graphs, where bf16 entries take 70.6; 64 x 1
+// over 8192 at 32, 64 and 128 heads 189, 192 and 195-199, most of a unit's 128 pairs padding at 32 and 64, bf16 entries
+// 112, 115 and 122; 32 x 16 over 8192 1408-1425, 0.44 of the measured tensor rate): a tile takes 3000 clocks, half of its way through the roles (two are in flight), in which 270 KB
 // pass through shared memory (S 108: Q's rows are read for each product, so that one of 64 keys takes as long as one of
 // 128, 30 clocks).  With a stage left out in turn the first case takes: a third of S 89 us, copies of an eighth 92, no loads
 // 92, stores of a quarter of the keys 95, a quarter of P V 97, no arithmetic on codes 99; without any of them 69, waits and
@@ -717,9 +718,9 @@ int64_t expanded_at() { return (tree_workspace_bytes() + 1023) & ~int64_t(1023);
 
 // With more pairs a request than a unit has, each row is read by two units and more, and making them bf16 once, for the
 // kernel over bf16 caches, is faster than making each unit's keys again.  (Replayed graphs, without and with: 32 x 3 over
-// 8192 at 64 heads, 192 pairs, 201 us and 183, 32 x 2 at 128 202 and 186, 32 x 4 384 and 281, 32 x 16 1408 and 812; 1 x 2
-// over 8192 at 128 heads 35 and 36, 1 x 16 64 and 40; of one unit, 32 x 1 over 8192 at 128 heads 110 and 140.)  It takes
-// 1152 bytes for each slot of the cache: above 4 GB of them it is left.
+// 8192 at 64 heads, 192 pairs, 194 us and 181, 32 x 2 at 128 196 and 182, 32 x 4 373 and 276, 32 x 16 1423 and 852; 1 x 2
+// over 8192 at 128 heads 35.6 and 35.8, 1 x 16 65 and 41; of one unit, 32 x 1 over 8192 at 128 heads 110 and 140.)  It takes
+// 1152 bytes for each slot of the cache, whatever the call reads of it: above 4 GB of them it is left.
 constexpr int64_t EXPAND_BYTES = int64_t(4) << 30;
 int64_t tree_workspace_fp4_bytes(int64_t total_rows, int num_heads, int batch, int64_t num_blocks, int block_size) {
   const int64_t rows = num_blocks * block_size * (576 * 2), base = tree_workspace_bytes();
@@ -737,9 +738,13 @@ cudaError_t launch_tree_attention_fp4(const TreeParams& t, cudaStream_t stream) 
     const cudaError_t e = launch_tree_expand(t, rows, stream);
     return e != cudaSuccess ? e : launch_tree_attention(expanded, stream, true);
   }
-  // Requests of up to 16 pairs, on average, have units of 16.  (Replayed graphs, this kernel and that one: 64 x 1 over
-  // 8192 at 16 heads 200 and 110 us, 1 x 1 over 700 15.4 and 16.4, over 8192 40 and 19; 16 x 1 over 700 20 and 22.5;
-  // units of 32 for 64 x 1 over 8192 at 32 heads: 202 and 197, 8 x 1 over 20000 73 and 77, 1 x 1 over 700 15 and 25.)
+  // Requests of up to 16 pairs, on average, have units of 16.  (Replayed graphs at 16 heads, units of 128 and of 16: 64 x 1
+  // over 8192 189 and 110 us, over 2000 58 and 42, over 700 30 and 26; 1 x 1 over 8192 39 and 18, over 2000 22 and 15.
+  // With few tiles for the SMs, where a call is its start and its end, units of 16 lose: 1 x 1 over 64 11.6 and 13.8, over
+  // 700 15.1 and 15.5; 16 x 1 over 64 12.8 and 14.7, over 700 19.0 and 22.1, over 2000 25.6 and 24.6; 64 x 1 over 64 and 300
+  // even.  The lengths are on the device, and a table is as wide as the longest request that a server allows, so that the
+  // rule goes by pairs alone: 3 us lost at most, up to 79 won.  Units of 32 for 64 x 1 over 8192 at 32 heads: 197, of 128
+  // 202 at that time; 8 x 1 over 20000 77 and 73.)
   if (pairs_of_a_request(t.total_rows, t.num_heads, t.batch) <= TREE_FEW) return launch_tree_attention_fp4_few(t, stream);
   const TreeLaunch p = tree_launch(t, max_workers());
   if (p.workers <= 0) return cudaErrorInvalidConfiguration;

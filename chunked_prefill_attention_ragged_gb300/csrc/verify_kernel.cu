@@ -10,8 +10,8 @@
 // Sums are integers in units of 2^-43: exact whatever their order, so that the token does not depend on
 // how the row is split; an entry is off by half a unit at most, at random.  An entry's integer comes from two
 // additions of constants, whose results' low bits it is (a conversion of fp32 to 64 bits takes eight times as long
-// here).  (p - a q)+ is made by two fp32 multiply-adds with a in two fp32 parts: off by 2^-24 of p at most, at
-// random; a itself is good to 2^-48.
+// here).  (p - a q)+ is made by two fp32 multiply-adds with a in two fp32 parts (2^-48 of it): off by 2^-24 of p at
+// most, at random, and so are, by less, the sums of them and the a of the next refusal.
 //
 // One launch; a cluster of up to eight CTAs has a request, each a slice of the vocabulary.  Every CTA walks
 // the tree by itself (its few numbers are loaded at once, for all nodes) and comes to the same end; only
@@ -19,7 +19,7 @@
 // leaves each such sum in shared memory, so that the search looks at the sums and one group of entries.
 // What bounds it: for few requests latencies, one behind the other (the nodes, the row's slice, the cluster's
 // sum, the group); for many the reading of the last nodes' rows.  (Replayed graphs: 1 request of 5 given nodes over 32,003
-// entries 8.5 us; 64 of up to 16 drawn ones over 131,072 28.5 us, of which the rows that are read, 67 MB, take 10 at a copy's rate: a node's
+// entries 8.7 us; 64 of up to 16 drawn ones over 131,072 28.1-28.7 us, of which the rows that are read, 67 MB, take 10 at a copy's rate: a node's
 // refusals are one pass over its rows each, and the next pass starts from the last one's sum.)
 #include <cuda_bf16.h>
 
