@@ -624,9 +624,9 @@ MLA_API int mla_tree_workspace_fp4(int64_t total_rows, int num_heads, int batch,
  * and everything else as there.  A workspace of mla_tree_workspace bytes serves every call; with one of
  * mla_tree_workspace_fp4 bytes a call of more than 128 pairs a request first makes the rows that it reads bf16
  * there, and is up to 1.8 times as fast.  How it is computed follows from the pairs a request, the total over
- * batch, empty requests counted: a large request among many empty ones is right but takes up to three times as
- * long as by itself (60 nodes of 16 heads over 8192 beside 63 empty requests: 103 us, alone 33).  Keys and values are the dequantized rows, which bf16 holds
- * exactly.  A cached row with a scale byte above 252 counts as NaN for the rows that see it
+ * batch, empty requests counted: a large request among many empty ones gets the same answer but takes longer than
+ * by itself (16 heads over 8192: 60 nodes beside 63 empty requests 103 us, alone 33; 256 beside 255 400, alone 60).
+ * Keys and values are the dequantized rows, which bf16 holds exactly.  A cached row with a scale byte above 252 counts as NaN for the rows that see it
  * (mla_cache_append writes none but 255).
  */
 MLA_API int mla_tree_attention_fp4(const void* q_abs, const void* cache, int64_t num_blocks, int block_size,
